@@ -526,6 +526,157 @@ moe_status moe_fused_forward(const moe_bf16* x, const float* w, const int32_t* r
  */
 moe_status moe_selftest_bounded_wait(int32_t* dev_status, uint64_t limit_ns, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The layer around the block: layer norm, routing with a balance bias and
+ * expert groups, and the linear layer.  These calls take their sizes
+ * themselves (no moe_dims).  Matrices come as moe_mat: row-major with `ld`
+ * elements from one row to the next (ld >= the row's length; the columns are
+ * contiguous), so that a column slice of a wider tensor needs no copy.
+ * Host-side errors, before anything is enqueued:
+ *   MOE_ERR_INVALID_ARG  a required pointer is NULL or misaligned (to 16 bytes
+ *                        unless a call says otherwise), an ld below the row's
+ *                        length, an enum out of range;
+ *   MOE_ERR_UNSUPPORTED  sizes or types a call does not take;
+ *   MOE_ERR_CUDA         a launch failed.
+ * They are part of version 4 of the ABI: they add entry points and change
+ * none. */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
+
+typedef struct {
+  void* p;
+  int64_t ld;
+} moe_mat;
+
+/*
+ * Layer norm over the last axis, with the residual add in front of it:
+ *   r = round(x + res)  (r = x, not written, when res.p is NULL)
+ *   mean = sum_d r / D,  rstd = 1 / sqrt(sum_d (r - mean)^2 / D + eps)
+ *   y = round((r - mean) * rstd * gamma + beta)
+ * r is rounded to the rows' type before its statistics are taken, so that a
+ * backward that reads the stored r sees the same rows; sums are fp32.
+ *   x, res, r, y  `type` [rows, D];  gamma, beta  `wtype` [D] (`type` or fp32)
+ *   mean, rstd    fp32 [rows] out, both or neither NULL
+ * r and y may share x's or res's memory (same ld).  1 <= D <= 8192,
+ * 0 <= rows < 2^31.
+ * Pointers need only the alignment of their elements.
+ */
+moe_status moe_layer_norm(moe_mat x, moe_mat res, const void* gamma, const void* beta, moe_mat r,
+                          moe_mat y, float* mean, float* rstd, float eps, int64_t rows, int32_t D,
+                          moe_dtype type, moe_dtype wtype, cudaStream_t stream);
+
+/*
+ * Its backward, from the stored rows r and their statistics:
+ *   xh = (r - mean) * rstd,  a = dy * gamma
+ *   dx = round(rstd * (a - sum_d a / D - xh * sum_d (a * xh) / D) + dres)
+ *   dgamma = round(sum_rows dy * xh),  dbeta = round(sum_rows dy)
+ * dx is the gradient of x and of res alike; dres (may be NULL) is what else
+ * flows into r.  dgamma and dbeta (`wtype` [D]) are both given or both NULL;
+ * they need ws (moe_layer_norm_workspace_bytes) and are reproducible bit for
+ * bit (partial sums joined in a fixed order).  dx may share dy's or dres's
+ * memory (same ld).  rows = 0 gives zero weight gradients.
+ */
+size_t moe_layer_norm_workspace_bytes(int64_t rows, int32_t D);
+moe_status moe_layer_norm_bwd(moe_mat dy, moe_mat r, const void* gamma, const float* mean,
+                              const float* rstd, moe_mat dres, moe_mat dx, void* dgamma,
+                              void* dbeta, void* ws, int64_t rows, int32_t D, moe_dtype type,
+                              moe_dtype wtype, cudaStream_t stream);
+
+typedef enum { MOE_GATE_SIGMOID = 0, MOE_GATE_SOFTMAX = 1 } moe_gate;
+
+typedef struct {
+  int32_t T;          /* tokens */
+  int32_t E;          /* experts, 1..1024 */
+  int32_t K;          /* experts taken per token, 1..32 */
+  int32_t gate;       /* moe_gate */
+  int32_t groups;     /* equal groups of consecutive experts, 1..32 (1: no groups) */
+  int32_t top_groups; /* groups a token may choose from, 1..groups */
+  int32_t group_top;  /* a group's score: its best (1) or its two best (2) added */
+  int32_t renorm;     /* weights divided by their sum over the K experts */
+  float scale;        /* and multiplied by this */
+} moe_topk_dims;
+
+/*
+ * Expert selection with a balance bias and group-limited top-k:
+ *   s_e   = sigmoid(l_e), or softmax over all E logits
+ *   sel_e = s_e + bias_e: the bias steers the selection and stays out of the
+ *           weights.  Without a bias the order is the logits' own.
+ *   a group's score is the sum of its group_top best sel (of s when bias is
+ *   NULL and group_top = 2); the top_groups best groups stay
+ *   ids = the K largest sel of the groups that stay, in descending order
+ *   w_k = scale * s[ids_k]  (/ sum_k s[ids_k] with renorm; 0 when that is 0)
+ * Ties go to the lowest expert id (the lowest group).  ids are those of the
+ * scores' real values to 64-bit rounding: where two fp32 scores lie too near
+ * to be told apart, the token is selected again in fp64.  A logit of -inf (or
+ * NaN) masks its expert: s = 0, behind every other; a token whose experts are
+ * all masked gets the lowest ids with weights 0.  bias must be finite.
+ * moe_route_histogram in mode MOE_SCORE_GIVEN takes ids and w from here.
+ *   logits fp32 [T,E];  bias fp32 [E] or NULL;  ids int32 [T,K] out;
+ *   w fp32 [T,K] out.  K <= top_groups * (E / groups), E % groups == 0.
+ */
+moe_status moe_route_topk(const float* logits, const float* bias, int32_t* ids, float* w,
+                          moe_topk_dims d, cudaStream_t stream);
+
+/*
+ * Its backward: dlogits (fp32 [T,E], written whole) from dw (fp32 [T,K]).
+ * The selection itself has no gradient; ids outside [0, E) carry none.
+ *   ds_k = scale * dw_k, and with renorm
+ *          ds_k = (scale * dw_k - sum_j scale * dw_j s_j / S) / S, S = sum_j s_j
+ *   sigmoid: dl[ids_k] = ds_k s_k (1 - s_k), 0 elsewhere
+ *   softmax: dl_e = s_e (ds_e - sum_k ds_k s_k) (0 outside ids with renorm,
+ *            where the sum vanishes)
+ * The fields groups, top_groups and group_top are not read.
+ */
+moe_status moe_route_topk_bwd(const float* logits, const int32_t* ids, const float* dw,
+                              float* dlogits, moe_topk_dims d, cudaStream_t stream);
+
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,      /* z * Phi(z) */
+  MOE_ACT_GELU_TANH = 3, /* z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))) */
+  MOE_ACT_SILU = 4       /* z * sigmoid(z) */
+} moe_act;
+
+typedef struct {
+  int64_t M;        /* rows, 0 .. 2^31 - 257 */
+  int32_t K;        /* input width, a multiple of 8 */
+  int32_t N;        /* output width, a multiple of 8 */
+  int32_t type;     /* moe_dtype of x, w, z: MOE_BF16 or MOE_FP16 */
+  int32_t out_type; /* moe_dtype of y, res and dy: `type` or MOE_FP32 */
+  int32_t act;      /* moe_act */
+} moe_linear_dims;
+
+/*
+ * Linear layer with its epilogue in the product:
+ *   z = x w + bias (fp32 accumulation),  y = round(act(z) + res)
+ *   x `type` [M,K];  w `type` [K,N];  bias fp32 [N] or NULL;
+ *   res `out_type` [M,N] or NULL p;  y `out_type` [M,N] out;
+ *   z `type` [M,N] out or NULL p: the rounded pre-activation a backward needs
+ *   (y is computed from the unrounded one).
+ * y may share res's memory (same ld).  Every ld is a multiple of 8, or of 4
+ * for fp32 matrices.  An fp32 y is summed over stretches of K of at most 512
+ * in registers, which keeps it as exact as a sum in fp32 arithmetic.
+ */
+moe_status moe_linear(moe_mat x, moe_mat w, const float* bias, moe_mat res, moe_mat y, moe_mat z,
+                      int32_t* dev_status, moe_linear_dims d, cudaStream_t stream);
+
+/*
+ * Its backward:
+ *   dz = dy * act'(z), rounded to `type` (the operand type of the products)
+ *   dx = round(dz w^T + dx_add),  dw = round(x^T dz),  db = sum_rows of the
+ *   unrounded dz (fp32 [N])
+ *   dy `out_type` [M,N];  z as saved (not read, may be NULL, for MOE_ACT_NONE);
+ *   dx_add `type` [M,K] or NULL p: another branch's gradient of x;
+ *   dx `type` [M,K], dw `type` [K,N], db: each may be NULL to skip it, not all.
+ * The residual's gradient is dy itself.  x is read for dw only, w for dx
+ * only.  dx may share dx_add's memory (same ld).  M = 0 gives zero dw and db.
+ * ws: moe_linear_workspace_bytes(d) bytes.
+ */
+size_t moe_linear_workspace_bytes(moe_linear_dims d);
+moe_status moe_linear_bwd(moe_mat dy, moe_mat z, moe_mat x, moe_mat w, moe_mat dx_add, moe_mat dx,
+                          moe_mat dw, float* db, int32_t* dev_status, void* ws, moe_linear_dims d,
+                          cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

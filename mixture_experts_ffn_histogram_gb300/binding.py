@@ -36,7 +36,16 @@ ENTRY_POINTS = (
     "moe_grouped_gemm_fc1_swiglu_experts", "moe_grouped_gemm_fc1_bwd_experts",
     "moe_fused_forward", "moe_mx_combine_bwd", "moe_mx_quantize_rows", "moe_mx_quantize_tokens", "moe_mx_grouped_gemm_fc2_bwd",
     "moe_mx_grouped_gemm_fc1_bwd",
+    "moe_layer_norm", "moe_layer_norm_bwd", "moe_layer_norm_workspace_bytes", "moe_route_topk",
+    "moe_route_topk_bwd", "moe_linear", "moe_linear_bwd", "moe_linear_workspace_bytes",
 )
+
+# moe_dtype
+BF16, FP16, FP32 = range(3)
+DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+# moe_gate, moe_act: names -> values
+GATES = {"sigmoid": 0, "softmax": 1}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 # moe_mx_buffer
 (MX_XQ, MX_XSC, MX_WIQ, MX_WISC, MX_WOQ, MX_WOSC, MX_HQ, MX_HSC, MX_DYQ, MX_DYSC, MX_DZQ,
@@ -55,6 +64,22 @@ class MoeDims(ctypes.Structure):
         return f"MoeDims(T={self.T}, D={self.D}, E={self.E}, K={self.K}, F={self.F})"
 
 
+class MoeMat(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class MoeTopkDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class MoeLinearDims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn: str, status: int, detail: str | None = None):
         super().__init__(f"{fn}: {detail or status_string(status)} (status {status})")
@@ -67,6 +92,15 @@ _lib = None
 
 def dims(T, D, E, K, F) -> MoeDims:
     return MoeDims(T, D, E, K, F)
+
+
+def topk_dims(T, E, K, gate="sigmoid", groups=1, top_groups=1, group_top=1, renorm=True,
+              scale=1.0) -> MoeTopkDims:
+    return MoeTopkDims(T, E, K, GATES[gate], groups, top_groups, group_top, int(renorm), scale)
+
+
+def linear_dims(M, K, N, dtype=torch.bfloat16, out_dtype=None, act="none") -> MoeLinearDims:
+    return MoeLinearDims(M, K, N, DTYPES[dtype], DTYPES[out_dtype or dtype], ACTS[act])
 
 
 def library_path() -> str:
@@ -116,6 +150,18 @@ def lib() -> ctypes.CDLL:
             "moe_mx_grouped_gemm_fc2_bwd": ([P] * 13 + [D_, P], I),
             "moe_mx_grouped_gemm_fc1_bwd": ([P] * 12 + [D_, P], I),
         }
+        M, L64, F = MoeMat, ctypes.c_int64, ctypes.c_float
+        sig.update({
+            "moe_layer_norm": ([M, M, P, P, M, M, P, P, F, L64, ctypes.c_int32, I, I, P], I),
+            "moe_layer_norm_bwd": ([M, M, P, P, P, M, M, P, P, P, L64, ctypes.c_int32, I, I, P],
+                                   I),
+            "moe_layer_norm_workspace_bytes": ([L64, ctypes.c_int32], ctypes.c_size_t),
+            "moe_route_topk": ([P, P, P, P, MoeTopkDims, P], I),
+            "moe_route_topk_bwd": ([P, P, P, P, MoeTopkDims, P], I),
+            "moe_linear": ([M, M, P, M, M, M, P, MoeLinearDims, P], I),
+            "moe_linear_bwd": ([M] * 7 + [P, P, P, MoeLinearDims, P], I),
+            "moe_linear_workspace_bytes": ([MoeLinearDims], ctypes.c_size_t),
+        })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -314,3 +360,63 @@ def moe_mx_grouped_gemm_fc1_bwd(dzq, dzsc, wiq, wisc, xt, xtsc, dzt, dztsc, grou
     _ok("moe_mx_grouped_gemm_fc1_bwd", lib().moe_mx_grouped_gemm_fc1_bwd(
         _p(dzq), _p(dzsc), _p(wiq), _p(wisc), _p(xt), _p(xtsc), _p(dzt), _p(dztsc),
         _p(group_offsets), _p(dxs), _p(dwi), _p(dev_status), d, _s(stream)))
+
+
+# ------------------------------------------------------------ layer operators
+_NO_MAT = MoeMat(None, 0)
+
+
+def _m(t):
+    """A 2-D tensor with contiguous columns (any row stride) as a moe_mat."""
+    if t is None:
+        return _NO_MAT
+    (rows, cols), (ld, inner) = t.shape, t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError("matrices passed to libmoe need contiguous columns")
+    if rows < 2:  # its row stride is never used, and torch leaves it arbitrary
+        ld = (cols + 7) // 8 * 8
+    return MoeMat(t.data_ptr(), ld)
+
+
+def moe_layer_norm(x, res, gamma, beta, r, y, mean, rstd, eps: float, stream=None):
+    rows, D = x.shape
+    _ok("moe_layer_norm", lib().moe_layer_norm(
+        _m(x), _m(res), _p(gamma), _p(beta), _m(r), _m(y), _p(mean), _p(rstd), float(eps), rows,
+        D, DTYPES[x.dtype], DTYPES[gamma.dtype], _s(stream)))
+
+
+def moe_layer_norm_workspace_bytes(rows: int, D: int) -> int:
+    return int(lib().moe_layer_norm_workspace_bytes(rows, D))
+
+
+def moe_layer_norm_bwd(dy, r, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, stream=None):
+    rows, D = dy.shape
+    _ok("moe_layer_norm_bwd", lib().moe_layer_norm_bwd(
+        _m(dy), _m(r), _p(gamma), _p(mean), _p(rstd), _m(dres), _m(dx), _p(dgamma), _p(dbeta),
+        _p(ws), rows, D, DTYPES[dy.dtype], DTYPES[gamma.dtype], _s(stream)))
+
+
+def moe_route_topk(logits, bias, ids, w, d: MoeTopkDims, stream=None):
+    _ok("moe_route_topk", lib().moe_route_topk(_p(logits), _p(bias), _p(ids), _p(w), d,
+                                               _s(stream)))
+
+
+def moe_route_topk_bwd(logits, ids, dw, dlogits, d: MoeTopkDims, stream=None):
+    _ok("moe_route_topk_bwd", lib().moe_route_topk_bwd(_p(logits), _p(ids), _p(dw), _p(dlogits),
+                                                       d, _s(stream)))
+
+
+def moe_linear(x, w, bias, res, y, z, dev_status, d: MoeLinearDims, stream=None):
+    _ok("moe_linear", lib().moe_linear(_m(x), _m(w), _p(bias), _m(res), _m(y), _m(z),
+                                       _p(dev_status), d, _s(stream)))
+
+
+def moe_linear_workspace_bytes(d: MoeLinearDims) -> int:
+    return int(lib().moe_linear_workspace_bytes(d))
+
+
+def moe_linear_bwd(dy, z, x, w, dx_add, dx, dw, db, dev_status, ws, d: MoeLinearDims,
+                   stream=None):
+    _ok("moe_linear_bwd", lib().moe_linear_bwd(
+        _m(dy), _m(z), _m(x), _m(w), _m(dx_add), _m(dx), _m(dw), _p(db), _p(dev_status), _p(ws),
+        d, _s(stream)))

@@ -1,0 +1,124 @@
+// dz = dy * act'(z) and its column sums, the first step of the linear
+// layer's backward.  Bound by HBM: dy and z are read once, dz is written
+// once, 16 bytes per access.  The column sums are of the unrounded fp32 dz;
+// each block leaves one row of partial sums per stretch of rows, joined in a
+// fixed order.
+#include <algorithm>
+
+#include "activation.cuh"
+#include "kernels.h"
+#include "layer.h"
+#include "layer_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T, typename Y>
+struct ActGradArgs {
+  const Y* dy;
+  const T* z;
+  T* dz;
+  float* partials;
+  int64_t lddy, ldz, M, N, rows_per_block;
+  int act, col_threads;
+};
+
+template <typename Y>
+__device__ __forceinline__ void load8(const Y* p, float (&f)[8]) {
+  if constexpr (sizeof(Y) == 4) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    Raw<Y, 8> r;
+    r.load(p, 0);
+    r.unpack(f);
+  }
+}
+
+// Blocks of col_threads x (kThreads / col_threads) threads, eight columns a thread.
+template <typename T, typename Y>
+__global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradArgs<T, Y> p) {
+  __shared__ float red[kThreads][9];
+  const int tx = threadIdx.x % p.col_threads, ty = threadIdx.x / p.col_threads;
+  const int nrow = kThreads / p.col_threads;
+  const int64_t col = (static_cast<int64_t>(blockIdx.x) * p.col_threads + tx) * 8;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rows_per_block;
+  const int64_t r1 = min(p.M, r0 + p.rows_per_block);
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  if (col < p.N) {
+#pragma unroll 2
+    for (int64_t r = r0 + ty; r < r1; r += nrow) {
+      float g[8];
+      load8<Y>(p.dy + r * p.lddy + col, g);
+      if (p.act != MOE_ACT_NONE) {
+        float z[8];
+        load8<T>(p.z + r * p.ldz + col, z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] *= act_slope<false>(z[j], p.act);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += g[j];
+      if (p.dz != nullptr) {
+        Raw<T, 8> o;
+        o.pack(g);
+        o.store(p.dz + r * p.N + col, 0);
+      }
+    }
+  }
+  if (p.partials == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) red[threadIdx.x][j] = sum[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.col_threads * 8; i += kThreads) {
+    const int c = i / 8, j = i % 8;
+    float s = 0.0f;
+    for (int y = 0; y < nrow; ++y) s += red[y * p.col_threads + c][j];
+    const int64_t cc = (static_cast<int64_t>(blockIdx.x) * p.col_threads + c) * 8 + j;
+    if (cc < p.N) p.partials[static_cast<int64_t>(blockIdx.y) * p.N + cc] = s;
+  }
+}
+
+template <typename T, typename Y>
+cudaError_t launch_t(const ActGradCall& c, cudaStream_t s) {
+  ActGradArgs<T, Y> a{};
+  a.dy = static_cast<const Y*>(c.dy);
+  a.z = static_cast<const T*>(c.z);
+  a.dz = static_cast<T*>(c.dz);
+  a.partials = c.db != nullptr ? c.partials : nullptr;
+  a.lddy = c.lddy;
+  a.ldz = c.ldz;
+  a.M = c.M;
+  a.N = c.N;
+  a.act = c.act;
+  int ct = 32;
+  while (ct > 1 && ct / 2 * 8 >= c.N) ct /= 2;
+  a.col_threads = ct;
+  const int64_t gx = (c.N + ct * 8 - 1) / (ct * 8);
+  // about eight blocks per SM, whole passes of the block's rows each
+  const int64_t pass = kThreads / ct;
+  int64_t gy = std::max<int64_t>(1, static_cast<int64_t>(sm_count()) * 8 / gx);
+  gy = std::min({gy, (c.M + pass - 1) / pass, kPartialRows});
+  a.rows_per_block = ((c.M + gy - 1) / gy + pass - 1) / pass * pass;
+  gy = (c.M + a.rows_per_block - 1) / a.rows_per_block;
+  act_grad_kernel<T, Y><<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kThreads, 0, s>>>(a);
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess || c.db == nullptr) return err;
+  return launch_join_partials(c.partials, static_cast<int>(gy), c.N, c.N, c.db, nullptr, MOE_FP32, s);
+}
+
+}  // namespace
+
+cudaError_t launch_act_grad(const ActGradCall& c, cudaStream_t s) {
+  const bool f32 = c.dy_type == MOE_FP32;
+  if (c.type == MOE_BF16)
+    return f32 ? launch_t<__nv_bfloat16, float>(c, s) : launch_t<__nv_bfloat16, __nv_bfloat16>(c, s);
+  return f32 ? launch_t<__half, float>(c, s) : launch_t<__half, __half>(c, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,79 @@
+// Activations of the linear layer and their derivatives, in fp32.
+//
+// EXACT false is for 16-bit results: the hardware exponential and division
+// (2 and a few ulp) and, for gelu, erfc by the rational approximation 7.1.26
+// of Abramowitz and Stegun, Handbook of Mathematical Functions (absolute
+// error at most 1.5e-7), far below half a step of bf16 or fp16.  EXACT true
+// is for fp32 results and uses the accurate functions.
+#pragma once
+
+#include "layer_common.cuh"
+
+namespace moe {
+
+template <bool EXACT>
+__device__ __forceinline__ float act_exp(float x) {
+  return EXACT ? expf(x) : __expf(x);
+}
+template <bool EXACT>
+__device__ __forceinline__ float act_div(float a, float b) {
+  return EXACT ? a / b : __fdividef(a, b);
+}
+template <bool EXACT>
+__device__ __forceinline__ float act_sigmoid(float x) {
+  return act_div<EXACT>(1.0f, 1.0f + act_exp<EXACT>(-x));
+}
+
+// Phi(z) and e^(-z^2/2).
+template <bool EXACT>
+__device__ __forceinline__ float2 normal_cdf(float z) {
+  if constexpr (EXACT) {
+    return make_float2(0.5f * erfcf(-0.70710678f * z), expf(-0.5f * z * z));
+  } else {
+    const float x = 0.70710678f * fabsf(z);
+    const float t = __fdividef(1.0f, 1.0f + 0.3275911f * x);
+    const float e = __expf(-x * x);
+    const float poly =
+        t * (0.254829592f +
+             t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    const float q = 0.5f * poly * e;  // Phi(-|z|)
+    return make_float2(z >= 0.0f ? 1.0f - q : q, e);
+  }
+}
+
+constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+template <bool EXACT>
+__device__ __forceinline__ float act_value(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.0f ? z : 0.0f;
+    case MOE_ACT_GELU: return z * normal_cdf<EXACT>(z).x;
+    case MOE_ACT_GELU_TANH:  // (1 + tanh u) / 2 = sigmoid(2 u)
+      return z * act_sigmoid<EXACT>(kGeluA * z * (1.0f + kGeluB * z * z));
+    case MOE_ACT_SILU: return z * act_sigmoid<EXACT>(z);
+    default: return z;
+  }
+}
+
+template <bool EXACT>
+__device__ __forceinline__ float act_slope(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case MOE_ACT_GELU: {
+      const float2 c = normal_cdf<EXACT>(z);
+      return c.x + 0.3989422804f * z * c.y;
+    }
+    case MOE_ACT_GELU_TANH: {
+      const float s = act_sigmoid<EXACT>(kGeluA * z * (1.0f + kGeluB * z * z));
+      return s + z * s * (1.0f - s) * kGeluA * (1.0f + 3.0f * kGeluB * z * z);
+    }
+    case MOE_ACT_SILU: {
+      const float s = act_sigmoid<EXACT>(z);
+      return s * (1.0f + z * (1.0f - s));
+    }
+    default: return 1.0f;
+  }
+}
+
+}  // namespace moe

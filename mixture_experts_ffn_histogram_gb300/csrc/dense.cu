@@ -1,0 +1,514 @@
+// Dense products of the linear layer on the fifth-generation tensor cores,
+// with its epilogue (bias, activation, residual) in the kernel.
+//
+//   forward  z = x w + bias, y = act(z) + res     (w [K, N]: its N axis contiguous)
+//   dgrad    dx = dz w^T + dx_add
+//   wgrad    dw = x^T dz
+// Operands are 16-bit, sums fp32 in tensor memory.
+//
+// split kernel: one 128 x BN tile per cluster, the reduction split over the
+// cluster's CTAs.  Each CTA runs a TMA ring over its share of the reduction,
+// leaves its fp32 partial tile in its own shared memory, and after a cluster
+// barrier every CTA sums one slice of the rows over all partials (in rank
+// order, so results are reproducible) and runs the epilogue on it.  With few
+// rows the roles of the operands are swapped (SWAP): the weights' columns are
+// the tile's 128 side and the rows its narrow side, so that a handful of rows
+// costs a 16-column MMA and the weights are read once by all SMs together.
+// For fp32 results the accumulators are drained into registers every
+// kChunkBlocks reduction blocks: the tensor core's additions truncate, and a
+// long chain of them would lose what an fp32 result is asked for.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "activation.cuh"
+#include "kernels.h"
+#include "layer.h"
+#include "layer_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTileM = 128;
+constexpr int kBlockK = 64;
+constexpr int kMmaK = 16;
+constexpr int kChunk = 64 * kBlockK * 2;         // 64 columns x 64 reduction rows: 8 KB
+constexpr int kATile = kTileM * kBlockK * 2;     // 16 KB
+constexpr int kSplitThreads = 192;
+constexpr int kSplitMaxStages = 12;
+constexpr int kChunkBlocks = 8;                  // fp32 results: 512 products per chain
+constexpr int kSplitSmemLimit = 220 * 1024;
+
+// Instruction descriptor, kind::f16: as instr_desc_bf16, with the operand
+// type as an argument (0: f16, 1: bf16; both operands the same).
+__host__ __device__ constexpr uint32_t dense_idesc(int M, int N, bool a_mn, bool b_mn, uint32_t ty) {
+  return (1u << 4) | (ty << 7) | (ty << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
+struct DenseParams {
+  const float* bias;
+  const void* res;
+  void* c;
+  void* z;
+  int64_t ldres, ldc, ldz;
+  int64_t M, N;      // of the output
+  int kblocks;       // reduction blocks of 64
+  int type, out_type, act;
+  int32_t* status;
+  uint64_t limit_ns;
+};
+
+// The epilogue of four neighbouring columns of one output row.
+template <typename T, typename O>
+__device__ __forceinline__ void epilogue4(float (&v)[4], int64_t row, int64_t col,
+                                          const DenseParams& p) {
+  constexpr bool kExact = sizeof(O) == 4;
+  if (p.bias != nullptr) {
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col));
+    v[0] += b.x;
+    v[1] += b.y;
+    v[2] += b.z;
+    v[3] += b.w;
+  }
+  if (p.z != nullptr) {
+    T* z = static_cast<T*>(p.z) + row * p.ldz + col;
+    *reinterpret_cast<uint2*>(z) = make_uint2(pack_pair(v[0], v[1], T{}), pack_pair(v[2], v[3], T{}));
+  }
+  if (p.act != MOE_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_value<kExact>(v[i], p.act);
+  }
+  O* c = static_cast<O*>(p.c) + row * p.ldc + col;
+  const O* res = static_cast<const O*>(p.res);
+  if constexpr (sizeof(O) == 4) {
+    if (res != nullptr) {
+      const float4 r = *reinterpret_cast<const float4*>(res + row * p.ldres + col);
+      v[0] += r.x;
+      v[1] += r.y;
+      v[2] += r.z;
+      v[3] += r.w;
+    }
+    *reinterpret_cast<float4*>(c) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    if (res != nullptr) {
+      const uint2 r = *reinterpret_cast<const uint2*>(res + row * p.ldres + col);
+      const float2 r0 = unpack_pair(r.x, O{}), r1 = unpack_pair(r.y, O{});
+      v[0] += r0.x;
+      v[1] += r0.y;
+      v[2] += r1.x;
+      v[3] += r1.y;
+    }
+    *reinterpret_cast<uint2*>(c) = make_uint2(pack_pair(v[0], v[1], O{}), pack_pair(v[2], v[3], O{}));
+  }
+}
+__device__ __forceinline__ void epilogue4_any(float (&v)[4], int64_t row, int64_t col,
+                                              const DenseParams& p) {
+  if (p.out_type == MOE_FP32) {
+    if (p.type == MOE_BF16) epilogue4<__nv_bfloat16, float>(v, row, col, p);
+    else epilogue4<__half, float>(v, row, col, p);
+  } else if (p.type == MOE_BF16) {
+    epilogue4<__nv_bfloat16, __nv_bfloat16>(v, row, col, p);
+  } else {
+    epilogue4<__half, __half>(v, row, col, p);
+  }
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+struct SplitCtl {
+  uint64_t full[kSplitMaxStages];
+  uint64_t empty[kSplitMaxStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Columns of a TMEM allocation: a power of two, at least 32.
+__host__ __device__ constexpr int tmem_cols(int n) { return n <= 32 ? 32 : (n <= 64 ? 64 : (n <= 128 ? 128 : (n <= 256 ? 256 : 512))); }
+
+// Shared memory of a CTA: the operand ring (in which the partial tile is laid
+// when the products are done), then the control block.
+__host__ __device__ constexpr int split_stage_bytes(int BN) { return kATile + BN * kBlockK * 2; }
+__host__ __device__ constexpr int split_partial_bytes(int BN, bool swap) {
+  return swap ? BN * (kTileM + 4) * 4 : kTileM * (BN + 4) * 4;
+}
+
+template <int BN, bool AMN, bool BMN, bool SWAP>
+__global__ void __launch_bounds__(kSplitThreads)
+    dense_split_kernel(const __grid_constant__ CUtensorMap map_a,
+                       const __grid_constant__ CUtensorMap map_b, const DenseParams p,
+                       const int stages, const int splits, const int chunk_blocks) {
+  static_assert(!BMN || BN % 64 == 0, "MN-major operands come in 64-wide chunks");
+  constexpr int kStage = split_stage_bytes(BN);
+  constexpr uint32_t kCols = tmem_cols(2 * BN);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  SplitCtl& s = *reinterpret_cast<SplitCtl*>(ring + stages * kStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int a0 = (blockIdx.x / splits) * kTileM;  // first row of the tile's 128 side
+  const int b0 = blockIdx.y * BN;                 // ... of its BN side
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / splits);
+  const int nkb = kb1 - kb0;
+
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_b);
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.tfull[i], 1);
+      mbar_init(&s.tempty[i], 4);
+    }
+    s.abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc<1>(&s.tmem_base, kCols);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0, filled = 0;
+      uint32_t phase = 0;
+      bool aborted = false;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&s.empty[stage], phase ^ 1u, wc)) {
+          aborted = true;
+          break;
+        }
+        uint8_t* sa = ring + stage * kStage;
+        uint8_t* sb = sa + kATile;
+        uint64_t* bar = &s.full[stage];
+        mbar_arrive_expect_tx(bar, kStage);
+        const int k0 = kb * kBlockK;
+        if constexpr (AMN) {
+          tma_load_2d(sa, &map_a, bar, a0, k0);
+          tma_load_2d(sa + kChunk, &map_a, bar, a0 + 64, k0);
+        } else {
+          tma_load_2d(sa, &map_a, bar, k0, a0);
+        }
+        if constexpr (BMN) {
+#pragma unroll
+          for (int j = 0; j < BN / 64; ++j) tma_load_2d(sb + j * kChunk, &map_b, bar, b0 + 64 * j, k0);
+        } else {
+          tma_load_2d(sb, &map_b, bar, k0, b0);
+        }
+        ++filled;
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (aborted) {  // copies in flight land before the CTA goes on
+        for (int i = 0; i < stages; ++i) {
+          const int f = filled > i ? (filled - i + stages - 1) / stages : 0;
+          if (f > 0) (void)mbar_wait_drain(&s.full[i], (f - 1) & 1, 100000000ull);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    const uint32_t idesc = dense_idesc(kTileM, BN, AMN, BMN, p.type == MOE_BF16 ? 1u : 0u);
+    int stage = 0, done = 0;
+    uint32_t phase = 0;
+    bool aborted = false;
+    for (int i = 0; i < nkb && !aborted; ++i) {
+      const int chunk = i / chunk_blocks, slot = chunk & 1;
+      const bool fresh = i % chunk_blocks == 0;
+      if (fresh && chunk >= 2 &&
+          !__all_sync(0xffffffffu, mbar_wait(&s.tempty[slot], ((chunk >> 1) - 1) & 1, wc))) {
+        aborted = true;
+        break;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&s.full[stage], phase, wc))) {
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t a = smem_u32(ring + stage * kStage), b = a + kATile;
+#pragma unroll
+        for (int kk = 0; kk < kBlockK / kMmaK; ++kk) {
+          const uint64_t ad = AMN ? smem_desc_sw128(a + kk * 2048, kChunk, 1024)
+                                  : smem_desc_sw128(a + kk * 32, 16, 1024);
+          const uint64_t bd = BMN ? smem_desc_sw128(b + kk * 2048, kChunk, 1024)
+                                  : smem_desc_sw128(b + kk * 32, 16, 1024);
+          umma_bf16<1>(tmem + slot * BN, ad, bd, idesc, (fresh && kk == 0) ? 0u : 1u);
+        }
+        umma_commit<1>(&s.empty[stage]);
+        if (i + 1 == nkb || (i + 1) % chunk_blocks == 0) umma_commit<1>(&s.tfull[slot]);
+      }
+      __syncwarp();
+      ++done;
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (aborted && done > 0) {  // issued products end before TMEM is freed
+      const int last = (done - 1) % stages;
+      (void)mbar_wait_drain(&s.empty[last], ((done - last + stages - 1) / stages - 1) & 1, 100000000ull);
+    }
+  } else {
+    // drain the accumulators into registers, chunk by chunk
+    const int q = warp & 3;  // TMEM lane quarter of this warp
+    const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    float acc[BN];
+#pragma unroll
+    for (int j = 0; j < BN; ++j) acc[j] = 0.0f;
+    const int chunks = (nkb + chunk_blocks - 1) / chunk_blocks;
+    bool ok = true;
+    for (int c = 0; c < chunks; ++c) {
+      const int slot = c & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(&s.tfull[slot], (c >> 1) & 1, wc));
+      if (!ok) break;
+      tc_fence_after();
+      if constexpr (BN >= 32) {
+#pragma unroll
+        for (int j = 0; j < BN; j += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tq + slot * BN + j, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) acc[j + e] += __uint_as_float(v[e]);
+        }
+      } else {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(tq + slot * BN, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] += __uint_as_float(v[e]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.tempty[slot]);
+    }
+    // every product has read its operands: the ring now holds the partial
+    // tile, in the output's orientation
+    if (ok) {
+      float* part = reinterpret_cast<float*>(ring);
+      const int r = q * 32 + lane;
+      if constexpr (SWAP) {
+#pragma unroll
+        for (int j = 0; j < BN; ++j) part[j * (kTileM + 4) + r] = acc[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < BN; j += 4)
+          *reinterpret_cast<float4*>(part + r * (BN + 4) + j) =
+              make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+      }
+    }
+  }
+  __syncwarp();
+  if (splits > 1) cluster_sync();
+  else __syncthreads();
+
+  // this CTA's rows of the tile: the sum over the partials, and the epilogue
+  constexpr int kRows = SWAP ? BN : kTileM, kColsOut = SWAP ? kTileM : BN, kLd = kColsOut + 4;
+  const int64_t row0 = SWAP ? b0 : a0, col0 = SWAP ? a0 : b0;
+  const int r0 = kRows * rank / splits, r1 = kRows * (rank + 1) / splits;
+  const uint32_t base = smem_u32(ring);
+  for (int i = threadIdx.x; i < (r1 - r0) * (kColsOut / 4); i += kSplitThreads) {
+    const int r = r0 + i / (kColsOut / 4), cc = (i % (kColsOut / 4)) * 4;
+    const int64_t row = row0 + r, col = col0 + cc;
+    if (row >= p.M || col >= p.N) continue;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t at = base + static_cast<uint32_t>(r * kLd + cc) * 4;
+    if (splits > 1) {
+#pragma unroll 8
+      for (int q = 0; q < splits; ++q) {
+        const float4 f = ld_cluster_f4(mapa_shared(at, q));
+        v[0] += f.x;
+        v[1] += f.y;
+        v[2] += f.z;
+        v[3] += f.w;
+      }
+    } else {
+      const float4 f = *reinterpret_cast<const float4*>(ring + (at - base));
+      v[0] = f.x;
+      v[1] = f.y;
+      v[2] = f.z;
+      v[3] = f.w;
+    }
+    epilogue4_any(v, row, col, p);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (splits > 1) cluster_sync();  // the others have read this CTA's partial tile
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, kCols);
+  }
+}
+
+// ------------------------------------------------------------- host side
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// 16-bit matrix [outer][inner] with `ld` elements between rows, in boxes of
+// box_inner x box_outer; what lies outside reads as zero.
+bool map2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
+           uint32_t box_inner, uint32_t box_outer) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {ld * 2};
+  const cuuint32_t box[2] = {box_inner, box_outer}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <class K>
+cudaError_t allow_smem(K kern, std::atomic<bool> (&set)[64], int bytes) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!set[dev].load(std::memory_order_acquire)) {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err != cudaSuccess) return err;
+    set[dev].store(true, std::memory_order_release);
+  }
+  return cudaSuccess;
+}
+
+DenseParams make_params(const DenseCall& c) {
+  DenseParams p{};
+  p.bias = c.bias;
+  p.res = c.res;
+  p.c = c.c;
+  p.z = c.z;
+  p.ldres = c.ldres;
+  p.ldc = c.ldc;
+  p.ldz = c.ldz;
+  p.M = c.M;
+  p.N = c.N;
+  p.kblocks = static_cast<int>(cdiv(c.Kred, kBlockK));
+  p.type = c.type;
+  p.out_type = c.out_type;
+  p.act = c.act;
+  p.status = c.dev_status;
+  p.limit_ns = kDefaultWaitLimitNs;
+  return p;
+}
+
+template <int BN, bool AMN, bool BMN, bool SWAP>
+cudaError_t launch_split(const DenseCall& c, int splits, int per_sm, cudaStream_t s) {
+  auto kern = dense_split_kernel<BN, AMN, BMN, SWAP>;
+  static std::atomic<bool> attr_set[64];
+  cudaError_t err = allow_smem(kern, attr_set, kSplitSmemLimit);
+  if (err != cudaSuccess) return err;
+  const DenseParams p = make_params(c);
+  // the 128 side is A's rows; swapped, that is the output's columns
+  const void* a = SWAP ? c.b : c.a;
+  const void* b = SWAP ? c.a : c.b;
+  const int64_t lda = SWAP ? c.ldb : c.lda, ldb = SWAP ? c.lda : c.ldb;
+  const int64_t na = SWAP ? c.N : c.M, nb = SWAP ? c.M : c.N;
+  CUtensorMap ma, mb;
+  const bool ok = (AMN ? map2d(&ma, a, na, c.Kred, lda, 64, kBlockK)
+                       : map2d(&ma, a, c.Kred, na, lda, kBlockK, kTileM)) &&
+                  (BMN ? map2d(&mb, b, nb, c.Kred, ldb, 64, kBlockK)
+                       : map2d(&mb, b, c.Kred, nb, ldb, kBlockK, BN));
+  if (!ok) return cudaErrorInvalidValue;
+  constexpr int kStage = split_stage_bytes(BN);
+  constexpr int kPart = split_partial_bytes(BN, SWAP);
+  // no more stages than reduction blocks, no fewer than the partial tile
+  // needs, and enough that the CTAs of an SM never ask for more than its
+  // 512 tensor-memory columns
+  constexpr int kFloorBytes = 228 * 1024 / (512 / tmem_cols(2 * BN) + 1) + 1024;
+  constexpr int kLeast = std::max({2, (kPart + kStage - 1) / kStage, (kFloorBytes + kStage - 1) / kStage});
+  const int budget = (kSplitSmemLimit / per_sm) - 2048 - static_cast<int>(sizeof(SplitCtl));
+  const int mine = static_cast<int>(cdiv(p.kblocks, splits));
+  int stages = std::min({budget / kStage, kSplitMaxStages, std::max(mine, 2)});
+  stages = std::max(stages, kLeast);
+  static_assert(kLeast <= kSplitMaxStages, "stages");
+  static_assert(kLeast * kStage + 1024 + static_cast<int>(sizeof(SplitCtl)) <= kSplitSmemLimit, "shared memory");
+  const size_t bytes = 1024 + static_cast<size_t>(stages) * kStage + sizeof(SplitCtl);
+  const int chunk = c.out_type == MOE_FP32 ? kChunkBlocks : p.kblocks;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(na, kTileM) * splits), static_cast<unsigned>(cdiv(nb, BN)), 1);
+  cfg.blockDim = dim3(kSplitThreads, 1, 1);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = splits > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, p, stages, splits, chunk);
+}
+
+// The splits of the reduction (1, 2, 4 or 8) for `tiles` tiles: as many as
+// the SMs take in one wave of one CTA each, with at least two reduction
+// blocks for each.
+int pick_splits(int64_t tiles, int64_t kblocks) {
+  int s = 1;
+  while (s < 8 && tiles * (s * 2) <= sm_count() && kblocks >= 4 * s) s *= 2;
+  return s;
+}
+
+}  // namespace
+
+cudaError_t launch_dense(const DenseCall& c, cudaStream_t s) {
+  const int64_t kb = cdiv(c.Kred, kBlockK);
+  // few rows: the weights' columns on the 128 side (wgrads have none: their
+  // rows are a weight axis too)
+  if (!c.a_mn && c.M <= 64) {
+    const int splits = pick_splits(cdiv(c.N, kTileM), kb);
+    if (c.M <= 16)
+      return c.b_mn ? launch_split<16, true, false, true>(c, splits, 1, s)
+                    : launch_split<16, false, false, true>(c, splits, 1, s);
+    if (c.M <= 32)
+      return c.b_mn ? launch_split<32, true, false, true>(c, splits, 1, s)
+                    : launch_split<32, false, false, true>(c, splits, 1, s);
+    return c.b_mn ? launch_split<64, true, false, true>(c, splits, 1, s)
+                  : launch_split<64, false, false, true>(c, splits, 1, s);
+  }
+  const int splits = pick_splits(cdiv(c.M, kTileM) * cdiv(c.N, 128), kb);
+  if (c.a_mn) return launch_split<128, true, true, false>(c, splits, 2, s);
+  if (c.b_mn) return launch_split<128, false, true, false>(c, splits, 2, s);
+  return launch_split<128, false, false, false>(c, splits, 2, s);
+}
+
+}  // namespace moe
