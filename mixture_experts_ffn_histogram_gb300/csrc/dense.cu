@@ -14,7 +14,16 @@
 // rows the roles of the operands are swapped (SWAP): the weights' columns are
 // the tile's 128 side and the rows its narrow side, so that a handful of rows
 // costs a 16-column MMA and the weights are read once by all SMs together.
-// For fp32 results the accumulators are drained into registers every
+// pair kernel: persistent, for products with enough 256 x 256 tiles for the
+// SMs.  The CTA pair of a 2-CTA cluster works on one tile: each CTA loads its
+// 128 rows of A and its 128 columns of B, the even CTA issues
+// tcgen05.mma.cta_group::2 (M = 256, N = 256), and each CTA's tensor memory
+// holds its 128 rows twice (the next tile's products overlap the epilogue).
+// Eight epilogue warps take a quarter of the rows and half of the columns
+// each; results, z and the residual move through swizzled shared-memory
+// buffers by TMA, the residual of the next tile while its products run.
+//
+// In the split kernel, for fp32 results the accumulators are drained into registers every
 // kChunkBlocks reduction blocks: the tensor core's additions truncate, and a
 // long chain of them would lose what an fp32 result is asked for.
 #include <cuda.h>
@@ -361,6 +370,358 @@ __global__ void __launch_bounds__(kSplitThreads)
   }
 }
 
+// ------------------------------------------------------------ pair kernel
+constexpr int kPairN = 256;
+constexpr int kPairStages = 5;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kPairStage = 2 * kATile;          // per CTA: 128 A rows, 128 B columns
+constexpr int kPairBuf = 32 * 128;              // 32 rows x 64 columns, 16-bit
+constexpr int kPairBufs = 2;                    // per epilogue warp
+
+struct PairCtl {
+  uint64_t full[kPairStages];
+  uint64_t empty[kPairStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t rbar[kPairEpiWarps][kPairBufs];  // a residual chunk landed in the buffer
+  uint32_t tmem_base;
+  int abort_flag;
+};
+constexpr size_t kPairSmem = 1024 + static_cast<size_t>(kPairStages) * kPairStage +
+                             kPairEpiWarps * kPairBufs * kPairBuf + sizeof(PairCtl);
+static_assert(kPairSmem <= 227 * 1024, "shared memory");
+
+struct PairParams {
+  const float* bias;
+  int64_t M, N;
+  int kblocks, m_tiles, n_tiles, act;
+  int a_chunks, b_chunks;  // MN-major operands: one box of two 64-wide chunks (3-D map)
+  int has_res, has_z;
+  uint32_t idesc;
+  int32_t* status;
+  uint64_t limit_ns;
+};
+
+template <int ACT>
+__device__ __forceinline__ void act32(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = act_value<false>(v[i], ACT);
+}
+__device__ __forceinline__ void act32_any(float (&v)[32], int act) {
+  switch (act) {
+    case MOE_ACT_RELU: act32<MOE_ACT_RELU>(v); break;
+    case MOE_ACT_GELU: act32<MOE_ACT_GELU>(v); break;
+    case MOE_ACT_GELU_TANH: act32<MOE_ACT_GELU_TANH>(v); break;
+    case MOE_ACT_SILU: act32<MOE_ACT_SILU>(v); break;
+    default: break;
+  }
+}
+
+// Half h (32 columns) of row `lane` of a 128-byte-swizzled buffer.
+__device__ __forceinline__ uint4* buf_unit(uint8_t* buf, int lane, int h, int j) {
+  return reinterpret_cast<uint4*>(buf + lane * 128 + (((h * 4 + j) ^ (lane & 7)) << 4));
+}
+template <typename T>
+__device__ __forceinline__ void put32(uint8_t* buf, int lane, int h, const float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float* f = v + 8 * j;
+    *buf_unit(buf, lane, h, j) = make_uint4(pack_pair(f[0], f[1], T{}), pack_pair(f[2], f[3], T{}),
+                                            pack_pair(f[4], f[5], T{}), pack_pair(f[6], f[7], T{}));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void add32(uint8_t* buf, int lane, int h, float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 q = *buf_unit(buf, lane, h, j);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack_pair(w[i], T{});
+      v[8 * j + 2 * i] += f.x;
+      v[8 * j + 2 * i + 1] += f.y;
+    }
+  }
+}
+
+// One operand's share of a stage: 128 rows (K-major), or two 64-wide chunks.
+template <bool MN>
+__device__ __forceinline__ void pair_load(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int x0,
+                                          int k0, int chunked) {
+  if constexpr (!MN) {
+    tma_load_2d_pair(dst, map, bar, k0, x0);
+  } else if (chunked) {
+    tma_load_3d_pair(dst, map, bar, 0, k0, x0 / 64);
+  } else {
+    tma_load_2d_pair(dst, map, bar, x0, k0);
+    tma_load_2d_pair(dst + kChunk, map, bar, x0 + 64, k0);
+  }
+}
+
+// FULL: bias, activation and z (the forward); otherwise only a residual.
+template <typename T, bool AMN, bool BMN, bool FULL>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    dense_pair_kernel(const __grid_constant__ CUtensorMap map_a,
+                      const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ CUtensorMap map_c,
+                      const __grid_constant__ CUtensorMap map_r,
+                      const __grid_constant__ CUtensorMap map_z, const PairParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* epi = ring + kPairStages * kPairStage;
+  PairCtl& s = *reinterpret_cast<PairCtl*>(epi + kPairEpiWarps * kPairBufs * kPairBuf);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool leader = rank == 0;
+  const int units = gridDim.x / 2;
+  const int ntiles = p.m_tiles * p.n_tiles;
+
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_b);
+    tma_prefetch_map(&map_c);
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.tfull[i], 1);
+      mbar_init(&s.tempty[i], 2 * kPairEpiWarps);
+    }
+    for (int i = 0; i < kPairEpiWarps; ++i)
+      for (int j = 0; j < kPairBufs; ++j) mbar_init(&s.rbar[i][j], 1);
+    s.abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc<2>(&s.tmem_base, 512);
+    tmem_relinquish<2>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers exist before any remote arrive
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
+
+  if (warp == 0) {
+    // producer: this CTA's operands; both CTAs' bytes complete on the even
+    // CTA's barrier
+    if (lane == 0) {
+      int stage = 0, filled = 0;
+      uint32_t phase = 0;
+      const uint32_t full0 = mapa_shared(smem_u32(&s.full[0]), 0);
+      bool aborted = false;
+      for (int t = blockIdx.x / 2; t < ntiles && !aborted; t += units) {
+        const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
+        const int a0 = mt * 256 + 128 * rank, b0 = nt * kPairN + 128 * rank;
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!mbar_wait(&s.empty[stage], phase ^ 1u, wc)) {
+            aborted = true;
+            break;
+          }
+          uint8_t* sa = ring + stage * kPairStage;
+          if (leader) mbar_arrive_expect_tx(&s.full[stage], 2 * kPairStage);
+          const uint32_t bar = full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
+          pair_load<AMN>(sa, &map_a, bar, a0, kb * kBlockK, p.a_chunks);
+          pair_load<BMN>(sa + kATile, &map_b, bar, b0, kb * kBlockK, p.b_chunks);
+          ++filled;
+          if (++stage == kPairStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (aborted && leader) {  // copies in flight land before the CTA exits
+        for (int i = 0; i < kPairStages; ++i) {
+          const int f = filled > i ? (filled - i + kPairStages - 1) / kPairStages : 0;
+          if (f > 0) (void)mbar_wait_drain(&s.full[i], (f - 1) & 1, 100000000ull);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      int stage = 0, done = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool aborted = false;
+      for (int t = blockIdx.x / 2; t < ntiles && !aborted; t += units) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&s.tempty[acc], acc_phase ^ 1u, wc))) {
+          aborted = true;
+          break;
+        }
+        tc_fence_after();
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!__all_sync(0xffffffffu, mbar_wait_cluster(&s.full[stage], phase, wc))) {
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t a = smem_u32(ring + stage * kPairStage), b = a + kATile;
+#pragma unroll
+            for (int kk = 0; kk < kBlockK / kMmaK; ++kk) {
+              const uint64_t ad = AMN ? smem_desc_sw128(a + kk * 2048, kChunk, 1024)
+                                      : smem_desc_sw128(a + kk * 32, 16, 1024);
+              const uint64_t bd = BMN ? smem_desc_sw128(b + kk * 2048, kChunk, 1024)
+                                      : smem_desc_sw128(b + kk * 32, 16, 1024);
+              umma_bf16<2>(tmem + acc * kPairN, ad, bd, p.idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+            }
+            umma_commit<2>(&s.empty[stage]);
+            if (kb + 1 == p.kblocks) umma_commit<2>(&s.tfull[acc]);
+          }
+          __syncwarp();
+          ++done;
+          if (++stage == kPairStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (aborted && done > 0) {  // issued products end before TMEM is freed
+        const int last = (done - 1) % kPairStages;
+        (void)mbar_wait_drain(&s.empty[last], ((done - last + kPairStages - 1) / kPairStages - 1) & 1,
+                              100000000ull);
+      }
+    }
+  } else {
+    // epilogue: rows 32 q.. of this CTA's 128, columns 128 half.. of the tile's 256
+    const int ew = warp - 2, q = warp & 3, half = ew >> 2;
+    uint8_t* bufs = epi + ew * kPairBufs * kPairBuf;
+    uint64_t* rbar = s.rbar[ew];
+    const uint32_t tempty_peer = mapa_shared(smem_u32(&s.tempty[0]), 0);
+    uint32_t rphase = 0;  // bit b: parity of buffer b's next residual
+    int pending = 0;      // bit b: a residual load into buffer b is in flight
+    uint32_t stored = 0;  // chunks stored so far
+    // without z both buffers hold results; with z buffer 1 stages z, and a
+    // chunk's residual can only be fetched when the one before is stored
+    const bool with_z = FULL && p.has_z;
+    auto fetch_res = [&](int y, int64_t col, int b) {
+      if (y >= p.M || col >= p.N) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&rbar[b], kPairBuf);
+        tma_load_2d(bufs + b * kPairBuf, &map_r, &rbar[b], static_cast<int>(col), y);
+      }
+      pending |= 1 << b;
+    };
+    auto prefetch_tile = [&](int t) {
+      if (!p.has_res || t >= ntiles) return;
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+      const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
+      const int y = mt * 256 + 128 * rank + 32 * q;
+      const int64_t col = static_cast<int64_t>(nt) * kPairN + 128 * half;
+      fetch_res(y, col, 0);
+      if (!with_z) fetch_res(y, col + 64, 1);
+    };
+    prefetch_tile(blockIdx.x / 2);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x / 2; t < ntiles; t += units) {
+      const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
+      const int y = mt * 256 + 128 * rank + 32 * q;
+      const int64_t col0 = static_cast<int64_t>(nt) * kPairN + 128 * half;
+      ok = __all_sync(0xffffffffu, mbar_wait(&s.tfull[acc], acc_phase, wc));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem + acc * kPairN + 128 * half + (static_cast<uint32_t>(q * 32) << 16);
+      if (y < p.M) {
+#pragma unroll 1
+        for (int ch = 0; ch < 2; ++ch) {
+          const int64_t col = col0 + 64 * ch;
+          if (col >= p.N) break;
+          // residuals were fetched into buffer ch; results alone alternate
+          const int b = with_z ? 0 : (p.has_res ? ch : (stored & 1));
+          uint8_t* buf = bufs + b * kPairBuf;
+          uint8_t* zbuf = bufs + kPairBuf;
+          if (p.has_res) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&rbar[b], (rphase >> b) & 1u, wc));
+            if (!ok) break;
+            rphase ^= 1u << b;
+            pending &= ~(1 << b);
+          } else if (!with_z) {
+            // the buffer's last store has read it; the one since may be pending
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+          } else {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t raw[32];
+            float v[32];
+            tmem_ld_32x32b_x32(tbase + 64 * ch + 32 * h, raw);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+            if constexpr (FULL) {
+              if (p.bias != nullptr) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const int64_t c4 = col + 32 * h + 4 * i;
+                  if (c4 < p.N) {
+                    const float4 f = __ldg(reinterpret_cast<const float4*>(p.bias + c4));
+                    v[4 * i] += f.x;
+                    v[4 * i + 1] += f.y;
+                    v[4 * i + 2] += f.z;
+                    v[4 * i + 3] += f.w;
+                  }
+                }
+              }
+              if (with_z) put32<T>(zbuf, lane, h, v);
+              act32_any(v, p.act);
+            }
+            if (p.has_res) add32<T>(buf, lane, h, v);
+            put32<T>(buf, lane, h, v);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&map_c, buf, static_cast<int>(col), y);
+            if (with_z) tma_store_2d(&map_z, zbuf, static_cast<int>(col), y);
+            bulk_commit();
+          }
+          ++stored;
+          if (with_z && p.has_res && ch == 0) {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+            fetch_res(y, col + 64, 0);
+          }
+        }
+      }
+      if (!ok) break;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(&s.tempty[acc]);
+        else mbar_arrive_remote(tempty_peer + acc * static_cast<uint32_t>(sizeof(uint64_t)));
+      }
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+      prefetch_tile(t + units);
+    }
+    // residuals in flight land (an abort left them), every store is done
+    for (int b = 0; b < kPairBufs; ++b)
+      if ((pending >> b) & 1) (void)mbar_wait_drain(&rbar[b], (rphase >> b) & 1u, 100000000ull);
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs are done with each other's memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<2>(tmem, 512);
+  }
+}
+
 // ------------------------------------------------------------- host side
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -391,6 +752,19 @@ bool map2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uin
   const cuuint64_t strides[1] = {ld * 2};
   const cuuint32_t box[2] = {box_inner, box_outer}, es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An MN-major operand [rows][inner] (inner a multiple of 64) as
+// [inner / 64][rows][64]: one box brings two 64-wide chunks of 64 rows.
+bool map_chunks(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {64, rows, inner / 64};
+  const cuuint64_t strides[2] = {ld * 2, 128};
+  const cuuint32_t box[3] = {64, kBlockK, 2}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -479,6 +853,71 @@ cudaError_t launch_split(const DenseCall& c, int splits, int per_sm, cudaStream_
   return cudaLaunchKernelEx(&cfg, kern, ma, mb, p, stages, splits, chunk);
 }
 
+template <bool MN>
+bool pair_operand(CUtensorMap* m, const void* base, int64_t outer, int64_t Kred, int64_t ld) {
+  if (!MN) return map2d(m, base, Kred, outer, ld, kBlockK, 128);
+  return outer % 64 == 0 ? map_chunks(m, base, outer, Kred, ld) : map2d(m, base, outer, Kred, ld, 64, kBlockK);
+}
+
+template <typename T, bool AMN, bool BMN, bool FULL>
+cudaError_t launch_pair(const DenseCall& c, cudaStream_t s) {
+  auto kern = dense_pair_kernel<T, AMN, BMN, FULL>;
+  static std::atomic<bool> attr_set[64];
+  cudaError_t err = allow_smem(kern, attr_set, static_cast<int>(kPairSmem));
+  if (err != cudaSuccess) return err;
+  PairParams p{};
+  p.bias = c.bias;
+  p.M = c.M;
+  p.N = c.N;
+  p.kblocks = static_cast<int>(cdiv(c.Kred, kBlockK));
+  p.m_tiles = static_cast<int>(cdiv(c.M, 256));
+  p.n_tiles = static_cast<int>(cdiv(c.N, kPairN));
+  p.act = c.act;
+  p.a_chunks = AMN && c.M % 64 == 0;
+  p.b_chunks = BMN && c.N % 64 == 0;
+  p.has_res = c.res != nullptr;
+  p.has_z = c.z != nullptr;
+  p.idesc = dense_idesc(256, kPairN, AMN, BMN, c.type == MOE_BF16 ? 1u : 0u);
+  p.status = c.dev_status;
+  p.limit_ns = kDefaultWaitLimitNs;
+  CUtensorMap ma, mb, mc, mr, mz;
+  bool ok = pair_operand<AMN>(&ma, c.a, c.M, c.Kred, c.lda) &&
+            pair_operand<BMN>(&mb, c.b, c.N, c.Kred, c.ldb) && map2d(&mc, c.c, c.N, c.M, c.ldc, 64, 32);
+  mr = mz = mc;
+  if (ok && p.has_res) ok = map2d(&mr, c.res, c.N, c.M, c.ldres, 64, 32);
+  if (ok && p.has_z) ok = map2d(&mz, c.z, c.N, c.M, c.ldz, 64, 32);
+  if (!ok) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kPairThreads, 1, 1);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // pairs that can be resident at once (one CTA per SM), cached per kernel
+  static int max_pairs = 0;
+  static std::once_flag once;
+  std::call_once(once, [&] {
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (sm_count() / 2)), 1, 1);
+    int n = 0;
+    max_pairs = (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0) ? n : sm_count() / 2;
+  });
+  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, max_pairs)), 1, 1);
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, mr, mz, p);
+}
+
+template <typename T>
+cudaError_t launch_pair_type(const DenseCall& c, cudaStream_t s) {
+  if (c.a_mn) return launch_pair<T, true, true, false>(c, s);
+  if (c.b_mn) return launch_pair<T, false, true, true>(c, s);
+  return launch_pair<T, false, false, false>(c, s);
+}
+
 // The splits of the reduction (1, 2, 4 or 8) for `tiles` tiles: as many as
 // the SMs take in one wave of one CTA each, with at least two reduction
 // blocks for each.
@@ -505,6 +944,9 @@ cudaError_t launch_dense(const DenseCall& c, cudaStream_t s) {
     return c.b_mn ? launch_split<64, true, false, true>(c, splits, 1, s)
                   : launch_split<64, false, false, true>(c, splits, 1, s);
   }
+  const int64_t pair_tiles = cdiv(c.M, 256) * cdiv(c.N, kPairN);
+  if (c.out_type != MOE_FP32 && 3 * pair_tiles >= sm_count())
+    return c.type == MOE_BF16 ? launch_pair_type<__nv_bfloat16>(c, s) : launch_pair_type<__half>(c, s);
   const int splits = pick_splits(cdiv(c.M, kTileM) * cdiv(c.N, 128), kb);
   if (c.a_mn) return launch_split<128, true, true, false>(c, splits, 2, s);
   if (c.b_mn) return launch_split<128, false, true, false>(c, splits, 2, s);
