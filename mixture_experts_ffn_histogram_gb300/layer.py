@@ -18,25 +18,59 @@ from . import binding as B
 from .block import MoEBlock
 
 
-def _check(name, t, shape, dtype, device):
-    """A tensor of another shape, type or device would be read (or written)
-    out of bounds or misread: reject it before any launch."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
-        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}, got {t.dtype} "
-                         f"{list(t.shape)} on {t.device}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} needs contiguous columns, got strides {list(t.stride())}")
+class _Arg:
+    """One tensor argument of an operator: its type, device and (where fixed)
+    shape, checked on every call before anything is launched, since a tensor
+    of another shape would be read or written out of bounds."""
+
+    __slots__ = ("name", "dtype", "device", "index", "shape", "mat", "contiguous")
+
+    def __init__(self, name, dtype, device, shape=None, contiguous=False):
+        self.name, self.dtype, self.device, self.shape = name, dtype, device, shape
+        self.index = device.index if device.type == "cuda" else -1
+        self.mat = B.MoeMat(None, 0)
+        self.contiguous = contiguous
+
+    def refuse(self, t, shape):
+        raise ValueError(f"{self.name} must be {self.dtype} {list(shape)} with contiguous "
+                         f"{'elements' if self.contiguous else 'columns'} on {self.device}, got "
+                         f"{t.dtype} {list(t.shape)}, strides {list(t.stride())} on {t.device}")
+
+    def rows(self, t, cap, width):
+        """The number of rows of the call, from its first matrix."""
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != width or shape[0] > cap:
+            self.refuse(t, (f"<= {cap}", width))
+        return shape[0]
+
+    def matrix(self, t, shape):
+        """A 2-D tensor as a MoeMat (of this argument: valid until its next call)."""
+        if t.dtype is not self.dtype or t.shape != shape or t.get_device() != self.index:
+            self.refuse(t, shape)
+        ld, inner = t.stride()
+        if inner != 1 and shape[1] > 1:
+            self.refuse(t, shape)
+        m = self.mat
+        m.p = t.data_ptr()
+        m.ld = ld if shape[0] > 1 else (shape[1] + 7) // 8 * 8
+        return m
+
+    def pointer(self, t, shape):
+        """A contiguous tensor as its address."""
+        if (t.dtype is not self.dtype or t.shape != shape or t.get_device() != self.index
+                or not t.is_contiguous()):
+            self.refuse(t, shape)
+        return t.data_ptr()
+
+
+def _own(t):
+    """A buffer of the operator's own, as a MoeMat."""
+    return B.MoeMat(t.data_ptr(), t.stride(0))
 
 
 def _launchable(device):
     if device.type != "cuda":
         raise RuntimeError(f"the operator's buffers are on {device}: its kernels need a CUDA device")
-
-
-def _rows(name, t, cap, width):
-    if t.dim() != 2 or t.shape[1] != width or t.shape[0] > cap:
-        raise ValueError(f"{name} must be [rows <= {cap}, {width}], got {list(t.shape)}")
-    return t.shape[0]
 
 
 class LayerNorm:
@@ -53,39 +87,54 @@ class LayerNorm:
         if dtype not in B.DTYPES or weight_dtype not in (dtype, torch.float32):
             raise ValueError(f"rows of {dtype} with weights of {weight_dtype} are not supported")
         self.rows, self.D, self.dtype, self.weight_dtype = rows, D, dtype, weight_dtype
-        self.eps, self.train = eps, train
+        self.eps, self.train = float(eps), train
         dev = torch.device(device)
         self._y = torch.empty((rows, D), dtype=dtype, device=dev)
+        self.device = dev = self._y.device
         self._r = None
-        self.device = self._y.device
         self.r = self.mean = self.rstd = None
+        self._my, self._p_stats = _own(self._y), (None, None)
         if train:
             self._stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
+            self._mean, self._rstd = self._stats[0], self._stats[1]
             self._dx = torch.empty((rows, D), dtype=dtype, device=dev)
             self.dgamma = torch.empty(D, dtype=weight_dtype, device=dev)
             self.dbeta = torch.empty(D, dtype=weight_dtype, device=dev)
             self.ws = torch.empty(max(B.moe_layer_norm_workspace_bytes(rows, D), 256),
                                   dtype=torch.uint8, device=dev)
+            self._mdx = _own(self._dx)
+            self._p_stats = (self._stats.data_ptr(), self._stats.data_ptr() + 4 * rows)
+            self._p_grads = (self.dgamma.data_ptr(), self.dbeta.data_ptr(), self.ws.data_ptr())
+        self._x, self._res = _Arg("x", dtype, dev), _Arg("res", dtype, dev)
+        self._dy, self._rin, self._dres = (_Arg(n, dtype, dev) for n in ("dy", "r", "dres"))
+        self._w = {n: _Arg(n, weight_dtype, dev, contiguous=True) for n in ("gamma", "beta")}
+        self._st = {n: _Arg(n, torch.float32, dev, contiguous=True) for n in ("mean", "rstd")}
+        self._types = (B.DTYPES[dtype], B.DTYPES[weight_dtype])
 
     def forward(self, x, gamma, beta, res=None, stream=None):
-        n = _rows("x", x, self.rows, self.D)
-        dev = self.device
-        _check("x", x, x.shape, self.dtype, dev)
-        _check("gamma", gamma, (self.D,), self.weight_dtype, dev)
-        _check("beta", beta, (self.D,), self.weight_dtype, dev)
-        r = None
+        D = self.D
+        n = self._x.rows(x, self.rows, D)
+        shape = (n, D)
+        mx = self._x.matrix(x, shape)
+        pg, pb = self._w["gamma"].pointer(gamma, (D,)), self._w["beta"].pointer(beta, (D,))
+        whole = n == self.rows
+        mres = mr = None
+        r = x
         if res is not None:
-            _check("res", res, x.shape, self.dtype, dev)
+            mres = self._res.matrix(res, shape)
             if self._r is None:
                 self._r = torch.empty_like(self._y)
-            r = self._r[:n]
-        y = self._y[:n]
+                self._mr = _own(self._r)
+            r, mr = self._r if whole else self._r[:n], self._mr
+        _launchable(self.device)
+        B.moe_layer_norm(mx, mres, pg, pb, mr, self._my, *self._p_stats, self.eps, stream,
+                         (n, D, *self._types))
+        self.r = r
         if self.train:
-            self.mean, self.rstd = self._stats[0, :n], self._stats[1, :n]
-        _launchable(dev)
-        B.moe_layer_norm(x, res, gamma, beta, r, y, self.mean, self.rstd, self.eps, stream)
-        self.r = x if r is None else r
-        return y
+            self.mean, self.rstd = self._mean, self._rstd
+            if not whole:
+                self.mean, self.rstd = self._mean[:n], self._rstd[:n]
+        return self._y if whole else self._y[:n]
 
     def backward(self, dy, r, gamma, mean=None, rstd=None, dres=None, stream=None):
         if not self.train:
@@ -94,20 +143,17 @@ class LayerNorm:
         rstd = self.rstd if rstd is None else rstd
         if mean is None or rstd is None:
             raise RuntimeError("backward needs a forward first, or its mean and rstd")
-        n = _rows("dy", dy, self.rows, self.D)
-        dev = self.device
-        _check("dy", dy, dy.shape, self.dtype, dev)
-        _check("r", r, dy.shape, self.dtype, dev)
-        _check("gamma", gamma, (self.D,), self.weight_dtype, dev)
-        _check("mean", mean, (n,), torch.float32, dev)
-        _check("rstd", rstd, (n,), torch.float32, dev)
-        if dres is not None:
-            _check("dres", dres, dy.shape, self.dtype, dev)
-        dx = self._dx[:n]
-        _launchable(dev)
-        B.moe_layer_norm_bwd(dy, r, gamma, mean, rstd, dres, dx, self.dgamma, self.dbeta, self.ws,
-                             stream)
-        return dx
+        D = self.D
+        n = self._dy.rows(dy, self.rows, D)
+        shape = (n, D)
+        mdy, mrin = self._dy.matrix(dy, shape), self._rin.matrix(r, shape)
+        pg = self._w["gamma"].pointer(gamma, (D,))
+        pm, ps = self._st["mean"].pointer(mean, (n,)), self._st["rstd"].pointer(rstd, (n,))
+        mres = None if dres is None else self._dres.matrix(dres, shape)
+        _launchable(self.device)
+        B.moe_layer_norm_bwd(mdy, mrin, pg, pm, ps, mres, self._mdx, *self._p_grads, stream,
+                             (n, D, *self._types))
+        return self._dx if n == self.rows else self._dx[:n]
 
 
 class TopKRouter:
@@ -129,20 +175,29 @@ class TopKRouter:
         dev = torch.device(device)
         self._ids = torch.empty((T, K), dtype=torch.int32, device=dev)
         self._w = torch.empty((T, K), dtype=torch.float32, device=dev)
-        self.device = self._w.device
+        self.device = dev = self._w.device
+        self._p_out = (self._ids.data_ptr(), self._w.data_ptr())
         self.ids = self.w = None
         if train:
             self._dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
+            self._p_dl = self._dlogits.data_ptr()
+        f32 = torch.float32
+        self._l = _Arg("logits", f32, dev, contiguous=True)
+        self._b = _Arg("bias", f32, dev, contiguous=True)
+        self._dw = _Arg("dw", f32, dev, contiguous=True)
+        self._i = _Arg("ids", torch.int32, dev, contiguous=True)
 
     def forward(self, logits, bias=None, stream=None):
-        n = _rows("logits", logits, self.T, self.E)
-        _check("logits", logits, logits.shape, torch.float32, self.device)
-        if bias is not None:
-            _check("bias", bias, (self.E,), torch.float32, self.device)
-        self.d.T = n
-        self.ids, self.w = self._ids[:n], self._w[:n]
+        n = self._l.rows(logits, self.T, self.E)
+        pl = self._l.pointer(logits, (n, self.E))
+        pb = None if bias is None else self._b.pointer(bias, (self.E,))
         _launchable(self.device)
-        B.moe_route_topk(logits, bias, self.ids, self.w, self.d, stream)
+        self.d.T = n
+        B.moe_route_topk(pl, pb, *self._p_out, self.d, stream)
+        if n == self.T:
+            self.ids, self.w = self._ids, self._w
+        else:
+            self.ids, self.w = self._ids[:n], self._w[:n]
         return self.ids, self.w
 
     def backward(self, dw, logits, ids=None, stream=None):
@@ -151,15 +206,13 @@ class TopKRouter:
         ids = self.ids if ids is None else ids
         if ids is None:
             raise RuntimeError("backward needs a forward first, or its ids")
-        n = _rows("logits", logits, self.T, self.E)
-        _check("logits", logits, logits.shape, torch.float32, self.device)
-        _check("dw", dw, (n, self.K), torch.float32, self.device)
-        _check("ids", ids, (n, self.K), torch.int32, self.device)
-        self.d.T = n
-        out = self._dlogits[:n]
+        n = self._l.rows(logits, self.T, self.E)
+        pl = self._l.pointer(logits, (n, self.E))
+        pd, pi = self._dw.pointer(dw, (n, self.K)), self._i.pointer(ids, (n, self.K))
         _launchable(self.device)
-        B.moe_route_topk_bwd(logits, ids, dw, out, self.d, stream)
-        return out
+        self.d.T = n
+        B.moe_route_topk_bwd(pl, pi, pd, self._p_dl, self.d, stream)
+        return self._dlogits if n == self.T else self._dlogits[:n]
 
 
 class Linear:
@@ -185,60 +238,63 @@ class Linear:
         self.d = B.linear_dims(M, K, N, dtype, out_dtype, act)
         dev = torch.device(device)
         self._y = torch.empty((M, N), dtype=out_dtype, device=dev)
-        self.device = self._y.device
+        self.device = dev = self._y.device
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.z = None
-        self._z = None
+        self.z = self._z = self._mz = None
+        self._my, self._p_status = _own(self._y), self.status.data_ptr()
         if train:
             if act != "none":
                 self._z = torch.empty((M, N), dtype=dtype, device=dev)
+                self._mz = _own(self._z)
             self._dx = torch.empty((M, K), dtype=dtype, device=dev)
             self.dw = torch.empty((K, N), dtype=dtype, device=dev)
             self.db = torch.empty(N, dtype=torch.float32, device=dev)
             self.ws = torch.empty(B.moe_linear_workspace_bytes(self.d), dtype=torch.uint8,
                                   device=dev)
+            self._mdx, self._mdw = _own(self._dx), _own(self.dw)
+            self._p_db, self._p_ws = self.db.data_ptr(), self.ws.data_ptr()
+        self._x, self._w = _Arg("x", dtype, dev), _Arg("w", dtype, dev)
+        self._b = _Arg("bias", torch.float32, dev, contiguous=True)
+        self._res, self._dy = _Arg("res", out_dtype, dev), _Arg("dy", out_dtype, dev)
+        self._zin, self._add = _Arg("z", dtype, dev), _Arg("dx_add", dtype, dev)
 
     def forward(self, x, w, bias=None, res=None, stream=None):
-        n = _rows("x", x, self.M, self.K)
-        dev = self.device
-        _check("x", x, x.shape, self.dtype, dev)
-        _check("w", w, (self.K, self.N), self.dtype, dev)
-        if bias is not None:
-            _check("bias", bias, (self.N,), torch.float32, dev)
-        if res is not None:
-            _check("res", res, (n, self.N), self.out_dtype, dev)
+        K, N = self.K, self.N
+        n = self._x.rows(x, self.M, K)
+        mx, mw = self._x.matrix(x, (n, K)), self._w.matrix(w, (K, N))
+        pb = None if bias is None else self._b.pointer(bias, (N,))
+        mres = None if res is None else self._res.matrix(res, (n, N))
+        _launchable(self.device)
         self.d.M = n
-        y = self._y[:n]
+        B.moe_linear(mx, mw, pb, mres, self._my, self._mz, self._p_status, self.d, stream)
+        whole = n == self.M
         if self._z is not None:
-            self.z = self._z[:n]
-        _launchable(dev)
-        B.moe_linear(x, w, bias, res, y, self.z, self.status, self.d, stream)
-        return y
+            self.z = self._z if whole else self._z[:n]
+        return self._y if whole else self._y[:n]
 
     def backward(self, dy, x, w, z=None, dx_add=None, need_dx=True, need_dw=True, need_db=True,
                  stream=None):
         if not self.train:
             raise RuntimeError("the linear layer was built without train=True")
-        n = _rows("x", x, self.M, self.K)
-        dev = self.device
-        _check("dy", dy, (n, self.N), self.out_dtype, dev)
-        _check("x", x, x.shape, self.dtype, dev)
-        _check("w", w, (self.K, self.N), self.dtype, dev)
+        K, N = self.K, self.N
+        n = self._x.rows(x, self.M, K)
+        mdy = self._dy.matrix(dy, (n, N))
+        mx, mw = self._x.matrix(x, (n, K)), self._w.matrix(w, (K, N))
+        mz = None
         if self.act != "none":
             z = self.z if z is None else z
             if z is None:
                 raise RuntimeError("backward needs a forward first, or its z")
-            _check("z", z, (n, self.N), self.dtype, dev)
-        else:
-            z = None
-        if dx_add is not None:
-            _check("dx_add", dx_add, x.shape, self.dtype, dev)
+            mz = self._zin.matrix(z, (n, N))
+        madd = None if dx_add is None else self._add.matrix(dx_add, (n, K))
+        _launchable(self.device)
         self.d.M = n
-        dx = self._dx[:n] if need_dx else None
-        _launchable(dev)
-        B.moe_linear_bwd(dy, z, x, w, dx_add, dx, self.dw if need_dw else None,
-                         self.db if need_db else None, self.status, self.ws, self.d, stream)
-        return dx
+        B.moe_linear_bwd(mdy, mz, mx, mw, madd, self._mdx if need_dx else None,
+                         self._mdw if need_dw else None, self._p_db if need_db else None,
+                         self._p_status, self._p_ws, self.d, stream)
+        if not need_dx:
+            return None
+        return self._dx if n == self.M else self._dx[:n]
 
 
 class MoELayer:
