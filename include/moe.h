@@ -611,7 +611,9 @@ typedef struct {
  * all masked gets the lowest ids with weights 0.  bias must be finite.
  * moe_route_histogram in mode MOE_SCORE_GIVEN takes ids and w from here.
  *   logits fp32 [T,E];  bias fp32 [E] or NULL;  ids int32 [T,K] out;
- *   w fp32 [T,K] out.  K <= top_groups * (E / groups), E % groups == 0.
+ *   w fp32 [T,K] out.  K <= top_groups * (E / groups), E % groups == 0, and a
+ *   group has at most 32 * floor(32 / groups) experts when top_groups < groups
+ *   (any E up to 1024 for 2, 4, 8, 16 or 32 groups).
  */
 moe_status moe_route_topk(const float* logits, const float* bias, int32_t* ids, float* w,
                           moe_topk_dims d, cudaStream_t stream);

@@ -36,6 +36,16 @@ cudaError_t launch_layer_norm_bwd(const NormCall& c, cudaStream_t s);
 cudaError_t launch_join_partials(const float* partials, int P, int64_t C, int64_t split, void* out0,
                                  void* out1, moe_dtype type, cudaStream_t s);
 
+// The selection kernel gives every group of experts its own lanes of a warp:
+// the largest power of two of lanes that divides the group, or all that there
+// are when that leaves more than kTopkPerLane experts to a lane.
+constexpr int kTopkPerLane = 32;
+inline int topk_group_lanes(const moe_topk_dims& d) {
+  const int gs = d.E / d.groups, most = 32 / d.groups;
+  int lanes = 1;
+  while (lanes * 2 <= most && gs % (lanes * 2) == 0) lanes *= 2;
+  return (gs + lanes - 1) / lanes <= kTopkPerLane ? lanes : most;
+}
 cudaError_t launch_route_topk(const float* logits, const float* bias, int32_t* ids, float* w,
                               const moe_topk_dims& d, cudaStream_t s);
 cudaError_t launch_route_topk_bwd(const float* logits, const int32_t* ids, const float* dw,

@@ -42,6 +42,9 @@ moe_status check_topk(const moe_topk_dims& d) {
   if (d.groups < 1 || d.groups > 32 || d.E % d.groups != 0) return MOE_ERR_UNSUPPORTED;
   if (d.top_groups < 1 || d.top_groups > d.groups) return MOE_ERR_UNSUPPORTED;
   if (d.K > d.top_groups * (d.E / d.groups)) return MOE_ERR_UNSUPPORTED;
+  const int lanes = moe::topk_group_lanes(d);
+  if (d.top_groups < d.groups && (d.E / d.groups + lanes - 1) / lanes > moe::kTopkPerLane)
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

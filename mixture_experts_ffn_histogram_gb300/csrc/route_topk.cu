@@ -7,17 +7,21 @@
 //   w_k = scale s_k (/ sum_k s_k).
 //   backward: dlogits from dw through the weights (the selection has none).
 //
-// One warp per token, lane i holding experts [i VPL, (i+1) VPL) in registers:
-// the row is read once with 16-byte loads, and each of the K rounds takes the
-// largest key of the warp with one warp-wide maximum (the lowest lane, and in
-// it the lowest index, wins a tie, which is the lowest expert id).
+// One warp per token; a lane holds up to `vpl` neighbouring experts in
+// registers, and `lpg` lanes hold a group.  Selection without K passes over the
+// experts: the K-th largest of the lanes' maxima bounds the K-th largest
+// expert from below, so the few experts at or above it (a dozen for 8 of 256)
+// hold the answer; they are compacted to one per lane, in the order of their
+// ids, and each counts those ahead of it.  Where they do not fit a warp (K
+// near 32), K rounds take one warp-wide maximum each.
 //
 // The selection compares fp32 scores, which a rounding can swap.  Each
-// comparison that decides something (neighbours in the list, the last expert
-// taken against the first left out, the last group taken against the first
-// left out) is therefore checked against the error bound of the two scores;
-// where they lie too near, the warp selects the token again in fp64.  With
-// scores spread as in training this happens to a token in some thousands.
+// comparison that decides something is therefore checked against the error
+// bounds of its two sides: neighbours in the sorted list up to the first
+// expert left out, and the groups on both sides of the last one taken.
+// Where they lie too near, those experts (one per lane) or those groups are
+// evaluated again in fp64.  With scores spread as in training this happens
+// to a token in some thousands.
 #include <cuda.h>
 
 #include <algorithm>
@@ -63,6 +67,10 @@ __device__ __forceinline__ void merge_top2(F& a1, F& a2, F b1, F b2) {
   a1 = hi;
   a2 = lo > m2 ? lo : m2;
 }
+__device__ __forceinline__ void merge_top2(float& a1, float& a2, float b1, float b2) {
+  a2 = fmaxf(fmaxf(a2, b2), fminf(a1, b1));
+  a1 = fmaxf(a1, b1);
+}
 // A group's score from its two best: masked experts (-inf) add nothing to
 // one that has others.
 template <typename F>
@@ -75,82 +83,116 @@ __device__ __forceinline__ float soft_num(float l, float m) {
   return l == kNegInf ? 0.0f : (l == m ? 1.0f : expf(l - m));
 }
 
-// The selection of one token in fp64, over the whole warp; returns the id of
-// slot `lane` (lane < K).
+// Largest value over the warp, in one instruction (no NaN among them).
+__device__ __forceinline__ float warp_max_f32(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// A logit with NaN taken as masked.
+__device__ __forceinline__ float clean(float l) { return l > kNegInf ? l : kNegInf; }
+
+// The score of one logit in fp64; m and inv_total are the softmax's.
+template <bool SOFTMAX>
+__device__ __forceinline__ double score_fp64(float l, double m, double inv_total) {
+  const double v = l;
+  if (l == kNegInf) return 0.0;
+  if constexpr (SOFTMAX) return (v == m ? 1.0 : exp(v - m)) * inv_total;
+  else return 1.0 / (1.0 + exp(-v));
+}
+// Largest logit and 1 / sum of e^(l - m) of a row in fp64, over the warp.
+__device__ __noinline__ double2 softmax_fp64(const float* row, int E, int lane) {
+  double m = -INFINITY, total = 0.0;
+  for (int e = lane; e < E; e += 32) m = fmax(m, static_cast<double>(clean(row[e])));
+  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kAll, m, o));
+  for (int e = lane; e < E; e += 32) {
+    const double v = clean(row[e]);
+    total += v == -INFINITY ? 0.0 : (v == m ? 1.0 : exp(v - m));
+  }
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+  return make_double2(m, total > 0.0 ? 1.0 / total : 0.0);
+}
+
+// Of the groups in `band`, the `need` best in fp64 (ties: the lowest group).
+template <bool SOFTMAX>
+__device__ __noinline__ uint32_t groups_fp64(const float* row, const float* bias,
+                                             const moe_topk_dims& d, uint32_t band, int need,
+                                             int lane) {
+  double2 st = make_double2(0.0, 0.0);
+  if constexpr (SOFTMAX) st = softmax_fp64(row, d.E, lane);
+  const int gs = d.E / d.groups;
+  double mine = -INFINITY;
+  for (uint32_t left = band; left != 0; left &= left - 1) {
+    const int g = __ffs(left) - 1;
+    double t1 = -INFINITY, t2 = -INFINITY;
+    for (int e = g * gs + lane; e < (g + 1) * gs; e += 32) {
+      const float l = clean(row[e]);
+      if (l == kNegInf) continue;
+      const double v = score_fp64<SOFTMAX>(l, st.x, st.y) + (bias != nullptr ? static_cast<double>(bias[e]) : 0.0);
+      merge_top2(t1, t2, v, static_cast<double>(-INFINITY));
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+      const double b1 = __shfl_xor_sync(kAll, t1, o), b2 = __shfl_xor_sync(kAll, t2, o);
+      merge_top2(t1, t2, b1, b2);
+    }
+    if (lane == g) mine = group_score(t1, t2, d.group_top);
+  }
+  int rank = 0;
+  for (uint32_t left = band; left != 0; left &= left - 1) {
+    const int g = __ffs(left) - 1;
+    const double other = __shfl_sync(kAll, mine, g);
+    if (other > mine || (other == mine && g < lane)) ++rank;
+  }
+  return __ballot_sync(kAll, ((band >> lane) & 1u) && rank < need);
+}
+
+// Rank in fp64 of this lane's expert `id` (logit l) among those of lanes < n,
+// which hold them in any order; ties go to the lowest id.
+template <bool SOFTMAX>
+__device__ __noinline__ int rank_fp64(const float* row, const float* bias, int E, int id, float l, int n,
+                                      int lane) {
+  double2 st = make_double2(0.0, 0.0);
+  if constexpr (SOFTMAX) st = softmax_fp64(row, E, lane);
+  const double sel = score_fp64<SOFTMAX>(l, st.x, st.y) + (lane < n ? static_cast<double>(bias[id]) : 0.0);
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const double other = __shfl_sync(kAll, sel, j);
+    const int o_id = __shfl_sync(kAll, id, j);
+    if (other > sel || (other == sel && o_id < id)) ++rank;
+  }
+  return rank;
+}
+
+// The selection of one token in fp64, over the whole warp, among the groups
+// in `stay`; returns the id of slot `lane` (lane < K).  Used where the
+// candidates do not fit one per lane.
 template <int VPL, bool SOFTMAX>
 __device__ __noinline__ int select_fp64(const float* row, const float* bias, const moe_topk_dims& d,
-                                        int lane) {
-  double sel[VPL], s[VPL];
-  const double ninf = -INFINITY;
-  double m = ninf;
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane * VPL + i;
-    float l = e < d.E ? row[e] : kNegInf;
-    if (!(l > kNegInf)) l = kNegInf;
-    s[i] = l;
-    m = fmax(m, s[i]);
-  }
-  if (SOFTMAX) {
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kAll, m, o));
-    double total = 0.0;
-    for (int i = 0; i < VPL; ++i) {
-      sel[i] = s[i];
-      s[i] = s[i] == ninf ? 0.0 : (s[i] == m ? 1.0 : exp(s[i] - m));
-      total += s[i];
-    }
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-    for (int i = 0; i < VPL; ++i) s[i] = total > 0.0 ? s[i] / total : 0.0;
-  } else {
-    for (int i = 0; i < VPL; ++i) {
-      sel[i] = s[i];
-      s[i] = s[i] == ninf ? 0.0 : 1.0 / (1.0 + exp(-s[i]));
-    }
-  }
-  const bool by_s = bias == nullptr && d.group_top == 2;  // groups scored by s
-  if (bias != nullptr)
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane * VPL + i;
-      if (sel[i] != ninf) sel[i] = s[i] + static_cast<double>(bias[e]);
-    }
+                                        int first, int mine, uint32_t stay, int lane) {
+  double sel[VPL];
+  double2 st = make_double2(0.0, 0.0);
+  if constexpr (SOFTMAX) st = softmax_fp64(row, d.E, lane);
+  const int gs = d.E / d.groups;
   uint32_t used = 0;  // bit i: expert i of this lane is out
-  for (int i = 0; i < VPL; ++i)
-    if (lane * VPL + i >= d.E) used |= 1u << i;
-  if (d.groups > 1) {
-    const int gs = d.E / d.groups;
-    double mine = ninf;
-    for (int g = 0; g < d.groups; ++g) {
-      double t1 = ninf, t2 = ninf;
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane * VPL + i;
-        if (e < d.E && e / gs == g)
-          merge_top2(t1, t2, sel[i] == ninf ? ninf : (by_s ? s[i] : sel[i]), ninf);
-      }
-      for (int o = 16; o > 0; o >>= 1) {
-        const double b1 = __shfl_xor_sync(kAll, t1, o), b2 = __shfl_xor_sync(kAll, t2, o);
-        merge_top2(t1, t2, b1, b2);
-      }
-      if (lane == g) mine = group_score(t1, t2, d.group_top);
-    }
-    int rank = 0;
-    for (int g = 0; g < d.groups; ++g) {
-      const double other = __shfl_sync(kAll, mine, g);
-      if (other > mine || (other == mine && g < lane)) ++rank;
-    }
-    const uint32_t stay = __ballot_sync(kAll, lane < d.groups && rank < d.top_groups);
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane * VPL + i;
-      if (e < d.E && !((stay >> (e / gs)) & 1u)) used |= 1u << i;
+  for (int i = 0; i < VPL; ++i) {
+    const int e = first + i;
+    sel[i] = -INFINITY;
+    if (i >= mine || !((stay >> (e / gs)) & 1u)) {
+      used |= 1u << i;
+    } else {
+      const float l = clean(row[e]);
+      if (l != kNegInf) sel[i] = score_fp64<SOFTMAX>(l, st.x, st.y) + static_cast<double>(bias[e]);
     }
   }
-  int mine = 0;
+  int slot = 0;
   for (int k = 0; k < d.K; ++k) {
-    double best = ninf;
+    double best = -INFINITY;
     int id = 1 << 30;  // no expert: behind every id
     for (int i = 0; i < VPL; ++i) {
-      const int e = lane * VPL + i;
       if (!((used >> i) & 1u) && (id == (1 << 30) || sel[i] > best)) {
         best = sel[i];
-        id = e;
+        id = first + i;
       }
     }
     for (int o = 16; o > 0; o >>= 1) {
@@ -161,10 +203,10 @@ __device__ __noinline__ int select_fp64(const float* row, const float* bias, con
         id = j;
       }
     }
-    if (id / VPL == lane) used |= 1u << (id % VPL);
-    if (lane == k) mine = id;
+    if (id >= first && id < first + mine) used |= 1u << (id - first);
+    if (lane == k) slot = id;
   }
-  return mine;
+  return slot;
 }
 
 // Bounds of the error of a fast score (see fast_score): s (6e-7 + 1.5e-7
@@ -176,38 +218,43 @@ __device__ __forceinline__ float score_error(float s, float l, float m) {
   return SOFTMAX ? s * (3e-6f + 2e-7f * fmaxf(m - l, 0.0f)) : s * (6e-7f + 1.5e-7f * fmaxf(-l, 0.0f));
 }
 constexpr float kSumError = 1.2e-7f;  // of the rounded sum s + bias, relative
+// Largest score_error of any logit: (1 - s) is folded in for the sigmoid, and
+// s e^-x x <= 0.37 for the softmax, relative to the row's largest score.
+template <bool SOFTMAX>
+__device__ __forceinline__ float worst_error(float largest) {
+  return SOFTMAX ? 3.1e-6f * largest : 6.5e-7f;
+}
 
+// vpl: experts a lane holds at most (<= VPL); lpg: lanes of a group.
 template <int VPL, bool SOFTMAX>
-__global__ void __launch_bounds__(32 * kTopkWarps) route_topk_kernel(const TopkArgs p) {
-  __shared__ float gval[kTopkWarps][VPL * 32];  // only for groups that split a lane's experts
+__global__ void __launch_bounds__(32 * kTopkWarps)
+    route_topk_kernel(const TopkArgs p, const int vpl, const int lpg) {
+  __shared__ float2 cand[kTopkWarps][32];  // (value, id) of the candidates
   const moe_topk_dims d = p.d;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = d.E, K = d.K;
   const bool biased = p.bias != nullptr;
   const bool grouped = d.groups > 1 && d.top_groups < d.groups;
-  const bool by_s = !biased && d.group_top == 2;      // groups scored by s
-  const bool scored = biased || (grouped && by_s);     // s takes part in the selection
-  const bool need_total = SOFTMAX && (scored || !d.renorm);
-  const int gs = E / d.groups;
-  const int lpg = gs / VPL;  // lanes of a group
-  const bool whole_lanes = lpg * VPL == gs && (lpg & (lpg - 1)) == 0;
-  const bool vec = VPL % 4 == 0 && E % 4 == 0;
+  const bool by_s = grouped && !biased && d.group_top == 2;  // groups scored by s
+  const bool need_total = SOFTMAX && (biased || by_s || !d.renorm);
+  // this lane's experts: `mine` of them from `first`
+  const int gs = grouped ? E / d.groups : E;  // experts a run of lpg lanes shares
+  const int group = lane / lpg, r = lane - group * lpg;
+  const int first = group * gs + r * vpl;
+  const int mine = group * gs < E ? max(0, min(vpl, gs - r * vpl)) : 0;
+  const bool vec = VPL % 4 == 0 && vpl % 4 == 0 && gs % 4 == 0 && E % 4 == 0;
+  const bool pow2 = (lpg & (lpg - 1)) == 0;
+  const uint32_t below = (1u << lane) - 1u;
   float b[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane * VPL + i;
-    b[i] = biased && e < E ? __ldg(p.bias + e) : 0.0f;
-  }
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTopkWarps;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTopkWarps + warp; t < d.T; t += stride) {
+  for (int i = 0; i < VPL; ++i) b[i] = biased && i < mine ? __ldg(p.bias + first + i) : 0.0f;
+  auto load_row = [&](int64_t t, float (&l)[VPL]) {
     const float* row = p.logits + t * E;
-    float l[VPL];
     if (vec) {
 #pragma unroll
       for (int i = 0; i + 3 < VPL; i += 4) {
-        const int e = lane * VPL + i;
-        const float4 v = e < E ? __ldg(reinterpret_cast<const float4*>(row + e))
-                               : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+        float4 v = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+        if (i < mine) v = __ldg(reinterpret_cast<const float4*>(row + first + i));
         l[i] = v.x;
         l[i + 1] = v.y;
         l[i + 2] = v.z;
@@ -215,20 +262,26 @@ __global__ void __launch_bounds__(32 * kTopkWarps) route_topk_kernel(const TopkA
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane * VPL + i;
-        l[i] = e < E ? __ldg(row + e) : kNegInf;
-      }
+      for (int i = 0; i < VPL; ++i) l[i] = i < mine ? __ldg(row + first + i) : kNegInf;
     }
+  };
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTopkWarps;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kTopkWarps + warp;
+  float ahead[VPL];
+  if (t < d.T) load_row(t, ahead);
+  for (; t < d.T; t += stride) {
+    const float* row = p.logits + t * E;
+    float l[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) l[i] = l[i] > kNegInf ? l[i] : kNegInf;  // NaN too
+    for (int i = 0; i < VPL; ++i) l[i] = clean(ahead[i]);
+    if (t + stride < d.T) load_row(t + stride, ahead);  // the next token's row, meanwhile
 
     float m = 0.0f, inv_total = 0.0f;
     if constexpr (SOFTMAX) {
-      float lm = l[0];
+      m = l[0];
 #pragma unroll
-      for (int i = 1; i < VPL; ++i) lm = fmaxf(lm, l[i]);
-      m = warp_max(lm);
+      for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+      m = warp_max_f32(m);
       if (need_total) {
         float total = 0.0f;
 #pragma unroll
@@ -244,129 +297,185 @@ __global__ void __launch_bounds__(32 * kTopkWarps) route_topk_kernel(const TopkA
       else
         return __fdividef(1.0f, 1.0f + __expf(-v));
     };
-    uint32_t key[VPL];
+    // the value that orders the experts; masked and absent ones are -inf
+    if (biased) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const float v = biased && l[i] != kNegInf ? fast_score(l[i]) + b[i] : l[i];
-      key[i] = lane * VPL + i < E ? order_key(v) : 0u;
+      for (int i = 0; i < VPL; ++i) l[i] = l[i] == kNegInf ? kNegInf : fast_score(l[i]) + b[i];
     }
-    bool unsure = false;
+    const float worst = worst_error<SOFTMAX>(inv_total);
+
+    uint32_t stay = kAll;  // groups that stay
+    bool out = false;      // this lane's group does not
     if (grouped) {
-      float mine = kNegInf;  // the score of group `lane`
-      if (whole_lanes) {
-        float t1 = kNegInf, t2 = kNegInf;
+      float t1 = kNegInf, t2 = kNegInf;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const float v = by_s ? (l[i] == kNegInf ? kNegInf : fast_score(l[i])) : key_value(key[i]);
-          merge_top2(t1, t2, key[i] ? v : kNegInf, kNegInf);
-        }
+      for (int i = 0; i < VPL; ++i) {
+        const float v = by_s && l[i] != kNegInf ? fast_score(l[i]) : l[i];
+        merge_top2(t1, t2, v, kNegInf);
+      }
+      if (pow2) {
         for (int o = 1; o < lpg; o <<= 1) {
           const float b1 = __shfl_xor_sync(kAll, t1, o), b2 = __shfl_xor_sync(kAll, t2, o);
           merge_top2(t1, t2, b1, b2);
         }
-        mine = __shfl_sync(kAll, group_score(t1, t2, d.group_top), (lane * lpg) & 31);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          gval[warp][lane * VPL + i] =
-              by_s ? (l[i] == kNegInf ? kNegInf : fast_score(l[i])) : (key[i] ? key_value(key[i]) : kNegInf);
-        __syncwarp();
-        if (lane < d.groups) {
-          float t1 = kNegInf, t2 = kNegInf;
-          for (int j = 0; j < gs; ++j) merge_top2(t1, t2, gval[warp][lane * gs + j], kNegInf);
-          mine = group_score(t1, t2, d.group_top);
+      } else {  // the group's other lanes in turn
+        const float own1 = t1, own2 = t2;
+        for (int o = 1; o < lpg; ++o) {
+          const int src = (group * lpg + (r + o) % lpg) & 31;
+          const float b1 = __shfl_sync(kAll, own1, src), b2 = __shfl_sync(kAll, own2, src);
+          merge_top2(t1, t2, b1, b2);
         }
-        __syncwarp();
       }
-      uint32_t gkey = lane < d.groups ? order_key(mine) : 0u, last = 0u, stay = 0u;
+      // the score of group `lane`
+      const float score = __shfl_sync(kAll, group_score(t1, t2, d.group_top), (lane * lpg) & 31);
+      uint32_t gkey = lane < d.groups ? order_key(score) : 0u, last = 0u;
+      stay = 0u;
       for (int g = 0; g < d.top_groups; ++g) {
         last = __reduce_max_sync(kAll, gkey);
         const int src = __ffs(__ballot_sync(kAll, gkey == last)) - 1;
         stay |= 1u << src;
         if (lane == src) gkey = 0u;
       }
-      if (scored) {
-        const float in = key_value(last), out = key_value(__reduce_max_sync(kAll, gkey));
-        // two scores a side, each within score_error's largest value
-        const float err = SOFTMAX ? 12.5e-6f * inv_total : 2.6e-6f;
-        unsure = out > kNegInf && in - out <= err + 2.0f * kSumError * (fabsf(in) + fabsf(out));
+      if (biased || by_s) {
+        const float in = key_value(last), next = key_value(__reduce_max_sync(kAll, gkey));
+        const float err = 4.0f * worst + 2.0f * kSumError * (fabsf(in) + fabsf(next));  // both sides
+        if (next > kNegInf && in - next <= err) {
+          // every group that may lie on either side of the border
+          const uint32_t band = __ballot_sync(
+              kAll, lane < d.groups && score <= next + 2.0f * err && score >= in - 2.0f * err);
+          const uint32_t sure = stay & ~band;
+          stay = sure | groups_fp64<SOFTMAX>(row, p.bias, d, band, d.top_groups - __popc(sure), lane);
+        }
       }
-      if (whole_lanes) {
-        if (!((stay >> (lane / lpg & 31)) & 1u)) {
+      out = !((stay >> group) & 1u);
+      if (out) {
 #pragma unroll
-          for (int i = 0; i < VPL; ++i) key[i] = 0u;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const int e = lane * VPL + i;
-          if (e < E && !((stay >> (e / gs)) & 1u)) key[i] = 0u;
-        }
+        for (int i = 0; i < VPL; ++i) l[i] = kNegInf;
       }
     }
 
-    // K rounds: the warp's largest key, and its lane's next one
-    uint32_t top = key[0];
+    // a lower bound of the K-th value: the K-th largest of the lanes' maxima
+    float top = l[0];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) top = max(top, key[i]);
+    for (int i = 1; i < VPL; ++i) top = fmaxf(top, l[i]);
+    float bound = kNegInf;
+    {
+      float rest = top;
+      for (int k = 0; k < K; ++k) {
+        bound = warp_max_f32(rest);
+        if (rest == bound) rest = kNegInf;
+      }
+    }
+    if (biased) bound -= 2.0f * (worst + kSumError * fabsf(bound));  // what may still pass it
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) count += l[i] >= bound && i < VPL ? 1 : 0;
+    // candidates before this lane's, in the order of the ids
+    int at = 0, n = 0;
+#pragma unroll
+    for (int w = 0; (1 << w) <= VPL; ++w) {
+      const uint32_t have = __ballot_sync(kAll, (count >> w) & 1);
+      at += __popc(have & below) << w;
+      n += __popc(have) << w;
+    }
     int my_id = 0;
-    uint32_t my_key = 0u;
-    auto take = [&](uint32_t best) -> int {
-      const int src = __ffs(__ballot_sync(kAll, top == best)) - 1;
-      int idx = 0;
-      if (lane == src) {
-        uint32_t rest = 0u;
+    if (bound > kNegInf && n >= K && n <= 32) {
+      __syncwarp();
 #pragma unroll
-        for (int i = VPL - 1; i >= 0; --i)
-          if (key[i] == best) idx = i;  // the lowest such index
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          if (i == idx) key[i] = 0u;
-          rest = max(rest, key[i]);
+      for (int i = 0; i < VPL; ++i)
+        if (l[i] >= bound) cand[warp][at++] = make_float2(l[i], __int_as_float(first + i));
+      __syncwarp();
+      float v = kNegInf;
+      int id = 0;
+      if (lane < n) {
+        const float2 c = cand[warp][lane];
+        v = c.x;
+        id = __float_as_int(c.y);
+      }
+      int rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const float o = __shfl_sync(kAll, v, j);
+        rank += (o > v || (o == v && j < lane)) ? 1 : 0;
+      }
+      __syncwarp();
+      if (lane < n) cand[warp][rank] = make_float2(v, __int_as_float(id));
+      __syncwarp();
+      if (lane < n) {
+        const float2 c = cand[warp][lane];
+        v = c.x;
+        id = __float_as_int(c.y);
+      }
+      if (biased) {
+        // lane r against the next of the list
+        const float bs = lane < n ? __ldg(p.bias + id) : 0.0f;
+        const float lo = lane < n ? clean(__ldg(row + id)) : kNegInf;
+        const float o_v = __shfl_down_sync(kAll, v, 1), o_b = __shfl_down_sync(kAll, bs, 1);
+        const float o_l = __shfl_down_sync(kAll, lo, 1);
+        const float s = v - bs, o_s = o_v - o_b;  // the scores, up to the rounded sum
+        const float err = score_error<SOFTMAX>(s, lo, m) + score_error<SOFTMAX>(o_s, o_l, m) +
+                          2.0f * kSumError * (fabsf(v) + fabsf(o_v));
+        const bool unsure = lane < K && lane + 1 < n && v - o_v <= err && !(lo == o_l && bs == o_b);
+        if (__any_sync(kAll, unsure)) {
+          rank = rank_fp64<SOFTMAX>(row, p.bias, E, id, lo, n, lane);
+          if (lane < n) cand[warp][rank] = make_float2(v, __int_as_float(id));
+          __syncwarp();
+          if (lane < n) id = __float_as_int(cand[warp][lane].y);
         }
-        top = rest;
       }
-      return __shfl_sync(kAll, lane * VPL + idx, src);
-    };
-    for (int k = 0; k < K; ++k) {
-      const uint32_t best = __reduce_max_sync(kAll, top);
-      const int id = take(best);
-      if (lane == k) {
-        my_id = id;
-        my_key = best;
+      my_id = id;
+    } else {
+      // K rounds: the warp's largest key, and its lane's next one
+      uint32_t key[VPL], ktop = 0u, my_key = 0u;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        key[i] = i < mine && !out ? order_key(l[i]) : 0u;
+        ktop = max(ktop, key[i]);
+      }
+      auto take = [&](uint32_t best) -> int {
+        const int src = __ffs(__ballot_sync(kAll, ktop == best)) - 1;
+        int idx = 0;
+        if (lane == src) {
+          uint32_t rest = 0u;
+#pragma unroll
+          for (int i = VPL - 1; i >= 0; --i)
+            if (key[i] == best) idx = i;  // the lowest such index
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) {
+            if (i == idx) key[i] = 0u;
+            rest = max(rest, key[i]);
+          }
+          ktop = rest;
+        }
+        return __shfl_sync(kAll, first + idx, src);
+      };
+      for (int k = 0; k < K; ++k) {
+        const uint32_t best = __reduce_max_sync(kAll, ktop);
+        const int id = take(best);
+        if (lane == k) {
+          my_id = id;
+          my_key = best;
+        }
+      }
+      if (biased) {
+        const uint32_t next = __reduce_max_sync(kAll, ktop);  // the first expert left out
+        const int next_id = next != 0u ? take(next) : 0;
+        const float v = key_value(my_key), bs = lane < K ? __ldg(p.bias + my_id) : 0.0f;
+        const float lo = lane < K ? clean(__ldg(row + my_id)) : kNegInf;
+        float o_v = __shfl_down_sync(kAll, v, 1), o_b = __shfl_down_sync(kAll, bs, 1);
+        float o_l = __shfl_down_sync(kAll, lo, 1);
+        if (lane == K - 1) {
+          o_v = next != 0u ? key_value(next) : kNegInf;
+          o_b = next != 0u ? __ldg(p.bias + next_id) : 0.0f;
+          o_l = next != 0u ? clean(__ldg(row + next_id)) : kNegInf;
+        }
+        const float err = score_error<SOFTMAX>(v - bs, lo, m) + score_error<SOFTMAX>(o_v - o_b, o_l, m) +
+                          2.0f * kSumError * (fabsf(v) + fabsf(o_v));
+        const bool unsure = lane < K && o_v > kNegInf && v - o_v <= err && !(lo == o_l && bs == o_b);
+        if (__any_sync(kAll, unsure))
+          my_id = select_fp64<VPL, SOFTMAX>(row, p.bias, d, first, mine, stay, lane);
       }
     }
-    float my_l = lane < K ? __ldg(row + my_id) : kNegInf;
-    if (!(my_l > kNegInf)) my_l = kNegInf;
-    if (biased) {
-      const uint32_t next = __reduce_max_sync(kAll, top);  // the first expert left out
-      int next_id = 0;
-      float next_l = kNegInf;
-      if (next != 0u) {
-        next_id = take(next);
-        next_l = __ldg(row + next_id);
-        if (!(next_l > kNegInf)) next_l = kNegInf;
-      }
-      const float my_sel = key_value(my_key), my_b = lane < K ? __ldg(p.bias + my_id) : 0.0f;
-      float o_sel = __shfl_down_sync(kAll, my_sel, 1);
-      float o_l = __shfl_down_sync(kAll, my_l, 1), o_b = __shfl_down_sync(kAll, my_b, 1);
-      if (lane == K - 1) {
-        o_sel = next != 0u ? key_value(next) : kNegInf;
-        o_l = next_l;
-        o_b = next != 0u ? __ldg(p.bias + next_id) : 0.0f;
-      }
-      if (lane < K && o_sel > kNegInf && !(my_l == o_l && my_b == o_b)) {
-        const float err = score_error<SOFTMAX>(fast_score(my_l), my_l, m) +
-                          score_error<SOFTMAX>(fast_score(o_l), o_l, m) +
-                          kSumError * (fabsf(my_sel) + fabsf(o_sel));
-        if (my_sel - o_sel <= err) unsure = true;
-      }
-    }
-    if (scored && __any_sync(kAll, unsure)) {
-      my_id = select_fp64<VPL, SOFTMAX>(row, p.bias, d, lane);
-      my_l = lane < K ? __ldg(row + my_id) : kNegInf;
-      if (!(my_l > kNegInf)) my_l = kNegInf;
-    }
+    const float my_l = lane < K ? clean(__ldg(row + my_id)) : kNegInf;
     float s = 0.0f;
     if (lane < K) {
       if constexpr (SOFTMAX) s = soft_num(my_l, m);
@@ -501,15 +610,15 @@ unsigned topk_grid(int T) {
   return static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(sm_count()) * 16));
 }
 
-// Calls go(n) with the experts a lane holds: E / 32 rounded up to a power of two.
+// Calls go(n) with the smallest compiled capacity for vpl experts per lane.
 template <class Go>
-void pick_vpl(int E, Go go) {
+void pick_vpl(int vpl, Go go) {
   using std::integral_constant;
-  if (E <= 32) go(integral_constant<int, 1>{});
-  else if (E <= 64) go(integral_constant<int, 2>{});
-  else if (E <= 128) go(integral_constant<int, 4>{});
-  else if (E <= 256) go(integral_constant<int, 8>{});
-  else if (E <= 512) go(integral_constant<int, 16>{});
+  if (vpl <= 1) go(integral_constant<int, 1>{});
+  else if (vpl <= 2) go(integral_constant<int, 2>{});
+  else if (vpl <= 4) go(integral_constant<int, 4>{});
+  else if (vpl <= 8) go(integral_constant<int, 8>{});
+  else if (vpl <= 16) go(integral_constant<int, 16>{});
   else go(integral_constant<int, 32>{});
 }
 
@@ -519,10 +628,15 @@ cudaError_t launch_route_topk(const float* logits, const float* bias, int32_t* i
                               const moe_topk_dims& d, cudaStream_t s) {
   const TopkArgs a{logits, bias, ids, w, d};
   const unsigned grid = topk_grid(d.T);
-  pick_vpl(d.E, [&](auto n) {
+  const bool grouped = d.groups > 1 && d.top_groups < d.groups;
+  const int lpg = grouped ? topk_group_lanes(d) : 32;
+  const int vpl = ((grouped ? d.E / d.groups : d.E) + lpg - 1) / lpg;
+  pick_vpl(vpl, [&](auto n) {
     constexpr int VPL = decltype(n)::value;
-    if (d.gate == MOE_GATE_SOFTMAX) route_topk_kernel<VPL, true><<<grid, 32 * kTopkWarps, 0, s>>>(a);
-    else route_topk_kernel<VPL, false><<<grid, 32 * kTopkWarps, 0, s>>>(a);
+    if (d.gate == MOE_GATE_SOFTMAX)
+      route_topk_kernel<VPL, true><<<grid, 32 * kTopkWarps, 0, s>>>(a, vpl, lpg);
+    else
+      route_topk_kernel<VPL, false><<<grid, 32 * kTopkWarps, 0, s>>>(a, vpl, lpg);
   });
   return cudaGetLastError();
 }
@@ -532,7 +646,7 @@ cudaError_t launch_route_topk_bwd(const float* logits, const int32_t* ids, const
   const TopkBwdArgs a{logits, ids, dw, dlogits, d};
   const unsigned grid = topk_grid(d.T);
   const bool dense = d.gate == MOE_GATE_SOFTMAX && !d.renorm;
-  pick_vpl(d.E, [&](auto n) {
+  pick_vpl((d.E + 31) / 32, [&](auto n) {
     constexpr int VPL = decltype(n)::value;
     if (dense) route_topk_bwd_kernel<VPL, true><<<grid, 32 * kTopkWarps, 0, s>>>(a);
     else route_topk_bwd_kernel<VPL, false><<<grid, 32 * kTopkWarps, 0, s>>>(a);

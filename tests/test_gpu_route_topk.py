@@ -28,6 +28,9 @@ CASES = [
     (60, 1024, 32, "sigmoid", True, 16, 4, 2, True, 1.0),
     (60, 1000, 9, "softmax", True, 1, 1, 1, True, 1.0),
     (20, 32, 4, "sigmoid", True, 32, 7, 2, True, 1.0),        # groups of one expert
+    (40, 1022, 8, "sigmoid", True, 2, 1, 2, True, 1.0),       # a group's size no power of two divides
+    (40, 960, 8, "softmax", True, 3, 2, 2, False, 1.0),
+    (40, 693, 8, "sigmoid", False, 7, 3, 2, True, 1.0),
 ]
 
 

@@ -73,7 +73,7 @@ def topk(logits=P, bias=P, ids=P, w=P, bwd=False, **kw):
     (dict(top_groups=0), UNSUP), (dict(top_groups=1, K=9), UNSUP), (dict(gate=2), BAD),
     (dict(group_top=3), BAD), (dict(group_top=0), BAD), (dict(logits=None), BAD), (dict(ids=None), BAD),
     (dict(w=None), BAD), (dict(logits=P + 4), BAD), (dict(bias=P + 4), BAD),
-    (dict(T=1 << 30, K=4), UNSUP),
+    (dict(T=1 << 30, K=4), UNSUP), (dict(E=1023, groups=3, top_groups=2), UNSUP),
 ])
 def test_topk_refusals(kw, want):
     assert topk(**kw) == want
