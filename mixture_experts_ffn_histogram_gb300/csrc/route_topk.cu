@@ -90,8 +90,21 @@ __device__ __forceinline__ float warp_max_f32(float v) {
   return r;
 }
 
-// A logit with NaN taken as masked.
-__device__ __forceinline__ float clean(float l) { return l > kNegInf ? l : kNegInf; }
+// A logit with NaN taken as masked (the maximum of NaN and a number is the number).
+__device__ __forceinline__ float clean(float l) { return fmaxf(l, kNegInf); }
+
+// 2^x to 2 ulp and 1 / x to 1 ulp, subnormals flushed.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 // The score of one logit in fp64; m and inv_total are the softmax's.
 template <bool SOFTMAX>
@@ -210,9 +223,9 @@ __device__ __noinline__ int select_fp64(const float* row, const float* bias, con
 }
 
 // Bounds of the error of a fast score (see fast_score): s (6e-7 + 1.5e-7
-// max(-l, 0)) for the sigmoid, from __expf's 2 + 1.17 |x| ulp and
-// __fdividef's 2 ulp; for the softmax s (3e-6 + 2e-7 (m - l)), which
-// includes the error of the sum over experts.
+// max(-l, 0)) for the sigmoid, from the exponential's 2 ulp and its rounded
+// argument (1.17 |l| ulp) and the reciprocal's ulp; for the softmax
+// s (3e-6 + 2e-7 (m - l)), which includes the error of the sum over experts.
 template <bool SOFTMAX>
 __device__ __forceinline__ float score_error(float s, float l, float m) {
   return SOFTMAX ? s * (3e-6f + 2e-7f * fmaxf(m - l, 0.0f)) : s * (6e-7f + 1.5e-7f * fmaxf(-l, 0.0f));
@@ -286,16 +299,16 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
         float total = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-          total += l[i] == kNegInf ? 0.0f : (l[i] == m ? 1.0f : __expf(l[i] - m));
-        total = warp_sum(total);
+          total += l[i] == m && l[i] != kNegInf ? 1.0f : exp2_fast((l[i] - m) * kLog2e);
+        total = m == kNegInf ? 0.0f : warp_sum(total);
         inv_total = total > 0.0f ? 1.0f / total : 0.0f;
       }
     }
     auto fast_score = [&](float v) -> float {
       if constexpr (SOFTMAX)
-        return v == kNegInf ? 0.0f : (v == m ? 1.0f : __expf(v - m)) * inv_total;
+        return (v == m ? 1.0f : exp2_fast((v - m) * kLog2e)) * inv_total;
       else
-        return __fdividef(1.0f, 1.0f + __expf(-v));
+        return rcp_fast(1.0f + exp2_fast(-kLog2e * v));
     };
     // the value that orders the experts; masked and absent ones are -inf
     if (biased) {
@@ -310,8 +323,12 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
       float t1 = kNegInf, t2 = kNegInf;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        const float v = by_s && l[i] != kNegInf ? fast_score(l[i]) : l[i];
-        merge_top2(t1, t2, v, kNegInf);
+        t2 = fmaxf(t2, fminf(t1, l[i]));
+        t1 = fmaxf(t1, l[i]);
+      }
+      if (by_s) {  // scores keep the logits' order
+        if (t1 != kNegInf) t1 = fast_score(t1);
+        if (t2 != kNegInf) t2 = fast_score(t2);
       }
       if (pow2) {
         for (int o = 1; o < lpg; o <<= 1) {
