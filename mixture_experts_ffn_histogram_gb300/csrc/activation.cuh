@@ -1,7 +1,7 @@
 // Activations of the linear layer and their derivatives, in fp32.
 //
-// EXACT false is for 16-bit results: the hardware exponential and division
-// (2 and a few ulp) and, for gelu, erfc by the rational approximation 7.1.26
+// EXACT false is for 16-bit results: the hardware exponential and reciprocal
+// (2 ulp and 1) and, for gelu, erfc by the rational approximation 7.1.26
 // of Abramowitz and Stegun, Handbook of Mathematical Functions (absolute
 // error at most 1.5e-7), far below half a step of bf16 or fp16.  EXACT true
 // is for fp32 results and uses the accurate functions.
@@ -12,16 +12,9 @@
 namespace moe {
 
 template <bool EXACT>
-__device__ __forceinline__ float act_exp(float x) {
-  return EXACT ? expf(x) : __expf(x);
-}
-template <bool EXACT>
-__device__ __forceinline__ float act_div(float a, float b) {
-  return EXACT ? a / b : __fdividef(a, b);
-}
-template <bool EXACT>
 __device__ __forceinline__ float act_sigmoid(float x) {
-  return act_div<EXACT>(1.0f, 1.0f + act_exp<EXACT>(-x));
+  if constexpr (EXACT) return 1.0f / (1.0f + expf(-x));
+  else return rcp_fast(1.0f + exp2_fast(-kLog2e * x));
 }
 
 // Phi(z) and e^(-z^2/2).
@@ -30,13 +23,14 @@ __device__ __forceinline__ float2 normal_cdf(float z) {
   if constexpr (EXACT) {
     return make_float2(0.5f * erfcf(-0.70710678f * z), expf(-0.5f * z * z));
   } else {
-    const float x = 0.70710678f * fabsf(z);
-    const float t = __fdividef(1.0f, 1.0f + 0.3275911f * x);
-    const float e = __expf(-x * x);
+    // at x = |z| / sqrt(2), the coefficients halved: Phi(-|z|) = erfc(x) / 2
+    const float t = rcp_fast(1.0f + (0.3275911f * 0.70710678f) * fabsf(z));
+    const float e = exp2_fast(z * z * (-0.5f * kLog2e));
     const float poly =
-        t * (0.254829592f +
-             t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-    const float q = 0.5f * poly * e;  // Phi(-|z|)
+        0.5f * 0.254829592f +
+        t * (0.5f * -0.284496736f +
+             t * (0.5f * 1.421413741f + t * (0.5f * -1.453152027f + t * (0.5f * 1.061405429f))));
+    const float q = poly * t * e;
     return make_float2(z >= 0.0f ? 1.0f - q : q, e);
   }
 }
@@ -53,6 +47,23 @@ __device__ __forceinline__ float act_value(float z, int act) {
       return z * act_sigmoid<EXACT>(kGeluA * z * (1.0f + kGeluB * z * z));
     case MOE_ACT_SILU: return z * act_sigmoid<EXACT>(z);
     default: return z;
+  }
+}
+
+// The activation of N values at once: one branch on its kind.
+template <bool EXACT, int N, int ACT>
+__device__ __forceinline__ void act_run(float* v) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = act_value<EXACT>(v[i], ACT);
+}
+template <bool EXACT, int N>
+__device__ __forceinline__ void act_all(float* v, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: act_run<EXACT, N, MOE_ACT_RELU>(v); break;
+    case MOE_ACT_GELU: act_run<EXACT, N, MOE_ACT_GELU>(v); break;
+    case MOE_ACT_GELU_TANH: act_run<EXACT, N, MOE_ACT_GELU_TANH>(v); break;
+    case MOE_ACT_SILU: act_run<EXACT, N, MOE_ACT_SILU>(v); break;
+    default: break;
   }
 }
 

@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <cstdlib>
 
 #include "activation.cuh"
 #include "kernels.h"
@@ -45,7 +46,6 @@ constexpr int kBlockK = 64;
 constexpr int kMmaK = 16;
 constexpr int kChunk = 64 * kBlockK * 2;         // 64 columns x 64 reduction rows: 8 KB
 constexpr int kATile = kTileM * kBlockK * 2;     // 16 KB
-constexpr int kSplitThreads = 192;
 constexpr int kSplitMaxStages = 12;
 constexpr int kChunkBlocks = 8;                  // fp32 results: 512 products per chain
 constexpr int kSplitSmemLimit = 220 * 1024;
@@ -70,58 +70,81 @@ struct DenseParams {
   uint64_t limit_ns;
 };
 
-// The epilogue of four neighbouring columns of one output row.
-template <typename T, typename O>
-__device__ __forceinline__ void epilogue4(float (&v)[4], int64_t row, int64_t col,
+// The epilogue of G groups of four neighbouring columns, each of one output
+// row: G independent chains, and one branch on the activation for all of
+// them.  A group outside the output (`on` false) comes with a place inside,
+// so that its loads need no branch, and is not stored.
+template <typename T, typename O, int G>
+__device__ __forceinline__ void epilogue4(float (&v)[G][4], const int64_t (&row)[G],
+                                          const int64_t (&col)[G], const bool (&on)[G],
                                           const DenseParams& p) {
   constexpr bool kExact = sizeof(O) == 4;
+  const O* res = static_cast<const O*>(p.res);
+  float r[G][4];
+  if (res != nullptr) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const O* at = res + row[g] * p.ldres + col[g];
+      if constexpr (sizeof(O) == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(at);
+        r[g][0] = f.x;
+        r[g][1] = f.y;
+        r[g][2] = f.z;
+        r[g][3] = f.w;
+      } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(at);
+        const float2 a = unpack_pair(q.x, O{}), b = unpack_pair(q.y, O{});
+        r[g][0] = a.x;
+        r[g][1] = a.y;
+        r[g][2] = b.x;
+        r[g][3] = b.y;
+      }
+    }
+  }
   if (p.bias != nullptr) {
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col));
-    v[0] += b.x;
-    v[1] += b.y;
-    v[2] += b.z;
-    v[3] += b.w;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col[g]));
+      v[g][0] += b.x;
+      v[g][1] += b.y;
+      v[g][2] += b.z;
+      v[g][3] += b.w;
+    }
   }
   if (p.z != nullptr) {
-    T* z = static_cast<T*>(p.z) + row * p.ldz + col;
-    *reinterpret_cast<uint2*>(z) = make_uint2(pack_pair(v[0], v[1], T{}), pack_pair(v[2], v[3], T{}));
-  }
-  if (p.act != MOE_ACT_NONE) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = act_value<kExact>(v[i], p.act);
+    for (int g = 0; g < G; ++g)
+      if (on[g])
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.z) + row[g] * p.ldz + col[g]) =
+            make_uint2(pack_pair(v[g][0], v[g][1], T{}), pack_pair(v[g][2], v[g][3], T{}));
   }
-  O* c = static_cast<O*>(p.c) + row * p.ldc + col;
-  const O* res = static_cast<const O*>(p.res);
-  if constexpr (sizeof(O) == 4) {
+  act_all<kExact, 4 * G>(&v[0][0], p.act);
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    if (!on[g]) continue;
     if (res != nullptr) {
-      const float4 r = *reinterpret_cast<const float4*>(res + row * p.ldres + col);
-      v[0] += r.x;
-      v[1] += r.y;
-      v[2] += r.z;
-      v[3] += r.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[g][i] += r[g][i];
     }
-    *reinterpret_cast<float4*>(c) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    if (res != nullptr) {
-      const uint2 r = *reinterpret_cast<const uint2*>(res + row * p.ldres + col);
-      const float2 r0 = unpack_pair(r.x, O{}), r1 = unpack_pair(r.y, O{});
-      v[0] += r0.x;
-      v[1] += r0.y;
-      v[2] += r1.x;
-      v[3] += r1.y;
-    }
-    *reinterpret_cast<uint2*>(c) = make_uint2(pack_pair(v[0], v[1], O{}), pack_pair(v[2], v[3], O{}));
+    O* c = static_cast<O*>(p.c) + row[g] * p.ldc + col[g];
+    if constexpr (sizeof(O) == 4)
+      *reinterpret_cast<float4*>(c) = make_float4(v[g][0], v[g][1], v[g][2], v[g][3]);
+    else
+      *reinterpret_cast<uint2*>(c) =
+          make_uint2(pack_pair(v[g][0], v[g][1], O{}), pack_pair(v[g][2], v[g][3], O{}));
   }
 }
-__device__ __forceinline__ void epilogue4_any(float (&v)[4], int64_t row, int64_t col,
+template <int G>
+__device__ __forceinline__ void epilogue4_any(float (&v)[G][4], const int64_t (&row)[G],
+                                              const int64_t (&col)[G], const bool (&on)[G],
                                               const DenseParams& p) {
   if (p.out_type == MOE_FP32) {
-    if (p.type == MOE_BF16) epilogue4<__nv_bfloat16, float>(v, row, col, p);
-    else epilogue4<__half, float>(v, row, col, p);
+    if (p.type == MOE_BF16) epilogue4<__nv_bfloat16, float, G>(v, row, col, on, p);
+    else epilogue4<__half, float, G>(v, row, col, on, p);
   } else if (p.type == MOE_BF16) {
-    epilogue4<__nv_bfloat16, __nv_bfloat16>(v, row, col, p);
+    epilogue4<__nv_bfloat16, __nv_bfloat16, G>(v, row, col, on, p);
   } else {
-    epilogue4<__half, __half>(v, row, col, p);
+    epilogue4<__half, __half, G>(v, row, col, on, p);
   }
 }
 
@@ -134,6 +157,67 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+// One lane of a converged warp, known to the compiler as such: what it issues
+// alone needs no loop over lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// One operand's share of a stage: W rows of 64 reduction elements (K-major,
+// one box), or W / 64 chunks of 64 columns (MN-major).
+template <int CG, bool MN, int W>
+__device__ __forceinline__ void operand_load(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int x0,
+                                             int k0) {
+  if constexpr (!MN) {
+    if constexpr (CG == 2) tma_load_2d_pair(dst, map, bar, k0, x0);
+    else tma_load_2d_addr(dst, map, bar, k0, x0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < W / 64; ++j) {
+      if constexpr (CG == 2) tma_load_2d_pair(dst + j * kChunk, map, bar, x0 + 64 * j, k0);
+      else tma_load_2d_addr(dst + j * kChunk, map, bar, x0 + 64 * j, k0);
+    }
+  }
+}
+
+// The products of one reduction block: operands at shared addresses a and b.
+template <int CG, bool AMN, bool BMN>
+__device__ __forceinline__ void issue_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                            uint32_t add) {
+  const uint64_t ad = AMN ? smem_desc_sw128(a, kChunk, 1024) : smem_desc_sw128(a, 16, 1024);
+  const uint64_t bd = BMN ? smem_desc_sw128(b, kChunk, 1024) : smem_desc_sw128(b, 16, 1024);
+#pragma unroll
+  for (int kk = 0; kk < kBlockK / kMmaK; ++kk)  // start addresses in units of 16 bytes
+    umma_bf16<CG>(d, ad + kk * (AMN ? 128 : 2), bd + kk * (BMN ? 128 : 2), idesc, kk > 0 ? 1u : add);
+}
+
+template <int CG>
+__device__ __forceinline__ bool wait_any(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
+  return CG == 2 ? mbar_wait_cluster(bar, parity, c) : mbar_wait(bar, parity, c);
+}
+
+// A wait of the whole warp, polled by one lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
+  bool ok = true;
+  if (elect_one()) ok = mbar_wait(bar, parity, c);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// umma_commit for the CTA pair of ranks `even`, even + 1 of a larger cluster.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, int even) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3u << even))
+      : "memory");
+}
+
 struct SplitCtl {
   uint64_t full[kSplitMaxStages];
   uint64_t empty[kSplitMaxStages];
@@ -144,32 +228,47 @@ struct SplitCtl {
 };
 
 // Columns of a TMEM allocation: a power of two, at least 32.
-__host__ __device__ constexpr int tmem_cols(int n) { return n <= 32 ? 32 : (n <= 64 ? 64 : (n <= 128 ? 128 : (n <= 256 ? 256 : 512))); }
-
-// Shared memory of a CTA: the operand ring (in which the partial tile is laid
-// when the products are done), then the control block.
-__host__ __device__ constexpr int split_stage_bytes(int BN) { return kATile + BN * kBlockK * 2; }
-__host__ __device__ constexpr int split_partial_bytes(int BN, bool swap) {
-  return swap ? BN * (kTileM + 4) * 4 : kTileM * (BN + 4) * 4;
+__host__ __device__ constexpr int tmem_cols(int n) {
+  return n <= 32 ? 32 : (n <= 64 ? 64 : (n <= 128 ? 128 : (n <= 256 ? 256 : 512)));
 }
 
-template <int BN, bool AMN, bool BMN, bool SWAP>
-__global__ void __launch_bounds__(kSplitThreads)
+// A tile of the split kernel: 128 CG rows by BN columns over CG CTAs.  SWAP:
+// the 128 side is the output's columns.
+template <int BN_, int CG_, bool AMN_, bool BMN_, bool SWAP_>
+struct SplitShape {
+  static constexpr int BN = BN_, CG = CG_;
+  static constexpr bool AMN = AMN_, BMN = BMN_, SWAP = SWAP_;
+  static constexpr int kBRows = BN / CG;                       // B columns a CTA loads
+  static constexpr int kStage = kATile + kBRows * kBlockK * 2;  // operand bytes of a block, per CTA
+  static constexpr int kEpiWarps = BN > 128 ? 8 : 4;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
+  static constexpr int kAcc = BN * 4 / kEpiWarps;              // columns of an epilogue thread
+  static constexpr int kCols = tmem_cols(2 * BN);
+  static constexpr int kRowsOut = SWAP ? BN : kTileM;          // a CTA's partial tile
+  static constexpr int kColsOut = SWAP ? kTileM : BN;
+  static constexpr int kLd = kColsOut + 4;
+  static constexpr int kPartial = kRowsOut * kLd * 4;          // laid over the operand ring
+  static_assert(!BMN || kBRows % 64 == 0, "MN-major operands come in 64-wide chunks");
+  static_assert(CG == 1 || !SWAP, "swapped tiles are one CTA's");
+};
+
+template <class S>
+__global__ void __launch_bounds__(S::kThreads)
     dense_split_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, const DenseParams p,
                        const int stages, const int splits, const int chunk_blocks) {
-  static_assert(!BMN || BN % 64 == 0, "MN-major operands come in 64-wide chunks");
-  constexpr int kStage = split_stage_bytes(BN);
-  constexpr uint32_t kCols = tmem_cols(2 * BN);
+  constexpr int BN = S::BN, CG = S::CG, kStage = S::kStage, kEpiWarps = S::kEpiWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   SplitCtl& s = *reinterpret_cast<SplitCtl*>(ring + stages * kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int a0 = (blockIdx.x / splits) * kTileM;  // first row of the tile's 128 side
-  const int b0 = blockIdx.y * BN;                 // ... of its BN side
-  const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / splits);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / splits);
+  const bool clustered = CG * splits > 1;
+  const int crank = clustered ? static_cast<int>(cluster_ctarank()) : 0;
+  const int split = crank / CG, sub = crank % CG, even = crank - sub;
+  const int a0 = (blockIdx.x / (CG * splits)) * (kTileM * CG) + kTileM * sub;  // this CTA's 128 side
+  const int b0 = blockIdx.y * BN;                                              // the tile's BN side
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * split / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (split + 1) / splits);
   const int nkb = kb1 - kb0;
 
   if (warp == 0 && lane == 0) {
@@ -181,55 +280,44 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.tfull[i], 1);
-      mbar_init(&s.tempty[i], 4);
+      mbar_init(&s.tempty[i], kEpiWarps * CG);
     }
     s.abort_flag = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc<1>(&s.tmem_base, kCols);
-    tmem_relinquish<1>();
+    tmem_alloc<CG>(&s.tmem_base, S::kCols);
+    tmem_relinquish<CG>();
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // the pair's barriers exist before any remote arrive
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0, filled = 0;
       uint32_t phase = 0;
-      bool aborted = false;
+      bool ok = true;
+      // a pair's bytes complete on the even CTA's barrier, which it arms for both
+      const uint32_t full0 = CG == 2 ? mapa_shared(smem_u32(&s.full[0]), even) : smem_u32(&s.full[0]);
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&s.empty[stage], phase ^ 1u, wc)) {
-          aborted = true;
-          break;
-        }
+        ok = mbar_wait(&s.empty[stage], phase ^ 1u, wc);
+        if (!ok) break;
         uint8_t* sa = ring + stage * kStage;
-        uint8_t* sb = sa + kATile;
-        uint64_t* bar = &s.full[stage];
-        mbar_arrive_expect_tx(bar, kStage);
-        const int k0 = kb * kBlockK;
-        if constexpr (AMN) {
-          tma_load_2d(sa, &map_a, bar, a0, k0);
-          tma_load_2d(sa + kChunk, &map_a, bar, a0 + 64, k0);
-        } else {
-          tma_load_2d(sa, &map_a, bar, k0, a0);
-        }
-        if constexpr (BMN) {
-#pragma unroll
-          for (int j = 0; j < BN / 64; ++j) tma_load_2d(sb + j * kChunk, &map_b, bar, b0 + 64 * j, k0);
-        } else {
-          tma_load_2d(sb, &map_b, bar, k0, b0);
-        }
+        if (sub == 0) mbar_arrive_expect_tx(&s.full[stage], CG * kStage);
+        const uint32_t bar = full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
+        operand_load<CG, S::AMN, kTileM>(sa, &map_a, bar, a0, kb * kBlockK);
+        operand_load<CG, S::BMN, S::kBRows>(sa + kATile, &map_b, bar, b0 + S::kBRows * sub, kb * kBlockK);
         ++filled;
         if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      if (aborted) {  // copies in flight land before the CTA goes on
+      if (!ok && sub == 0) {  // copies in flight land before the CTA goes on
         for (int i = 0; i < stages; ++i) {
           const int f = filled > i ? (filled - i + stages - 1) / stages : 0;
           if (f > 0) (void)mbar_wait_drain(&s.full[i], (f - 1) & 1, 100000000ull);
@@ -237,64 +325,66 @@ __global__ void __launch_bounds__(kSplitThreads)
       }
     }
   } else if (warp == 1) {
-    const uint32_t idesc = dense_idesc(kTileM, BN, AMN, BMN, p.type == MOE_BF16 ? 1u : 0u);
-    int stage = 0, done = 0;
-    uint32_t phase = 0;
-    bool aborted = false;
-    for (int i = 0; i < nkb && !aborted; ++i) {
-      const int chunk = i / chunk_blocks, slot = chunk & 1;
-      const bool fresh = i % chunk_blocks == 0;
-      if (fresh && chunk >= 2 &&
-          !__all_sync(0xffffffffu, mbar_wait(&s.tempty[slot], ((chunk >> 1) - 1) & 1, wc))) {
-        aborted = true;
-        break;
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait(&s.full[stage], phase, wc))) {
-        aborted = true;
-        break;
-      }
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t a = smem_u32(ring + stage * kStage), b = a + kATile;
-#pragma unroll
-        for (int kk = 0; kk < kBlockK / kMmaK; ++kk) {
-          const uint64_t ad = AMN ? smem_desc_sw128(a + kk * 2048, kChunk, 1024)
-                                  : smem_desc_sw128(a + kk * 32, 16, 1024);
-          const uint64_t bd = BMN ? smem_desc_sw128(b + kk * 2048, kChunk, 1024)
-                                  : smem_desc_sw128(b + kk * 32, 16, 1024);
-          umma_bf16<1>(tmem + slot * BN, ad, bd, idesc, (fresh && kk == 0) ? 0u : 1u);
+    // one thread waits, issues and commits: between two blocks there is
+    // nothing for the others to do, and every warp-wide step is latency that
+    // the tensor core would idle through
+    if (sub == 0 && elect_one()) {
+      const uint32_t idesc = dense_idesc(kTileM * CG, BN, S::AMN, S::BMN, p.type == MOE_BF16 ? 1u : 0u);
+      const uint32_t base = smem_u32(ring);
+      int stage = 0, done = 0, left = nkb;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int chunk = 0; left > 0 && ok; ++chunk) {
+        const int n = min(left, chunk_blocks);
+        const int slot = chunk & 1;
+        if (chunk >= 2) ok = wait_any<CG>(&s.tempty[slot], ((chunk >> 1) - 1) & 1, wc);
+        tc_fence_after();
+        uint32_t add = 0u;
+        for (int i = 0; i < n && ok; ++i) {
+          ok = wait_any<CG>(&s.full[stage], phase, wc);
+          if (!ok) break;
+          tc_fence_after();
+          issue_block<CG, S::AMN, S::BMN>(tmem + slot * BN, base + stage * kStage,
+                                          base + stage * kStage + kATile, idesc, add);
+          add = 1u;
+          if constexpr (CG == 2) umma_commit_pair(&s.empty[stage], even);
+          else umma_commit<1>(&s.empty[stage]);
+          ++done;
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        umma_commit<1>(&s.empty[stage]);
-        if (i + 1 == nkb || (i + 1) % chunk_blocks == 0) umma_commit<1>(&s.tfull[slot]);
+        if (ok) {
+          if constexpr (CG == 2) umma_commit_pair(&s.tfull[slot], even);
+          else umma_commit<1>(&s.tfull[slot]);
+        }
+        left -= n;
       }
-      __syncwarp();
-      ++done;
-      if (++stage == stages) {
-        stage = 0;
-        phase ^= 1u;
+      if (!ok && done > 0) {  // issued products end before TMEM is freed
+        const int last = (done - 1) % stages;
+        (void)mbar_wait_drain(&s.empty[last], ((done - last + stages - 1) / stages - 1) & 1, 100000000ull);
       }
-    }
-    if (aborted && done > 0) {  // issued products end before TMEM is freed
-      const int last = (done - 1) % stages;
-      (void)mbar_wait_drain(&s.empty[last], ((done - last + stages - 1) / stages - 1) & 1, 100000000ull);
     }
   } else {
-    // drain the accumulators into registers, chunk by chunk
-    const int q = warp & 3;  // TMEM lane quarter of this warp
-    const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    float acc[BN];
+    // drain the accumulators into registers, chunk by chunk: rows 32 q.. of
+    // this CTA's 128, columns kAcc half..
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tq = tmem + half * S::kAcc + (static_cast<uint32_t>(q * 32) << 16);
+    float acc[S::kAcc];
 #pragma unroll
-    for (int j = 0; j < BN; ++j) acc[j] = 0.0f;
+    for (int j = 0; j < S::kAcc; ++j) acc[j] = 0.0f;
     const int chunks = (nkb + chunk_blocks - 1) / chunk_blocks;
+    const uint32_t tempty0 = CG == 2 ? mapa_shared(smem_u32(&s.tempty[0]), even) : 0u;
     bool ok = true;
     for (int c = 0; c < chunks; ++c) {
       const int slot = c & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(&s.tfull[slot], (c >> 1) & 1, wc));
+      ok = warp_wait(&s.tfull[slot], (c >> 1) & 1, wc);
       if (!ok) break;
       tc_fence_after();
-      if constexpr (BN >= 32) {
+      if constexpr (S::kAcc >= 32) {
 #pragma unroll
-        for (int j = 0; j < BN; j += 32) {
+        for (int j = 0; j < S::kAcc; j += 32) {
           uint32_t v[32];
           tmem_ld_32x32b_x32(tq + slot * BN + j, v);
           tmem_ld_wait();
@@ -310,63 +400,79 @@ __global__ void __launch_bounds__(kSplitThreads)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.tempty[slot]);
+      if (lane == 0) {
+        if (CG == 2 && sub != 0) mbar_arrive_remote(tempty0 + slot * static_cast<uint32_t>(sizeof(uint64_t)));
+        else mbar_arrive(&s.tempty[slot]);
+      }
     }
     // every product has read its operands: the ring now holds the partial
     // tile, in the output's orientation
     if (ok) {
       float* part = reinterpret_cast<float*>(ring);
       const int r = q * 32 + lane;
-      if constexpr (SWAP) {
+      if constexpr (S::SWAP) {
 #pragma unroll
-        for (int j = 0; j < BN; ++j) part[j * (kTileM + 4) + r] = acc[j];
+        for (int j = 0; j < S::kAcc; ++j) part[j * S::kLd + r] = acc[j];
       } else {
 #pragma unroll
-        for (int j = 0; j < BN; j += 4)
-          *reinterpret_cast<float4*>(part + r * (BN + 4) + j) =
+        for (int j = 0; j < S::kAcc; j += 4)
+          *reinterpret_cast<float4*>(part + r * S::kLd + half * S::kAcc + j) =
               make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
       }
     }
   }
   __syncwarp();
-  if (splits > 1) cluster_sync();
+  if (clustered) cluster_sync();
   else __syncthreads();
 
-  // this CTA's rows of the tile: the sum over the partials, and the epilogue
-  constexpr int kRows = SWAP ? BN : kTileM, kColsOut = SWAP ? kTileM : BN, kLd = kColsOut + 4;
-  const int64_t row0 = SWAP ? b0 : a0, col0 = SWAP ? a0 : b0;
-  const int r0 = kRows * rank / splits, r1 = kRows * (rank + 1) / splits;
+  // this CTA's share of the tile's rows: the sum over the partials of the
+  // splits, and the epilogue, four groups of four columns at a time where
+  // there are as many
+  constexpr int kPer = S::kColsOut / 4;
+  const int64_t row0 = S::SWAP ? b0 : a0, col0 = S::SWAP ? a0 : b0;
+  const int r0 = S::kRowsOut * split / splits, r1 = S::kRowsOut * (split + 1) / splits;
   const uint32_t base = smem_u32(ring);
-  for (int i = threadIdx.x; i < (r1 - r0) * (kColsOut / 4); i += kSplitThreads) {
-    const int r = r0 + i / (kColsOut / 4), cc = (i % (kColsOut / 4)) * 4;
-    const int64_t row = row0 + r, col = col0 + cc;
-    if (row >= p.M || col >= p.N) continue;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const uint32_t at = base + static_cast<uint32_t>(r * kLd + cc) * 4;
-    if (splits > 1) {
-#pragma unroll 8
-      for (int q = 0; q < splits; ++q) {
-        const float4 f = ld_cluster_f4(mapa_shared(at, q));
-        v[0] += f.x;
-        v[1] += f.y;
-        v[2] += f.z;
-        v[3] += f.w;
-      }
-    } else {
-      const float4 f = *reinterpret_cast<const float4*>(ring + (at - base));
-      v[0] = f.x;
-      v[1] = f.y;
-      v[2] = f.z;
-      v[3] = f.w;
+  auto finish = [&](auto groups, int i) {  // `groups` groups from the i-th on
+    constexpr int G = decltype(groups)::value;
+    float v[G][4];
+    int64_t row[G], col[G];
+    bool on[G];
+    uint32_t at[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int k = i + g * S::kThreads;
+      const int r = r0 + k / kPer, cc = (k % kPer) * 4;
+      on[g] = row0 + r < p.M && col0 + cc < p.N;
+      row[g] = min(row0 + r, p.M - 1);
+      col[g] = min(col0 + cc, p.N - 4);
+      at[g] = base + static_cast<uint32_t>(r * S::kLd + cc) * 4;
+      v[g][0] = v[g][1] = v[g][2] = v[g][3] = 0.0f;
     }
-    epilogue4_any(v, row, col, p);
-  }
+#pragma unroll 2
+    for (int q = 0; q < splits; ++q) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float4 f;
+        if (splits > 1) f = ld_cluster_f4(mapa_shared(at[g], q * CG + sub));
+        else f = *reinterpret_cast<const float4*>(ring + (at[g] - base));
+        v[g][0] += f.x;
+        v[g][1] += f.y;
+        v[g][2] += f.z;
+        v[g][3] += f.w;
+      }
+    }
+    epilogue4_any<G>(v, row, col, on, p);
+  };
+  const int total = (r1 - r0) * kPer;
+  int i = threadIdx.x;
+  for (; i + 3 * S::kThreads < total; i += 4 * S::kThreads) finish(std::integral_constant<int, 4>{}, i);
+  for (; i < total; i += S::kThreads) finish(std::integral_constant<int, 1>{}, i);
   tc_fence_before();
   __syncthreads();
-  if (splits > 1) cluster_sync();  // the others have read this CTA's partial tile
+  if (clustered) cluster_sync();  // the others have read this CTA's partial tile
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc<1>(tmem, kCols);
+    tmem_dealloc<CG>(tmem, S::kCols);
   }
 }
 
@@ -402,21 +508,6 @@ struct PairParams {
   int32_t* status;
   uint64_t limit_ns;
 };
-
-template <int ACT>
-__device__ __forceinline__ void act32(float (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = act_value<false>(v[i], ACT);
-}
-__device__ __forceinline__ void act32_any(float (&v)[32], int act) {
-  switch (act) {
-    case MOE_ACT_RELU: act32<MOE_ACT_RELU>(v); break;
-    case MOE_ACT_GELU: act32<MOE_ACT_GELU>(v); break;
-    case MOE_ACT_GELU_TANH: act32<MOE_ACT_GELU_TANH>(v); break;
-    case MOE_ACT_SILU: act32<MOE_ACT_SILU>(v); break;
-    default: break;
-  }
-}
 
 // Half h (32 columns) of row `lane` of a 128-byte-swizzled buffer.
 __device__ __forceinline__ uint4* buf_unit(uint8_t* buf, int lane, int h, int j) {
@@ -509,7 +600,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (warp == 0) {
     // producer: this CTA's operands; both CTAs' bytes complete on the even
     // CTA's barrier
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0, filled = 0;
       uint32_t phase = 0;
       const uint32_t full0 = mapa_shared(smem_u32(&s.full[0]), 0);
@@ -542,46 +633,35 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (leader) {
+    if (leader && elect_one()) {  // as in the split kernel, one thread
+      const uint32_t base = smem_u32(ring);
       int stage = 0, done = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      bool aborted = false;
-      for (int t = blockIdx.x / 2; t < ntiles && !aborted; t += units) {
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&s.tempty[acc], acc_phase ^ 1u, wc))) {
-          aborted = true;
-          break;
-        }
+      bool ok = true;
+      for (int t = blockIdx.x / 2; t < ntiles && ok; t += units) {
+        ok = mbar_wait_cluster(&s.tempty[acc], acc_phase ^ 1u, wc);
+        if (!ok) break;
         tc_fence_after();
+        uint32_t add = 0u;
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!__all_sync(0xffffffffu, mbar_wait_cluster(&s.full[stage], phase, wc))) {
-            aborted = true;
-            break;
-          }
+          ok = mbar_wait_cluster(&s.full[stage], phase, wc);
+          if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t a = smem_u32(ring + stage * kPairStage), b = a + kATile;
-#pragma unroll
-            for (int kk = 0; kk < kBlockK / kMmaK; ++kk) {
-              const uint64_t ad = AMN ? smem_desc_sw128(a + kk * 2048, kChunk, 1024)
-                                      : smem_desc_sw128(a + kk * 32, 16, 1024);
-              const uint64_t bd = BMN ? smem_desc_sw128(b + kk * 2048, kChunk, 1024)
-                                      : smem_desc_sw128(b + kk * 32, 16, 1024);
-              umma_bf16<2>(tmem + acc * kPairN, ad, bd, p.idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-            }
-            umma_commit<2>(&s.empty[stage]);
-            if (kb + 1 == p.kblocks) umma_commit<2>(&s.tfull[acc]);
-          }
-          __syncwarp();
+          const uint32_t a = base + stage * kPairStage;
+          issue_block<2, AMN, BMN>(tmem + acc * kPairN, a, a + kATile, p.idesc, add);
+          add = 1u;
+          umma_commit<2>(&s.empty[stage]);
           ++done;
           if (++stage == kPairStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
+        if (ok) umma_commit<2>(&s.tfull[acc]);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      if (aborted && done > 0) {  // issued products end before TMEM is freed
+      if (!ok && done > 0) {  // issued products end before TMEM is freed
         const int last = (done - 1) % kPairStages;
         (void)mbar_wait_drain(&s.empty[last], ((done - last + kPairStages - 1) / kPairStages - 1) & 1,
                               100000000ull);
@@ -625,7 +705,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
       const int y = mt * 256 + 128 * rank + 32 * q;
       const int64_t col0 = static_cast<int64_t>(nt) * kPairN + 128 * half;
-      ok = __all_sync(0xffffffffu, mbar_wait(&s.tfull[acc], acc_phase, wc));
+      // the bias of columns col0 + 32 j + lane, while the products still run
+      float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (FULL && p.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bias[j] = __ldg(p.bias + min(col0 + 32 * j + lane, p.N - 1));
+      }
+      ok = warp_wait(&s.tfull[acc], acc_phase, wc);
       if (!ok) break;
       tc_fence_after();
       const uint32_t tbase = tmem + acc * kPairN + 128 * half + (static_cast<uint32_t>(q * 32) << 16);
@@ -639,7 +725,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           uint8_t* buf = bufs + b * kPairBuf;
           uint8_t* zbuf = bufs + kPairBuf;
           if (p.has_res) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&rbar[b], (rphase >> b) & 1u, wc));
+            ok = warp_wait(&rbar[b], (rphase >> b) & 1u, wc);
             if (!ok) break;
             rphase ^= 1u << b;
             pending &= ~(1 << b);
@@ -661,20 +747,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
             if constexpr (FULL) {
               if (p.bias != nullptr) {
+                const float mine = ch == 0 ? bias[h] : bias[2 + h];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const int64_t c4 = col + 32 * h + 4 * i;
-                  if (c4 < p.N) {
-                    const float4 f = __ldg(reinterpret_cast<const float4*>(p.bias + c4));
-                    v[4 * i] += f.x;
-                    v[4 * i + 1] += f.y;
-                    v[4 * i + 2] += f.z;
-                    v[4 * i + 3] += f.w;
-                  }
-                }
+                for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, mine, i);
               }
               if (with_z) put32<T>(zbuf, lane, h, v);
-              act32_any(v, p.act);
+              act_all<false, 32>(v, p.act);
             }
             if (p.has_res) add32<T>(buf, lane, h, v);
             put32<T>(buf, lane, h, v);
@@ -805,52 +883,61 @@ DenseParams make_params(const DenseCall& c) {
   return p;
 }
 
-template <int BN, bool AMN, bool BMN, bool SWAP>
-cudaError_t launch_split(const DenseCall& c, int splits, int per_sm, cudaStream_t s) {
-  auto kern = dense_split_kernel<BN, AMN, BMN, SWAP>;
+// How the splits of a product are laid out on the device.
+struct SplitPlan {
+  int splits;  // of the reduction: 1, 2, 4 or 8
+  int per_sm;  // CTAs that an SM should be able to hold
+};
+
+template <class S>
+cudaError_t launch_split(const DenseCall& c, const SplitPlan& plan, cudaStream_t s) {
+  auto kern = dense_split_kernel<S>;
   static std::atomic<bool> attr_set[64];
   cudaError_t err = allow_smem(kern, attr_set, kSplitSmemLimit);
   if (err != cudaSuccess) return err;
   const DenseParams p = make_params(c);
   // the 128 side is A's rows; swapped, that is the output's columns
-  const void* a = SWAP ? c.b : c.a;
-  const void* b = SWAP ? c.a : c.b;
-  const int64_t lda = SWAP ? c.ldb : c.lda, ldb = SWAP ? c.lda : c.ldb;
-  const int64_t na = SWAP ? c.N : c.M, nb = SWAP ? c.M : c.N;
+  const void* a = S::SWAP ? c.b : c.a;
+  const void* b = S::SWAP ? c.a : c.b;
+  const int64_t lda = S::SWAP ? c.ldb : c.lda, ldb = S::SWAP ? c.lda : c.ldb;
+  const int64_t na = S::SWAP ? c.N : c.M, nb = S::SWAP ? c.M : c.N;
   CUtensorMap ma, mb;
-  const bool ok = (AMN ? map2d(&ma, a, na, c.Kred, lda, 64, kBlockK)
-                       : map2d(&ma, a, c.Kred, na, lda, kBlockK, kTileM)) &&
-                  (BMN ? map2d(&mb, b, nb, c.Kred, ldb, 64, kBlockK)
-                       : map2d(&mb, b, c.Kred, nb, ldb, kBlockK, BN));
+  const bool ok = (S::AMN ? map2d(&ma, a, na, c.Kred, lda, 64, kBlockK)
+                          : map2d(&ma, a, c.Kred, na, lda, kBlockK, kTileM)) &&
+                  (S::BMN ? map2d(&mb, b, nb, c.Kred, ldb, 64, kBlockK)
+                          : map2d(&mb, b, c.Kred, nb, ldb, kBlockK, S::kBRows));
   if (!ok) return cudaErrorInvalidValue;
-  constexpr int kStage = split_stage_bytes(BN);
-  constexpr int kPart = split_partial_bytes(BN, SWAP);
   // no more stages than reduction blocks, no fewer than the partial tile
-  // needs, and enough that the CTAs of an SM never ask for more than its
-  // 512 tensor-memory columns
-  constexpr int kFloorBytes = 228 * 1024 / (512 / tmem_cols(2 * BN) + 1) + 1024;
-  constexpr int kLeast = std::max({2, (kPart + kStage - 1) / kStage, (kFloorBytes + kStage - 1) / kStage});
-  const int budget = (kSplitSmemLimit / per_sm) - 2048 - static_cast<int>(sizeof(SplitCtl));
-  const int mine = static_cast<int>(cdiv(p.kblocks, splits));
-  int stages = std::min({budget / kStage, kSplitMaxStages, std::max(mine, 2)});
-  stages = std::max(stages, kLeast);
-  static_assert(kLeast <= kSplitMaxStages, "stages");
-  static_assert(kLeast * kStage + 1024 + static_cast<int>(sizeof(SplitCtl)) <= kSplitSmemLimit, "shared memory");
-  const size_t bytes = 1024 + static_cast<size_t>(stages) * kStage + sizeof(SplitCtl);
+  // needs, and so many that CTAs that fit an SM's shared memory together never
+  // ask for more than its 512 tensor-memory columns: clusters that overlap
+  // (on two streams) would otherwise wait for each other's columns.  The
+  // smallest CTA takes 38 KB, which is not left beside one with 512 columns.
+  constexpr int kFloorBytes =
+      S::kCols == 512 ? 192 * 1024 : 228 * 1024 / (512 / S::kCols + 1) + 1024;
+  constexpr int kLeast =
+      std::max({2, (S::kPartial + S::kStage - 1) / S::kStage, (kFloorBytes + S::kStage - 1) / S::kStage});
+  constexpr int kOver = 1024 + static_cast<int>(sizeof(SplitCtl));
+  static_assert(kLeast <= kSplitMaxStages && kLeast * S::kStage + kOver <= kSplitSmemLimit, "shared memory");
+  const int budget = kSplitSmemLimit / plan.per_sm - kOver - 1024;
+  const int mine = static_cast<int>(cdiv(p.kblocks, plan.splits));
+  const int stages = std::max(kLeast, std::min({budget / S::kStage, kSplitMaxStages, mine}));
+  const size_t bytes = static_cast<size_t>(stages) * S::kStage + kOver;
   const int chunk = c.out_type == MOE_FP32 ? kChunkBlocks : p.kblocks;
+  const unsigned ctas = static_cast<unsigned>(S::CG * plan.splits);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(na, kTileM) * splits), static_cast<unsigned>(cdiv(nb, BN)), 1);
-  cfg.blockDim = dim3(kSplitThreads, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(na, kTileM * S::CG)) * ctas,
+                     static_cast<unsigned>(cdiv(nb, S::BN)), 1);
+  cfg.blockDim = dim3(S::kThreads, 1, 1);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mb, p, stages, splits, chunk);
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, p, stages, plan.splits, chunk);
 }
 
 template <bool MN>
@@ -918,12 +1005,11 @@ cudaError_t launch_pair_type(const DenseCall& c, cudaStream_t s) {
   return launch_pair<T, false, false, false>(c, s);
 }
 
-// The splits of the reduction (1, 2, 4 or 8) for `tiles` tiles: as many as
-// the SMs take in one wave of one CTA each, with at least two reduction
-// blocks for each.
-int pick_splits(int64_t tiles, int64_t kblocks) {
+// The splits of the reduction for `tiles` tiles of `ctas` CTAs: as many as
+// fit `room` CTAs, up to `most`, with at least two reduction blocks for each.
+int pick_splits(int64_t tiles, int64_t kblocks, int ctas, int64_t room, int most) {
   int s = 1;
-  while (s < 8 && tiles * (s * 2) <= sm_count() && kblocks >= 4 * s) s *= 2;
+  while (s < most && tiles * ctas * (s * 2) <= room && kblocks >= 4 * s) s *= 2;
   return s;
 }
 
@@ -931,26 +1017,34 @@ int pick_splits(int64_t tiles, int64_t kblocks) {
 
 cudaError_t launch_dense(const DenseCall& c, cudaStream_t s) {
   const int64_t kb = cdiv(c.Kred, kBlockK);
+  const int64_t sms = sm_count();
   // few rows: the weights' columns on the 128 side (wgrads have none: their
-  // rows are a weight axis too)
+  // rows are a weight axis too).  Two CTAs per SM, so that clusters of eight
+  // find room beside one another.
   if (!c.a_mn && c.M <= 64) {
-    const int splits = pick_splits(cdiv(c.N, kTileM), kb);
+    const SplitPlan plan{pick_splits(cdiv(c.N, kTileM), kb, 1, sms, 8), 2};
     if (c.M <= 16)
-      return c.b_mn ? launch_split<16, true, false, true>(c, splits, 1, s)
-                    : launch_split<16, false, false, true>(c, splits, 1, s);
+      return c.b_mn ? launch_split<SplitShape<16, 1, true, false, true>>(c, plan, s)
+                    : launch_split<SplitShape<16, 1, false, false, true>>(c, plan, s);
     if (c.M <= 32)
-      return c.b_mn ? launch_split<32, true, false, true>(c, splits, 1, s)
-                    : launch_split<32, false, false, true>(c, splits, 1, s);
-    return c.b_mn ? launch_split<64, true, false, true>(c, splits, 1, s)
-                  : launch_split<64, false, false, true>(c, splits, 1, s);
+      return c.b_mn ? launch_split<SplitShape<32, 1, true, false, true>>(c, plan, s)
+                    : launch_split<SplitShape<32, 1, false, false, true>>(c, plan, s);
+    return c.b_mn ? launch_split<SplitShape<64, 1, true, false, true>>(c, plan, s)
+                  : launch_split<SplitShape<64, 1, false, false, true>>(c, plan, s);
   }
   const int64_t pair_tiles = cdiv(c.M, 256) * cdiv(c.N, kPairN);
-  if (c.out_type != MOE_FP32 && 3 * pair_tiles >= sm_count())
+  if (c.out_type != MOE_FP32 && 2 * pair_tiles * 3 >= sms)
     return c.type == MOE_BF16 ? launch_pair_type<__nv_bfloat16>(c, s) : launch_pair_type<__half>(c, s);
-  const int splits = pick_splits(cdiv(c.M, kTileM) * cdiv(c.N, 128), kb);
-  if (c.a_mn) return launch_split<128, true, true, false>(c, splits, 2, s);
-  if (c.b_mn) return launch_split<128, false, true, false>(c, splits, 2, s);
-  return launch_split<128, false, false, false>(c, splits, 2, s);
+  if (2 * pair_tiles * 6 >= sms) {
+    const SplitPlan plan{pick_splits(pair_tiles, kb, 2, sms, 4), 1};
+    if (c.a_mn) return launch_split<SplitShape<256, 2, true, true, false>>(c, plan, s);
+    if (c.b_mn) return launch_split<SplitShape<256, 2, false, true, false>>(c, plan, s);
+    return launch_split<SplitShape<256, 2, false, false, false>>(c, plan, s);
+  }
+  const SplitPlan plan{pick_splits(cdiv(c.M, kTileM) * cdiv(c.N, 128), kb, 1, sms, 8), 2};
+  if (c.a_mn) return launch_split<SplitShape<128, 1, true, true, false>>(c, plan, s);
+  if (c.b_mn) return launch_split<SplitShape<128, 1, false, true, false>>(c, plan, s);
+  return launch_split<SplitShape<128, 1, false, false, false>>(c, plan, s);
 }
 
 }  // namespace moe

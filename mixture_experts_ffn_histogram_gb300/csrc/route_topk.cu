@@ -93,19 +93,6 @@ __device__ __forceinline__ float warp_max_f32(float v) {
 // A logit with NaN taken as masked (the maximum of NaN and a number is the number).
 __device__ __forceinline__ float clean(float l) { return fmaxf(l, kNegInf); }
 
-// 2^x to 2 ulp and 1 / x to 1 ulp, subnormals flushed.
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-constexpr float kLog2e = 1.4426950408889634f;
-
 // The score of one logit in fp64; m and inv_total are the softmax's.
 template <bool SOFTMAX>
 __device__ __forceinline__ double score_fp64(float l, double m, double inv_total) {
