@@ -39,6 +39,21 @@ __device__ __forceinline__ void load8(const Y* p, float (&f)[8]) {
   }
 }
 
+// g *= act'(z), with one branch on the activation.
+template <int ACT>
+__device__ __forceinline__ void slope_run(const float (&z)[8], float (&g)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[j] *= act_slope<false>(z[j], ACT);
+}
+__device__ __forceinline__ void slope_all(const float (&z)[8], float (&g)[8], int act) {
+  switch (act) {
+    case MOE_ACT_RELU: slope_run<MOE_ACT_RELU>(z, g); break;
+    case MOE_ACT_GELU: slope_run<MOE_ACT_GELU>(z, g); break;
+    case MOE_ACT_GELU_TANH: slope_run<MOE_ACT_GELU_TANH>(z, g); break;
+    default: slope_run<MOE_ACT_SILU>(z, g); break;
+  }
+}
+
 // Blocks of col_threads x (kThreads / col_threads) threads, eight columns a thread.
 template <typename T, typename Y>
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradArgs<T, Y> p) {
@@ -52,22 +67,26 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradArgs<T,
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
   if (col < p.N) {
-#pragma unroll 2
-    for (int64_t r = r0 + ty; r < r1; r += nrow) {
-      float g[8];
-      load8<Y>(p.dy + r * p.lddy + col, g);
-      if (p.act != MOE_ACT_NONE) {
-        float z[8];
-        load8<T>(p.z + r * p.ldz + col, z);
+    // four rows at a time: their loads are under way together
+    for (int64_t r = r0 + ty; r < r1; r += 4 * nrow) {
+      float g[4][8], z[4][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] *= act_slope<false>(z[j], p.act);
+      for (int k = 0; k < 4; ++k) {
+        const int64_t rk = min(r + k * nrow, p.M - 1);
+        load8<Y>(p.dy + rk * p.lddy + col, g[k]);
+        if (p.act != MOE_ACT_NONE) load8<T>(p.z + rk * p.ldz + col, z[k]);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += g[j];
-      if (p.dz != nullptr) {
-        Raw<T, 8> o;
-        o.pack(g);
-        o.store(p.dz + r * p.N + col, 0);
+      for (int k = 0; k < 4; ++k) {
+        if (r + k * nrow >= r1) break;
+        if (p.act != MOE_ACT_NONE) slope_all(z[k], g[k], p.act);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += g[k][j];
+        if (p.dz != nullptr) {
+          Raw<T, 8> o;
+          o.pack(g[k]);
+          o.store(p.dz + (r + k * nrow) * p.N + col, 0);
+        }
       }
     }
   }

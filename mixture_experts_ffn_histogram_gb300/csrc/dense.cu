@@ -19,8 +19,9 @@
 // 128 rows of A and its 128 columns of B, the even CTA issues
 // tcgen05.mma.cta_group::2 (M = 256, N = 256), and each CTA's tensor memory
 // holds its 128 rows twice (the next tile's products overlap the epilogue).
-// Eight epilogue warps take a quarter of the rows and half of the columns
-// each; results, z and the residual move through swizzled shared-memory
+// Sixteen epilogue warps take a quarter of the rows and of the columns each
+// (one warp's chain of waits, loads and stores is latency: fewer warps leave
+// the epilogue behind short reductions); results, z and the residual move through swizzled shared-memory
 // buffers by TMA, the residual of the next tile while its products run.
 //
 // In the split kernel, for fp32 results the accumulators are drained into registers every
@@ -478,24 +479,26 @@ __global__ void __launch_bounds__(S::kThreads)
 
 // ------------------------------------------------------------ pair kernel
 constexpr int kPairN = 256;
-constexpr int kPairStages = 5;
-constexpr int kPairEpiWarps = 8;
+constexpr int kPairEpiWarps = 16;
 constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
 constexpr int kPairStage = 2 * kATile;          // per CTA: 128 A rows, 128 B columns
 constexpr int kPairBuf = 32 * 128;              // 32 rows x 64 columns, 16-bit
-constexpr int kPairBufs = 2;                    // per epilogue warp
+constexpr int kPairStages = 5;
 
 struct PairCtl {
   uint64_t full[kPairStages];
   uint64_t empty[kPairStages];
   uint64_t tfull[2];
   uint64_t tempty[2];
-  uint64_t rbar[kPairEpiWarps][kPairBufs];  // a residual chunk landed in the buffer
+  uint64_t rbar[kPairEpiWarps];  // a residual chunk landed in the warp's buffer
   uint32_t tmem_base;
   int abort_flag;
 };
+// The ring takes what the staging buffers leave: with three stages and two
+// buffers per warp, 32768 x 704 -> 2816 takes 126 us instead of 108, and
+// every longer reduction more.
 constexpr size_t kPairSmem = 1024 + static_cast<size_t>(kPairStages) * kPairStage +
-                             kPairEpiWarps * kPairBufs * kPairBuf + sizeof(PairCtl);
+                             kPairEpiWarps * kPairBuf + sizeof(PairCtl);
 static_assert(kPairSmem <= 227 * 1024, "shared memory");
 
 struct PairParams {
@@ -504,6 +507,8 @@ struct PairParams {
   int kblocks, m_tiles, n_tiles, act;
   int a_chunks, b_chunks;  // MN-major operands: one box of two 64-wide chunks (3-D map)
   int has_res, has_z;
+  const void* res;
+  int64_t ldres;
   uint32_t idesc;
   int32_t* status;
   uint64_t limit_ns;
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* epi = ring + kPairStages * kPairStage;
-  PairCtl& s = *reinterpret_cast<PairCtl*>(epi + kPairEpiWarps * kPairBufs * kPairBuf);
+  PairCtl& s = *reinterpret_cast<PairCtl*>(epi + kPairEpiWarps * kPairBuf);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const bool leader = rank == 0;
@@ -581,8 +586,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&s.tfull[i], 1);
       mbar_init(&s.tempty[i], 2 * kPairEpiWarps);
     }
-    for (int i = 0; i < kPairEpiWarps; ++i)
-      for (int j = 0; j < kPairBufs; ++j) mbar_init(&s.rbar[i][j], 1);
+    for (int i = 0; i < kPairEpiWarps; ++i) mbar_init(&s.rbar[i], 1);
     s.abort_flag = 0;
     mbar_fence_init();
   }
@@ -668,112 +672,122 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     }
   } else {
-    // epilogue: rows 32 q.. of this CTA's 128, columns 128 half.. of the tile's 256
-    const int ew = warp - 2, q = warp & 3, half = ew >> 2;
-    uint8_t* bufs = epi + ew * kPairBufs * kPairBuf;
-    uint64_t* rbar = s.rbar[ew];
+    // epilogue: rows 32 q.. of this CTA's 128, columns 64 part.. of the
+    // tile's 256.  A residual comes by TMA, one tile ahead, into the buffer
+    // from which the result is stored.  With z the buffer is used for z and
+    // then for the result, and a residual is read by the threads.
+    const int ew = warp - 2, q = warp & 3, part = ew >> 2;
+    uint8_t* buf = epi + ew * kPairBuf;
+    uint64_t* rbar = &s.rbar[ew];
     const uint32_t tempty_peer = mapa_shared(smem_u32(&s.tempty[0]), 0);
-    uint32_t rphase = 0;  // bit b: parity of buffer b's next residual
-    int pending = 0;      // bit b: a residual load into buffer b is in flight
-    uint32_t stored = 0;  // chunks stored so far
-    // without z both buffers hold results; with z buffer 1 stages z, and a
-    // chunk's residual can only be fetched when the one before is stored
     const bool with_z = FULL && p.has_z;
-    auto fetch_res = [&](int y, int64_t col, int b) {
-      if (y >= p.M || col >= p.N) return;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&rbar[b], kPairBuf);
-        tma_load_2d(bufs + b * kPairBuf, &map_r, &rbar[b], static_cast<int>(col), y);
-      }
-      pending |= 1 << b;
-    };
-    auto prefetch_tile = [&](int t) {
-      if (!p.has_res || t >= ntiles) return;
-      if (lane == 0) bulk_wait_read<0>();
-      __syncwarp();
+    const bool res_tma = p.has_res && !with_z;
+    const int unit = blockIdx.x / 2;
+    auto place = [&](int t, int& y, int64_t& col) -> bool {  // of this warp's chunk of tile t
       const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
-      const int y = mt * 256 + 128 * rank + 32 * q;
-      const int64_t col = static_cast<int64_t>(nt) * kPairN + 128 * half;
-      fetch_res(y, col, 0);
-      if (!with_z) fetch_res(y, col + 64, 1);
+      y = mt * 256 + 128 * rank + 32 * q;
+      col = static_cast<int64_t>(nt) * kPairN + 64 * part;
+      return y < p.M && col < p.N;
     };
-    prefetch_tile(blockIdx.x / 2);
+    bool flying = false;  // a residual is under way
+    uint32_t rphase = 0;
+    auto fetch = [&](int t) {  // the residual of this warp's next chunk, from tile t on
+      int y;
+      int64_t col;
+      while (t < ntiles && !place(t, y, col)) t += units;
+      if (t >= ntiles) return;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(rbar, kPairBuf);
+        tma_load_2d(buf, &map_r, rbar, static_cast<int>(col), y);
+      }
+      __syncwarp();
+      flying = true;
+    };
+    if (res_tma) fetch(unit);
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int t = blockIdx.x / 2; t < ntiles; t += units) {
-      const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
-      const int y = mt * 256 + 128 * rank + 32 * q;
-      const int64_t col0 = static_cast<int64_t>(nt) * kPairN + 128 * half;
-      // the bias of columns col0 + 32 j + lane, while the products still run
-      float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (FULL && p.bias != nullptr) {
+    for (int t = unit; t < ntiles; t += units) {
+      int y;
+      int64_t col;
+      const bool mine = place(t, y, col);
+      float bias[2] = {0.0f, 0.0f};  // of columns col + 32 h + lane, while the products still run
+      if (FULL && mine && p.bias != nullptr) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bias[j] = __ldg(p.bias + min(col0 + 32 * j + lane, p.N - 1));
+        for (int h = 0; h < 2; ++h) bias[h] = __ldg(p.bias + min(col + 32 * h + lane, p.N - 1));
       }
       ok = warp_wait(&s.tfull[acc], acc_phase, wc);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t tbase = tmem + acc * kPairN + 128 * half + (static_cast<uint32_t>(q * 32) << 16);
-      if (y < p.M) {
-#pragma unroll 1
-        for (int ch = 0; ch < 2; ++ch) {
-          const int64_t col = col0 + 64 * ch;
-          if (col >= p.N) break;
-          // residuals were fetched into buffer ch; results alone alternate
-          const int b = with_z ? 0 : (p.has_res ? ch : (stored & 1));
-          uint8_t* buf = bufs + b * kPairBuf;
-          uint8_t* zbuf = bufs + kPairBuf;
-          if (p.has_res) {
-            ok = warp_wait(&rbar[b], (rphase >> b) & 1u, wc);
-            if (!ok) break;
-            rphase ^= 1u << b;
-            pending &= ~(1 << b);
-          } else if (!with_z) {
-            // the buffer's last store has read it; the one since may be pending
-            if (lane == 0) bulk_wait_read<1>();
-            __syncwarp();
-          } else {
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
+      const uint32_t tbase = tmem + acc * kPairN + 64 * part + (static_cast<uint32_t>(q * 32) << 16);
+      if (mine) {
+        if (res_tma) {
+          ok = warp_wait(rbar, rphase, wc);
+          if (!ok) break;
+          rphase ^= 1u;
+          flying = false;
+        } else {
+          if (lane == 0) bulk_wait_read<0>();  // the buffer's last store has read it
+          __syncwarp();
+        }
+        auto values = [&](int h, float (&v)[32]) {  // z of half h
+          uint32_t raw[32];
+          tmem_ld_32x32b_x32(tbase + 32 * h, raw);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+          if (FULL && p.bias != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, h == 0 ? bias[0] : bias[1], i);
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t raw[32];
-            float v[32];
-            tmem_ld_32x32b_x32(tbase + 64 * ch + 32 * h, raw);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
-            if constexpr (FULL) {
-              if (p.bias != nullptr) {
-                const float mine = ch == 0 ? bias[h] : bias[2 + h];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, mine, i);
-              }
-              if (with_z) put32<T>(zbuf, lane, h, v);
-              act_all<false, 32>(v, p.act);
-            }
-            if (p.has_res) add32<T>(buf, lane, h, v);
-            put32<T>(buf, lane, h, v);
-          }
+        };
+        auto send = [&](const CUtensorMap* map) {  // the staged chunk
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&map_c, buf, static_cast<int>(col), y);
-            if (with_z) tma_store_2d(&map_z, zbuf, static_cast<int>(col), y);
+            tma_store_2d(map, buf, static_cast<int>(col), y);
             bulk_commit();
           }
-          ++stored;
-          if (with_z && p.has_res && ch == 0) {
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
-            fetch_res(y, col + 64, 0);
+        };
+        if (with_z) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[32];
+            values(h, v);
+            put32<T>(buf, lane, h, v);
           }
+          send(&map_z);
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[32];
+          values(h, v);
+          if constexpr (FULL) act_all<false, 32>(v, p.act);
+          if (res_tma) {
+            add32<T>(buf, lane, h, v);
+          } else if (p.has_res && y + lane < p.M) {
+            const T* r = static_cast<const T*>(p.res) + (y + lane) * p.ldres + col + 32 * h;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (col + 32 * h + 8 * j >= p.N) break;
+              const uint4 u = *reinterpret_cast<const uint4*>(r + 8 * j);
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack_pair(w[i], T{});
+                v[8 * j + 2 * i] += f.x;
+                v[8 * j + 2 * i + 1] += f.y;
+              }
+            }
+          }
+          put32<T>(buf, lane, h, v);
+        }
+        // the accumulator is read: the next tile's products may overwrite it
+        tc_fence_before();
+        send(&map_c);
       }
-      if (!ok) break;
-      tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (leader) mbar_arrive(&s.tempty[acc]);
@@ -781,11 +795,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
-      prefetch_tile(t + units);
+      if (res_tma && mine) {  // once the store has read the buffer
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        fetch(t + units);
+      }
     }
-    // residuals in flight land (an abort left them), every store is done
-    for (int b = 0; b < kPairBufs; ++b)
-      if ((pending >> b) & 1) (void)mbar_wait_drain(&rbar[b], (rphase >> b) & 1u, 100000000ull);
+    // a residual in flight lands (an abort left it), every store is done
+    if (flying) (void)mbar_wait_drain(rbar, rphase, 100000000ull);
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
@@ -964,6 +981,8 @@ cudaError_t launch_pair(const DenseCall& c, cudaStream_t s) {
   p.b_chunks = BMN && c.N % 64 == 0;
   p.has_res = c.res != nullptr;
   p.has_z = c.z != nullptr;
+  p.res = c.res;
+  p.ldres = c.ldres;
   p.idesc = dense_idesc(256, kPairN, AMN, BMN, c.type == MOE_BF16 ? 1u : 0u);
   p.status = c.dev_status;
   p.limit_ns = kDefaultWaitLimitNs;
