@@ -5,6 +5,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace moe {
@@ -89,6 +91,76 @@ struct Raw {
   __device__ __forceinline__ void store(T* row, int i) const {
     if constexpr (kVec) reinterpret_cast<uint4*>(row)[i] = v;
     else row[i] = v;
+  }
+};
+
+// Two fp32 values that are computed on together (packed fp32 instructions take
+// one issue slot for two operations), or one, under the same names.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 make_f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(a.v));
+  return f;
+}
+__device__ __forceinline__ F2 fadd(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fmul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 ffma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float fadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float fmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float ffma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float fold(F2 a) {
+  const float2 f = split(a);
+  return f.x + f.y;
+}
+__device__ __forceinline__ float fold(float a) { return a; }
+
+// VEC fp32 values as kN of those.
+template <int VEC>
+struct Nums {
+  static constexpr int kN = VEC == 1 ? 1 : VEC / 2;
+  using F = typename std::conditional<VEC == 1, float, F2>::type;
+  static __device__ __forceinline__ F splat(float v) {
+    if constexpr (VEC == 1) return v;
+    else return make_f2(v, v);
+  }
+  static __device__ __forceinline__ void gather(const float (&f)[VEC], F (&n)[kN]) {
+    if constexpr (VEC == 1) {
+      n[0] = f[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) n[i] = make_f2(f[2 * i], f[2 * i + 1]);
+    }
+  }
+  static __device__ __forceinline__ void scatter(const F (&n)[kN], float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+      f[0] = n[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const float2 q = split(n[i]);
+        f[2 * i] = q.x;
+        f[2 * i + 1] = q.y;
+      }
+    }
   }
 };
 

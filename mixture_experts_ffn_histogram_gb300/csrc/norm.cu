@@ -148,13 +148,16 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormArgs<T>
 }
 
 // ---------------------------------------------------------------- backward
-// Each thread copies its own vectors of a row into its own shared-memory
-// slots with cp.async, up to three rows ahead, and reads back only what it
-// copied: the copies need no barrier, and the bytes in flight do not depend
-// on registers.  A block walks rows with the grid's stride and keeps its
-// columns' weight-gradient sums in registers; at the end they become one row
-// of `partials` ([blocks][2][D]: dgamma, dbeta).
-constexpr int kBwdGroups = 4;  // rows of one warp each per block
+// A block takes R rows at a time (R = 2 where they fit) so that their two sums
+// each share one pass through the warps and one barrier: with one row at a
+// time the chain from a row's load to its store, not HBM, set the rate
+// (32768 x 2816 bf16: 141 us).  Each thread copies its own vectors of a row
+// into its own shared-memory slots with cp.async, one or two steps ahead, and
+// reads back only what it copied: the copies need no barrier, and the bytes
+// in flight do not depend on registers.  A block walks rows with the grid's
+// stride and keeps its columns' weight-gradient sums in registers; at the end
+// they become one row of `partials` ([blocks][2][D]: dgamma, dbeta).
+constexpr int kBwdGroups = 4;  // ONE_WARP: warps of a block, each on rows of its own
 
 template <typename T, int VEC>
 __device__ __forceinline__ void copy_async(void* dst, const T* src) {
@@ -168,104 +171,221 @@ __device__ __forceinline__ void copy_async(void* dst, const T* src) {
   }
 }
 
-template <typename T, typename W, int VEC, int NV, bool ONE_WARP, bool RES>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs<T> p, const int stages) {
-  using R = Raw<T, VEC>;
-  constexpr int kArr = RES ? 3 : 2;
-  __shared__ float red[2][32][2];
+// Sums of N = 2 or 4 values over the threads of a row group.  Within a warp
+// the lanes first halve the values they carry (16, then 8 lanes to a value),
+// so that four values cost 6 exchanges instead of 20; across warps through
+// `red`, which the caller alternates, so that one barrier is enough.
+template <bool ONE_WARP, int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], float (*red)[4], int nwarps) {
+  static_assert(N == 2 || N == 4, "two sums for each of one or two rows");
+  constexpr int kLanes = 32 / N;  // lanes that end up with one value
+  const int lane = threadIdx.x & 31;
+  float c;
+  if constexpr (N == 4) {
+    const bool hi = lane & 16, h8 = lane & 8;
+    float a0 = hi ? v[2] : v[0], a1 = hi ? v[3] : v[1];
+    a0 += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+    a1 += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
+    c = h8 ? a1 : a0;
+    c += __shfl_xor_sync(0xffffffffu, h8 ? a0 : a1, 8);
+  } else {
+    const bool hi = lane & 16;
+    c = hi ? v[1] : v[0];
+    c += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[1], 16);
+    c += __shfl_xor_sync(0xffffffffu, c, 8);
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+  const int which = lane / kLanes, part = lane % kLanes;
+  if constexpr (!ONE_WARP) {
+    if (part == 0) red[threadIdx.x >> 5][which] = c;
+    __syncthreads();
+    c = 0.0f;
+    for (int w = part; w < nwarps; w += kLanes) c += red[w][which];
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, c, i * kLanes);
+}
+
+// Slots of a thread; slot u of all threads lies together, so that a warp's
+// copy fills whole lines (with each thread's slots together instead, the same
+// copies took 192 us where these take 130).
+template <int NV, bool RES, int R>
+__host__ __device__ constexpr int bwd_slots(int steps) { return steps * R * (RES ? 3 : 2) * NV; }
+
+template <typename T, typename W, int VEC, int NV, bool ONE_WARP, bool RES, int R>
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs<T> p, const int steps) {
+  using Q = Raw<T, VEC>;
+  using N = Nums<VEC>;
+  using F = typename N::F;
+  constexpr int kArr = RES ? 3 : 2, kN = N::kN, kPerStep = R * kArr * NV;
+  __shared__ float red[2][kMaxThreads / 32][4];
   extern __shared__ __align__(16) unsigned char stage_mem[];
   const int tpr = ONE_WARP ? 32 : blockDim.x;
   const int t = ONE_WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int groups = ONE_WARP ? (blockDim.x >> 5) : 1;
   const int group = ONE_WARP ? (threadIdx.x >> 5) : 0;
   const int nwarps = blockDim.x >> 5;
-  using Slot = typename R::Store;
-  Slot* slots = reinterpret_cast<Slot*>(stage_mem) + threadIdx.x;
-  auto slot = [&](int stage, int arr, int i) -> Slot* {
-    return slots + ((stage * kArr + arr) * NV + i) * static_cast<int>(blockDim.x);
-  };
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  auto fetch = [&](int64_t row, int stage) {
-    if (row < p.rows) {
+  const int bd = blockDim.x;
+  typename Q::Store* const slots = reinterpret_cast<typename Q::Store*>(stage_mem) + threadIdx.x;
+  // this group's rows: first, first + step, ... (n of them)
+  const int first = blockIdx.x * groups + group, step = gridDim.x * groups;
+  const int n = first < p.rows ? static_cast<int>((p.rows - 1 - first) / step) + 1 : 0;
+  const int64_t sx = step * p.ldx, sr = step * p.ldr, ss = step * p.ldres, sy = step * p.ldy;
+  const T* dy_at = p.x + first * p.ldx + t * VEC;  // of the next row to fetch
+  const T* r_at = p.rin + first * p.ldr + t * VEC;
+  const T* s_at = RES ? p.res + first * p.ldres + t * VEC : nullptr;
+  T* y_at = p.y + first * p.ldy + t * VEC;
+  int fetched = 0;
+  auto fetch = [&](int stage) {
+    typename Q::Store* to = slots + stage * kPerStep * bd;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = i * tpr + t;
-        if (c < p.nvec) {
-          copy_async<T, VEC>(slot(stage, 0, i), p.x + row * p.ldx + c * VEC);
-          copy_async<T, VEC>(slot(stage, 1, i), p.rin + row * p.ldr + c * VEC);
-          if constexpr (RES) copy_async<T, VEC>(slot(stage, 2, i), p.res + row * p.ldres + c * VEC);
+    for (int r = 0; r < R; ++r) {
+      if (fetched + r < n) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (i * tpr + t < p.nvec) {
+            copy_async<T, VEC>(to + ((r * kArr + 0) * NV + i) * bd, dy_at + i * tpr * VEC);
+            copy_async<T, VEC>(to + ((r * kArr + 1) * NV + i) * bd, r_at + i * tpr * VEC);
+            if constexpr (RES) copy_async<T, VEC>(to + ((r * kArr + 2) * NV + i) * bd, s_at + i * tpr * VEC);
+          }
         }
       }
+      dy_at += sx;
+      r_at += sr;
+      if constexpr (RES) s_at += ss;
     }
+    fetched += R;
     cp_async_commit();
   };
-  for (int q = 0; q < stages - 1; ++q) fetch(first + q * step, q);
+  for (int q = 0; q < steps - 1; ++q) fetch(q);
 
   const W* gamma = static_cast<const W*>(p.gamma);
-  float g[NV][VEC], dg[NV][VEC], db[NV][VEC];
+  F g[NV][kN], dg[NV][kN], db[NV][kN];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
+    float w[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) g[i][j] = dg[i][j] = db[i][j] = 0.0f;
-    if (i * tpr + t < p.nvec) load_weights<W, VEC>(gamma, i * tpr + t, g[i]);
+    for (int j = 0; j < VEC; ++j) w[j] = 0.0f;
+    if (i * tpr + t < p.nvec) load_weights<W, VEC>(gamma, i * tpr + t, w);
+    N::gather(w, g[i]);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) dg[i][j] = db[i][j] = N::splat(0.0f);
   }
+  // the rows' statistics, read one step ahead
+  float next_mean[R], next_rstd[R];
+  const float* mean_at = p.mean + first;
+  const float* rstd_at = p.rstd + first;
+#pragma unroll
+  for (int r = 0; r < R; ++r) next_mean[r] = next_rstd[r] = 0.0f;
+  auto stats = [&](int k) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (k + r < n) {
+        next_mean[r] = __ldg(mean_at);
+        next_rstd[r] = __ldg(rstd_at);
+      }
+      mean_at += step;
+      rstd_at += step;
+    }
+  };
+  stats(0);
   int stage = 0, par = 0;
-  for (int64_t row = first; row < p.rows; row += step) {
-    fetch(row + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
-    const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
-    if (stages == 4) cp_async_wait_group<3>();
+  for (int k = 0; k < n; k += R) {
+    fetch(stage == 0 ? steps - 1 : stage - 1);
+    float rstd[R];
+    F away[R];  // minus the mean
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      rstd[r] = next_rstd[r];
+      away[r] = N::splat(-next_mean[r]);
+    }
+    stats(k + R);
+    if (steps == 3) cp_async_wait_group<2>();
     else cp_async_wait_group<1>();
-    float dy[NV][VEC], xh[NV][VEC];
-    float sums[2] = {0.0f, 0.0f};
+    const typename Q::Store* from = slots + stage * kPerStep * bd;
+    Q raw[R][kArr][NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i * tpr + t < p.nvec) {
-        R u;
-        u.v = *slot(stage, 0, i);
-        u.unpack(dy[i]);
-        u.v = *slot(stage, 1, i);
-        u.unpack(xh[i]);
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          xh[i][j] = (xh[i][j] - mean) * rstd;
-          dg[i][j] += dy[i][j] * xh[i][j];
-          db[i][j] += dy[i][j];
-          dy[i][j] *= g[i][j];  // a
-          sums[0] += dy[i][j];
-          sums[1] += dy[i][j] * xh[i][j];
+      for (int q = 0; q < kArr; ++q)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) raw[r][q][i].v = from[((r * kArr + q) * NV + i) * bd];
+    F a[R][NV][kN], xh[R][NV][kN];
+    float sums[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      F s1 = N::splat(0.0f), s2 = s1;
+      const F rs = N::splat(rstd[r]);
+      if (r == 0 || k + r < n) {  // past the last row the slots hold nothing
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (i * tpr + t < p.nvec) {
+            float f[VEC];
+            raw[r][0][i].unpack(f);
+            N::gather(f, a[r][i]);
+            raw[r][1][i].unpack(f);
+            N::gather(f, xh[r][i]);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+              const F dy = a[r][i][j];
+              xh[r][i][j] = fmul(fadd(xh[r][i][j], away[r]), rs);
+              dg[i][j] = ffma(dy, xh[r][i][j], dg[i][j]);
+              db[i][j] = fadd(db[i][j], dy);
+              a[r][i][j] = fmul(dy, g[i][j]);
+              s1 = fadd(s1, a[r][i][j]);
+              s2 = ffma(a[r][i][j], xh[r][i][j], s2);
+            }
+          }
         }
       }
+      sums[2 * r] = fold(s1);
+      sums[2 * r + 1] = fold(s2);
     }
-    row_sums<ONE_WARP, 2>(sums, red[par], nwarps);
+    group_sums<ONE_WARP, 2 * R>(sums, red[par], nwarps);
     par ^= 1;
-    const float m1 = sums[0] * p.inv_d, m2 = sums[1] * p.inv_d;
-    T* dx = p.y + row * p.ldy;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = i * tpr + t;
-      if (c < p.nvec) {
-        float f[VEC];
-        if constexpr (RES) {
-          R u;
-          u.v = *slot(stage, 2, i);
-          u.unpack(f);
-        }
+    for (int r = 0; r < R; ++r) {
+      if (r == 0 || k + r < n) {
+        // dx = rstd a - (rstd m1 + xh rstd m2) + dres
+        const F rs = N::splat(rstd[r]), c1 = N::splat(-rstd[r] * (sums[2 * r] * p.inv_d)),
+                c2 = N::splat(-rstd[r] * (sums[2 * r + 1] * p.inv_d));
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float d = rstd * (dy[i][j] - m1 - xh[i][j] * m2);
-          f[j] = RES ? d + f[j] : d;
+        for (int i = 0; i < NV; ++i) {
+          if (i * tpr + t < p.nvec) {
+            Q u;
+            float f[VEC];
+            F d[kN];
+#pragma unroll
+            for (int j = 0; j < kN; ++j) d[j] = ffma(a[r][i][j], rs, ffma(xh[r][i][j], c2, c1));
+            if constexpr (RES) {
+              F e[kN];
+              raw[r][kArr - 1][i].unpack(f);
+              N::gather(f, e);
+#pragma unroll
+              for (int j = 0; j < kN; ++j) d[j] = fadd(d[j], e[j]);
+            }
+            N::scatter(d, f);
+            u.pack(f);
+            u.store(y_at + i * tpr * VEC, 0);
+          }
         }
-        R u;
-        u.pack(f);
-        u.store(dx, c);
       }
+      y_at += sy;
     }
-    if (++stage == stages) stage = 0;
+    if (++stage == steps) stage = 0;
   }
   cp_async_wait_all();
   if (p.partials == nullptr) return;
   float* part = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
+  float fg[NV][VEC], fb[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    N::scatter(dg[i], fg[i]);
+    N::scatter(db[i], fb[i]);
+  }
   if constexpr (ONE_WARP) {
     // join the warps' sums in shared memory, in the warps' order
     float* acc = reinterpret_cast<float*>(stage_mem);  // [groups][2][NV * VEC][32]
@@ -274,8 +394,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs<T>
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        acc[((group * 2 + 0) * NV * VEC + i * VEC + j) * 32 + t] = dg[i][j];
-        acc[((group * 2 + 1) * NV * VEC + i * VEC + j) * 32 + t] = db[i][j];
+        acc[((group * 2 + 0) * NV * VEC + i * VEC + j) * 32 + t] = fg[i][j];
+        acc[((group * 2 + 1) * NV * VEC + i * VEC + j) * 32 + t] = fb[i][j];
       }
     __syncthreads();
     for (int k = threadIdx.x; k < 2 * NV * VEC * 32; k += blockDim.x) {
@@ -292,34 +412,37 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs<T>
       if (c < p.nvec) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          part[c * VEC + j] = dg[i][j];
-          part[p.D + c * VEC + j] = db[i][j];
+          part[c * VEC + j] = fg[i][j];
+          part[p.D + c * VEC + j] = fb[i][j];
         }
       }
     }
   }
 }
 
-// Column sums of partials [P][C]: 32 columns x 32 rows of threads per block,
-// each thread adding every 32nd row, then the 32 partial sums in order.
-constexpr int kJoinRows = 32;
+// Column sums of partials [P][C]: 16 columns x 64 rows of threads per block,
+// each thread adding every 64th row, then the 64 partial sums in a fixed order.
+constexpr int kJoinCols = 16, kJoinRows = 64;
 template <typename O>
-__global__ void __launch_bounds__(32 * kJoinRows)
+__global__ void __launch_bounds__(kJoinCols* kJoinRows)
     join_partials_kernel(const float* __restrict__ part, int P, int64_t C, int64_t split, O* out0,
                          O* out1) {
-  __shared__ float acc[kJoinRows][33];
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
+  __shared__ float acc[kJoinRows][kJoinCols + 1];
+  const int tx = threadIdx.x % kJoinCols, ty = threadIdx.x / kJoinCols;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kJoinCols + tx;
   float s = 0.0f;
   if (c < C) {
-#pragma unroll 4
-    for (int r = threadIdx.y; r < P; r += kJoinRows) s += part[static_cast<int64_t>(r) * C + c];
+#pragma unroll 8
+    for (int r = ty; r < P; r += kJoinRows) s += part[static_cast<int64_t>(r) * C + c];
   }
-  acc[threadIdx.y][threadIdx.x] = s;
+  acc[ty][tx] = s;
   __syncthreads();
-  // warp y sums column y of the block over the 32 row groups
-  s = warp_sum(acc[threadIdx.x][threadIdx.y]);
-  const int64_t cw = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && cw < C) {
+  // warp w < 16 sums column w of the block
+  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (w >= kJoinCols) return;
+  s = warp_sum(acc[lane][w] + acc[lane + 32][w]);
+  const int64_t cw = static_cast<int64_t>(blockIdx.x) * kJoinCols + w;
+  if (lane == 0 && cw < C) {
     if (cw < split) out0[cw] = from_f32<O>(s);
     else out1[cw - split] = from_f32<O>(s);
   }
@@ -413,7 +536,7 @@ cudaError_t fwd_type(const NormCall& c, cudaStream_t s) {
 struct KernelLimits {
   std::atomic<int> regs[64];  // 0: not looked up
 };
-constexpr int kMaxDynamicSmem = 220 * 1024;
+constexpr size_t kMaxDynamicSmem = 220 * 1024;
 
 template <class K>
 cudaError_t kernel_regs(K kern, KernelLimits& lim, int* regs) {
@@ -426,49 +549,59 @@ cudaError_t kernel_regs(K kern, KernelLimits& lim, int* regs) {
   cudaFuncAttributes at{};
   err = cudaFuncGetAttributes(&at, kern);
   if (err != cudaSuccess) return err;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kMaxDynamicSmem));
   if (err != cudaSuccess) return err;
   *regs = std::max(at.numRegs, 1);
   lim.regs[dev].store(*regs, std::memory_order_release);
   return cudaSuccess;
 }
 
-template <typename T, typename W, int VEC, int NV, bool ONE_WARP, bool RES>
+template <typename T, typename W, int VEC, int NV, bool ONE_WARP, bool RES, int R>
 cudaError_t bwd_launch(const NormCall& c, cudaStream_t s) {
   NormArgs<T> a = make_args<T>(c, VEC);
   const int threads = ONE_WARP ? 32 * kBwdGroups : round32((a.nvec + NV - 1) / NV);
   const int groups = ONE_WARP ? kBwdGroups : 1;
-  // four rows of slots, or two where four do not fit (wide fp32 rows)
-  const size_t row_bytes = static_cast<size_t>(RES ? 3 : 2) * NV * threads * sizeof(T) * VEC;
-  const int stages = 4 * row_bytes <= kMaxDynamicSmem ? 4 : 2;
-  size_t bytes = stages * row_bytes;
-  if (ONE_WARP) bytes = std::max(bytes, static_cast<size_t>(groups) * 2 * NV * VEC * 32 * 4);
-  auto kern = norm_bwd_kernel<T, W, VEC, NV, ONE_WARP, RES>;
+  auto kern = norm_bwd_kernel<T, W, VEC, NV, ONE_WARP, RES, R>;
   static KernelLimits limits;
   int regs = 0;
   cudaError_t err = kernel_regs(kern, limits, &regs);
   if (err != cudaSuccess) return err;
-  // blocks that can be resident: by threads, registers (in units of 8 per
-  // thread) and shared memory (1 KB more per block is the system's)
-  const int per_sm = std::min({2048 / threads, 65536 / ((regs + 7) / 8 * 8 * threads),
-                               static_cast<int>(228 * 1024 / (bytes + 2048))});
+  // blocks that threads and registers (in units of 8 per thread) let an SM
+  // hold; two steps ahead where shared memory (1 KB more per block is the
+  // system's) keeps that number, else one
+  int per_sm = std::min(2048 / threads, 65536 / ((regs + 7) / 8 * 8 * threads));
+  const auto slot_bytes = [&](int steps) {
+    return static_cast<size_t>(bwd_slots<NV, RES, R>(steps)) * threads * sizeof(T) * VEC;
+  };
+  const int steps = (slot_bytes(3) + 2048) * std::max(per_sm, 1) <= kMaxDynamicSmem ? 3 : 2;
+  size_t bytes = slot_bytes(steps);
+  if (ONE_WARP) bytes = std::max(bytes, static_cast<size_t>(groups) * 2 * NV * VEC * 32 * 4);
+  per_sm = std::min(per_sm, static_cast<int>(228 * 1024 / (bytes + 2048)));
   int64_t blocks = static_cast<int64_t>(sm_count()) * std::max(per_sm, 1);
-  blocks = std::min({blocks, (c.rows + groups - 1) / groups, kPartialRows});
-  kern<<<static_cast<unsigned>(blocks), threads, bytes, s>>>(a, stages);
+  blocks = std::min({blocks, (c.rows + groups * R - 1) / (groups * R), kPartialRows});
+  kern<<<static_cast<unsigned>(blocks), threads, bytes, s>>>(a, steps);
   err = cudaGetLastError();
   if (err != cudaSuccess || c.dgamma == nullptr) return err;
   return launch_join_partials(c.partials, static_cast<int>(blocks), 2 * static_cast<int64_t>(c.D),
                               c.D, c.dgamma, c.dbeta, c.wtype, s);
 }
 
+template <typename T, typename W, int VEC, int NV, bool ONE_WARP, int R>
+cudaError_t bwd_res(const NormCall& c, cudaStream_t s) {
+  return c.res != nullptr ? bwd_launch<T, W, VEC, NV, ONE_WARP, true, R>(c, s)
+                          : bwd_launch<T, W, VEC, NV, ONE_WARP, false, R>(c, s);
+}
+
+// Two rows at a time where a thread holds up to eight columns; with sixteen
+// (the widest rows) two would not fit its registers.
 template <typename T, typename W, int VEC, int NV>
 cudaError_t bwd_nv(const NormCall& c, cudaStream_t s) {
-  const bool one = (c.D / VEC + NV - 1) / NV <= 32;
-  if (one)
-    return c.res != nullptr ? bwd_launch<T, W, VEC, NV, true, true>(c, s)
-                            : bwd_launch<T, W, VEC, NV, true, false>(c, s);
-  return c.res != nullptr ? bwd_launch<T, W, VEC, NV, false, true>(c, s)
-                          : bwd_launch<T, W, VEC, NV, false, false>(c, s);
+  constexpr int R = NV * VEC <= 8 ? 2 : 1;
+  if constexpr (NV == (VEC == 1 ? 4 : 1)) {  // more vectors per thread are only taken by wide rows
+    if (c.D / VEC <= 32 * NV) return bwd_res<T, W, VEC, NV, true, R>(c, s);
+  }
+  return bwd_res<T, W, VEC, NV, false, R>(c, s);
 }
 
 template <typename T, typename W, int VEC>
@@ -508,7 +641,7 @@ cudaError_t launch_layer_norm_bwd(const NormCall& c, cudaStream_t s) { return by
 
 cudaError_t launch_join_partials(const float* partials, int P, int64_t C, int64_t split, void* out0,
                                  void* out1, moe_dtype type, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((C + 31) / 32)), block(32, kJoinRows);
+  const dim3 grid(static_cast<unsigned>((C + kJoinCols - 1) / kJoinCols)), block(kJoinCols * kJoinRows);
   switch (type) {
     case MOE_BF16:
       join_partials_kernel<<<grid, block, 0, s>>>(partials, P, C, split,
