@@ -192,12 +192,20 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _s(stream):
     if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def stream_of(stream, device) -> int:
+    """The stream of a call: the given one (a Stream or its integer), or the
+    device's current one."""
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(device.index)
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _ok(name, st):
@@ -375,12 +383,9 @@ _NO_MAT = MoeMat(None, 0)
 
 
 def _m(t):
-    """A 2-D tensor with contiguous columns (any row stride) as a moe_mat; a
-    MoeMat passes through."""
+    """A 2-D tensor with contiguous columns (any row stride) as a moe_mat."""
     if t is None:
         return _NO_MAT
-    if type(t) is MoeMat:
-        return t
     (rows, cols), (ld, inner) = t.shape, t.stride()
     if inner != 1 and cols > 1:
         raise ValueError("matrices passed to libmoe need contiguous columns")
@@ -389,26 +394,22 @@ def _m(t):
     return MoeMat(t.data_ptr(), ld)
 
 
-def moe_layer_norm(x, res, gamma, beta, r, y, mean, rstd, eps: float, stream=None, sizes=None):
-    """sizes: (rows, D, type, wtype) where x and gamma do not tell them (MoeMat, pointer)."""
-    rows, D, ty, wt = sizes or (*x.shape, DTYPES[x.dtype], DTYPES[gamma.dtype])
-    st = lib().moe_layer_norm(_m(x), _m(res), _p(gamma), _p(beta), _m(r), _m(y), _p(mean),
-                              _p(rstd), eps, rows, D, ty, wt, _s(stream))
-    if st:
-        raise MoeError("moe_layer_norm", st)
+def moe_layer_norm(x, res, gamma, beta, r, y, mean, rstd, eps: float, stream=None):
+    rows, D = x.shape
+    _ok("moe_layer_norm", lib().moe_layer_norm(
+        _m(x), _m(res), _p(gamma), _p(beta), _m(r), _m(y), _p(mean), _p(rstd), eps, rows, D,
+        DTYPES[x.dtype], DTYPES[gamma.dtype], _s(stream)))
 
 
 def moe_layer_norm_workspace_bytes(rows: int, D: int) -> int:
     return int(lib().moe_layer_norm_workspace_bytes(rows, D))
 
 
-def moe_layer_norm_bwd(dy, r, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, stream=None,
-                       sizes=None):
-    rows, D, ty, wt = sizes or (*dy.shape, DTYPES[dy.dtype], DTYPES[gamma.dtype])
-    st = lib().moe_layer_norm_bwd(_m(dy), _m(r), _p(gamma), _p(mean), _p(rstd), _m(dres), _m(dx),
-                                  _p(dgamma), _p(dbeta), _p(ws), rows, D, ty, wt, _s(stream))
-    if st:
-        raise MoeError("moe_layer_norm_bwd", st)
+def moe_layer_norm_bwd(dy, r, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, stream=None):
+    rows, D = dy.shape
+    _ok("moe_layer_norm_bwd", lib().moe_layer_norm_bwd(
+        _m(dy), _m(r), _p(gamma), _p(mean), _p(rstd), _m(dres), _m(dx), _p(dgamma), _p(dbeta),
+        _p(ws), rows, D, DTYPES[dy.dtype], DTYPES[gamma.dtype], _s(stream)))
 
 
 def moe_route_topk(logits, bias, ids, w, d: MoeTopkDims, stream=None):

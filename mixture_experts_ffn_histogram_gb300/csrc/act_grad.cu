@@ -14,6 +14,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kOneBlockRows = 64;
 
 template <typename T, typename Y>
 struct ActGradArgs {
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradArgs<T,
     float s = 0.0f;
     for (int y = 0; y < nrow; ++y) s += red[y * p.col_threads + c][j];
     const int64_t cc = (static_cast<int64_t>(blockIdx.x) * p.col_threads + c) * 8 + j;
-    if (cc < p.N) p.partials[static_cast<int64_t>(blockIdx.y) * p.N + cc] = s;
+    if (cc < p.N) p.partials[static_cast<int64_t>(blockIdx.y) * p.N + cc] = s;  // (the sums themselves for one block)
   }
 }
 
@@ -122,12 +123,15 @@ cudaError_t launch_t(const ActGradCall& c, cudaStream_t s) {
   // about eight blocks per SM, whole passes of the block's rows each
   const int64_t pass = kThreads / ct;
   int64_t gy = std::max<int64_t>(1, static_cast<int64_t>(sm_count()) * 8 / gx);
-  gy = std::min({gy, (c.M + pass - 1) / pass, kPartialRows});
+  // few rows: one block down the rows writes the sums themselves, which
+  // saves the second launch
+  gy = c.M <= kOneBlockRows ? 1 : std::min({gy, (c.M + pass - 1) / pass, kPartialRows});
   a.rows_per_block = ((c.M + gy - 1) / gy + pass - 1) / pass * pass;
   gy = (c.M + a.rows_per_block - 1) / a.rows_per_block;
+  if (gy == 1 && c.db != nullptr) a.partials = c.db;
   act_grad_kernel<T, Y><<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kThreads, 0, s>>>(a);
   const cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess || c.db == nullptr) return err;
+  if (err != cudaSuccess || c.db == nullptr || gy == 1) return err;
   return launch_join_partials(c.partials, static_cast<int>(gy), c.N, c.N, c.db, nullptr, MOE_FP32, s);
 }
 

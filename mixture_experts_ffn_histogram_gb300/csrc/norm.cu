@@ -29,6 +29,7 @@ struct NormArgs {
   T *r, *y;
   float *mean, *rstd;
   float* partials;
+  void *dgamma, *dbeta;  // backward by one block
   int64_t ldx, ldres, ldr, ldy, rows;
   float eps, inv_d;
   int D, nvec;
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormArgs<T>
 // in flight do not depend on registers.  A block walks rows with the grid's
 // stride and keeps its columns' weight-gradient sums in registers; at the end
 // they become one row of `partials` ([blocks][2][D]: dgamma, dbeta).
+constexpr int64_t kOneBlockRows = 8;
 constexpr int kBwdGroups = 4;  // ONE_WARP: warps of a block, each on rows of its own
 
 template <typename T, int VEC>
@@ -378,8 +380,20 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
     if (++stage == steps) stage = 0;
   }
   cp_async_wait_all();
-  if (p.partials == nullptr) return;
+  if (p.partials == nullptr && p.dgamma == nullptr) return;
+  // one block alone writes the gradients themselves
+  W* dgamma = static_cast<W*>(p.dgamma);
+  W* dbeta = static_cast<W*>(p.dbeta);
   float* part = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
+  auto put = [&](int col, float vg, float vb) {
+    if (dgamma != nullptr) {
+      dgamma[col] = from_f32<W>(vg);
+      dbeta[col] = from_f32<W>(vb);
+    } else {
+      part[col] = vg;
+      part[p.D + col] = vb;
+    }
+  };
   float fg[NV][VEC], fb[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -398,12 +412,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
         acc[((group * 2 + 1) * NV * VEC + i * VEC + j) * 32 + t] = fb[i][j];
       }
     __syncthreads();
-    for (int k = threadIdx.x; k < 2 * NV * VEC * 32; k += blockDim.x) {
-      float s = 0.0f;
-      for (int gq = 0; gq < groups; ++gq) s += acc[gq * 2 * NV * VEC * 32 + k];
-      const int which = k / (NV * VEC * 32), e = (k / 32) % (NV * VEC), lane = k & 31;
-      const int c = (e / VEC) * 32 + lane;
-      if (c < p.nvec) part[which * p.D + c * VEC + e % VEC] = s;
+    for (int k = threadIdx.x; k < NV * VEC * 32; k += blockDim.x) {
+      float sg = 0.0f, sb = 0.0f;
+      for (int gq = 0; gq < groups; ++gq) {
+        sg += acc[gq * 2 * NV * VEC * 32 + k];
+        sb += acc[(gq * 2 + 1) * NV * VEC * 32 + k];
+      }
+      const int e = k / 32, c = (e / VEC) * 32 + (k & 31);
+      if (c < p.nvec) put(c * VEC + e % VEC, sg, sb);
     }
   } else {
 #pragma unroll
@@ -412,8 +428,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
       if (c < p.nvec) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          part[c * VEC + j] = fg[i][j];
-          part[p.D + c * VEC + j] = fb[i][j];
+          put(c * VEC + j, fg[i][j], fb[i][j]);
         }
       }
     }
@@ -580,9 +595,16 @@ cudaError_t bwd_launch(const NormCall& c, cudaStream_t s) {
   per_sm = std::min(per_sm, static_cast<int>(228 * 1024 / (bytes + 2048)));
   int64_t blocks = static_cast<int64_t>(sm_count()) * std::max(per_sm, 1);
   blocks = std::min({blocks, (c.rows + groups * R - 1) / (groups * R), kPartialRows});
+  // few rows: one block, which needs no second launch
+  if (c.rows <= kOneBlockRows) blocks = 1;
+  if (blocks == 1) {
+    a.partials = nullptr;
+    a.dgamma = c.dgamma;
+    a.dbeta = c.dbeta;
+  }
   kern<<<static_cast<unsigned>(blocks), threads, bytes, s>>>(a, steps);
   err = cudaGetLastError();
-  if (err != cudaSuccess || c.dgamma == nullptr) return err;
+  if (err != cudaSuccess || c.dgamma == nullptr || blocks == 1) return err;
   return launch_join_partials(c.partials, static_cast<int>(blocks), 2 * static_cast<int64_t>(c.D),
                               c.D, c.dgamma, c.dbeta, c.wtype, s);
 }

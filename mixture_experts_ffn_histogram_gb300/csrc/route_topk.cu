@@ -53,12 +53,6 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
-}
-
 // The two largest of (a1 >= a2) and (b1 >= b2).
 template <typename F>
 __device__ __forceinline__ void merge_top2(F& a1, F& a2, F b1, F b2) {
@@ -509,7 +503,8 @@ struct TopkBwdArgs {
 
 // One warp per token.  Only the softmax without renormalisation has a dense
 // gradient (and reads the row); the others write zeros and the K values.
-// The K values overwrite the row's after a warp barrier.
+// The K values overwrite the row's after a warp barrier.  Bound by HBM once
+// the loads of a warp's next token are under way while it works on this one.
 template <int VPL, bool DENSE>
 __global__ void __launch_bounds__(32 * kTopkWarps) route_topk_bwd_kernel(const TopkBwdArgs p) {
   const moe_topk_dims d = p.d;
@@ -518,61 +513,74 @@ __global__ void __launch_bounds__(32 * kTopkWarps) route_topk_bwd_kernel(const T
   const bool vec = VPL % 4 == 0 && E % 4 == 0;
   const bool softmax = d.gate == MOE_GATE_SOFTMAX;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kTopkWarps;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTopkWarps + warp; t < d.T; t += stride) {
-    const float* row = p.logits + t * E;
-    float* out = p.dlogits + t * E;
-    int id = -1;
-    float g = 0.0f, l = kNegInf;
+  int next_id = -1;
+  float next_dw = 0.0f, ahead[VPL];
+  auto fetch = [&](int64_t t) {
+    if (t >= d.T) return;
     if (lane < K) {
-      id = p.ids[t * K + lane];
-      if (id < 0 || id >= E) id = -1;
-      if (id >= 0) {
-        g = p.dw[t * K + lane] * d.scale;
-        l = __ldg(row + id);
-        if (!(l > kNegInf)) l = kNegInf;
-      }
+      next_id = __ldg(p.ids + t * K + lane);
+      next_dw = __ldg(p.dw + t * K + lane);
     }
-    float v[VPL];
-    float base = 0.0f, value;
     if constexpr (DENSE) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) v[i] = kNegInf;
+      const float* row = p.logits + t * E;
       if (vec) {
 #pragma unroll
         for (int i = 0; i + 3 < VPL; i += 4) {
           const int e = lane * VPL + i;
-          if (e < E) {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(row + e));
-            v[i] = q.x;
-            v[i + 1] = q.y;
-            v[i + 2] = q.z;
-            v[i + 3] = q.w;
-          }
+          float4 q = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+          if (e < E) q = __ldg(reinterpret_cast<const float4*>(row + e));
+          ahead[i] = q.x;
+          ahead[i + 1] = q.y;
+          ahead[i + 2] = q.z;
+          ahead[i + 3] = q.w;
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (lane * VPL + i < E) v[i] = __ldg(row + lane * VPL + i);
+        for (int i = 0; i < VPL; ++i) {
+          const int e = lane * VPL + i;
+          ahead[i] = e < E ? __ldg(row + e) : kNegInf;
+        }
       }
-      float m = kNegInf;
+    }
+  };
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kTopkWarps + warp;
+  fetch(t);
+  for (; t < d.T; t += stride) {
+    float* out = p.dlogits + t * E;
+    const int id = lane < K && next_id >= 0 && next_id < E ? next_id : -1;
+    const float g = id >= 0 ? next_dw * d.scale : 0.0f;
+    const float l = id >= 0 ? clean(__ldg(p.logits + t * E + id)) : kNegInf;
+    float v[VPL];
+    if constexpr (DENSE) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) m = fmaxf(m, v[i]);
-      m = warp_max(m);
+      for (int i = 0; i < VPL; ++i) v[i] = clean(ahead[i]);
+    }
+    fetch(t + stride);
+    float base = 0.0f, value;
+    if constexpr (DENSE) {
+      float m = v[0];
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) m = fmaxf(m, v[i]);
+      m = warp_max_f32(m);
       float total = 0.0f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        v[i] = v[i] > kNegInf ? soft_num(v[i], m) : 0.0f;
+        v[i] = v[i] == m && m != kNegInf ? 1.0f : exp2_fast((v[i] - m) * kLog2e);
         total += v[i];
       }
-      total = warp_sum(total);
+      total = m == kNegInf ? 0.0f : warp_sum(total);
       const float inv = total > 0.0f ? 1.0f / total : 0.0f;
       const float s = soft_num(l, m) * inv;
       const float dot = warp_sum(g * s);
       base = -dot * inv;  // times e^(l - m)
       value = s * (g - dot);
+      if (m == kNegInf) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[i] = 0.0f;
+      }
     } else if (softmax) {
       // shares of the selected experts: the sum over all others cancels
-      const float m = warp_max(l);
+      const float m = warp_max_f32(l);
       const float e = soft_num(l, m);
       const float total = warp_sum(e);
       const float q = total > 0.0f ? e / total : 0.0f;
@@ -609,9 +617,12 @@ __global__ void __launch_bounds__(32 * kTopkWarps) route_topk_bwd_kernel(const T
   }
 }
 
-unsigned topk_grid(int T) {
+// Blocks: a warp per token, at most per_sm blocks per SM (a warp that takes a
+// few tokens reads the next one's row ahead; of 4 to 64 blocks these measured
+// best at 32768 tokens).
+unsigned topk_grid(int T, int per_sm) {
   const int64_t want = (static_cast<int64_t>(T) + kTopkWarps - 1) / kTopkWarps;
-  return static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(sm_count()) * 16));
+  return static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(sm_count()) * per_sm));
 }
 
 // Calls go(n) with the smallest compiled capacity for vpl experts per lane.
@@ -631,7 +642,7 @@ void pick_vpl(int vpl, Go go) {
 cudaError_t launch_route_topk(const float* logits, const float* bias, int32_t* ids, float* w,
                               const moe_topk_dims& d, cudaStream_t s) {
   const TopkArgs a{logits, bias, ids, w, d};
-  const unsigned grid = topk_grid(d.T);
+  const unsigned grid = topk_grid(d.T, 12);
   const bool grouped = d.groups > 1 && d.top_groups < d.groups;
   const int lpg = grouped ? topk_group_lanes(d) : 32;
   const int vpl = ((grouped ? d.E / d.groups : d.E) + lpg - 1) / lpg;
@@ -648,8 +659,8 @@ cudaError_t launch_route_topk(const float* logits, const float* bias, int32_t* i
 cudaError_t launch_route_topk_bwd(const float* logits, const int32_t* ids, const float* dw,
                                   float* dlogits, const moe_topk_dims& d, cudaStream_t s) {
   const TopkBwdArgs a{logits, ids, dw, dlogits, d};
-  const unsigned grid = topk_grid(d.T);
   const bool dense = d.gate == MOE_GATE_SOFTMAX && !d.renorm;
+  const unsigned grid = topk_grid(d.T, dense ? 8 : 12);
   pick_vpl((d.E + 31) / 32, [&](auto n) {
     constexpr int VPL = decltype(n)::value;
     if (dense) route_topk_bwd_kernel<VPL, true><<<grid, 32 * kTopkWarps, 0, s>>>(a);

@@ -68,6 +68,13 @@ def _own(t):
     return B.MoeMat(t.data_ptr(), t.stride(0))
 
 
+_NO = B.MoeMat(None, 0)     # a matrix that is not given
+
+
+def _refused(fn, status):
+    raise B.MoeError(fn, status)
+
+
 def _launchable(device):
     if device.type != "cuda":
         raise RuntimeError(f"the operator's buffers are on {device}: its kernels need a CUDA device")
@@ -110,6 +117,7 @@ class LayerNorm:
         self._w = {n: _Arg(n, weight_dtype, dev, contiguous=True) for n in ("gamma", "beta")}
         self._st = {n: _Arg(n, torch.float32, dev, contiguous=True) for n in ("mean", "rstd")}
         self._types = (B.DTYPES[dtype], B.DTYPES[weight_dtype])
+        self._fwd, self._bwd = B.lib().moe_layer_norm, B.lib().moe_layer_norm_bwd
 
     def forward(self, x, gamma, beta, res=None, stream=None):
         D = self.D
@@ -118,7 +126,7 @@ class LayerNorm:
         mx = self._x.matrix(x, shape)
         pg, pb = self._w["gamma"].pointer(gamma, (D,)), self._w["beta"].pointer(beta, (D,))
         whole = n == self.rows
-        mres = mr = None
+        mres = mr = _NO
         r = x
         if res is not None:
             mres = self._res.matrix(res, shape)
@@ -127,8 +135,10 @@ class LayerNorm:
                 self._mr = _own(self._r)
             r, mr = self._r if whole else self._r[:n], self._mr
         _launchable(self.device)
-        B.moe_layer_norm(mx, mres, pg, pb, mr, self._my, *self._p_stats, self.eps, stream,
-                         (n, D, *self._types))
+        st = self._fwd(mx, mres, pg, pb, mr, self._my, *self._p_stats, self.eps, n, D,
+                       *self._types, B.stream_of(stream, self.device))
+        if st:
+            _refused("moe_layer_norm", st)
         self.r = r
         if self.train:
             self.mean, self.rstd = self._mean, self._rstd
@@ -149,10 +159,12 @@ class LayerNorm:
         mdy, mrin = self._dy.matrix(dy, shape), self._rin.matrix(r, shape)
         pg = self._w["gamma"].pointer(gamma, (D,))
         pm, ps = self._st["mean"].pointer(mean, (n,)), self._st["rstd"].pointer(rstd, (n,))
-        mres = None if dres is None else self._dres.matrix(dres, shape)
+        mres = _NO if dres is None else self._dres.matrix(dres, shape)
         _launchable(self.device)
-        B.moe_layer_norm_bwd(mdy, mrin, pg, pm, ps, mres, self._mdx, *self._p_grads, stream,
-                             (n, D, *self._types))
+        st = self._bwd(mdy, mrin, pg, pm, ps, mres, self._mdx, *self._p_grads, n, D, *self._types,
+                       B.stream_of(stream, self.device))
+        if st:
+            _refused("moe_layer_norm_bwd", st)
         return self._dx if n == self.rows else self._dx[:n]
 
 
@@ -186,6 +198,7 @@ class TopKRouter:
         self._b = _Arg("bias", f32, dev, contiguous=True)
         self._dw = _Arg("dw", f32, dev, contiguous=True)
         self._i = _Arg("ids", torch.int32, dev, contiguous=True)
+        self._fwd, self._bwd = B.lib().moe_route_topk, B.lib().moe_route_topk_bwd
 
     def forward(self, logits, bias=None, stream=None):
         n = self._l.rows(logits, self.T, self.E)
@@ -193,7 +206,9 @@ class TopKRouter:
         pb = None if bias is None else self._b.pointer(bias, (self.E,))
         _launchable(self.device)
         self.d.T = n
-        B.moe_route_topk(pl, pb, *self._p_out, self.d, stream)
+        st = self._fwd(pl, pb, *self._p_out, self.d, B.stream_of(stream, self.device))
+        if st:
+            _refused("moe_route_topk", st)
         if n == self.T:
             self.ids, self.w = self._ids, self._w
         else:
@@ -211,7 +226,9 @@ class TopKRouter:
         pd, pi = self._dw.pointer(dw, (n, self.K)), self._i.pointer(ids, (n, self.K))
         _launchable(self.device)
         self.d.T = n
-        B.moe_route_topk_bwd(pl, pi, pd, self._p_dl, self.d, stream)
+        st = self._bwd(pl, pi, pd, self._p_dl, self.d, B.stream_of(stream, self.device))
+        if st:
+            _refused("moe_route_topk_bwd", st)
         return self._dlogits if n == self.T else self._dlogits[:n]
 
 
@@ -240,7 +257,8 @@ class Linear:
         self._y = torch.empty((M, N), dtype=out_dtype, device=dev)
         self.device = dev = self._y.device
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.z = self._z = self._mz = None
+        self.z = self._z = None
+        self._mz = _NO
         self._my, self._p_status = _own(self._y), self.status.data_ptr()
         if train:
             if act != "none":
@@ -257,16 +275,20 @@ class Linear:
         self._b = _Arg("bias", torch.float32, dev, contiguous=True)
         self._res, self._dy = _Arg("res", out_dtype, dev), _Arg("dy", out_dtype, dev)
         self._zin, self._add = _Arg("z", dtype, dev), _Arg("dx_add", dtype, dev)
+        self._fwd, self._bwd = B.lib().moe_linear, B.lib().moe_linear_bwd
 
     def forward(self, x, w, bias=None, res=None, stream=None):
         K, N = self.K, self.N
         n = self._x.rows(x, self.M, K)
         mx, mw = self._x.matrix(x, (n, K)), self._w.matrix(w, (K, N))
         pb = None if bias is None else self._b.pointer(bias, (N,))
-        mres = None if res is None else self._res.matrix(res, (n, N))
+        mres = _NO if res is None else self._res.matrix(res, (n, N))
         _launchable(self.device)
         self.d.M = n
-        B.moe_linear(mx, mw, pb, mres, self._my, self._mz, self._p_status, self.d, stream)
+        st = self._fwd(mx, mw, pb, mres, self._my, self._mz, self._p_status, self.d,
+                       B.stream_of(stream, self.device))
+        if st:
+            _refused("moe_linear", st)
         whole = n == self.M
         if self._z is not None:
             self.z = self._z if whole else self._z[:n]
@@ -280,18 +302,20 @@ class Linear:
         n = self._x.rows(x, self.M, K)
         mdy = self._dy.matrix(dy, (n, N))
         mx, mw = self._x.matrix(x, (n, K)), self._w.matrix(w, (K, N))
-        mz = None
+        mz = _NO
         if self.act != "none":
             z = self.z if z is None else z
             if z is None:
                 raise RuntimeError("backward needs a forward first, or its z")
             mz = self._zin.matrix(z, (n, N))
-        madd = None if dx_add is None else self._add.matrix(dx_add, (n, K))
+        madd = _NO if dx_add is None else self._add.matrix(dx_add, (n, K))
         _launchable(self.device)
         self.d.M = n
-        B.moe_linear_bwd(mdy, mz, mx, mw, madd, self._mdx if need_dx else None,
-                         self._mdw if need_dw else None, self._p_db if need_db else None,
-                         self._p_status, self._p_ws, self.d, stream)
+        st = self._bwd(mdy, mz, mx, mw, madd, self._mdx if need_dx else _NO,
+                       self._mdw if need_dw else _NO, self._p_db if need_db else None,
+                       self._p_status, self._p_ws, self.d, B.stream_of(stream, self.device))
+        if st:
+            _refused("moe_linear_bwd", st)
         if not need_dx:
             return None
         return self._dx if n == self.M else self._dx[:n]
