@@ -71,82 +71,29 @@ struct DenseParams {
   uint64_t limit_ns;
 };
 
-// The epilogue of G groups of four neighbouring columns, each of one output
-// row: G independent chains, and one branch on the activation for all of
-// them.  A group outside the output (`on` false) comes with a place inside,
-// so that its loads need no branch, and is not stored.
-template <typename T, typename O, int G>
-__device__ __forceinline__ void epilogue4(float (&v)[G][4], const int64_t (&row)[G],
-                                          const int64_t (&col)[G], const bool (&on)[G],
-                                          const DenseParams& p) {
-  constexpr bool kExact = sizeof(O) == 4;
-  const O* res = static_cast<const O*>(p.res);
-  float r[G][4];
-  if (res != nullptr) {
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const O* at = res + row[g] * p.ldres + col[g];
-      if constexpr (sizeof(O) == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(at);
-        r[g][0] = f.x;
-        r[g][1] = f.y;
-        r[g][2] = f.z;
-        r[g][3] = f.w;
-      } else {
-        const uint2 q = *reinterpret_cast<const uint2*>(at);
-        const float2 a = unpack_pair(q.x, O{}), b = unpack_pair(q.y, O{});
-        r[g][0] = a.x;
-        r[g][1] = a.y;
-        r[g][2] = b.x;
-        r[g][3] = b.y;
-      }
+// Four neighbouring values of an output row, 16-bit or fp32, as they lie in
+// memory.
+template <typename O>
+struct Quad {
+  using Store = typename std::conditional<sizeof(O) == 4, float4, uint2>::type;
+  Store v;
+  __device__ __forceinline__ void load(const O* at) { v = *reinterpret_cast<const Store*>(at); }
+  __device__ __forceinline__ float4 get() const {
+    if constexpr (sizeof(O) == 4) {
+      return v;
+    } else {
+      const float2 a = unpack_pair(v.x, O{}), b = unpack_pair(v.y, O{});
+      return make_float4(a.x, a.y, b.x, b.y);
     }
   }
-  if (p.bias != nullptr) {
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + col[g]));
-      v[g][0] += b.x;
-      v[g][1] += b.y;
-      v[g][2] += b.z;
-      v[g][3] += b.w;
-    }
-  }
-  if (p.z != nullptr) {
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-      if (on[g])
-        *reinterpret_cast<uint2*>(static_cast<T*>(p.z) + row[g] * p.ldz + col[g]) =
-            make_uint2(pack_pair(v[g][0], v[g][1], T{}), pack_pair(v[g][2], v[g][3], T{}));
-  }
-  act_all<kExact, 4 * G>(&v[0][0], p.act);
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    if (!on[g]) continue;
-    if (res != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[g][i] += r[g][i];
-    }
-    O* c = static_cast<O*>(p.c) + row[g] * p.ldc + col[g];
-    if constexpr (sizeof(O) == 4)
-      *reinterpret_cast<float4*>(c) = make_float4(v[g][0], v[g][1], v[g][2], v[g][3]);
-    else
-      *reinterpret_cast<uint2*>(c) =
-          make_uint2(pack_pair(v[g][0], v[g][1], O{}), pack_pair(v[g][2], v[g][3], O{}));
-  }
-}
-template <int G>
-__device__ __forceinline__ void epilogue4_any(float (&v)[G][4], const int64_t (&row)[G],
-                                              const int64_t (&col)[G], const bool (&on)[G],
-                                              const DenseParams& p) {
-  if (p.out_type == MOE_FP32) {
-    if (p.type == MOE_BF16) epilogue4<__nv_bfloat16, float, G>(v, row, col, on, p);
-    else epilogue4<__half, float, G>(v, row, col, on, p);
-  } else if (p.type == MOE_BF16) {
-    epilogue4<__nv_bfloat16, __nv_bfloat16, G>(v, row, col, on, p);
-  } else {
-    epilogue4<__half, __half, G>(v, row, col, on, p);
-  }
+};
+template <typename O>
+__device__ __forceinline__ void store4(O* at, const float (&v)[4]) {
+  if constexpr (sizeof(O) == 4)
+    *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(at) =
+        make_uint2(pack_pair(v[0], v[1], O{}), pack_pair(v[2], v[3], O{}));
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -253,6 +200,114 @@ struct SplitShape {
   static_assert(CG == 1 || !SWAP, "swapped tiles are one CTA's");
 };
 
+// A CTA's part of a finished tile: rows [r0, r1) of the partial tile that lies
+// in shared memory at `ring`, the output's rows from row0 + r0 on.
+struct TileEnd {
+  int64_t row0, col0;
+  int r0, r1;
+  uint32_t ring;        // shared address of the partial tile
+  const uint8_t* smem;  // ... and its pointer
+  int sub;
+};
+
+// Sums the SP partials (in rank order) and runs the epilogue.  A thread keeps
+// to four columns and walks down the rows, G of them at a time: G * SP loads
+// are under way together, and addresses advance by constants.
+template <class S, typename T, typename O, int G, int SP>
+__device__ __forceinline__ void finish_rows(const TileEnd& te, const DenseParams& p) {
+  constexpr bool kExact = sizeof(O) == 4;
+  constexpr int kPer = S::kColsOut / 4;          // threads across a row
+  constexpr int kDown = S::kThreads / kPer;      // rows of one pass
+  static_assert(kDown * kPer == S::kThreads, "threads cover whole rows");
+  const int cc = (threadIdx.x % kPer) * 4;
+  const int64_t col = te.col0 + cc;
+  const int64_t last = min(static_cast<int64_t>(te.r1), p.M - te.row0);  // rows below exist
+  if (col >= p.N) return;
+  int r = te.r0 + threadIdx.x / kPer;
+  float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (p.bias != nullptr) bias = __ldg(reinterpret_cast<const float4*>(p.bias + col));
+  uint32_t from[SP];
+#pragma unroll
+  for (int q = 0; q < SP; ++q) {
+    const uint32_t at = te.ring + static_cast<uint32_t>(r * S::kLd + cc) * 4;
+    from[q] = SP > 1 ? mapa_shared(at, q * S::CG + te.sub) : at;
+  }
+  const int64_t row = te.row0 + r;
+  O* c = static_cast<O*>(p.c) + row * p.ldc + col;
+  const O* res = p.res != nullptr ? static_cast<const O*>(p.res) + row * p.ldres + col : nullptr;
+  T* z = p.z != nullptr ? static_cast<T*>(p.z) + row * p.ldz + col : nullptr;
+  for (; r < last; r += G * kDown) {
+    // all loads first and without branches: a row past the end reads the
+    // last (and is not stored: its residual may already be overwritten)
+    float4 f[G][SP];
+    Quad<O> e[G];
+    int down[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      down[g] = min(g * kDown, static_cast<int>(last - 1) - r);
+#pragma unroll
+      for (int q = 0; q < SP; ++q) {
+        const uint32_t at = from[q] + static_cast<uint32_t>(down[g] * (S::kLd * 4));
+        if constexpr (SP > 1) f[g][q] = ld_cluster_f4(at);
+        else f[g][q] = *reinterpret_cast<const float4*>(te.smem + (at - te.ring));
+      }
+    }
+    if (res != nullptr) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) e[g].load(res + down[g] * p.ldres);
+    }
+    float v[G][4];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float4 t = f[g][0];
+#pragma unroll
+      for (int q = 1; q < SP; ++q) {
+        t.x += f[g][q].x;
+        t.y += f[g][q].y;
+        t.z += f[g][q].z;
+        t.w += f[g][q].w;
+      }
+      v[g][0] = t.x + bias.x;
+      v[g][1] = t.y + bias.y;
+      v[g][2] = t.z + bias.z;
+      v[g][3] = t.w + bias.w;
+    }
+    if (z != nullptr) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (down[g] == g * kDown) store4<T>(z + down[g] * p.ldz, v[g]);
+    }
+    act_all<kExact, 4 * G>(&v[0][0], p.act);
+    if (res != nullptr) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float4 a = e[g].get();
+        v[g][0] += a.x;
+        v[g][1] += a.y;
+        v[g][2] += a.z;
+        v[g][3] += a.w;
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      if (down[g] == g * kDown) store4<O>(c + down[g] * p.ldc, v[g]);
+#pragma unroll
+    for (int q = 0; q < SP; ++q) from[q] += G * kDown * S::kLd * 4;
+    c += G * kDown * p.ldc;
+    if (res != nullptr) res += G * kDown * p.ldres;
+    if (z != nullptr) z += G * kDown * p.ldz;
+  }
+}
+template <class S, typename T, typename O>
+__device__ __forceinline__ void finish_tile(const TileEnd& te, int splits, const DenseParams& p) {
+  switch (splits) {
+    case 1: finish_rows<S, T, O, 4, 1>(te, p); break;
+    case 2: finish_rows<S, T, O, 4, 2>(te, p); break;
+    case 4: finish_rows<S, T, O, 2, 4>(te, p); break;
+    default: finish_rows<S, T, O, 1, 8>(te, p); break;
+  }
+}
+
 template <class S>
 __global__ void __launch_bounds__(S::kThreads)
     dense_split_kernel(const __grid_constant__ CUtensorMap map_a,
@@ -285,6 +340,15 @@ __global__ void __launch_bounds__(S::kThreads)
     }
     s.abort_flag = 0;
     mbar_fence_init();
+    if constexpr (CG == 1) {  // the barriers are this thread's own so far
+      for (int i = 0; i < min(stages, nkb); ++i) {
+        uint8_t* sa = ring + i * kStage;
+        const uint32_t bar = smem_u32(&s.full[i]);
+        mbar_arrive_expect_tx(&s.full[i], kStage);
+        operand_load<1, S::AMN, kTileM>(sa, &map_a, bar, a0, (kb0 + i) * kBlockK);
+        operand_load<1, S::BMN, S::kBRows>(sa + kATile, &map_b, bar, b0, (kb0 + i) * kBlockK);
+      }
+    }
   }
   if (warp == 1) {
     tmem_alloc<CG>(&s.tmem_base, S::kCols);
@@ -302,9 +366,14 @@ __global__ void __launch_bounds__(S::kThreads)
       int stage = 0, filled = 0;
       uint32_t phase = 0;
       bool ok = true;
+      if constexpr (CG == 1) {  // the first stages were requested before the barrier
+        filled = min(stages, nkb);
+        stage = filled == stages ? 0 : filled;
+        phase = filled == stages ? 1u : 0u;
+      }
       // a pair's bytes complete on the even CTA's barrier, which it arms for both
       const uint32_t full0 = CG == 2 ? mapa_shared(smem_u32(&s.full[0]), even) : smem_u32(&s.full[0]);
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = kb0 + filled; kb < kb1; ++kb) {
         ok = mbar_wait(&s.empty[stage], phase ^ 1u, wc);
         if (!ok) break;
         uint8_t* sa = ring + stage * kStage;
@@ -427,47 +496,16 @@ __global__ void __launch_bounds__(S::kThreads)
   else __syncthreads();
 
   // this CTA's share of the tile's rows: the sum over the partials of the
-  // splits, and the epilogue, four groups of four columns at a time where
-  // there are as many
-  constexpr int kPer = S::kColsOut / 4;
-  const int64_t row0 = S::SWAP ? b0 : a0, col0 = S::SWAP ? a0 : b0;
+  // splits, and the epilogue
   const int r0 = S::kRowsOut * split / splits, r1 = S::kRowsOut * (split + 1) / splits;
-  const uint32_t base = smem_u32(ring);
-  auto finish = [&](auto groups, int i) {  // `groups` groups from the i-th on
-    constexpr int G = decltype(groups)::value;
-    float v[G][4];
-    int64_t row[G], col[G];
-    bool on[G];
-    uint32_t at[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int k = i + g * S::kThreads;
-      const int r = r0 + k / kPer, cc = (k % kPer) * 4;
-      on[g] = row0 + r < p.M && col0 + cc < p.N;
-      row[g] = min(row0 + r, p.M - 1);
-      col[g] = min(col0 + cc, p.N - 4);
-      at[g] = base + static_cast<uint32_t>(r * S::kLd + cc) * 4;
-      v[g][0] = v[g][1] = v[g][2] = v[g][3] = 0.0f;
-    }
-#pragma unroll 2
-    for (int q = 0; q < splits; ++q) {
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        float4 f;
-        if (splits > 1) f = ld_cluster_f4(mapa_shared(at[g], q * CG + sub));
-        else f = *reinterpret_cast<const float4*>(ring + (at[g] - base));
-        v[g][0] += f.x;
-        v[g][1] += f.y;
-        v[g][2] += f.z;
-        v[g][3] += f.w;
-      }
-    }
-    epilogue4_any<G>(v, row, col, on, p);
-  };
-  const int total = (r1 - r0) * kPer;
-  int i = threadIdx.x;
-  for (; i + 3 * S::kThreads < total; i += 4 * S::kThreads) finish(std::integral_constant<int, 4>{}, i);
-  for (; i < total; i += S::kThreads) finish(std::integral_constant<int, 1>{}, i);
+  const TileEnd te{S::SWAP ? b0 : a0, S::SWAP ? a0 : b0, r0, r1, smem_u32(ring), ring, sub};
+  if (p.out_type == MOE_FP32) {
+    if (p.type == MOE_BF16) finish_tile<S, __nv_bfloat16, float>(te, splits, p);
+    else finish_tile<S, __half, float>(te, splits, p);
+  } else {
+    if (p.type == MOE_BF16) finish_tile<S, __nv_bfloat16, __nv_bfloat16>(te, splits, p);
+    else finish_tile<S, __half, __half>(te, splits, p);
+  }
   tc_fence_before();
   __syncthreads();
   if (clustered) cluster_sync();  // the others have read this CTA's partial tile
