@@ -10,10 +10,14 @@
 // cluster's CTAs.  Each CTA runs a TMA ring over its share of the reduction,
 // leaves its fp32 partial tile in its own shared memory, and after a cluster
 // barrier every CTA sums one slice of the rows over all partials (in rank
-// order, so results are reproducible) and runs the epilogue on it.  With few
-// rows the roles of the operands are swapped (SWAP): the weights' columns are
-// the tile's 128 side and the rows its narrow side, so that a handful of rows
-// costs a 16-column MMA and the weights are read once by all SMs together.
+// order, so results are reproducible) and runs the epilogue on it.  Narrow
+// tiles swap the roles of the operands (SWAP): the weights' columns are the
+// tile's 128 side and 16, 32 or 64 rows its narrow side, so that a handful of
+// rows costs a 16-column MMA, the weights are read once by all SMs together,
+// and small products have tiles enough for the SMs and short epilogues.
+// For fp32 results the accumulators are drained into registers every
+// kChunkBlocks reduction blocks: the tensor core's additions truncate, and a
+// long chain of them would lose what an fp32 result is asked for.
 // pair kernel: persistent, for products with enough 256 x 256 tiles for the
 // SMs.  The CTA pair of a 2-CTA cluster works on one tile: each CTA loads its
 // 128 rows of A and its 128 columns of B, the even CTA issues
@@ -24,9 +28,6 @@
 // the epilogue behind short reductions); results, z and the residual move through swizzled shared-memory
 // buffers by TMA, the residual of the next tile while its products run.
 //
-// In the split kernel, for fp32 results the accumulators are drained into registers every
-// kChunkBlocks reduction blocks: the tensor core's additions truncate, and a
-// long chain of them would lose what an fp32 result is asked for.
 #include <cuda.h>
 
 #include <algorithm>
@@ -119,18 +120,14 @@ __device__ __forceinline__ bool elect_one() {
 
 // One operand's share of a stage: W rows of 64 reduction elements (K-major,
 // one box), or W / 64 chunks of 64 columns (MN-major).
-template <int CG, bool MN, int W>
-__device__ __forceinline__ void operand_load(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int x0,
+template <bool MN, int W>
+__device__ __forceinline__ void operand_load(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int x0,
                                              int k0) {
   if constexpr (!MN) {
-    if constexpr (CG == 2) tma_load_2d_pair(dst, map, bar, k0, x0);
-    else tma_load_2d_addr(dst, map, bar, k0, x0);
+    tma_load_2d(dst, map, bar, k0, x0);
   } else {
 #pragma unroll
-    for (int j = 0; j < W / 64; ++j) {
-      if constexpr (CG == 2) tma_load_2d_pair(dst + j * kChunk, map, bar, x0 + 64 * j, k0);
-      else tma_load_2d_addr(dst + j * kChunk, map, bar, x0 + 64 * j, k0);
-    }
+    for (int j = 0; j < W / 64; ++j) tma_load_2d(dst + j * kChunk, map, bar, x0 + 64 * j, k0);
   }
 }
 
@@ -145,25 +142,11 @@ __device__ __forceinline__ void issue_block(uint32_t d, uint32_t a, uint32_t b, 
     umma_bf16<CG>(d, ad + kk * (AMN ? 128 : 2), bd + kk * (BMN ? 128 : 2), idesc, kk > 0 ? 1u : add);
 }
 
-template <int CG>
-__device__ __forceinline__ bool wait_any(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
-  return CG == 2 ? mbar_wait_cluster(bar, parity, c) : mbar_wait(bar, parity, c);
-}
-
 // A wait of the whole warp, polled by one lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
   bool ok = true;
   if (elect_one()) ok = mbar_wait(bar, parity, c);
   return __all_sync(0xffffffffu, ok);
-}
-
-// umma_commit for the CTA pair of ranks `even`, even + 1 of a larger cluster.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, int even) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3u << even))
-      : "memory");
 }
 
 struct SplitCtl {
@@ -180,24 +163,20 @@ __host__ __device__ constexpr int tmem_cols(int n) {
   return n <= 32 ? 32 : (n <= 64 ? 64 : (n <= 128 ? 128 : (n <= 256 ? 256 : 512)));
 }
 
-// A tile of the split kernel: 128 CG rows by BN columns over CG CTAs.  SWAP:
-// the 128 side is the output's columns.
-template <int BN_, int CG_, bool AMN_, bool BMN_, bool SWAP_>
+// A tile of the split kernel: 128 by BN.  SWAP: the 128 side is the output's
+// columns.
+constexpr int kSplitThreads = 192;
+template <int BN_, bool AMN_, bool BMN_, bool SWAP_>
 struct SplitShape {
-  static constexpr int BN = BN_, CG = CG_;
+  static constexpr int BN = BN_;
   static constexpr bool AMN = AMN_, BMN = BMN_, SWAP = SWAP_;
-  static constexpr int kBRows = BN / CG;                       // B columns a CTA loads
-  static constexpr int kStage = kATile + kBRows * kBlockK * 2;  // operand bytes of a block, per CTA
-  static constexpr int kEpiWarps = BN > 128 ? 8 : 4;
-  static constexpr int kThreads = 64 + 32 * kEpiWarps;
-  static constexpr int kAcc = BN * 4 / kEpiWarps;              // columns of an epilogue thread
+  static constexpr int kStage = kATile + BN * kBlockK * 2;  // operand bytes of a block
   static constexpr int kCols = tmem_cols(2 * BN);
-  static constexpr int kRowsOut = SWAP ? BN : kTileM;          // a CTA's partial tile
+  static constexpr int kRowsOut = SWAP ? BN : kTileM;       // the partial tile
   static constexpr int kColsOut = SWAP ? kTileM : BN;
   static constexpr int kLd = kColsOut + 4;
-  static constexpr int kPartial = kRowsOut * kLd * 4;          // laid over the operand ring
-  static_assert(!BMN || kBRows % 64 == 0, "MN-major operands come in 64-wide chunks");
-  static_assert(CG == 1 || !SWAP, "swapped tiles are one CTA's");
+  static constexpr int kPartial = kRowsOut * kLd * 4;       // laid over the operand ring
+  static_assert(!BMN || BN % 64 == 0, "MN-major operands come in 64-wide chunks");
 };
 
 // A CTA's part of a finished tile: rows [r0, r1) of the partial tile that lies
@@ -207,7 +186,6 @@ struct TileEnd {
   int r0, r1;
   uint32_t ring;        // shared address of the partial tile
   const uint8_t* smem;  // ... and its pointer
-  int sub;
 };
 
 // Sums the SP partials (in rank order) and runs the epilogue.  A thread keeps
@@ -217,8 +195,8 @@ template <class S, typename T, typename O, int G, int SP>
 __device__ __forceinline__ void finish_rows(const TileEnd& te, const DenseParams& p) {
   constexpr bool kExact = sizeof(O) == 4;
   constexpr int kPer = S::kColsOut / 4;          // threads across a row
-  constexpr int kDown = S::kThreads / kPer;      // rows of one pass
-  static_assert(kDown * kPer == S::kThreads, "threads cover whole rows");
+  constexpr int kDown = kSplitThreads / kPer;    // rows of one pass
+  static_assert(kDown * kPer == kSplitThreads, "threads cover whole rows");
   const int cc = (threadIdx.x % kPer) * 4;
   const int64_t col = te.col0 + cc;
   const int64_t last = min(static_cast<int64_t>(te.r1), p.M - te.row0);  // rows below exist
@@ -230,7 +208,7 @@ __device__ __forceinline__ void finish_rows(const TileEnd& te, const DenseParams
 #pragma unroll
   for (int q = 0; q < SP; ++q) {
     const uint32_t at = te.ring + static_cast<uint32_t>(r * S::kLd + cc) * 4;
-    from[q] = SP > 1 ? mapa_shared(at, q * S::CG + te.sub) : at;
+    from[q] = SP > 1 ? mapa_shared(at, q) : at;
   }
   const int64_t row = te.row0 + r;
   O* c = static_cast<O*>(p.c) + row * p.ldc + col;
@@ -309,20 +287,18 @@ __device__ __forceinline__ void finish_tile(const TileEnd& te, int splits, const
 }
 
 template <class S>
-__global__ void __launch_bounds__(S::kThreads)
+__global__ void __launch_bounds__(kSplitThreads)
     dense_split_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, const DenseParams p,
                        const int stages, const int splits, const int chunk_blocks) {
-  constexpr int BN = S::BN, CG = S::CG, kStage = S::kStage, kEpiWarps = S::kEpiWarps;
+  constexpr int BN = S::BN, kStage = S::kStage;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   SplitCtl& s = *reinterpret_cast<SplitCtl*>(ring + stages * kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool clustered = CG * splits > 1;
-  const int crank = clustered ? static_cast<int>(cluster_ctarank()) : 0;
-  const int split = crank / CG, sub = crank % CG, even = crank - sub;
-  const int a0 = (blockIdx.x / (CG * splits)) * (kTileM * CG) + kTileM * sub;  // this CTA's 128 side
-  const int b0 = blockIdx.y * BN;                                              // the tile's BN side
+  const int split = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int a0 = (blockIdx.x / splits) * kTileM;  // first row of the tile's 128 side
+  const int b0 = blockIdx.y * BN;                 // ... of its BN side
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * split / splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (split + 1) / splits);
   const int nkb = kb1 - kb0;
@@ -336,58 +312,49 @@ __global__ void __launch_bounds__(S::kThreads)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.tfull[i], 1);
-      mbar_init(&s.tempty[i], kEpiWarps * CG);
+      mbar_init(&s.tempty[i], 4);
     }
     s.abort_flag = 0;
     mbar_fence_init();
-    if constexpr (CG == 1) {  // the barriers are this thread's own so far
-      for (int i = 0; i < min(stages, nkb); ++i) {
-        uint8_t* sa = ring + i * kStage;
-        const uint32_t bar = smem_u32(&s.full[i]);
-        mbar_arrive_expect_tx(&s.full[i], kStage);
-        operand_load<1, S::AMN, kTileM>(sa, &map_a, bar, a0, (kb0 + i) * kBlockK);
-        operand_load<1, S::BMN, S::kBRows>(sa + kATile, &map_b, bar, b0, (kb0 + i) * kBlockK);
-      }
+    // the first stages' operands come while the rest is set up (the barriers
+    // are this thread's own so far)
+    for (int i = 0; i < min(stages, nkb); ++i) {
+      uint8_t* sa = ring + i * kStage;
+      mbar_arrive_expect_tx(&s.full[i], kStage);
+      operand_load<S::AMN, kTileM>(sa, &map_a, &s.full[i], a0, (kb0 + i) * kBlockK);
+      operand_load<S::BMN, BN>(sa + kATile, &map_b, &s.full[i], b0, (kb0 + i) * kBlockK);
     }
   }
   if (warp == 1) {
-    tmem_alloc<CG>(&s.tmem_base, S::kCols);
-    tmem_relinquish<CG>();
+    tmem_alloc<1>(&s.tmem_base, S::kCols);
+    tmem_relinquish<1>();
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();  // the pair's barriers exist before any remote arrive
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
 
   if (warp == 0) {
     if (elect_one()) {
-      int stage = 0, filled = 0;
-      uint32_t phase = 0;
+      int filled = min(stages, nkb), stage = filled % stages;
+      uint32_t phase = filled / stages;
       bool ok = true;
-      if constexpr (CG == 1) {  // the first stages were requested before the barrier
-        filled = min(stages, nkb);
-        stage = filled == stages ? 0 : filled;
-        phase = filled == stages ? 1u : 0u;
-      }
-      // a pair's bytes complete on the even CTA's barrier, which it arms for both
-      const uint32_t full0 = CG == 2 ? mapa_shared(smem_u32(&s.full[0]), even) : smem_u32(&s.full[0]);
       for (int kb = kb0 + filled; kb < kb1; ++kb) {
         ok = mbar_wait(&s.empty[stage], phase ^ 1u, wc);
         if (!ok) break;
         uint8_t* sa = ring + stage * kStage;
-        if (sub == 0) mbar_arrive_expect_tx(&s.full[stage], CG * kStage);
-        const uint32_t bar = full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
-        operand_load<CG, S::AMN, kTileM>(sa, &map_a, bar, a0, kb * kBlockK);
-        operand_load<CG, S::BMN, S::kBRows>(sa + kATile, &map_b, bar, b0 + S::kBRows * sub, kb * kBlockK);
+        uint64_t* bar = &s.full[stage];
+        mbar_arrive_expect_tx(bar, kStage);
+        operand_load<S::AMN, kTileM>(sa, &map_a, bar, a0, kb * kBlockK);
+        operand_load<S::BMN, BN>(sa + kATile, &map_b, bar, b0, kb * kBlockK);
         ++filled;
         if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      if (!ok && sub == 0) {  // copies in flight land before the CTA goes on
+      if (!ok) {  // copies in flight land before the CTA goes on
         for (int i = 0; i < stages; ++i) {
           const int f = filled > i ? (filled - i + stages - 1) / stages : 0;
           if (f > 0) (void)mbar_wait_drain(&s.full[i], (f - 1) & 1, 100000000ull);
@@ -398,8 +365,8 @@ __global__ void __launch_bounds__(S::kThreads)
     // one thread waits, issues and commits: between two blocks there is
     // nothing for the others to do, and every warp-wide step is latency that
     // the tensor core would idle through
-    if (sub == 0 && elect_one()) {
-      const uint32_t idesc = dense_idesc(kTileM * CG, BN, S::AMN, S::BMN, p.type == MOE_BF16 ? 1u : 0u);
+    if (elect_one()) {
+      const uint32_t idesc = dense_idesc(kTileM, BN, S::AMN, S::BMN, p.type == MOE_BF16 ? 1u : 0u);
       const uint32_t base = smem_u32(ring);
       int stage = 0, done = 0, left = nkb;
       uint32_t phase = 0;
@@ -407,28 +374,24 @@ __global__ void __launch_bounds__(S::kThreads)
       for (int chunk = 0; left > 0 && ok; ++chunk) {
         const int n = min(left, chunk_blocks);
         const int slot = chunk & 1;
-        if (chunk >= 2) ok = wait_any<CG>(&s.tempty[slot], ((chunk >> 1) - 1) & 1, wc);
+        if (chunk >= 2) ok = mbar_wait(&s.tempty[slot], ((chunk >> 1) - 1) & 1, wc);
         tc_fence_after();
         uint32_t add = 0u;
         for (int i = 0; i < n && ok; ++i) {
-          ok = wait_any<CG>(&s.full[stage], phase, wc);
+          ok = mbar_wait(&s.full[stage], phase, wc);
           if (!ok) break;
           tc_fence_after();
-          issue_block<CG, S::AMN, S::BMN>(tmem + slot * BN, base + stage * kStage,
+          issue_block<1, S::AMN, S::BMN>(tmem + slot * BN, base + stage * kStage,
                                           base + stage * kStage + kATile, idesc, add);
           add = 1u;
-          if constexpr (CG == 2) umma_commit_pair(&s.empty[stage], even);
-          else umma_commit<1>(&s.empty[stage]);
+          umma_commit<1>(&s.empty[stage]);
           ++done;
           if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (ok) {
-          if constexpr (CG == 2) umma_commit_pair(&s.tfull[slot], even);
-          else umma_commit<1>(&s.tfull[slot]);
-        }
+        if (ok) umma_commit<1>(&s.tfull[slot]);
         left -= n;
       }
       if (!ok && done > 0) {  // issued products end before TMEM is freed
@@ -437,24 +400,22 @@ __global__ void __launch_bounds__(S::kThreads)
       }
     }
   } else {
-    // drain the accumulators into registers, chunk by chunk: rows 32 q.. of
-    // this CTA's 128, columns kAcc half..
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t tq = tmem + half * S::kAcc + (static_cast<uint32_t>(q * 32) << 16);
-    float acc[S::kAcc];
+    // drain the accumulators into registers, chunk by chunk
+    const int q = warp & 3;  // TMEM lane quarter of this warp
+    const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    float acc[BN];
 #pragma unroll
-    for (int j = 0; j < S::kAcc; ++j) acc[j] = 0.0f;
+    for (int j = 0; j < BN; ++j) acc[j] = 0.0f;
     const int chunks = (nkb + chunk_blocks - 1) / chunk_blocks;
-    const uint32_t tempty0 = CG == 2 ? mapa_shared(smem_u32(&s.tempty[0]), even) : 0u;
     bool ok = true;
     for (int c = 0; c < chunks; ++c) {
       const int slot = c & 1;
       ok = warp_wait(&s.tfull[slot], (c >> 1) & 1, wc);
       if (!ok) break;
       tc_fence_after();
-      if constexpr (S::kAcc >= 32) {
+      if constexpr (BN >= 32) {
 #pragma unroll
-        for (int j = 0; j < S::kAcc; j += 32) {
+        for (int j = 0; j < BN; j += 32) {
           uint32_t v[32];
           tmem_ld_32x32b_x32(tq + slot * BN + j, v);
           tmem_ld_wait();
@@ -470,10 +431,7 @@ __global__ void __launch_bounds__(S::kThreads)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (CG == 2 && sub != 0) mbar_arrive_remote(tempty0 + slot * static_cast<uint32_t>(sizeof(uint64_t)));
-        else mbar_arrive(&s.tempty[slot]);
-      }
+      if (lane == 0) mbar_arrive(&s.tempty[slot]);
     }
     // every product has read its operands: the ring now holds the partial
     // tile, in the output's orientation
@@ -482,23 +440,23 @@ __global__ void __launch_bounds__(S::kThreads)
       const int r = q * 32 + lane;
       if constexpr (S::SWAP) {
 #pragma unroll
-        for (int j = 0; j < S::kAcc; ++j) part[j * S::kLd + r] = acc[j];
+        for (int j = 0; j < BN; ++j) part[j * S::kLd + r] = acc[j];
       } else {
 #pragma unroll
-        for (int j = 0; j < S::kAcc; j += 4)
-          *reinterpret_cast<float4*>(part + r * S::kLd + half * S::kAcc + j) =
+        for (int j = 0; j < BN; j += 4)
+          *reinterpret_cast<float4*>(part + r * S::kLd + j) =
               make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
       }
     }
   }
   __syncwarp();
-  if (clustered) cluster_sync();
+  if (splits > 1) cluster_sync();
   else __syncthreads();
 
   // this CTA's share of the tile's rows: the sum over the partials of the
   // splits, and the epilogue
   const int r0 = S::kRowsOut * split / splits, r1 = S::kRowsOut * (split + 1) / splits;
-  const TileEnd te{S::SWAP ? b0 : a0, S::SWAP ? a0 : b0, r0, r1, smem_u32(ring), ring, sub};
+  const TileEnd te{S::SWAP ? b0 : a0, S::SWAP ? a0 : b0, r0, r1, smem_u32(ring), ring};
   if (p.out_type == MOE_FP32) {
     if (p.type == MOE_BF16) finish_tile<S, __nv_bfloat16, float>(te, splits, p);
     else finish_tile<S, __half, float>(te, splits, p);
@@ -508,10 +466,10 @@ __global__ void __launch_bounds__(S::kThreads)
   }
   tc_fence_before();
   __syncthreads();
-  if (clustered) cluster_sync();  // the others have read this CTA's partial tile
+  if (splits > 1) cluster_sync();  // the others have read this CTA's partial tile
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc<CG>(tmem, S::kCols);
+    tmem_dealloc<1>(tmem, S::kCols);
   }
 }
 
@@ -938,14 +896,8 @@ DenseParams make_params(const DenseCall& c) {
   return p;
 }
 
-// How the splits of a product are laid out on the device.
-struct SplitPlan {
-  int splits;  // of the reduction: 1, 2, 4 or 8
-  int per_sm;  // CTAs that an SM should be able to hold
-};
-
 template <class S>
-cudaError_t launch_split(const DenseCall& c, const SplitPlan& plan, cudaStream_t s) {
+cudaError_t launch_split(const DenseCall& c, int splits, cudaStream_t s) {
   auto kern = dense_split_kernel<S>;
   static std::atomic<bool> attr_set[64];
   cudaError_t err = allow_smem(kern, attr_set, kSplitSmemLimit);
@@ -960,39 +912,39 @@ cudaError_t launch_split(const DenseCall& c, const SplitPlan& plan, cudaStream_t
   const bool ok = (S::AMN ? map2d(&ma, a, na, c.Kred, lda, 64, kBlockK)
                           : map2d(&ma, a, c.Kred, na, lda, kBlockK, kTileM)) &&
                   (S::BMN ? map2d(&mb, b, nb, c.Kred, ldb, 64, kBlockK)
-                          : map2d(&mb, b, c.Kred, nb, ldb, kBlockK, S::kBRows));
+                          : map2d(&mb, b, c.Kred, nb, ldb, kBlockK, S::BN));
   if (!ok) return cudaErrorInvalidValue;
   // no more stages than reduction blocks, no fewer than the partial tile
   // needs, and so many that CTAs that fit an SM's shared memory together never
   // ask for more than its 512 tensor-memory columns: clusters that overlap
   // (on two streams) would otherwise wait for each other's columns.  The
-  // smallest CTA takes 38 KB, which is not left beside one with 512 columns.
-  constexpr int kFloorBytes =
-      S::kCols == 512 ? 192 * 1024 : 228 * 1024 / (512 / S::kCols + 1) + 1024;
+  // smallest CTA takes 38 KB, which is not left beside the pair kernel's.
+  constexpr int kFloorBytes = 228 * 1024 / (512 / S::kCols + 1) + 1024;
   constexpr int kLeast =
       std::max({2, (S::kPartial + S::kStage - 1) / S::kStage, (kFloorBytes + S::kStage - 1) / S::kStage});
   constexpr int kOver = 1024 + static_cast<int>(sizeof(SplitCtl));
   static_assert(kLeast <= kSplitMaxStages && kLeast * S::kStage + kOver <= kSplitSmemLimit, "shared memory");
-  const int budget = kSplitSmemLimit / plan.per_sm - kOver - 1024;
-  const int mine = static_cast<int>(cdiv(p.kblocks, plan.splits));
+  // two CTAs to an SM: clusters of eight find room beside one another, and
+  // one's epilogue overlaps the other's products
+  const int budget = kSplitSmemLimit / 2 - kOver - 1024;
+  const int mine = static_cast<int>(cdiv(p.kblocks, splits));
   const int stages = std::max(kLeast, std::min({budget / S::kStage, kSplitMaxStages, mine}));
   const size_t bytes = static_cast<size_t>(stages) * S::kStage + kOver;
   const int chunk = c.out_type == MOE_FP32 ? kChunkBlocks : p.kblocks;
-  const unsigned ctas = static_cast<unsigned>(S::CG * plan.splits);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(na, kTileM * S::CG)) * ctas,
+  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(na, kTileM) * splits),
                      static_cast<unsigned>(cdiv(nb, S::BN)), 1);
-  cfg.blockDim = dim3(S::kThreads, 1, 1);
+  cfg.blockDim = dim3(kSplitThreads, 1, 1);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = ctas > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mb, p, stages, plan.splits, chunk);
+  cfg.numAttrs = splits > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, p, stages, splits, chunk);
 }
 
 template <bool MN>
@@ -1062,46 +1014,77 @@ cudaError_t launch_pair_type(const DenseCall& c, cudaStream_t s) {
   return launch_pair<T, false, false, false>(c, s);
 }
 
-// The splits of the reduction for `tiles` tiles of `ctas` CTAs: as many as
-// fit `room` CTAs, up to `most`, with at least two reduction blocks for each.
-int pick_splits(int64_t tiles, int64_t kblocks, int ctas, int64_t room, int most) {
-  int s = 1;
-  while (s < most && tiles * ctas * (s * 2) <= room && kblocks >= 4 * s) s *= 2;
-  return s;
+// The kernel, tile and splits of a product, by an estimate in cycles fitted to
+// measurements (bf16, 25 shapes from 1 x 320 x 192 to 19709 x 448 x 576, each
+// under every tile and split; it takes the fastest or one within 15% of it).
+//   split kernel: 7000 to launch, set up and end; per reduction block 450 to
+//   700 for the wider tiles (bound by the operands' way from L2); 900 to 6000
+//   for a tile's epilogue, shared by the splits; 4000 for a cluster's
+//   barriers; all of the per-tile part times the CTAs per SM above one.
+//   pair kernel: 17500, and per wave of tiles 600 a block, or the epilogue's
+//   6500 where that is more.
+struct DensePlan {
+  bool pair;
+  int bn, splits;
+};
+DensePlan plan_dense(const DenseCall& c) {
+  struct Tile { int bn; double block, end; };
+  static const Tile kTiles[] = {{16, 450, 900}, {32, 480, 1500}, {64, 520, 2700}, {128, 700, 6000}};
+  const double sms = sm_count();
+  const double kb = static_cast<double>(cdiv(c.Kred, kBlockK));
+  DensePlan best{false, 128, 1};
+  double least = 1e300;
+  for (const Tile& t : kTiles) {
+    // 16 and 32 wide only swapped (their B is K-major); a wgrad has no rows
+    // to swap, its 64 wide tile is a plain one
+    const bool swap = t.bn < 128 && !c.a_mn;
+    if (t.bn < 64 && !swap) continue;
+    const double tiles = static_cast<double>(swap ? cdiv(c.N, kTileM) * cdiv(c.M, t.bn)
+                                                  : cdiv(c.M, kTileM) * cdiv(c.N, t.bn));
+    for (int s = 1; s <= 8; s *= 2) {
+      // many tiles are the 128 wide ones' alone; a split gets two blocks at least
+      if (tiles * s > 2 * sms && (t.bn < 128 || s > 1)) break;
+      if (s > 1 && kb < 2 * s) break;
+      const double est = 7000 + (kb / s * t.block + t.end / s) * std::max(1.0, tiles * s / sms) +
+                         (s > 1 ? 4000 : 0);
+      if (est < least) {
+        least = est;
+        best = DensePlan{false, t.bn, s};
+      }
+    }
+  }
+  if (c.out_type != MOE_FP32) {
+    const int64_t pairs = sm_count() / 2;
+    const double waves = static_cast<double>(cdiv(cdiv(c.M, 256) * cdiv(c.N, kPairN), pairs));
+    if (17500 + waves * std::max(kb * 600, 6500.0) < least) best.pair = true;
+  }
+  return best;
 }
 
 }  // namespace
 
 cudaError_t launch_dense(const DenseCall& c, cudaStream_t s) {
-  const int64_t kb = cdiv(c.Kred, kBlockK);
-  const int64_t sms = sm_count();
-  // few rows: the weights' columns on the 128 side (wgrads have none: their
-  // rows are a weight axis too).  Two CTAs per SM, so that clusters of eight
-  // find room beside one another.
-  if (!c.a_mn && c.M <= 64) {
-    const SplitPlan plan{pick_splits(cdiv(c.N, kTileM), kb, 1, sms, 8), 2};
-    if (c.M <= 16)
-      return c.b_mn ? launch_split<SplitShape<16, 1, true, false, true>>(c, plan, s)
-                    : launch_split<SplitShape<16, 1, false, false, true>>(c, plan, s);
-    if (c.M <= 32)
-      return c.b_mn ? launch_split<SplitShape<32, 1, true, false, true>>(c, plan, s)
-                    : launch_split<SplitShape<32, 1, false, false, true>>(c, plan, s);
-    return c.b_mn ? launch_split<SplitShape<64, 1, true, false, true>>(c, plan, s)
-                  : launch_split<SplitShape<64, 1, false, false, true>>(c, plan, s);
-  }
-  const int64_t pair_tiles = cdiv(c.M, 256) * cdiv(c.N, kPairN);
-  if (c.out_type != MOE_FP32 && 2 * pair_tiles * 3 >= sms)
+  const DensePlan plan = plan_dense(c);
+  if (plan.pair)
     return c.type == MOE_BF16 ? launch_pair_type<__nv_bfloat16>(c, s) : launch_pair_type<__half>(c, s);
-  if (2 * pair_tiles * 6 >= sms) {
-    const SplitPlan plan{pick_splits(pair_tiles, kb, 2, sms, 4), 1};
-    if (c.a_mn) return launch_split<SplitShape<256, 2, true, true, false>>(c, plan, s);
-    if (c.b_mn) return launch_split<SplitShape<256, 2, false, true, false>>(c, plan, s);
-    return launch_split<SplitShape<256, 2, false, false, false>>(c, plan, s);
+  if (c.a_mn) {
+    if (plan.bn == 64) return launch_split<SplitShape<64, true, true, false>>(c, plan.splits, s);
+    return launch_split<SplitShape<128, true, true, false>>(c, plan.splits, s);
   }
-  const SplitPlan plan{pick_splits(cdiv(c.M, kTileM) * cdiv(c.N, 128), kb, 1, sms, 8), 2};
-  if (c.a_mn) return launch_split<SplitShape<128, 1, true, true, false>>(c, plan, s);
-  if (c.b_mn) return launch_split<SplitShape<128, 1, false, true, false>>(c, plan, s);
-  return launch_split<SplitShape<128, 1, false, false, false>>(c, plan, s);
+  switch (plan.bn) {
+    case 16:
+      return c.b_mn ? launch_split<SplitShape<16, true, false, true>>(c, plan.splits, s)
+                    : launch_split<SplitShape<16, false, false, true>>(c, plan.splits, s);
+    case 32:
+      return c.b_mn ? launch_split<SplitShape<32, true, false, true>>(c, plan.splits, s)
+                    : launch_split<SplitShape<32, false, false, true>>(c, plan.splits, s);
+    case 64:
+      return c.b_mn ? launch_split<SplitShape<64, true, false, true>>(c, plan.splits, s)
+                    : launch_split<SplitShape<64, false, false, true>>(c, plan.splits, s);
+    default:
+      return c.b_mn ? launch_split<SplitShape<128, false, true, false>>(c, plan.splits, s)
+                    : launch_split<SplitShape<128, false, false, false>>(c, plan.splits, s);
+  }
 }
 
 }  // namespace moe
