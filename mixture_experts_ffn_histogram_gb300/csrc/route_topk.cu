@@ -219,31 +219,32 @@ __device__ __forceinline__ float worst_error(float largest) {
   return SOFTMAX ? 3.1e-6f * largest : 6.5e-7f;
 }
 
-// vpl: experts a lane holds at most (<= VPL); lpg: lanes of a group.
+// One token by a whole warp.  vpl: experts a lane holds at most (<= VPL); lpg:
+// lanes of a group; cand: room for 32 (value, id) candidates.
 template <int VPL, bool SOFTMAX>
-__global__ void __launch_bounds__(32 * kTopkWarps)
-    route_topk_kernel(const TopkArgs p, const int vpl, const int lpg) {
-  __shared__ float2 cand[kTopkWarps][32];  // (value, id) of the candidates
-  const moe_topk_dims d = p.d;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int E = d.E, K = d.K;
-  const bool biased = p.bias != nullptr;
-  const bool grouped = d.groups > 1 && d.top_groups < d.groups;
-  const bool by_s = grouped && !biased && d.group_top == 2;  // groups scored by s
-  const bool need_total = SOFTMAX && (biased || by_s || !d.renorm);
-  // this lane's experts: `mine` of them from `first`
-  const int gs = grouped ? E / d.groups : E;  // experts a run of lpg lanes shares
-  const int group = lane / lpg, r = lane - group * lpg;
-  const int first = group * gs + r * vpl;
-  const int mine = group * gs < E ? max(0, min(vpl, gs - r * vpl)) : 0;
-  const bool vec = VPL % 4 == 0 && vpl % 4 == 0 && gs % 4 == 0 && E % 4 == 0;
-  const bool pow2 = (lpg & (lpg - 1)) == 0;
-  const uint32_t below = (1u << lane) - 1u;
-  float b[VPL];
+struct WarpToken {
+  const TopkArgs& p;
+  float2* cand;
+  int vpl, lpg, lane, first, mine, group, r;
+  bool vec;
+
+  __device__ __forceinline__ WarpToken(const TopkArgs& p_, float2* cand_, int vpl_, int lpg_)
+      : p(p_), cand(cand_), vpl(vpl_), lpg(lpg_), lane(threadIdx.x & 31) {
+    // this lane's experts: `mine` of them from `first`
+    const moe_topk_dims& d = p.d;
+    const int gs = d.groups > 1 && d.top_groups < d.groups ? d.E / d.groups : d.E;
+    group = lane / lpg;
+    r = lane - group * lpg;
+    first = group * gs + r * vpl;
+    mine = group * gs < d.E ? max(0, min(vpl, gs - r * vpl)) : 0;
+    vec = VPL % 4 == 0 && vpl % 4 == 0 && gs % 4 == 0 && d.E % 4 == 0;
+  }
+  __device__ __forceinline__ void load_bias(float (&b)[VPL]) const {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) b[i] = biased && i < mine ? __ldg(p.bias + first + i) : 0.0f;
-  auto load_row = [&](int64_t t, float (&l)[VPL]) {
-    const float* row = p.logits + t * E;
+    for (int i = 0; i < VPL; ++i) b[i] = p.bias != nullptr && i < mine ? __ldg(p.bias + first + i) : 0.0f;
+  }
+  __device__ __forceinline__ void load_row(int64_t t, float (&l)[VPL]) const {
+    const float* row = p.logits + t * p.d.E;
     if (vec) {
 #pragma unroll
       for (int i = 0; i + 3 < VPL; i += 4) {
@@ -258,17 +259,21 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
 #pragma unroll
       for (int i = 0; i < VPL; ++i) l[i] = i < mine ? __ldg(row + first + i) : kNegInf;
     }
-  };
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTopkWarps;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * kTopkWarps + warp;
-  float ahead[VPL];
-  if (t < d.T) load_row(t, ahead);
-  for (; t < d.T; t += stride) {
+  }
+
+  // Selects and writes token t from its row l (NaN not yet taken as masked).
+  __device__ __forceinline__ void run(int64_t t, float (&l)[VPL], const float (&b)[VPL]) {
+  const moe_topk_dims& d = p.d;
+  const int E = d.E, K = d.K;
+  const bool biased = p.bias != nullptr;
+  const bool grouped = d.groups > 1 && d.top_groups < d.groups;
+  const bool by_s = grouped && !biased && d.group_top == 2;  // groups scored by s
+  const bool need_total = SOFTMAX && (biased || by_s || !d.renorm);
+  const bool pow2 = (lpg & (lpg - 1)) == 0;
+  const uint32_t below = (1u << lane) - 1u;
     const float* row = p.logits + t * E;
-    float l[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) l[i] = clean(ahead[i]);
-    if (t + stride < d.T) load_row(t + stride, ahead);  // the next token's row, meanwhile
+    for (int i = 0; i < VPL; ++i) l[i] = clean(l[i]);
 
     float m = 0.0f, inv_total = 0.0f;
     if constexpr (SOFTMAX) {
@@ -381,12 +386,12 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (l[i] >= bound) cand[warp][at++] = make_float2(l[i], __int_as_float(first + i));
+        if (l[i] >= bound) cand[at++] = make_float2(l[i], __int_as_float(first + i));
       __syncwarp();
       float v = kNegInf;
       int id = 0;
       if (lane < n) {
-        const float2 c = cand[warp][lane];
+        const float2 c = cand[lane];
         v = c.x;
         id = __float_as_int(c.y);
       }
@@ -396,10 +401,10 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
         rank += (o > v || (o == v && j < lane)) ? 1 : 0;
       }
       __syncwarp();
-      if (lane < n) cand[warp][rank] = make_float2(v, __int_as_float(id));
+      if (lane < n) cand[rank] = make_float2(v, __int_as_float(id));
       __syncwarp();
       if (lane < n) {
-        const float2 c = cand[warp][lane];
+        const float2 c = cand[lane];
         v = c.x;
         id = __float_as_int(c.y);
       }
@@ -415,9 +420,9 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
         const bool unsure = lane < K && lane + 1 < n && v - o_v <= err && !(lo == o_l && bs == o_b);
         if (__any_sync(kAll, unsure)) {
           rank = rank_fp64<SOFTMAX>(row, p.bias, E, id, lo, n, lane);
-          if (lane < n) cand[warp][rank] = make_float2(v, __int_as_float(id));
+          if (lane < n) cand[rank] = make_float2(v, __int_as_float(id));
           __syncwarp();
-          if (lane < n) id = __float_as_int(cand[warp][lane].y);
+          if (lane < n) id = __float_as_int(cand[lane].y);
         }
       }
       my_id = id;
@@ -488,6 +493,356 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
     if (lane < K) {
       p.ids[t * K + lane] = my_id;
       p.w[t * K + lane] = s * d.scale;
+    }
+  }
+};
+
+template <int VPL, bool SOFTMAX>
+__global__ void __launch_bounds__(32 * kTopkWarps)
+    route_topk_kernel(const __grid_constant__ TopkArgs p, const int vpl, const int lpg) {
+  __shared__ float2 cand[kTopkWarps][32];
+  const int warp = threadIdx.x >> 5;
+  WarpToken<VPL, SOFTMAX> w(p, cand[warp], vpl, lpg);
+  float b[VPL];
+  w.load_bias(b);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTopkWarps;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kTopkWarps + warp;
+  float ahead[VPL];
+  if (t < p.d.T) w.load_row(t, ahead);
+  for (; t < p.d.T; t += stride) {
+    float l[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = ahead[i];
+    if (t + stride < p.d.T) w.load_row(t + stride, ahead);  // the next token's row, meanwhile
+    w.run(t, l, b);
+  }
+}
+
+// --------------------------------------------------- several tokens a warp
+// The same selection with LANES = 8 or 16 lanes to a token: most of a token's
+// instructions are not its experts' but the selection's, which a few lanes
+// share as well as thirty-two do.  A lane
+// holds up to 32 experts; the bound comes from the best of each quarter of
+// a lane's, and the candidates (up to 32) are ranked through shared memory.  A token whose
+// candidates do not fit, and one with near ties, is finished by the whole
+// warp.  Bound by latency (96 registers leave 20 warps an SM, which issue in
+// half of the cycles).  32768 tokens, 256 experts in 8 groups: 8 taken 27 us,
+// 35 us with a token a warp; 16 taken 38 us and 94 us.
+template <int LANES>
+__device__ __forceinline__ float sub_max(float v) {
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float sub_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// A token that the packed kernel leaves to the whole warp (at most 256 experts).
+template <bool SOFTMAX>
+__device__ __noinline__ void whole_warp_token(const TopkArgs& p, float2* cand, int vpl, int lpg,
+                                              int64_t t) {
+  WarpToken<8, SOFTMAX> w(p, cand, vpl, lpg);
+  float b[8], l[8];
+  w.load_bias(b);
+  w.load_row(t, l);
+  w.run(t, l, b);
+}
+
+// The order of a token's n sorted candidates, checked pair by pair against
+// the bounds of their scores and redone in fp64 where one fails.  Whole warp.
+template <bool SOFTMAX>
+__device__ __noinline__ void settle_order(const float* row, const float* bias, int E, int K, float2* cand,
+                                          int n, float m, int lane) {
+  float v = kNegInf, bs = 0.0f, lo = kNegInf;
+  int id = 0;
+  if (lane < n) {
+    v = cand[lane].x;
+    id = __float_as_int(cand[lane].y);
+    bs = __ldg(bias + id);
+    lo = clean(__ldg(row + id));
+  }
+  const float o_v = __shfl_down_sync(kAll, v, 1), o_b = __shfl_down_sync(kAll, bs, 1);
+  const float o_l = __shfl_down_sync(kAll, lo, 1);
+  const float err = score_error<SOFTMAX>(v - bs, lo, m) + score_error<SOFTMAX>(o_v - o_b, o_l, m) +
+                    2.0f * kSumError * (fabsf(v) + fabsf(o_v));
+  const bool unsure = lane < K && lane + 1 < n && v - o_v <= err && !(lo == o_l && bs == o_b);
+  if (!__any_sync(kAll, unsure)) return;
+  const int rank = rank_fp64<SOFTMAX>(row, bias, E, id, lo, n, lane);
+  __syncwarp();
+  if (lane < n) cand[rank] = make_float2(v, __int_as_float(id));
+  __syncwarp();
+}
+
+template <int LANES, int VPL, bool SOFTMAX>
+__global__ void __launch_bounds__(32 * kTopkWarps)
+    route_topk_packed_kernel(const __grid_constant__ TopkArgs p, const int vpl, const int lpg,
+                             const int warp_vpl, const int warp_lpg) {
+  constexpr int kTokens = 32 / LANES, kEach = 32 / LANES;  // tokens a warp, candidates a lane
+  constexpr uint32_t kTokenMask = LANES == 32 ? kAll : (1u << LANES) - 1u;
+  constexpr int kRow = VPL + 4;  // a lane's part of a row: 16-byte accesses without bank conflicts
+  __shared__ __align__(16) float rows[kTopkWarps][32][kRow];
+  __shared__ __align__(16) float bias[LANES][kRow];
+  __shared__ float2 cands[kTopkWarps][kTokens][32];
+  const moe_topk_dims& d = p.d;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tok = lane / LANES, r = lane % LANES;
+  const int E = d.E, K = d.K;
+  const bool biased = p.bias != nullptr;
+  const bool grouped = d.groups > 1 && d.top_groups < d.groups;
+  const bool by_s = grouped && !biased && d.group_top == 2;
+  const bool need_total = SOFTMAX && (biased || by_s || !d.renorm);
+  const int gs = grouped ? E / d.groups : E;
+  const int group = r / lpg, part = r - group * lpg;
+  const int first = group * gs + part * vpl;
+  const int mine = group * gs < E ? max(0, min(vpl, gs - part * vpl)) : 0;
+  const bool vec = vpl % 4 == 0 && gs % 4 == 0 && E % 4 == 0;
+  if (biased) {
+    for (int k = threadIdx.x; k < LANES * VPL; k += 32 * kTopkWarps) {
+      const int q = k / VPL, i = k % VPL;
+      const int e = (q / lpg) * gs + (q % lpg) * vpl + i;
+      bias[q][i] = i < vpl && e < E ? __ldg(p.bias + e) : 0.0f;
+    }
+    __syncthreads();
+  }
+  float2* cand = cands[warp][tok];
+  float* own_row = rows[warp][lane];
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTopkWarps * kTokens;
+  for (int64_t base = (static_cast<int64_t>(blockIdx.x) * kTopkWarps + warp) * kTokens; base < d.T;
+       base += stride) {
+    const int64_t t = base + tok;
+    const bool real = t < d.T;
+    const float* row = p.logits + (real ? t : d.T - 1) * E;
+    float l[VPL];
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < VPL; i += 4) {
+        float4 v = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+        if (i < mine) v = __ldg(reinterpret_cast<const float4*>(row + first + i));
+        l[i] = clean(v.x);
+        l[i + 1] = clean(v.y);
+        l[i + 2] = clean(v.z);
+        l[i + 3] = clean(v.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) l[i] = i < mine ? clean(__ldg(row + first + i)) : kNegInf;
+    }
+    float m = 0.0f, inv_total = 0.0f;
+    if constexpr (SOFTMAX) {
+      m = l[0];
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+      m = sub_max<LANES>(m);
+      if (need_total) {
+        float total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          total += l[i] == m && l[i] != kNegInf ? 1.0f : exp2_fast((l[i] - m) * kLog2e);
+        total = sub_sum<LANES>(total);
+        inv_total = m != kNegInf ? 1.0f / total : 0.0f;
+      }
+    }
+    auto fast_score = [&](float v) -> float {
+      if constexpr (SOFTMAX)
+        return (v == m ? 1.0f : exp2_fast((v - m) * kLog2e)) * inv_total;
+      else
+        return rcp_fast(1.0f + exp2_fast(-kLog2e * v));
+    };
+    if (biased) {
+#pragma unroll
+      for (int i = 0; i < VPL; i += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(&bias[r][i]);
+        l[i] = l[i] == kNegInf ? kNegInf : fast_score(l[i]) + b.x;
+        l[i + 1] = l[i + 1] == kNegInf ? kNegInf : fast_score(l[i + 1]) + b.y;
+        l[i + 2] = l[i + 2] == kNegInf ? kNegInf : fast_score(l[i + 2]) + b.z;
+        l[i + 3] = l[i + 3] == kNegInf ? kNegInf : fast_score(l[i + 3]) + b.w;
+      }
+    }
+    const float worst = worst_error<SOFTMAX>(inv_total);
+
+    // the best of each quarter of the lane's experts, then in order
+    float q4[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      q4[c] = l[c * (VPL / 4)];
+#pragma unroll
+      for (int i = 1; i < VPL / 4; ++i) q4[c] = fmaxf(q4[c], l[c * (VPL / 4) + i]);
+    }
+    bool out = mine == 0;
+    if (grouped) {
+      float t1 = kNegInf, t2 = kNegInf;
+      if (d.group_top == 2) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          t2 = fmaxf(t2, fminf(t1, l[i]));
+          t1 = fmaxf(t1, l[i]);
+        }
+        if (by_s) {  // scores keep the logits' order
+          if (t1 != kNegInf) t1 = fast_score(t1);
+          if (t2 != kNegInf) t2 = fast_score(t2);
+        }
+      } else {
+        t1 = fmaxf(fmaxf(q4[0], q4[1]), fmaxf(q4[2], q4[3]));
+      }
+      for (int o = 1; o < lpg; o <<= 1) {
+        const float b1 = __shfl_xor_sync(kAll, t1, o), b2 = __shfl_xor_sync(kAll, t2, o);
+        merge_top2(t1, t2, b1, b2);
+      }
+      const float score = group < d.groups ? group_score(t1, t2, d.group_top) : kNegInf;
+      int ahead = 0;  // groups before this lane's
+      for (int o = lpg; o < LANES; o += lpg) {
+        const int q = (r + o) % LANES;
+        const float other = __shfl_sync(kAll, score, tok * LANES + q);
+        if (q / lpg < d.groups && (other > score || (other == score && q / lpg < group))) ++ahead;
+      }
+      bool stays = group < d.groups && ahead < d.top_groups;
+      if (biased || by_s) {
+        const float in = -sub_max<LANES>(stays ? -score : kNegInf);
+        const float next = sub_max<LANES>(!stays && group < d.groups ? score : kNegInf);
+        const float err = 4.0f * worst + 2.0f * kSumError * (fabsf(in) + fabsf(next));
+        const bool near = real && next > kNegInf && in - next <= err;
+        uint32_t left = __ballot_sync(kAll, near);
+        while (left != 0) {  // a token at a time, by the whole warp
+          const int q = (__ffs(left) - 1) / LANES;
+          left &= ~(kTokenMask << (q * LANES));
+          const bool mineq = tok == q && group < d.groups;
+          const bool in_band = mineq && score <= next + 2.0f * err && score >= in - 2.0f * err;
+          const uint32_t band = __reduce_or_sync(kAll, in_band ? 1u << group : 0u);
+          const uint32_t sure = __reduce_or_sync(kAll, mineq && stays && !in_band ? 1u << group : 0u);
+          const uint32_t stay = sure | groups_fp64<SOFTMAX>(p.logits + (base + q) * E, p.bias, d, band,
+                                                            d.top_groups - __popc(sure), lane);
+          if (mineq) stays = (stay >> group) & 1u;
+        }
+      }
+      out = out || !stays;
+    }
+    // a lower bound of the K-th value: the K-th largest of the quarters' bests
+    auto order = [&](int x, int y) {
+      const float hi = fmaxf(q4[x], q4[y]);
+      q4[y] = fminf(q4[x], q4[y]);
+      q4[x] = hi;
+    };
+    if (out) q4[0] = q4[1] = q4[2] = q4[3] = kNegInf;
+    order(0, 1);
+    order(2, 3);
+    order(0, 2);
+    order(1, 3);
+    order(1, 2);
+    float bound = kNegInf;
+    for (int k = 0; k < K; ++k) {
+      bound = sub_max<LANES>(q4[0]);
+      if (q4[0] == bound) {
+        q4[0] = q4[1];
+        q4[1] = q4[2];
+        q4[2] = q4[3];
+        q4[3] = kNegInf;
+      }
+    }
+    const bool bounded = bound > kNegInf;
+    if (biased) bound -= 2.0f * (worst + kSumError * fabsf(bound));
+    uint32_t mask = 0u;  // the lane's candidates
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (l[i] >= bound) mask |= 1u << i;
+    if (out || !bounded) mask = 0u;
+    const int count = __popc(mask);
+    int upto = count;
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, upto, o, LANES);
+      if (r >= o) upto += v;
+    }
+    const int n = __shfl_sync(kAll, upto, LANES - 1, LANES);
+    const bool good = real && bounded && n >= K && n <= 32;
+    __syncwarp();
+    if (good && mask != 0u) {  // candidates one by one: their values through shared memory
+#pragma unroll
+      for (int i = 0; i < VPL; i += 4)
+        *reinterpret_cast<float4*>(own_row + i) = make_float4(l[i], l[i + 1], l[i + 2], l[i + 3]);
+      int at = upto - count;
+      while (mask != 0u) {
+        const int i = __ffs(mask) - 1;
+        mask &= mask - 1u;
+        cand[at++] = make_float2(own_row[i], __int_as_float(first + i));
+      }
+    }
+    __syncwarp();
+    const int most = __reduce_max_sync(kAll, good ? n : 0);
+    float v[kEach];
+    int id[kEach], rank[kEach];
+#pragma unroll
+    for (int c = 0; c < kEach; ++c) {
+      v[c] = kNegInf;
+      id[c] = rank[c] = 0;
+      if (good && c * LANES + r < n) {
+        const float2 q = cand[c * LANES + r];
+        v[c] = q.x;
+        id[c] = __float_as_int(q.y);
+      }
+    }
+    // candidates lie in the order of their ids, so that an equal one counts as
+    // ahead exactly where it lies before
+#pragma unroll
+    for (int w = 0; w < kEach; ++w) {
+      if (w * LANES >= most) break;
+      const int upper = min(LANES, most - w * LANES);
+      for (int j = 0; j < upper; ++j) {
+        const float o = w * LANES + j < n ? cand[w * LANES + j].x : kNegInf;
+#pragma unroll
+        for (int c = 0; c < kEach; ++c) {
+          if (c < w) rank[c] += o > v[c] ? 1 : 0;
+          else if (c > w) rank[c] += o >= v[c] ? 1 : 0;
+          else rank[c] += (o > v[c] || (o == v[c] && j < r)) ? 1 : 0;
+        }
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < kEach; ++c)
+      if (good && c * LANES + r < n) cand[rank[c]] = make_float2(v[c], __int_as_float(id[c]));
+    __syncwarp();
+    if (biased) {
+      bool near = false;
+      if (good && r < K && r + 1 < n) {
+        const float a = cand[r].x, b = cand[r + 1].x;
+        near = a - b <= 2.0f * (worst + kSumError * (fabsf(a) + fabsf(b)));
+      }
+      uint32_t left = __ballot_sync(kAll, near);
+      while (left != 0) {
+        const int q = (__ffs(left) - 1) / LANES;
+        left &= ~(kTokenMask << (q * LANES));
+        settle_order<SOFTMAX>(p.logits + (base + q) * E, p.bias, E, K, cands[warp][q],
+                              __shfl_sync(kAll, n, q * LANES), __shfl_sync(kAll, m, q * LANES), lane);
+      }
+    }
+    const bool slot = good && r < K;
+    const int my_id = slot ? __float_as_int(cand[r].y) : 0;
+    const float my_l = slot ? clean(__ldg(row + my_id)) : kNegInf;
+    float s = 0.0f;
+    if (slot) {
+      if constexpr (SOFTMAX) s = soft_num(my_l, m);
+      else s = 1.0f / (1.0f + expf(-my_l));
+    }
+    if (d.renorm) {
+      const float total = sub_sum<LANES>(s);
+      s = total > 0.0f ? s / total : 0.0f;
+    } else if constexpr (SOFTMAX) {
+      s *= inv_total;
+    }
+    if (slot) {
+      p.ids[t * K + r] = my_id;
+      p.w[t * K + r] = s * d.scale;
+    }
+    uint32_t rest = __ballot_sync(kAll, real && !good && r == 0);
+    while (rest != 0) {
+      const int q = (__ffs(rest) - 1) / LANES;
+      rest &= rest - 1u;
+      whole_warp_token<SOFTMAX>(p, cands[warp][0], warp_vpl, warp_lpg, base + q);
+      __syncwarp();
     }
   }
 }
@@ -642,10 +997,38 @@ void pick_vpl(int vpl, Go go) {
 cudaError_t launch_route_topk(const float* logits, const float* bias, int32_t* ids, float* w,
                               const moe_topk_dims& d, cudaStream_t s) {
   const TopkArgs a{logits, bias, ids, w, d};
-  const unsigned grid = topk_grid(d.T, 12);
   const bool grouped = d.groups > 1 && d.top_groups < d.groups;
   const int lpg = grouped ? topk_group_lanes(d) : 32;
-  const int vpl = ((grouped ? d.E / d.groups : d.E) + lpg - 1) / lpg;
+  const int gs = grouped ? d.E / d.groups : d.E;
+  const int vpl = (gs + lpg - 1) / lpg;
+  // Several tokens a warp, where the experts, groups and slots fit LANES lanes
+  // and the lanes whose groups stay offer K values for the bound.
+  auto packed = [&](auto lanes) -> bool {
+    constexpr int LANES = decltype(lanes)::value;
+    int lp = LANES;
+    if (grouped) {
+      lp = d.groups <= LANES ? LANES / d.groups : 0;
+      while (lp & (lp - 1)) lp &= lp - 1;  // a power of two
+    }
+    const int vp = lp > 0 ? (gs + lp - 1) / lp : 33;
+    const int alive = lp * (grouped ? d.top_groups : 1);
+    if (vp > 32 || d.E > 256 || d.K > LANES || d.K > 4 * alive) return false;
+    const unsigned grid = topk_grid((d.T + 32 / LANES - 1) / (32 / LANES), LANES == 8 ? 12 : 6);
+    pick_vpl(vp, [&](auto n) {
+      constexpr int VPL = decltype(n)::value < 8 ? 8 : decltype(n)::value;
+      if (d.gate == MOE_GATE_SOFTMAX)
+        route_topk_packed_kernel<LANES, VPL, true><<<grid, 32 * kTopkWarps, 0, s>>>(a, vp, lp, vpl, lpg);
+      else
+        route_topk_packed_kernel<LANES, VPL, false><<<grid, 32 * kTopkWarps, 0, s>>>(a, vp, lp, vpl, lpg);
+    });
+    return true;
+  };
+  // below this a token a warp fills the SMs better (4096 tokens: 9.7 us both
+  // ways, 2048: 6.4 and 7.6)
+  if (d.T >= 32 * static_cast<int64_t>(sm_count()) &&
+      (d.K <= 8 ? packed(std::integral_constant<int, 8>{}) : packed(std::integral_constant<int, 16>{})))
+    return cudaGetLastError();
+  const unsigned grid = topk_grid(d.T, 12);
   pick_vpl(vpl, [&](auto n) {
     constexpr int VPL = decltype(n)::value;
     if (d.gate == MOE_GATE_SOFTMAX)

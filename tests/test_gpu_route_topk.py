@@ -65,6 +65,46 @@ def test_selection_and_weights(T, E, K, gate, bias, groups, top_groups, group_to
     _check(l, b, K, gate, groups, top_groups, group_top, renorm, scale)
 
 
+# enough tokens that they go four to a warp (and a last warp that is not full)
+MANY = [
+    (5003, 256, 8, "sigmoid", True, 8, 4, 2, True, 2.5),
+    (5001, 256, 8, "sigmoid", False, 8, 4, 2, False, 1.0),
+    (5002, 256, 8, "softmax", True, 1, 1, 1, False, 1.0),
+    (5003, 128, 8, "softmax", False, 1, 1, 1, True, 1.0),
+    (5003, 160, 6, "softmax", True, 8, 3, 1, False, 16.0),
+    (5003, 48, 5, "sigmoid", True, 3, 2, 2, True, 1.0),
+    (5003, 50, 4, "sigmoid", True, 2, 1, 2, True, 1.0),
+    (5003, 35, 2, "softmax", True, 7, 1, 2, False, 1.0),
+    (5003, 8, 8, "sigmoid", True, 1, 1, 1, True, 1.0),
+    (5003, 64, 1, "sigmoid", True, 4, 2, 1, True, 1.0),
+    (5003, 250, 7, "softmax", True, 5, 4, 2, True, 1.0),
+    (5003, 256, 16, "sigmoid", True, 8, 4, 2, True, 1.0),
+    (5003, 96, 11, "softmax", True, 12, 5, 2, False, 1.0),
+    (5003, 130, 13, "softmax", False, 1, 1, 1, False, 1.0),
+    (5003, 512, 8, "sigmoid", True, 8, 4, 2, True, 1.0),     # too many experts for it
+]
+
+
+@pytest.mark.parametrize("T,E,K,gate,bias,groups,top_groups,group_top,renorm,scale", MANY)
+def test_many_tokens(T, E, K, gate, bias, groups, top_groups, group_top, renorm, scale):
+    """As above; some tokens with masked experts, few or none left, with equal
+    logits, and with logits a few units in the last place apart."""
+    need_gpu()
+    rng = np.random.default_rng(T + E)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l[:400][rng.random((400, E)) < 0.6] = -np.inf
+    l[400] = -np.inf
+    l[401] = np.nan
+    l[402:440] = 0.25
+    l[440:800] = np.float32(0.7) + rng.integers(-4, 5, (360, E)).astype(np.float32) * np.float32(2.0 ** -24)
+    l[800:900] = np.round(l[800:900], 1)
+    l[900, E // 2] = np.inf
+    b = (0.1 * rng.standard_normal(E)).astype(np.float32) if bias else None
+    if bias:
+        b[: E // 2] = (rng.integers(-3, 4, E // 2) * 2.0 ** -26).astype(np.float32)
+    _check(l, b, K, gate, groups, top_groups, group_top, renorm, scale)
+
+
 @pytest.mark.parametrize("gate", ["sigmoid", "softmax"])
 def test_scores_next_to_one_another(gate):
     """Logits a few units in the last place apart, under biases that differ as
