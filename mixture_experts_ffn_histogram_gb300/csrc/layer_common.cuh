@@ -83,6 +83,18 @@ struct Raw {
       v = make_uint4(q[0], q[1], q[2], q[3]);
     }
   }
+  // zeros for the first e < VEC elements
+  __device__ __forceinline__ void clear_below(int e) {
+    static_assert(kVec, "a vector");
+    constexpr int kPer = 4 / sizeof(T);  // elements of a word
+    uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((i + 1) * kPer <= e) q[i] = 0u;
+      else if (kPer == 2 && 2 * i < e) q[i] &= 0xffff0000u;
+    }
+    v = make_uint4(q[0], q[1], q[2], q[3]);
+  }
   // element i * VEC of a row
   __device__ __forceinline__ void load(const T* row, int i) {
     if constexpr (kVec) v = __ldcs(reinterpret_cast<const uint4*>(row) + i);

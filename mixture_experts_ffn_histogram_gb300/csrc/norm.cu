@@ -10,7 +10,19 @@
 // (or in the thread's own shared-memory slots) between its statistics and its
 // output, and written once.  The variance is taken in a second pass over the
 // registers, sum (r - mean)^2, which costs no memory and loses nothing to an
-// offset of the row.
+// offset of the row.  32768 x 2816 bf16 with a residual (738 MB each way) takes
+// 110 us forward and 117 us backward, 0.99 and 0.93 of a copy's rate; a few
+// rows are bound by the launch and two sums' latency (1 x 7168: 2.9 us).
+//
+// Rows of whole, aligned 16-byte vectors move in such vectors.  Rows that
+// start inside a 16-byte unit, or end inside one (odd widths), do so too where
+// all arrays of the call lie alike (SHIFT): every 8th row (fp32: every 4th)
+// starts at the same place of its unit, so a block that walks rows by a
+// multiple of 8 keeps its threads' vectors at fixed columns, shifted by that
+// place, and only a row's first and last vector need care.  Rows that lie
+// unlike each other move element by element, which takes two to three times
+// as long (32768 x 1407 bf16: 138 us forward and 256 backward, against 86
+// and 84).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -148,6 +160,178 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormArgs<T>
   }
 }
 
+// ------------------------------------------------------------ shifted rows
+// Vector c of a row that starts `e` elements into its first 16-byte unit: its
+// elements [lo, hi) are the row's.
+template <int VEC>
+struct Edge {
+  int lo, hi;
+  __device__ __forceinline__ Edge(int c, int e, int D) : lo(c == 0 ? e : 0), hi(min(VEC, e + D - c * VEC)) {}
+  __device__ __forceinline__ bool whole() const { return lo == 0 && hi == VEC; }
+};
+template <typename T>
+__device__ __forceinline__ int unit_offset(const T* row) {  // in elements
+  return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u) / static_cast<int>(sizeof(T));
+}
+// The vector's 16-byte unit up to the row's end, zeros behind.  Ahead of the
+// row's start it reads the rest of the unit, which is the same allocation's
+// (allocations start at such units), whatever it holds.
+template <typename T, int VEC>
+__device__ __forceinline__ void copy_unit(void* slot, const T* unit, const Edge<VEC>& g) {
+  cp_async16_zfill(slot, unit, g.hi * static_cast<int>(sizeof(T)));
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_part(const float (&f)[VEC], T* unit, const Edge<VEC>& g) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    if (j >= g.lo && j < g.hi) unit[j] = from_f32<T>(f[j]);
+}
+template <typename W, int VEC>
+__device__ __forceinline__ void load_shifted_weights(const W* w, int c, int e, int D, float (&f)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    const int col = c * VEC + j - e;
+    f[j] = col >= 0 && col < D ? to_f32<W>(__ldg(w + col)) : 0.0f;
+  }
+}
+
+// The forward of shifted rows: as norm_fwd_kernel, but a group of threads
+// walks rows, whose copies come `steps` - 1 ahead into the threads' own slots
+// (as in the backward below), and keeps the weights of its columns.
+template <typename T, typename W, int VEC, int NV, bool ONE_WARP>
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_shift_kernel(const NormArgs<T> p, const int steps) {
+  using Q = Raw<T, VEC>;
+  __shared__ float red[2][32][1];
+  extern __shared__ __align__(16) unsigned char stage_mem[];
+  const int tpr = ONE_WARP ? 32 : blockDim.x;
+  const int t = ONE_WARP ? (threadIdx.x & 31) : threadIdx.x;
+  const int groups = ONE_WARP ? (blockDim.x >> 5) : 1;
+  const int nwarps = blockDim.x >> 5, bd = blockDim.x;
+  const bool has_res = p.res != nullptr;
+  const int stage_slots = (has_res ? 2 : 1) * NV * bd;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + (ONE_WARP ? (threadIdx.x >> 5) : 0);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const int n = first < p.rows ? static_cast<int>((p.rows - 1 - first) / step) + 1 : 0;
+  const int e = unit_offset(p.x + first * p.ldx), nvec = (e + p.D + VEC - 1) / VEC;
+  typename Q::Store* const slots = reinterpret_cast<typename Q::Store*>(stage_mem) + threadIdx.x;
+  const T* x_at = p.x + first * p.ldx - e;
+  const T* s_at = has_res ? p.res + first * p.ldres - e : nullptr;
+  T* y_at = p.y + first * p.ldy - e;
+  T* r_at = has_res ? p.r + first * p.ldr - e : nullptr;
+  int fetched = 0;
+  auto fetch = [&](int stage) {
+    if (fetched < n) {
+      typename Q::Store* to = slots + stage * stage_slots;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = i * tpr + t;
+        if (c < nvec) {
+          const Edge<VEC> g(c, e, p.D);
+          copy_unit(to + i * bd, x_at + c * VEC, g);
+          if (has_res) copy_unit(to + (NV + i) * bd, s_at + c * VEC, g);
+        }
+      }
+      x_at += step * p.ldx;
+      if (has_res) s_at += step * p.ldres;
+    }
+    ++fetched;
+    cp_async_commit();
+  };
+  for (int q = 0; q < steps - 1; ++q) fetch(q);
+  float gm[NV][VEC], bt[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    load_shifted_weights(static_cast<const W*>(p.gamma), i * tpr + t, e, p.D, gm[i]);
+    load_shifted_weights(static_cast<const W*>(p.beta), i * tpr + t, e, p.D, bt[i]);
+  }
+  int stage = 0;
+  for (int k = 0; k < n; ++k) {
+    fetch(stage == 0 ? steps - 1 : stage - 1);
+    if (steps == 3) cp_async_wait_group<2>();
+    else cp_async_wait_group<1>();
+    const typename Q::Store* from = slots + stage * stage_slots;
+    float f[NV][VEC], sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * tpr + t;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) f[i][j] = 0.0f;
+      if (c < nvec) {
+        const Edge<VEC> g(c, e, p.D);
+        Q a;
+        a.v = from[i * bd];
+        a.unpack(f[i]);
+        if (has_res) {
+          float h[VEC];
+          a.v = from[(NV + i) * bd];
+          a.unpack(h);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) f[i][j] += h[j];
+          if (g.whole()) {
+            a.pack(f[i]);
+            a.store(r_at + c * VEC, 0);
+            a.unpack(f[i]);  // the stored row is what is normalised
+          } else {
+            store_part<T, VEC>(f[i], r_at + c * VEC, g);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) f[i][j] = to_f32<T>(from_f32<T>(f[i][j]));
+          }
+        }
+        if (!g.whole()) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j)
+            if (j < g.lo || j >= g.hi) f[i][j] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sum[0] += f[i][j];
+      }
+    }
+    row_sums<ONE_WARP, 1>(sum, red[0], nwarps);
+    const float mean = sum[0] * p.inv_d;
+    float sq[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * tpr + t;
+      if (c < nvec) {
+        const Edge<VEC> g(c, e, p.D);
+        if (!g.whole()) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j)
+            if (j < g.lo || j >= g.hi) f[i][j] = mean;
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sq[0] += (f[i][j] - mean) * (f[i][j] - mean);
+      }
+    }
+    row_sums<ONE_WARP, 1>(sq, red[1], nwarps);
+    const float rstd = 1.0f / sqrtf(sq[0] * p.inv_d + p.eps);
+    if (t == 0 && p.mean != nullptr) {
+      p.mean[first + k * step] = mean;
+      p.rstd[first + k * step] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * tpr + t;
+      if (c < nvec) {
+        const Edge<VEC> g(c, e, p.D);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f[i][j] = (f[i][j] - mean) * rstd * gm[i][j] + bt[i][j];
+        if (g.whole()) {
+          Q a;
+          a.pack(f[i]);
+          a.store(y_at + c * VEC, 0);
+        } else {
+          store_part<T, VEC>(f[i], y_at + c * VEC, g);
+        }
+      }
+    }
+    y_at += step * p.ldy;
+    if (has_res) r_at += step * p.ldr;
+    if (++stage == steps) stage = 0;
+  }
+  cp_async_wait_all();
+}
+
 // ---------------------------------------------------------------- backward
 // A block takes R rows at a time (R = 2 where they fit) so that their two sums
 // each share one pass through the warps and one barrier: with one row at a
@@ -213,11 +397,11 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float (*red)[4], int n
 
 // Slots of a thread; slot u of all threads lies together, so that a warp's
 // copy fills whole lines (with each thread's slots together instead, the same
-// copies took 192 us where these take 130).
+// copies took 192 us where these took 130).
 template <int NV, bool RES, int R>
 __host__ __device__ constexpr int bwd_slots(int steps) { return steps * R * (RES ? 3 : 2) * NV; }
 
-template <typename T, typename W, int VEC, int NV, bool ONE_WARP, bool RES, int R>
+template <typename T, typename W, int VEC, int NV, bool ONE_WARP, bool RES, int R, bool SHIFT>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs<T> p, const int steps) {
   using Q = Raw<T, VEC>;
   using N = Nums<VEC>;
@@ -236,10 +420,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
   const int first = blockIdx.x * groups + group, step = gridDim.x * groups;
   const int n = first < p.rows ? static_cast<int>((p.rows - 1 - first) / step) + 1 : 0;
   const int64_t sx = step * p.ldx, sr = step * p.ldr, ss = step * p.ldres, sy = step * p.ldy;
-  const T* dy_at = p.x + first * p.ldx + t * VEC;  // of the next row to fetch
-  const T* r_at = p.rin + first * p.ldr + t * VEC;
-  const T* s_at = RES ? p.res + first * p.ldres + t * VEC : nullptr;
-  T* y_at = p.y + first * p.ldy + t * VEC;
+  const int e = SHIFT ? unit_offset(p.x + first * p.ldx) : 0;
+  const int nvec = SHIFT ? (e + p.D + VEC - 1) / VEC : p.nvec;
+  const T* dy_at = p.x + first * p.ldx - e + t * VEC;  // of the next row to fetch
+  const T* r_at = p.rin + first * p.ldr - e + t * VEC;
+  const T* s_at = RES ? p.res + first * p.ldres - e + t * VEC : nullptr;
+  T* y_at = p.y + first * p.ldy - e + t * VEC;
   int fetched = 0;
   auto fetch = [&](int stage) {
     typename Q::Store* to = slots + stage * kPerStep * bd;
@@ -248,10 +434,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
       if (fetched + r < n) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          if (i * tpr + t < p.nvec) {
-            copy_async<T, VEC>(to + ((r * kArr + 0) * NV + i) * bd, dy_at + i * tpr * VEC);
-            copy_async<T, VEC>(to + ((r * kArr + 1) * NV + i) * bd, r_at + i * tpr * VEC);
-            if constexpr (RES) copy_async<T, VEC>(to + ((r * kArr + 2) * NV + i) * bd, s_at + i * tpr * VEC);
+          if (i * tpr + t < nvec) {
+            const auto copy = [&](int q, const T* at) {
+              auto* slot = to + ((r * kArr + q) * NV + i) * bd;
+              if constexpr (SHIFT) copy_unit(slot, at, Edge<VEC>(i * tpr + t, e, p.D));
+              else copy_async<T, VEC>(slot, at);
+            };
+            copy(0, dy_at + i * tpr * VEC);
+            copy(1, r_at + i * tpr * VEC);
+            if constexpr (RES) copy(2, s_at + i * tpr * VEC);
           }
         }
       }
@@ -271,7 +462,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
     float w[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) w[j] = 0.0f;
-    if (i * tpr + t < p.nvec) load_weights<W, VEC>(gamma, i * tpr + t, w);
+    if constexpr (SHIFT) load_shifted_weights(gamma, i * tpr + t, e, p.D, w);
+    else if (i * tpr + t < nvec) load_weights<W, VEC>(gamma, i * tpr + t, w);
     N::gather(w, g[i]);
 #pragma unroll
     for (int j = 0; j < kN; ++j) dg[i][j] = db[i][j] = N::splat(0.0f);
@@ -315,8 +507,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
       if (r == 0 || k + r < n) {  // past the last row the slots hold nothing
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          if (i * tpr + t < p.nvec) {
+          if (i * tpr + t < nvec) {
             float f[VEC];
+            if constexpr (SHIFT) {  // ahead of the row's start the unit may hold anything
+              if (i == 0 && t == 0 && e > 0) {
+                raw[r][0][i].clear_below(e);
+                raw[r][1][i].clear_below(e);
+              }
+            }
             raw[r][0][i].unpack(f);
             N::gather(f, a[r][i]);
             raw[r][1][i].unpack(f);
@@ -347,7 +545,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
                 c2 = N::splat(-rstd[r] * (sums[2 * r + 1] * p.inv_d));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          if (i * tpr + t < p.nvec) {
+          if (i * tpr + t < nvec) {
             Q u;
             float f[VEC];
             F d[kN];
@@ -361,6 +559,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
               for (int j = 0; j < kN; ++j) d[j] = fadd(d[j], e[j]);
             }
             N::scatter(d, f);
+            if constexpr (SHIFT) {
+              const Edge<VEC> part(i * tpr + t, e, p.D);
+              if (!part.whole()) {
+                store_part<T, VEC>(f, y_at + i * tpr * VEC, part);
+                continue;
+              }
+            }
             u.pack(f);
             u.store(y_at + i * tpr * VEC, 0);
           }
@@ -395,6 +600,28 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
     // join the warps' sums in shared memory, in the warps' order
     float* acc = reinterpret_cast<float*>(stage_mem);  // [groups][2][NV * VEC][32]
     __syncthreads();
+    if constexpr (SHIFT) {  // the warps' columns differ: [groups][2][column]
+      constexpr int kRow = NV * VEC * 32;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const int col = (i * 32 + t) * VEC + j - e;
+          if (col < 0 || col >= p.D) continue;
+          acc[group * 2 * kRow + col] = fg[i][j];
+          acc[(group * 2 + 1) * kRow + col] = fb[i][j];
+        }
+      __syncthreads();
+      for (int col = threadIdx.x; col < p.D; col += blockDim.x) {
+        float sg = 0.0f, sb = 0.0f;
+        for (int gq = 0; gq < groups; ++gq) {
+          sg += acc[gq * 2 * kRow + col];
+          sb += acc[(gq * 2 + 1) * kRow + col];
+        }
+        put(col, sg, sb);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -409,19 +636,44 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
         sg += acc[gq * 2 * NV * VEC * 32 + k];
         sb += acc[(gq * 2 + 1) * NV * VEC * 32 + k];
       }
-      const int e = k / 32, c = (e / VEC) * 32 + (k & 31);
-      if (c < p.nvec) put(c * VEC + e % VEC, sg, sb);
+      const int el = k / 32, c = (el / VEC) * 32 + (k & 31);
+      if (c < nvec) put(c * VEC + el % VEC, sg, sb);
     }
+  } else if constexpr (SHIFT) {
+    // by way of shared memory (2 D floats: no more than the slots, which hold
+    // two steps of two rows' vectors or more), so that neighbouring threads
+    // write neighbouring columns
+    float* acc = reinterpret_cast<float*>(stage_mem);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const int col = (i * tpr + t) * VEC + j - e;
+        if (col < 0 || col >= p.D) continue;
+        acc[col] = fg[i][j];
+        acc[p.D + col] = fb[i][j];
+      }
+    __syncthreads();
+    for (int k = t; k < 2 * p.D; k += tpr) part[k] = acc[k];
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * tpr + t;
-      if (c < p.nvec) {
+      if (c >= nvec) break;
+      if constexpr (VEC > 1) {
+        if (dgamma == nullptr) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          put(c * VEC + j, fg[i][j], fb[i][j]);
+          for (int j = 0; j < VEC; j += 4) {
+            float* at = part + c * VEC + j;
+            *reinterpret_cast<float4*>(at) = make_float4(fg[i][j], fg[i][j + 1], fg[i][j + 2], fg[i][j + 3]);
+            *reinterpret_cast<float4*>(at + p.D) = make_float4(fb[i][j], fb[i][j + 1], fb[i][j + 2], fb[i][j + 3]);
+          }
+          continue;
         }
       }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) put(c * VEC + j, fg[i][j], fb[i][j]);
     }
   }
 }
@@ -491,6 +743,31 @@ bool vector_rows(const NormCall& c, size_t elem) {
          ok(c.r, c.ldr) && ok(c.r_in, c.ldr) && ok(c.y, c.ldy) && ok(c.gamma, 0) && ok(c.beta, 0);
 }
 
+// Whether the arrays' rows lie alike within their 16-byte units, and the most
+// vectors that such a row touches.
+bool alike_rows(const NormCall& c, size_t elem) {
+  const auto place = [&](const void* p, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) | ((static_cast<uint64_t>(ld) * elem & 15u) << 4);
+  };
+  const auto ok = [&](const void* p, int64_t ld) { return p == nullptr || place(p, ld) == place(c.x, c.ldx); };
+  return ok(c.res, c.ldres) && ok(c.r, c.ldr) && ok(c.r_in, c.ldr) && ok(c.y, c.ldy);
+}
+int shifted_vectors(int D, int vec) { return (D + 2 * vec - 2) / vec; }
+
+// A number of blocks whose groups walk rows by a multiple of `period` (the
+// rows after which a shifted row's place repeats), if they walk at all.
+int64_t walk_blocks(int64_t blocks, int groups, int64_t rows, int period) {
+  if (blocks * groups >= rows) return blocks;
+  const int64_t unit = std::max(1, period / groups);
+  return std::max(unit, blocks / unit * unit);
+}
+
+// Blocks that an SM holds: a warp's registers (in units of 8 per thread) lie
+// in one of its four partitions of 512 per lane, 16 warps' places each.
+int resident_blocks(int threads, int regs) {
+  return std::max(1, std::min(64, 4 * (512 / ((regs + 7) / 8 * 8))) / (threads / 32));
+}
+
 template <typename T, typename W, int VEC, int NV>
 cudaError_t fwd_nv(const NormCall& c, cudaStream_t s) {
   const NormArgs<T> a = make_args<T>(c, VEC);
@@ -532,12 +809,7 @@ cudaError_t fwd_vec(const NormCall& c, cudaStream_t s) {
   const int want = many ? std::min(4, (nvec + 31) / 32) : 1;
   return pick_nv<VEC, 4>(nvec, want, [&](auto n) { return fwd_nv<T, W, VEC, decltype(n)::value>(c, s); });
 }
-template <typename T, typename W>
-cudaError_t fwd_type(const NormCall& c, cudaStream_t s) {
-  return vector_rows(c, sizeof(T)) ? fwd_vec<T, W, 16 / sizeof(T)>(c, s) : fwd_vec<T, W, 1>(c, s);
-}
-
-// What the launch of a backward needs to know of its kernel, looked up once
+// What the launch of a walking kernel needs to know of it, looked up once
 // per device: a captured launch then makes no such call.
 struct KernelLimits {
   std::atomic<int> regs[64];  // 0: not looked up
@@ -563,26 +835,78 @@ cudaError_t kernel_regs(K kern, KernelLimits& lim, int* regs) {
   return cudaSuccess;
 }
 
-template <typename T, typename W, int VEC, int NV, bool ONE_WARP, bool RES, int R>
+template <typename T, typename W, int VEC, int NV, bool ONE_WARP>
+cudaError_t fwd_shift_launch(const NormCall& c, cudaStream_t s) {
+  const int groups = ONE_WARP ? kRowsPerBlock : 1;
+  const int threads = ONE_WARP ? 32 * groups : round32((shifted_vectors(c.D, VEC) + NV - 1) / NV);
+  auto kern = norm_fwd_shift_kernel<T, W, VEC, NV, ONE_WARP>;
+  static KernelLimits limits;
+  int regs = 0;
+  const cudaError_t err = kernel_regs(kern, limits, &regs);
+  if (err != cudaSuccess) return err;
+  int per_sm = resident_blocks(threads, regs);
+  const size_t stage = static_cast<size_t>(c.res != nullptr ? 2 : 1) * NV * threads * 16;
+  const int steps = (3 * stage + 2048) * per_sm <= kMaxDynamicSmem ? 3 : 2;
+  const size_t bytes = steps * stage;
+  per_sm = std::min(per_sm, static_cast<int>(228 * 1024 / (bytes + 2048)));
+  const int64_t blocks = walk_blocks(
+      std::min<int64_t>(static_cast<int64_t>(sm_count()) * per_sm, (c.rows + groups - 1) / groups),
+      groups, c.rows, VEC);
+  kern<<<static_cast<unsigned>(blocks), threads, bytes, s>>>(make_args<T>(c, VEC), steps);
+  return cudaGetLastError();
+}
+template <typename T, typename W, int VEC>
+cudaError_t fwd_shift(const NormCall& c, cudaStream_t s) {
+  const int nvec = shifted_vectors(c.D, VEC);
+  return pick_nv<VEC, 1>(nvec, 1, [&](auto n) {
+    constexpr int NV = decltype(n)::value;
+    if constexpr (NV == 1)
+      if (nvec <= 32 * NV) return fwd_shift_launch<T, W, VEC, NV, true>(c, s);
+    return fwd_shift_launch<T, W, VEC, NV, false>(c, s);
+  });
+}
+
+enum class Rows { kVectors, kShifted, kElements };
+template <typename T>
+Rows kind_of_rows(const NormCall& c) {
+  constexpr int VEC = 16 / sizeof(T);
+  if (vector_rows(c, sizeof(T))) return Rows::kVectors;
+  // narrow rows and few of them are left to single elements: 32768 x 63 bf16
+  // takes 8 us so forward (19 shifted) and 13 backward (15), 1000 x 1001
+  // backward 8.8 (12.4); 20000 x 201 takes 16.4 and 25 (13.4 and 14)
+  const bool worth = c.D > 128 && c.rows >= 16 * static_cast<int64_t>(sm_count());
+  return worth && alike_rows(c, sizeof(T)) && shifted_vectors(c.D, VEC) <= kMaxD / VEC ? Rows::kShifted
+                                                                                      : Rows::kElements;
+}
+
+template <typename T, typename W>
+cudaError_t fwd_type(const NormCall& c, cudaStream_t s) {
+  constexpr int VEC = 16 / sizeof(T);
+  switch (kind_of_rows<T>(c)) {
+    case Rows::kVectors: return fwd_vec<T, W, VEC>(c, s);
+    case Rows::kShifted: return fwd_shift<T, W, VEC>(c, s);
+    default: return fwd_vec<T, W, 1>(c, s);
+  }
+}
+
+template <typename T, typename W, int VEC, int NV, bool ONE_WARP, bool RES, int R, bool SHIFT>
 cudaError_t bwd_launch(const NormCall& c, cudaStream_t s) {
   NormArgs<T> a = make_args<T>(c, VEC);
-  const int threads = ONE_WARP ? 32 * kBwdGroups : round32((a.nvec + NV - 1) / NV);
+  const int nvec = SHIFT ? shifted_vectors(c.D, VEC) : a.nvec;
+  const int threads = ONE_WARP ? 32 * kBwdGroups : round32((nvec + NV - 1) / NV);
   const int groups = ONE_WARP ? kBwdGroups : 1;
-  auto kern = norm_bwd_kernel<T, W, VEC, NV, ONE_WARP, RES, R>;
+  auto kern = norm_bwd_kernel<T, W, VEC, NV, ONE_WARP, RES, R, SHIFT>;
   static KernelLimits limits;
   int regs = 0;
   cudaError_t err = kernel_regs(kern, limits, &regs);
   if (err != cudaSuccess) return err;
-  // blocks that an SM holds: a warp's registers (in units of 8 per thread) lie
-  // in one of its four partitions of 512 per lane, 16 warps' places each; two
-  // steps ahead where shared memory (1 KB more per block is the system's)
-  // keeps that number, else one
-  const int warps = threads / 32;
-  int per_sm = std::min(64, 4 * (512 / ((regs + 7) / 8 * 8))) / warps;
+  // two steps ahead where shared memory (1 KB more per block is the system's)
+  // keeps the number of blocks that an SM holds, else one
+  int per_sm = resident_blocks(threads, regs);
   const auto slot_bytes = [&](int steps) {
     return static_cast<size_t>(bwd_slots<NV, RES, R>(steps)) * threads * sizeof(T) * VEC;
   };
-  const int steps = (slot_bytes(3) + 2048) * std::max(per_sm, 1) <= kMaxDynamicSmem ? 3 : 2;
+  const int steps = (slot_bytes(3) + 2048) * per_sm <= kMaxDynamicSmem ? 3 : 2;
   size_t bytes = slot_bytes(steps);
   if (ONE_WARP) bytes = std::max(bytes, static_cast<size_t>(groups) * 2 * NV * VEC * 32 * 4);
   per_sm = std::min(per_sm, static_cast<int>(228 * 1024 / (bytes + 2048)));
@@ -590,6 +914,7 @@ cudaError_t bwd_launch(const NormCall& c, cudaStream_t s) {
   blocks = std::min({blocks, (c.rows + groups * R - 1) / (groups * R), kPartialRows});
   // few rows: one block, which needs no second launch
   if (c.rows <= kOneBlockRows) blocks = 1;
+  if (SHIFT) blocks = walk_blocks(blocks, groups, c.rows, VEC);
   if (blocks == 1) {
     a.partials = nullptr;
     a.dgamma = c.dgamma;
@@ -602,30 +927,34 @@ cudaError_t bwd_launch(const NormCall& c, cudaStream_t s) {
                               c.D, c.dgamma, c.dbeta, c.wtype, s);
 }
 
-template <typename T, typename W, int VEC, int NV, bool ONE_WARP, int R>
+template <typename T, typename W, int VEC, int NV, bool ONE_WARP, int R, bool SHIFT>
 cudaError_t bwd_res(const NormCall& c, cudaStream_t s) {
-  return c.res != nullptr ? bwd_launch<T, W, VEC, NV, ONE_WARP, true, R>(c, s)
-                          : bwd_launch<T, W, VEC, NV, ONE_WARP, false, R>(c, s);
+  return c.res != nullptr ? bwd_launch<T, W, VEC, NV, ONE_WARP, true, R, SHIFT>(c, s)
+                          : bwd_launch<T, W, VEC, NV, ONE_WARP, false, R, SHIFT>(c, s);
 }
 
 // Two rows at a time where a thread holds up to eight columns; with sixteen
 // (the widest rows) two would not fit its registers.
-template <typename T, typename W, int VEC, int NV>
-cudaError_t bwd_nv(const NormCall& c, cudaStream_t s) {
-  constexpr int R = NV * VEC <= 8 ? 2 : 1;
-  if constexpr (NV == (VEC == 1 ? 4 : 1)) {  // more vectors per thread are only taken by wide rows
-    if (c.D / VEC <= 32 * NV) return bwd_res<T, W, VEC, NV, true, R>(c, s);
-  }
-  return bwd_res<T, W, VEC, NV, false, R>(c, s);
-}
-
-template <typename T, typename W, int VEC>
+template <typename T, typename W, int VEC, bool SHIFT>
 cudaError_t bwd_vec(const NormCall& c, cudaStream_t s) {
-  return pick_nv<VEC, 1>(c.D / VEC, 1, [&](auto n) { return bwd_nv<T, W, VEC, decltype(n)::value>(c, s); });
+  const int nvec = SHIFT ? shifted_vectors(c.D, VEC) : c.D / VEC;
+  return pick_nv<VEC, 1>(nvec, 1, [&](auto n) {
+    constexpr int NV = decltype(n)::value;
+    constexpr int R = NV * VEC <= 8 ? 2 : 1;
+    if constexpr (NV == (VEC == 1 ? 4 : 1)) {  // more vectors per thread are only taken by wide rows
+      if (nvec <= 32 * NV) return bwd_res<T, W, VEC, NV, true, R, SHIFT>(c, s);
+    }
+    return bwd_res<T, W, VEC, NV, false, R, SHIFT>(c, s);
+  });
 }
 template <typename T, typename W>
 cudaError_t bwd_type(const NormCall& c, cudaStream_t s) {
-  return vector_rows(c, sizeof(T)) ? bwd_vec<T, W, 16 / sizeof(T)>(c, s) : bwd_vec<T, W, 1>(c, s);
+  constexpr int VEC = 16 / sizeof(T);
+  switch (kind_of_rows<T>(c)) {
+    case Rows::kVectors: return bwd_vec<T, W, VEC, false>(c, s);
+    case Rows::kShifted: return bwd_vec<T, W, VEC, true>(c, s);
+    default: return bwd_vec<T, W, 1, false>(c, s);
+  }
 }
 
 template <template <typename, typename> class F>

@@ -177,3 +177,128 @@ def test_reproducible_other_stream_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+# many rows (each block walks several, some past 32) whose arrays start at
+# offsets of their own within a 16-byte unit; rows, D, type, weights' type,
+# residual, offsets and row strides' padding of x, res, dy, dres
+MANY = [
+    (40000, 21, BF, F32, True, (0, 1, 2, 3), (0, 3, 1, 0)),
+    (6000, 125, F32, F32, True, (1, 0, 3, 2), (0, 1, 0, 2)),
+    (13000, 333, HF, HF, True, (0, 7, 5, 3), (0, 0, 1, 3)),
+    (7000, 1001, BF, BF, False, (5, 0, 2, 0), (0, 0, 7, 0)),
+    (1300, 2047, F32, F32, True, (3, 3, 3, 3), (1, 1, 1, 1)),
+    (900, 4095, BF, F32, True, (1, 2, 3, 4), (0, 1, 2, 3)),
+    (12000, 264, BF, F32, True, (0, 0, 0, 0), (0, 0, 0, 0)),
+    # alike: odd widths, one after the other
+    (9000, 129, BF, F32, True, (0, 0, 0, 0), (0, 0, 0, 0)),
+    (13000, 251, F32, F32, True, (0, 0, 0, 0), (0, 0, 0, 0)),
+    (3000, 333, HF, HF, False, (0, 0, 0, 0), (0, 0, 0, 0)),
+    (2750, 1001, BF, BF, True, (0, 0, 0, 0), (0, 0, 0, 0)),
+    (5200, 1406, F32, F32, False, (0, 0, 0, 0), (0, 0, 0, 0)),
+    (2500, 4097, BF, F32, True, (0, 0, 0, 0), (0, 0, 0, 0)),
+    (2500, 8177, HF, F32, True, (0, 0, 0, 0), (0, 0, 0, 0)),
+    (2437, 8185, F32, F32, True, (0, 0, 0, 0), (0, 0, 0, 0)),
+    (2500, 8191, BF, BF, True, (0, 0, 0, 0), (0, 0, 0, 0)),
+    (6000, 1408, HF, F32, False, (0, 0, 0, 0), (8, 8, 8, 8)),
+]
+
+
+@pytest.mark.parametrize("rows,D,dt,wt,res,offs,pads", MANY)
+def test_many_rows_at_any_offset(rows, D, dt, wt, res, offs, pads):
+    need_gpu()
+    from mixture_experts_ffn_histogram_gb300.layer import LayerNorm
+    g = torch.Generator(device="cuda").manual_seed(rows + D)
+
+    def mat(i):
+        ld = D + pads[i]
+        flat = torch.randn(offs[i] + rows * ld, generator=g, device="cuda").to(dt)
+        return flat[offs[i]:].view(rows, ld)[:, :D]
+
+    x, s, dy, dres = (mat(i) for i in range(4))
+    gamma = (1 + 0.3 * torch.randn(D, generator=g, device="cuda")).to(wt)
+    beta = (0.3 * torch.randn(D, generator=g, device="cuda")).to(wt)
+    op = LayerNorm(rows, D, dt, wt, EPS)
+    y = op.forward(x, gamma, beta, res=s if res else None)
+    r = (x.float() + s.float()).to(dt) if res else x
+    if res:
+        assert torch.equal(op.r, r)
+    yr, mean, rstd, mag = norm_fwd(r, gamma, beta, EPS)
+    assert_within("y", y, yr, 64 * U32 * mag)
+    dx = op.backward(dy, r, gamma, dres=dres if res else None)
+    want, mags = norm_bwd(dy, r, gamma, op.mean, op.rstd, dres if res else None)
+    assert_within("dx", dx, want[0], 64 * U32 * mags[0])
+    # a thread's sum over its rows (152 blocks at least), then at most 160 terms
+    assert_within("dgamma", op.dgamma, want[1], (160 + rows / 152) * U32 * mags[1])
+    assert_within("dbeta", op.dbeta, want[2], (160 + rows / 152) * U32 * mags[2])
+
+
+def test_neighbours_of_ragged_rows_stay():
+    """Rows inside a wider matrix: what lies between them is not written."""
+    need_gpu()
+    from mixture_experts_ffn_histogram_gb300 import binding as B
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for dt in (BF, F32):
+        wide = torch.randn(60, 45, generator=g, device="cuda").to(dt)
+        x = wide[:, 3:40]
+        y = torch.full((60, 51), 7.0, dtype=dt, device="cuda")
+        r = torch.full((60, 47), 9.0, dtype=dt, device="cuda")
+        w = torch.ones(37, device="cuda")
+        b = torch.zeros(37, device="cuda")
+        B.moe_layer_norm(x, x, w, b, r[:, 1:38], y[:, 5:42], None, None, EPS)
+        assert torch.equal(r[:, 1:38], (2 * x.float()).to(dt))
+        assert bool((r[:, :1] == 9).all()) and bool((r[:, 38:] == 9).all())
+        assert bool((y[:, :5] == 7).all()) and bool((y[:, 42:] == 7).all())
+        assert bool((y[:, 5:42] != 7).all())
+        st = torch.rand(2, 60, device="cuda")
+        dx = torch.full((60, 41), 3.0, dtype=dt, device="cuda")
+        B.moe_layer_norm_bwd(x, x, w, st[0], st[1], x, dx[:, 2:39], None, None, None)
+        assert bool((dx[:, :2] == 3).all()) and bool((dx[:, 39:] == 3).all())
+
+
+@pytest.mark.parametrize("dt,D,off,pad", [(BF, 333, 0, 0), (BF, 264, 3, 5), (F32, 1001, 1, 2), (HF, 150, 7, 0)])
+def test_shifted_rows_and_their_neighbours(dt, D, off, pad):
+    """All arrays with the same odd offset and stride: what lies between the
+    rows is not written, and neither it nor a bad row reaches another row."""
+    need_gpu()
+    from mixture_experts_ffn_histogram_gb300 import binding as B
+    rows, ld = 2600, D + pad
+    g = torch.Generator(device="cuda").manual_seed(D)
+
+    def mat(fill):
+        flat = torch.full((off + rows * ld + 8,), fill, dtype=dt, device="cuda")
+        return flat, flat[off:off + rows * ld].view(rows, ld)[:, :D]
+
+    bad = {100: (0, float("nan")), 200: (D - 1, float("nan")), 300: (D - 1, float("inf"))}
+    (_, x), (_, s), (_, dy), (_, dres) = (mat(float("nan")) for _ in range(4))
+    for m in (x, s, dy, dres):
+        m.copy_(torch.randn(rows, D, generator=g, device="cuda"))
+    w, b = torch.rand(D, generator=g, device="cuda"), torch.rand(D, generator=g, device="cuda")
+    (yf, y), (rf, r), (df, dx) = (mat(7.0) for _ in range(3))
+    clean = x.clone()
+    for row, (col, v) in bad.items():
+        x[row, col] = v
+    st = torch.empty(2, rows, device="cuda")
+    B.moe_layer_norm(x, s, w, b, r, y, st[0], st[1], EPS)
+    assert (~torch.isfinite(y.float())).any(1).nonzero().flatten().tolist() == sorted(bad)
+    x.copy_(clean)
+    B.moe_layer_norm(x, s, w, b, r, y, st[0], st[1], EPS)
+    want = (x.float() + s.float()).to(dt)
+    assert torch.equal(r, want)
+    yr, mean, rstd, mag = norm_fwd(want, w, b, EPS)
+    assert_within("y", y, yr, 64 * U32 * mag)
+    ws = torch.empty(B.moe_layer_norm_workspace_bytes(rows, D), dtype=torch.uint8, device="cuda")
+    dg, db = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    B.moe_layer_norm_bwd(dy, r, w, st[0], st[1], dres, dx, dg, db, ws)
+    ref, mags = norm_bwd(dy, r, w, st[0], st[1], dres)
+    assert_within("dx", dx, ref[0], 64 * U32 * mags[0])
+    assert_within("dgamma", dg, ref[1], (160 + rows / 152) * U32 * mags[1])
+    assert_within("dbeta", db, ref[2], (160 + rows / 152) * U32 * mags[2])
+    for flat in (yf, rf, df):  # only the rows were written
+        keep = torch.ones_like(flat, dtype=torch.bool)
+        keep[off:off + rows * ld].view(rows, ld)[:, :D] = False
+        assert bool((flat[keep] == 7).all())
+    dy[400, D - 1] = float("nan")
+    B.moe_layer_norm_bwd(dy, r, w, st[0], st[1], dres, dx, dg, db, ws)
+    assert (~torch.isfinite(dx.float())).any(1).nonzero().flatten().tolist() == [400]
+    assert (~torch.isfinite(dg)).nonzero().flatten().tolist() == [D - 1]
