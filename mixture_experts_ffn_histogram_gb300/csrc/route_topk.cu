@@ -142,13 +142,15 @@ __device__ __noinline__ uint32_t groups_fp64(const float* row, const float* bias
 }
 
 // Rank in fp64 of this lane's expert `id` (logit l) among those of lanes < n,
-// which hold them in any order; ties go to the lowest id.
+// which hold them in any order; ties go to the lowest id, masked ones last.
 template <bool SOFTMAX>
 __device__ __noinline__ int rank_fp64(const float* row, const float* bias, int E, int id, float l, int n,
                                       int lane) {
   double2 st = make_double2(0.0, 0.0);
   if constexpr (SOFTMAX) st = softmax_fp64(row, E, lane);
-  const double sel = score_fp64<SOFTMAX>(l, st.x, st.y) + (lane < n ? static_cast<double>(bias[id]) : 0.0);
+  const double sel = l == kNegInf ? -INFINITY
+                                  : score_fp64<SOFTMAX>(l, st.x, st.y) +
+                                        (lane < n ? static_cast<double>(bias[id]) : 0.0);
   int rank = 0;
   for (int j = 0; j < n; ++j) {
     const double other = __shfl_sync(kAll, sel, j);
@@ -226,13 +228,15 @@ struct WarpToken {
   const TopkArgs& p;
   float2* cand;
   int vpl, lpg, lane, first, mine, group, r;
-  bool vec;
+  bool vec, few;  // few: 32 experts at most to choose from, on fewer than K lanes
 
   __device__ __forceinline__ WarpToken(const TopkArgs& p_, float2* cand_, int vpl_, int lpg_)
       : p(p_), cand(cand_), vpl(vpl_), lpg(lpg_), lane(threadIdx.x & 31) {
     // this lane's experts: `mine` of them from `first`
     const moe_topk_dims& d = p.d;
-    const int gs = d.groups > 1 && d.top_groups < d.groups ? d.E / d.groups : d.E;
+    const bool grouped = d.groups > 1 && d.top_groups < d.groups;
+    const int gs = grouped ? d.E / d.groups : d.E, staying = grouped ? d.top_groups : 1;
+    few = staying * gs <= 32 && d.K > staying * ((gs + vpl - 1) / vpl);
     group = lane / lpg;
     r = lane - group * lpg;
     first = group * gs + r * vpl;
@@ -358,11 +362,12 @@ struct WarpToken {
     }
 
     // a lower bound of the K-th value: the K-th largest of the lanes' maxima
+    // (none where those lanes are fewer: then all experts are candidates)
     float top = l[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) top = fmaxf(top, l[i]);
     float bound = kNegInf;
-    {
+    if (!few) {
       float rest = top;
       for (int k = 0; k < K; ++k) {
         bound = warp_max_f32(rest);
@@ -372,7 +377,8 @@ struct WarpToken {
     if (biased) bound -= 2.0f * (worst + kSumError * fabsf(bound));  // what may still pass it
     int count = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) count += l[i] >= bound && i < VPL ? 1 : 0;
+    for (int i = 0; i < VPL; ++i) count += l[i] >= bound && i < mine ? 1 : 0;
+    if (out) count = 0;
     // candidates before this lane's, in the order of the ids
     int at = 0, n = 0;
 #pragma unroll
@@ -382,11 +388,11 @@ struct WarpToken {
       n += __popc(have) << w;
     }
     int my_id = 0;
-    if (bound > kNegInf && n >= K && n <= 32) {
+    if ((few || bound > kNegInf) && n >= K && n <= 32) {
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (l[i] >= bound) cand[at++] = make_float2(l[i], __int_as_float(first + i));
+        if (l[i] >= bound && i < mine && !out) cand[at++] = make_float2(l[i], __int_as_float(first + i));
       __syncwarp();
       float v = kNegInf;
       int id = 0;
@@ -523,7 +529,7 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
 // instructions are not its experts' but the selection's, which a few lanes
 // share as well as thirty-two do.  A lane
 // holds up to 32 experts; the bound comes from the best of each quarter of
-// a lane's, and the candidates (up to 32) are ranked through shared memory.  A token whose
+// a lane's (every fourth expert), and the candidates (up to 32) are ranked through shared memory.  A token whose
 // candidates do not fit, and one with near ties, is finished by the whole
 // warp.  Bound by latency (96 registers leave 20 warps an SM, which issue in
 // half of the cycles).  32768 tokens, 256 experts in 8 groups: 8 taken 27 us,
@@ -541,12 +547,13 @@ __device__ __forceinline__ float sub_sum(float v) {
   return v;
 }
 
-// A token that the packed kernel leaves to the whole warp (at most 256 experts).
-template <bool SOFTMAX>
+// A token that the packed kernel leaves to the whole warp, with VPL experts to
+// a lane at most.
+template <int VPL, bool SOFTMAX>
 __device__ __noinline__ void whole_warp_token(const TopkArgs& p, float2* cand, int vpl, int lpg,
                                               int64_t t) {
-  WarpToken<8, SOFTMAX> w(p, cand, vpl, lpg);
-  float b[8], l[8];
+  WarpToken<VPL, SOFTMAX> w(p, cand, vpl, lpg);
+  float b[VPL], l[VPL];
   w.load_bias(b);
   w.load_row(t, l);
   w.run(t, l, b);
@@ -577,10 +584,13 @@ __device__ __noinline__ void settle_order(const float* row, const float* bias, i
   __syncwarp();
 }
 
+// Experts of a lane when the whole warp takes a token over.
+__host__ __device__ constexpr int packed_warp_vpl(int lanes, int vpl) { return lanes == 16 && vpl == 32 ? 16 : 8; }
+
 template <int LANES, int VPL, bool SOFTMAX>
 __global__ void __launch_bounds__(32 * kTopkWarps)
     route_topk_packed_kernel(const __grid_constant__ TopkArgs p, const int vpl, const int lpg,
-                             const int warp_vpl, const int warp_lpg) {
+                             const int warp_vpl, const int warp_lpg, const bool few) {
   constexpr int kTokens = 32 / LANES, kEach = 32 / LANES;  // tokens a warp, candidates a lane
   constexpr uint32_t kTokenMask = LANES == 32 ? kAll : (1u << LANES) - 1u;
   constexpr int kRow = VPL + 4;  // a lane's part of a row: 16-byte accesses without bank conflicts
@@ -668,9 +678,9 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
     float q4[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      q4[c] = l[c * (VPL / 4)];
+      q4[c] = l[c];
 #pragma unroll
-      for (int i = 1; i < VPL / 4; ++i) q4[c] = fmaxf(q4[c], l[c * (VPL / 4) + i]);
+      for (int i = c + 4; i < VPL; i += 4) q4[c] = fmaxf(q4[c], l[i]);
     }
     bool out = mine == 0;
     if (grouped) {
@@ -721,6 +731,7 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
       out = out || !stays;
     }
     // a lower bound of the K-th value: the K-th largest of the quarters' bests
+    // (none where there are fewer of those: then all experts are candidates)
     auto order = [&](int x, int y) {
       const float hi = fmaxf(q4[x], q4[y]);
       q4[y] = fminf(q4[x], q4[y]);
@@ -733,7 +744,7 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
     order(1, 3);
     order(1, 2);
     float bound = kNegInf;
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; k < K && !few; ++k) {
       bound = sub_max<LANES>(q4[0]);
       if (q4[0] == bound) {
         q4[0] = q4[1];
@@ -742,12 +753,13 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
         q4[3] = kNegInf;
       }
     }
-    const bool bounded = bound > kNegInf;
+    const bool bounded = few || bound > kNegInf;
     if (biased) bound -= 2.0f * (worst + kSumError * fabsf(bound));
     uint32_t mask = 0u;  // the lane's candidates
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (l[i] >= bound) mask |= 1u << i;
+    if (mine < 32) mask &= (1u << mine) - 1u;
     if (out || !bounded) mask = 0u;
     const int count = __popc(mask);
     int upto = count;
@@ -841,7 +853,7 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
     while (rest != 0) {
       const int q = (__ffs(rest) - 1) / LANES;
       rest &= rest - 1u;
-      whole_warp_token<SOFTMAX>(p, cands[warp][0], warp_vpl, warp_lpg, base + q);
+      whole_warp_token<packed_warp_vpl(LANES, VPL), SOFTMAX>(p, cands[warp][0], warp_vpl, warp_lpg, base + q);
       __syncwarp();
     }
   }
@@ -1002,7 +1014,8 @@ cudaError_t launch_route_topk(const float* logits, const float* bias, int32_t* i
   const int gs = grouped ? d.E / d.groups : d.E;
   const int vpl = (gs + lpg - 1) / lpg;
   // Several tokens a warp, where the experts, groups and slots fit LANES lanes
-  // and the lanes whose groups stay offer K values for the bound.
+  // and the lanes whose groups stay offer K values for the bound (a lane's
+  // experts in four quarters) or few enough experts to need none.
   auto packed = [&](auto lanes) -> bool {
     constexpr int LANES = decltype(lanes)::value;
     int lp = LANES;
@@ -1011,22 +1024,30 @@ cudaError_t launch_route_topk(const float* logits, const float* bias, int32_t* i
       while (lp & (lp - 1)) lp &= lp - 1;  // a power of two
     }
     const int vp = lp > 0 ? (gs + lp - 1) / lp : 33;
-    const int alive = lp * (grouped ? d.top_groups : 1);
-    if (vp > 32 || d.E > 256 || d.K > LANES || d.K > 4 * alive) return false;
+    if (vp > 32 || d.K > LANES) return false;
+    const int staying = grouped ? d.top_groups : 1;
+    int offered = 0;
+    for (int r = 0; r < lp; ++r) offered += std::max(0, std::min({4, vp, gs - r * vp}));
+    // 32 experts at most to choose from: ranking them all costs less than the
+    // bound for more than eight of them (30000 tokens, 16 of one of 4 groups of
+    // 32: 24.6 us, 28.8 with it), more for fewer (28006, 5 of 16: 12.7 and 10.6)
+    const bool few = staying * gs <= 32 && (LANES == 16 || d.K > staying * offered);
+    if (!few && d.K > staying * offered) return false;
+    if (vpl > packed_warp_vpl(LANES, vp > 16 ? 32 : 16)) return false;
     const unsigned grid = topk_grid((d.T + 32 / LANES - 1) / (32 / LANES), LANES == 8 ? 12 : 6);
     pick_vpl(vp, [&](auto n) {
-      constexpr int VPL = decltype(n)::value < 8 ? 8 : decltype(n)::value;
+      constexpr int VPL = decltype(n)::value < 4 ? 4 : decltype(n)::value;
       if (d.gate == MOE_GATE_SOFTMAX)
-        route_topk_packed_kernel<LANES, VPL, true><<<grid, 32 * kTopkWarps, 0, s>>>(a, vp, lp, vpl, lpg);
+        route_topk_packed_kernel<LANES, VPL, true><<<grid, 32 * kTopkWarps, 0, s>>>(a, vp, lp, vpl, lpg, few);
       else
-        route_topk_packed_kernel<LANES, VPL, false><<<grid, 32 * kTopkWarps, 0, s>>>(a, vp, lp, vpl, lpg);
+        route_topk_packed_kernel<LANES, VPL, false><<<grid, 32 * kTopkWarps, 0, s>>>(a, vp, lp, vpl, lpg, few);
     });
     return true;
   };
   // below this a token a warp fills the SMs better (4096 tokens: 9.7 us both
   // ways, 2048: 6.4 and 7.6)
   if (d.T >= 32 * static_cast<int64_t>(sm_count()) &&
-      (d.K <= 8 ? packed(std::integral_constant<int, 8>{}) : packed(std::integral_constant<int, 16>{})))
+      ((d.K <= 8 && packed(std::integral_constant<int, 8>{})) || packed(std::integral_constant<int, 16>{})))
     return cudaGetLastError();
   const unsigned grid = topk_grid(d.T, 12);
   pick_vpl(vpl, [&](auto n) {

@@ -81,7 +81,17 @@ MANY = [
     (5003, 256, 16, "sigmoid", True, 8, 4, 2, True, 1.0),
     (5003, 96, 11, "softmax", True, 12, 5, 2, False, 1.0),
     (5003, 130, 13, "softmax", False, 1, 1, 1, False, 1.0),
-    (5003, 512, 8, "sigmoid", True, 8, 4, 2, True, 1.0),     # too many experts for it
+    (5003, 512, 8, "sigmoid", True, 8, 4, 2, True, 1.0),
+    (5003, 512, 16, "softmax", True, 8, 3, 2, False, 1.0),
+    (5003, 384, 6, "sigmoid", True, 1, 1, 1, True, 1.0),
+    (5003, 255, 12, "sigmoid", True, 3, 2, 2, True, 1.0),
+    (5003, 96, 16, "softmax", False, 8, 2, 2, False, 1.0),   # all of the groups' experts are candidates
+    (5003, 160, 16, "sigmoid", True, 8, 2, 1, True, 1.0),
+    (5003, 16, 5, "softmax", True, 1, 1, 1, True, 1.0),
+    (5003, 32, 4, "sigmoid", True, 2, 1, 1, True, 1.0),
+    (5003, 20, 16, "sigmoid", True, 1, 1, 1, False, 1.0),
+    (1003, 20, 7, "sigmoid", True, 1, 1, 1, False, 1.0),
+    (1003, 64, 9, "softmax", True, 8, 3, 2, True, 1.0),
 ]
 
 
