@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) act_grad_kernel(const 
       }
     }
   }
+  let_next_launch();
   if (p.partials == nullptr) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) red[threadIdx.x][j] = sum[j];

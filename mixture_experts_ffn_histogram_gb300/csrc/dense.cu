@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
     s.abort_flag = 0;
     mbar_fence_init();
+    wait_for_previous();
     // the first stages' operands come while the rest is set up (the barriers
     // are this thread's own so far)
     for (int i = 0; i < min(stages, nkb); ++i) {
@@ -332,6 +333,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  wait_for_previous();
   const uint32_t tmem = s.tmem_base;
   const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
 
@@ -452,6 +454,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   __syncwarp();
   if (splits > 1) cluster_sync();
   else __syncthreads();
+  let_next_launch();
 
   // this CTA's share of the tile's rows: the sum over the partials of the
   // splits, and the epilogue
@@ -594,6 +597,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   cluster_sync();  // the peer's barriers exist before any remote arrive
   tc_fence_after();
+  wait_for_previous();
   const uint32_t tmem = s.tmem_base;
   const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
 
@@ -804,6 +808,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
 
   __syncwarp();
+  let_next_launch();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs are done with each other's memory
@@ -932,18 +937,22 @@ cudaError_t launch_split(const DenseCall& c, int splits, cudaStream_t s) {
   const size_t bytes = static_cast<size_t>(stages) * S::kStage + kOver;
   const int chunk = c.out_type == MOE_FP32 ? kChunkBlocks : p.kblocks;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  unsigned attrs = 0;
+  if (c.follows) attr[attrs++] = overlap_attribute();
+  if (splits > 1) {
+    attr[attrs].id = cudaLaunchAttributeClusterDimension;
+    attr[attrs].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[attrs].val.clusterDim.y = 1;
+    attr[attrs++].val.clusterDim.z = 1;
+  }
   cfg.gridDim = dim3(static_cast<unsigned>(cdiv(na, kTileM) * splits),
                      static_cast<unsigned>(cdiv(nb, S::BN)), 1);
   cfg.blockDim = dim3(kSplitThreads, 1, 1);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 1 : 0;
+  cfg.numAttrs = attrs;
   return cudaLaunchKernelEx(&cfg, kern, ma, mb, p, stages, splits, chunk);
 }
 
@@ -984,7 +993,8 @@ cudaError_t launch_pair(const DenseCall& c, cudaStream_t s) {
   if (ok && p.has_z) ok = map2d(&mz, c.z, c.N, c.M, c.ldz, 64, 32);
   if (!ok) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1] = overlap_attribute();
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -1004,6 +1014,7 @@ cudaError_t launch_pair(const DenseCall& c, cudaStream_t s) {
   });
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, max_pairs)), 1, 1);
+  cfg.numAttrs = c.follows ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, mr, mz, p);
 }
 

@@ -15,6 +15,15 @@ namespace moe {
 // workspace at most: a few per SM on any device.
 constexpr int64_t kPartialRows = 1024;
 
+// The launch attribute of a kernel that starts with wait_for_previous, behind
+// a kernel of the same call.
+inline cudaLaunchAttribute overlap_attribute() {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
 struct NormCall {
   const void *x, *res, *gamma, *beta;  // backward: x = dy, res = dres
   const void* r_in;                    // backward: the stored rows
@@ -32,7 +41,8 @@ cudaError_t launch_layer_norm(const NormCall& c, cudaStream_t s);
 cudaError_t launch_layer_norm_bwd(const NormCall& c, cudaStream_t s);
 
 // out0[c] (c < split) and out1[c - split] = sum over P rows of partials
-// [P][C], in a fixed order.  type: of out0 and out1.
+// [P][C], in a fixed order.  type: of out0 and out1.  The launch before it on
+// the stream is the one that writes the partials.
 cudaError_t launch_join_partials(const float* partials, int P, int64_t C, int64_t split, void* out0,
                                  void* out1, moe_dtype type, cudaStream_t s);
 
@@ -71,6 +81,7 @@ struct DenseCall {
   moe_dtype type, out_type;
   int act;
   int32_t* dev_status;
+  bool follows;  // the launch before it on the stream is one of the same call
 };
 cudaError_t launch_dense(const DenseCall& c, cudaStream_t s);
 

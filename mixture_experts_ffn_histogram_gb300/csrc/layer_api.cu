@@ -282,10 +282,12 @@ moe_status moe_linear_bwd(moe_mat dy, moe_mat z, moe_mat x, moe_mat w, moe_mat d
     c.ldres = dx_add.ld;
     c.c = dx.p;
     c.ldc = dx.ld;
+    c.follows = own_dz || db != nullptr;
     const cudaError_t err = moe::launch_dense(c, stream);
     if (err != cudaSuccess) return from_cuda(err);
   }
   if (dw.p != nullptr) {
+    c.follows = own_dz || db != nullptr || dx.p != nullptr;
     c.a = x.p;
     c.lda = x.ld;
     c.a_mn = true;

@@ -176,6 +176,14 @@ struct Nums {
   }
 };
 
+// A kernel that a call launches behind another of its own may start before
+// that one has ended (its launch and set-up overlap the other's end); it waits
+// here before it touches global memory.  Returns at once in a kernel that was
+// launched without the attribute.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The kernel behind this one may be launched once every block has come here.
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // VEC weights (fp32 or T) as fp32; VEC > 1 asks for 16-byte alignment of W.
 template <typename W, int VEC>
 __device__ __forceinline__ void load_weights(const W* w, int i, float (&f)[VEC]) {

@@ -576,6 +576,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
     if (++stage == steps) stage = 0;
   }
   cp_async_wait_all();
+  let_next_launch();
   if (p.partials == nullptr && p.dgamma == nullptr) return;
   // one block alone writes the gradients themselves
   W* dgamma = static_cast<W*>(p.dgamma);
@@ -686,6 +687,7 @@ __global__ void __launch_bounds__(kJoinCols* kJoinRows)
     join_partials_kernel(const float* __restrict__ part, int P, int64_t C, int64_t split, O* out0,
                          O* out1) {
   __shared__ float acc[kJoinRows][kJoinCols + 1];
+  wait_for_previous();
   const int tx = threadIdx.x % kJoinCols, ty = threadIdx.x / kJoinCols;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * kJoinCols + tx;
   float s = 0.0f;
@@ -985,22 +987,24 @@ cudaError_t launch_layer_norm_bwd(const NormCall& c, cudaStream_t s) { return by
 
 cudaError_t launch_join_partials(const float* partials, int P, int64_t C, int64_t split, void* out0,
                                  void* out1, moe_dtype type, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((C + kJoinCols - 1) / kJoinCols)), block(kJoinCols * kJoinRows);
+  cudaLaunchAttribute overlap = overlap_attribute();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((C + kJoinCols - 1) / kJoinCols));
+  cfg.blockDim = dim3(kJoinCols * kJoinRows);
+  cfg.stream = s;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
   switch (type) {
     case MOE_BF16:
-      join_partials_kernel<<<grid, block, 0, s>>>(partials, P, C, split,
-                                                  static_cast<__nv_bfloat16*>(out0),
-                                                  static_cast<__nv_bfloat16*>(out1));
-      break;
+      return cudaLaunchKernelEx(&cfg, join_partials_kernel<__nv_bfloat16>, partials, P, C, split,
+                                static_cast<__nv_bfloat16*>(out0), static_cast<__nv_bfloat16*>(out1));
     case MOE_FP16:
-      join_partials_kernel<<<grid, block, 0, s>>>(partials, P, C, split, static_cast<__half*>(out0),
-                                                  static_cast<__half*>(out1));
-      break;
+      return cudaLaunchKernelEx(&cfg, join_partials_kernel<__half>, partials, P, C, split,
+                                static_cast<__half*>(out0), static_cast<__half*>(out1));
     default:
-      join_partials_kernel<<<grid, block, 0, s>>>(partials, P, C, split, static_cast<float*>(out0),
-                                                  static_cast<float*>(out1));
+      return cudaLaunchKernelEx(&cfg, join_partials_kernel<float>, partials, P, C, split,
+                                static_cast<float*>(out0), static_cast<float*>(out1));
   }
-  return cudaGetLastError();
 }
 
 }  // namespace moe
