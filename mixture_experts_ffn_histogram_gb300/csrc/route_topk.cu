@@ -205,6 +205,26 @@ __device__ __noinline__ int select_fp64(const float* row, const float* bias, con
   return slot;
 }
 
+// Four values in descending order, and the first of them taken off.
+__device__ __forceinline__ void sort4(float (&q)[4]) {
+  auto order = [&](int x, int y) {
+    const float hi = fmaxf(q[x], q[y]);
+    q[y] = fminf(q[x], q[y]);
+    q[x] = hi;
+  };
+  order(0, 1);
+  order(2, 3);
+  order(0, 2);
+  order(1, 3);
+  order(1, 2);
+}
+__device__ __forceinline__ void pop4(float (&q)[4]) {
+  q[0] = q[1];
+  q[1] = q[2];
+  q[2] = q[3];
+  q[3] = kNegInf;
+}
+
 // Bounds of the error of a fast score (see fast_score): s (6e-7 + 1.5e-7
 // max(-l, 0)) for the sigmoid, from the exponential's 2 ulp and its rounded
 // argument (1.17 |l| ulp) and the reciprocal's ulp; for the softmax
@@ -228,7 +248,11 @@ struct WarpToken {
   const TopkArgs& p;
   float2* cand;
   int vpl, lpg, lane, first, mine, group, r;
-  bool vec, few;  // few: 32 experts at most to choose from, on fewer than K lanes
+  // tight: the experts to choose from lie on fewer than 2 K lanes, whose maxima
+  // alone would leave too many candidates (2400 tokens, 11 of 512 experts in
+  // one of 4 groups: 29 us so, 8.5 with four maxima a lane); few: and are 32
+  // at most
+  bool vec, tight, few;
 
   __device__ __forceinline__ WarpToken(const TopkArgs& p_, float2* cand_, int vpl_, int lpg_)
       : p(p_), cand(cand_), vpl(vpl_), lpg(lpg_), lane(threadIdx.x & 31) {
@@ -236,7 +260,8 @@ struct WarpToken {
     const moe_topk_dims& d = p.d;
     const bool grouped = d.groups > 1 && d.top_groups < d.groups;
     const int gs = grouped ? d.E / d.groups : d.E, staying = grouped ? d.top_groups : 1;
-    few = staying * gs <= 32 && d.K > staying * ((gs + vpl - 1) / vpl);
+    tight = 2 * d.K > staying * ((gs + vpl - 1) / vpl);
+    few = tight && staying * gs <= 32;
     group = lane / lpg;
     r = lane - group * lpg;
     first = group * gs + r * vpl;
@@ -361,17 +386,26 @@ struct WarpToken {
       }
     }
 
-    // a lower bound of the K-th value: the K-th largest of the lanes' maxima
-    // (none where those lanes are fewer: then all experts are candidates)
-    float top = l[0];
-#pragma unroll
-    for (int i = 1; i < VPL; ++i) top = fmaxf(top, l[i]);
+    // a lower bound of the K-th value: the K-th largest of the lanes' maxima,
+    // or (tight) of the maxima of every fourth of a lane's experts; none where
+    // all experts are candidates
     float bound = kNegInf;
-    if (!few) {
-      float rest = top;
+    if (!tight) {
+      float rest = l[0];
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) rest = fmaxf(rest, l[i]);
       for (int k = 0; k < K; ++k) {
         bound = warp_max_f32(rest);
         if (rest == bound) rest = kNegInf;
+      }
+    } else if (!few) {
+      float q4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) q4[i % 4] = fmaxf(q4[i % 4], l[i]);
+      sort4(q4);
+      for (int k = 0; k < K; ++k) {
+        bound = warp_max_f32(q4[0]);
+        if (q4[0] == bound) pop4(q4);
       }
     }
     if (biased) bound -= 2.0f * (worst + kSumError * fabsf(bound));  // what may still pass it
@@ -732,26 +766,12 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
     }
     // a lower bound of the K-th value: the K-th largest of the quarters' bests
     // (none where there are fewer of those: then all experts are candidates)
-    auto order = [&](int x, int y) {
-      const float hi = fmaxf(q4[x], q4[y]);
-      q4[y] = fminf(q4[x], q4[y]);
-      q4[x] = hi;
-    };
     if (out) q4[0] = q4[1] = q4[2] = q4[3] = kNegInf;
-    order(0, 1);
-    order(2, 3);
-    order(0, 2);
-    order(1, 3);
-    order(1, 2);
+    sort4(q4);
     float bound = kNegInf;
     for (int k = 0; k < K && !few; ++k) {
       bound = sub_max<LANES>(q4[0]);
-      if (q4[0] == bound) {
-        q4[0] = q4[1];
-        q4[1] = q4[2];
-        q4[2] = q4[3];
-        q4[3] = kNegInf;
-      }
+      if (q4[0] == bound) pop4(q4);
     }
     const bool bounded = few || bound > kNegInf;
     if (biased) bound -= 2.0f * (worst + kSumError * fabsf(bound));
@@ -1044,9 +1064,10 @@ cudaError_t launch_route_topk(const float* logits, const float* bias, int32_t* i
     });
     return true;
   };
-  // below this a token a warp fills the SMs better (4096 tokens: 9.7 us both
-  // ways, 2048: 6.4 and 7.6)
-  if (d.T >= 32 * static_cast<int64_t>(sm_count()) &&
+  // below this a token a warp fills the SMs better (256 experts in 8 groups, 8
+  // taken: 2400 tokens 6.5 us, 8.0 packed; 4000 9.9 and 10.2; 8000 13.1 and
+  // 11.9; 512 experts, 8 taken, 4000: 12.5 and 9.8)
+  if (d.T >= 24 * static_cast<int64_t>(sm_count()) &&
       ((d.K <= 8 && packed(std::integral_constant<int, 8>{})) || packed(std::integral_constant<int, 16>{})))
     return cudaGetLastError();
   const unsigned grid = topk_grid(d.T, 12);
