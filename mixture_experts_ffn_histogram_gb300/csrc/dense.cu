@@ -32,8 +32,8 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
-#include <cstdlib>
 
 #include "activation.cuh"
 #include "kernels.h"
@@ -188,11 +188,12 @@ struct TileEnd {
   const uint8_t* smem;  // ... and its pointer
 };
 
-// Sums the SP partials (in rank order) and runs the epilogue.  A thread keeps
+// Sums the partials of the splits (SP or fewer, in rank order) and runs the
+// epilogue.  A thread keeps
 // to four columns and walks down the rows, G of them at a time: G * SP loads
 // are under way together, and addresses advance by constants.
 template <class S, typename T, typename O, int G, int SP>
-__device__ __forceinline__ void finish_rows(const TileEnd& te, const DenseParams& p) {
+__device__ __forceinline__ void finish_rows(const TileEnd& te, const DenseParams& p, int splits) {
   constexpr bool kExact = sizeof(O) == 4;
   constexpr int kPer = S::kColsOut / 4;          // threads across a row
   constexpr int kDown = kSplitThreads / kPer;    // rows of one pass
@@ -208,7 +209,7 @@ __device__ __forceinline__ void finish_rows(const TileEnd& te, const DenseParams
 #pragma unroll
   for (int q = 0; q < SP; ++q) {
     const uint32_t at = te.ring + static_cast<uint32_t>(r * S::kLd + cc) * 4;
-    from[q] = SP > 1 ? mapa_shared(at, q) : at;
+    from[q] = SP > 1 ? mapa_shared(at, min(q, splits - 1)) : at;
   }
   const int64_t row = te.row0 + r;
   O* c = static_cast<O*>(p.c) + row * p.ldc + col;
@@ -240,6 +241,7 @@ __device__ __forceinline__ void finish_rows(const TileEnd& te, const DenseParams
       float4 t = f[g][0];
 #pragma unroll
       for (int q = 1; q < SP; ++q) {
+        if (q >= splits) break;
         t.x += f[g][q].x;
         t.y += f[g][q].y;
         t.z += f[g][q].z;
@@ -278,12 +280,10 @@ __device__ __forceinline__ void finish_rows(const TileEnd& te, const DenseParams
 }
 template <class S, typename T, typename O>
 __device__ __forceinline__ void finish_tile(const TileEnd& te, int splits, const DenseParams& p) {
-  switch (splits) {
-    case 1: finish_rows<S, T, O, 4, 1>(te, p); break;
-    case 2: finish_rows<S, T, O, 4, 2>(te, p); break;
-    case 4: finish_rows<S, T, O, 2, 4>(te, p); break;
-    default: finish_rows<S, T, O, 1, 8>(te, p); break;
-  }
+  if (splits == 1) finish_rows<S, T, O, 4, 1>(te, p, splits);
+  else if (splits == 2) finish_rows<S, T, O, 4, 2>(te, p, splits);
+  else if (splits <= 4) finish_rows<S, T, O, 2, 4>(te, p, splits);
+  else finish_rows<S, T, O, 1, 8>(te, p, splits);
 }
 
 template <class S>
@@ -901,6 +901,14 @@ DenseParams make_params(const DenseCall& c) {
   return p;
 }
 
+// Clusters of 1 to 8 CTAs that find an SM for each CTA (as the driver counts
+// them for 152 SMs): a cluster lies within one group of SMs, so that clusters
+// of 7 or 8 leave a fifth of the SMs idle or pair up on some.
+int64_t lone_clusters(int splits) {
+  static const int kOf152[8] = {152, 76, 46, 36, 28, 23, 15, 15};
+  return kOf152[splits - 1] * static_cast<int64_t>(sm_count()) / 152;
+}
+
 template <class S>
 cudaError_t launch_split(const DenseCall& c, int splits, cudaStream_t s) {
   auto kern = dense_split_kernel<S>;
@@ -929,9 +937,13 @@ cudaError_t launch_split(const DenseCall& c, int splits, cudaStream_t s) {
       std::max({2, (S::kPartial + S::kStage - 1) / S::kStage, (kFloorBytes + S::kStage - 1) / S::kStage});
   constexpr int kOver = 1024 + static_cast<int>(sizeof(SplitCtl));
   static_assert(kLeast <= kSplitMaxStages && kLeast * S::kStage + kOver <= kSplitSmemLimit, "shared memory");
-  // two CTAs to an SM: clusters of eight find room beside one another, and
-  // one's epilogue overlaps the other's products
-  const int budget = kSplitSmemLimit / 2 - kOver - 1024;
+  // All of an SM's shared memory where every cluster finds SMs of its own: six
+  // 32 KB stages instead of three keep a lone CTA's operands coming (8191 x
+  // 7168 -> 256: 33.5 us, 48 with three; 203 x 5224 -> 3904 in two splits 19.3
+  // and 25.2).  Otherwise two CTAs to an SM, one's epilogue behind the other's
+  // products.
+  const bool alone = cdiv(na, kTileM) * cdiv(nb, S::BN) <= lone_clusters(splits);
+  const int budget = (alone ? kSplitSmemLimit : kSplitSmemLimit / 2) - kOver - 1024;
   const int mine = static_cast<int>(cdiv(p.kblocks, splits));
   const int stages = std::max(kLeast, std::min({budget / S::kStage, kSplitMaxStages, mine}));
   const size_t bytes = static_cast<size_t>(stages) * S::kStage + kOver;
@@ -1026,23 +1038,25 @@ cudaError_t launch_pair_type(const DenseCall& c, cudaStream_t s) {
 }
 
 // The kernel, tile and splits of a product, by an estimate in cycles fitted to
-// measurements (bf16, 25 shapes from 1 x 320 x 192 to 19709 x 448 x 576, each
-// under every tile and split; it takes the fastest or one within 15% of it).
-//   split kernel: 7000 to launch, set up and end; per reduction block 450 to
-//   700 for the wider tiles (bound by the operands' way from L2); 900 to 6000
-//   for a tile's epilogue, shared by the splits; 4000 for a cluster's
-//   barriers; all of the per-tile part times the CTAs per SM above one.
-//   pair kernel: 17500, and per wave of tiles 600 a block, or the epilogue's
-//   6500 where that is more.
+// measurements (bf16, 172 products from 1 x 320 x 192 to 31528 x 120 x 472,
+// forward, fp32 results and wgrads, each under every tile and split; the one
+// it takes is 0.6% behind the fastest on average, at worst 1.12 times).
+//   split kernel: 7000 to launch, set up and end and 1450 for a cluster's
+//   barriers; per reduction block 350 to 640 (the operands' way from L2), per
+//   tile an epilogue shared by the splits.  With u clusters to each place for
+//   one that has its SMs to itself, blocks overlap and take 0.65 of that, but
+//   all of a cluster's part 1 + 1.1 (u - 1) + 1.5 (ceil(u) - 1) times as long.
+//   pair kernel: 10400, and per wave of tiles 770 a block, or the epilogue's
+//   6200 where that is more.
 struct DensePlan {
   bool pair;
   int bn, splits;
 };
 DensePlan plan_dense(const DenseCall& c) {
-  struct Tile { int bn; double block, end; };
-  static const Tile kTiles[] = {{16, 450, 900}, {32, 480, 1500}, {64, 520, 2700}, {128, 700, 6000}};
+  struct Tile { int bn; double block, end, most; };  // most: CTAs per SM that were measured
+  static const Tile kTiles[] = {{16, 350, 50, 2.6}, {32, 365, 100, 2.6}, {64, 500, 50, 2.6}, {128, 640, 4800, 4.6}};
   const double sms = sm_count();
-  const double kb = static_cast<double>(cdiv(c.Kred, kBlockK));
+  const int kb = static_cast<int>(cdiv(c.Kred, kBlockK));
   DensePlan best{false, 128, 1};
   double least = 1e300;
   for (const Tile& t : kTiles) {
@@ -1052,12 +1066,13 @@ DensePlan plan_dense(const DenseCall& c) {
     if (t.bn < 64 && !swap) continue;
     const double tiles = static_cast<double>(swap ? cdiv(c.N, kTileM) * cdiv(c.M, t.bn)
                                                   : cdiv(c.M, kTileM) * cdiv(c.N, t.bn));
-    for (int s = 1; s <= 8; s *= 2) {
-      // many tiles are the 128 wide ones' alone; a split gets two blocks at least
-      if (tiles * s > 2 * sms && (t.bn < 128 || s > 1)) break;
-      if (s > 1 && kb < 2 * s) break;
-      const double est = 7000 + (kb / s * t.block + t.end / s) * std::max(1.0, tiles * s / sms) +
-                         (s > 1 ? 4000 : 0);
+    for (int s = 1; s <= 8; ++s) {
+      if (s > 1 && kb < 2 * s) break;  // a split gets two blocks at least
+      if (tiles * s > t.most * sms && (t.bn < 128 || s > 1)) break;
+      const double u = tiles / static_cast<double>(lone_clusters(s));
+      const double load = u <= 1 ? 1 : 1 + 1.1 * (u - 1) + 1.5 * (std::ceil(u) - 1);
+      const double est = 7000 + (cdiv(kb, s) * t.block * (u <= 1 ? 1 : 0.65) + t.end / s) * load +
+                         (s > 1 ? 1450 : 0);
       if (est < least) {
         least = est;
         best = DensePlan{false, t.bn, s};
@@ -1067,7 +1082,7 @@ DensePlan plan_dense(const DenseCall& c) {
   if (c.out_type != MOE_FP32) {
     const int64_t pairs = sm_count() / 2;
     const double waves = static_cast<double>(cdiv(cdiv(c.M, 256) * cdiv(c.N, kPairN), pairs));
-    if (17500 + waves * std::max(kb * 600, 6500.0) < least) best.pair = true;
+    if (10400 + waves * std::max(kb * 770.0, 6200.0) < least) best.pair = true;
   }
   return best;
 }
