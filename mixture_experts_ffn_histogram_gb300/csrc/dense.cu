@@ -18,10 +18,10 @@
 // For fp32 results the accumulators are drained into registers every
 // kChunkBlocks reduction blocks: the tensor core's additions truncate, and a
 // long chain of them would lose what an fp32 result is asked for.
-// pair kernel: persistent, for products with enough 256 x 256 tiles for the
-// SMs.  The CTA pair of a 2-CTA cluster works on one tile: each CTA loads its
-// 128 rows of A and its 128 columns of B, the even CTA issues
-// tcgen05.mma.cta_group::2 (M = 256, N = 256), and each CTA's tensor memory
+// pair kernel: persistent, for products with enough 256 x 256 tiles (or of 192
+// or 128 columns) for the SMs.  The CTA pair of a 2-CTA cluster works on one
+// tile: each CTA loads its 128 rows of A and half of the columns of B, the even
+// CTA issues tcgen05.mma.cta_group::2 (M = 256), and each CTA's tensor memory
 // holds its 128 rows twice (the next tile's products overlap the epilogue).
 // Sixteen epilogue warps take a quarter of the rows and of the columns each
 // (one warp's chain of waits, loads and stores is latency: fewer warps leave
@@ -131,15 +131,30 @@ __device__ __forceinline__ void operand_load(uint8_t* dst, const CUtensorMap* ma
   }
 }
 
+// The matrix descriptor of an operand's block at shared address 0, and the
+// step from one MMA's 16 reduction elements to the next (in units of 16 bytes).
+struct Operand {
+  uint64_t desc;
+  uint32_t step;
+};
+template <bool MN>
+__device__ __forceinline__ Operand operand128() {
+  return MN ? Operand{smem_desc_sw128(0, kChunk, 1024), 128} : Operand{smem_desc_sw128(0, 16, 1024), 2};
+}
+// MN-major in 32-wide chunks, 64-byte swizzling (mode 4): eight reduction rows
+// of a chunk are 512 bytes.
+constexpr int kChunk32 = 32 * kBlockK * 2;
+__device__ __forceinline__ Operand operand64() {
+  return Operand{(smem_desc_sw128(0, kChunk32, 512) & ~(7ull << 61)) | (4ull << 61), 64};
+}
 // The products of one reduction block: operands at shared addresses a and b.
-template <int CG, bool AMN, bool BMN>
-__device__ __forceinline__ void issue_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                            uint32_t add) {
-  const uint64_t ad = AMN ? smem_desc_sw128(a, kChunk, 1024) : smem_desc_sw128(a, 16, 1024);
-  const uint64_t bd = BMN ? smem_desc_sw128(b, kChunk, 1024) : smem_desc_sw128(b, 16, 1024);
+template <int CG>
+__device__ __forceinline__ void issue_block(uint32_t d, uint32_t a, uint32_t b, const Operand& oa,
+                                            const Operand& ob, uint32_t idesc, uint32_t add) {
+  const uint64_t ad = oa.desc | ((a >> 4) & 0x3FFFu), bd = ob.desc | ((b >> 4) & 0x3FFFu);
 #pragma unroll
-  for (int kk = 0; kk < kBlockK / kMmaK; ++kk)  // start addresses in units of 16 bytes
-    umma_bf16<CG>(d, ad + kk * (AMN ? 128 : 2), bd + kk * (BMN ? 128 : 2), idesc, kk > 0 ? 1u : add);
+  for (int kk = 0; kk < kBlockK / kMmaK; ++kk)
+    umma_bf16<CG>(d, ad + kk * oa.step, bd + kk * ob.step, idesc, kk > 0 ? 1u : add);
 }
 
 // A wait of the whole warp, polled by one lane.
@@ -383,8 +398,8 @@ __global__ void __launch_bounds__(kSplitThreads)
           ok = mbar_wait(&s.full[stage], phase, wc);
           if (!ok) break;
           tc_fence_after();
-          issue_block<1, S::AMN, S::BMN>(tmem + slot * BN, base + stage * kStage,
-                                          base + stage * kStage + kATile, idesc, add);
+          issue_block<1>(tmem + slot * BN, base + stage * kStage, base + stage * kStage + kATile,
+                         operand128<S::AMN>(), operand128<S::BMN>(), idesc, add);
           add = 1u;
           umma_commit<1>(&s.empty[stage]);
           ++done;
@@ -504,6 +519,8 @@ struct PairParams {
   const float* bias;
   int64_t M, N;
   int kblocks, m_tiles, n_tiles, act;
+  int bn;                  // columns of a tile: 128, 192 or 256
+  int b_boxes, stage_bytes;  // boxes of an MN-major B per CTA; bytes of a CTA's stage
   int a_chunks, b_chunks;  // MN-major operands: one box of two 64-wide chunks (3-D map)
   int has_res, has_z;
   const void* res;
@@ -541,17 +558,21 @@ __device__ __forceinline__ void add32(uint8_t* buf, int lane, int h, float (&v)[
   }
 }
 
-// One operand's share of a stage: 128 rows (K-major), or two 64-wide chunks.
+// One operand's share of a stage: up to 128 rows (K-major); or one or two
+// 64-wide chunks (two in one box where the map has them), or three 32-wide.
 template <bool MN>
 __device__ __forceinline__ void pair_load(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int x0,
-                                          int k0, int chunked) {
+                                          int k0, int chunked, int boxes) {
   if constexpr (!MN) {
     tma_load_2d_pair(dst, map, bar, k0, x0);
   } else if (chunked) {
     tma_load_3d_pair(dst, map, bar, 0, k0, x0 / 64);
+  } else if (boxes == 3) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) tma_load_2d_pair(dst + i * kChunk32, map, bar, x0 + 32 * i, k0);
   } else {
     tma_load_2d_pair(dst, map, bar, x0, k0);
-    tma_load_2d_pair(dst + kChunk, map, bar, x0 + 64, k0);
+    if (boxes == 2) tma_load_2d_pair(dst + kChunk, map, bar, x0 + 64, k0);
   }
 }
 
@@ -611,17 +632,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       bool aborted = false;
       for (int t = blockIdx.x / 2; t < ntiles && !aborted; t += units) {
         const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
-        const int a0 = mt * 256 + 128 * rank, b0 = nt * kPairN + 128 * rank;
+        const int a0 = mt * 256 + 128 * rank, b0 = nt * p.bn + p.bn / 2 * rank;
         for (int kb = 0; kb < p.kblocks; ++kb) {
           if (!mbar_wait(&s.empty[stage], phase ^ 1u, wc)) {
             aborted = true;
             break;
           }
           uint8_t* sa = ring + stage * kPairStage;
-          if (leader) mbar_arrive_expect_tx(&s.full[stage], 2 * kPairStage);
+          if (leader) mbar_arrive_expect_tx(&s.full[stage], 2 * p.stage_bytes);
           const uint32_t bar = full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
-          pair_load<AMN>(sa, &map_a, bar, a0, kb * kBlockK, p.a_chunks);
-          pair_load<BMN>(sa + kATile, &map_b, bar, b0, kb * kBlockK, p.b_chunks);
+          pair_load<AMN>(sa, &map_a, bar, a0, kb * kBlockK, p.a_chunks, 2);
+          pair_load<BMN>(sa + kATile, &map_b, bar, b0, kb * kBlockK, p.b_chunks, p.b_boxes);
           ++filled;
           if (++stage == kPairStages) {
             stage = 0;
@@ -639,6 +660,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     if (leader && elect_one()) {  // as in the split kernel, one thread
       const uint32_t base = smem_u32(ring);
+      const Operand ob = BMN && p.b_boxes == 3 ? operand64() : operand128<BMN>();
       int stage = 0, done = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -652,7 +674,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t a = base + stage * kPairStage;
-          issue_block<2, AMN, BMN>(tmem + acc * kPairN, a, a + kATile, p.idesc, add);
+          issue_block<2>(tmem + acc * kPairN, a, a + kATile, operand128<AMN>(), ob, p.idesc, add);
           add = 1u;
           umma_commit<2>(&s.empty[stage]);
           ++done;
@@ -673,7 +695,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else {
     // epilogue: rows 32 q.. of this CTA's 128, columns 64 part.. of the
-    // tile's 256.  A residual comes by TMA, one tile ahead, into the buffer
+    // tile's (narrower tiles leave some of these warps idle).  A residual comes by TMA, one tile ahead, into the buffer
     // from which the result is stored.  With z the buffer is used for z and
     // then for the result, and a residual is read by the threads.
     const int ew = warp - 2, q = warp & 3, part = ew >> 2;
@@ -686,8 +708,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     auto place = [&](int t, int& y, int64_t& col) -> bool {  // of this warp's chunk of tile t
       const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
       y = mt * 256 + 128 * rank + 32 * q;
-      col = static_cast<int64_t>(nt) * kPairN + 64 * part;
-      return y < p.M && col < p.N;
+      col = static_cast<int64_t>(nt) * p.bn + 64 * part;
+      return 64 * part < p.bn && y < p.M && col < p.N;
     };
     bool flying = false;  // a residual is under way
     uint32_t rphase = 0;
@@ -842,13 +864,15 @@ EncodeTiledFn encode_fn() {
 // box_inner x box_outer; what lies outside reads as zero.
 bool map2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
            uint32_t box_inner, uint32_t box_outer) {
+  // rows of a box as wide as the swizzle: 128 bytes, 64 for boxes of 32
+  const CUtensorMapSwizzle swizzle = box_inner == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {ld * 2};
   const cuuint32_t box[2] = {box_inner, box_outer}, es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -969,13 +993,15 @@ cudaError_t launch_split(const DenseCall& c, int splits, cudaStream_t s) {
 }
 
 template <bool MN>
-bool pair_operand(CUtensorMap* m, const void* base, int64_t outer, int64_t Kred, int64_t ld) {
-  if (!MN) return map2d(m, base, Kred, outer, ld, kBlockK, 128);
-  return outer % 64 == 0 ? map_chunks(m, base, outer, Kred, ld) : map2d(m, base, outer, Kred, ld, 64, kBlockK);
+bool pair_operand(CUtensorMap* m, const void* base, int64_t outer, int64_t Kred, int64_t ld, int rows,
+                  int chunked) {
+  if (!MN) return map2d(m, base, Kred, outer, ld, kBlockK, rows);
+  return chunked ? map_chunks(m, base, outer, Kred, ld)
+                 : map2d(m, base, outer, Kred, ld, rows == 96 ? 32 : 64, kBlockK);
 }
 
 template <typename T, bool AMN, bool BMN, bool FULL>
-cudaError_t launch_pair(const DenseCall& c, cudaStream_t s) {
+cudaError_t launch_pair(const DenseCall& c, int bn, cudaStream_t s) {
   auto kern = dense_pair_kernel<T, AMN, BMN, FULL>;
   static std::atomic<bool> attr_set[64];
   cudaError_t err = allow_smem(kern, attr_set, static_cast<int>(kPairSmem));
@@ -986,20 +1012,23 @@ cudaError_t launch_pair(const DenseCall& c, cudaStream_t s) {
   p.N = c.N;
   p.kblocks = static_cast<int>(cdiv(c.Kred, kBlockK));
   p.m_tiles = static_cast<int>(cdiv(c.M, 256));
-  p.n_tiles = static_cast<int>(cdiv(c.N, kPairN));
+  p.n_tiles = static_cast<int>(cdiv(c.N, bn));
+  p.bn = bn;
+  p.b_boxes = bn / 64 == 3 ? 3 : bn / 128;  // a CTA's 64, 96 or 128 columns
+  p.stage_bytes = kATile + bn / 2 * kBlockK * 2;
   p.act = c.act;
   p.a_chunks = AMN && c.M % 64 == 0;
-  p.b_chunks = BMN && c.N % 64 == 0;
+  p.b_chunks = BMN && c.N % 64 == 0 && bn == kPairN;
   p.has_res = c.res != nullptr;
   p.has_z = c.z != nullptr;
   p.res = c.res;
   p.ldres = c.ldres;
-  p.idesc = dense_idesc(256, kPairN, AMN, BMN, c.type == MOE_BF16 ? 1u : 0u);
+  p.idesc = dense_idesc(256, bn, AMN, BMN, c.type == MOE_BF16 ? 1u : 0u);
   p.status = c.dev_status;
   p.limit_ns = kDefaultWaitLimitNs;
   CUtensorMap ma, mb, mc, mr, mz;
-  bool ok = pair_operand<AMN>(&ma, c.a, c.M, c.Kred, c.lda) &&
-            pair_operand<BMN>(&mb, c.b, c.N, c.Kred, c.ldb) && map2d(&mc, c.c, c.N, c.M, c.ldc, 64, 32);
+  bool ok = pair_operand<AMN>(&ma, c.a, c.M, c.Kred, c.lda, 128, p.a_chunks) &&
+            pair_operand<BMN>(&mb, c.b, c.N, c.Kred, c.ldb, bn / 2, p.b_chunks) && map2d(&mc, c.c, c.N, c.M, c.ldc, 64, 32);
   mr = mz = mc;
   if (ok && p.has_res) ok = map2d(&mr, c.res, c.N, c.M, c.ldres, 64, 32);
   if (ok && p.has_z) ok = map2d(&mz, c.z, c.N, c.M, c.ldz, 64, 32);
@@ -1031,10 +1060,10 @@ cudaError_t launch_pair(const DenseCall& c, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t launch_pair_type(const DenseCall& c, cudaStream_t s) {
-  if (c.a_mn) return launch_pair<T, true, true, false>(c, s);
-  if (c.b_mn) return launch_pair<T, false, true, true>(c, s);
-  return launch_pair<T, false, false, false>(c, s);
+cudaError_t launch_pair_type(const DenseCall& c, int bn, cudaStream_t s) {
+  if (c.a_mn) return launch_pair<T, true, true, false>(c, bn, s);
+  if (c.b_mn) return launch_pair<T, false, true, true>(c, bn, s);
+  return launch_pair<T, false, false, false>(c, bn, s);
 }
 
 // The kernel, tile and splits of a product, by an estimate in cycles fitted to
@@ -1046,8 +1075,10 @@ cudaError_t launch_pair_type(const DenseCall& c, cudaStream_t s) {
 //   tile an epilogue shared by the splits.  With u clusters to each place for
 //   one that has its SMs to itself, blocks overlap and take 0.65 of that, but
 //   all of a cluster's part 1 + 1.1 (u - 1) + 1.5 (ceil(u) - 1) times as long.
-//   pair kernel: 10400, and per wave of tiles 770 a block, or the epilogue's
-//   6200 where that is more.
+//   pair kernel: 10400, and per wave of tiles 770 a block (690, 560 for 192 and
+//   128 columns), or the epilogue's 6200 (5000, 4300) where that is more.
+//   Narrower tiles fill the pairs better: 4096 x 2048 -> 768 takes 20.1 us with
+//   256 columns and 19.0 with 192, 4096 x 4096 -> 1152 48 and 41 with 128.
 struct DensePlan {
   bool pair;
   int bn, splits;
@@ -1080,9 +1111,17 @@ DensePlan plan_dense(const DenseCall& c) {
     }
   }
   if (c.out_type != MOE_FP32) {
-    const int64_t pairs = sm_count() / 2;
-    const double waves = static_cast<double>(cdiv(cdiv(c.M, 256) * cdiv(c.N, kPairN), pairs));
-    if (10400 + waves * std::max(kb * 770.0, 6200.0) < least) best.pair = true;
+    struct PairTile { int bn; double block, end; };
+    static const PairTile kPairTiles[] = {{256, 770, 6200}, {192, 690, 5000}, {128, 560, 4300}};
+    for (const PairTile& t : kPairTiles) {
+      const int64_t pairs = sm_count() / 2;
+      const double waves = static_cast<double>(cdiv(cdiv(c.M, 256) * cdiv(c.N, t.bn), pairs));
+      const double est = 10400 + waves * std::max(kb * t.block, t.end);
+      if (est < least) {
+        least = est;
+        best = DensePlan{true, t.bn, 1};
+      }
+    }
   }
   return best;
 }
@@ -1092,7 +1131,8 @@ DensePlan plan_dense(const DenseCall& c) {
 cudaError_t launch_dense(const DenseCall& c, cudaStream_t s) {
   const DensePlan plan = plan_dense(c);
   if (plan.pair)
-    return c.type == MOE_BF16 ? launch_pair_type<__nv_bfloat16>(c, s) : launch_pair_type<__half>(c, s);
+    return c.type == MOE_BF16 ? launch_pair_type<__nv_bfloat16>(c, plan.bn, s)
+                              : launch_pair_type<__half>(c, plan.bn, s);
   if (c.a_mn) {
     if (plan.bn == 64) return launch_split<SplitShape<64, true, true, false>>(c, plan.splits, s);
     return launch_split<SplitShape<128, true, true, false>>(c, plan.splits, s);

@@ -30,6 +30,12 @@ CASES = [
     (1030, 520, 1032, BF, BF, "silu", True, True, 0),
     (2100, 328, 1544, HF, HF, "gelu", True, True, 8),
     (4100, 704, 2816, BF, BF, "none", True, True, 0),
+    # shapes of the pair kernel's narrower tiles, in one of the three products each
+    (4096, 1096, 760, BF, BF, "gelu", True, False, 0),
+    (4096, 1032, 1160, HF, HF, "none", True, True, 8),
+    (1100, 4224, 760, BF, BF, "silu", True, True, 0),
+    (700, 4096, 1152, BF, BF, "none", False, True, 0),
+    (4096, 520, 1096, BF, BF, "relu", True, True, 8),
 ]
 
 
