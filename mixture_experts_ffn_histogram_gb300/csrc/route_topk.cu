@@ -13,7 +13,8 @@
 // expert from below, so the few experts at or above it (a dozen for 8 of 256)
 // hold the answer; they are compacted to one per lane, in the order of their
 // ids, and each counts those ahead of it.  Where they do not fit a warp (K
-// near 32), K rounds take one warp-wide maximum each.
+// near 32), K rounds take one warp-wide maximum each.  A few tokens are bound
+// by the launch and this chain (16 tokens, 256 experts: 4.1 us).
 //
 // The selection compares fp32 scores, which a rounding can swap.  Each
 // comparison that decides something is therefore checked against the error
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
 // candidates do not fit, and one with near ties, is finished by the whole
 // warp.  Bound by latency (96 registers leave 20 warps an SM, which issue in
 // half of the cycles).  32768 tokens, 256 experts in 8 groups: 8 taken 27 us,
-// 35 us with a token a warp; 16 taken 38 us and 94 us.
+// 35 us with a token a warp; 16 taken 38 us (5600 tokens: 12.1 and 13.3).
 template <int LANES>
 __device__ __forceinline__ float sub_max(float v) {
 #pragma unroll
@@ -891,7 +892,8 @@ struct TopkBwdArgs {
 // One warp per token.  Only the softmax without renormalisation has a dense
 // gradient (and reads the row); the others write zeros and the K values.
 // The K values overwrite the row's after a warp barrier.  Bound by HBM once
-// the loads of a warp's next token are under way while it works on this one.
+// the loads of a warp's next token are under way while it works on this one:
+// 32768 x 128, softmax, 8.1 us (36 MB, 5.3 us of HBM, behind the launch).
 template <int VPL, bool DENSE>
 __global__ void __launch_bounds__(32 * kTopkWarps) route_topk_bwd_kernel(const TopkBwdArgs p) {
   const moe_topk_dims d = p.d;
