@@ -36,8 +36,24 @@ class _Arg:
                          f"{'elements' if self.contiguous else 'columns'} on {self.device}, got "
                          f"{t.dtype} {list(t.shape)}, strides {list(t.stride())} on {t.device}")
 
+    def first(self, t, cap, width):
+        """The number of rows of the call, from its first matrix, whose MoeMat
+        this leaves in ``mat``."""
+        shape = t.shape
+        if (len(shape) != 2 or shape[1] != width or shape[0] > cap or t.dtype is not self.dtype
+                or t.get_device() != self.index):
+            self.refuse(t, (f"<= {cap}", width))
+        ld, inner = t.stride()
+        if inner != 1 and width > 1:
+            self.refuse(t, shape)
+        n = shape[0]
+        m = self.mat
+        m.p = t.data_ptr()
+        m.ld = ld if n > 1 else (width + 7) // 8 * 8
+        return n
+
     def rows(self, t, cap, width):
-        """The number of rows of the call, from its first matrix."""
+        """The number of rows of the call, from its first contiguous tensor."""
         shape = t.shape
         if len(shape) != 2 or shape[1] != width or shape[0] > cap:
             self.refuse(t, (f"<= {cap}", width))
@@ -75,9 +91,14 @@ def _refused(fn, status):
     raise B.MoeError(fn, status)
 
 
-def _launchable(device):
-    if device.type != "cuda":
+def _entry(name, device):
+    """A C entry point, for an operator whose buffers lie on `device`."""
+    if device.type == "cuda":
+        return getattr(B.lib(), name)
+
+    def refuse(*args):
         raise RuntimeError(f"the operator's buffers are on {device}: its kernels need a CUDA device")
+    return refuse
 
 
 class LayerNorm:
@@ -100,7 +121,8 @@ class LayerNorm:
         self.device = dev = self._y.device
         self._r = None
         self.r = self.mean = self.rstd = None
-        self._my, self._p_stats = _own(self._y), (None, None)
+        self._my, self._p_mean, self._p_rstd = _own(self._y), None, None
+        self._width = (D,)
         if train:
             self._stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
             self._mean, self._rstd = self._stats[0], self._stats[1]
@@ -110,33 +132,33 @@ class LayerNorm:
             self.ws = torch.empty(max(B.moe_layer_norm_workspace_bytes(rows, D), 256),
                                   dtype=torch.uint8, device=dev)
             self._mdx = _own(self._dx)
-            self._p_stats = (self._stats.data_ptr(), self._stats.data_ptr() + 4 * rows)
-            self._p_grads = (self.dgamma.data_ptr(), self.dbeta.data_ptr(), self.ws.data_ptr())
+            self._p_mean, self._p_rstd = self._mean.data_ptr(), self._rstd.data_ptr()
+            self._p_dgamma, self._p_dbeta = self.dgamma.data_ptr(), self.dbeta.data_ptr()
+            self._p_ws = self.ws.data_ptr()
         self._x, self._res = _Arg("x", dtype, dev), _Arg("res", dtype, dev)
         self._dy, self._rin, self._dres = (_Arg(n, dtype, dev) for n in ("dy", "r", "dres"))
-        self._w = {n: _Arg(n, weight_dtype, dev, contiguous=True) for n in ("gamma", "beta")}
-        self._st = {n: _Arg(n, torch.float32, dev, contiguous=True) for n in ("mean", "rstd")}
-        self._types = (B.DTYPES[dtype], B.DTYPES[weight_dtype])
-        self._fwd, self._bwd = B.lib().moe_layer_norm, B.lib().moe_layer_norm_bwd
+        self._gamma, self._beta = (_Arg(n, weight_dtype, dev, contiguous=True)
+                                   for n in ("gamma", "beta"))
+        self._amean, self._arstd = (_Arg(n, torch.float32, dev, contiguous=True)
+                                    for n in ("mean", "rstd"))
+        self._type, self._wtype = B.DTYPES[dtype], B.DTYPES[weight_dtype]
+        self._fwd, self._bwd = _entry("moe_layer_norm", dev), _entry("moe_layer_norm_bwd", dev)
 
     def forward(self, x, gamma, beta, res=None, stream=None):
         D = self.D
-        n = self._x.rows(x, self.rows, D)
-        shape = (n, D)
-        mx = self._x.matrix(x, shape)
-        pg, pb = self._w["gamma"].pointer(gamma, (D,)), self._w["beta"].pointer(beta, (D,))
+        n = self._x.first(x, self.rows, D)
+        pg, pb = self._gamma.pointer(gamma, self._width), self._beta.pointer(beta, self._width)
         whole = n == self.rows
         mres = mr = _NO
         r = x
         if res is not None:
-            mres = self._res.matrix(res, shape)
+            mres = self._res.matrix(res, (n, D))
             if self._r is None:
                 self._r = torch.empty_like(self._y)
                 self._mr = _own(self._r)
             r, mr = self._r if whole else self._r[:n], self._mr
-        _launchable(self.device)
-        st = self._fwd(mx, mres, pg, pb, mr, self._my, *self._p_stats, self.eps, n, D,
-                       *self._types, B.stream_of(stream, self.device))
+        st = self._fwd(self._x.mat, mres, pg, pb, mr, self._my, self._p_mean, self._p_rstd, self.eps,
+                       n, D, self._type, self._wtype, B.stream_of(stream, self.device))
         if st:
             _refused("moe_layer_norm", st)
         self.r = r
@@ -154,15 +176,13 @@ class LayerNorm:
         if mean is None or rstd is None:
             raise RuntimeError("backward needs a forward first, or its mean and rstd")
         D = self.D
-        n = self._dy.rows(dy, self.rows, D)
-        shape = (n, D)
-        mdy, mrin = self._dy.matrix(dy, shape), self._rin.matrix(r, shape)
-        pg = self._w["gamma"].pointer(gamma, (D,))
-        pm, ps = self._st["mean"].pointer(mean, (n,)), self._st["rstd"].pointer(rstd, (n,))
-        mres = _NO if dres is None else self._dres.matrix(dres, shape)
-        _launchable(self.device)
-        st = self._bwd(mdy, mrin, pg, pm, ps, mres, self._mdx, *self._p_grads, n, D, *self._types,
-                       B.stream_of(stream, self.device))
+        n = self._dy.first(dy, self.rows, D)
+        mrin = self._rin.matrix(r, (n, D))
+        pg = self._gamma.pointer(gamma, self._width)
+        pm, ps = self._amean.pointer(mean, (n,)), self._arstd.pointer(rstd, (n,))
+        mres = _NO if dres is None else self._dres.matrix(dres, (n, D))
+        st = self._bwd(self._dy.mat, mrin, pg, pm, ps, mres, self._mdx, self._p_dgamma, self._p_dbeta,
+                       self._p_ws, n, D, self._type, self._wtype, B.stream_of(stream, self.device))
         if st:
             _refused("moe_layer_norm_bwd", st)
         return self._dx if n == self.rows else self._dx[:n]
@@ -188,7 +208,8 @@ class TopKRouter:
         self._ids = torch.empty((T, K), dtype=torch.int32, device=dev)
         self._w = torch.empty((T, K), dtype=torch.float32, device=dev)
         self.device = dev = self._w.device
-        self._p_out = (self._ids.data_ptr(), self._w.data_ptr())
+        self._p_ids, self._p_w = self._ids.data_ptr(), self._w.data_ptr()
+        self._experts = (E,)
         self.ids = self.w = None
         if train:
             self._dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
@@ -198,15 +219,14 @@ class TopKRouter:
         self._b = _Arg("bias", f32, dev, contiguous=True)
         self._dw = _Arg("dw", f32, dev, contiguous=True)
         self._i = _Arg("ids", torch.int32, dev, contiguous=True)
-        self._fwd, self._bwd = B.lib().moe_route_topk, B.lib().moe_route_topk_bwd
+        self._fwd, self._bwd = _entry("moe_route_topk", dev), _entry("moe_route_topk_bwd", dev)
 
     def forward(self, logits, bias=None, stream=None):
         n = self._l.rows(logits, self.T, self.E)
         pl = self._l.pointer(logits, (n, self.E))
-        pb = None if bias is None else self._b.pointer(bias, (self.E,))
-        _launchable(self.device)
+        pb = None if bias is None else self._b.pointer(bias, self._experts)
         self.d.T = n
-        st = self._fwd(pl, pb, *self._p_out, self.d, B.stream_of(stream, self.device))
+        st = self._fwd(pl, pb, self._p_ids, self._p_w, self.d, B.stream_of(stream, self.device))
         if st:
             _refused("moe_route_topk", st)
         if n == self.T:
@@ -224,7 +244,6 @@ class TopKRouter:
         n = self._l.rows(logits, self.T, self.E)
         pl = self._l.pointer(logits, (n, self.E))
         pd, pi = self._dw.pointer(dw, (n, self.K)), self._i.pointer(ids, (n, self.K))
-        _launchable(self.device)
         self.d.T = n
         st = self._bwd(pl, pi, pd, self._p_dl, self.d, B.stream_of(stream, self.device))
         if st:
@@ -275,17 +294,16 @@ class Linear:
         self._b = _Arg("bias", torch.float32, dev, contiguous=True)
         self._res, self._dy = _Arg("res", out_dtype, dev), _Arg("dy", out_dtype, dev)
         self._zin, self._add = _Arg("z", dtype, dev), _Arg("dx_add", dtype, dev)
-        self._fwd, self._bwd = B.lib().moe_linear, B.lib().moe_linear_bwd
+        self._fwd, self._bwd = _entry("moe_linear", dev), _entry("moe_linear_bwd", dev)
+        self._wshape, self._bshape = (K, N), (N,)
 
     def forward(self, x, w, bias=None, res=None, stream=None):
-        K, N = self.K, self.N
-        n = self._x.rows(x, self.M, K)
-        mx, mw = self._x.matrix(x, (n, K)), self._w.matrix(w, (K, N))
-        pb = None if bias is None else self._b.pointer(bias, (N,))
-        mres = _NO if res is None else self._res.matrix(res, (n, N))
-        _launchable(self.device)
+        n = self._x.first(x, self.M, self.K)
+        mw = self._w.matrix(w, self._wshape)
+        pb = None if bias is None else self._b.pointer(bias, self._bshape)
+        mres = _NO if res is None else self._res.matrix(res, (n, self.N))
         self.d.M = n
-        st = self._fwd(mx, mw, pb, mres, self._my, self._mz, self._p_status, self.d,
+        st = self._fwd(self._x.mat, mw, pb, mres, self._my, self._mz, self._p_status, self.d,
                        B.stream_of(stream, self.device))
         if st:
             _refused("moe_linear", st)
@@ -299,9 +317,8 @@ class Linear:
         if not self.train:
             raise RuntimeError("the linear layer was built without train=True")
         K, N = self.K, self.N
-        n = self._x.rows(x, self.M, K)
-        mdy = self._dy.matrix(dy, (n, N))
-        mx, mw = self._x.matrix(x, (n, K)), self._w.matrix(w, (K, N))
+        n = self._x.first(x, self.M, K)
+        mdy, mw = self._dy.matrix(dy, (n, N)), self._w.matrix(w, self._wshape)
         mz = _NO
         if self.act != "none":
             z = self.z if z is None else z
@@ -309,9 +326,8 @@ class Linear:
                 raise RuntimeError("backward needs a forward first, or its z")
             mz = self._zin.matrix(z, (n, N))
         madd = _NO if dx_add is None else self._add.matrix(dx_add, (n, K))
-        _launchable(self.device)
         self.d.M = n
-        st = self._bwd(mdy, mz, mx, mw, madd, self._mdx if need_dx else _NO,
+        st = self._bwd(mdy, mz, self._x.mat, mw, madd, self._mdx if need_dx else _NO,
                        self._mdw if need_dw else _NO, self._p_db if need_db else None,
                        self._p_status, self._p_ws, self.d, B.stream_of(stream, self.device))
         if st:
