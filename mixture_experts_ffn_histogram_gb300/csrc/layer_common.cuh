@@ -178,8 +178,11 @@ struct Nums {
 
 // A kernel that a call launches behind another of its own may start before
 // that one has ended (its launch and set-up overlap the other's end); it waits
-// here before it touches global memory.  Returns at once in a kernel that was
-// launched without the attribute.
+// here before it touches global memory.  What the other wrote is read by
+// ordinary loads: __ldg and const __restrict__ pointers allow the read-only
+// path, which asks that the data stay unchanged for as long as the kernel is
+// resident.  Returns at once in a kernel that was launched without the
+// attribute.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The kernel behind this one may be launched once every block has come here.
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;"); }

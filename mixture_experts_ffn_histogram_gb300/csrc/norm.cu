@@ -681,11 +681,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
 
 // Column sums of partials [P][C]: 16 columns x 64 rows of threads per block,
 // each thread adding every 64th row, then the 64 partial sums in a fixed order.
+// The kernel may be resident while the one before it still writes `part`, so
+// the sums are read from L2 by ordinary loads (see wait_for_previous).
 constexpr int kJoinCols = 16, kJoinRows = 64;
 template <typename O>
 __global__ void __launch_bounds__(kJoinCols* kJoinRows)
-    join_partials_kernel(const float* __restrict__ part, int P, int64_t C, int64_t split, O* out0,
-                         O* out1) {
+    join_partials_kernel(const float* part, int P, int64_t C, int64_t split, O* out0, O* out1) {
   __shared__ float acc[kJoinRows][kJoinCols + 1];
   wait_for_previous();
   const int tx = threadIdx.x % kJoinCols, ty = threadIdx.x / kJoinCols;
@@ -693,7 +694,7 @@ __global__ void __launch_bounds__(kJoinCols* kJoinRows)
   float s = 0.0f;
   if (c < C) {
 #pragma unroll 8
-    for (int r = ty; r < P; r += kJoinRows) s += part[static_cast<int64_t>(r) * C + c];
+    for (int r = ty; r < P; r += kJoinRows) s += __ldcg(part + static_cast<int64_t>(r) * C + c);
   }
   acc[ty][tx] = s;
   __syncthreads();
