@@ -47,6 +47,7 @@
 #include "kernels.h"
 #include "layer.h"
 #include "layer_common.cuh"
+#include "tmem_share.h"
 
 namespace moe {
 namespace {
@@ -200,7 +201,37 @@ struct SplitShape {
   static constexpr int kLd = kColsOut + 4;
   static constexpr int kPartial = kRowsOut * kLd * 4;       // laid over the operand ring
   static_assert(!BMN || BN % 64 == 0, "MN-major operands come in 64-wide chunks");
+  // The fewest stages: what the partial tile needs, and so many that CTAs that
+  // fit an SM's shared memory together never ask for more than its 512
+  // tensor-memory columns, beside a kernel of CTA pairs or beside one another
+  // (tmem_share.h).
+  static constexpr int kOver = 1024 + static_cast<int>(sizeof(SplitCtl));
+  static constexpr int stages_of(int bytes) { return (bytes + kStage - 1) / kStage; }
+  static constexpr int kFloorBytes = static_cast<int>(kSmSmem) / (kSmTmemCols / kCols + 1) + 1024;
+  static constexpr int kBesidePair = static_cast<int>(kSmSmem - kLeastPairSmem - 2 * kBlockSmem) + 1 - kOver;
+  static constexpr int kLeast =
+      std::max({2, stages_of(kPartial), stages_of(kFloorBytes), stages_of(kBesidePair)});
+  static constexpr int kLeastBytes = kLeast * kStage + kOver;
+  static_assert(kLeast <= kSplitMaxStages && kLeastBytes <= kSplitSmemLimit, "shared memory");
+  static_assert(!fits_beside_pair(kLeastBytes), "a cluster's CTA must not fit beside a pair's");
 };
+
+// No mix of split CTAs that fits an SM's shared memory asks for more columns
+// than the SM has.
+constexpr bool split_mixes_fit() {
+  constexpr size_t b16 = SplitShape<16, false, false, true>::kLeastBytes + kBlockSmem;
+  constexpr size_t b32 = SplitShape<32, false, false, true>::kLeastBytes + kBlockSmem;
+  constexpr size_t b64 = std::min(SplitShape<64, false, false, true>::kLeastBytes,
+                                  SplitShape<64, true, true, false>::kLeastBytes) + kBlockSmem;
+  constexpr size_t b128 = SplitShape<128, false, false, false>::kLeastBytes + kBlockSmem;
+  for (size_t i = 0; i * b16 <= kSmSmem; ++i)
+    for (size_t j = 0; i * b16 + j * b32 <= kSmSmem; ++j)
+      for (size_t k = 0; i * b16 + j * b32 + k * b64 <= kSmSmem; ++k)
+        for (size_t l = 0; i * b16 + j * b32 + k * b64 + l * b128 <= kSmSmem; ++l)
+          if (32 * i + 64 * j + 128 * k + 256 * l > kSmTmemCols) return false;
+  return true;
+}
+static_assert(split_mixes_fit(), "split clusters must not wait for each other's columns");
 
 // A CTA's part of a finished tile: rows [r0, r1) of the partial tile that lies
 // in shared memory at `ring`, the output's rows from row0 + r0 on.
@@ -522,6 +553,7 @@ struct PairCtl {
 constexpr size_t kPairSmem = 1024 + static_cast<size_t>(kPairStages) * kPairStage +
                              kPairEpiWarps * kPairBuf + sizeof(PairCtl);
 static_assert(kPairSmem <= 227 * 1024, "shared memory");
+static_assert(kPairSmem >= kLeastPairSmem, "clusters of other kernels must not fit beside");
 
 struct PairParams {
   const float* bias;
@@ -959,26 +991,17 @@ cudaError_t launch_split(const DenseCall& c, int splits, cudaStream_t s) {
                   (S::BMN ? map2d(&mb, b, nb, c.Kred, ldb, 64, kBlockK)
                           : map2d(&mb, b, c.Kred, nb, ldb, kBlockK, S::BN));
   if (!ok) return cudaErrorInvalidValue;
-  // no more stages than reduction blocks, no fewer than the partial tile
-  // needs, and so many that CTAs that fit an SM's shared memory together never
-  // ask for more than its 512 tensor-memory columns: clusters that overlap
-  // (on two streams) would otherwise wait for each other's columns.  The
-  // smallest CTA takes 38 KB, which is not left beside the pair kernel's.
-  constexpr int kFloorBytes = 228 * 1024 / (512 / S::kCols + 1) + 1024;
-  constexpr int kLeast =
-      std::max({2, (S::kPartial + S::kStage - 1) / S::kStage, (kFloorBytes + S::kStage - 1) / S::kStage});
-  constexpr int kOver = 1024 + static_cast<int>(sizeof(SplitCtl));
-  static_assert(kLeast <= kSplitMaxStages && kLeast * S::kStage + kOver <= kSplitSmemLimit, "shared memory");
+  // No more stages than reduction blocks.
   // All of an SM's shared memory where every cluster finds SMs of its own: six
   // 32 KB stages instead of three keep a lone CTA's operands coming (8191 x
   // 7168 -> 256: 33.5 us, 48 with three; 203 x 5224 -> 3904 in two splits 19.3
   // and 25.2).  Otherwise two CTAs to an SM, one's epilogue behind the other's
   // products.
   const bool alone = cdiv(na, kTileM) * cdiv(nb, S::BN) <= lone_clusters(splits);
-  const int budget = (alone ? kSplitSmemLimit : kSplitSmemLimit / 2) - kOver - 1024;
+  const int budget = (alone ? kSplitSmemLimit : kSplitSmemLimit / 2) - S::kOver - 1024;
   const int mine = static_cast<int>(cdiv(p.kblocks, splits));
-  const int stages = std::max(kLeast, std::min({budget / S::kStage, kSplitMaxStages, mine}));
-  const size_t bytes = static_cast<size_t>(stages) * S::kStage + kOver;
+  const int stages = std::max(S::kLeast, std::min({budget / S::kStage, kSplitMaxStages, mine}));
+  const size_t bytes = static_cast<size_t>(stages) * S::kStage + S::kOver;
   const int chunk = c.out_type == MOE_FP32 ? kChunkBlocks : p.kblocks;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];

@@ -51,6 +51,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tmem_share.h"
 
 namespace moe {
 namespace {
@@ -131,6 +132,7 @@ struct Shape {
   static_assert(ZB_ == 0 || ZB_ == 2, "z slots");
   static_assert(ZW_ == 64 || ZW_ == 32, "z chunk width");
   static_assert(kSmemBytes <= kSmemLimit, "shared memory");
+  static_assert(CG == 1 || kSmemBytes >= kLeastPairSmem, "clusters of other kernels must not fit beside");
 };
 
 struct Params {
