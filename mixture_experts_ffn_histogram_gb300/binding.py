@@ -188,6 +188,7 @@ def _p(t):
 
 # the current stream of a device as an integer, without building a Stream object
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _s(stream):
@@ -199,8 +200,12 @@ def _s(stream):
 
 
 def stream_of(stream, device) -> int:
-    """The stream of a call: the given one (a Stream or its integer), or the
-    device's current one."""
+    """The stream of a call on `device`: the given one (a Stream or its
+    integer), or the device's current one.  A launch goes to the thread's
+    current device whatever its pointers are, so that has to be `device`."""
+    if device.type == "cuda" and _current_device() != device.index:
+        raise RuntimeError(f"the call's tensors are on {device}, which is not the current device "
+                           f"(cuda:{_current_device()}): make it so with torch.cuda.device")
     if stream is None:
         if _raw_stream is not None:
             return _raw_stream(device.index)

@@ -5,7 +5,8 @@ selection with a balance bias and expert groups) and ``Linear`` (bias,
 activation and residual in the product's epilogue) each own their output
 buffers and workspace, like ``MoEBlock``: allocated once for a largest number
 of rows, written by every call (a call's outputs are views of them and hold
-until the next one).  Calls run on the current stream, or the one given.
+until the next one).  Calls run on the current stream, or the one given, of
+the device that the operator was built on, which has to be the current one.
 
 ``MoELayer`` runs them together with the expert block as one pre-norm
 feed-forward layer, forward and backward.
