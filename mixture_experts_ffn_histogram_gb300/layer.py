@@ -120,9 +120,10 @@ class LayerNorm:
         dev = torch.device(device)
         self._y = torch.empty((rows, D), dtype=dtype, device=dev)
         self.device = dev = self._y.device
-        self._r = None
+        self._r = torch.empty_like(self._y)
         self.r = self.mean = self.rstd = None
-        self._my, self._p_mean, self._p_rstd = _own(self._y), None, None
+        self._my, self._mr = _own(self._y), _own(self._r)
+        self._p_mean = self._p_rstd = None
         self._width = (D,)
         if train:
             self._stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
@@ -154,9 +155,6 @@ class LayerNorm:
         r = x
         if res is not None:
             mres = self._res.matrix(res, (n, D))
-            if self._r is None:
-                self._r = torch.empty_like(self._y)
-                self._mr = _own(self._r)
             r, mr = self._r if whole else self._r[:n], self._mr
         st = self._fwd(self._x.mat, mres, pg, pb, mr, self._my, self._p_mean, self._p_rstd, self.eps,
                        n, D, self._type, self._wtype, B.stream_of(stream, self.device))

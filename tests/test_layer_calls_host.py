@@ -29,17 +29,19 @@ def _stand_in(op, launched):
 
 
 def _calls():
-    g = t(64, dtype=F32)
+    """(operator, a call of it) for each operator and direction."""
+    g, st, l = t(64, dtype=F32), t(8, dtype=F32), t(8, 16, dtype=F32)
+    x, y, w = t(8, 64), t(8, 128), t(64, 128)
+    dw, ids = t(8, 2, dtype=F32), t(8, 2, dtype=torch.int32)
     norm, router = LayerNorm(8, 64, device="cpu"), TopKRouter(8, 16, 2, train=True, device="cpu")
     lin = Linear(8, 64, 128, train=True, device="cpu")
-    st, l = t(8, dtype=F32), t(8, 16, dtype=F32)
     return [
-        (norm, lambda **k: norm.forward(t(8, 64), g, g, res=t(8, 64), **k)),
-        (norm, lambda **k: norm.backward(t(8, 64), t(8, 64), g, mean=st, rstd=st, **k)),
+        (norm, lambda **k: norm.forward(x, g, g, res=x, **k)),
+        (norm, lambda **k: norm.backward(x, x, g, mean=st, rstd=st, **k)),
         (router, lambda **k: router.forward(l, **k)),
-        (router, lambda **k: router.backward(t(8, 2, dtype=F32), l, ids=t(8, 2, dtype=torch.int32), **k)),
-        (lin, lambda **k: lin.forward(t(8, 64), t(64, 128), **k)),
-        (lin, lambda **k: lin.backward(t(8, 128), t(8, 64), t(64, 128), **k)),
+        (router, lambda **k: router.backward(dw, l, ids=ids, **k)),
+        (lin, lambda **k: lin.forward(x, w, **k)),
+        (lin, lambda **k: lin.backward(y, x, w, **k)),
     ]
 
 
@@ -57,3 +59,18 @@ def test_another_current_device_is_refused(monkeypatch, which, stream):
     monkeypatch.setattr(B, "_current_device", lambda: 0)
     call(**stream)
     assert len(launched) == 1
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_calls_allocate_no_memory(monkeypatch, which):
+    """A buffer allocated in a call would come from the current stream's
+    memory, which that stream may still use, and be written on the call's."""
+    op, call = _calls()[which]
+    _stand_in(op, [])
+
+    def no(*args, **kw):
+        raise AssertionError("an allocation in a call")
+
+    for name in ("empty", "empty_like", "zeros", "zeros_like", "full"):
+        monkeypatch.setattr(torch, name, no)
+    call(stream=0)
