@@ -235,6 +235,14 @@ __device__ __forceinline__ float score_error(float s, float l, float m) {
   return SOFTMAX ? s * (3e-6f + 2e-7f * fmaxf(m - l, 0.0f)) : s * (6e-7f + 1.5e-7f * fmaxf(-l, 0.0f));
 }
 constexpr float kSumError = 1.2e-7f;  // of the rounded sum s + bias, relative
+// Of a group's score, the sum of its best two t1 and t2 (or t1 alone): the
+// scores' own errors, their sums with the biases rounded at |t1| and |t2|, and
+// the last sum.  The terms count, not their sum, which may be far smaller
+// (biases of opposite sign).
+__device__ __forceinline__ float group_error(float t1, float t2, int group_top, float worst) {
+  const float a = t1 > kNegInf ? fabsf(t1) : 0.0f, b = group_top == 2 && t2 > kNegInf ? fabsf(t2) : 0.0f;
+  return 2.0f * worst + (kSumError * a + kSumError * b);
+}
 // Largest score_error of any logit: (1 - s) is folded in for the sigmoid, and
 // s e^-x x <= 0.37 for the softmax, relative to the row's largest score.
 template <bool SOFTMAX>
@@ -361,21 +369,23 @@ struct WarpToken {
       }
       // the score of group `lane`
       const float score = __shfl_sync(kAll, group_score(t1, t2, d.group_top), (lane * lpg) & 31);
-      uint32_t gkey = lane < d.groups ? order_key(score) : 0u, last = 0u;
+      uint32_t gkey = lane < d.groups ? order_key(score) : 0u;
       stay = 0u;
       for (int g = 0; g < d.top_groups; ++g) {
-        last = __reduce_max_sync(kAll, gkey);
+        const uint32_t last = __reduce_max_sync(kAll, gkey);
         const int src = __ffs(__ballot_sync(kAll, gkey == last)) - 1;
         stay |= 1u << src;
         if (lane == src) gkey = 0u;
       }
       if (biased || by_s) {
-        const float in = key_value(last), next = key_value(__reduce_max_sync(kAll, gkey));
-        const float err = 4.0f * worst + 2.0f * kSumError * (fabsf(in) + fabsf(next));  // both sides
-        if (next > kNegInf && in - next <= err) {
-          // every group that may lie on either side of the border
-          const uint32_t band = __ballot_sync(
-              kAll, lane < d.groups && score <= next + 2.0f * err && score >= in - 2.0f * err);
+        // the groups taken, each at its least, against those left, each at its
+        // most; those that do not clear the other side are taken again in fp64
+        const float err = __shfl_sync(kAll, group_error(t1, t2, d.group_top, worst), (lane * lpg) & 31);
+        const bool taken = (stay >> lane) & 1u, left = lane < d.groups && !taken;
+        const float least = -warp_max_f32(taken ? err - score : kNegInf);
+        const float most = warp_max_f32(left ? score + err : kNegInf);
+        if (most > kNegInf && least <= most) {
+          const uint32_t band = __ballot_sync(kAll, taken ? score - err <= most : left && score + err >= least);
           const uint32_t sure = stay & ~band;
           stay = sure | groups_fp64<SOFTMAX>(row, p.bias, d, band, d.top_groups - __popc(sure), lane);
         }
@@ -746,16 +756,17 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
       }
       bool stays = group < d.groups && ahead < d.top_groups;
       if (biased || by_s) {
-        const float in = -sub_max<LANES>(stays ? -score : kNegInf);
-        const float next = sub_max<LANES>(!stays && group < d.groups ? score : kNegInf);
-        const float err = 4.0f * worst + 2.0f * kSumError * (fabsf(in) + fabsf(next));
-        const bool near = real && next > kNegInf && in - next <= err;
+        const bool left_out = group < d.groups && !stays;
+        const float gerr = group_error(t1, t2, d.group_top, worst);
+        const float least = -sub_max<LANES>(stays ? gerr - score : kNegInf);
+        const float most = sub_max<LANES>(left_out ? score + gerr : kNegInf);
+        const bool near = real && most > kNegInf && least <= most;
         uint32_t left = __ballot_sync(kAll, near);
         while (left != 0) {  // a token at a time, by the whole warp
           const int q = (__ffs(left) - 1) / LANES;
           left &= ~(kTokenMask << (q * LANES));
           const bool mineq = tok == q && group < d.groups;
-          const bool in_band = mineq && score <= next + 2.0f * err && score >= in - 2.0f * err;
+          const bool in_band = mineq && (stays ? score - gerr <= most : score + gerr >= least);
           const uint32_t band = __reduce_or_sync(kAll, in_band ? 1u << group : 0u);
           const uint32_t sure = __reduce_or_sync(kAll, mineq && stays && !in_band ? 1u << group : 0u);
           const uint32_t stay = sure | groups_fp64<SOFTMAX>(p.logits + (base + q) * E, p.bias, d, band,
