@@ -26,6 +26,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "kernels.h"
 #include "layer.h"
@@ -68,9 +69,13 @@ __device__ __forceinline__ void merge_top2(float& a1, float& a2, float b1, float
 }
 // A group's score from its two best: masked experts (-inf) add nothing to
 // one that has others.
-template <typename F>
-__device__ __forceinline__ F group_score(F t1, F t2, int group_top) {
-  return (group_top == 2 && t2 > static_cast<F>(kNegInf)) ? t1 + t2 : t1;
+__device__ __forceinline__ double group_score(double t1, double t2, int group_top) {
+  return (group_top == 2 && t2 > static_cast<double>(kNegInf)) ? t1 + t2 : t1;
+}
+// The same in fp32, where a sum past the largest number stays ahead of a group
+// whose experts are all masked (its error, see group_error, covers the rest).
+__device__ __forceinline__ float group_score(float t1, float t2, int group_top) {
+  return (group_top == 2 && t2 > kNegInf) ? fminf(fmaxf(t1 + t2, -FLT_MAX), FLT_MAX) : t1;
 }
 
 // e^(l - m), with the limit at l = m = +inf and 0 for a masked logit.

@@ -28,3 +28,21 @@ def test_groups_under_biases_of_opposite_sign(gate, T, E, K, groups, top_groups,
     b = np.full(E, -size, dtype=np.float32)
     b[rng.integers(0, E // groups, groups) + np.arange(groups) * (E // groups)] = size
     _check(l, b, K, gate, groups, top_groups, 2, True, 1.0)
+
+
+@pytest.mark.parametrize("T", [300, 5003])
+def test_groups_under_the_lowest_bias(T):
+    """Experts switched off by the lowest finite bias stay ahead of masked
+    ones, and their group (whose sum is past the lowest number) ahead of a
+    masked group."""
+    need_gpu()
+    rng = np.random.default_rng(T)
+    E, low = 64, np.finfo(np.float32).min
+    b = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    b[8:16] = low                            # group 1: all off
+    b[17:24] = low                           # group 2: one left
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l[:, :8] = -np.inf                       # group 0: masked
+    l[:, 27:] = -np.inf                      # ... and all but three of the rest
+    for top_groups in (2, 3, 4):
+        _check(l, b, 8, "sigmoid", 8, top_groups, 2, True, 1.0)
