@@ -18,8 +18,8 @@
 //
 // The selection compares fp32 scores, which a rounding can swap.  Each
 // comparison that decides something is therefore checked against the error
-// bounds of its two sides: neighbours in the sorted list up to the first
-// expert left out, and the groups on both sides of the last one taken.
+// bounds of its two sides: neighbours in the sorted list, the last expert
+// taken and every one left out, the groups taken and those left.
 // Where they lie too near, those experts (one per lane) or those groups are
 // evaluated again in fp64.  With scores spread as in training this happens
 // to a token in some thousands.
@@ -255,6 +255,26 @@ __device__ __forceinline__ float worst_error(float largest) {
   return SOFTMAX ? 3.1e-6f * largest : 6.5e-7f;
 }
 
+// Of the score v = s + bias of an expert with logit l.
+template <bool SOFTMAX>
+__device__ __forceinline__ float value_error(float v, float bias, float l, float m) {
+  return v > kNegInf ? score_error<SOFTMAX>(v - bias, l, m) + 2.0f * kSumError * fabsf(v) : 0.0f;
+}
+
+// Whether a list of n candidates, sorted by v over the lanes, may be out of
+// order as far as its first K: each of those against the next, and each one
+// left out against the last one taken (one further down may have a larger
+// error than the first).  Equal logits under equal biases are equal in fp64.
+template <bool SOFTMAX>
+__device__ __forceinline__ bool unsure_order(float v, float bias, float l, float m, int n, int K, int lane) {
+  const float err = value_error<SOFTMAX>(v, bias, l, m);
+  const int other = lane < K - 1 ? lane + 1 : K - 1;
+  const float o_v = __shfl_sync(kAll, v, other), o_b = __shfl_sync(kAll, bias, other);
+  const float o_l = __shfl_sync(kAll, l, other), o_err = __shfl_sync(kAll, err, other);
+  const bool unsure = lane < n && lane != K - 1 && fabsf(v - o_v) <= err + o_err && !(l == o_l && bias == o_b);
+  return __any_sync(kAll, unsure);
+}
+
 // One token by a whole warp.  vpl: experts a lane holds at most (<= VPL); lpg:
 // lanes of a group; cand: room for 32 (value, id) candidates.
 template <int VPL, bool SOFTMAX>
@@ -465,16 +485,9 @@ struct WarpToken {
         id = __float_as_int(c.y);
       }
       if (biased) {
-        // lane r against the next of the list
         const float bs = lane < n ? __ldg(p.bias + id) : 0.0f;
         const float lo = lane < n ? clean(__ldg(row + id)) : kNegInf;
-        const float o_v = __shfl_down_sync(kAll, v, 1), o_b = __shfl_down_sync(kAll, bs, 1);
-        const float o_l = __shfl_down_sync(kAll, lo, 1);
-        const float s = v - bs, o_s = o_v - o_b;  // the scores, up to the rounded sum
-        const float err = score_error<SOFTMAX>(s, lo, m) + score_error<SOFTMAX>(o_s, o_l, m) +
-                          2.0f * kSumError * (fabsf(v) + fabsf(o_v));
-        const bool unsure = lane < K && lane + 1 < n && v - o_v <= err && !(lo == o_l && bs == o_b);
-        if (__any_sync(kAll, unsure)) {
+        if (unsure_order<SOFTMAX>(v, bs, lo, m, n, K, lane)) {
           rank = rank_fp64<SOFTMAX>(row, p.bias, E, id, lo, n, lane);
           if (lane < n) cand[rank] = make_float2(v, __int_as_float(id));
           __syncwarp();
@@ -516,20 +529,23 @@ struct WarpToken {
         }
       }
       if (biased) {
-        const uint32_t next = __reduce_max_sync(kAll, ktop);  // the first expert left out
-        const int next_id = next != 0u ? take(next) : 0;
-        const float v = key_value(my_key), bs = lane < K ? __ldg(p.bias + my_id) : 0.0f;
+        const float v = lane < K ? key_value(my_key) : kNegInf, bs = lane < K ? __ldg(p.bias + my_id) : 0.0f;
         const float lo = lane < K ? clean(__ldg(row + my_id)) : kNegInf;
-        float o_v = __shfl_down_sync(kAll, v, 1), o_b = __shfl_down_sync(kAll, bs, 1);
-        float o_l = __shfl_down_sync(kAll, lo, 1);
-        if (lane == K - 1) {
-          o_v = next != 0u ? key_value(next) : kNegInf;
-          o_b = next != 0u ? __ldg(p.bias + next_id) : 0.0f;
-          o_l = next != 0u ? clean(__ldg(row + next_id)) : kNegInf;
+        bool unsure = unsure_order<SOFTMAX>(v, bs, lo, m, K, K, lane);
+        // the last one taken against every expert that is left
+        const float last = __shfl_sync(kAll, v, K - 1), last_b = __shfl_sync(kAll, bs, K - 1);
+        const float last_l = __shfl_sync(kAll, lo, K - 1);
+        const float reach = worst + value_error<SOFTMAX>(last, last_b, last_l, m);
+        uint32_t near = 0u;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          const float f = key_value(key[i]);
+          if (key[i] != 0u && f > kNegInf && last - f <= reach + 2.0f * kSumError * fabsf(f)) near |= 1u << i;
         }
-        const float err = score_error<SOFTMAX>(v - bs, lo, m) + score_error<SOFTMAX>(o_v - o_b, o_l, m) +
-                          2.0f * kSumError * (fabsf(v) + fabsf(o_v));
-        const bool unsure = lane < K && o_v > kNegInf && v - o_v <= err && !(lo == o_l && bs == o_b);
+        for (; near != 0u; near &= near - 1u) {
+          const int e = first + __ffs(near) - 1;
+          unsure = unsure || !(clean(__ldg(row + e)) == last_l && __ldg(p.bias + e) == last_b);
+        }
         if (__any_sync(kAll, unsure))
           my_id = select_fp64<VPL, SOFTMAX>(row, p.bias, d, first, mine, stay, lane);
       }
@@ -609,8 +625,8 @@ __device__ __noinline__ void whole_warp_token(const TopkArgs& p, float2* cand, i
   w.run(t, l, b);
 }
 
-// The order of a token's n sorted candidates, checked pair by pair against
-// the bounds of their scores and redone in fp64 where one fails.  Whole warp.
+// The order of a token's n sorted candidates, checked against the bounds of
+// their scores and redone in fp64 where that fails.  Whole warp.
 template <bool SOFTMAX>
 __device__ __noinline__ void settle_order(const float* row, const float* bias, int E, int K, float2* cand,
                                           int n, float m, int lane) {
@@ -622,12 +638,7 @@ __device__ __noinline__ void settle_order(const float* row, const float* bias, i
     bs = __ldg(bias + id);
     lo = clean(__ldg(row + id));
   }
-  const float o_v = __shfl_down_sync(kAll, v, 1), o_b = __shfl_down_sync(kAll, bs, 1);
-  const float o_l = __shfl_down_sync(kAll, lo, 1);
-  const float err = score_error<SOFTMAX>(v - bs, lo, m) + score_error<SOFTMAX>(o_v - o_b, o_l, m) +
-                    2.0f * kSumError * (fabsf(v) + fabsf(o_v));
-  const bool unsure = lane < K && lane + 1 < n && v - o_v <= err && !(lo == o_l && bs == o_b);
-  if (!__any_sync(kAll, unsure)) return;
+  if (!unsure_order<SOFTMAX>(v, bs, lo, m, n, K, lane)) return;
   const int rank = rank_fp64<SOFTMAX>(row, bias, E, id, lo, n, lane);
   __syncwarp();
   if (lane < n) cand[rank] = make_float2(v, __int_as_float(id));
