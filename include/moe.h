@@ -603,7 +603,8 @@ typedef struct {
  *   a group's score is the sum of its group_top best sel (of s when bias is
  *   NULL and group_top = 2); the top_groups best groups stay
  *   ids = the K largest sel of the groups that stay, in descending order
- *   w_k = scale * s[ids_k]  (/ sum_k s[ids_k] with renorm; 0 when that is 0)
+ *   w_k = scale * s[ids_k]  (/ sum_k s[ids_k] with renorm; 0 when that is 0).
+ *           The shares hold where the scores are too small for fp32.
  * Ties go to the lowest expert id (the lowest group).  ids are those of the
  * scores' real values to 64-bit rounding: where two fp32 scores lie too near
  * to be told apart, the token is selected again in fp64.  A logit of -inf (or

@@ -83,6 +83,22 @@ __device__ __forceinline__ float soft_num(float l, float m) {
   return l == kNegInf ? 0.0f : (l == m ? 1.0f : expf(l - m));
 }
 
+// A token's weights are shares of its K scores, which may all lie below what
+// fp32 holds.  Where none of the chosen logits lies within kDeep of `base` (0
+// for the sigmoid, the row's largest logit for the softmax), the scores are
+// taken relative to the largest chosen one instead, which leaves the shares as
+// they are.
+constexpr float kDeep = 64.0f;
+__device__ __forceinline__ bool shallow(float l, float base) { return l - base >= -kDeep || l == base; }
+__device__ __forceinline__ float deep_base(float most, float base) {
+  return most > kNegInf && base < INFINITY ? most : base;
+}
+// sigmoid(l) e^-base, base being 0 or below -kDeep (there the sigmoid is e^l to
+// fp32's precision, down to the smallest numbers).
+__device__ __forceinline__ float sigmoid_num(float l, float base) {
+  return l < -kDeep ? expf(l - base) : 1.0f / (1.0f + expf(-l));
+}
+
 // Largest value over the warp, in one instruction (no NaN among them).
 __device__ __forceinline__ float warp_max_f32(float v) {
   float r;
@@ -551,10 +567,12 @@ struct WarpToken {
       }
     }
     const float my_l = lane < K ? clean(__ldg(row + my_id)) : kNegInf;
-    float s = 0.0f;
+    float s = 0.0f, base = m;  // (m is 0 for the sigmoid)
+    if (d.renorm && __ballot_sync(kAll, lane < K && shallow(my_l, base)) == 0u)
+      base = deep_base(warp_max_f32(my_l), base);
     if (lane < K) {
-      if constexpr (SOFTMAX) s = soft_num(my_l, m);
-      else s = 1.0f / (1.0f + expf(-my_l));
+      if constexpr (SOFTMAX) s = soft_num(my_l, base);
+      else s = sigmoid_num(my_l, base);
     }
     if (d.renorm) {
       const float total = warp_sum(s);
@@ -882,10 +900,20 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
     const bool slot = good && r < K;
     const int my_id = slot ? __float_as_int(cand[r].y) : 0;
     const float my_l = slot ? clean(__ldg(row + my_id)) : kNegInf;
-    float s = 0.0f;
+    float s = 0.0f, base_l = m;  // (m is 0 for the sigmoid)
+    if (d.renorm) {
+      const uint32_t some = __ballot_sync(kAll, slot && shallow(my_l, base_l));
+      bool all = true;
+#pragma unroll
+      for (int q = 0; q < kTokens; ++q) all = all && ((some >> (q * LANES)) & kTokenMask) != 0u;
+      if (!all) {
+        const float most = sub_max<LANES>(my_l);
+        if (((some >> (tok * LANES)) & kTokenMask) == 0u) base_l = deep_base(most, base_l);
+      }
+    }
     if (slot) {
-      if constexpr (SOFTMAX) s = soft_num(my_l, m);
-      else s = 1.0f / (1.0f + expf(-my_l));
+      if constexpr (SOFTMAX) s = soft_num(my_l, base_l);
+      else s = sigmoid_num(my_l, base_l);
     }
     if (d.renorm) {
       const float total = sub_sum<LANES>(s);
@@ -1002,13 +1030,18 @@ __global__ void __launch_bounds__(32 * kTopkWarps) route_topk_bwd_kernel(const T
       const float q = total > 0.0f ? e / total : 0.0f;
       value = q * (g - warp_sum(g * q));
     } else {
-      const float s = 1.0f / (1.0f + expf(-l));
-      float ds = g;
+      float top = 0.0f;
+      if (d.renorm && __ballot_sync(kAll, shallow(l, top)) == 0u) top = deep_base(warp_max_f32(l), top);
+      const float s = sigmoid_num(l, top);
       if (d.renorm) {
-        const float total = warp_sum(s), dot = warp_sum(g * s);
-        ds = total > 0.0f ? (g - dot / total) / total : 0.0f;
+        const float total = warp_sum(s);
+        const float q = total > 0.0f ? s / total : 0.0f;
+        const float dot = warp_sum(g * q);
+        value = total > 0.0f ? q * (g - dot) : 0.0f;
+      } else {
+        value = g * s;
       }
-      value = ds * s * (1.0f / (1.0f + expf(l)));  // 1 - s without cancellation
+      value *= 1.0f / (1.0f + expf(l));  // 1 - s without cancellation
     }
     if (vec) {
 #pragma unroll
