@@ -41,7 +41,7 @@ constexpr float kGeluB = 0.044715f;
 template <bool EXACT>
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
-    case MOE_ACT_RELU: return z > 0.0f ? z : 0.0f;
+    case MOE_ACT_RELU: return z <= 0.0f ? 0.0f : z;  // NaN passes
     case MOE_ACT_GELU: return z * normal_cdf<EXACT>(z).x;
     case MOE_ACT_GELU_TANH:  // (1 + tanh u) / 2 = sigmoid(2 u)
       return z * act_sigmoid<EXACT>(kGeluA * z * (1.0f + kGeluB * z * z));
@@ -70,7 +70,7 @@ __device__ __forceinline__ void act_all(float* v, int act) {
 template <bool EXACT>
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
-    case MOE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case MOE_ACT_RELU: return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
     case MOE_ACT_GELU: {
       const float2 c = normal_cdf<EXACT>(z);
       return c.x + 0.3989422804f * z * c.y;
