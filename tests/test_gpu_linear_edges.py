@@ -29,3 +29,30 @@ def test_a_nan_row_stays_nan(name, M, dt, out):
     dx = op.backward(torch.randn(M, N, generator=g).to(out).cuda(), x, w)
     assert torch.equal(torch.isnan(dx), rows[:, None].expand(M, K))
     assert bool(torch.isnan(op.db).all())
+
+
+@pytest.mark.parametrize("dt,low", [(BF, -13.0), (HF, -5.8)])
+def test_the_tail_of_gelu(dt, low):
+    """Value and slope far below zero, where both are tiny: to half a step of
+    the result.  (About the slope's zero at -0.75 an absolute bound holds.)"""
+    need_gpu()
+    from mixture_experts_ffn_histogram_gb300.layer import Linear
+    n = 64
+    x = torch.linspace(low, -1.5, 64 * n).to(dt).view(-1, n).cuda()
+    w = torch.eye(n).to(dt).cuda()
+    op = Linear(x.shape[0], n, n, dt, act="gelu", train=True)
+    y = op.forward(x, w)
+    assert torch.equal(op.z, x)
+    dx = op.backward(torch.ones_like(x), x, w)
+    z = x.double()
+    cdf = 0.5 * torch.erfc(-z / 2 ** 0.5)
+    pdf = torch.exp(-z * z / 2) / (2 * torch.pi) ** 0.5
+    # the tail's polynomial, some ten roundings, the exponential's argument
+    # (z^2/2 log2 e, 1.5 roundings of it), and the result's own rounding
+    own = 2.0 ** -17 + 10 * 2.0 ** -24 + 1.5 * z * z * 2.0 ** -24
+    half = torch.finfo(dt).eps / 2 * (1 + 2.0 ** -8)
+    sub = torch.finfo(dt).smallest_normal * torch.finfo(dt).eps / 2
+    for name, got, want, mag in (("gelu", y, z * cdf, z.abs() * cdf),
+                                 ("slope", dx, cdf + z * pdf, cdf + z.abs() * pdf)):
+        off = (got.double() - want).abs() - (half * want.abs() + sub + own * mag)
+        assert float(off.max()) <= 0, f"{name}: at z = {float(z.flatten()[off.flatten().argmax()])}"
