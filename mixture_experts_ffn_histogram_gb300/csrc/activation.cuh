@@ -86,7 +86,8 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     }
     case MOE_ACT_GELU_TANH: {
       const float s = act_sigmoid<EXACT>(kGeluA * z * (1.0f + kGeluB * z * z));
-      return s + z * s * (1.0f - s) * kGeluA * (1.0f + 3.0f * kGeluB * z * z);
+      const float d = s * (1.0f - s);  // 0 long before z * z overflows
+      return d > 0.0f ? s + z * d * kGeluA * (1.0f + 3.0f * kGeluB * z * z) : s;
     }
     case MOE_ACT_SILU: {
       const float s = act_sigmoid<EXACT>(z);

@@ -56,3 +56,26 @@ def test_the_tail_of_gelu(dt, low):
                                  ("slope", dx, cdf + z * pdf, cdf + z.abs() * pdf)):
         off = (got.double() - want).abs() - (half * want.abs() + sub + own * mag)
         assert float(off.max()) <= 0, f"{name}: at z = {float(z.flatten()[off.flatten().argmax()])}"
+
+
+@pytest.mark.parametrize("name", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_the_largest_numbers(name, dt):
+    """act(z) = z and act'(z) = 1 far above zero, 0 and 0 far below, up to the
+    type's largest and lowest number."""
+    need_gpu()
+    from mixture_experts_ffn_histogram_gb300.layer import Linear
+    n, most = 64, torch.finfo(dt).max
+    x = torch.logspace(2.4, torch.tensor(most).double().log10().item(), 4 * n, dtype=torch.float64).clamp(max=most)
+    x = torch.cat([x, -x]).to(dt).view(-1, n).cuda()
+    w = torch.eye(n).to(dt).cuda()
+    op = Linear(x.shape[0], n, n, dt, act=name, train=True)
+    y = op.forward(x, w)
+    up = x > 0 if name != "none" else torch.ones_like(x, dtype=torch.bool)
+    assert torch.equal(y, torch.where(up, x, torch.zeros_like(x)))
+    if name == "none":
+        return
+    assert torch.equal(op.z, x)
+    dx = op.backward(torch.ones_like(x), x, w, need_dw=False)
+    assert torch.equal(dx, up.to(dt))
+    assert torch.equal(op.db, up.float().sum(0))
