@@ -271,10 +271,11 @@ __device__ __forceinline__ float worst_error(float largest) {
   return SOFTMAX ? 3.1e-6f * largest : 6.5e-7f;
 }
 
-// Of the score v = s + bias of an expert with logit l.
+// Of the score v = s + bias of an expert with logit l; a fast score below
+// 2^-126 is 0.
 template <bool SOFTMAX>
 __device__ __forceinline__ float value_error(float v, float bias, float l, float m) {
-  return v > kNegInf ? score_error<SOFTMAX>(v - bias, l, m) + 2.0f * kSumError * fabsf(v) : 0.0f;
+  return v > kNegInf ? score_error<SOFTMAX>(v - bias, l, m) + (2.0f * kSumError * fabsf(v) + 1.2e-38f) : 0.0f;
 }
 
 // Whether a list of n candidates, sorted by v over the lanes, may be out of

@@ -104,3 +104,19 @@ def test_many_equal_experts():
         l[1::3, 3] = np.float32(-2.0 ** -23)
         _check(l, b, 8, "sigmoid", 1, 1, 1, True, 1.0)
         _check(l, b, 8, "softmax", 1, 1, 1, True, 1.0)
+
+
+@pytest.mark.parametrize("gate", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T", [300, 5003])
+def test_scores_that_fp32_flushes(gate, T):
+    """A score just below 2^-126 beside one just above, under biases as small."""
+    need_gpu()
+    rng = np.random.default_rng(T)
+    l = np.full((T, 16), -120.0, dtype=np.float32)
+    b = np.zeros(16, dtype=np.float32)
+    l[:, 2] = rng.uniform(-87.6, -87.4, T)
+    l[:, 7] = rng.uniform(-87.2, -87.1, T)
+    b[2] = 8e-39
+    if gate == "softmax":
+        l[:, 5], b[5] = 0.0, -3.0
+    _check(l, b, 1, gate, 1, 1, 1, False, 1e30)
