@@ -247,7 +247,14 @@ __device__ __forceinline__ void pop4(float (&q)[4]) {
   q[3] = kNegInf;
 }
 
-// Bounds of the error of a fast score (see fast_score): s (6e-7 + 1.5e-7
+// The score of a logit that is not -inf, fast.
+template <bool SOFTMAX>
+__device__ __forceinline__ float quick_score(float v, float m, float inv_total) {
+  if constexpr (SOFTMAX) return (v == m ? 1.0f : exp2_fast((v - m) * kLog2e)) * inv_total;
+  else return rcp_fast(1.0f + exp2_fast(-kLog2e * v));
+}
+
+// Bounds of the error of a fast score (see quick_score): s (6e-7 + 1.5e-7
 // max(-l, 0)) for the sigmoid, from the exponential's 2 ulp and its rounded
 // argument (1.17 |l| ulp) and the reciprocal's ulp; for the softmax
 // s (3e-6 + 2e-7 (m - l)), which includes the error of the sum over experts.
@@ -292,6 +299,21 @@ __device__ __forceinline__ bool unsure_order(float v, float bias, float l, float
   return __any_sync(kAll, unsure);
 }
 
+// Whether one of this lane's experts, taken or not, lies within `reach` (and
+// its own rounding) of the last one taken without being equal to it.
+template <bool SOFTMAX>
+__device__ __noinline__ bool others_near(const float* row, const float* bias, int first, int mine, float m,
+                                         float inv_total, float last, float last_l, float last_b, float reach) {
+  bool near = false;
+  for (int e = first; e < first + mine; ++e) {
+    const float l = clean(__ldg(row + e)), b = __ldg(bias + e);
+    if (l == kNegInf || (l == last_l && b == last_b)) continue;
+    const float f = quick_score<SOFTMAX>(l, m, inv_total) + b;
+    near = near || fabsf(last - f) <= reach + 2.0f * kSumError * fabsf(f);
+  }
+  return near;
+}
+
 // One token by a whole warp.  vpl: experts a lane holds at most (<= VPL); lpg:
 // lanes of a group; cand: room for 32 (value, id) candidates.
 template <int VPL, bool SOFTMAX>
@@ -301,7 +323,7 @@ struct WarpToken {
   int vpl, lpg, lane, first, mine, group, r;
   // tight: the experts to choose from lie on fewer than 2 K lanes, whose maxima
   // alone would leave too many candidates (2400 tokens, 11 of 512 experts in
-  // one of 4 groups: 29 us so, 8.5 with four maxima a lane); few: and are 32
+  // one of 4 groups: 29 us so, 9.0 with four maxima a lane); few: and are 32
   // at most
   bool vec, tight, few;
 
@@ -370,12 +392,7 @@ struct WarpToken {
         inv_total = total > 0.0f ? 1.0f / total : 0.0f;
       }
     }
-    auto fast_score = [&](float v) -> float {
-      if constexpr (SOFTMAX)
-        return (v == m ? 1.0f : exp2_fast((v - m) * kLog2e)) * inv_total;
-      else
-        return rcp_fast(1.0f + exp2_fast(-kLog2e * v));
-    };
+    auto fast_score = [&](float v) -> float { return quick_score<SOFTMAX>(v, m, inv_total); };
     // the value that orders the experts; masked and absent ones are -inf
     if (biased) {
 #pragma unroll
@@ -553,16 +570,11 @@ struct WarpToken {
         const float last = __shfl_sync(kAll, v, K - 1), last_b = __shfl_sync(kAll, bs, K - 1);
         const float last_l = __shfl_sync(kAll, lo, K - 1);
         const float reach = worst + value_error<SOFTMAX>(last, last_b, last_l, m);
-        uint32_t near = 0u;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const float f = key_value(key[i]);
-          if (key[i] != 0u && f > kNegInf && last - f <= reach + 2.0f * kSumError * fabsf(f)) near |= 1u << i;
-        }
-        for (; near != 0u; near &= near - 1u) {
-          const int e = first + __ffs(near) - 1;
-          unsure = unsure || !(clean(__ldg(row + e)) == last_l && __ldg(p.bias + e) == last_b);
-        }
+        const uint32_t next = __reduce_max_sync(kAll, ktop);
+        const float most = next != 0u ? key_value(next) : kNegInf;
+        if (most > kNegInf && last - most <= reach + 2.0f * kSumError * fabsf(most))
+          unsure = unsure || others_near<SOFTMAX>(row, p.bias, first, out ? 0 : mine, m, inv_total, last, last_l,
+                                                  last_b, reach);
         if (__any_sync(kAll, unsure))
           my_id = select_fp64<VPL, SOFTMAX>(row, p.bias, d, first, mine, stay, lane);
       }
@@ -618,7 +630,7 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
 // candidates do not fit, and one with near ties, is finished by the whole
 // warp.  Bound by latency (96 registers leave 20 warps an SM, which issue in
 // half of the cycles).  32768 tokens, 256 experts in 8 groups: 8 taken 27 us,
-// 35 us with a token a warp; 16 taken 38 us (5600 tokens: 12.1 and 13.3).
+// 38 us with a token a warp; 16 taken 39 and 46 (5600 tokens: 12.3 and 13.2).
 template <int LANES>
 __device__ __forceinline__ float sub_max(float v) {
 #pragma unroll
@@ -736,12 +748,7 @@ __global__ void __launch_bounds__(32 * kTopkWarps)
         inv_total = m != kNegInf ? 1.0f / total : 0.0f;
       }
     }
-    auto fast_score = [&](float v) -> float {
-      if constexpr (SOFTMAX)
-        return (v == m ? 1.0f : exp2_fast((v - m) * kLog2e)) * inv_total;
-      else
-        return rcp_fast(1.0f + exp2_fast(-kLog2e * v));
-    };
+    auto fast_score = [&](float v) -> float { return quick_score<SOFTMAX>(v, m, inv_total); };
     if (biased) {
 #pragma unroll
       for (int i = 0; i < VPL; i += 4) {
@@ -947,9 +954,11 @@ struct TopkBwdArgs {
 
 // One warp per token.  Only the softmax without renormalisation has a dense
 // gradient (and reads the row); the others write zeros and the K values.
-// The K values overwrite the row's after a warp barrier.  Bound by HBM once
-// the loads of a warp's next token are under way while it works on this one:
-// 32768 x 128, softmax, 8.1 us (36 MB, 5.3 us of HBM, behind the launch).
+// The K values overwrite the row's after a warp barrier.  The loads of a warp's
+// next token are under way while it works on this one; what is left is the
+// chain of dependent sums and the gather of the chosen logits (DRAM is busy a
+// fifth of the time, issue half): 32768 x 128, softmax, 9.5 us (36 MB, 5.3 us
+// of HBM); sigmoid with renorm 10.2 us.
 template <int VPL, bool DENSE>
 __global__ void __launch_bounds__(32 * kTopkWarps) route_topk_bwd_kernel(const TopkBwdArgs p) {
   const moe_topk_dims d = p.d;
@@ -1113,7 +1122,7 @@ cudaError_t launch_route_topk(const float* logits, const float* bias, int32_t* i
     for (int r = 0; r < lp; ++r) offered += std::max(0, std::min({4, vp, gs - r * vp}));
     // 32 experts at most to choose from: ranking them all costs less than the
     // bound for more than eight of them (30000 tokens, 16 of one of 4 groups of
-    // 32: 24.6 us, 28.8 with it), more for fewer (28006, 5 of 16: 12.7 and 10.6)
+    // 32: 26.4 us, 32.1 with it), more for fewer (28006, 5 of 16: 9.4 and 8.1)
     const bool few = staying * gs <= 32 && (LANES == 16 || d.K > staying * offered);
     if (!few && d.K > staying * offered) return false;
     if (vpl > packed_warp_vpl(LANES, vp > 16 ? 32 : 16)) return false;
@@ -1128,8 +1137,8 @@ cudaError_t launch_route_topk(const float* logits, const float* bias, int32_t* i
     return true;
   };
   // below this a token a warp fills the SMs better (256 experts in 8 groups, 8
-  // taken: 2400 tokens 6.5 us, 8.0 packed; 4000 9.9 and 10.2; 8000 13.1 and
-  // 11.9; 512 experts, 8 taken, 4000: 12.5 and 9.8)
+  // taken: 2400 tokens 7.0 us, 8.2 packed; 4000 9.9 and 9.8; 8000 13.1 and
+  // 11.6; 512 experts, 8 taken, 4000: 12.0 and 9.2)
   if (d.T >= 24 * static_cast<int64_t>(sm_count()) &&
       ((d.K <= 8 && packed(std::integral_constant<int, 8>{})) || packed(std::integral_constant<int, 16>{})))
     return cudaGetLastError();
