@@ -658,7 +658,10 @@ typedef struct {
  *   (y is computed from the unrounded one).
  * y may share res's memory (same ld).  Every ld is a multiple of 8, or of 4
  * for fp32 matrices.  An fp32 y is summed over stretches of K of at most 512
- * in registers, which keeps it as exact as a sum in fp32 arithmetic.
+ * in registers, which keeps it as exact as a sum in fp32 arithmetic; a 16-bit
+ * result's sum stays in the tensor core, which truncates each addition: a sum
+ * of n terms of one sign is low by up to n * 1e-9 of its value.
+ * NaN in a row of x is NaN in that row of y and z, whatever the activation.
  */
 moe_status moe_linear(moe_mat x, moe_mat w, const float* bias, moe_mat res, moe_mat y, moe_mat z,
                       int32_t* dev_status, moe_linear_dims d, cudaStream_t stream);
