@@ -177,11 +177,11 @@ def prepare(case, seed):
 def _handle(s, c):
     """The framework's operator with its output buffers and workspace, as a program keeps it
     (for the adapters with the batch's grouping, which all of a step's projections share)."""
-    from mixture_experts_ffn_histogram_gb300 import binding, block, layer
+    from mixture_experts_ffn_histogram_gb300 import binding, layer
     if c["op"] == "experts":
         mode = {"softmax": binding.SCORE_SOFTMAX_TOPK, "sigmoid": binding.SCORE_SIGMOID_NORM,
                 "given": binding.SCORE_GIVEN}[c["route"]]
-        s["op"] = block.MoEDecode(c["T"], c["D"], c["E"], c["K"], c["F"], mode, dtype=DTYPES[c["dtype"]])
+        s["op"] = layer.MoEDecode(c["T"], c["D"], c["E"], c["K"], c["F"], mode, dtype=DTYPES[c["dtype"]])
     elif c["op"] == "norm":
         s["op"] = layer.BlockNorm(c["rows"], c["D"], dtype=DTYPES[c["dtype"]],
                                   weight_dtype=DTYPES[c["weights"]], eps=EPS, scale=c["scale"],
