@@ -683,6 +683,37 @@ moe_status moe_linear_bwd(moe_mat dy, moe_mat z, moe_mat x, moe_mat w, moe_mat d
                           moe_mat dw, float* db, int32_t* dev_status, void* ws, moe_linear_dims d,
                           cudaStream_t stream);
 
+/*
+ * The whole expert layer for a few tokens, in one kernel: routing, FC1 with
+ * SwiGLU, FC2 and the weighted combine.
+ *   ids, w  as moe_route_histogram's (mode, logits, bias), or given
+ *   h[t,k]  = round(silu(a[:F]) * a[F:]),  a = x[t] . wi[ids[t,k]]   (fp32 sums)
+ *   out[t]  = round(sum_{k ascending} w[t,k] * (h[t,k] . wo[ids[t,k]]) + res[t])
+ *   x, res, out  `type` [n, D] (bf16 or fp16);  wi [E, D, 2F], wo [E, F, D]
+ *                dense, of the same type; res.p may be NULL; out may be res's
+ *                memory (same ld), not x's
+ *   logits  fp32 [n, E], bias fp32 [E] or NULL (both ignored for GIVEN)
+ *   ids, w  int32 and fp32 [n, K]: in for GIVEN (a token may name an expert
+ *           more than once), else out (either may be NULL).  logits, bias,
+ *           ids, w and dev_status need only their elements' alignment.
+ *   n       tokens of this call, at most d.T
+ * d.T is the capacity, which fixes the workspace's layout: T <= 256,
+ * T * K <= 2048, K <= min(E, 32), E <= 1024; D and F multiples of 64 up to
+ * 16384.  An id outside [0, E) is reported as MOE_ERR_DEVICE and its slot
+ * dropped.  Each distinct expert's weights are read once (again for every 64
+ * of its slots beyond the first 64).
+ * ws: moe_decode_workspace_bytes(d) bytes that are ZERO before the first
+ * call; every call leaves the counters in them zero for the next, except one
+ * that reports MOE_ERR_TIMEOUT (clear ws then).  Calls that share a ws must be
+ * ordered on one stream.  Results are reproducible bit for bit.  The launch is
+ * cooperative (one block to an SM): it starts when every SM has room.
+ */
+size_t moe_decode_workspace_bytes(moe_dims d);
+moe_status moe_decode(moe_mat x, const void* wi, const void* wo, const float* logits,
+                      const float* bias, moe_score_mode mode, int32_t* ids, float* w, moe_mat res,
+                      moe_mat out, int32_t* dev_status, void* ws, int32_t n, moe_dims d,
+                      moe_dtype type, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

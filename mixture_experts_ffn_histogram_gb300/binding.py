@@ -38,6 +38,7 @@ ENTRY_POINTS = (
     "moe_mx_grouped_gemm_fc1_bwd",
     "moe_layer_norm", "moe_layer_norm_bwd", "moe_layer_norm_workspace_bytes", "moe_route_topk",
     "moe_route_topk_bwd", "moe_linear", "moe_linear_bwd", "moe_linear_workspace_bytes",
+    "moe_decode", "moe_decode_workspace_bytes",
 )
 
 # moe_dtype
@@ -163,6 +164,8 @@ def lib() -> ctypes.CDLL:
             "moe_linear": ([M, M, P, M, M, M, P, MoeLinearDims, P], I),
             "moe_linear_bwd": ([M] * 7 + [P, P, P, MoeLinearDims, P], I),
             "moe_linear_workspace_bytes": ([MoeLinearDims], ctypes.c_size_t),
+            "moe_decode": ([M, P, P, P, P, I, P, P, M, M, P, P, ctypes.c_int32, D_, I, P], I),
+            "moe_decode_workspace_bytes": ([D_], ctypes.c_size_t),
         })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -441,3 +444,14 @@ def moe_linear_bwd(dy, z, x, w, dx_add, dx, dw, db, dev_status, ws, d: MoeLinear
     _ok("moe_linear_bwd", lib().moe_linear_bwd(
         _m(dy), _m(z), _m(x), _m(w), _m(dx_add), _m(dx), _m(dw), _p(db), _p(dev_status), _p(ws),
         d, _s(stream)))
+
+
+def moe_decode_workspace_bytes(d: MoeDims) -> int:
+    return int(lib().moe_decode_workspace_bytes(d))
+
+
+def moe_decode(x, wi, wo, logits, bias, mode, ids, w, res, out, dev_status, ws, d: MoeDims,
+               stream=None):
+    _ok("moe_decode", lib().moe_decode(
+        _m(x), _p(wi), _p(wo), _p(logits), _p(bias), int(mode), _p(ids), _p(w), _m(res), _m(out),
+        _p(dev_status), _p(ws), x.shape[0], d, DTYPES[x.dtype], _s(stream)))

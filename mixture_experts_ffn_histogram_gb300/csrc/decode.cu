@@ -1,0 +1,911 @@
+// The expert layer for a few tokens, in one kernel: routing, FC1 with SwiGLU,
+// FC2 and the weighted combine (with a residual).
+//
+//   ids, p = top-K of the scores, or given     z[t,k] = x[t] . wi[e_tk]
+//   h[t,k] = silu(z[:F]) z[F:]                 out[t] = sum_k p_tk h[t,k] . wo[e_tk] + res[t]
+//
+// With a few tokens the layer is bound by reading the weights of the experts
+// that the tokens name, each once.  So the weights' columns are the 128 side
+// of the MMA and the expert's tokens its narrow side (16 to 64), and the work
+// is cut by weight bytes alone: a phase is a list of 64-deep blocks of 128
+// weight columns (16 KB each), expert by expert, and each of the grid's CTAs
+// (one to an SM) takes an equal run of it, FC1's list and then FC2's, through
+// one ring of shared memory that keeps 128 KB or more under way (with 32 KB an
+// SM streams at two thirds of the rate).  Whole tiles to a CTA would leave a
+// tenth to a third of the SMs idle in the last wave, since a token names some
+// 90 tiles and 64 tokens some ten times that.  Runs begin and end inside a
+// tile; the CTA that adds a tile's last part joins the parts, in the order of
+// the reduction, so that results do not depend on who was last.
+//
+// FC2's weights start to stream as soon as FC1's have been issued; only the
+// rows of h wait, tile by tile, for the flags that FC1's epilogue sets.  Every
+// CTA routes all tokens for itself (a few hundred scores a warp), which costs
+// less than handing the result around.  The launch is cooperative: the CTAs
+// wait (bounded) for one another's flags, so all have to be resident.
+//
+// h is rounded to the operands' type: the tensor core multiplies no wider one,
+// and its error, half a step on each of F terms of both signs, stays below the
+// result's own rounding.  Partial sums, routing weights and the combine are fp32.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kernels.h"
+#include "layer.h"
+#include "layer_common.cuh"
+#include "tmem_share.h"
+#include "umma_tile.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCols = 128;                         // weight columns of a tile
+constexpr int kWeightStage = kCols * kBlockK * 2;  // 16 KB
+constexpr int kMaxStages = 12;
+constexpr int kMinStages = 3;
+constexpr int kBufLd = kCols + 4;
+constexpr int kBufBytes = 16 * kBufLd * 4;  // 16 tokens of a tile
+constexpr size_t kSmemLimit = 227 * 1024;
+constexpr int kFirstEpiWarp = 4;
+constexpr uint16_t kNone = 0xffff;
+static_assert(!fits_beside_pair(kMinStages * (kWeightStage + 16 * kBlockK * 2)),
+              "CTAs that wait for one another must not fit beside a pair's: tmem_share.h");
+
+struct Params {
+  const float *logits, *bias, *w_in;
+  const int32_t* ids_in;
+  int32_t* ids_out;
+  float* w_out;
+  const void* res;
+  void* out;
+  int64_t ldres, ldout;
+  int n, D, E, K, F;  // n: tokens of this call
+  int mode;
+  int nt, stages;     // tokens of a tile at most (16, 32 or 64)
+  uint32_t type;      // of the instruction descriptor
+  void* h;            // [n * K][F]
+  float* y;           // [n * K][D]: FC2's rows of tiles that one CTA summed alone
+  float* part;        // [2 phases][CTA][head, tail][nt][128]: sums of parts of tiles
+  int32_t* leave;     // CTAs that read no more flags
+  int32_t* done;      // [tile of FC1]: its h is stored
+  int32_t* sum1;      // [tile of FC1]: blocks summed so far
+  int32_t* sum2;      // [token][tile of FC2]
+  int32_t* status;
+  uint64_t limit_ns;
+};
+
+struct Ctl {
+  uint64_t fullw[kMaxStages];  // a stage's weights landed
+  uint64_t fullt[kMaxStages];  // ... and its tokens' rows
+  uint64_t empty[kMaxStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint32_t tmem_base;
+  int abort_flag;
+  int last;
+  uint32_t last_tokens[4];
+  int tiles;  // virtual experts: expert and up to nt of its slots
+};
+
+// The routing, in shared memory.  Slot j = t * K + k.  Experts are numbered in
+// the order in which the slots first name them (`ord`), and an expert with
+// more than nt slots makes several entries of the list that the tiles follow
+// ("virtual experts").
+struct Route {
+  float* w;                                  // [R]
+  uint16_t *expert, *rank, *at, *list;       // [R]; at: the slot's virtual expert
+  uint16_t *vexp, *vstart, *vcnt;            // [V]
+  uint16_t *ord, *ocnt, *obase, *ostart, *oexp;
+  uint16_t* valid;                           // [n]: slots of a token that name an expert
+};
+__host__ __device__ inline int most_virtual(int R, int E, int nt) {
+  const int v = E + R / nt;
+  return v < R ? v : R;
+}
+__host__ __device__ inline size_t route_bytes(int R, int E, int n, int nt) {
+  const int o = E < R ? E : R;
+  const size_t half = 4 * static_cast<size_t>(R) + 3 * static_cast<size_t>(most_virtual(R, E, nt)) + E +
+                      4 * static_cast<size_t>(o) + n;
+  return 4 * static_cast<size_t>(R) + (half * 2 + 15) / 16 * 16;
+}
+__device__ __forceinline__ Route route_at(uint8_t* p, int R, int E, int n, int nt) {
+  const int V = most_virtual(R, E, nt), o = min(E, R);
+  Route r;
+  r.w = reinterpret_cast<float*>(p);
+  uint16_t* q = reinterpret_cast<uint16_t*>(p + 4 * static_cast<size_t>(R));
+  auto take = [&](int count) {
+    uint16_t* a = q;
+    q += count;
+    return a;
+  };
+  r.expert = take(R);
+  r.rank = take(R);
+  r.at = take(R);
+  r.list = take(R);
+  r.vexp = take(V);
+  r.vstart = take(V);
+  r.vcnt = take(V);
+  r.ord = take(E);
+  r.ocnt = take(o);
+  r.obase = take(o);
+  r.ostart = take(o);
+  r.oexp = take(o);
+  r.valid = take(n);
+  return r;
+}
+
+__device__ __forceinline__ int ld_acquire(const int32_t* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release(int32_t* p, int v) {
+  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+// Between generic and asynchronous (TMA) accesses to global memory.
+__device__ __forceinline__ void fence_proxy_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+// Barriers of the four epilogue warps; the second tells whether all had `ok`.
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool epi_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// Four rows of a map whose box is 64 columns of one row, into 512 consecutive
+// bytes (swizzled by their address like any tile).
+__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                        const int (&r)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+      "r"(r[3])
+      : "memory");
+}
+
+// A score as an unsigned number of the same order (-0 as +0).
+__device__ __forceinline__ uint32_t order_of(float v) {
+  uint32_t u = __float_as_uint(v);
+  if (u == 0x80000000u) u = 0u;
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float score_of(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+}
+
+// The K best of a token's E scores by one warp: K rounds of a maximum over the
+// lanes' own best, the lower expert first among equal scores.
+template <int PER>
+__device__ __forceinline__ void select_token(const Params& p, const Route& r, int t, int lane) {
+  uint32_t key[PER];
+  const float* row = p.logits + static_cast<int64_t>(t) * p.E;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = 0u;  // below every score's (a NaN with all bits set apart, which counts as this)
+    if (e < p.E) {
+      float s = __ldg(row + e);
+      if (p.bias != nullptr) s = __fadd_rn(s, __ldg(p.bias + e));
+      key[i] = max(order_of(s), 1u);
+    }
+  }
+  uint32_t mine = 0u;
+  int mine_e = 0;
+  for (int k = 0; k < p.K; ++k) {
+    uint32_t best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < PER; ++i) {
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+      }
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const int e = static_cast<int>(
+        __reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(at * 32 + lane) : 0xffffffffu));
+    if ((e & 31) == lane) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i == (e >> 5)) key[i] = 0u;
+    }
+    if (lane == k) {
+      mine = top;
+      mine_e = e;
+    }
+  }
+  const float v = score_of(mine), first = __shfl_sync(0xffffffffu, v, 0);
+  float ex = 0.0f;
+  if (lane < p.K) ex = p.mode == MOE_SCORE_SOFTMAX_TOPK ? expf(v - first) : 1.0f / (1.0f + expf(-v));
+  float sum = 0.0f;  // in the slots' order
+  for (int k = 0; k < p.K; ++k) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, ex, k));
+  if (lane < p.K) {
+    const int j = t * p.K + lane;
+    const float w = __fdiv_rn(ex, sum);
+    r.expert[j] = static_cast<uint16_t>(mine_e);
+    r.w[j] = w;
+    if (blockIdx.x == 0) {
+      if (p.ids_out != nullptr) p.ids_out[j] = mine_e;
+      if (p.w_out != nullptr) p.w_out[j] = w;
+    }
+  }
+}
+
+// The list of virtual experts, by one warp: 32 slots at a time.
+__device__ __forceinline__ int build_list(const Params& p, const Route& r, int lane) {
+  const int R = p.n * p.K;
+  const uint32_t below = (1u << lane) - 1u;
+  int live = 0;
+  for (int base = 0; base < R; base += 32) {
+    const int j = base + lane;
+    const int e = j < R ? r.expert[j] : kNone;
+    const uint32_t peers = __match_any_sync(0xffffffffu, e);
+    const bool valid = e != kNone, lead = lane == __ffs(peers) - 1;
+    const bool fresh = valid && lead && r.ord[e] == kNone;
+    const uint32_t news = __ballot_sync(0xffffffffu, fresh);
+    if (fresh) {
+      const int o = live + __popc(news & below);
+      r.ord[e] = static_cast<uint16_t>(o);
+      r.oexp[o] = static_cast<uint16_t>(e);
+      r.ocnt[o] = 0;
+    }
+    __syncwarp();
+    const int o = valid ? r.ord[e] : 0;
+    const int before = valid ? r.ocnt[o] : 0;
+    __syncwarp();
+    if (valid) {
+      r.rank[j] = static_cast<uint16_t>(before + __popc(peers & below));
+      if (lead) r.ocnt[o] = static_cast<uint16_t>(before + __popc(peers));
+    }
+    __syncwarp();
+    live += __popc(news);
+  }
+  int entries = 0, slots = 0;
+  for (int base = 0; base < live; base += 32) {
+    const int o = base + lane;
+    const int c = o < live ? r.ocnt[o] : 0, v = (c + p.nt - 1) / p.nt;
+    int sc = c, sv = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, sc, d), b = __shfl_up_sync(0xffffffffu, sv, d);
+      if (lane >= d) {
+        sc += a;
+        sv += b;
+      }
+    }
+    if (o < live) {
+      const int start = slots + sc - c, first = entries + sv - v;
+      r.ostart[o] = static_cast<uint16_t>(start);
+      r.obase[o] = static_cast<uint16_t>(first);
+      for (int i = 0; i < v; ++i) {
+        r.vexp[first + i] = r.oexp[o];
+        r.vstart[first + i] = static_cast<uint16_t>(start + i * p.nt);
+        r.vcnt[first + i] = static_cast<uint16_t>(min(p.nt, c - i * p.nt));
+      }
+    }
+    slots += __shfl_sync(0xffffffffu, sc, 31);
+    entries += __shfl_sync(0xffffffffu, sv, 31);
+  }
+  return entries;
+}
+
+// One phase's list of blocks, and this CTA's run of it.
+struct Phase {
+  int kb;     // blocks of a tile
+  int cols;   // tiles of a virtual expert
+  int64_t all, b0, b1;
+  int64_t ctas;  // no more than blocks: every one of them has a run
+  __device__ __forceinline__ Phase(const Params& p, int which, int entries) {
+    kb = which == 0 ? p.D / kBlockK : p.F / kBlockK;
+    cols = which == 0 ? p.F / 64 : (p.D + kCols - 1) / kCols;
+    all = static_cast<int64_t>(entries) * cols * kb;
+    ctas = min(static_cast<int64_t>(gridDim.x), all);
+    b0 = b1 = 0;
+    if (blockIdx.x < ctas) {
+      b0 = all * blockIdx.x / ctas;
+      b1 = all * (blockIdx.x + 1) / ctas;
+    }
+  }
+  // the CTA whose run holds block b
+  __device__ __forceinline__ int owner(int64_t b) const {
+    return static_cast<int>((static_cast<uint64_t>(b + 1) * ctas - 1) / static_cast<uint64_t>(all));
+  }
+};
+// A part of a tile: blocks [k0, k1) of tile `col` of virtual expert `v`.
+struct Piece {
+  int tile, v, col, k0, k1;
+  __device__ __forceinline__ Piece(const Phase& f, int64_t b) {
+    tile = static_cast<int>(b / f.kb);
+    k0 = static_cast<int>(b - static_cast<int64_t>(tile) * f.kb);
+    k1 = static_cast<int>(min(static_cast<int64_t>(f.kb), k0 + (f.b1 - b)));
+    v = tile / f.cols;
+    col = tile - v * f.cols;
+  }
+  __device__ __forceinline__ bool whole(const Phase& f) const { return k0 == 0 && k1 == f.kb; }
+};
+// Where CTA c keeps the sums of a part that starts its tile (tail = 1: it is
+// the CTA's last part) or not (tail = 0: its first).
+__device__ __forceinline__ float* part_rows(const Params& p, int phase, int c, int tail) {
+  return p.part + ((static_cast<int64_t>(phase) * gridDim.x + c) * 2 + tail) * p.nt * kCols;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_h(const Params& p, int slot, int f, const float (&g)[8], const float (&u)[8]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid_fast(g[i]) * u[i];
+  Raw<T, 8> o;
+  o.pack(v);
+  *reinterpret_cast<uint4*>(static_cast<T*>(p.h) + static_cast<int64_t>(slot) * p.F + f) = o.v;
+}
+__device__ __forceinline__ void load8(const float* at, float (&f)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(at), b = *reinterpret_cast<const float4*>(at + 4);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+__device__ __forceinline__ void add8(const float* at, float (&f)[8]) {
+  const float4 a = __ldcg(reinterpret_cast<const float4*>(at)), b = __ldcg(reinterpret_cast<const float4*>(at) + 1);
+  f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w, f[4] += b.x, f[5] += b.y, f[6] += b.z, f[7] += b.w;
+}
+
+// out[t, 128 col ..] by one warp, four columns a lane: the token's slots in
+// order, each the sum of its tile's parts in the reduction's order.
+template <typename T>
+__device__ __forceinline__ void combine_token(const Params& p, const Route& r, const Phase& f, int t, int col,
+                                              int lane) {
+  constexpr int kAhead = 8;
+  const int c4 = col * kCols + lane * 4;
+  const bool in = c4 < p.D;
+  // lane k looks at slot k: its first and last CTA, its row in their parts
+  int first = 0, last = 0, idx = 0;
+  float w = 0.0f;
+  bool valid = false;
+  if (lane < p.K) {
+    const int j = t * p.K + lane;
+    valid = r.expert[j] != kNone;
+    if (valid) {
+      const int64_t tile = static_cast<int64_t>(r.at[j]) * f.cols + col;
+      first = f.owner(tile * f.kb);
+      last = f.owner(tile * f.kb + f.kb - 1);
+      idx = r.rank[j] & (p.nt - 1);
+      w = r.w[j];
+    }
+  }
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int k0 = 0; k0 < p.K; k0 += kAhead) {
+    float4 a[kAhead], b[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = min(k0 + i, p.K - 1);
+      const int c0 = __shfl_sync(0xffffffffu, first, k), c1 = __shfl_sync(0xffffffffu, last, k);
+      const int row = __shfl_sync(0xffffffffu, idx, k);
+      const bool named = __shfl_sync(0xffffffffu, valid ? 1 : 0, k) != 0;
+      a[i] = b[i] = zero;
+      if (named && in && k0 + i < p.K) {
+        const float* at = c0 == c1 ? p.y + (static_cast<int64_t>(t) * p.K + k) * p.D + c4
+                                   : part_rows(p, 1, c0, 1) + row * kCols + lane * 4;
+        a[i] = __ldcg(reinterpret_cast<const float4*>(at));
+        if (c0 != c1) b[i] = __ldcg(reinterpret_cast<const float4*>(part_rows(p, 1, c0 + 1, 0) + row * kCols + lane * 4));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = min(k0 + i, p.K - 1);
+      const int c0 = __shfl_sync(0xffffffffu, first, k), c1 = __shfl_sync(0xffffffffu, last, k);
+      const int row = __shfl_sync(0xffffffffu, idx, k);
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const bool named = __shfl_sync(0xffffffffu, valid ? 1 : 0, k) != 0;
+      if (!named || k0 + i >= p.K) continue;
+      float4 s = make_float4(a[i].x + b[i].x, a[i].y + b[i].y, a[i].z + b[i].z, a[i].w + b[i].w);
+      for (int c = c0 + 2; c <= c1 && in; ++c) {
+        const float4 q = __ldcg(reinterpret_cast<const float4*>(part_rows(p, 1, c, 0) + row * kCols + lane * 4));
+        s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
+      }
+      acc[0] = fmaf(wk, s.x, acc[0]);
+      acc[1] = fmaf(wk, s.y, acc[1]);
+      acc[2] = fmaf(wk, s.z, acc[2]);
+      acc[3] = fmaf(wk, s.w, acc[3]);
+    }
+  }
+  if (!in) return;
+  if (p.res != nullptr) {
+    const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.res) + t * p.ldres + c4);
+    const float2 lo = unpack_pair(q.x, T{}), hi = unpack_pair(q.y, T{});
+    acc[0] += lo.x, acc[1] += lo.y, acc[2] += hi.x, acc[3] += hi.y;
+  }
+  *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + t * p.ldout + c4) =
+      make_uint2(pack_pair(acc[0], acc[1], T{}), pack_pair(acc[2], acc[3], T{}));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap map_wi, const __grid_constant__ CUtensorMap map_wo,
+                  const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_h,
+                  const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int stage_bytes = kWeightStage + p.nt * kBlockK * 2;
+  float* buf = reinterpret_cast<float*>(ring + p.stages * stage_bytes);
+  Ctl& s = *reinterpret_cast<Ctl*>(reinterpret_cast<uint8_t*>(buf) + kBufBytes);
+  const int R = p.n * p.K;
+  const Route r = route_at(reinterpret_cast<uint8_t*>(&s) + sizeof(Ctl), R, p.E, p.n, p.nt);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&s.fullw[i], 1);
+      mbar_init(&s.fullt[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.tfull[i], 1);
+      mbar_init(&s.tempty[i], 4);
+    }
+    s.abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_map(&map_wi);
+    tma_prefetch_map(&map_x);
+    tma_prefetch_map(&map_wo);
+    tma_prefetch_map(&map_h);
+  }
+  if (warp == 1) {
+    tmem_alloc<1>(&s.tmem_base, 2 * p.nt);
+    tmem_relinquish<1>();
+  }
+  for (int e = threadIdx.x; e < p.E; e += kThreads) r.ord[e] = kNone;
+  if (p.mode == MOE_SCORE_GIVEN) {
+    for (int j = threadIdx.x; j < R; j += kThreads) {
+      const int e = __ldg(p.ids_in + j);
+      const bool ok = e >= 0 && e < p.E;
+      r.expert[j] = ok ? static_cast<uint16_t>(e) : kNone;
+      r.w[j] = __ldg(p.w_in + j);
+      if (!ok && blockIdx.x == 0) report(p.status, MOE_ERR_DEVICE);
+    }
+  } else {
+    for (int t = warp; t < p.n; t += kThreads / 32) {
+      if (p.E <= 128) select_token<4>(p, r, t, lane);
+      else if (p.E <= 256) select_token<8>(p, r, t, lane);
+      else select_token<32>(p, r, t, lane);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int entries = build_list(p, r, lane);
+    if (lane == 0) s.tiles = entries;
+  } else {
+    for (int t = threadIdx.x - 32; t < p.n; t += kThreads - 32) {
+      int c = 0;
+      for (int k = 0; k < p.K; ++k) c += r.expert[t * p.K + k] != kNone;
+      r.valid[t] = static_cast<uint16_t>(c);
+    }
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < R; j += kThreads) {
+    if (r.expert[j] != kNone) {
+      const int o = r.ord[r.expert[j]], rank = r.rank[j];
+      r.list[r.ostart[o] + rank] = static_cast<uint16_t>(j);
+      r.at[j] = static_cast<uint16_t>(r.obase[o] + rank / p.nt);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  const int entries = s.tiles;
+  const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
+
+  if (warp == 0) {
+    // ------------------------------------------------------ weights' producer
+    if (elect_one()) {
+      int stage = 0, filled = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int ph = 0; ph < 2 && ok; ++ph) {
+        const Phase f(p, ph, entries);
+        for (int64_t b = f.b0; b < f.b1 && ok;) {
+          const Piece q(f, b);
+          const int e = r.vexp[q.v];
+          const int c0 = ph == 0 ? q.col * 64 : q.col * kCols;
+          const int c1 = ph == 0 ? p.F + c0 : c0 + 64;
+          const void* map = ph == 0 ? &map_wi : &map_wo;
+          for (int kb = q.k0; kb < q.k1; ++kb) {
+            ok = mbar_wait(&s.empty[stage], phase ^ 1u, wc);
+            if (!ok) break;
+            uint8_t* at = ring + stage * stage_bytes;
+            mbar_arrive_expect_tx(&s.fullw[stage], kWeightStage);
+            tma_load_3d(at, map, &s.fullw[stage], c0, kb * kBlockK, e);
+            tma_load_3d(at + kChunk, map, &s.fullw[stage], c1, kb * kBlockK, e);
+            ++filled;
+            if (++stage == p.stages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          b += q.k1 - q.k0;
+        }
+      }
+      if (!ok) {  // copies in flight land before the CTA goes on
+        for (int i = 0; i < p.stages; ++i) {
+          const int n = filled > i ? (filled - i + p.stages - 1) / p.stages : 0;
+          if (n > 0) (void)mbar_wait_drain(&s.fullw[i], (n - 1) & 1, 100000000ull);
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------- tokens' producer
+    // Lane i gathers rows 4i .. 4i + 3 of the tile's tokens: of x, then of h
+    // once the flag of the block's h is set.  (Rows past the last are the last
+    // again; their columns of the product are not read.)
+    int stage = 0, filled = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int ph = 0; ph < 2 && ok; ++ph) {
+      const Phase f(p, ph, entries);
+      const int flags = p.F / 64;  // of a virtual expert
+      for (int64_t b = f.b0; b < f.b1 && ok;) {
+        const Piece q(f, b);
+        const int cnt = r.vcnt[q.v], groups = (cnt + 3) / 4;
+        int row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int slot = r.list[r.vstart[q.v] + min(4 * lane + i, cnt - 1)];
+          row[i] = ph == 0 ? slot / p.K : slot;
+        }
+        if (ph == 1) {
+          const int32_t* flag = p.done + static_cast<int64_t>(q.v) * flags;
+          for (int i = q.k0 + lane; i < q.k1 && ok; i += 32) {
+            if (ld_acquire(flag + i) != 0) continue;
+            const uint64_t t0 = global_timer_ns();
+            ok = false;
+            for (uint32_t it = 0; it < kMaxWaitIters; ++it) {
+              if (ld_acquire(flag + i) != 0) {
+                ok = true;
+                break;
+              }
+              if ((it & 31u) == 31u) {
+                if (*wc.abort) break;
+                if (global_timer_ns() - t0 > p.limit_ns) {
+                  *wc.abort = 1;
+                  report(p.status, MOE_ERR_TIMEOUT);
+                  break;
+                }
+              }
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          __syncwarp();  // a lane's rows may lie behind other lanes' flags
+          fence_proxy_async_global();
+        }
+        for (int kb = q.k0; kb < q.k1; ++kb) {
+          ok = warp_wait(&s.empty[stage], phase ^ 1u, wc);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&s.fullt[stage], groups * 512);
+          __syncwarp();
+          if (lane < groups)
+            gather4(ring + stage * stage_bytes + kWeightStage + 512 * lane, ph == 0 ? &map_x : &map_h,
+                    &s.fullt[stage], kb * kBlockK, row);
+          ++filled;
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        b += q.k1 - q.k0;
+      }
+    }
+    // This CTA reads no more flags.  The last to say so clears them: each was
+    // waited for by some CTA, so each has been set.
+    int left = 0;
+    if (lane == 0) {
+      __threadfence();
+      left = atomicAdd(p.leave, 1);
+    }
+    if (__shfl_sync(0xffffffffu, left, 0) == static_cast<int>(gridDim.x) - 1) {
+      __threadfence();
+      const int64_t n = static_cast<int64_t>(entries) * (p.F / 64);
+      for (int64_t i = lane; i < n; i += 32) p.done[i] = 0;
+      if (lane == 0) *p.leave = 0;
+    }
+    if (!ok && lane == 0) {
+      for (int i = 0; i < p.stages; ++i) {
+        const int n = filled > i ? (filled - i + p.stages - 1) / p.stages : 0;
+        if (n > 0) (void)mbar_wait_drain(&s.fullt[i], (n - 1) & 1, 100000000ull);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- products
+    if (elect_one()) {
+      const uint32_t base = smem_u32(ring);
+      const Operand weights = operand128<true>(), tokens = operand128<false>();
+      int stage = 0, done = 0, piece = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int ph = 0; ph < 2 && ok; ++ph) {
+        const Phase f(p, ph, entries);
+        for (int64_t b = f.b0; b < f.b1 && ok; ++piece) {
+          const Piece q(f, b);
+          const int slot = piece & 1;
+          const uint32_t idesc = dense_idesc(kCols, (r.vcnt[q.v] + 15) & ~15, true, false, p.type);
+          if (piece >= 2) ok = mbar_wait(&s.tempty[slot], ((piece >> 1) - 1) & 1, wc);
+          tc_fence_after();
+          for (int kb = q.k0; kb < q.k1 && ok; ++kb) {
+            ok = mbar_wait(&s.fullw[stage], phase, wc) && mbar_wait(&s.fullt[stage], phase, wc);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t at = base + stage * stage_bytes;
+            issue_block<1>(tmem + slot * p.nt, at, at + kWeightStage, weights, tokens, idesc, kb > q.k0 ? 1u : 0u);
+            umma_commit<1>(&s.empty[stage]);
+            ++done;
+            if (++stage == p.stages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (ok) umma_commit<1>(&s.tfull[slot]);
+          b += q.k1 - q.k0;
+        }
+      }
+      if (!ok && done > 0) {  // issued products end before TMEM is freed
+        const int last = (done - 1) % p.stages;
+        (void)mbar_wait_drain(&s.empty[last], ((done - last + p.stages - 1) / p.stages - 1) & 1, 100000000ull);
+      }
+    }
+  } else if (warp >= kFirstEpiWarp) {
+    // -------------------------------------------------------------- epilogue
+    const int tid = threadIdx.x - kFirstEpiWarp * 32, ew = warp - kFirstEpiWarp;
+    const int col = (warp & 3) * 32 + lane;  // the tile's column: this thread's TMEM lane
+    const uint32_t tq = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    int piece = 0;
+    bool ok = true;
+    for (int ph = 0; ph < 2 && ok; ++ph) {
+      const Phase f(p, ph, entries);
+      for (int64_t b = f.b0; b < f.b1; ++piece) {
+        const Piece q(f, b);
+        const int slot = piece & 1, cnt = r.vcnt[q.v], start = r.vstart[q.v];
+        const bool whole = q.whole(f);
+        // the four warps meet at barriers below: all go on or none does
+        ok = epi_all(warp_wait(&s.tfull[slot], (piece >> 1) & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+        float* rows = part_rows(p, ph, blockIdx.x, q.k0 == 0 ? 1 : 0);
+        for (int t0 = 0; t0 < cnt; t0 += 16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tq + slot * p.nt + t0, v);
+          tmem_ld_wait();
+          const int m = min(16, cnt - t0);
+          if (ph == 0 && whole) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) buf[i * kBufLd + col] = __uint_as_float(v[i]);
+            epi_sync();
+            const int i = tid / 8, c8 = (tid % 8) * 8;
+            if (i < m) {
+              float g[8], u[8];
+              load8(buf + i * kBufLd + c8, g);
+              load8(buf + i * kBufLd + 64 + c8, u);
+              store_h<T>(p, r.list[start + t0 + i], q.col * 64 + c8, g, u);
+            }
+            epi_sync();
+          } else if (whole) {
+            const int c = q.col * kCols + col;
+            if (c < p.D) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (i < m) __stcg(p.y + static_cast<int64_t>(r.list[start + t0 + i]) * p.D + c, __uint_as_float(v[i]));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (i < m) __stcg(rows + (t0 + i) * kCols + col, __uint_as_float(v[i]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.tempty[slot]);
+        const int blocks = q.k1 - q.k0;
+        if (ph == 0) {
+          bool stored = whole;
+          if (!whole) {
+            __threadfence();
+            epi_sync();
+            if (tid == 0) s.last = atomicAdd(p.sum1 + q.tile, blocks) + blocks == f.kb ? 1 : 0;
+            epi_sync();
+            if (s.last) {  // join the parts, in the reduction's order
+              __threadfence();
+              const int64_t first_block = static_cast<int64_t>(q.tile) * f.kb;
+              const int first = f.owner(first_block), last = f.owner(first_block + f.kb - 1);
+              const int c8 = (tid % 8) * 8;
+              for (int i = tid / 8; i < cnt; i += 16) {
+                float g[8] = {}, u[8] = {};
+                for (int c = first; c <= last; ++c) {
+                  const float* at = part_rows(p, 0, c, c == first ? 1 : 0) + i * kCols;
+                  add8(at + c8, g);
+                  add8(at + 64 + c8, u);
+                }
+                store_h<T>(p, r.list[start + i], q.col * 64 + c8, g, u);
+              }
+              if (tid == 0) p.sum1[q.tile] = 0;
+              stored = true;
+            }
+          }
+          if (stored) {
+            fence_proxy_async_global();
+            __threadfence();
+            epi_sync();
+            if (tid == 0) st_release(p.done + q.tile, 1);
+          }
+        } else {
+          __threadfence();
+          epi_sync();
+          bool last = false;
+          if (tid < cnt) {
+            const int t = r.list[start + tid] / p.K;
+            last = atomicAdd(p.sum2 + static_cast<int64_t>(t) * f.cols + q.col, blocks) + blocks == r.valid[t] * f.kb;
+          }
+          const uint32_t mask = __ballot_sync(0xffffffffu, last);
+          if (lane == 0) s.last_tokens[ew] = mask;
+          __threadfence();
+          epi_sync();
+          int seen = 0;
+          for (int g = 0; g < (cnt + 31) / 32; ++g) {
+            for (uint32_t m = s.last_tokens[g]; m != 0u; m &= m - 1u, ++seen) {
+              if ((seen & 3) != ew) continue;
+              const int t = r.list[start + g * 32 + __ffs(m) - 1] / p.K;
+              combine_token<T>(p, r, f, t, q.col, lane);
+              if (lane == 0) p.sum2[static_cast<int64_t>(t) * f.cols + q.col] = 0;
+            }
+          }
+        }
+        b += blocks;
+      }
+    }
+    // tokens none of whose slots names an expert
+    for (int t = blockIdx.x; t < p.n; t += gridDim.x) {
+      if (r.valid[t] != 0) continue;
+      for (int c = tid; c < p.D; c += 128) {
+        const T v = p.res != nullptr ? static_cast<const T*>(p.res)[t * p.ldres + c] : from_f32<T>(0.0f);
+        static_cast<T*>(p.out)[t * p.ldout + c] = v;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, 2 * p.nt);
+  }
+}
+
+// 16-bit [outer][mid][inner], boxes of 64 x `box` x 1.
+bool map3(CUtensorMap* m, const void* base, uint64_t inner, uint64_t mid, uint64_t outer) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {inner, mid, outer}, strides[2] = {inner * 2, inner * mid * 2};
+  const cuuint32_t box[3] = {64, kBlockK, 1}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// 16-bit rows for four-row gathers: a box is 64 columns of one row.
+bool map_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {inner, rows}, strides[1] = {ld * 2};
+  const cuuint32_t box[2] = {64, 1}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tokens of a tile at most.  Up to 64, so that a stage's rows leave 128 KB of
+// the ring to the weights; an expert with more tokens reads its weights again.
+int tile_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+
+constexpr int kMaxGrid = 192;  // CTAs that the workspace has room for: no device of this kind has more SMs
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+// Workspace: counters (zero between calls; placed by the capacity, not by a
+// call's tokens), then the data.
+struct Layout {
+  size_t done, sum1, sum2, h, y, part, all;
+  explicit Layout(const moe_dims& d) {
+    const size_t R = static_cast<size_t>(d.T) * d.K, nt = tile_tokens(d.T);
+    const size_t tiles = static_cast<size_t>(most_virtual(static_cast<int>(R), d.E, static_cast<int>(nt))) * (d.F / 64);
+    done = 256;
+    sum1 = done + up(tiles * 4);
+    sum2 = sum1 + up(tiles * 4);
+    h = sum2 + up(static_cast<size_t>(d.T) * ((d.D + kCols - 1) / kCols) * 4);
+    y = h + up(R * d.F * 2);
+    part = y + up(R * d.D * 4);
+    all = part + up(static_cast<size_t>(kMaxGrid) * 4 * nt * kCols * 4);
+  }
+};
+
+}  // namespace
+
+size_t decode_ws_bytes(const moe_dims& d) { return Layout(d).all; }
+
+template <typename T>
+static cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
+  const moe_dims& d = c.d;
+  Params p{};
+  p.logits = c.logits;
+  p.bias = c.bias;
+  p.ids_in = c.ids;
+  p.w_in = c.w;
+  p.ids_out = c.ids_out;
+  p.w_out = c.w_out;
+  p.res = c.res;
+  p.ldres = c.ldres;
+  p.out = c.out;
+  p.ldout = c.ldout;
+  p.n = c.n;
+  p.D = d.D;
+  p.E = d.E;
+  p.K = d.K;
+  p.F = d.F;
+  p.mode = c.mode;
+  p.nt = tile_tokens(d.T);
+  p.type = c.type == MOE_BF16 ? 1u : 0u;
+  p.status = c.dev_status;
+  p.limit_ns = kDefaultWaitLimitNs;
+  const int grid = std::min(sm_count(), kMaxGrid);
+  const Layout at(d);
+  uint8_t* ws = static_cast<uint8_t*>(c.ws);
+  p.leave = reinterpret_cast<int32_t*>(ws);
+  p.done = reinterpret_cast<int32_t*>(ws + at.done);
+  p.sum1 = reinterpret_cast<int32_t*>(ws + at.sum1);
+  p.sum2 = reinterpret_cast<int32_t*>(ws + at.sum2);
+  p.h = ws + at.h;
+  p.y = reinterpret_cast<float*>(ws + at.y);
+  p.part = reinterpret_cast<float*>(ws + at.part);
+  const size_t R = static_cast<size_t>(c.n) * d.K;
+  const size_t fixed = 1024 + kBufBytes + sizeof(Ctl) + route_bytes(static_cast<int>(R), d.E, c.n, p.nt);
+  const size_t stage = kWeightStage + static_cast<size_t>(p.nt) * kBlockK * 2;
+  p.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemLimit - fixed) / stage));
+  if (p.stages < kMinStages) return cudaErrorInvalidValue;
+  CUtensorMap wi, wo, x, h;
+  if (!map3(&wi, c.wi, 2 * static_cast<uint64_t>(d.F), d.D, d.E) || !map3(&wo, c.wo, d.D, d.F, d.E) ||
+      !map_rows(&x, c.x, d.D, c.n, c.ldx) || !map_rows(&h, p.h, d.F, R, d.F))
+    return cudaErrorInvalidValue;
+  static std::atomic<bool> attr_set[64];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    err = cudaFuncSetAttribute(decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kSmemLimit));
+    if (err != cudaSuccess) return err;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = fixed + p.stages * stage;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_kernel<T>, wi, wo, x, h, p);
+}
+
+cudaError_t launch_decode(const DecodeCall& c, cudaStream_t s) {
+  return c.type == MOE_BF16 ? launch_typed<__nv_bfloat16>(c, s) : launch_typed<__half>(c, s);
+}
+
+}  // namespace moe

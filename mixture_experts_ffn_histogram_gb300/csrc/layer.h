@@ -101,4 +101,29 @@ struct ActGradCall {
 };
 cudaError_t launch_act_grad(const ActGradCall& c, cudaStream_t s);
 
+// The expert layer for a few tokens: d.T is the capacity that the workspace
+// was made for, n <= d.T the call's tokens.
+struct DecodeCall {
+  const void* x;
+  int64_t ldx;
+  const void *wi, *wo;
+  const float *logits, *bias;
+  const int32_t* ids;
+  const float* w;
+  int32_t* ids_out;
+  float* w_out;
+  const void* res;
+  int64_t ldres;
+  void* out;
+  int64_t ldout;
+  int32_t* dev_status;
+  void* ws;
+  int32_t n;
+  moe_dims d;
+  int mode;
+  moe_dtype type;
+};
+size_t decode_ws_bytes(const moe_dims& d);
+cudaError_t launch_decode(const DecodeCall& c, cudaStream_t s);
+
 }  // namespace moe

@@ -59,6 +59,16 @@ moe_status check_linear(const moe_linear_dims& d) {
   return MOE_OK;
 }
 
+moe_status check_decode(const moe_dims& d, int type) {
+  if (!is_dtype(type)) return MOE_ERR_INVALID_ARG;
+  if (type == MOE_FP32) return MOE_ERR_UNSUPPORTED;
+  if (d.D < 64 || d.D > 16384 || d.D % 64 != 0 || d.F < 64 || d.F > 16384 || d.F % 64 != 0)
+    return MOE_ERR_UNSUPPORTED;
+  if (d.E < 1 || d.E > 1024 || d.K < 1 || d.K > 32 || d.K > d.E || d.T < 0 || d.T > 256)
+    return MOE_ERR_UNSUPPORTED;
+  return d.T * d.K <= 2048 ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
 // Workspace of the linear backward: dz [M, N], then the partial column sums.
 size_t dz_bytes(const moe_linear_dims& d) {
   const bool own = d.act != MOE_ACT_NONE || d.out_type != d.type;
@@ -210,6 +220,56 @@ moe_status moe_linear(moe_mat x, moe_mat w, const float* bias, moe_mat res, moe_
   c.act = d.act;
   c.dev_status = dev_status;
   return from_cuda(moe::launch_dense(c, stream));
+}
+
+size_t moe_decode_workspace_bytes(moe_dims d) {
+  return check_decode(d, MOE_BF16) == MOE_OK ? moe::decode_ws_bytes(d) : 0;
+}
+
+moe_status moe_decode(moe_mat x, const void* wi, const void* wo, const float* logits, const float* bias,
+                      moe_score_mode mode, int32_t* ids, float* w, moe_mat res, moe_mat out,
+                      int32_t* dev_status, void* ws, int32_t n, moe_dims d, moe_dtype type,
+                      cudaStream_t stream) {
+  const moe_status st = check_decode(d, type);
+  if (st != MOE_OK) return st;
+  if (mode != MOE_SCORE_SOFTMAX_TOPK && mode != MOE_SCORE_SIGMOID_NORM && mode != MOE_SCORE_GIVEN)
+    return MOE_ERR_INVALID_ARG;
+  if (n < 0 || n > d.T) return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  const auto given = [](const void* p) { return p != nullptr && aligned(p, 16); };
+  if (!vector_mat(x, d.D, type) || !vector_mat(out, d.D, type) || !given(wi) || !given(wo) || !given(ws))
+    return MOE_ERR_INVALID_ARG;
+  if (res.p != nullptr && !vector_mat(res, d.D, type)) return MOE_ERR_INVALID_ARG;
+  // read and written element by element
+  if (!aligned(ids, 4) || !aligned(w, 4) || !aligned(logits, 4) || !aligned(bias, 4) || !aligned(dev_status, 4))
+    return MOE_ERR_INVALID_ARG;
+  const bool chosen = mode == MOE_SCORE_GIVEN;  // by the caller
+  if (chosen ? ids == nullptr || w == nullptr : logits == nullptr) return MOE_ERR_INVALID_ARG;
+  moe::DecodeCall c{};
+  c.x = x.p;
+  c.ldx = x.ld;
+  c.wi = wi;
+  c.wo = wo;
+  c.logits = logits;
+  c.bias = bias;
+  if (chosen) {
+    c.ids = ids;
+    c.w = w;
+  } else {
+    c.ids_out = ids;
+    c.w_out = w;
+  }
+  c.res = res.p;
+  c.ldres = res.ld;
+  c.out = out.p;
+  c.ldout = out.ld;
+  c.dev_status = dev_status;
+  c.ws = ws;
+  c.n = n;
+  c.d = d;
+  c.mode = mode;
+  c.type = type;
+  return from_cuda(moe::launch_decode(c, stream));
 }
 
 size_t moe_linear_workspace_bytes(moe_linear_dims d) {

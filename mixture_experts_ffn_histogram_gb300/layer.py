@@ -336,6 +336,75 @@ class Linear:
         return self._dx if n == self.M else self._dx[:n]
 
 
+class MoEDecode:
+    """The whole expert layer for up to T tokens, a few (T <= 256): routing,
+    both expert products with SwiGLU and the weighted combine, in one kernel
+    that reads the weights of the experts named, once.
+
+    ``score_mode`` and the routing arguments are ``MoEBlock``'s: logits (and
+    bias), or ids and w of a router's own (``SCORE_GIVEN``).  ``forward``
+    returns out = experts(x) + res for bf16 or fp16 rows; ``ids`` and ``w``
+    hold the selection.  ``status`` is MoEBlock's: an id outside [0, E) is
+    reported there and its slot dropped.  Longer batches and training:
+    ``MoEBlock``."""
+
+    def __init__(self, T, D, E, K, F, score_mode=B.SCORE_SOFTMAX_TOPK, dtype=torch.bfloat16,
+                 device="cuda"):
+        if score_mode not in (B.SCORE_SOFTMAX_TOPK, B.SCORE_SIGMOID_NORM, B.SCORE_GIVEN):
+            raise ValueError(f"unknown score mode {score_mode!r}")
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"an expert layer of {dtype} is not supported")
+        self.T, self.D, self.E, self.K, self.F = T, D, E, K, F
+        self.mode, self.dtype = score_mode, dtype
+        self.d = B.dims(T, D, E, K, F)
+        need = B.moe_decode_workspace_bytes(self.d)
+        if need == 0:
+            raise ValueError(f"unsupported sizes: {self.d} (T <= 256, T * K <= 2048, K <= min(E, 32), "
+                             "E <= 1024, D and F multiples of 64 up to 16384)")
+        dev = torch.device(device)
+        self._out = torch.empty((T, D), dtype=dtype, device=dev)
+        self.device = dev = self._out.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+        self._given = score_mode == B.SCORE_GIVEN
+        self.ids = self.w = None
+        if not self._given:
+            self._ids = torch.empty((T, K), dtype=torch.int32, device=dev)
+            self._w = torch.empty((T, K), dtype=torch.float32, device=dev)
+        self._mout, self._p_status, self._p_ws = _own(self._out), self.status.data_ptr(), self.ws.data_ptr()
+        f32 = torch.float32
+        self._x, self._res = _Arg("x", dtype, dev), _Arg("res", dtype, dev)
+        self._wi, self._wo = (_Arg(n, dtype, dev, contiguous=True) for n in ("wi", "wo"))
+        self._l, self._b = (_Arg(n, f32, dev, contiguous=True) for n in ("logits", "bias"))
+        self._i, self._win = _Arg("ids", torch.int32, dev, contiguous=True), _Arg("w", f32, dev, contiguous=True)
+        self._wishape, self._woshape = (E, D, 2 * F), (E, F, D)
+        self._type, self._fwd = B.DTYPES[dtype], _entry("moe_decode", dev)
+
+    def forward(self, x, wi, wo, logits=None, bias=None, ids=None, w=None, res=None, stream=None):
+        n = self._x.first(x, self.T, self.D)
+        pwi, pwo = self._wi.pointer(wi, self._wishape), self._wo.pointer(wo, self._woshape)
+        pl = pb = None
+        slots = (n, self.K)
+        if self._given:
+            if ids is None or w is None:
+                raise ValueError("the layer was built for a given selection: it needs ids and w")
+            pi, pw = self._i.pointer(ids, slots), self._win.pointer(w, slots)
+        else:
+            if logits is None:
+                raise ValueError("the layer selects the experts itself: it needs logits")
+            pl = self._l.pointer(logits, (n, self.E))
+            pb = None if bias is None else self._b.pointer(bias, (self.E,))
+            ids, w = self._ids[:n], self._w[:n]
+            pi, pw = ids.data_ptr(), w.data_ptr()
+        mres = _NO if res is None else self._res.matrix(res, (n, self.D))
+        st = self._fwd(self._x.mat, pwi, pwo, pl, pb, self.mode, pi, pw, mres, self._mout, self._p_status,
+                       self._p_ws, n, self.d, self._type, B.stream_of(stream, self.device))
+        if st:
+            _refused("moe_decode", st)
+        self.ids, self.w = ids, w
+        return self._out if n == self.T else self._out[:n]
+
+
 class MoELayer:
     """A pre-norm feed-forward layer: routed experts beside a shared dense one.
 
