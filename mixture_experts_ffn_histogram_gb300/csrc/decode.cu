@@ -1,5 +1,5 @@
-// The expert layer for a few tokens, in one kernel: routing, FC1 with SwiGLU,
-// FC2 and the weighted combine (with a residual).
+// The expert layer for a few tokens, in two kernels: routing, FC1 with SwiGLU
+// and FC2, then the weighted combine (with a residual).
 //
 //   ids, p = top-K of the scores, or given     z[t,k] = x[t] . wi[e_tk]
 //   h[t,k] = silu(z[:F]) z[F:]                 out[t] = sum_k p_tk h[t,k] . wo[e_tk] + res[t]
@@ -7,21 +7,22 @@
 // With a few tokens the layer is bound by reading the weights of the experts
 // that the tokens name, each once.  So the weights' columns are the 128 side
 // of the MMA and the expert's tokens its narrow side (16 to 64), and the work
-// is cut by weight bytes alone: a phase is a list of 64-deep blocks of 128
-// weight columns (16 KB each), expert by expert, and each of the grid's CTAs
-// (one to an SM) takes an equal run of it, FC1's list and then FC2's, through
-// one ring of shared memory that keeps 128 KB or more under way (with 32 KB an
-// SM streams at two thirds of the rate).  Whole tiles to a CTA would leave a
-// tenth to a third of the SMs idle in the last wave, since a token names some
-// 90 tiles and 64 tokens some ten times that.  Runs begin and end inside a
-// tile; the CTA that adds a tile's last part joins the parts, in the order of
-// the reduction, so that results do not depend on who was last.
+// is cut by weight bytes alone: a phase is a list of tiles of 128 weight
+// columns (64 of gate and 64 of up, or 128 of wo), expert by expert, each a
+// row of 64-deep blocks of 16 KB.  Each of the grid's CTAs (one to an SM)
+// takes every so manieth tile as long as there is one for each, so that
+// neighbouring columns are read at the same time; the tiles that are left (all
+// of them for one token, some 90) are cut into equal runs of blocks, which
+// begin and end inside a tile.  Whole tiles alone would leave a tenth to a
+// third of the SMs idle in the last wave.  Parts of a tile are joined in the
+// order of the reduction, so results do not depend on who was last.
 //
-// FC2's weights start to stream as soon as FC1's have been issued; only the
-// rows of h wait, tile by tile, for the flags that FC1's epilogue sets.  Every
-// CTA routes all tokens for itself (a few hundred scores a warp), which costs
-// less than handing the result around.  The launch is cooperative: the CTAs
-// wait (bounded) for one another's flags, so all have to be resident.
+// One ring of shared memory carries both phases' blocks and keeps 128 KB or
+// more under way (with 32 KB an SM streams at two thirds of the rate): FC2's
+// weights start to stream as soon as FC1's have been asked for, and only the
+// rows of h wait, block by block, for the flags that FC1's epilogue sets.  The
+// launch is cooperative: CTAs wait (bounded) for one another's flags, so all
+// have to be resident.
 //
 // h is rounded to the operands' type: the tensor core multiplies no wider one,
 // and its error, half a step on each of F terms of both signs, stays below the
@@ -58,9 +59,6 @@ struct Params {
   const int32_t* ids_in;
   int32_t* ids_out;
   float* w_out;
-  const void* res;
-  void* out;
-  int64_t ldres, ldout;
   int n, D, E, K, F;  // n: tokens of this call
   int mode;
   int nt, stages;     // tokens of a tile at most (16, 32 or 64)
@@ -68,10 +66,13 @@ struct Params {
   void* h;            // [n * K][F]
   float* y;           // [n * K][D]: FC2's rows of tiles that one CTA summed alone
   float* part;        // [2 phases][CTA][head, tail][nt][128]: sums of parts of tiles
+  uint2* slots;       // [n * K]: for the combine (slot_word, the weight's bits); [n * K].x: virtual experts
+  int32_t* gids;      // [n * K] and its weights: selections that the CTAs exchange
+  float* gw;
   int32_t* leave;     // CTAs that read no more flags
+  int32_t* routed;    // tokens whose selection is stored
   int32_t* done;      // [tile of FC1]: its h is stored
-  int32_t* sum1;      // [tile of FC1]: blocks summed so far
-  int32_t* sum2;      // [token][tile of FC2]
+  int32_t* sum;       // [tile of FC1]: blocks summed so far
   int32_t* status;
   uint64_t limit_ns;
 };
@@ -85,33 +86,31 @@ struct Ctl {
   uint32_t tmem_base;
   int abort_flag;
   int last;
-  uint32_t last_tokens[4];
-  int tiles;  // virtual experts: expert and up to nt of its slots
+  uint2 warp_sums[kThreads / 32];
 };
 
-// The routing, in shared memory.  Slot j = t * K + k.  Experts are numbered in
-// the order in which the slots first name them (`ord`), and an expert with
-// more than nt slots makes several entries of the list that the tiles follow
-// ("virtual experts").
+// The routing, in shared memory.  Slot j = t * K + k.  An expert with more than
+// nt slots makes several entries of the list that the tiles follow ("virtual
+// experts").
 struct Route {
   float* w;                                  // [R]
   uint16_t *expert, *rank, *at, *list;       // [R]; at: the slot's virtual expert
   uint16_t *vexp, *vstart, *vcnt;            // [V]
-  uint16_t *ord, *ocnt, *obase, *ostart, *oexp;
-  uint16_t* valid;                           // [n]: slots of a token that name an expert
+  uint16_t* before;                          // [warps][E]: slots of the expert in the warps ahead
+  uint16_t *first, *start;                   // [E]: its first virtual expert, its place in the list
 };
+constexpr int kWarps = kThreads / 32;
 __host__ __device__ inline int most_virtual(int R, int E, int nt) {
   const int v = E + R / nt;
   return v < R ? v : R;
 }
-__host__ __device__ inline size_t route_bytes(int R, int E, int n, int nt) {
-  const int o = E < R ? E : R;
-  const size_t half = 4 * static_cast<size_t>(R) + 3 * static_cast<size_t>(most_virtual(R, E, nt)) + E +
-                      4 * static_cast<size_t>(o) + n;
+__host__ __device__ inline size_t route_bytes(int R, int E, int nt) {
+  const size_t half = 4 * static_cast<size_t>(R) + 3 * static_cast<size_t>(most_virtual(R, E, nt)) +
+                      (kWarps + 2) * static_cast<size_t>(E);
   return 4 * static_cast<size_t>(R) + (half * 2 + 15) / 16 * 16;
 }
-__device__ __forceinline__ Route route_at(uint8_t* p, int R, int E, int n, int nt) {
-  const int V = most_virtual(R, E, nt), o = min(E, R);
+__device__ __forceinline__ Route route_at(uint8_t* p, int R, int E, int nt) {
+  const int V = most_virtual(R, E, nt);
   Route r;
   r.w = reinterpret_cast<float*>(p);
   uint16_t* q = reinterpret_cast<uint16_t*>(p + 4 * static_cast<size_t>(R));
@@ -127,12 +126,9 @@ __device__ __forceinline__ Route route_at(uint8_t* p, int R, int E, int n, int n
   r.vexp = take(V);
   r.vstart = take(V);
   r.vcnt = take(V);
-  r.ord = take(E);
-  r.ocnt = take(o);
-  r.obase = take(o);
-  r.ostart = take(o);
-  r.oexp = take(o);
-  r.valid = take(n);
+  r.before = take(kWarps * E);
+  r.first = take(E);
+  r.start = take(E);
   return r;
 }
 
@@ -163,6 +159,26 @@ __device__ __forceinline__ bool epi_all(bool ok) {
   return r != 0;
 }
 
+// Waits until *at is `want`, for wc's limit.
+__device__ __forceinline__ bool wait_for(const int32_t* at, int want, const WaitCtl& wc) {
+  if (ld_acquire(at) == want) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1; it < kMaxWaitIters; ++it) {
+    if (ld_acquire(at) == want) return true;
+    if ((it & 31u) == 0) {
+      if (*wc.abort) return false;
+      if (global_timer_ns() - t0 > wc.limit_ns) break;
+    }
+  }
+  *wc.abort = 1;
+  report(wc.status, MOE_ERR_TIMEOUT);
+  return false;
+}
+
+// A slot as the combine reads it: its virtual expert, its row there, and
+// whether it names an expert at all.
+__device__ __forceinline__ uint32_t slot_word(uint32_t v, uint32_t row) { return 0x80000000u | row << 16 | v; }
+
 // Four rows of a map whose box is 64 columns of one row, into 512 consecutive
 // bytes (swizzled by their address like any tile).
 __device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
@@ -187,8 +203,9 @@ __device__ __forceinline__ float score_of(uint32_t u) {
 
 // The K best of a token's E scores by one warp: K rounds of a maximum over the
 // lanes' own best, the lower expert first among equal scores.
+// Lane k < K of the warp gets slot k.
 template <int PER>
-__device__ __forceinline__ void select_token(const Params& p, const Route& r, int t, int lane) {
+__device__ __forceinline__ void select_token(const Params& p, int t, int lane, int* id, float* weight) {
   uint32_t key[PER];
   const float* row = p.logits + static_cast<int64_t>(t) * p.E;
 #pragma unroll
@@ -231,114 +248,213 @@ __device__ __forceinline__ void select_token(const Params& p, const Route& r, in
   if (lane < p.K) ex = p.mode == MOE_SCORE_SOFTMAX_TOPK ? expf(v - first) : 1.0f / (1.0f + expf(-v));
   float sum = 0.0f;  // in the slots' order
   for (int k = 0; k < p.K; ++k) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, ex, k));
-  if (lane < p.K) {
-    const int j = t * p.K + lane;
-    const float w = __fdiv_rn(ex, sum);
-    r.expert[j] = static_cast<uint16_t>(mine_e);
-    r.w[j] = w;
-    if (blockIdx.x == 0) {
-      if (p.ids_out != nullptr) p.ids_out[j] = mine_e;
-      if (p.w_out != nullptr) p.w_out[j] = w;
-    }
-  }
+  *id = mine_e;
+  *weight = __fdiv_rn(ex, sum);
+}
+__device__ __forceinline__ void select_one(const Params& p, int t, int lane, int* id, float* weight) {
+  if (p.E <= 128) select_token<4>(p, t, lane, id, weight);
+  else if (p.E <= 256) select_token<8>(p, t, lane, id, weight);
+  else select_token<32>(p, t, lane, id, weight);
 }
 
-// The list of virtual experts, by one warp: 32 slots at a time.
-__device__ __forceinline__ int build_list(const Params& p, const Route& r, int lane) {
+// Everyone's selection in r.expert and r.w.  Up to a token for each of its warps a
+// CTA selects all for itself; of more tokens each CTA selects its own, and they
+// exchange them through global memory (128 tokens of 128 experts: 42 us when
+// every CTA selected all).  False: a wait gave up.
+__device__ __forceinline__ bool select_all(const Params& p, const Route& r, const WaitCtl& wc, int warp, int lane) {
   const int R = p.n * p.K;
-  const uint32_t below = (1u << lane) - 1u;
-  int live = 0;
-  for (int base = 0; base < R; base += 32) {
-    const int j = base + lane;
+  bool ok = true;
+  if (p.mode == MOE_SCORE_GIVEN) {
+    for (int j = threadIdx.x; j < R; j += kThreads) {
+      const int e = __ldg(p.ids_in + j);
+      const bool in = e >= 0 && e < p.E;
+      r.expert[j] = in ? static_cast<uint16_t>(e) : kNone;
+      r.w[j] = __ldg(p.w_in + j);
+      if (!in && blockIdx.x == 0) report(p.status, MOE_ERR_DEVICE);
+    }
+  } else if (p.n <= kWarps) {
+    if (warp < p.n) {
+      int e;
+      float w;
+      select_one(p, warp, lane, &e, &w);
+      if (lane < p.K) {
+        const int j = warp * p.K + lane;
+        r.expert[j] = static_cast<uint16_t>(e);
+        r.w[j] = w;
+        if (blockIdx.x == 0) {
+          if (p.ids_out != nullptr) p.ids_out[j] = e;
+          if (p.w_out != nullptr) p.w_out[j] = w;
+        }
+      }
+    }
+  } else {
+    for (int t = blockIdx.x + gridDim.x * warp; t < p.n; t += gridDim.x * kWarps) {
+      int e;
+      float w;
+      select_one(p, t, lane, &e, &w);
+      if (lane < p.K) {
+        const int j = t * p.K + lane;
+        p.gids[j] = e;
+        p.gw[j] = w;
+        if (p.ids_out != nullptr) p.ids_out[j] = e;
+        if (p.w_out != nullptr) p.w_out[j] = w;
+        __threadfence();
+      }
+      __syncwarp();
+      if (lane == 0) atomicAdd(p.routed, 1);
+    }
+    if (threadIdx.x == 0) ok = wait_for(p.routed, p.n, wc);
+    ok = __syncthreads_and(ok);
+    for (int j = threadIdx.x; j < R && ok; j += kThreads) {
+      r.expert[j] = static_cast<uint16_t>(__ldcg(p.gids + j));
+      r.w[j] = __ldcg(p.gw + j);
+    }
+  }
+  return ok;
+}
+
+// The list of virtual experts, by number of expert; the slots of one in their
+// order.  Warp w ranks the slots of the w-th stretch of whole 32, then every
+// expert's counts are summed over the warps, then over the experts.
+__device__ __forceinline__ int build_list(const Params& p, const Route& r, Ctl& s, int warp, int lane) {
+  const int R = p.n * p.K, span = (R + kThreads - 1) / kThreads * 32;
+  uint16_t* mine = r.before + warp * p.E;
+  for (int j0 = warp * span; j0 < min(R, (warp + 1) * span); j0 += 32) {
+    const int j = j0 + lane;
     const int e = j < R ? r.expert[j] : kNone;
     const uint32_t peers = __match_any_sync(0xffffffffu, e);
-    const bool valid = e != kNone, lead = lane == __ffs(peers) - 1;
-    const bool fresh = valid && lead && r.ord[e] == kNone;
-    const uint32_t news = __ballot_sync(0xffffffffu, fresh);
-    if (fresh) {
-      const int o = live + __popc(news & below);
-      r.ord[e] = static_cast<uint16_t>(o);
-      r.oexp[o] = static_cast<uint16_t>(e);
-      r.ocnt[o] = 0;
+    const int ahead = e != kNone ? mine[e] : 0;
+    __syncwarp();
+    if (e != kNone) {
+      r.rank[j] = static_cast<uint16_t>(ahead + __popc(peers & ((1u << lane) - 1u)));
+      if (lane == __ffs(peers) - 1) mine[e] = static_cast<uint16_t>(ahead + __popc(peers));
     }
     __syncwarp();
-    const int o = valid ? r.ord[e] : 0;
-    const int before = valid ? r.ocnt[o] : 0;
-    __syncwarp();
-    if (valid) {
-      r.rank[j] = static_cast<uint16_t>(before + __popc(peers & below));
-      if (lead) r.ocnt[o] = static_cast<uint16_t>(before + __popc(peers));
-    }
-    __syncwarp();
-    live += __popc(news);
   }
-  int entries = 0, slots = 0;
-  for (int base = 0; base < live; base += 32) {
-    const int o = base + lane;
-    const int c = o < live ? r.ocnt[o] : 0, v = (c + p.nt - 1) / p.nt;
-    int sc = c, sv = v;
+  __syncthreads();
+  // a thread's experts: counts over the warps become what lies ahead of each
+  const int per = (p.E + kThreads - 1) / kThreads, e0 = min(static_cast<int>(threadIdx.x) * per, p.E);
+  const int e1 = min(e0 + per, p.E);
+  int slots = 0, lists = 0;
+  for (int e = e0; e < e1; ++e) {
+    int sum = 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, sc, d), b = __shfl_up_sync(0xffffffffu, sv, d);
-      if (lane >= d) {
-        sc += a;
-        sv += b;
-      }
+    for (int w = 0; w < kWarps; ++w) {
+      const int c = r.before[w * p.E + e];
+      r.before[w * p.E + e] = static_cast<uint16_t>(sum);
+      sum += c;
     }
-    if (o < live) {
-      const int start = slots + sc - c, first = entries + sv - v;
-      r.ostart[o] = static_cast<uint16_t>(start);
-      r.obase[o] = static_cast<uint16_t>(first);
-      for (int i = 0; i < v; ++i) {
-        r.vexp[first + i] = r.oexp[o];
-        r.vstart[first + i] = static_cast<uint16_t>(start + i * p.nt);
-        r.vcnt[first + i] = static_cast<uint16_t>(min(p.nt, c - i * p.nt));
-      }
-    }
-    slots += __shfl_sync(0xffffffffu, sc, 31);
-    entries += __shfl_sync(0xffffffffu, sv, 31);
+    r.start[e] = static_cast<uint16_t>(sum);  // the count, until its place is known
+    slots += sum;
+    lists += (sum + p.nt - 1) / p.nt;
   }
+  int ss = slots, sl = lists;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, ss, d), b = __shfl_up_sync(0xffffffffu, sl, d);
+    if (lane >= d) {
+      ss += a;
+      sl += b;
+    }
+  }
+  if (lane == 31) s.warp_sums[warp] = make_uint2(ss, sl);
+  __syncthreads();
+  int entries = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const uint2 q = s.warp_sums[w];
+    if (w < warp) {
+      ss += q.x;
+      sl += q.y;
+    }
+    entries += q.y;
+  }
+  int at = ss - slots, v = sl - lists;
+  for (int e = e0; e < e1; ++e) {
+    const int count = r.start[e];
+    r.start[e] = static_cast<uint16_t>(at);
+    r.first[e] = static_cast<uint16_t>(v);
+    for (int c = 0; c < count; c += p.nt, ++v) {
+      r.vexp[v] = static_cast<uint16_t>(e);
+      r.vstart[v] = static_cast<uint16_t>(at + c);
+      r.vcnt[v] = static_cast<uint16_t>(min(p.nt, count - c));
+    }
+    at += count;
+  }
+  __syncthreads();
+  for (int j0 = warp * span; j0 < min(R, (warp + 1) * span); j0 += 32) {
+    const int j = j0 + lane;
+    if (j >= R) break;
+    const int e = r.expert[j];
+    const int rank = e != kNone ? r.rank[j] + mine[e] : 0;
+    if (e != kNone) {
+      r.list[r.start[e] + rank] = static_cast<uint16_t>(j);
+      r.at[j] = static_cast<uint16_t>(r.first[e] + rank / p.nt);
+    }
+    if (blockIdx.x == 0) p.slots[j] = make_uint2(e != kNone ? slot_word(r.at[j], rank & (p.nt - 1)) : 0u, __float_as_uint(r.w[j]));
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.slots[R] = make_uint2(entries, 0u);
   return entries;
 }
 
-// One phase's list of blocks, and this CTA's run of it.
+// One phase's tiles and blocks.  (At most 1056 virtual experts of 256 tiles; the
+// blocks cut into runs are of fewer tiles than CTAs: 32 bits hold all products.)
+constexpr uint32_t kLeastBlocks = 4;  // of a run: shorter ones cost more to join than they save
 struct Phase {
-  int kb;     // blocks of a tile
-  int cols;   // tiles of a virtual expert
-  int64_t all, b0, b1;
-  int64_t ctas;  // no more than blocks: every one of them has a run
-  __device__ __forceinline__ Phase(const Params& p, int which, int entries) {
-    kb = which == 0 ? p.D / kBlockK : p.F / kBlockK;
-    cols = which == 0 ? p.F / 64 : (p.D + kCols - 1) / kCols;
-    all = static_cast<int64_t>(entries) * cols * kb;
-    ctas = min(static_cast<int64_t>(gridDim.x), all);
-    b0 = b1 = 0;
-    if (blockIdx.x < ctas) {
-      b0 = all * blockIdx.x / ctas;
-      b1 = all * (blockIdx.x + 1) / ctas;
-    }
+  uint32_t kb;                       // blocks of a tile
+  uint32_t cols;                     // tiles of a virtual expert
+  uint32_t grid, waves;              // every CTA takes `waves` whole tiles
+  uint32_t blocks, ctas;             // of the tiles behind them; the CTAs that take runs of these
+  __device__ __forceinline__ Phase(int D, int F, uint32_t grid, int which, uint32_t entries) : grid(grid) {
+    kb = (which == 0 ? D : F) / kBlockK;
+    cols = which == 0 ? F / 64 : (D + kCols - 1) / kCols;
+    const uint32_t tiles = entries * cols;
+    waves = tiles / grid;
+    blocks = (tiles - waves * grid) * kb;
+    ctas = min(grid, (blocks + kLeastBlocks - 1) / kLeastBlocks);
   }
+  __device__ __forceinline__ uint32_t run(uint32_t c) const { return blocks * c / ctas; }
   // the CTA whose run holds block b
-  __device__ __forceinline__ int owner(int64_t b) const {
-    return static_cast<int>((static_cast<uint64_t>(b + 1) * ctas - 1) / static_cast<uint64_t>(all));
-  }
+  __device__ __forceinline__ uint32_t owner(uint32_t b) const { return ((b + 1) * ctas - 1) / blocks; }
 };
 // A part of a tile: blocks [k0, k1) of tile `col` of virtual expert `v`.
 struct Piece {
-  int tile, v, col, k0, k1;
-  __device__ __forceinline__ Piece(const Phase& f, int64_t b) {
-    tile = static_cast<int>(b / f.kb);
-    k0 = static_cast<int>(b - static_cast<int64_t>(tile) * f.kb);
-    k1 = static_cast<int>(min(static_cast<int64_t>(f.kb), k0 + (f.b1 - b)));
-    v = tile / f.cols;
-    col = tile - v * f.cols;
+  uint32_t tile, v, col;
+  int k0, k1;
+};
+// The CTA's pieces in their order.
+struct Walk {
+  uint32_t wave, b, end;
+  __device__ __forceinline__ explicit Walk(const Phase& f) : wave(0), b(0), end(0) {
+    if (blockIdx.x < f.ctas) {
+      b = f.run(blockIdx.x);
+      end = f.run(blockIdx.x + 1);
+    }
   }
-  __device__ __forceinline__ bool whole(const Phase& f) const { return k0 == 0 && k1 == f.kb; }
+  __device__ __forceinline__ bool next(const Phase& f, Piece& q) {
+    if (wave < f.waves) {
+      q.tile = wave * f.grid + blockIdx.x;
+      q.k0 = 0;
+      q.k1 = static_cast<int>(f.kb);
+      ++wave;
+    } else if (b < end) {
+      const uint32_t t = b / f.kb;
+      q.tile = f.waves * f.grid + t;
+      q.k0 = static_cast<int>(b - t * f.kb);
+      q.k1 = static_cast<int>(min(f.kb, q.k0 + (end - b)));
+      b += q.k1 - q.k0;
+    } else {
+      return false;
+    }
+    q.v = q.tile / f.cols;
+    q.col = q.tile - q.v * f.cols;
+    return true;
+  }
 };
 // Where CTA c keeps the sums of a part that starts its tile (tail = 1: it is
-// the CTA's last part) or not (tail = 0: its first).
-__device__ __forceinline__ float* part_rows(const Params& p, int phase, int c, int tail) {
-  return p.part + ((static_cast<int64_t>(phase) * gridDim.x + c) * 2 + tail) * p.nt * kCols;
+// the last of the CTA's run) or not (tail = 0: its first).
+__device__ __forceinline__ float* part_rows(float* part, uint32_t grid, int nt, int phase, uint32_t c, int tail) {
+  return part + ((static_cast<int64_t>(phase) * grid + c) * 2 + tail) * nt * kCols;
 }
 
 template <typename T>
@@ -360,57 +476,88 @@ __device__ __forceinline__ void add8(const float* at, float (&f)[8]) {
 }
 
 // out[t, 128 col ..] by one warp, four columns a lane: the token's slots in
-// order, each the sum of its tile's parts in the reduction's order.
+// order, each the sum of its tile's parts in the reduction's order.  The
+// first kernel's tables and sums are read by ordinary loads (see
+// wait_for_previous).
+struct CombineParams {
+  const uint2* slots;
+  const float *y, *part;
+  const void* res;
+  void* out;
+  int64_t ldres, ldout;
+  int n, D, F, K, nt;
+  uint32_t grid;  // of the first kernel
+};
+constexpr int kCombineWarps = 4;
 template <typename T>
-__device__ __forceinline__ void combine_token(const Params& p, const Route& r, const Phase& f, int t, int col,
-                                              int lane) {
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const CombineParams p) {
   constexpr int kAhead = 8;
+  const int lane = threadIdx.x & 31;
+  const int tiles = (p.D + kCols - 1) / kCols;
+  const int unit = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+  const int t = unit / tiles, col = unit - t * tiles;
+  wait_for_previous();
+  if (t >= p.n) return;
   const int c4 = col * kCols + lane * 4;
   const bool in = c4 < p.D;
-  // lane k looks at slot k: its first and last CTA, its row in their parts
-  int first = 0, last = 0, idx = 0;
+  const Phase f(p.D, p.F, p.grid, 1, __ldcg(&p.slots[static_cast<int64_t>(p.n) * p.K].x));
+  float r4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.res != nullptr && in) {
+    const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.res) + t * p.ldres + c4);
+    const float2 lo = unpack_pair(q.x, T{}), hi = unpack_pair(q.y, T{});
+    r4[0] = lo.x, r4[1] = lo.y, r4[2] = hi.x, r4[3] = hi.y;
+  }
+  // lane k looks at slot k: the CTAs of its tile's first and last part (the
+  // same where one summed it alone) and its row in their parts
+  uint32_t first = 0, last = 0, row = 0;
   float w = 0.0f;
   bool valid = false;
   if (lane < p.K) {
-    const int j = t * p.K + lane;
-    valid = r.expert[j] != kNone;
-    if (valid) {
-      const int64_t tile = static_cast<int64_t>(r.at[j]) * f.cols + col;
-      first = f.owner(tile * f.kb);
-      last = f.owner(tile * f.kb + f.kb - 1);
-      idx = r.rank[j] & (p.nt - 1);
-      w = r.w[j];
+    const uint2 q = __ldcg(p.slots + static_cast<int64_t>(t) * p.K + lane);
+    valid = (q.x & 0x80000000u) != 0u;
+    w = __uint_as_float(q.y);
+    row = (q.x >> 16) & 0xffu;
+    const uint32_t tile = (q.x & 0xffffu) * f.cols + col;
+    if (valid && tile >= f.waves * f.grid) {
+      const uint32_t b = (tile - f.waves * f.grid) * f.kb;
+      first = f.owner(b);
+      last = f.owner(b + f.kb - 1);
     }
   }
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const auto part = [&](uint32_t c, int tail, uint32_t at) {
+    return __ldcg(reinterpret_cast<const float4*>(part_rows(const_cast<float*>(p.part), p.grid, p.nt, 1, c, tail) +
+                                                  at * kCols + lane * 4));
+  };
   for (int k0 = 0; k0 < p.K; k0 += kAhead) {
     float4 a[kAhead], b[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int k = min(k0 + i, p.K - 1);
-      const int c0 = __shfl_sync(0xffffffffu, first, k), c1 = __shfl_sync(0xffffffffu, last, k);
-      const int row = __shfl_sync(0xffffffffu, idx, k);
+      const uint32_t c0 = __shfl_sync(0xffffffffu, first, k), c1 = __shfl_sync(0xffffffffu, last, k);
+      const uint32_t at = __shfl_sync(0xffffffffu, row, k);
       const bool named = __shfl_sync(0xffffffffu, valid ? 1 : 0, k) != 0;
-      a[i] = b[i] = zero;
+      a[i] = b[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (named && in && k0 + i < p.K) {
-        const float* at = c0 == c1 ? p.y + (static_cast<int64_t>(t) * p.K + k) * p.D + c4
-                                   : part_rows(p, 1, c0, 1) + row * kCols + lane * 4;
-        a[i] = __ldcg(reinterpret_cast<const float4*>(at));
-        if (c0 != c1) b[i] = __ldcg(reinterpret_cast<const float4*>(part_rows(p, 1, c0 + 1, 0) + row * kCols + lane * 4));
+        if (c0 == c1) {
+          a[i] = __ldcg(reinterpret_cast<const float4*>(p.y + (static_cast<int64_t>(t) * p.K + k) * p.D + c4));
+        } else {
+          a[i] = part(c0, 1, at);
+          b[i] = part(c0 + 1, 0, at);
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int k = min(k0 + i, p.K - 1);
-      const int c0 = __shfl_sync(0xffffffffu, first, k), c1 = __shfl_sync(0xffffffffu, last, k);
-      const int row = __shfl_sync(0xffffffffu, idx, k);
+      const uint32_t c0 = __shfl_sync(0xffffffffu, first, k), c1 = __shfl_sync(0xffffffffu, last, k);
+      const uint32_t at = __shfl_sync(0xffffffffu, row, k);
       const float wk = __shfl_sync(0xffffffffu, w, k);
       const bool named = __shfl_sync(0xffffffffu, valid ? 1 : 0, k) != 0;
-      if (!named || k0 + i >= p.K) continue;
+      if (!named || k0 + i >= p.K) continue;  // a slot left out: whatever its weight
       float4 s = make_float4(a[i].x + b[i].x, a[i].y + b[i].y, a[i].z + b[i].z, a[i].w + b[i].w);
-      for (int c = c0 + 2; c <= c1 && in; ++c) {
-        const float4 q = __ldcg(reinterpret_cast<const float4*>(part_rows(p, 1, c, 0) + row * kCols + lane * 4));
+      for (uint32_t c = c0 + 2; c <= c1 && in; ++c) {
+        const float4 q = part(c, 0, at);
         s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
       }
       acc[0] = fmaf(wk, s.x, acc[0]);
@@ -420,13 +567,8 @@ __device__ __forceinline__ void combine_token(const Params& p, const Route& r, c
     }
   }
   if (!in) return;
-  if (p.res != nullptr) {
-    const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.res) + t * p.ldres + c4);
-    const float2 lo = unpack_pair(q.x, T{}), hi = unpack_pair(q.y, T{});
-    acc[0] += lo.x, acc[1] += lo.y, acc[2] += hi.x, acc[3] += hi.y;
-  }
   *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + t * p.ldout + c4) =
-      make_uint2(pack_pair(acc[0], acc[1], T{}), pack_pair(acc[2], acc[3], T{}));
+      make_uint2(pack_pair(acc[0] + r4[0], acc[1] + r4[1], T{}), pack_pair(acc[2] + r4[2], acc[3] + r4[3], T{}));
 }
 
 template <typename T>
@@ -439,8 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int stage_bytes = kWeightStage + p.nt * kBlockK * 2;
   float* buf = reinterpret_cast<float*>(ring + p.stages * stage_bytes);
   Ctl& s = *reinterpret_cast<Ctl*>(reinterpret_cast<uint8_t*>(buf) + kBufBytes);
-  const int R = p.n * p.K;
-  const Route r = route_at(reinterpret_cast<uint8_t*>(&s) + sizeof(Ctl), R, p.E, p.n, p.nt);
+  const Route r = route_at(reinterpret_cast<uint8_t*>(&s) + sizeof(Ctl), p.n * p.K, p.E, p.nt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -464,47 +605,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc<1>(&s.tmem_base, 2 * p.nt);
     tmem_relinquish<1>();
   }
-  for (int e = threadIdx.x; e < p.E; e += kThreads) r.ord[e] = kNone;
-  if (p.mode == MOE_SCORE_GIVEN) {
-    for (int j = threadIdx.x; j < R; j += kThreads) {
-      const int e = __ldg(p.ids_in + j);
-      const bool ok = e >= 0 && e < p.E;
-      r.expert[j] = ok ? static_cast<uint16_t>(e) : kNone;
-      r.w[j] = __ldg(p.w_in + j);
-      if (!ok && blockIdx.x == 0) report(p.status, MOE_ERR_DEVICE);
-    }
-  } else {
-    for (int t = warp; t < p.n; t += kThreads / 32) {
-      if (p.E <= 128) select_token<4>(p, r, t, lane);
-      else if (p.E <= 256) select_token<8>(p, r, t, lane);
-      else select_token<32>(p, r, t, lane);
-    }
-  }
+  for (int i = threadIdx.x; i < kWarps * p.E; i += kThreads) r.before[i] = 0;
+  const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
   __syncthreads();
-  if (warp == 0) {
-    const int entries = build_list(p, r, lane);
-    if (lane == 0) s.tiles = entries;
-  } else {
-    for (int t = threadIdx.x - 32; t < p.n; t += kThreads - 32) {
-      int c = 0;
-      for (int k = 0; k < p.K; ++k) c += r.expert[t * p.K + k] != kNone;
-      r.valid[t] = static_cast<uint16_t>(c);
-    }
-  }
+  const bool routed = select_all(p, r, wc, warp, lane);
   __syncthreads();
-  for (int j = threadIdx.x; j < R; j += kThreads) {
-    if (r.expert[j] != kNone) {
-      const int o = r.ord[r.expert[j]], rank = r.rank[j];
-      r.list[r.ostart[o] + rank] = static_cast<uint16_t>(j);
-      r.at[j] = static_cast<uint16_t>(r.obase[o] + rank / p.nt);
-    }
+  int entries = 0;
+  if (routed) {
+    entries = build_list(p, r, s, warp, lane);
+  } else if (blockIdx.x == 0) {  // the combine finds no slot
+    for (int j = threadIdx.x; j <= p.n * p.K; j += kThreads) p.slots[j] = make_uint2(0u, 0u);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  let_next_launch();  // the combine's blocks: they need what this kernel leaves of an SM
   const uint32_t tmem = s.tmem_base;
-  const int entries = s.tiles;
-  const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
 
   if (warp == 0) {
     // ------------------------------------------------------ weights' producer
@@ -513,9 +629,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
-        const Phase f(p, ph, entries);
-        for (int64_t b = f.b0; b < f.b1 && ok;) {
-          const Piece q(f, b);
+        const Phase f(p.D, p.F, gridDim.x, ph, entries);
+        Walk walk(f);
+        Piece q;
+        while (ok && walk.next(f, q)) {
           const int e = r.vexp[q.v];
           const int c0 = ph == 0 ? q.col * 64 : q.col * kCols;
           const int c1 = ph == 0 ? p.F + c0 : c0 + 64;
@@ -533,7 +650,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               phase ^= 1u;
             }
           }
-          b += q.k1 - q.k0;
         }
       }
       if (!ok) {  // copies in flight land before the CTA goes on
@@ -552,10 +668,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int ph = 0; ph < 2 && ok; ++ph) {
-      const Phase f(p, ph, entries);
+      const Phase f(p.D, p.F, gridDim.x, ph, entries);
+      Walk walk(f);
+      Piece q;
       const int flags = p.F / 64;  // of a virtual expert
-      for (int64_t b = f.b0; b < f.b1 && ok;) {
-        const Piece q(f, b);
+      while (ok && walk.next(f, q)) {
         const int cnt = r.vcnt[q.v], groups = (cnt + 3) / 4;
         int row[4];
 #pragma unroll
@@ -565,25 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ph == 1) {
           const int32_t* flag = p.done + static_cast<int64_t>(q.v) * flags;
-          for (int i = q.k0 + lane; i < q.k1 && ok; i += 32) {
-            if (ld_acquire(flag + i) != 0) continue;
-            const uint64_t t0 = global_timer_ns();
-            ok = false;
-            for (uint32_t it = 0; it < kMaxWaitIters; ++it) {
-              if (ld_acquire(flag + i) != 0) {
-                ok = true;
-                break;
-              }
-              if ((it & 31u) == 31u) {
-                if (*wc.abort) break;
-                if (global_timer_ns() - t0 > p.limit_ns) {
-                  *wc.abort = 1;
-                  report(p.status, MOE_ERR_TIMEOUT);
-                  break;
-                }
-              }
-            }
-          }
+          for (int i = q.k0 + lane; i < q.k1 && ok; i += 32) ok = wait_for(flag + i, 1, wc);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           __syncwarp();  // a lane's rows may lie behind other lanes' flags
@@ -603,7 +702,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1u;
           }
         }
-        b += q.k1 - q.k0;
       }
     }
     // This CTA reads no more flags.  The last to say so clears them: each was
@@ -615,9 +713,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (__shfl_sync(0xffffffffu, left, 0) == static_cast<int>(gridDim.x) - 1) {
       __threadfence();
-      const int64_t n = static_cast<int64_t>(entries) * (p.F / 64);
-      for (int64_t i = lane; i < n; i += 32) p.done[i] = 0;
-      if (lane == 0) *p.leave = 0;
+      const int n = entries * (p.F / 64);
+      for (int i = lane; i < n; i += 32) p.done[i] = 0;
+      if (lane == 0) *p.leave = *p.routed = 0;
     }
     if (!ok && lane == 0) {
       for (int i = 0; i < p.stages; ++i) {
@@ -634,9 +732,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
-        const Phase f(p, ph, entries);
-        for (int64_t b = f.b0; b < f.b1 && ok; ++piece) {
-          const Piece q(f, b);
+        const Phase f(p.D, p.F, gridDim.x, ph, entries);
+        Walk walk(f);
+        Piece q;
+        for (; ok && walk.next(f, q); ++piece) {
           const int slot = piece & 1;
           const uint32_t idesc = dense_idesc(kCols, (r.vcnt[q.v] + 15) & ~15, true, false, p.type);
           if (piece >= 2) ok = mbar_wait(&s.tempty[slot], ((piece >> 1) - 1) & 1, wc);
@@ -655,7 +754,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (ok) umma_commit<1>(&s.tfull[slot]);
-          b += q.k1 - q.k0;
         }
       }
       if (!ok && done > 0) {  // issued products end before TMEM is freed
@@ -665,22 +763,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kFirstEpiWarp) {
     // -------------------------------------------------------------- epilogue
-    const int tid = threadIdx.x - kFirstEpiWarp * 32, ew = warp - kFirstEpiWarp;
+    const int tid = threadIdx.x - kFirstEpiWarp * 32;
     const int col = (warp & 3) * 32 + lane;  // the tile's column: this thread's TMEM lane
     const uint32_t tq = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     int piece = 0;
     bool ok = true;
     for (int ph = 0; ph < 2 && ok; ++ph) {
-      const Phase f(p, ph, entries);
-      for (int64_t b = f.b0; b < f.b1; ++piece) {
-        const Piece q(f, b);
+      const Phase f(p.D, p.F, gridDim.x, ph, entries);
+      Walk walk(f);
+      Piece q;
+      for (; walk.next(f, q); ++piece) {
         const int slot = piece & 1, cnt = r.vcnt[q.v], start = r.vstart[q.v];
-        const bool whole = q.whole(f);
+        const bool whole = q.k1 - q.k0 == static_cast<int>(f.kb);
         // the four warps meet at barriers below: all go on or none does
         ok = epi_all(warp_wait(&s.tfull[slot], (piece >> 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
-        float* rows = part_rows(p, ph, blockIdx.x, q.k0 == 0 ? 1 : 0);
+        float* rows = part_rows(p.part, gridDim.x, p.nt, ph, blockIdx.x, q.k0 == 0 ? 1 : 0);
         for (int t0 = 0; t0 < cnt; t0 += 16) {
           uint32_t v[16];
           tmem_ld_32x32b_x16(tq + slot * p.nt + t0, v);
@@ -699,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             epi_sync();
           } else if (whole) {
-            const int c = q.col * kCols + col;
+            const int c = static_cast<int>(q.col) * kCols + col;
             if (c < p.D) {
 #pragma unroll
               for (int i = 0; i < 16; ++i)
@@ -714,69 +813,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.tempty[slot]);
-        const int blocks = q.k1 - q.k0;
-        if (ph == 0) {
-          bool stored = whole;
-          if (!whole) {
+        if (ph == 1) continue;
+        bool stored = whole;
+        if (!whole) {
+          epi_sync();
+          if (tid == 0) {
             __threadfence();
-            epi_sync();
-            if (tid == 0) s.last = atomicAdd(p.sum1 + q.tile, blocks) + blocks == f.kb ? 1 : 0;
-            epi_sync();
-            if (s.last) {  // join the parts, in the reduction's order
-              __threadfence();
-              const int64_t first_block = static_cast<int64_t>(q.tile) * f.kb;
-              const int first = f.owner(first_block), last = f.owner(first_block + f.kb - 1);
-              const int c8 = (tid % 8) * 8;
-              for (int i = tid / 8; i < cnt; i += 16) {
-                float g[8] = {}, u[8] = {};
-                for (int c = first; c <= last; ++c) {
-                  const float* at = part_rows(p, 0, c, c == first ? 1 : 0) + i * kCols;
-                  add8(at + c8, g);
-                  add8(at + 64 + c8, u);
-                }
-                store_h<T>(p, r.list[start + i], q.col * 64 + c8, g, u);
+            const int blocks = q.k1 - q.k0;
+            s.last = atomicAdd(p.sum + q.tile, blocks) + blocks == static_cast<int>(f.kb) ? 1 : 0;
+            __threadfence();
+          }
+          epi_sync();
+          if (s.last) {  // join the parts, in the reduction's order
+            const uint32_t b = (q.tile - f.waves * f.grid) * f.kb;
+            const uint32_t first = f.owner(b), last = f.owner(b + f.kb - 1);
+            const int c8 = (tid % 8) * 8;
+            for (int i = tid / 8; i < cnt; i += 16) {
+              float g[8] = {}, u[8] = {};
+#pragma unroll 4
+              for (uint32_t c = first; c <= last; ++c) {
+                const float* at = part_rows(p.part, gridDim.x, p.nt, 0, c, c == first ? 1 : 0) + i * kCols;
+                add8(at + c8, g);
+                add8(at + 64 + c8, u);
               }
-              if (tid == 0) p.sum1[q.tile] = 0;
-              stored = true;
+              store_h<T>(p, r.list[start + i], q.col * 64 + c8, g, u);
             }
-          }
-          if (stored) {
-            fence_proxy_async_global();
-            __threadfence();
-            epi_sync();
-            if (tid == 0) st_release(p.done + q.tile, 1);
-          }
-        } else {
-          __threadfence();
-          epi_sync();
-          bool last = false;
-          if (tid < cnt) {
-            const int t = r.list[start + tid] / p.K;
-            last = atomicAdd(p.sum2 + static_cast<int64_t>(t) * f.cols + q.col, blocks) + blocks == r.valid[t] * f.kb;
-          }
-          const uint32_t mask = __ballot_sync(0xffffffffu, last);
-          if (lane == 0) s.last_tokens[ew] = mask;
-          __threadfence();
-          epi_sync();
-          int seen = 0;
-          for (int g = 0; g < (cnt + 31) / 32; ++g) {
-            for (uint32_t m = s.last_tokens[g]; m != 0u; m &= m - 1u, ++seen) {
-              if ((seen & 3) != ew) continue;
-              const int t = r.list[start + g * 32 + __ffs(m) - 1] / p.K;
-              combine_token<T>(p, r, f, t, q.col, lane);
-              if (lane == 0) p.sum2[static_cast<int64_t>(t) * f.cols + q.col] = 0;
-            }
+            if (tid == 0) p.sum[q.tile] = 0;
+            stored = true;
           }
         }
-        b += blocks;
-      }
-    }
-    // tokens none of whose slots names an expert
-    for (int t = blockIdx.x; t < p.n; t += gridDim.x) {
-      if (r.valid[t] != 0) continue;
-      for (int c = tid; c < p.D; c += 128) {
-        const T v = p.res != nullptr ? static_cast<const T*>(p.res)[t * p.ldres + c] : from_f32<T>(0.0f);
-        static_cast<T*>(p.out)[t * p.ldout + c] = v;
+        if (stored) {
+          fence_proxy_async_global();
+          epi_sync();
+          if (tid == 0) {
+            __threadfence();
+            st_release(p.done + q.tile, 1);
+          }
+        }
       }
     }
   }
@@ -788,14 +861,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// 16-bit [outer][mid][inner], boxes of 64 x `box` x 1.
+// 16-bit [outer][mid][inner], boxes of 64 x 64 x 1.  L2 fetches the box's 128
+// bytes of a row and no more: the next 128 are another tile's, and gone again by
+// its turn (7168 -> 2048, FC1: 366 us with 256 bytes, 280 with 128).
 bool map3(CUtensorMap* m, const void* base, uint64_t inner, uint64_t mid, uint64_t outer) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {inner, mid, outer}, strides[2] = {inner * 2, inner * mid * 2};
   const cuuint32_t box[3] = {64, kBlockK, 1}, es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // 16-bit rows for four-row gathers: a box is 64 columns of one row.
@@ -819,26 +894,24 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 // Workspace: counters (zero between calls; placed by the capacity, not by a
 // call's tokens), then the data.
 struct Layout {
-  size_t done, sum1, sum2, h, y, part, all;
+  size_t done, sum, slots, gids, gw, h, y, part, all;
   explicit Layout(const moe_dims& d) {
     const size_t R = static_cast<size_t>(d.T) * d.K, nt = tile_tokens(d.T);
     const size_t tiles = static_cast<size_t>(most_virtual(static_cast<int>(R), d.E, static_cast<int>(nt))) * (d.F / 64);
     done = 256;
-    sum1 = done + up(tiles * 4);
-    sum2 = sum1 + up(tiles * 4);
-    h = sum2 + up(static_cast<size_t>(d.T) * ((d.D + kCols - 1) / kCols) * 4);
+    sum = done + up(tiles * 4);
+    slots = sum + up(tiles * 4);
+    gids = slots + up((R + 1) * 8);
+    gw = gids + up(R * 4);
+    h = gw + up(R * 4);
     y = h + up(R * d.F * 2);
     part = y + up(R * d.D * 4);
     all = part + up(static_cast<size_t>(kMaxGrid) * 4 * nt * kCols * 4);
   }
 };
 
-}  // namespace
-
-size_t decode_ws_bytes(const moe_dims& d) { return Layout(d).all; }
-
 template <typename T>
-static cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
+cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   const moe_dims& d = c.d;
   Params p{};
   p.logits = c.logits;
@@ -847,10 +920,6 @@ static cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   p.w_in = c.w;
   p.ids_out = c.ids_out;
   p.w_out = c.w_out;
-  p.res = c.res;
-  p.ldres = c.ldres;
-  p.out = c.out;
-  p.ldout = c.ldout;
   p.n = c.n;
   p.D = d.D;
   p.E = d.E;
@@ -866,13 +935,16 @@ static cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(c.ws);
   p.leave = reinterpret_cast<int32_t*>(ws);
   p.done = reinterpret_cast<int32_t*>(ws + at.done);
-  p.sum1 = reinterpret_cast<int32_t*>(ws + at.sum1);
-  p.sum2 = reinterpret_cast<int32_t*>(ws + at.sum2);
+  p.routed = p.leave + 1;
+  p.sum = reinterpret_cast<int32_t*>(ws + at.sum);
+  p.slots = reinterpret_cast<uint2*>(ws + at.slots);
+  p.gids = reinterpret_cast<int32_t*>(ws + at.gids);
+  p.gw = reinterpret_cast<float*>(ws + at.gw);
   p.h = ws + at.h;
   p.y = reinterpret_cast<float*>(ws + at.y);
   p.part = reinterpret_cast<float*>(ws + at.part);
   const size_t R = static_cast<size_t>(c.n) * d.K;
-  const size_t fixed = 1024 + kBufBytes + sizeof(Ctl) + route_bytes(static_cast<int>(R), d.E, c.n, p.nt);
+  const size_t fixed = 1024 + kBufBytes + sizeof(Ctl) + route_bytes(static_cast<int>(R), d.E, p.nt);
   const size_t stage = kWeightStage + static_cast<size_t>(p.nt) * kBlockK * 2;
   p.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemLimit - fixed) / stage));
   if (p.stages < kMinStages) return cudaErrorInvalidValue;
@@ -901,8 +973,36 @@ static cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_kernel<T>, wi, wo, x, h, p);
+  err = cudaLaunchKernelEx(&cfg, decode_kernel<T>, wi, wo, x, h, p);
+  if (err != cudaSuccess) return err;
+  CombineParams q{};
+  q.slots = p.slots;
+  q.y = p.y;
+  q.part = p.part;
+  q.res = c.res;
+  q.ldres = c.ldres;
+  q.out = c.out;
+  q.ldout = c.ldout;
+  q.n = c.n;
+  q.D = d.D;
+  q.F = d.F;
+  q.K = d.K;
+  q.nt = p.nt;
+  q.grid = static_cast<uint32_t>(grid);
+  cudaLaunchAttribute overlap = overlap_attribute();
+  const int units = c.n * ((d.D + kCols - 1) / kCols);
+  cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((units + kCombineWarps - 1) / kCombineWarps));
+  cfg.blockDim = dim3(32 * kCombineWarps);
+  cfg.stream = s;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<T>, q);
 }
+
+}  // namespace
+
+size_t decode_ws_bytes(const moe_dims& d) { return Layout(d).all; }
 
 cudaError_t launch_decode(const DecodeCall& c, cudaStream_t s) {
   return c.type == MOE_BF16 ? launch_typed<__nv_bfloat16>(c, s) : launch_typed<__half>(c, s);
