@@ -14,8 +14,11 @@
 // neighbouring columns are read at the same time; the tiles that are left (all
 // of them for one token, some 90) are cut into equal runs of blocks, which
 // begin and end inside a tile.  Whole tiles alone would leave a tenth to a
-// third of the SMs idle in the last wave.  Parts of a tile are joined in the
-// order of the reduction, so results do not depend on who was last.
+// third of the SMs idle in the last wave.  The CTA that has a tile's first
+// part joins the others to it, in their order: it comes to that part last, the
+// others to theirs first, so it need not wait, and results do not depend on
+// who was faster.  (Joining by whoever adds the last part took 3 us longer from
+// the last product to h.)
 //
 // One ring of shared memory carries both phases' blocks and keeps 128 KB or
 // more under way (with 32 KB an SM streams at two thirds of the rate): FC2's
@@ -72,7 +75,7 @@ struct Params {
   int32_t* leave;     // CTAs that read no more flags
   int32_t* routed;    // tokens whose selection is stored
   int32_t* done;      // [tile of FC1]: its h is stored
-  int32_t* sum;       // [tile of FC1]: blocks summed so far
+  int32_t* stored;    // [CTA]: its part of an FC1 tile that began before its run is stored
   int32_t* status;
   uint64_t limit_ns;
 };
@@ -85,7 +88,6 @@ struct Ctl {
   uint64_t tempty[2];
   uint32_t tmem_base;
   int abort_flag;
-  int last;
   uint2 warp_sums[kThreads / 32];
 };
 
@@ -319,6 +321,8 @@ __device__ __forceinline__ bool select_all(const Params& p, const Route& r, cons
 __device__ __forceinline__ int build_list(const Params& p, const Route& r, Ctl& s, int warp, int lane) {
   const int R = p.n * p.K, span = (R + kThreads - 1) / kThreads * 32;
   uint16_t* mine = r.before + warp * p.E;
+  for (int e = lane; e < p.E; e += 32) mine[e] = 0;
+  __syncwarp();
   for (int j0 = warp * span; j0 < min(R, (warp + 1) * span); j0 += 32) {
     const int j = j0 + lane;
     const int e = j < R ? r.expert[j] : kNone;
@@ -466,12 +470,12 @@ __device__ __forceinline__ void store_h(const Params& p, int slot, int f, const 
   o.pack(v);
   *reinterpret_cast<uint4*>(static_cast<T*>(p.h) + static_cast<int64_t>(slot) * p.F + f) = o.v;
 }
-__device__ __forceinline__ void load8(const float* at, float (&f)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(at), b = *reinterpret_cast<const float4*>(at + 4);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
+template <bool SHARED>  // or of another CTA's part: never by the read-only path
 __device__ __forceinline__ void add8(const float* at, float (&f)[8]) {
-  const float4 a = __ldcg(reinterpret_cast<const float4*>(at)), b = __ldcg(reinterpret_cast<const float4*>(at) + 1);
+  const float4* p = reinterpret_cast<const float4*>(at);
+  float4 a, b;
+  if constexpr (SHARED) a = p[0], b = p[1];
+  else a = __ldcg(p), b = __ldcg(p + 1);
   f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w, f[4] += b.x, f[5] += b.y, f[6] += b.z, f[7] += b.w;
 }
 
@@ -584,7 +588,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Route r = route_at(reinterpret_cast<uint8_t*>(&s) + sizeof(Ctl), p.n * p.K, p.E, p.nt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) {
+  // set up by the last warps, while the first ones select
+  if (threadIdx.x == 0) s.abort_flag = 0;
+  if (warp == kWarps - 2) {
+    tmem_alloc<1>(&s.tmem_base, 2 * p.nt);
+    tmem_relinquish<1>();
+  } else if (threadIdx.x == 32 * (kWarps - 1)) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&s.fullw[i], 1);
       mbar_init(&s.fullt[i], 1);
@@ -594,20 +603,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.tfull[i], 1);
       mbar_init(&s.tempty[i], 4);
     }
-    s.abort_flag = 0;
     mbar_fence_init();
     tma_prefetch_map(&map_wi);
     tma_prefetch_map(&map_x);
     tma_prefetch_map(&map_wo);
     tma_prefetch_map(&map_h);
   }
-  if (warp == 1) {
-    tmem_alloc<1>(&s.tmem_base, 2 * p.nt);
-    tmem_relinquish<1>();
-  }
-  for (int i = threadIdx.x; i < kWarps * p.E; i += kThreads) r.before[i] = 0;
+  __syncwarp();
   const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
-  __syncthreads();
   const bool routed = select_all(p, r, wc, warp, lane);
   __syncthreads();
   int entries = 0;
@@ -704,8 +707,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    // This CTA reads no more flags.  The last to say so clears them: each was
-    // waited for by some CTA, so each has been set.
+    // This CTA's producer reads no more flags.  The last to say so clears them:
+    // each tile's flag was waited for by some CTA's producer, so it has been
+    // set, and the parts that were joined before it was are no more waited for.
     int left = 0;
     if (lane == 0) {
       __threadfence();
@@ -715,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __threadfence();
       const int n = entries * (p.F / 64);
       for (int i = lane; i < n; i += 32) p.done[i] = 0;
+      for (int i = lane; i < static_cast<int>(gridDim.x); i += 32) p.stored[i] = 0;
       if (lane == 0) *p.leave = *p.routed = 0;
     }
     if (!ok && lane == 0) {
@@ -775,7 +780,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; walk.next(f, q); ++piece) {
         const int slot = piece & 1, cnt = r.vcnt[q.v], start = r.vstart[q.v];
         const bool whole = q.k1 - q.k0 == static_cast<int>(f.kb);
+        const int i16 = tid / 8, c8 = (tid % 8) * 8;  // FC1: this thread's token of 16, its columns
+        // FC1, the tile's first part: the CTAs that have the others
+        uint32_t join0 = blockIdx.x + 1, join1 = blockIdx.x;
+        if (ph == 0 && q.k0 == 0 && !whole) {
+          join1 = f.owner((q.tile - f.waves * f.grid + 1) * f.kb - 1);
+          for (uint32_t c = join0 + tid; c <= join1 && ok; c += 128) ok = wait_for(p.stored + c, 1, wc);
+        }
         // the four warps meet at barriers below: all go on or none does
+        ok = epi_all(ok);
+        if (!ok) break;
+        const auto joined = [&](int t0, float (&g)[8], float (&u)[8]) {
+          for (uint32_t c = join0; c <= join1; ++c) {
+            const float* at = part_rows(p.part, gridDim.x, p.nt, 0, c, 0) + (t0 + i16) * kCols;
+            add8<false>(at + c8, g);
+            add8<false>(at + 64 + c8, u);
+          }
+        };
+        float g[8] = {}, u[8] = {};
+        if (i16 < cnt) joined(0, g, u);  // while the products end
         ok = epi_all(warp_wait(&s.tfull[slot], (piece >> 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
@@ -785,19 +808,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_32x32b_x16(tq + slot * p.nt + t0, v);
           tmem_ld_wait();
           const int m = min(16, cnt - t0);
-          if (ph == 0 && whole) {
+          if (ph == 0 && q.k0 == 0) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) buf[i * kBufLd + col] = __uint_as_float(v[i]);
             epi_sync();
-            const int i = tid / 8, c8 = (tid % 8) * 8;
-            if (i < m) {
-              float g[8], u[8];
-              load8(buf + i * kBufLd + c8, g);
-              load8(buf + i * kBufLd + 64 + c8, u);
-              store_h<T>(p, r.list[start + t0 + i], q.col * 64 + c8, g, u);
+            if (i16 < m) {
+              if (t0 > 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] = u[i] = 0.0f;
+                joined(t0, g, u);
+              }
+              add8<true>(buf + i16 * kBufLd + c8, g);
+              add8<true>(buf + i16 * kBufLd + 64 + c8, u);
+              store_h<T>(p, r.list[start + t0 + i16], q.col * 64 + c8, g, u);
             }
             epi_sync();
-          } else if (whole) {
+          } else if (whole) {  // FC2
             const int c = static_cast<int>(q.col) * kCols + col;
             if (c < p.D) {
 #pragma unroll
@@ -814,48 +840,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.tempty[slot]);
         if (ph == 1) continue;
-        bool stored = whole;
-        if (!whole) {
-          epi_sync();
-          if (tid == 0) {
-            __threadfence();
-            const int blocks = q.k1 - q.k0;
-            s.last = atomicAdd(p.sum + q.tile, blocks) + blocks == static_cast<int>(f.kb) ? 1 : 0;
-            __threadfence();
-          }
-          epi_sync();
-          if (s.last) {  // join the parts, in the reduction's order
-            const uint32_t b = (q.tile - f.waves * f.grid) * f.kb;
-            const uint32_t first = f.owner(b), last = f.owner(b + f.kb - 1);
-            const int c8 = (tid % 8) * 8;
-            for (int i = tid / 8; i < cnt; i += 16) {
-              float g[8] = {}, u[8] = {};
-#pragma unroll 4
-              for (uint32_t c = first; c <= last; ++c) {
-                const float* at = part_rows(p.part, gridDim.x, p.nt, 0, c, c == first ? 1 : 0) + i * kCols;
-                add8(at + c8, g);
-                add8(at + 64 + c8, u);
-              }
-              store_h<T>(p, r.list[start + i], q.col * 64 + c8, g, u);
-            }
-            if (tid == 0) p.sum[q.tile] = 0;
-            stored = true;
-          }
-        }
-        if (stored) {
-          fence_proxy_async_global();
-          epi_sync();
-          if (tid == 0) {
-            __threadfence();
-            st_release(p.done + q.tile, 1);
-          }
-        }
+        if (q.k0 == 0) fence_proxy_async_global();  // h is read by TMA
+        epi_sync();
+        if (tid == 0) st_release(q.k0 == 0 ? p.done + q.tile : p.stored + blockIdx.x, 1);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kWarps - 2) {
     tc_fence_after();
     tmem_dealloc<1>(tmem, 2 * p.nt);
   }
@@ -889,18 +882,18 @@ bool map_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, u
 int tile_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 
 constexpr int kMaxGrid = 192;  // CTAs that the workspace has room for: no device of this kind has more SMs
+static_assert((32 + kMaxGrid) * 4 <= 1024, "counters and flags ahead of the tiles' flags");
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 // Workspace: counters (zero between calls; placed by the capacity, not by a
 // call's tokens), then the data.
 struct Layout {
-  size_t done, sum, slots, gids, gw, h, y, part, all;
+  size_t done, slots, gids, gw, h, y, part, all;
   explicit Layout(const moe_dims& d) {
     const size_t R = static_cast<size_t>(d.T) * d.K, nt = tile_tokens(d.T);
     const size_t tiles = static_cast<size_t>(most_virtual(static_cast<int>(R), d.E, static_cast<int>(nt))) * (d.F / 64);
-    done = 256;
-    sum = done + up(tiles * 4);
-    slots = sum + up(tiles * 4);
+    done = 1024;  // behind the two counters and the CTAs' flags
+    slots = done + up(tiles * 4);
     gids = slots + up((R + 1) * 8);
     gw = gids + up(R * 4);
     h = gw + up(R * 4);
@@ -936,7 +929,7 @@ cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   p.leave = reinterpret_cast<int32_t*>(ws);
   p.done = reinterpret_cast<int32_t*>(ws + at.done);
   p.routed = p.leave + 1;
-  p.sum = reinterpret_cast<int32_t*>(ws + at.sum);
+  p.stored = p.leave + 32;
   p.slots = reinterpret_cast<uint2*>(ws + at.slots);
   p.gids = reinterpret_cast<int32_t*>(ws + at.gids);
   p.gw = reinterpret_cast<float*>(ws + at.gw);

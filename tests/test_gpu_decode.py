@@ -34,7 +34,7 @@ def _check(op, d, ids, w, res, out, own):
     assert int(op.status.item()) == 0
     want, err = experts(d["x"], d["wi"], d["wo"], ids, w, res, own)
     assert_within("out", out, want, err)
-    assert not bool(op.ws[:256].any())
+    assert not bool(op.ws[:1024].any())
 
 
 @pytest.mark.parametrize("T,D,E,K,F,dt,mode", [
