@@ -714,6 +714,57 @@ moe_status moe_decode(moe_mat x, const void* wi, const void* wo, const float* lo
                       moe_mat out, int32_t* dev_status, void* ws, int32_t n, moe_dims d,
                       moe_dtype type, cudaStream_t stream);
 
+/*
+ * RMS norms after and before a block, with its gate and residual scale:
+ *   yh = y * rstd_y,  rstd_y = 1 / sqrt(sum_d y^2 / D + eps)
+ *   r  = round(res + scale * token_gate * gate * (post + offset) * yh)
+ *   u  = round((pre + offset) * r * rstd_r),  rstd_r likewise, of the rounded r
+ *   y, res, r, u     `type` [rows, D];  post, pre, gate  `wtype` [D]
+ *   token_gate       fp32 [rows];  rstd_y, rstd_r  fp32 [rows] out, or NULL
+ * post NULL: no norm after the block (yh = y).  pre NULL: none before the next
+ * (u is not written).  gate, token_gate NULL: ones.  y.p NULL: r is res, and
+ * not written (pre is then required; post, gate and token_gate not taken).
+ * Sums are fp32.  r may be res's memory, u may be y's (same ld).
+ * 1 <= D <= 8192, 0 <= rows < 2^31; types as moe_layer_norm's.  Pointers need
+ * only the alignment of their elements.
+ */
+typedef struct {
+  int64_t rows;
+  int32_t D;
+  int32_t type;  /* moe_dtype */
+  int32_t wtype; /* moe_dtype: type or MOE_FP32 */
+  float eps, scale, offset;
+} moe_block_norm_dims;
+
+moe_status moe_block_norm(moe_mat y, moe_mat res, const void* post, const void* pre,
+                          const void* gate, const float* token_gate, moe_mat r, moe_mat u,
+                          float* rstd_y, float* rstd_r, moe_block_norm_dims d,
+                          cudaStream_t stream);
+
+/*
+ * Its backward, from y, the stored r and their statistics (rstd_y with post,
+ * rstd_r with pre):
+ *   a = du * (pre + offset),  rh = r * rstd_r,  g = scale * gate * (post + offset)
+ *   d = dr + rstd_r * (a - rh * sum_d(a rh) / D)      dres = round(d)
+ *   b = sum_d g * yh * d                              dtoken_gate = b
+ *   dy = round(rstd_y * token_gate * (g * d - yh * b / D))    (post NULL: token_gate * g * d)
+ *   dpre = sum_rows du rh,  e = sum_rows token_gate d yh,
+ *   dpost = scale * gate * e,  dgate = scale * (post + offset) * e
+ * du.p is given with pre, and only then; dr.p may be NULL with pre (nothing
+ * else flows into r).  y.p may be NULL: then dy.p, dpost, dgate and dtoken_gate
+ * are too.  dy.p may be NULL also with y.  Each gradient of a weight may be
+ * NULL, and must be where the weight is.  Weights' gradients need ws
+ * (moe_block_norm_workspace_bytes) and are reproducible bit for bit.  dres may
+ * be dr's memory, dy may be y's or du's (same ld).  rows = 0 gives zero weight
+ * gradients.
+ */
+size_t moe_block_norm_workspace_bytes(moe_block_norm_dims d);
+moe_status moe_block_norm_bwd(moe_mat du, moe_mat dr, moe_mat r, moe_mat y, const void* post,
+                              const void* pre, const void* gate, const float* token_gate,
+                              const float* rstd_y, const float* rstd_r, moe_mat dres, moe_mat dy,
+                              void* dpost, void* dpre, void* dgate, float* dtoken_gate, void* ws,
+                              moe_block_norm_dims d, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

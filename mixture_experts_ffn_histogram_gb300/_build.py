@@ -20,12 +20,12 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmoe.so")
 SOURCES = ["api.cu", "route.cu", "permute_combine.cu", "gemm.cu", "mx.cu",
            "layer_api.cu", "norm.cu", "route_topk.cu", "dense.cu", "act_grad.cu",
-           "decode.cu"]
+           "decode.cu", "block_norm.cu"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "kernels.h"),
            os.path.join(CSRC, "mx.h"), os.path.join(CSRC, "mx_common.cuh"),
            os.path.join(CSRC, "layer.h"), os.path.join(CSRC, "layer_common.cuh"),
            os.path.join(CSRC, "activation.cuh"), os.path.join(CSRC, "tmem_share.h"),
-           os.path.join(CSRC, "umma_tile.cuh"), os.path.join(INCLUDE, "moe.h")]
+           os.path.join(CSRC, "umma_tile.cuh"), os.path.join(CSRC, "row_common.cuh"), os.path.join(INCLUDE, "moe.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -38,7 +38,8 @@ ENTRY_POINTS = (
     "moe_mx_grouped_gemm_fc1_bwd",
     "moe_layer_norm", "moe_layer_norm_bwd", "moe_layer_norm_workspace_bytes", "moe_route_topk",
     "moe_route_topk_bwd", "moe_linear", "moe_linear_bwd", "moe_linear_workspace_bytes",
-    "moe_decode", "moe_decode_workspace_bytes",
+    "moe_decode", "moe_decode_workspace_bytes", "moe_block_norm", "moe_block_norm_bwd",
+    "moe_block_norm_workspace_bytes",
 )
 
 # moe_dtype
@@ -81,6 +82,12 @@ class MoeLinearDims(ctypes.Structure):
                 ("type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
+class MoeBlockNormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("wtype", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("offset", ctypes.c_float)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn: str, status: int, detail: str | None = None):
         super().__init__(f"{fn}: {detail or status_string(status)} (status {status})")
@@ -102,6 +109,11 @@ def topk_dims(T, E, K, gate="sigmoid", groups=1, top_groups=1, group_top=1, reno
 
 def linear_dims(M, K, N, dtype=torch.bfloat16, out_dtype=None, act="none") -> MoeLinearDims:
     return MoeLinearDims(M, K, N, DTYPES[dtype], DTYPES[out_dtype or dtype], ACTS[act])
+
+
+def block_norm_dims(rows, D, dtype=torch.bfloat16, weight_dtype=torch.float32, eps=1e-6, scale=1.0,
+                    offset=0.0) -> MoeBlockNormDims:
+    return MoeBlockNormDims(rows, D, DTYPES[dtype], DTYPES[weight_dtype], eps, scale, offset)
 
 
 def library_path() -> str:
@@ -166,6 +178,9 @@ def lib() -> ctypes.CDLL:
             "moe_linear_workspace_bytes": ([MoeLinearDims], ctypes.c_size_t),
             "moe_decode": ([M, P, P, P, P, I, P, P, M, M, P, P, ctypes.c_int32, D_, I, P], I),
             "moe_decode_workspace_bytes": ([D_], ctypes.c_size_t),
+            "moe_block_norm": ([M, M, P, P, P, P, M, M, P, P, MoeBlockNormDims, P], I),
+            "moe_block_norm_bwd": ([M] * 4 + [P] * 6 + [M, M] + [P] * 5 + [MoeBlockNormDims, P], I),
+            "moe_block_norm_workspace_bytes": ([MoeBlockNormDims], ctypes.c_size_t),
         })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -455,3 +470,22 @@ def moe_decode(x, wi, wo, logits, bias, mode, ids, w, res, out, dev_status, ws, 
     _ok("moe_decode", lib().moe_decode(
         _m(x), _p(wi), _p(wo), _p(logits), _p(bias), int(mode), _p(ids), _p(w), _m(res), _m(out),
         _p(dev_status), _p(ws), x.shape[0], d, DTYPES[x.dtype], _s(stream)))
+
+
+def moe_block_norm(y, res, post, pre, gate, token_gate, r, u, rstd_y, rstd_r, d: MoeBlockNormDims,
+                   stream=None):
+    _ok("moe_block_norm", lib().moe_block_norm(
+        _m(y), _m(res), _p(post), _p(pre), _p(gate), _p(token_gate), _m(r), _m(u), _p(rstd_y),
+        _p(rstd_r), d, _s(stream)))
+
+
+def moe_block_norm_workspace_bytes(d: MoeBlockNormDims) -> int:
+    return int(lib().moe_block_norm_workspace_bytes(d))
+
+
+def moe_block_norm_bwd(du, dr, r, y, post, pre, gate, token_gate, rstd_y, rstd_r, dres, dy, dpost,
+                       dpre, dgate, dtoken_gate, ws, d: MoeBlockNormDims, stream=None):
+    _ok("moe_block_norm_bwd", lib().moe_block_norm_bwd(
+        _m(du), _m(dr), _m(r), _m(y), _p(post), _p(pre), _p(gate), _p(token_gate), _p(rstd_y),
+        _p(rstd_r), _m(dres), _m(dy), _p(dpost), _p(dpre), _p(dgate), _p(dtoken_gate), _p(ws), d,
+        _s(stream)))

@@ -101,6 +101,21 @@ struct ActGradCall {
 };
 cudaError_t launch_act_grad(const ActGradCall& c, cudaStream_t s);
 
+// Norms around a block.  Backward where dres is given.
+struct BlockNormCall {
+  const void *y, *res, *r_in, *du, *dr;
+  const void *post, *pre, *gate;
+  const float* token_gate;
+  void *r, *u, *dres, *dy;
+  float *rstd_y, *rstd_r;  // backward: read
+  void *dpost, *dpre, *dgate;
+  float* dtoken_gate;
+  float* partials;
+  int64_t ldy, ldres, ldr, ldu, lddu, lddr, lddres, lddy;
+  moe_block_norm_dims d;
+};
+cudaError_t launch_block_norm(const BlockNormCall& c, cudaStream_t s);
+
 // The expert layer for a few tokens: d.T is the capacity that the workspace
 // was made for, n <= d.T the call's tokens.
 struct DecodeCall {

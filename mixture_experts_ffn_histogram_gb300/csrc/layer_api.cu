@@ -59,6 +59,10 @@ moe_status check_linear(const moe_linear_dims& d) {
   return MOE_OK;
 }
 
+moe_status check_block_norm(const moe_block_norm_dims& d) {
+  return check_norm(d.rows, d.D, static_cast<moe_dtype>(d.type), static_cast<moe_dtype>(d.wtype));
+}
+
 moe_status check_decode(const moe_dims& d, int type) {
   if (!is_dtype(type)) return MOE_ERR_INVALID_ARG;
   if (type == MOE_FP32) return MOE_ERR_UNSUPPORTED;
@@ -270,6 +274,117 @@ moe_status moe_decode(moe_mat x, const void* wi, const void* wo, const float* lo
   c.mode = mode;
   c.type = type;
   return from_cuda(moe::launch_decode(c, stream));
+}
+
+moe_status moe_block_norm(moe_mat y, moe_mat res, const void* post, const void* pre, const void* gate,
+                          const float* token_gate, moe_mat r, moe_mat u, float* rstd_y, float* rstd_r,
+                          moe_block_norm_dims d, cudaStream_t stream) {
+  const moe_status st = check_block_norm(d);
+  if (st != MOE_OK) return st;
+  const size_t w = size_of(d.wtype);
+  if (!aligned(post, w) || !aligned(pre, w) || !aligned(gate, w) || !aligned(token_gate, 4) ||
+      !aligned(rstd_y, 4) || !aligned(rstd_r, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (d.rows == 0) return MOE_OK;
+  if (y.p == nullptr && (pre == nullptr || post != nullptr || gate != nullptr || token_gate != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!element_mat(res, d.D, d.type) || (pre != nullptr && !element_mat(u, d.D, d.type)))
+    return MOE_ERR_INVALID_ARG;
+  if (y.p != nullptr && (!element_mat(y, d.D, d.type) || !element_mat(r, d.D, d.type)))
+    return MOE_ERR_INVALID_ARG;
+  moe::BlockNormCall c{};
+  c.res = res.p;
+  c.ldres = res.ld;
+  if (y.p != nullptr) {
+    c.y = y.p;
+    c.ldy = y.ld;
+    c.r = r.p;
+    c.ldr = r.ld;
+  }
+  if (pre != nullptr) {
+    c.u = u.p;
+    c.ldu = u.ld;
+  }
+  c.post = post;
+  c.pre = pre;
+  c.gate = gate;
+  c.token_gate = token_gate;
+  c.rstd_y = rstd_y;
+  c.rstd_r = rstd_r;
+  c.d = d;
+  return from_cuda(moe::launch_block_norm(c, stream));
+}
+
+size_t moe_block_norm_workspace_bytes(moe_block_norm_dims d) {
+  if (check_block_norm(d) != MOE_OK) return 0;
+  const int64_t parts = d.rows < moe::kPartialRows ? d.rows : moe::kPartialRows;
+  return round256(static_cast<size_t>(parts) * 2 * static_cast<size_t>(d.D) * sizeof(float));
+}
+
+moe_status moe_block_norm_bwd(moe_mat du, moe_mat dr, moe_mat r, moe_mat y, const void* post,
+                              const void* pre, const void* gate, const float* token_gate,
+                              const float* rstd_y, const float* rstd_r, moe_mat dres, moe_mat dy,
+                              void* dpost, void* dpre, void* dgate, float* dtoken_gate, void* ws,
+                              moe_block_norm_dims d, cudaStream_t stream) {
+  const moe_status st = check_block_norm(d);
+  if (st != MOE_OK) return st;
+  const size_t w = size_of(d.wtype);
+  for (const void* p : {post, pre, gate, static_cast<const void*>(dpost), static_cast<const void*>(dpre),
+                        static_cast<const void*>(dgate)})
+    if (!aligned(p, w)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(token_gate, 4) || !aligned(rstd_y, 4) || !aligned(rstd_r, 4) || !aligned(dtoken_gate, 4))
+    return MOE_ERR_INVALID_ARG;
+  if ((dpost != nullptr && post == nullptr) || (dpre != nullptr && pre == nullptr) ||
+      (dgate != nullptr && gate == nullptr) || (dtoken_gate != nullptr && token_gate == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  const bool weights = dpost != nullptr || dpre != nullptr || dgate != nullptr;
+  if (d.rows == 0) {
+    cudaError_t err = cudaSuccess;
+    for (void* p : {dpost, dpre, dgate})
+      if (p != nullptr && err == cudaSuccess) err = cudaMemsetAsync(p, 0, d.D * w, stream);
+    return from_cuda(err);
+  }
+  const auto mat = [&](const moe_mat& m) { return element_mat(m, d.D, d.type); };
+  if (!mat(dres)) return MOE_ERR_INVALID_ARG;
+  if (pre != nullptr ? !mat(du) || !mat(r) || rstd_r == nullptr || (dr.p != nullptr && !mat(dr))
+                     : du.p != nullptr || !mat(dr))
+    return MOE_ERR_INVALID_ARG;
+  if (y.p != nullptr ? !mat(y) || (post != nullptr && rstd_y == nullptr) || (dy.p != nullptr && !mat(dy))
+                     : pre == nullptr || post != nullptr || gate != nullptr || token_gate != nullptr ||
+                           dy.p != nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (weights && (ws == nullptr || !aligned(ws, 16))) return MOE_ERR_INVALID_ARG;
+  moe::BlockNormCall c{};
+  if (pre != nullptr) {
+    c.du = du.p;
+    c.lddu = du.ld;
+    c.r_in = r.p;
+    c.ldr = r.ld;
+    c.rstd_r = const_cast<float*>(rstd_r);
+  }
+  c.dr = dr.p;
+  c.lddr = dr.p != nullptr ? dr.ld : 0;
+  // y is read where something of it is asked for
+  if (post != nullptr || gate != nullptr || token_gate != nullptr) {
+    c.y = y.p;
+    c.ldy = y.ld;
+    c.rstd_y = const_cast<float*>(rstd_y);
+  }
+  c.post = post;
+  c.pre = pre;
+  c.gate = gate;
+  c.token_gate = token_gate;
+  c.dres = dres.p;
+  c.lddres = dres.ld;
+  c.dy = dy.p;
+  c.lddy = dy.p != nullptr ? dy.ld : 0;
+  c.dpost = dpost;
+  c.dpre = dpre;
+  c.dgate = dgate;
+  c.dtoken_gate = dtoken_gate;
+  c.partials = weights ? static_cast<float*>(ws) : nullptr;
+  c.d = d;
+  return from_cuda(moe::launch_block_norm(c, stream));
 }
 
 size_t moe_linear_workspace_bytes(moe_linear_dims d) {

@@ -30,6 +30,7 @@
 #include "kernels.h"
 #include "layer.h"
 #include "layer_common.cuh"
+#include "row_common.cuh"
 
 namespace moe {
 namespace {
@@ -46,32 +47,6 @@ struct NormArgs {
   float eps, inv_d;
   int D, nvec;
 };
-
-// Sum over the TPR threads of a row: within the warp, then (rows wider than
-// one warp own the whole block) over the warps' sums in shared memory.
-// `slot` alternates so that one barrier per sum is enough.
-template <bool ONE_WARP, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N], int nwarps) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if constexpr (!ONE_WARP) {
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) red[warp][i] = v[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float p = (threadIdx.x & 31) < nwarps ? red[threadIdx.x & 31][i] : 0.0f;
-      v[i] = warp_sum(p);
-    }
-  }
-}
-
-constexpr int kMaxThreads = 512;  // threads of a row at most: 128 registers each
-constexpr int kMaxD = 8192;
-constexpr int kRowsPerBlock = 4;  // rows of one warp each
 
 // One row per block of blockDim.x threads, or (ONE_WARP) one row per warp.
 template <typename T, typename W, int VEC, int NV, bool ONE_WARP>
@@ -157,41 +132,6 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormArgs<T>
       a[i].pack(f);
       a[i].store(y, c);
     }
-  }
-}
-
-// ------------------------------------------------------------ shifted rows
-// Vector c of a row that starts `e` elements into its first 16-byte unit: its
-// elements [lo, hi) are the row's.
-template <int VEC>
-struct Edge {
-  int lo, hi;
-  __device__ __forceinline__ Edge(int c, int e, int D) : lo(c == 0 ? e : 0), hi(min(VEC, e + D - c * VEC)) {}
-  __device__ __forceinline__ bool whole() const { return lo == 0 && hi == VEC; }
-};
-template <typename T>
-__device__ __forceinline__ int unit_offset(const T* row) {  // in elements
-  return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u) / static_cast<int>(sizeof(T));
-}
-// The vector's 16-byte unit up to the row's end, zeros behind.  Ahead of the
-// row's start it reads the rest of the unit, which is the same allocation's
-// (allocations start at such units), whatever it holds.
-template <typename T, int VEC>
-__device__ __forceinline__ void copy_unit(void* slot, const T* unit, const Edge<VEC>& g) {
-  cp_async16_zfill(slot, unit, g.hi * static_cast<int>(sizeof(T)));
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store_part(const float (&f)[VEC], T* unit, const Edge<VEC>& g) {
-#pragma unroll
-  for (int j = 0; j < VEC; ++j)
-    if (j >= g.lo && j < g.hi) unit[j] = from_f32<T>(f[j]);
-}
-template <typename W, int VEC>
-__device__ __forceinline__ void load_shifted_weights(const W* w, int c, int e, int D, float (&f)[VEC]) {
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    const int col = c * VEC + j - e;
-    f[j] = col >= 0 && col < D ? to_f32<W>(__ldg(w + col)) : 0.0f;
   }
 }
 
@@ -344,18 +284,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_shift_kernel(const No
 // they become one row of `partials` ([blocks][2][D]: dgamma, dbeta).
 constexpr int64_t kOneBlockRows = 8;
 constexpr int kBwdGroups = 4;  // ONE_WARP: warps of a block, each on rows of its own
-
-template <typename T, int VEC>
-__device__ __forceinline__ void copy_async(void* dst, const T* src) {
-  if constexpr (VEC * sizeof(T) == 16) {
-    cp_async16(dst, src);
-  } else if constexpr (sizeof(T) == 4) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
-                 : "memory");
-  } else {
-    *static_cast<T*>(dst) = *src;  // two bytes: below cp.async's smallest copy
-  }
-}
 
 // Sums of N = 2 or 4 values over the threads of a row group.  Within a warp
 // the lanes first halve the values they carry (16, then 8 lanes to a value),
@@ -709,8 +637,6 @@ __global__ void __launch_bounds__(kJoinCols* kJoinRows)
   }
 }
 
-int round32(int64_t v) { return static_cast<int>((v + 31) / 32 * 32); }
-
 template <typename T>
 NormArgs<T> make_args(const NormCall& c, int vec) {
   NormArgs<T> a{};
@@ -755,22 +681,6 @@ bool alike_rows(const NormCall& c, size_t elem) {
   const auto ok = [&](const void* p, int64_t ld) { return p == nullptr || place(p, ld) == place(c.x, c.ldx); };
   return ok(c.res, c.ldres) && ok(c.r, c.ldr) && ok(c.r_in, c.ldr) && ok(c.y, c.ldy);
 }
-int shifted_vectors(int D, int vec) { return (D + 2 * vec - 2) / vec; }
-
-// A number of blocks whose groups walk rows by a multiple of `period` (the
-// rows after which a shifted row's place repeats), if they walk at all.
-int64_t walk_blocks(int64_t blocks, int groups, int64_t rows, int period) {
-  if (blocks * groups >= rows) return blocks;
-  const int64_t unit = std::max(1, period / groups);
-  return std::max(unit, blocks / unit * unit);
-}
-
-// Blocks that an SM holds: a warp's registers (in units of 8 per thread) lie
-// in one of its four partitions of 512 per lane, 16 warps' places each.
-int resident_blocks(int threads, int regs) {
-  return std::max(1, std::min(64, 4 * (512 / ((regs + 7) / 8 * 8))) / (threads / 32));
-}
-
 template <typename T, typename W, int VEC, int NV>
 cudaError_t fwd_nv(const NormCall& c, cudaStream_t s) {
   const NormArgs<T> a = make_args<T>(c, VEC);
@@ -784,24 +694,6 @@ cudaError_t fwd_nv(const NormCall& c, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Calls go(n) with the smallest of the compiled vector counts per thread
-// that is at least `want` and covers nvec with kMaxThreads threads.
-template <int VEC, int MOST_WANTED, class Go>
-cudaError_t pick_nv(int nvec, int want, Go go) {
-  const int n = std::max(want, (nvec + kMaxThreads - 1) / kMaxThreads);
-  using std::integral_constant;
-  if constexpr (VEC == 1) {
-    if (n <= 4) return go(integral_constant<int, 4>{});
-    return go(integral_constant<int, 16>{});
-  } else {
-    if (n <= 1) return go(integral_constant<int, 1>{});
-    constexpr int kNeeded = kMaxD / VEC / kMaxThreads;
-    if constexpr (std::max(kNeeded, MOST_WANTED) > 2)
-      if (n > 2) return go(integral_constant<int, 4>{});
-    return go(integral_constant<int, 2>{});
-  }
-}
-
 // Vectors per thread: four keep enough bytes in flight per thread when there
 // are rows for every SM; a few rows are bound by latency and get as many
 // threads as their vectors.
@@ -812,32 +704,6 @@ cudaError_t fwd_vec(const NormCall& c, cudaStream_t s) {
   const int want = many ? std::min(4, (nvec + 31) / 32) : 1;
   return pick_nv<VEC, 4>(nvec, want, [&](auto n) { return fwd_nv<T, W, VEC, decltype(n)::value>(c, s); });
 }
-// What the launch of a walking kernel needs to know of it, looked up once
-// per device: a captured launch then makes no such call.
-struct KernelLimits {
-  std::atomic<int> regs[64];  // 0: not looked up
-};
-constexpr size_t kMaxDynamicSmem = 220 * 1024;
-
-template <class K>
-cudaError_t kernel_regs(K kern, KernelLimits& lim, int* regs) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  *regs = lim.regs[dev].load(std::memory_order_acquire);
-  if (*regs > 0) return cudaSuccess;
-  cudaFuncAttributes at{};
-  err = cudaFuncGetAttributes(&at, kern);
-  if (err != cudaSuccess) return err;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kMaxDynamicSmem));
-  if (err != cudaSuccess) return err;
-  *regs = std::max(at.numRegs, 1);
-  lim.regs[dev].store(*regs, std::memory_order_release);
-  return cudaSuccess;
-}
-
 template <typename T, typename W, int VEC, int NV, bool ONE_WARP>
 cudaError_t fwd_shift_launch(const NormCall& c, cudaStream_t s) {
   const int groups = ONE_WARP ? kRowsPerBlock : 1;

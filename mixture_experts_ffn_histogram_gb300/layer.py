@@ -187,6 +187,134 @@ class LayerNorm:
         return self._dx if n == self.rows else self._dx[:n]
 
 
+class BlockNorm:
+    """RMS norms after and before a block, with its gate and residual scale:
+
+        r = res + scale * token_gate * gate * norm(y) * (post + offset)
+        u = norm(r) * (pre + offset)
+
+    over rows of D, up to ``rows`` of them: y is what the block returned, res
+    the residual stream, r the stream behind the block and u the next block's
+    input.  Any of post, pre, gate (a weight for each channel) and token_gate
+    (fp32, one for each row) may be None: no norm, no gate.  y None: u =
+    norm(res), in front of the first block.
+
+    ``forward`` returns u (r without pre) and leaves ``r``, ``u``, and with
+    ``train`` the rows' ``rstd_y`` and ``rstd_r``.  ``backward`` takes the
+    gradients of u and of r (what else flows into the stream; may be None with
+    pre) and returns the gradient of res; ``dy``, ``dpost``, ``dpre``,
+    ``dgate`` and ``dtoken_gate`` hold the others, None where the call gave no
+    such argument."""
+
+    def __init__(self, rows, D, dtype=torch.bfloat16, weight_dtype=torch.float32, eps=1e-6, scale=1.0,
+                 offset=0.0, train=True, device="cuda"):
+        if dtype not in B.DTYPES or weight_dtype not in (dtype, torch.float32):
+            raise ValueError(f"rows of {dtype} with weights of {weight_dtype} are not supported")
+        self.rows, self.D, self.dtype, self.weight_dtype, self.train = rows, D, dtype, weight_dtype, train
+        self.d = B.block_norm_dims(rows, D, dtype, weight_dtype, eps, scale, offset)
+        dev = torch.device(device)
+        self._r = torch.empty((rows, D), dtype=dtype, device=dev)
+        self.device = dev = self._r.device
+        self._u = torch.empty_like(self._r)
+        self.r = self.u = self.rstd_y = self.rstd_r = None
+        self.dy = self.dpost = self.dpre = self.dgate = self.dtoken_gate = None
+        self._mr, self._mu = _own(self._r), _own(self._u)
+        self._p_stats = (None, None)
+        if train:
+            self._stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
+            self._dres, self._dy_out = torch.empty_like(self._r), torch.empty_like(self._r)
+            self._dw = torch.empty((3, D), dtype=weight_dtype, device=dev)
+            self._dtg = torch.empty(rows, dtype=torch.float32, device=dev)
+            self.ws = torch.empty(max(B.moe_block_norm_workspace_bytes(self.d), 256), dtype=torch.uint8,
+                                  device=dev)
+            self._mdres, self._mdy = _own(self._dres), _own(self._dy_out)
+            self._p_stats = tuple(t.data_ptr() for t in self._stats)
+            self._p_dw, self._p_ws = [t.data_ptr() for t in self._dw], self.ws.data_ptr()
+            self._p_dtg = self._dtg.data_ptr()
+        self._res, self._y, self._rin, self._du, self._dr = (
+            _Arg(n, dtype, dev) for n in ("res", "y", "r", "du", "dr"))
+        self._weights = tuple(_Arg(n, weight_dtype, dev, contiguous=True) for n in ("post", "pre", "gate"))
+        self._rowwise = tuple(_Arg(n, torch.float32, dev, contiguous=True)
+                              for n in ("token_gate", "rstd_y", "rstd_r"))
+        self._width = (D,)
+        self._fwd, self._bwd = _entry("moe_block_norm", dev), _entry("moe_block_norm_bwd", dev)
+
+    def _given(self, n, y, post, pre, gate, token_gate):
+        """The addresses of the weights and gates (None where not given)."""
+        if y is None and (pre is None or post is not None or gate is not None or token_gate is not None):
+            raise ValueError("without y there is only the norm before the block: pre, and no post or gates")
+        w = self._width
+        a, b, c = self._weights
+        return (None if post is None else a.pointer(post, w), None if pre is None else b.pointer(pre, w),
+                None if gate is None else c.pointer(gate, w),
+                None if token_gate is None else self._rowwise[0].pointer(token_gate, (n,)))
+
+    def forward(self, res, y=None, post=None, pre=None, gate=None, token_gate=None, stream=None):
+        D = self.D
+        n = self._res.first(res, self.rows, D)
+        p = self._given(n, y, post, pre, gate, token_gate)
+        my = _NO if y is None else self._y.matrix(y, (n, D))
+        self.d.rows = n
+        st = self._fwd(my, self._res.mat, *p, self._mr, self._mu, *self._p_stats, self.d,
+                       B.stream_of(stream, self.device))
+        if st:
+            _refused("moe_block_norm", st)
+        whole = n == self.rows
+        self.r = res if y is None else (self._r if whole else self._r[:n])
+        self.u = None if pre is None else (self._u if whole else self._u[:n])
+        if self.train:
+            self.rstd_y = None if post is None else self._stats[0, :n]
+            self.rstd_r = None if pre is None else self._stats[1, :n]
+        return self.r if pre is None else self.u
+
+    def backward(self, du, dr, r=None, y=None, post=None, pre=None, gate=None, token_gate=None,
+                 rstd_y=None, rstd_r=None, stream=None):
+        if not self.train:
+            raise RuntimeError("the norms were built without train=True")
+        if (du is None) != (pre is None):
+            raise ValueError("du is the gradient of the norm before the next block: given with pre, and only then")
+        if dr is None and pre is None:
+            raise ValueError("without pre the gradient of r has to be given")
+        D = self.D
+        first, arg = (du, self._du) if du is not None else (dr, self._dr)
+        n = arg.first(first, self.rows, D)
+        p = self._given(n, y, post, pre, gate, token_gate)
+        mdu = mr = mdr = my = _NO
+        py = pr = None
+        if du is not None:
+            mdu = self._du.mat
+            r = self.r if r is None else r
+            rstd_r = self.rstd_r if rstd_r is None else rstd_r
+            if r is None or rstd_r is None:
+                raise RuntimeError("backward needs a forward first, or its r and rstd_r")
+            mr, pr = self._rin.matrix(r, (n, D)), self._rowwise[2].pointer(rstd_r, (n,))
+        if dr is not None:
+            mdr = self._dr.matrix(dr, (n, D))
+        if y is not None:
+            my = self._y.matrix(y, (n, D))
+            if post is not None:
+                rstd_y = self.rstd_y if rstd_y is None else rstd_y
+                if rstd_y is None:
+                    raise RuntimeError("backward needs a forward first, or its rstd_y")
+                py = self._rowwise[1].pointer(rstd_y, (n,))
+        self.d.rows = n
+        dpost, dpre, dgate = (a if given else None for a, given in zip(self._p_dw, (post is not None,
+                                                                                   pre is not None,
+                                                                                   gate is not None)))
+        st = self._bwd(mdu, mdr, mr, my, *p, py, pr, self._mdres, _NO if y is None else self._mdy, dpost, dpre,
+                       dgate, self._p_dtg if token_gate is not None else None, self._p_ws, self.d,
+                       B.stream_of(stream, self.device))
+        if st:
+            _refused("moe_block_norm_bwd", st)
+        whole = n == self.rows
+        self.dy = None if y is None else (self._dy_out if whole else self._dy_out[:n])
+        self.dpost = None if post is None else self._dw[0]
+        self.dpre = None if pre is None else self._dw[1]
+        self.dgate = None if gate is None else self._dw[2]
+        self.dtoken_gate = None if token_gate is None else self._dtg[:n]
+        return self._dres if whole else self._dres[:n]
+
+
 class TopKRouter:
     """Selection of K of E experts for up to T tokens: scores sigmoid(l) or
     softmax(l), a balance bias that steers the selection only, choice limited

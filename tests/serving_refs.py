@@ -52,3 +52,76 @@ def experts(x, wi, wo, ids, w, res, own_weights):
         out = out + res.double()
         err = err + 2 * U32 * out.abs()
     return out, err
+
+
+# ----------------------------------------------------------- norms around a block
+def block_norm(res, y, post, pre, gate, token_gate, scale, offset, eps, r=None):
+    """dict of r, u, rstd_y, rstd_r in 64 bits (u from the given stored r), and
+    the bounds' magnitudes of r and u."""
+    out, f = {}, res.double()
+    D = f.shape[1]
+    out["r"], out["r_mag"] = f, f.abs()
+    if y is not None:
+        n = y.double()
+        if post is not None:
+            out["rstd_y"] = 1 / (n.square().mean(1) + eps).sqrt()
+            n = n * out["rstd_y"][:, None] * (post.double() + offset)
+        c = scale * torch.ones(D, dtype=torch.float64, device=f.device) if gate is None else scale * gate.double()
+        branch = n * c
+        if token_gate is not None:
+            branch = branch * token_gate.double()[:, None]
+        out["r"], out["r_mag"] = f + branch, f.abs() + branch.abs()
+        if post is not None and offset:
+            out["r_mag"] = out["r_mag"] + branch.abs() * ((post.double().abs() + abs(offset))
+                                                          / (post.double() + offset).abs().clamp(min=1e-30))
+    if pre is not None:
+        s = out["r"] if r is None else r.double()
+        out["rstd_r"] = 1 / (s.square().mean(1) + eps).sqrt()
+        out["u"] = s * out["rstd_r"][:, None] * (pre.double() + offset)
+        out["u_mag"] = s.abs() * out["rstd_r"][:, None] * (pre.double().abs() + abs(offset))
+    return out
+
+
+def block_norm_bwd(du, dr, r, y, post, pre, gate, token_gate, rstd_y, rstd_r, scale, offset):
+    """dict of name -> (gradient, magnitude of what enters it), in 64 bits from
+    the stored rows and statistics."""
+    shape = (dr if dr is not None else du).shape
+    n, D = shape
+    dev = (dr if dr is not None else du).device
+    zero, one = torch.zeros(shape, dtype=torch.float64, device=dev), torch.ones(D, dtype=torch.float64, device=dev)
+    d, dm, out = zero, zero, {}
+    if dr is not None:
+        d, dm = dr.double(), dr.double().abs()
+    if pre is not None:
+        rs, q, qm = rstd_r.double()[:, None], pre.double() + offset, pre.double().abs() + abs(offset)
+        rh, u = r.double() * rs, du.double()
+        a, am = u * q, u.abs() * qm
+        m, mm = (a * rh).mean(1, keepdim=True), (am * rh.abs()).mean(1, keepdim=True)
+        d, dm = d + rs * (a - m * rh), dm + rs * (am + mm * rh.abs())
+        out["dpre"] = ((u * rh).sum(0), (u * rh).abs().sum(0))
+    out["dres"] = (d, dm)
+    if y is None:
+        return out
+    yh, ry = y.double(), 1.0
+    if post is not None:
+        ry = rstd_y.double()[:, None]
+        yh = yh * ry
+    p = one if post is None else post.double() + offset
+    pm = one if post is None else post.double().abs() + abs(offset)
+    g0 = one if gate is None else gate.double()
+    g, gm = scale * g0 * p, abs(scale) * g0.abs() * pm
+    t = 1.0 if token_gate is None else token_gate.double()[:, None]
+    ta = abs(t) if token_gate is None else t.abs()
+    b, bm = (g * yh * d).sum(1, keepdim=True), (gm * yh.abs() * dm).sum(1, keepdim=True)
+    dy, dym = t * g * d, ta * gm * dm
+    if post is not None:
+        dy, dym = ry * (dy - t * b * yh / D), ry * (dym + ta * bm * yh.abs() / D)
+    out["dy"] = (dy, dym)
+    e, em = (t * d * yh).sum(0), (ta * dm * yh.abs()).sum(0)
+    if post is not None:
+        out["dpost"] = (scale * g0 * e, abs(scale) * g0.abs() * em)
+    if gate is not None:
+        out["dgate"] = (scale * p * e, abs(scale) * pm * em)
+    if token_gate is not None:
+        out["dtoken_gate"] = (b[:, 0], bm[:, 0])
+    return out
