@@ -70,7 +70,10 @@ __device__ __forceinline__ float square_sum(const float (&f)[VEC]) {
 // ---------------------------------------------------------------- forward
 // One row per block of blockDim.x threads, or (ONE_WARP) one row per warp.
 template <typename T, typename W, int VEC, int NV, bool ONE_WARP>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const Args<T, W> p) {
+__global__ void __launch_bounds__(kMaxThreads, NV <= 2 ? 3 : 1) block_norm_kernel(const Args<T, W> p) {
+  using N = Nums<VEC>;
+  using F = typename N::F;
+  constexpr int kN = N::kN;
   __shared__ float red[2][32][1];
   const int tpr = ONE_WARP ? 32 : blockDim.x;
   const int t = ONE_WARP ? (threadIdx.x & 31) : threadIdx.x;
@@ -78,6 +81,38 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const Args<T, W
                                : static_cast<int64_t>(blockIdx.x);
   if (ONE_WARP && row >= p.rows) return;
   const int nwarps = blockDim.x >> 5;
+  const auto values = [](const Raw<T, VEC>& raw, F (&v)[kN]) {
+    float f[VEC];
+    raw.unpack(f);
+    N::gather(f, v);
+  };
+  const auto weights = [&](const W* w, float offset, int at, F (&v)[kN]) {
+    float f[VEC];
+    weights_or_one<W, VEC, false>(w, offset, at, 0, p.D, f);
+    N::gather(f, v);
+  };
+  // of the row whose vectors are in x
+  const auto rstd_of = [&](const Raw<T, VEC> (&x)[NV], float (*slots)[1]) {
+    F s = N::splat(0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i * tpr + t < p.nvec) {
+        F v[kN];
+        values(x[i], v);
+#pragma unroll
+        for (int j = 0; j < kN; ++j) s = ffma(v[j], v[j], s);
+      }
+    }
+    float sum[1] = {fold(s)};
+    row_sums<ONE_WARP, 1>(sum, slots, nwarps);
+    return 1.0f / sqrtf(sum[0] * p.inv_d + p.eps);
+  };
+  const auto put = [&](const F (&v)[kN], Raw<T, VEC>& raw, T* to, int at) {
+    float f[VEC];
+    N::scatter(v, f);
+    raw.pack(f);
+    raw.store(to, at);
+  };
   Raw<T, VEC> a[NV], b[NV];
   const T* res = p.res + row * p.ldres;
 #pragma unroll
@@ -90,17 +125,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const Args<T, W
       if (i * tpr + t < p.nvec) a[i].load(y, i * tpr + t);
     float c = p.token_gate != nullptr ? p.scale * __ldg(p.token_gate + row) : p.scale;
     if (p.post != nullptr) {
-      float sum[1] = {0.0f};
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (i * tpr + t < p.nvec) {
-          float f[VEC];
-          a[i].unpack(f);
-          sum[0] += square_sum(f);
-        }
-      }
-      row_sums<ONE_WARP, 1>(sum, red[0], nwarps);
-      const float rstd = 1.0f / sqrtf(sum[0] * p.inv_d + p.eps);
+      const float rstd = rstd_of(a, red[0]);
       if (t == 0 && p.rstd_y != nullptr) p.rstd_y[row] = rstd;
       c *= rstd;
     }
@@ -109,51 +134,47 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const Args<T, W
     for (int i = 0; i < NV; ++i) {
       const int at = i * tpr + t;
       if (at < p.nvec) {
-        float f[VEC], g[VEC], w[VEC], m[VEC];
-        a[i].unpack(f);
-        b[i].unpack(g);
-        weights_or_one<W, VEC, false>(p.post, p.offset, at, 0, p.D, w);
-        weights_or_one<W, VEC, false>(p.gate, 0.0f, at, 0, p.D, m);
+        F f[kN], g[kN], w[kN];
+        values(a[i], f);
+        values(b[i], g);
+        weights(p.post, p.offset, at, w);
+        if (p.gate != nullptr) {
+          F m[kN];
+          weights(p.gate, 0.0f, at, m);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) g[j] = fmaf(f[j] * c, w[j] * m[j], g[j]);
-        b[i].pack(g);  // the stored row is what is normalised next
-        b[i].store(r, at);
+          for (int j = 0; j < kN; ++j) w[j] = fmul(w[j], m[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kN; ++j) g[j] = ffma(fmul(f[j], N::splat(c)), w[j], g[j]);
+        put(g, b[i], r, at);  // the stored row is what is normalised next
       }
     }
   }
   if (p.pre == nullptr) return;
-  float sum[1] = {0.0f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (i * tpr + t < p.nvec) {
-      float g[VEC];
-      b[i].unpack(g);
-      sum[0] += square_sum(g);
-    }
-  }
-  row_sums<ONE_WARP, 1>(sum, red[1], nwarps);
-  const float rstd = 1.0f / sqrtf(sum[0] * p.inv_d + p.eps);
+  const float rstd = rstd_of(b, red[1]);
   if (t == 0 && p.rstd_r != nullptr) p.rstd_r[row] = rstd;
   T* u = p.u + row * p.ldu;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int at = i * tpr + t;
     if (at < p.nvec) {
-      float g[VEC], w[VEC];
-      b[i].unpack(g);
-      weights_or_one<W, VEC, false>(p.pre, p.offset, at, 0, p.D, w);
+      F g[kN], w[kN];
+      values(b[i], g);
+      weights(p.pre, p.offset, at, w);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) g[j] = g[j] * rstd * w[j];
-      b[i].pack(g);
-      b[i].store(u, at);
+      for (int j = 0; j < kN; ++j) g[j] = fmul(fmul(g[j], N::splat(rstd)), w[j]);
+      put(g, b[i], u, at);
     }
   }
 }
 
 // Shifted rows: a group of threads walks rows, whose copies come `steps` - 1
 // ahead into the threads' own slots, and keeps the weights of its columns.
+// (Bound by instructions and by what is under way: held to 40 registers more
+// rows are (32768 x 1407 bf16 114 us, 119 without); two rows to a barrier
+// changed nothing, since few blocks then fit.)
 template <typename T, typename W, int VEC, int NV, bool ONE_WARP>
-__global__ void __launch_bounds__(kMaxThreads, 1) block_norm_shift_kernel(const Args<T, W> p, const int steps) {
+__global__ void __launch_bounds__(kMaxThreads, NV == 1 ? (ONE_WARP ? 2 : 3) : 1) block_norm_shift_kernel(const Args<T, W> p, const int steps) {
   using Q = Raw<T, VEC>;
   __shared__ float red[2][32][1];
   extern __shared__ __align__(16) unsigned char stage_mem[];
@@ -349,12 +370,19 @@ constexpr int kBwdGroups = 4;  // ONE_WARP: warps of a block, each on rows of it
 constexpr int64_t kOneBlockRows = 8;
 enum { kDu, kR, kDr, kY, kArrays };  // arrays of a row, each in its own slots
 
-template <typename T, typename W, int VEC, int NV, bool ONE_WARP, int R, bool SHIFT>
+// FULL: every array is given and all have the same ld, as between two blocks
+// of a contiguous model.  A row's place is then one offset, and no array is
+// asked for; where a thread has eight columns at most (HOLD) it keeps its
+// values between the sums and the gradients instead of unpacking them again.
+// (32768 x 2816 bf16 with neither: 460 instructions of a warp for a vector and
+// 262 us.)
+template <typename T, typename W, int VEC, int NV, bool ONE_WARP, int R, bool SHIFT, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const Args<T, W> p, const int steps) {
   using Q = Raw<T, VEC>;
   using N = Nums<VEC>;
   using F = typename N::F;
   constexpr int kN = N::kN, kPerStep = R * kArrays * NV, kSums = 4 * R;
+  constexpr bool HOLD = FULL && NV * VEC <= 8;
   __shared__ float red[2][kMaxThreads / 32][8];
   extern __shared__ __align__(16) unsigned char stage_mem[];
   const int tpr = ONE_WARP ? 32 : blockDim.x;
@@ -369,30 +397,32 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const Ar
   const int64_t ld[kArrays] = {p.lddu, p.ldr, p.lddr, p.ldy};
   const int e = SHIFT ? unit_offset(p.dres + first * p.lddres) : 0;
   const int nvec = SHIFT ? (e + p.D + VEC - 1) / VEC : p.nvec;
-  const T* at[kArrays];  // of the next row to fetch
-#pragma unroll
-  for (int q = 0; q < kArrays; ++q) at[q] = base[q] != nullptr ? base[q] + first * ld[q] - e + t * VEC : nullptr;
-  T* ds_at = p.dres + first * p.lddres - e + t * VEC;
-  T* dy_at = p.dy != nullptr ? p.dy + first * p.lddy - e + t * VEC : nullptr;
+  // (Addresses are made from the row's number each time: pointers kept for six
+  // arrays cost 16 registers.)
+  const auto place = [&](int64_t ld0, int k) {
+    return (first + static_cast<int64_t>(k) * step) * ld0 + (t * VEC - e);
+  };
   int fetched = 0;
   auto fetch = [&](int stage) {
     typename Q::Store* to = slots + stage * kPerStep * bd;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      if (fetched + r >= n) break;
+      int64_t off = FULL ? place(p.lddres, fetched + r) : 0;
 #pragma unroll
       for (int q = 0; q < kArrays; ++q) {
-        if (at[q] == nullptr) continue;
-        if (fetched + r < n) {
+        if constexpr (!FULL) {
+          if (base[q] == nullptr) continue;
+          off = place(ld[q], fetched + r);
+        }
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            if (i * tpr + t < nvec) {
-              auto* slot = to + ((r * kArrays + q) * NV + i) * bd;
-              if constexpr (SHIFT) copy_unit(slot, at[q] + i * tpr * VEC, Edge<VEC>(i * tpr + t, e, p.D));
-              else copy_async<T, VEC>(slot, at[q] + i * tpr * VEC);
-            }
+        for (int i = 0; i < NV; ++i) {
+          if (i * tpr + t < nvec) {
+            auto* slot = to + ((r * kArrays + q) * NV + i) * bd;
+            if constexpr (SHIFT) copy_unit(slot, base[q] + off + i * tpr * VEC, Edge<VEC>(i * tpr + t, e, p.D));
+            else copy_async<T, VEC>(slot, base[q] + off + i * tpr * VEC);
           }
         }
-        at[q] += step * ld[q];
       }
     }
     fetched += R;
@@ -433,10 +463,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const Ar
     else if (steps == 2) cp_async_wait_group<1>();
     else cp_async_wait_group<0>();
     const typename Q::Store* from = slots + stage * kPerStep * bd;
-    // rh, yh and dr + a / rms(r) of vector i of row r of the step; du too
-    const auto load = [&](int r, int i, float ry, float rr, F (&rh)[kN], F (&yh)[kN], F (&d)[kN], F (&du)[kN]) {
+    // of vector i of row r of the step: du q_pre as `a` (and du, if asked for),
+    // rh, yh and dr + a / rms(r)
+    const auto load = [&](int r, int i, float ry, float rr, F (&du)[kN], F (&a)[kN], F (&rh)[kN], F (&yh)[kN],
+                          F (&d)[kN]) {
       const auto get = [&](int q, F (&v)[kN]) {
-        if (base[q] != nullptr) {
+        if (FULL || base[q] != nullptr) {
           Q raw;
           raw.v = from[((r * kArrays + q) * NV + i) * bd];
           // ahead of the row's start the unit may hold anything
@@ -457,14 +489,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const Ar
       const F sr = N::splat(rr), sy = N::splat(ry);
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
+        a[j] = fmul(du[j], wa[i][j]);
         rh[j] = fmul(rh[j], sr);
         yh[j] = fmul(yh[j], sy);
-        d[j] = ffma(fmul(du[j], wa[i][j]), sr, d[j]);
+        d[j] = ffma(a[j], sr, d[j]);
       }
     };
     float ry[R], rr[R], tg[R], sums[kSums];
+    F rh[HOLD ? R : 1][NV][kN], yh[HOLD ? R : 1][NV][kN], d[HOLD ? R : 1][NV][kN];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      const int h = HOLD ? r : 0;
       ry[r] = __shfl_sync(0xffffffffu, lane_y, (k + r) & 31);
       rr[r] = __shfl_sync(0xffffffffu, lane_r, (k + r) & 31);
       tg[r] = __shfl_sync(0xffffffffu, lane_t, (k + r) & 31);
@@ -473,15 +508,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const Ar
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           if (i * tpr + t < nvec) {
-            F rh[kN], yh[kN], d[kN], du[kN];
-            load(r, i, ry[r], rr[r], rh, yh, d, du);
+            F du[kN], a[kN];
+            load(r, i, ry[r], rr[r], du, a, rh[h][i], yh[h][i], d[h][i]);
 #pragma unroll
             for (int j = 0; j < kN; ++j) {
-              const F dp = fmul(du[j], rh[j]), gy = fmul(wg[i][j], yh[j]);
-              sp[i][j] = fadd(sp[i][j], dp);
-              s1 = ffma(dp, wa[i][j], s1);
-              s2 = ffma(gy, d[j], s2);
-              s3 = ffma(gy, rh[j], s3);
+              const F gy = fmul(wg[i][j], yh[h][i][j]);
+              sp[i][j] = ffma(du[j], rh[h][i][j], sp[i][j]);
+              s1 = ffma(a[j], rh[h][i][j], s1);
+              s2 = ffma(gy, d[h][i][j], s2);
+              s3 = ffma(gy, rh[h][i][j], s3);
             }
           }
         }
@@ -495,22 +530,28 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const Ar
     par ^= 1;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      const int h = HOLD ? r : 0;
       if (r == 0 || k + r < n) {
         const float m = rr[r] * (sums[4 * r] * p.inv_d);
         const float b = sums[4 * r + 1] - m * sums[4 * r + 2];
         if (t == 0 && p.dtoken_gate != nullptr) p.dtoken_gate[first + static_cast<int64_t>(k + r) * step] = b;
         const float cy = p.post != nullptr ? tg[r] * b * p.inv_d : 0.0f;
-        const F nm = N::splat(-m), ts = N::splat(tg[r]), nc = N::splat(-cy * ry[r]), ty = N::splat(tg[r] * ry[r]);
+        const F nm = N::splat(-m), ts = N::splat(tg[r]), nc = N::splat(-cy * ry[r]), sy = N::splat(ry[r]);
+        const int64_t off = place(p.lddres, k + r);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           if (i * tpr + t < nvec) {
-            F rh[kN], yh[kN], d[kN], g[kN];
-            load(r, i, ry[r], rr[r], rh, yh, d, g);
+            F g[kN];
+            if constexpr (!HOLD) {
+              F a[kN];
+              load(r, i, ry[r], rr[r], g, a, rh[0][i], yh[0][i], d[0][i]);
+            }
 #pragma unroll
             for (int j = 0; j < kN; ++j) {
-              d[j] = ffma(rh[j], nm, d[j]);
-              se[i][j] = ffma(fmul(d[j], ts), yh[j], se[i][j]);
-              g[j] = ffma(fmul(wg[i][j], d[j]), ty, fmul(yh[j], nc));
+              d[h][i][j] = ffma(rh[h][i][j], nm, d[h][i][j]);
+              const F dt = fmul(d[h][i][j], ts);
+              se[i][j] = ffma(dt, yh[h][i][j], se[i][j]);
+              g[j] = ffma(fmul(wg[i][j], dt), sy, fmul(yh[h][i][j], nc));
             }
             const auto put = [&](const F (&v)[kN], T* to) {
               float f[VEC];
@@ -526,13 +567,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const Ar
               u.pack(f);
               u.store(to, 0);
             };
-            put(d, ds_at + i * tpr * VEC);
-            if (dy_at != nullptr) put(g, dy_at + i * tpr * VEC);
+            put(d[h][i], p.dres + off + i * tpr * VEC);
+            if constexpr (FULL) put(g, p.dy + off + i * tpr * VEC);
+            else if (p.dy != nullptr) put(g, p.dy + place(p.lddy, k + r) + i * tpr * VEC);
           }
         }
       }
-      ds_at += step * p.lddres;
-      if (dy_at != nullptr) dy_at += step * p.lddy;
     }
     if (++stage == steps) stage = 0;
   }
@@ -694,11 +734,12 @@ Rows kind_of_rows(const BlockNormCall& c) {
 template <typename T, typename W, int VEC>
 cudaError_t fwd_rows(const BlockNormCall& c, cudaStream_t s) {
   const int nvec = c.d.D / VEC;
-  // four vectors a thread keep enough bytes in flight when there are rows for
-  // every SM; a few rows are bound by latency and get as many threads as vectors
+  // two vectors a thread where there are rows for every SM: one takes 163 us for
+  // 32768 x 2816 bf16, four 125, two 123 (and 66 instead of 74 for 1408 columns);
+  // a few rows are bound by latency and get as many threads as vectors
   const bool many = c.d.rows >= 4 * static_cast<int64_t>(sm_count());
-  const int want = many ? std::min(4, (nvec + 31) / 32) : 1;
-  return pick_nv<VEC, 4>(nvec, want, [&](auto nv) {
+  const int want = many ? std::min(2, (nvec + 31) / 32) : 1;
+  return pick_nv<VEC, 2>(nvec, want, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
     const Args<T, W> a = make_args<T, W>(c, VEC);
     const int tpr = round32((nvec + NV - 1) / NV);
@@ -743,13 +784,13 @@ cudaError_t fwd_shift(const BlockNormCall& c, cudaStream_t s) {
   });
 }
 
-template <typename T, typename W, int VEC, int NV, bool ONE_WARP, int R, bool SHIFT>
+template <typename T, typename W, int VEC, int NV, bool ONE_WARP, int R, bool SHIFT, bool FULL>
 cudaError_t bwd_launch(const BlockNormCall& c, cudaStream_t s) {
   Args<T, W> a = make_args<T, W>(c, VEC);
   const int nvec = SHIFT ? shifted_vectors(c.d.D, VEC) : a.nvec;
   const int threads = ONE_WARP ? 32 * kBwdGroups : round32((nvec + NV - 1) / NV);
   const int groups = ONE_WARP ? kBwdGroups : 1;
-  auto kern = block_norm_bwd_kernel<T, W, VEC, NV, ONE_WARP, R, SHIFT>;
+  auto kern = block_norm_bwd_kernel<T, W, VEC, NV, ONE_WARP, R, SHIFT, FULL>;
   static KernelLimits limits;
   int regs = 0;
   cudaError_t err = kernel_regs(kern, limits, &regs);
@@ -797,6 +838,16 @@ cudaError_t bwd_launch(const BlockNormCall& c, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, block_norm_join_kernel<W>, j);
 }
 
+template <typename T, typename W, int VEC, int NV, bool ONE_WARP, int R, bool SHIFT>
+cudaError_t bwd_full(const BlockNormCall& c, cudaStream_t s) {
+  if constexpr (VEC > 1) {
+    bool full = true;
+    for (const void* p : {c.du, c.r_in, c.dr, c.y, static_cast<const void*>(c.dy)}) full = full && p != nullptr;
+    for (int64_t ld : {c.lddu, c.ldr, c.lddr, c.ldy, c.lddy}) full = full && ld == c.lddres;
+    if (full) return bwd_launch<T, W, VEC, NV, ONE_WARP, R, SHIFT, true>(c, s);
+  }
+  return bwd_launch<T, W, VEC, NV, ONE_WARP, R, SHIFT, false>(c, s);
+}
 // Two rows at a time where a thread holds up to eight columns.
 template <typename T, typename W, int VEC, bool SHIFT>
 cudaError_t bwd_rows(const BlockNormCall& c, cudaStream_t s) {
@@ -805,9 +856,9 @@ cudaError_t bwd_rows(const BlockNormCall& c, cudaStream_t s) {
     constexpr int NV = decltype(nv)::value;
     constexpr int R = NV * VEC <= 8 ? 2 : 1;
     if constexpr (NV == (VEC == 1 ? 4 : 1)) {  // more vectors per thread are only taken by wide rows
-      if (nvec <= 32 * NV) return bwd_launch<T, W, VEC, NV, true, R, SHIFT>(c, s);
+      if (nvec <= 32 * NV) return bwd_full<T, W, VEC, NV, true, R, SHIFT>(c, s);
     }
-    return bwd_launch<T, W, VEC, NV, false, R, SHIFT>(c, s);
+    return bwd_full<T, W, VEC, NV, false, R, SHIFT>(c, s);
   });
 }
 
