@@ -765,6 +765,43 @@ moe_status moe_block_norm_bwd(moe_mat du, moe_mat dr, moe_mat r, moe_mat y, cons
                               void* dpost, void* dpre, void* dgate, float* dtoken_gate, void* ws,
                               moe_block_norm_dims d, cudaStream_t stream);
 
+/*
+ * Low-rank adapters of many requests beside a shared projection.  A pool keeps
+ * `slots` adapters of one rank (narrower ones are padded with zeros): a
+ * [slots, rank, K] and b [slots, N, rank]; each of the batch's tokens names one
+ * of them, or none.
+ *
+ * The plan sorts a batch's tokens by adapter; all projections of the batch
+ * share it.
+ *   ids   int32 [n]   the token's slot, or -1; another value is reported as
+ *                     MOE_ERR_DEVICE and taken as -1
+ *   plan  moe_adapter_plan_bytes(T, slots) bytes, for up to T tokens
+ * 1 <= slots <= 1024, 0 <= n <= T <= 2^20.
+ */
+size_t moe_adapter_plan_bytes(int32_t T, int32_t slots);
+moe_status moe_adapter_plan(const int32_t* ids, int32_t n, int32_t T, int32_t slots, void* plan,
+                            int32_t* dev_status, cudaStream_t stream);
+
+/*
+ *   v = x[t] . a[s]^T  (fp32 sums),  y[t] = round(res[t] + round(scale[s] v) . b[s]^T),
+ *   s = ids[t];  y[t] = res[t] where the token names none (res.p NULL: 0)
+ *   x  `type` [n, K] (bf16 or fp16);  res, y  `type` [n, N], y may be res's
+ *   memory (same ld);  a, b  dense, of the same type;  scale  fp32 [slots]
+ *   (4-byte aligned, as ids)
+ * K, N and rank multiples of 8, rank <= 128.  plan: of d.T, d.slots and the
+ * call's n tokens; one of another number of tokens or slots is reported as
+ * MOE_ERR_DEVICE, and y is left as it was.  ws: moe_adapters_workspace_bytes(d) bytes.
+ * Results are reproducible bit for bit.
+ */
+typedef struct {
+  int32_t T, K, N, slots, rank;
+  int32_t type; /* moe_dtype */
+} moe_adapter_dims;
+size_t moe_adapters_workspace_bytes(moe_adapter_dims d);
+moe_status moe_adapters(moe_mat x, const void* a, const void* b, const float* scale, moe_mat res,
+                        moe_mat y, const void* plan, int32_t* dev_status, void* ws, int32_t n,
+                        moe_adapter_dims d, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,7 +20,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmoe.so")
 SOURCES = ["api.cu", "route.cu", "permute_combine.cu", "gemm.cu", "mx.cu",
            "layer_api.cu", "norm.cu", "route_topk.cu", "dense.cu", "act_grad.cu",
-           "decode.cu", "block_norm.cu"]
+           "decode.cu", "block_norm.cu",
+           "adapters.cu"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "kernels.h"),
            os.path.join(CSRC, "mx.h"), os.path.join(CSRC, "mx_common.cuh"),
            os.path.join(CSRC, "layer.h"), os.path.join(CSRC, "layer_common.cuh"),

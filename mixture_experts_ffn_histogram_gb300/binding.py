@@ -39,7 +39,8 @@ ENTRY_POINTS = (
     "moe_layer_norm", "moe_layer_norm_bwd", "moe_layer_norm_workspace_bytes", "moe_route_topk",
     "moe_route_topk_bwd", "moe_linear", "moe_linear_bwd", "moe_linear_workspace_bytes",
     "moe_decode", "moe_decode_workspace_bytes", "moe_block_norm", "moe_block_norm_bwd",
-    "moe_block_norm_workspace_bytes",
+    "moe_block_norm_workspace_bytes", "moe_adapter_plan", "moe_adapter_plan_bytes", "moe_adapters",
+    "moe_adapters_workspace_bytes",
 )
 
 # moe_dtype
@@ -88,6 +89,10 @@ class MoeBlockNormDims(ctypes.Structure):
                 ("offset", ctypes.c_float)]
 
 
+class MoeAdapterDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "slots", "rank", "type")]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn: str, status: int, detail: str | None = None):
         super().__init__(f"{fn}: {detail or status_string(status)} (status {status})")
@@ -114,6 +119,10 @@ def linear_dims(M, K, N, dtype=torch.bfloat16, out_dtype=None, act="none") -> Mo
 def block_norm_dims(rows, D, dtype=torch.bfloat16, weight_dtype=torch.float32, eps=1e-6, scale=1.0,
                     offset=0.0) -> MoeBlockNormDims:
     return MoeBlockNormDims(rows, D, DTYPES[dtype], DTYPES[weight_dtype], eps, scale, offset)
+
+
+def adapter_dims(T, K, N, slots, rank, dtype=torch.bfloat16) -> MoeAdapterDims:
+    return MoeAdapterDims(T, K, N, slots, rank, DTYPES[dtype])
 
 
 def library_path() -> str:
@@ -181,6 +190,10 @@ def lib() -> ctypes.CDLL:
             "moe_block_norm": ([M, M, P, P, P, P, M, M, P, P, MoeBlockNormDims, P], I),
             "moe_block_norm_bwd": ([M] * 4 + [P] * 6 + [M, M] + [P] * 5 + [MoeBlockNormDims, P], I),
             "moe_block_norm_workspace_bytes": ([MoeBlockNormDims], ctypes.c_size_t),
+            "moe_adapter_plan": ([P] + [ctypes.c_int32] * 3 + [P, P, P], I),
+            "moe_adapter_plan_bytes": ([ctypes.c_int32, ctypes.c_int32], ctypes.c_size_t),
+            "moe_adapters": ([M, P, P, P, M, M, P, P, P, ctypes.c_int32, MoeAdapterDims, P], I),
+            "moe_adapters_workspace_bytes": ([MoeAdapterDims], ctypes.c_size_t),
         })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -488,4 +501,23 @@ def moe_block_norm_bwd(du, dr, r, y, post, pre, gate, token_gate, rstd_y, rstd_r
     _ok("moe_block_norm_bwd", lib().moe_block_norm_bwd(
         _m(du), _m(dr), _m(r), _m(y), _p(post), _p(pre), _p(gate), _p(token_gate), _p(rstd_y),
         _p(rstd_r), _m(dres), _m(dy), _p(dpost), _p(dpre), _p(dgate), _p(dtoken_gate), _p(ws), d,
+        _s(stream)))
+
+
+def moe_adapter_plan_bytes(T: int, slots: int) -> int:
+    return int(lib().moe_adapter_plan_bytes(int(T), int(slots)))
+
+
+def moe_adapter_plan(ids, T: int, slots: int, plan, dev_status, stream=None):
+    _ok("moe_adapter_plan", lib().moe_adapter_plan(
+        _p(ids), ids.shape[0], int(T), int(slots), _p(plan), _p(dev_status), _s(stream)))
+
+
+def moe_adapters_workspace_bytes(d: MoeAdapterDims) -> int:
+    return int(lib().moe_adapters_workspace_bytes(d))
+
+
+def moe_adapters(x, a, b, scale, res, y, plan, dev_status, ws, d: MoeAdapterDims, stream=None):
+    _ok("moe_adapters", lib().moe_adapters(
+        _m(x), _p(a), _p(b), _p(scale), _m(res), _m(y), _p(plan), _p(dev_status), _p(ws), x.shape[0], d,
         _s(stream)))

@@ -70,7 +70,7 @@ __device__ __forceinline__ float square_sum(const float (&f)[VEC]) {
 // ---------------------------------------------------------------- forward
 // One row per block of blockDim.x threads, or (ONE_WARP) one row per warp.
 template <typename T, typename W, int VEC, int NV, bool ONE_WARP>
-__global__ void __launch_bounds__(kMaxThreads, NV <= 2 ? 3 : 1) block_norm_kernel(const Args<T, W> p) {
+__global__ void __launch_bounds__(kMaxThreads, NV <= 2 ? 3 : NV == 4 ? 2 : 1) block_norm_kernel(const Args<T, W> p) {
   using N = Nums<VEC>;
   using F = typename N::F;
   constexpr int kN = N::kN;
@@ -734,12 +734,12 @@ Rows kind_of_rows(const BlockNormCall& c) {
 template <typename T, typename W, int VEC>
 cudaError_t fwd_rows(const BlockNormCall& c, cudaStream_t s) {
   const int nvec = c.d.D / VEC;
-  // two vectors a thread where there are rows for every SM: one takes 163 us for
-  // 32768 x 2816 bf16, four 125, two 123 (and 66 instead of 74 for 1408 columns);
-  // a few rows are bound by latency and get as many threads as vectors
+  // Where there are rows for every SM, four vectors a thread for wide rows, two
+  // for others (32768 x 2816 bf16: 125 us against 129; 1408 columns: 68 against
+  // 64); a few rows are bound by latency and get as many threads as vectors.
   const bool many = c.d.rows >= 4 * static_cast<int64_t>(sm_count());
-  const int want = many ? std::min(2, (nvec + 31) / 32) : 1;
-  return pick_nv<VEC, 2>(nvec, want, [&](auto nv) {
+  const int want = many ? std::min(nvec > 256 ? 4 : 2, (nvec + 31) / 32) : 1;
+  return pick_nv<VEC, 4>(nvec, want, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
     const Args<T, W> a = make_args<T, W>(c, VEC);
     const int tpr = round32((nvec + NV - 1) / NV);

@@ -116,6 +116,28 @@ struct BlockNormCall {
 };
 cudaError_t launch_block_norm(const BlockNormCall& c, cudaStream_t s);
 
+// Low-rank adapters: d.T is the plan's capacity, n the call's tokens.
+struct AdapterCall {
+  const void* x;
+  int64_t ldx;
+  const void *a, *b;
+  const float* scale;
+  const void* res;
+  int64_t ldres;
+  void* y;
+  int64_t ldy;
+  const void* plan;
+  void* ws;
+  int32_t* dev_status;
+  int32_t n;
+  moe_adapter_dims d;
+};
+size_t adapter_plan_bytes(int64_t T, int slots);
+size_t adapter_ws_bytes(const moe_adapter_dims& d);
+cudaError_t launch_adapter_plan(const int32_t* ids, int32_t n, int32_t T, int32_t slots, void* plan,
+                                int32_t* dev_status, cudaStream_t s);
+cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s);
+
 // The expert layer for a few tokens: d.T is the capacity that the workspace
 // was made for, n <= d.T the call's tokens.
 struct DecodeCall {

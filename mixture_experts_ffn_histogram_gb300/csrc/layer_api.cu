@@ -59,6 +59,17 @@ moe_status check_linear(const moe_linear_dims& d) {
   return MOE_OK;
 }
 
+moe_status check_plan(int32_t T, int32_t slots) {
+  return T < 0 || T > (1 << 20) || slots < 1 || slots > 1024 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+moe_status check_adapters(const moe_adapter_dims& d) {
+  if (!is_dtype(d.type)) return MOE_ERR_INVALID_ARG;
+  if (d.type == MOE_FP32 || check_plan(d.T, d.slots) != MOE_OK) return MOE_ERR_UNSUPPORTED;
+  if (d.K < 8 || d.N < 8 || d.K % 8 != 0 || d.N % 8 != 0 || d.K > (1 << 22) || d.N > (1 << 22))
+    return MOE_ERR_UNSUPPORTED;
+  return d.rank < 8 || d.rank > 128 || d.rank % 8 != 0 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
 moe_status check_block_norm(const moe_block_norm_dims& d) {
   return check_norm(d.rows, d.D, static_cast<moe_dtype>(d.type), static_cast<moe_dtype>(d.wtype));
 }
@@ -385,6 +396,54 @@ moe_status moe_block_norm_bwd(moe_mat du, moe_mat dr, moe_mat r, moe_mat y, cons
   c.partials = weights ? static_cast<float*>(ws) : nullptr;
   c.d = d;
   return from_cuda(moe::launch_block_norm(c, stream));
+}
+
+size_t moe_adapter_plan_bytes(int32_t T, int32_t slots) {
+  return check_plan(T, slots) == MOE_OK ? moe::adapter_plan_bytes(T, slots) : 0;
+}
+
+moe_status moe_adapter_plan(const int32_t* ids, int32_t n, int32_t T, int32_t slots, void* plan,
+                            int32_t* dev_status, cudaStream_t stream) {
+  const moe_status st = check_plan(T, slots);
+  if (st != MOE_OK) return st;
+  if (n < 0 || n > T || plan == nullptr || !aligned(plan, 16) || !aligned(dev_status, 4) || !aligned(ids, 4) ||
+      (n > 0 && ids == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  return from_cuda(moe::launch_adapter_plan(ids, n, T, slots, plan, dev_status, stream));
+}
+
+size_t moe_adapters_workspace_bytes(moe_adapter_dims d) {
+  return check_adapters(d) == MOE_OK ? round256(moe::adapter_ws_bytes(d)) : 0;
+}
+
+moe_status moe_adapters(moe_mat x, const void* a, const void* b, const float* scale, moe_mat res, moe_mat y,
+                        const void* plan, int32_t* dev_status, void* ws, int32_t n, moe_adapter_dims d,
+                        cudaStream_t stream) {
+  const moe_status st = check_adapters(d);
+  if (st != MOE_OK) return st;
+  if (n < 0 || n > d.T) return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  const auto given = [](const void* p) { return p != nullptr && aligned(p, 16); };
+  if (!vector_mat(x, d.K, d.type) || !vector_mat(y, d.N, d.type) || !given(a) || !given(b) || !given(plan) ||
+      !given(ws) || scale == nullptr || !aligned(scale, 4) || !aligned(dev_status, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (res.p != nullptr && !vector_mat(res, d.N, d.type)) return MOE_ERR_INVALID_ARG;
+  moe::AdapterCall c{};
+  c.x = x.p;
+  c.ldx = x.ld;
+  c.a = a;
+  c.b = b;
+  c.scale = scale;
+  c.res = res.p;
+  c.ldres = res.ld;
+  c.y = y.p;
+  c.ldy = y.ld;
+  c.plan = plan;
+  c.ws = ws;
+  c.dev_status = dev_status;
+  c.n = n;
+  c.d = d;
+  return from_cuda(moe::launch_adapters(c, stream));
 }
 
 size_t moe_linear_workspace_bytes(moe_linear_dims d) {

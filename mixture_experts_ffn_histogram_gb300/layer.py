@@ -464,6 +464,87 @@ class Linear:
         return self._dx if n == self.M else self._dx[:n]
 
 
+class AdapterBatch:
+    """Which adapter each token of a batch uses: up to T tokens, ``slots``
+    adapters in the pool.  ``group`` takes ids (int32, one a token: a slot, or
+    -1 for none) and sorts the tokens by adapter on the device; every
+    ``LowRankAdapters`` of the batch's step takes it so.  An id outside
+    [-1, slots) is reported in ``status`` and taken as -1."""
+
+    def __init__(self, T, slots, device="cuda"):
+        need = B.moe_adapter_plan_bytes(T, slots)
+        if need == 0:
+            raise ValueError(f"unsupported sizes: T={T}, slots={slots} (T <= 2^20, 1 <= slots <= 1024)")
+        self.T, self.slots, self.n = T, slots, None
+        dev = torch.device(device)
+        self.plan = torch.zeros(need, dtype=torch.uint8, device=dev)
+        self.device = dev = self.plan.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._ids = _Arg("ids", torch.int32, dev, contiguous=True)
+        self._p_plan, self._p_status = self.plan.data_ptr(), self.status.data_ptr()
+        self._fwd = _entry("moe_adapter_plan", dev)
+
+    def group(self, ids, stream=None):
+        n = ids.shape[0] if ids.dim() == 1 else -1
+        if not 0 <= n <= self.T:
+            self._ids.refuse(ids, (f"<= {self.T}",))
+        p = self._ids.pointer(ids, (n,))
+        st = self._fwd(p, n, self.T, self.slots, self._p_plan, self._p_status, B.stream_of(stream, self.device))
+        if st:
+            _refused("moe_adapter_plan", st)
+        self.n = n
+        return self
+
+
+class LowRankAdapters:
+    """y = res + scale[s] (x a[s]^T) b[s]^T for up to T tokens, each with the
+    adapter s that the batch names for it (none: y = res), beside a shared
+    projection whose result is res (None: zeros).
+
+    A pool of ``slots`` adapters of one ``rank`` (a multiple of 8 up to 128;
+    narrower ones padded with zeros): a [slots, rank, K], b [slots, N, rank]
+    in bf16 or fp16 like the rows, scale fp32 [slots].  ``batch`` is an
+    ``AdapterBatch`` of the same T and slots, grouped for these tokens on the
+    same stream or before.  ``status`` is the kernels' error word."""
+
+    def __init__(self, T, K, N, slots, rank, dtype=torch.bfloat16, device="cuda"):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"adapters of {dtype} are not supported")
+        self.T, self.K, self.N, self.slots, self.rank, self.dtype = T, K, N, slots, rank, dtype
+        self.d = B.adapter_dims(T, K, N, slots, rank, dtype)
+        need = B.moe_adapters_workspace_bytes(self.d)
+        if need == 0:
+            raise ValueError(f"unsupported sizes: T={T}, K={K}, N={N}, slots={slots}, rank={rank} (K, N and rank "
+                             "multiples of 8, rank <= 128, T <= 2^20, 1 <= slots <= 1024)")
+        dev = torch.device(device)
+        self._y = torch.empty((T, N), dtype=dtype, device=dev)
+        self.device = dev = self._y.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        self._my, self._p_status, self._p_ws = _own(self._y), self.status.data_ptr(), self.ws.data_ptr()
+        self._x, self._res = _Arg("x", dtype, dev), _Arg("res", dtype, dev)
+        self._a, self._b = (_Arg(n, dtype, dev, contiguous=True) for n in ("a", "b"))
+        self._scale = _Arg("scale", torch.float32, dev, contiguous=True)
+        self._ashape, self._bshape = (slots, rank, K), (slots, N, rank)
+        self._fwd = _entry("moe_adapters", dev)
+
+    def forward(self, batch, x, a, b, scale, res=None, stream=None):
+        n = self._x.first(x, self.T, self.K)
+        if batch.T != self.T or batch.slots != self.slots or batch.device != self.device:
+            raise ValueError(f"the batch is for {batch.T} tokens and {batch.slots} slots on {batch.device}, the "
+                             f"adapters for {self.T} and {self.slots} on {self.device}")
+        if batch.n != n:
+            raise ValueError(f"the batch was grouped for {batch.n} tokens, the call has {n}")
+        pa, pb = self._a.pointer(a, self._ashape), self._b.pointer(b, self._bshape)
+        ps = self._scale.pointer(scale, (self.slots,))
+        mres = _NO if res is None else self._res.matrix(res, (n, self.N))
+        st = self._fwd(self._x.mat, pa, pb, ps, mres, self._my, batch._p_plan, self._p_status, self._p_ws, n,
+                       self.d, B.stream_of(stream, self.device))
+        if st:
+            _refused("moe_adapters", st)
+        return self._y if n == self.T else self._y[:n]
+
+
 class MoEDecode:
     """The whole expert layer for up to T tokens, a few (T <= 256): routing,
     both expert products with SwiGLU and the weighted combine, in one kernel

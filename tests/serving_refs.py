@@ -125,3 +125,27 @@ def block_norm_bwd(du, dr, r, y, post, pre, gate, token_gate, rstd_y, rstd_r, sc
     if token_gate is not None:
         out["dtoken_gate"] = (b[:, 0], bm[:, 0])
     return out
+
+
+# ------------------------------------------------------------- low-rank adapters
+def adapters(x, a, b, scale, ids, res):
+    """(y, its bound's arithmetic part)."""
+    T, K = x.shape
+    S, r = a.shape[:2]
+    y = torch.zeros(T, b.shape[1], dtype=torch.float64, device=x.device)
+    err = torch.zeros_like(y)
+    u = half_step(x.dtype)
+    sub = torch.finfo(x.dtype).smallest_normal * torch.finfo(x.dtype).eps  # v below the normal numbers
+    for s in range(S):
+        t = torch.nonzero(ids == s)[:, 0]
+        c = float(scale[s])
+        p, q, w = x[t].double(), a[s].double(), b[s].double()
+        v, vm = c * (p @ q.t()), abs(c) * (p.abs() @ q.abs().t())
+        # the sum over K (cut in up to 32 parts), the scale, the rounding
+        dv = (sum_error(K, False) + 34 * U32) * vm + u * v.abs() * (1 + 2.0 ** -6) + sub
+        y[t] = v @ w.t()
+        err[t] = dv @ w.abs().t() + (r / 16 + 18) * 2 * U32 * (v.abs() @ w.abs().t())
+    if res is not None:
+        y = y + res.double()
+        err = err + 2 * U32 * y.abs()
+    return y, err
