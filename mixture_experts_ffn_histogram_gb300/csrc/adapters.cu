@@ -9,15 +9,16 @@
 // list of tiles of up to 128 tokens of one adapter (those without one come
 // last).  Made once for a batch: all of its projections share it.
 // shrink: v = x a_s^T by tile on the tensor cores.  The tile's tokens are
-// gathered straight from x (four rows of 128 bytes to a TMA gather) as the 128
-// side, the rank is the narrow side, and the reduction over K is cut among
-// CTAs where tiles are few.  Bound by reading x; for a few tokens by latency.
+// gathered straight from x (four rows of 128 bytes to a TMA gather, or one box
+// where they follow one another) as the 128 side, the rank is the narrow side,
+// and the reduction over K is cut among CTAs where tiles are few.  Bound by
+// reading x; for a few tokens by latency.
 // expand: y = res + scale v b_s^T.  Its reduction is the rank, one to eight
 // MMAs deep, so that nearly all of it is moving res and y: the products are
 // mma.sync's, whose accumulators already lie in the registers that add and
 // store (tensor memory would add a round trip to a kernel without a main loop).
 // Columns and reduction indices are permuted among the fragments so that every
-// access is 8 or 16 contiguous bytes; nothing goes through shared memory.
+// access is 8 or 16 contiguous bytes.
 //
 // v is summed in fp32 (over the cuts in their order) and rounded once to the
 // operands' type for the second product, with the scale: half a step on each of
@@ -40,10 +41,14 @@ constexpr int kTile = 128;  // tokens
 
 // A plan in memory: the header, the tiles, the tokens in their order.
 struct PlanHead {
-  int32_t n, slots, tiles, pad;
+  int32_t n, slots;
+  int32_t tiles;  // of tokens with an adapter
+  int32_t none;   // tiles behind them, of tokens without
+  int32_t live;   // tokens with an adapter: the first ones in the order
+  int32_t pad[3];
 };
 struct PlanTile {
-  int32_t adapter, start, count, pad;  // adapter -1: none
+  int32_t adapter, start, count, pad;
 };
 __host__ __device__ inline int64_t most_tiles(int64_t T, int64_t slots) {
   return T / kTile + (slots + 1 < T ? slots + 1 : T);
@@ -121,10 +126,13 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int c = count[b - b0];
     for (int w = 0; w < kPlanWarps; ++w) before[w * buckets + b] += at;  // places in the order
     for (int i = 0; i < c; i += kTile)
-      tiles[tile++] = PlanTile{b < slots ? b : -1, at + i, min(kTile, c - i), 0};
+      tiles[tile++] = PlanTile{b, at + i, min(kTile, c - i), 0};
+    if (b == slots) {  // the last bucket
+      const int none = (c + kTile - 1) / kTile;
+      *head = PlanHead{n, slots, all - none, none, at, {0, 0, 0}};
+    }
     at += c;
   }
-  if (threadIdx.x == 0) *head = PlanHead{n, slots, all, 0};
   __syncthreads();
   for (int j = j0; j < j1; j += 32) {
     const int b = bucket_of(j + lane);
@@ -143,13 +151,20 @@ __global__ void __launch_bounds__(kPlanThreads)
 constexpr int kShrinkThreads = 192;
 constexpr int kTokenStage = kTile * kBlockK * 2;  // 16 KB
 constexpr int kMaxStages = 8;
+constexpr int kLeastCutBlocks = 4;
+
+// The cuts of a tile's reduction: as many as give every CTA of the grid (two
+// to an SM) at most one, of four blocks at least.
+__device__ __forceinline__ int cuts_of(int tiles, int grid, int kblocks) {
+  return tiles > 0 ? max(1, min(grid / tiles, kblocks / kLeastCutBlocks)) : 1;
+}
 
 struct ShrinkParams {
   const PlanHead* head;
   const PlanTile* tiles;
   const int32_t* order;
-  float* v;             // [splits][n][r]: by place in the order
-  int n, slots, rank, width, kblocks, splits, stages;  // width: rank in whole 16s
+  float* v;  // [cuts][live tokens][r], by place in the order
+  int n, slots, rank, width, kblocks, stages;  // width: rank in whole 16s
   uint32_t type;
   int32_t* status;
   uint64_t limit_ns;
@@ -157,7 +172,8 @@ struct ShrinkParams {
 struct ShrinkCtl {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
-  uint64_t done;
+  uint64_t done;     // a unit's products
+  uint64_t drained;  // ... have been read
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -175,26 +191,24 @@ __device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, uint6
       : "memory");
 }
 
-// Block (tile, split): the tile's products over the split's reduction blocks.
+// A CTA takes every so manieth unit (tile, cut): the tile's products over the
+// cut's reduction blocks.
 __global__ void __launch_bounds__(kShrinkThreads)
-    shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
-                  const ShrinkParams p) {
+    shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_rows,
+                  const __grid_constant__ CUtensorMap map_a, const ShrinkParams p) {
   extern __shared__ uint8_t smem_raw[];
   let_next_launch();
   const PlanHead head = *p.head;
   if (head.n != p.n || head.slots != p.slots) {  // another batch's plan
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report(p.status, MOE_ERR_DEVICE);
+    if (blockIdx.x == 0 && threadIdx.x == 0) report(p.status, MOE_ERR_DEVICE);
     return;
   }
-  if (static_cast<int>(blockIdx.x) >= head.tiles) return;
-  const PlanTile tile = p.tiles[blockIdx.x];
-  if (tile.adapter < 0) return;
+  const int cuts = cuts_of(head.tiles, gridDim.x, p.kblocks), units = head.tiles * cuts;
+  if (static_cast<int>(blockIdx.x) >= units) return;
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int stage_bytes = kTokenStage + p.width * kBlockK * 2;
   ShrinkCtl& s = *reinterpret_cast<ShrinkCtl*>(ring + p.stages * stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * blockIdx.y / p.splits);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (blockIdx.y + 1) / p.splits);
   const int cols = tmem_width(p.width);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -202,9 +216,11 @@ __global__ void __launch_bounds__(kShrinkThreads)
       mbar_init(&s.empty[i], 1);
     }
     mbar_init(&s.done, 1);
+    mbar_init(&s.drained, 4);
     s.abort_flag = 0;
     mbar_fence_init();
     tma_prefetch_map(&map_x);
+    tma_prefetch_map(&map_rows);
     tma_prefetch_map(&map_a);
   }
   if (warp == 1) {
@@ -216,31 +232,41 @@ __global__ void __launch_bounds__(kShrinkThreads)
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
+  const auto first_block = [&](int cut) { return static_cast<int>(static_cast<int64_t>(p.kblocks) * cut / cuts); };
 
   if (warp == 0) {
-    // lane i gathers tokens 4i .. 4i + 3 of the tile (past the last: the last
-    // again; their rows of the product are not stored)
-    const int groups = (tile.count + 3) / 4;
-    int row[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) row[i] = __ldg(p.order + tile.start + min(4 * lane + i, tile.count - 1));
     int stage = 0, filled = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      ok = warp_wait(&s.empty[stage], phase ^ 1u, wc);
-      if (!ok) break;
-      uint8_t* at = ring + stage * stage_bytes;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&s.full[stage], groups * 512 + p.width * kBlockK * 2);
-        tma_load_3d(at + kTokenStage, &map_a, &s.full[stage], kb * kBlockK, 0, tile.adapter);
-      }
-      __syncwarp();  // armed before any gather lands
-      if (lane < groups) gather4(at + 512 * lane, &map_x, &s.full[stage], kb * kBlockK, row);
-      ++filled;
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1u;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const PlanTile tile = p.tiles[u / cuts];
+      const int kb1 = first_block(u % cuts + 1);
+      // Tokens that follow one another come as one box of 128 rows.  Others
+      // are gathered, lane i the tile's tokens 4i .. 4i + 3 (past the last: the
+      // last again).  Rows of the product past the tile's are not stored.
+      const int t0 = __ldg(p.order + tile.start), t1 = __ldg(p.order + tile.start + tile.count - 1);
+      const bool run = t1 - t0 == tile.count - 1;
+      const int groups = run ? 0 : (tile.count + 3) / 4;
+      int row[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) row[i] = run ? 0 : __ldg(p.order + tile.start + min(4 * lane + i, tile.count - 1));
+      const int bytes = (run ? kTokenStage : groups * 512) + p.width * kBlockK * 2;
+      for (int kb = first_block(u % cuts); kb < kb1; ++kb) {
+        ok = warp_wait(&s.empty[stage], phase ^ 1u, wc);
+        if (!ok) break;
+        uint8_t* at = ring + stage * stage_bytes;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&s.full[stage], bytes);
+          if (run) tma_load_2d(at, &map_rows, &s.full[stage], kb * kBlockK, t0);
+          tma_load_3d(at + kTokenStage, &map_a, &s.full[stage], kb * kBlockK, 0, tile.adapter);
+        }
+        __syncwarp();  // armed before any gather lands
+        if (lane < groups) gather4(at + 512 * lane, &map_x, &s.full[stage], kb * kBlockK, row);
+        ++filled;
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
     if (!ok && lane == 0) {  // copies in flight land before the CTA goes on
@@ -254,34 +280,41 @@ __global__ void __launch_bounds__(kShrinkThreads)
       const uint32_t idesc = dense_idesc(kTile, p.width, false, false, p.type);
       const uint32_t base = smem_u32(ring);
       const Operand op = operand128<false>();
-      int stage = 0, done = 0;
+      int stage = 0, done = 0, unit = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        ok = mbar_wait(&s.full[stage], phase, wc);
-        if (!ok) break;
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++unit) {
+        if (unit > 0) ok = mbar_wait(&s.drained, (unit - 1) & 1, wc);
         tc_fence_after();
-        const uint32_t at = base + stage * stage_bytes;
-        issue_block<1>(tmem, at, at + kTokenStage, op, op, idesc, kb > kb0 ? 1u : 0u);
-        umma_commit<1>(&s.empty[stage]);
-        ++done;
-        if (++stage == p.stages) {
-          stage = 0;
-          phase ^= 1u;
+        const int kb0 = first_block(u % cuts), kb1 = first_block(u % cuts + 1);
+        for (int kb = kb0; kb < kb1 && ok; ++kb) {
+          ok = mbar_wait(&s.full[stage], phase, wc);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = base + stage * stage_bytes;
+          issue_block<1>(tmem, at, at + kTokenStage, op, op, idesc, kb > kb0 ? 1u : 0u);
+          umma_commit<1>(&s.empty[stage]);
+          ++done;
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
+        if (ok) umma_commit<1>(&s.done);
       }
-      if (ok) {
-        umma_commit<1>(&s.done);
-      } else if (done > 0) {  // issued products end before TMEM is freed
+      if (!ok && done > 0) {  // issued products end before TMEM is freed
         const int last = (done - 1) % p.stages;
         (void)mbar_wait_drain(&s.empty[last], ((done - last + p.stages - 1) / p.stages - 1) & 1, 100000000ull);
       }
     }
   } else {
     const int q = warp & 3, i = q * 32 + lane;  // this thread's token of the tile
-    if (warp_wait(&s.done, 0, wc)) {
+    int unit = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, ++unit) {
+      const PlanTile tile = p.tiles[u / cuts];
+      if (!warp_wait(&s.done, unit & 1, wc)) break;
       tc_fence_after();
-      float* to = p.v + (static_cast<int64_t>(blockIdx.y) * p.n + tile.start + i) * p.rank;
+      float* to = p.v + (static_cast<int64_t>(u % cuts) * head.live + tile.start + i) * p.rank;
       for (int c0 = 0; c0 < p.width; c0 += 16) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0, v);
@@ -294,6 +327,9 @@ __global__ void __launch_bounds__(kShrinkThreads)
                                                                     __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.drained);
     }
   }
   tc_fence_before();
@@ -305,8 +341,9 @@ __global__ void __launch_bounds__(kShrinkThreads)
 }
 
 // ------------------------------------------------------------------ expand
-constexpr int kExpandWarps = 4;
-constexpr int kExpandTokens = 32;  // of a block: two MMAs of 16
+constexpr int kExpandThreads = 256;
+constexpr int kExpandCols = 32 * kExpandThreads / 32;  // of a block: 32 to a warp
+constexpr int kSteps = kTile / 16;                     // MMAs' worth of tokens of a tile
 struct ExpandParams {
   const PlanHead* head;
   const PlanTile* tiles;
@@ -316,8 +353,14 @@ struct ExpandParams {
   const float* scale;
   void* y;
   int64_t ldres, ldy;
-  int n, slots, N, rank, splits, groups;  // groups: of 32 columns, to a warp
+  int n, slots, N, rank, kblocks, shrink_grid;
 };
+// Words of a row of v in shared memory: 8 more than whole 32s, so that the
+// eight rows of a fragment lie in different banks.
+__host__ __device__ constexpr int v_words(int kb) { return 8 * kb + (40 - 8 * kb % 32) % 32; }
+__host__ __device__ constexpr size_t expand_smem(int kb) {
+  return static_cast<size_t>(2 * kSteps) * kExpandThreads * 16 + static_cast<size_t>(kTile) * v_words(kb) * 4;
+}
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -333,117 +376,142 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Block (tile, columns, quarter of the tile): 32 tokens by 4 * groups * 32
-// columns, a warp a quarter of these.  In a fragment, lane 4 g + q holds
-// reduction elements 4 q .. 4 q + 3 of each 16 (in both operands), and of a
-// group of 32 columns the columns 8 q .. 8 q + 7 of rows g and g + 8: column c
-// of the j-th of its four MMAs is column 8 (c / 2) + 2 j + c % 2 of the group.
+// Block (tile, 256 columns), a warp 32 of these: it keeps its columns of b in
+// registers and walks down the tile's tokens, 16 at a time.  All of its part of
+// res is asked for at once, ahead of everything else, into the threads' own
+// slots of shared memory (64 KB; with two blocks to an SM that keeps 128 KB
+// under way); v is summed over the cuts, scaled and rounded into shared memory
+// by the whole block.  In a fragment, lane 4 g + q holds reduction elements
+// 4 q .. 4 q + 3 of each 16 (in both operands), and the columns 8 q .. 8 q + 7 of
+// rows g and g + 8: column c of the j-th of its four MMAs is column
+// 8 (c / 2) + 2 j + c % 2 of the warp's.
 template <typename T, int KB>
-__global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const ExpandParams p) {
-  // the plan is older than the call: no need to wait for that
+__global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint4* const slots = reinterpret_cast<uint4*>(smem) + threadIdx.x;
+  uint32_t* const vs = reinterpret_cast<uint32_t*>(smem + static_cast<size_t>(2 * kSteps) * kExpandThreads * 16);
+  constexpr int kWords = v_words(KB);
+  // the plan and res are older than the call: no need to wait for those
   const PlanHead head = *p.head;
-  if (head.n != p.n || head.slots != p.slots || static_cast<int>(blockIdx.x) >= head.tiles) {
+  if (head.n != p.n || head.slots != p.slots || static_cast<int>(blockIdx.x) >= head.tiles + head.none) {
     wait_for_previous();
     return;
   }
   const PlanTile tile = p.tiles[blockIdx.x];
-  const int t0 = blockIdx.z * kExpandTokens;
-  if (t0 >= tile.count) {
-    wait_for_previous();
-    return;
-  }
+  const bool named = static_cast<int>(blockIdx.x) < head.tiles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int m_tiles = tile.count - t0 > 16 ? 2 : 1;
-  const int first = (blockIdx.y * kExpandWarps + warp) * p.groups * 32;  // column
-  // rows g and g + 8 of either 16 tokens
-  int row[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = t0 + 8 * i + g;
-    row[i] = at < tile.count ? __ldg(p.order + tile.start + at) : -1;
+  const int c0 = blockIdx.y * kExpandCols + warp * 32, col = c0 + 8 * q;  // of this lane's eight results
+  const int steps = (tile.count + 15) / 16;
+  const bool in = col < p.N;
+  const int32_t* const order = p.order + tile.start;
+  if (p.res != nullptr && in) {
+    for (int i = 0; i < 2 * steps; ++i) {
+      const int at = 8 * i + g;
+      if (at < tile.count)
+        cp_async16(slots + i * kExpandThreads, static_cast<const T*>(p.res) + __ldg(order + at) * p.ldres + col);
+    }
   }
-  uint32_t a[2][KB][4];
-  wait_for_previous();
-  if (tile.adapter >= 0) {
-    const float scale = __ldg(p.scale + tile.adapter);
+  cp_async_commit();
+  uint32_t b[4][KB][2];
+  if (named) {
+    const T* pool = static_cast<const T*>(p.b) + static_cast<int64_t>(tile.adapter) * p.N * p.rank;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float* at = p.v + static_cast<int64_t>(tile.start + t0 + 8 * i + g) * p.rank + 4 * q;
+    for (int j = 0; j < 4; ++j) {
+      const int bc = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
-        float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (row[i] >= 0 && 16 * k + 4 * q < p.rank) {
-          for (int sp = 0; sp < p.splits; ++sp) {
-            const float4 d = *reinterpret_cast<const float4*>(at + static_cast<int64_t>(sp) * p.n * p.rank + 16 * k);
-            f.x += d.x, f.y += d.y, f.z += d.z, f.w += d.w;
-          }
-        }
-        a[i / 2][k][i % 2] = pack_pair(scale * f.x, scale * f.y, T{});
-        a[i / 2][k][2 + i % 2] = pack_pair(scale * f.z, scale * f.w, T{});
+        uint2 w = make_uint2(0u, 0u);
+        if (bc < p.N && 16 * k + 4 * q < p.rank)
+          w = __ldg(reinterpret_cast<const uint2*>(pool + static_cast<int64_t>(bc) * p.rank + 16 * k + 4 * q));
+        b[j][k][0] = w.x;
+        b[j][k][1] = w.y;
       }
     }
   }
-  const T* b = static_cast<const T*>(p.b) + static_cast<int64_t>(max(tile.adapter, 0)) * p.N * p.rank;
-  for (int grp = 0; grp < p.groups; ++grp) {
-    const int c0 = first + grp * 32;
-    if (c0 >= p.N) break;
-    const int col = c0 + 8 * q;  // of this lane's eight results
-    uint4 r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (p.res != nullptr && row[i] >= 0 && col < p.N)
-        r[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.res) + row[i] * p.ldres + col);
-    }
-    float acc[2][4][4];
-    if (tile.adapter >= 0) {
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int bc = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
-        const T* at = b + static_cast<int64_t>(bc) * p.rank + 4 * q;
-#pragma unroll
-        for (int k = 0; k < KB; ++k) {
-          uint2 w = make_uint2(0u, 0u);
-          if (bc < p.N && 16 * k + 4 * q < p.rank) w = __ldg(reinterpret_cast<const uint2*>(at + 16 * k));
-          mma16816<T>(acc[0][j], a[0][k], w.x, w.y);
-          if (m_tiles > 1) mma16816<T>(acc[1][j], a[1][k], w.x, w.y);
+  wait_for_previous();
+  if (named) {
+    const float scale = __ldg(p.scale + tile.adapter);
+    const int cuts = cuts_of(head.tiles, p.shrink_grid, p.kblocks);
+    const int64_t cut = static_cast<int64_t>(head.live) * p.rank;
+    constexpr int kQuads = 4 * KB;  // of a row
+    for (int i = threadIdx.x; i < tile.count * kQuads; i += kExpandThreads) {
+      const int row = i / kQuads, e = i % kQuads * 4;
+      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (e < p.rank) {  // past the rank: zeros
+        const float* at = p.v + static_cast<int64_t>(tile.start + row) * p.rank + e;
+        for (int c = 0; c < cuts; ++c) {
+          const float4 d = *reinterpret_cast<const float4*>(at + c * cut);
+          f.x += d.x, f.y += d.y, f.z += d.z, f.w += d.w;
         }
       }
+      *reinterpret_cast<uint2*>(vs + row * kWords + e / 2) =
+          make_uint2(pack_pair(scale * f.x, scale * f.y, T{}), pack_pair(scale * f.z, scale * f.w, T{}));
     }
+    __syncthreads();
+  }
+  cp_async_wait_all();
+  if (!in && !named) return;
+  for (int s = 0; s < steps; ++s) {
+    float acc[4][4];
+    uint4 r[2];
+    int row[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (row[i] < 0 || col >= p.N) continue;
-      uint4 out = r[i];
-      if (tile.adapter >= 0) {
+    for (int i = 0; i < 2; ++i) {
+      const int at = 16 * s + 8 * i + g;
+      row[i] = at < tile.count ? __ldg(order + at) : -1;
+      r[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.res != nullptr && in && row[i] >= 0) r[i] = slots[(2 * s + i) * kExpandThreads];
+    }
+    if (named) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // the products are added to res
         Raw<T, 8> raw;
         raw.v = r[i];
         float f[8];
         raw.unpack(f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          f[2 * j] += acc[i / 2][j][2 * (i % 2)];
-          f[2 * j + 1] += acc[i / 2][j][2 * (i % 2) + 1];
+          acc[j][2 * i] = f[2 * j];
+          acc[j][2 * i + 1] = f[2 * j + 1];
+        }
+      }
+      // (rows past the tile's last hold anything: their results are dropped)
+      const uint32_t* at = vs + (16 * s + g) * kWords + 2 * q;
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+        const uint2 lo = *reinterpret_cast<const uint2*>(at + 8 * k);
+        const uint2 hi = *reinterpret_cast<const uint2*>(at + 8 * kWords + 8 * k);
+        const uint32_t a[4] = {lo.x, hi.x, lo.y, hi.y};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma16816<T>(acc[j], a, b[j][k][0], b[j][k][1]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (row[i] < 0 || !in) continue;
+      Raw<T, 8> raw;
+      raw.v = r[i];
+      if (named) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[2 * j] = acc[j][2 * i];
+          f[2 * j + 1] = acc[j][2 * i + 1];
         }
         raw.pack(f);
-        out = raw.v;
       }
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.y) + row[i] * p.ldy + col) = out;
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.y) + row[i] * p.ldy + col) = raw.v;
     }
   }
 }
 
 // --------------------------------------------------------------- host side
-bool map_gather(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld) {
+// Rows of x in boxes of 64 elements of `rows_per_box` rows (one: for gathers).
+bool map_tokens(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld, uint32_t rows_per_box) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {inner, rows}, strides[1] = {ld * 2};
-  const cuuint32_t box[2] = {64, 1}, es[2] = {1, 1};
+  const cuuint32_t box[2] = {64, rows_per_box}, es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -460,31 +528,7 @@ bool map_pool(CUtensorMap* m, const void* base, uint64_t K, uint64_t rank, uint6
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kMostSms = 192;       // any device of this kind has fewer
-constexpr int kLeastSplitBlocks = 4;
-
-// Cuts of the reduction: CTAs for two to an SM, by the tiles that n tokens
-// probably make, and four blocks to a CTA at least.
-int shrink_splits(int64_t n, int slots, int kblocks, int sms) {
-  const int64_t tiles = std::max<int64_t>((n + kTile - 1) / kTile, std::min<int64_t>(n, slots));
-  const int64_t want = 2 * static_cast<int64_t>(sms) / tiles;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, kblocks / kLeastSplitBlocks)));
-}
-
-template <typename T>
-cudaError_t launch_expand(const ExpandParams& p, dim3 grid, int kb, cudaStream_t s) {
-  cudaLaunchAttribute overlap = overlap_attribute();
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(32 * kExpandWarps);
-  cfg.stream = s;
-  cfg.attrs = &overlap;
-  cfg.numAttrs = 1;
-  if (kb <= 1) return cudaLaunchKernelEx(&cfg, expand_kernel<T, 1>, p);
-  if (kb <= 2) return cudaLaunchKernelEx(&cfg, expand_kernel<T, 2>, p);
-  if (kb <= 4) return cudaLaunchKernelEx(&cfg, expand_kernel<T, 4>, p);
-  return cudaLaunchKernelEx(&cfg, expand_kernel<T, 8>, p);
-}
+constexpr int kMostSms = 192;  // any device of this kind has fewer
 
 cudaError_t allow_smem(const void* kern, std::atomic<bool> (&set)[64], int bytes) {
   int dev = 0;
@@ -497,13 +541,37 @@ cudaError_t allow_smem(const void* kern, std::atomic<bool> (&set)[64], int bytes
   return err;
 }
 
+template <typename T, int KB>
+cudaError_t launch_expand(const ExpandParams& p, dim3 grid, cudaStream_t s) {
+  static std::atomic<bool> set[64];
+  constexpr size_t bytes = expand_smem(KB);
+  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(expand_kernel<T, KB>), set, static_cast<int>(bytes));
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute overlap = overlap_attribute();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kExpandThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, expand_kernel<T, KB>, p);
+}
+template <typename T>
+cudaError_t launch_expand(const ExpandParams& p, dim3 grid, int kb, cudaStream_t s) {
+  if (kb <= 1) return launch_expand<T, 1>(p, grid, s);
+  if (kb <= 2) return launch_expand<T, 2>(p, grid, s);
+  if (kb <= 4) return launch_expand<T, 4>(p, grid, s);
+  return launch_expand<T, 8>(p, grid, s);
+}
+
 }  // namespace
 
 size_t adapter_plan_bytes(int64_t T, int slots) {
   return plan_order_at(T, slots) + (static_cast<size_t>(T) * 4 + 255) / 256 * 256;
 }
 size_t adapter_ws_bytes(const moe_adapter_dims& d) {
-  // splits * n rows: splits is 1, or at most 2 SMs' worth over the tiles
+  // cuts * live tokens: one cut, or as many as make the tiles of 128 tokens fill the grid
   return (static_cast<size_t>(d.T) + 2 * static_cast<size_t>(kMostSms) * kTile) * d.rank * sizeof(float);
 }
 
@@ -522,23 +590,17 @@ cudaError_t launch_adapter_plan(const int32_t* ids, int32_t n, int32_t T, int32_
 cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   const moe_adapter_dims& d = c.d;
   const uint8_t* at = static_cast<const uint8_t*>(c.plan);
-  const auto* head = reinterpret_cast<const PlanHead*>(at);
-  const auto* tiles = reinterpret_cast<const PlanTile*>(at + sizeof(PlanHead));
-  const auto* order = reinterpret_cast<const int32_t*>(at + plan_order_at(d.T, d.slots));
-  const int sms = std::min(sm_count(), kMostSms);
-  const unsigned most = static_cast<unsigned>(most_tiles(c.n, d.slots));
-
+  const int64_t most = most_tiles(c.n, d.slots);
   ShrinkParams p{};
-  p.head = head;
-  p.tiles = tiles;
-  p.order = order;
+  p.head = reinterpret_cast<const PlanHead*>(at);
+  p.tiles = reinterpret_cast<const PlanTile*>(at + sizeof(PlanHead));
+  p.order = reinterpret_cast<const int32_t*>(at + plan_order_at(d.T, d.slots));
   p.v = static_cast<float*>(c.ws);
   p.n = c.n;
   p.slots = d.slots;
   p.rank = d.rank;
   p.width = (d.rank + 15) / 16 * 16;
   p.kblocks = (d.K + kBlockK - 1) / kBlockK;
-  p.splits = shrink_splits(c.n, d.slots, p.kblocks, sms);
   p.type = d.type == MOE_BF16 ? 1u : 0u;
   p.status = c.dev_status;
   p.limit_ns = kDefaultWaitLimitNs;
@@ -547,19 +609,23 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   p.stages = static_cast<int>(std::min<size_t>(kMaxStages, (110 * 1024 - 1024 - sizeof(ShrinkCtl)) / stage));
   const size_t bytes = 1024 + p.stages * stage + sizeof(ShrinkCtl);
   static std::atomic<bool> set[64];
-  cudaError_t err = allow_smem(reinterpret_cast<const void*>(shrink_kernel), set, 110 * 1024);
+  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(shrink_kernel), set, 110 * 1024);
   if (err != cudaSuccess) return err;
-  CUtensorMap mx, ma;
-  if (!map_gather(&mx, c.x, d.K, c.n, c.ldx) || !map_pool(&ma, c.a, d.K, d.rank, d.slots, p.width))
+  CUtensorMap mx, mr, ma;
+  if (!map_tokens(&mx, c.x, d.K, c.n, c.ldx, 1) || !map_tokens(&mr, c.x, d.K, c.n, c.ldx, kTile) ||
+      !map_pool(&ma, c.a, d.K, d.rank, d.slots, p.width))
     return cudaErrorInvalidValue;
-  shrink_kernel<<<dim3(most, p.splits), kShrinkThreads, bytes, s>>>(mx, ma, p);
-  err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
+  // no more CTAs than units of the fewest blocks
+  const int grid = static_cast<int>(std::min<int64_t>(
+      2 * std::min(sm_count(), kMostSms), most * std::max(1, p.kblocks / kLeastCutBlocks)));
+  shrink_kernel<<<grid, kShrinkThreads, bytes, s>>>(mx, mr, ma, p);
+  const cudaError_t launched = cudaGetLastError();
+  if (launched != cudaSuccess) return launched;
 
   ExpandParams e{};
-  e.head = head;
-  e.tiles = tiles;
-  e.order = order;
+  e.head = p.head;
+  e.tiles = p.tiles;
+  e.order = p.order;
   e.v = p.v;
   e.b = c.b;
   e.res = c.res;
@@ -571,15 +637,11 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   e.slots = d.slots;
   e.N = d.N;
   e.rank = d.rank;
-  e.splits = p.splits;
-  // four groups of 32 columns to a warp where that leaves blocks for all SMs
-  const int64_t blocks = (static_cast<int64_t>(c.n) / kExpandTokens + std::min(c.n, d.slots)) * (d.N / 512);
-  e.groups = blocks >= 4 * sms ? 4 : 1;
-  const unsigned across = static_cast<unsigned>((d.N + 128 * e.groups - 1) / (128 * e.groups));
-  const unsigned down = static_cast<unsigned>((std::min(c.n, kTile) + kExpandTokens - 1) / kExpandTokens);
-  const dim3 grid(most, across, down);
+  e.kblocks = p.kblocks;
+  e.shrink_grid = grid;
+  const dim3 blocks(static_cast<unsigned>(most), static_cast<unsigned>((d.N + kExpandCols - 1) / kExpandCols));
   const int kb = p.width / 16;
-  return d.type == MOE_BF16 ? launch_expand<__nv_bfloat16>(e, grid, kb, s) : launch_expand<__half>(e, grid, kb, s);
+  return d.type == MOE_BF16 ? launch_expand<__nv_bfloat16>(e, blocks, kb, s) : launch_expand<__half>(e, blocks, kb, s);
 }
 
 }  // namespace moe

@@ -57,18 +57,18 @@ def test_the_plan(T, slots):
         batch.group(ids.int().cuda())
         torch.cuda.synchronize()
         plan = batch.plan.cpu()
-        head = plan[:16].view(torch.int32).tolist()
+        head = plan[:32].view(torch.int32).tolist()
         most = T // 128 + min(slots + 1, T)
-        tiles = plan[16:16 + 16 * most].view(torch.int32).view(-1, 4)[:head[2]].tolist()
-        order = plan[16 + 16 * most:].view(torch.int32)[:n].long()
+        tiles = plan[32:32 + 16 * most].view(torch.int32).view(-1, 4)[:head[2] + head[3]].tolist()
+        order = plan[32 + 16 * most:].view(torch.int32)[:n].long()
         key = torch.where(ids < 0, slots, ids)
-        assert head[:2] == [n, slots]
+        assert head[:2] == [n, slots] and head[4] == int((ids >= 0).sum())
         assert torch.equal(order, torch.argsort(key, stable=True))
         want = []
         at = 0
         for s in range(slots + 1):
             c = int((key == s).sum())
-            want += [[s if s < slots else -1, at + i, min(128, c - i)] for i in range(0, c, 128)]
+            want += [[s, at + i, min(128, c - i)] for i in range(0, c, 128)]
             at += c
         assert [t[:3] for t in tiles] == want
     assert int(batch.status.item()) == 0
