@@ -790,8 +790,11 @@ moe_status moe_adapter_plan(const int32_t* ids, int32_t n, int32_t T, int32_t sl
  *   (4-byte aligned, as ids)
  * K, N and rank multiples of 8, rank <= 128.  plan: of d.T, d.slots and the
  * call's n tokens; one of another number of tokens or slots is reported as
- * MOE_ERR_DEVICE, and y is left as it was.  ws: moe_adapters_workspace_bytes(d) bytes.
- * Results are reproducible bit for bit.
+ * MOE_ERR_DEVICE, and y is left as it was.
+ * ws: moe_adapters_workspace_bytes(d) bytes that are ZERO before the first
+ * call; every call leaves the counters in them zero for the next, except one
+ * that reports MOE_ERR_TIMEOUT (clear ws then).  Calls that share a ws must be
+ * ordered on one stream.  Results are reproducible bit for bit.
  */
 typedef struct {
   int32_t T, K, N, slots, rank;

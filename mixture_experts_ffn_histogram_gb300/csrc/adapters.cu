@@ -20,9 +20,10 @@
 // Columns and reduction indices are permuted among the fragments so that every
 // access is 8 or 16 contiguous bytes.
 //
-// v is summed in fp32 (over the cuts in their order) and rounded once to the
-// operands' type for the second product, with the scale: half a step on each of
-// r terms, below the result's own rounding.
+// v is summed in fp32 (over the cuts in a fixed order, by the CTA that stores a
+// tile's last part) and rounded once, with the scale, to the operands' type for
+// the second product: half a step on each of r terms, below the result's own
+// rounding.
 #include <cuda.h>
 
 #include <algorithm>
@@ -163,7 +164,11 @@ struct ShrinkParams {
   const PlanHead* head;
   const PlanTile* tiles;
   const int32_t* order;
-  float* v;  // [cuts][live tokens][r], by place in the order
+  void* v;           // 16-bit [live tokens][width], by place in the order: scaled
+  float* parts;      // [cuts][live tokens][width], where there is more than one cut
+  int32_t* arrived;  // [tile]: cuts whose part is stored; zero between calls
+  const float* scale;
+  bool join;         // here, not in a kernel of its own
   int n, slots, rank, width, kblocks, stages;  // width: rank in whole 16s
   uint32_t type;
   int32_t* status;
@@ -174,8 +179,10 @@ struct ShrinkCtl {
   uint64_t empty[kMaxStages];
   uint64_t done;     // a unit's products
   uint64_t drained;  // ... have been read
+  float4 sums[128];
   uint32_t tmem_base;
   int abort_flag;
+  int last;
 };
 __host__ __device__ constexpr int tmem_width(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : 128; }
 
@@ -191,8 +198,120 @@ __device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, uint6
       : "memory");
 }
 
-// A CTA takes every so manieth unit (tile, cut): the tile's products over the
-// cut's reduction blocks.
+// The reduction blocks of unit u, in the order in which they are read: every
+// so manieth, from another one on for each unit.
+struct Blocks {
+  int kb, count, first, step, kblocks;
+  __device__ __forceinline__ Blocks(int u, int cuts, int kblocks) : first(u % cuts), step(cuts), kblocks(kblocks) {
+    count = (kblocks - first + cuts - 1) / cuts;
+    kb = first + u % count * cuts;
+  }
+  __device__ __forceinline__ void next() {
+    kb += step;
+    if (kb >= kblocks) kb = first;
+  }
+};
+
+// Barriers of the four epilogue warps; the second tells whether all had `ok`.
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool epi_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// v of a tile from its parts.  Few tokens: by the 128 epilogue threads of the
+// CTA that stored the last part, four neighbouring ranks of a token to a thread;
+// where there are fewer of those than threads, 2^k threads take the cuts in
+// turns and their sums are added in the threads' order.  (61 tokens: 1.2 us,
+// about a launch.)  Many tokens: by a kernel of its own, as wide as there are
+// values, since the last CTAs' 128 threads took 14 us of 73 for 8191 tokens.
+template <typename T>
+__device__ __forceinline__ void join_parts(const ShrinkParams& p, const PlanTile& tile, int live, int cuts, int tid,
+                                           float4* sums) {
+  const int per_row = p.width / 4, quads = tile.count * per_row;
+  int share = 1;
+  while (share < 32 && quads * share * 2 <= 128 && share * 2 <= cuts) share *= 2;
+  const float scale = __ldg(p.scale + tile.adapter);
+  const int64_t cut = static_cast<int64_t>(live) * p.width;
+  const float* parts = p.parts + static_cast<int64_t>(tile.start) * p.width;
+  const auto add = [](float4& f, const float4& d) { f.x += d.x, f.y += d.y, f.z += d.z, f.w += d.w; };
+  const auto store = [&](int i, const float4& f) {
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.v) + static_cast<int64_t>(tile.start) * p.width + 4 * i) =
+        make_uint2(pack_pair(scale * f.x, scale * f.y, T{}), pack_pair(scale * f.z, scale * f.w, T{}));
+  };
+  if (share > 1) {
+    const int sub = tid % share, i = tid / share;
+    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i < quads) {
+#pragma unroll 4
+      for (int c = sub; c < cuts; c += share) add(f, __ldcg(reinterpret_cast<const float4*>(parts + 4 * i + c * cut)));
+    }
+    sums[tid] = f;
+    epi_sync();
+    if (i < quads && sub == 0) {
+      for (int k = 1; k < share; ++k) add(f, sums[tid + k]);
+      store(i, f);
+    }
+    return;
+  }
+  for (int i = tid; i < quads; i += 128) {
+    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int c = 0; c < cuts; ++c) add(f, __ldcg(reinterpret_cast<const float4*>(parts + 4 * i + c * cut)));
+    store(i, f);
+  }
+}
+
+struct JoinParams {
+  const PlanHead* head;
+  const PlanTile* tiles;
+  const float *parts, *scale;
+  void* v;
+  int n, slots, width, kblocks, shrink_grid;
+};
+constexpr int kJoinThreads = 256;
+// A block takes a tile at a time.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) {
+  let_next_launch();
+  const PlanHead head = *p.head;
+  const int cuts = cuts_of(head.tiles, p.shrink_grid, p.kblocks);
+  wait_for_previous();
+  if (head.n != p.n || head.slots != p.slots || cuts == 1) return;
+  const int per_row = p.width / 4;
+  const int64_t cut = static_cast<int64_t>(head.live) * per_row;
+  const float4* parts = reinterpret_cast<const float4*>(p.parts);
+  // a slice of a tile's values to a block
+  constexpr int kSlices = 4;
+  for (int u = blockIdx.x; u < head.tiles * kSlices; u += gridDim.x) {
+    const PlanTile tile = p.tiles[u / kSlices];
+    const float scale = __ldg(p.scale + tile.adapter);
+    const int64_t first = static_cast<int64_t>(tile.start) * per_row;
+    for (int i = u % kSlices * kJoinThreads + threadIdx.x; i < tile.count * per_row; i += kSlices * kJoinThreads) {
+      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int c = 0; c < cuts; ++c) {
+        const float4 d = __ldcg(parts + first + i + c * cut);
+        f.x += d.x, f.y += d.y, f.z += d.z, f.w += d.w;
+      }
+      reinterpret_cast<uint2*>(p.v)[first + i] =
+          make_uint2(pack_pair(scale * f.x, scale * f.y, T{}), pack_pair(scale * f.z, scale * f.w, T{}));
+    }
+  }
+}
+
+// A CTA takes every so manieth unit (tile, cut): the tile's products over every
+// so manieth reduction block, so that a tile's CTAs read neighbouring pieces of
+// its rows at the same time.
+template <typename T>
 __global__ void __launch_bounds__(kShrinkThreads)
     shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_rows,
                   const __grid_constant__ CUtensorMap map_a, const ShrinkParams p) {
@@ -232,7 +351,6 @@ __global__ void __launch_bounds__(kShrinkThreads)
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   const WaitCtl wc{&s.abort_flag, p.status, p.limit_ns};
-  const auto first_block = [&](int cut) { return static_cast<int>(static_cast<int64_t>(p.kblocks) * cut / cuts); };
 
   if (warp == 0) {
     int stage = 0, filled = 0;
@@ -240,7 +358,6 @@ __global__ void __launch_bounds__(kShrinkThreads)
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const PlanTile tile = p.tiles[u / cuts];
-      const int kb1 = first_block(u % cuts + 1);
       // Tokens that follow one another come as one box of 128 rows.  Others
       // are gathered, lane i the tile's tokens 4i .. 4i + 3 (past the last: the
       // last again).  Rows of the product past the tile's are not stored.
@@ -251,17 +368,19 @@ __global__ void __launch_bounds__(kShrinkThreads)
 #pragma unroll
       for (int i = 0; i < 4; ++i) row[i] = run ? 0 : __ldg(p.order + tile.start + min(4 * lane + i, tile.count - 1));
       const int bytes = (run ? kTokenStage : groups * 512) + p.width * kBlockK * 2;
-      for (int kb = first_block(u % cuts); kb < kb1; ++kb) {
+      Blocks at(u, cuts, p.kblocks);
+      for (int i = 0; i < at.count; ++i, at.next()) {
+        const int kb = at.kb;
         ok = warp_wait(&s.empty[stage], phase ^ 1u, wc);
         if (!ok) break;
-        uint8_t* at = ring + stage * stage_bytes;
+        uint8_t* to = ring + stage * stage_bytes;
         if (lane == 0) {
           mbar_arrive_expect_tx(&s.full[stage], bytes);
-          if (run) tma_load_2d(at, &map_rows, &s.full[stage], kb * kBlockK, t0);
-          tma_load_3d(at + kTokenStage, &map_a, &s.full[stage], kb * kBlockK, 0, tile.adapter);
+          if (run) tma_load_2d(to, &map_rows, &s.full[stage], kb * kBlockK, t0);
+          tma_load_3d(to + kTokenStage, &map_a, &s.full[stage], kb * kBlockK, 0, tile.adapter);
         }
         __syncwarp();  // armed before any gather lands
-        if (lane < groups) gather4(at + 512 * lane, &map_x, &s.full[stage], kb * kBlockK, row);
+        if (lane < groups) gather4(to + 512 * lane, &map_x, &s.full[stage], kb * kBlockK, row);
         ++filled;
         if (++stage == p.stages) {
           stage = 0;
@@ -286,13 +405,13 @@ __global__ void __launch_bounds__(kShrinkThreads)
       for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++unit) {
         if (unit > 0) ok = mbar_wait(&s.drained, (unit - 1) & 1, wc);
         tc_fence_after();
-        const int kb0 = first_block(u % cuts), kb1 = first_block(u % cuts + 1);
-        for (int kb = kb0; kb < kb1 && ok; ++kb) {
+        const int count = Blocks(u, cuts, p.kblocks).count;
+        for (int i = 0; i < count && ok; ++i) {
           ok = mbar_wait(&s.full[stage], phase, wc);
           if (!ok) break;
           tc_fence_after();
           const uint32_t at = base + stage * stage_bytes;
-          issue_block<1>(tmem, at, at + kTokenStage, op, op, idesc, kb > kb0 ? 1u : 0u);
+          issue_block<1>(tmem, at, at + kTokenStage, op, op, idesc, i > 0 ? 1u : 0u);
           umma_commit<1>(&s.empty[stage]);
           ++done;
           if (++stage == p.stages) {
@@ -308,28 +427,54 @@ __global__ void __launch_bounds__(kShrinkThreads)
       }
     }
   } else {
-    const int q = warp & 3, i = q * 32 + lane;  // this thread's token of the tile
+    const int q = warp & 3, tid = q * 32 + lane;  // also this thread's token of the tile
     int unit = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++unit) {
       const PlanTile tile = p.tiles[u / cuts];
-      if (!warp_wait(&s.done, unit & 1, wc)) break;
+      // the four warps meet at barriers below: all go on or none does
+      if (!epi_all(warp_wait(&s.done, unit & 1, wc))) break;
       tc_fence_after();
-      float* to = p.v + (static_cast<int64_t>(u % cuts) * head.live + tile.start + i) * p.rank;
-      for (int c0 = 0; c0 < p.width; c0 += 16) {
+      const int64_t at = static_cast<int64_t>(tile.start + tid) * p.width;
+      const float scale = __ldg(p.scale + tile.adapter);
+      for (int c0 = 0; c0 < p.width; c0 += 16) {  // ranks past the last are zero, like their rows of a
         uint32_t v[16];
         tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0, v);
         tmem_ld_wait();
-        if (i < tile.count) {
+        if (tid < tile.count) {
+          if (cuts > 1) {
+            float* to = p.parts + static_cast<int64_t>(u % cuts) * head.live * p.width + at + c0;
 #pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            if (c0 + j < p.rank)
-              *reinterpret_cast<float4*>(to + c0 + j) = make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
-                                                                    __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+            for (int j = 0; j < 16; j += 4)
+              __stcg(reinterpret_cast<float4*>(to + j),
+                     make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
+                                 __uint_as_float(v[j + 3])));
+          } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              w[j] = pack_pair(scale * __uint_as_float(v[2 * j]), scale * __uint_as_float(v[2 * j + 1]), T{});
+            uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(p.v) + at + c0);
+            to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.drained);
+      if (cuts > 1 && p.join) {
+        epi_sync();
+        if (tid == 0) {  // releases the four warps' part, and acquires the others' where it is the last
+          int before;
+          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.arrived + u / cuts) : "memory");
+          s.last = before == cuts - 1 ? 1 : 0;
+        }
+        epi_sync();
+        if (s.last) {
+          join_parts<T>(p, tile, head.live, cuts, tid, s.sums);
+          if (tid == 0) p.arrived[u / cuts] = 0;
+        }
+      }
     }
   }
   tc_fence_before();
@@ -341,25 +486,28 @@ __global__ void __launch_bounds__(kShrinkThreads)
 }
 
 // ------------------------------------------------------------------ expand
-constexpr int kExpandThreads = 256;
-constexpr int kExpandCols = 32 * kExpandThreads / 32;  // of a block: 32 to a warp
-constexpr int kSteps = kTile / 16;                     // MMAs' worth of tokens of a tile
+constexpr int kExpandThreads = 128;
+constexpr int kExpandBlocks = 4;                  // to an SM (three of rank 128)
+constexpr int kExpandCols = kExpandThreads;       // of a unit: 32 to a warp
+constexpr int kExpandTokens = 64;                 // of a unit: half a tile
+constexpr int kPieces = kExpandTokens / 8;        // 16-byte pieces of res of a thread
 struct ExpandParams {
   const PlanHead* head;
   const PlanTile* tiles;
   const int32_t* order;
-  const float* v;
+  const void* v;
   const void *b, *res;
-  const float* scale;
   void* y;
   int64_t ldres, ldy;
-  int n, slots, N, rank, kblocks, shrink_grid;
+  int n, slots, N, rank, width;
+  int halves;    // of a tile: one where no tile can have more tokens than a unit
+  bool in_place;  // y is res: nothing to do for tokens without an adapter
 };
 // Words of a row of v in shared memory: 8 more than whole 32s, so that the
 // eight rows of a fragment lie in different banks.
 __host__ __device__ constexpr int v_words(int kb) { return 8 * kb + (40 - 8 * kb % 32) % 32; }
 __host__ __device__ constexpr size_t expand_smem(int kb) {
-  return static_cast<size_t>(2 * kSteps) * kExpandThreads * 16 + static_cast<size_t>(kTile) * v_words(kb) * 4;
+  return static_cast<size_t>(2 * kPieces) * kExpandThreads * 16 + static_cast<size_t>(2 * kExpandTokens) * v_words(kb) * 4;
 }
 
 template <typename T>
@@ -376,133 +524,170 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Block (tile, 256 columns), a warp 32 of these: it keeps its columns of b in
-// registers and walks down the tile's tokens, 16 at a time.  All of its part of
-// res is asked for at once, ahead of everything else, into the threads' own
-// slots of shared memory (64 KB; with two blocks to an SM that keeps 128 KB
-// under way); v is summed over the cuts, scaled and rounded into shared memory
-// by the whole block.  In a fragment, lane 4 g + q holds reduction elements
-// 4 q .. 4 q + 3 of each 16 (in both operands), and the columns 8 q .. 8 q + 7 of
-// rows g and g + 8: column c of the j-th of its four MMAs is column
-// 8 (c / 2) + 2 j + c % 2 of the warp's.
+// Units of up to 64 of a tile's tokens by 128 columns, the columns of the same
+// tokens one after another; a block takes an equal run of them.  A warp has 32
+// columns: it holds its part of b in registers and walks down the tokens, 16 at
+// a time.  The next unit's part of res is on its way into the threads' own
+// slots of shared memory meanwhile (64 KB to an SM; one unit to a block, with
+// its loads, its products and its stores one after another, took 60 us where
+// this takes 40, at 32768 tokens of 1536 columns), and so is v where the tokens
+// change.  In a fragment, lane 4 g + q holds reduction elements 4 q .. 4 q + 3 of
+// each 16 (in both operands), and the columns 8 q .. 8 q + 7 of rows g and g + 8:
+// column c of the j-th of its four MMAs is column 8 (c / 2) + 2 j + c % 2 of the
+// warp's.
 template <typename T, int KB>
-__global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandParams p) {
+__global__ void __launch_bounds__(kExpandThreads, kExpandBlocks) expand_kernel(const ExpandParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   uint4* const slots = reinterpret_cast<uint4*>(smem) + threadIdx.x;
-  uint32_t* const vs = reinterpret_cast<uint32_t*>(smem + static_cast<size_t>(2 * kSteps) * kExpandThreads * 16);
+  uint32_t* const vs = reinterpret_cast<uint32_t*>(smem + static_cast<size_t>(2 * kPieces) * kExpandThreads * 16);
   constexpr int kWords = v_words(KB);
   // the plan and res are older than the call: no need to wait for those
   const PlanHead head = *p.head;
-  if (head.n != p.n || head.slots != p.slots || static_cast<int>(blockIdx.x) >= head.tiles + head.none) {
-    wait_for_previous();
-    return;
-  }
-  const PlanTile tile = p.tiles[blockIdx.x];
-  const bool named = static_cast<int>(blockIdx.x) < head.tiles;
+  const bool mine = head.n == p.n && head.slots == p.slots;
+  const int chunks = (p.N + kExpandCols - 1) / kExpandCols;
+  const int64_t units = mine ? static_cast<int64_t>(head.tiles + (p.in_place ? 0 : head.none)) * p.halves * chunks : 0;
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int c0 = blockIdx.y * kExpandCols + warp * 32, col = c0 + 8 * q;  // of this lane's eight results
-  const int steps = (tile.count + 15) / 16;
-  const bool in = col < p.N;
-  const int32_t* const order = p.order + tile.start;
-  if (p.res != nullptr && in) {
-    for (int i = 0; i < 2 * steps; ++i) {
-      const int at = 8 * i + g;
-      if (at < tile.count)
-        cp_async16(slots + i * kExpandThreads, static_cast<const T*>(p.res) + __ldg(order + at) * p.ldres + col);
+
+  // where the next unit lies, and its rows 8 i + g (-1: none)
+  int64_t next = u0;
+  int t_next = u0 < u1 ? static_cast<int>(u0 / chunks) : 0, c_next = u0 < u1 ? static_cast<int>(u0 % chunks) : 0;
+  PlanTile tile_next{};
+  int count_next = 0, row_next[kPieces];
+  const auto look = [&] {
+    tile_next = p.tiles[t_next / p.halves];
+    tile_next.start += t_next % p.halves * kExpandTokens;
+    count_next = max(0, min(kExpandTokens, tile_next.count - t_next % p.halves * kExpandTokens));
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      row_next[i] = 8 * i + g < count_next ? __ldg(p.order + tile_next.start + 8 * i + g) : -1;
+  };
+  // v of the next unit's tokens, by the whole block: 16-byte pieces of rows, and
+  // zeros past the ranks that there are
+  const auto fetch_v = [&](int half) {
+    constexpr int kRow = 2 * KB;  // pieces
+    const bool named = t_next / p.halves < head.tiles;
+    for (int i = threadIdx.x; named && i < count_next * kRow; i += kExpandThreads) {
+      const int r = i / kRow, e = i % kRow * 8;
+      cp_async16_zfill(vs + (half * kExpandTokens + r) * kWords + e / 2,
+                       static_cast<const T*>(p.v) + static_cast<int64_t>(tile_next.start + r) * p.width +
+                           (e < p.width ? e : 0),
+                       e < p.width ? 16 : 0);
     }
-  }
+  };
+  const auto fetch = [&](int buffer) {  // the next unit's part of res
+    const int col = c_next * kExpandCols + warp * 32 + 8 * q;
+    if (next < u1 && p.res != nullptr && col < p.N) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        if (row_next[i] >= 0)
+          cp_async16(slots + (buffer * kPieces + i) * kExpandThreads,
+                     static_cast<const T*>(p.res) + row_next[i] * p.ldres + col);
+    }
+    cp_async_commit();
+  };
+  if (u0 < u1) look();
+  fetch(0);
+  wait_for_previous();
+  int half = 0, buffer = 0;  // of v's, of res's slots
+  if (u0 < u1) fetch_v(0);
   cp_async_commit();
-  uint32_t b[4][KB][2];
-  if (named) {
-    const T* pool = static_cast<const T*>(p.b) + static_cast<int64_t>(tile.adapter) * p.N * p.rank;
+  bool fresh = true;  // this block's other threads have copied v for this unit
+  for (int64_t u = u0; u < u1; ++u, buffer ^= 1) {
+    const PlanTile tile = tile_next;
+    const int count = count_next, c0 = c_next * kExpandCols + warp * 32, col = c0 + 8 * q;
+    const bool in = col < p.N, named = t_next / p.halves < head.tiles;
+    int row[kPieces];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int bc = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        uint2 w = make_uint2(0u, 0u);
-        if (bc < p.N && 16 * k + 4 * q < p.rank)
-          w = __ldg(reinterpret_cast<const uint2*>(pool + static_cast<int64_t>(bc) * p.rank + 16 * k + 4 * q));
-        b[j][k][0] = w.x;
-        b[j][k][1] = w.y;
+    for (int i = 0; i < kPieces; ++i) row[i] = row_next[i];
+    next = u + 1;
+    const bool first = fresh;
+    fresh = ++c_next == chunks;
+    if (fresh) {
+      // the other half of v was read for the tile before this one: ahead of this
+      // tile's barrier below, unless that is still to come
+      if (first) __syncthreads();
+      c_next = 0;
+      ++t_next;
+      if (next < u1) {
+        look();
+        fetch_v(half ^ 1);
       }
     }
-  }
-  wait_for_previous();
-  if (named) {
-    const float scale = __ldg(p.scale + tile.adapter);
-    const int cuts = cuts_of(head.tiles, p.shrink_grid, p.kblocks);
-    const int64_t cut = static_cast<int64_t>(head.live) * p.rank;
-    constexpr int kQuads = 4 * KB;  // of a row
-    for (int i = threadIdx.x; i < tile.count * kQuads; i += kExpandThreads) {
-      const int row = i / kQuads, e = i % kQuads * 4;
-      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (e < p.rank) {  // past the rank: zeros
-        const float* at = p.v + static_cast<int64_t>(tile.start + row) * p.rank + e;
-        for (int c = 0; c < cuts; ++c) {
-          const float4 d = *reinterpret_cast<const float4*>(at + c * cut);
-          f.x += d.x, f.y += d.y, f.z += d.z, f.w += d.w;
+    fetch(buffer ^ 1);
+    uint32_t b[4][KB][2];
+    if (named) {
+      const T* pool = static_cast<const T*>(p.b) + static_cast<int64_t>(tile.adapter) * p.N * p.rank;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int bc = c0 + 8 * (g >> 1) + 2 * j + (g & 1);
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+          uint2 w = make_uint2(0u, 0u);
+          if (bc < p.N && 16 * k + 4 * q < p.rank)
+            w = __ldg(reinterpret_cast<const uint2*>(pool + static_cast<int64_t>(bc) * p.rank + 16 * k + 4 * q));
+          b[j][k][0] = w.x;
+          b[j][k][1] = w.y;
         }
       }
-      *reinterpret_cast<uint2*>(vs + row * kWords + e / 2) =
-          make_uint2(pack_pair(scale * f.x, scale * f.y, T{}), pack_pair(scale * f.z, scale * f.w, T{}));
     }
-    __syncthreads();
+    cp_async_wait_group<1>();
+    if (first) __syncthreads();  // the same for the whole block
+#pragma unroll
+    for (int s = 0; s < kPieces / 2; ++s) {
+      if (16 * s >= count) break;
+      uint4 r[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        r[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.res != nullptr && in && row[2 * s + i] >= 0)
+          r[i] = slots[(buffer * kPieces + 2 * s + i) * kExpandThreads];
+      }
+      if (named) {
+        float acc[4][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // the products are added to res
+          Raw<T, 8> raw;
+          raw.v = r[i];
+          float f[8];
+          raw.unpack(f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[j][2 * i] = f[2 * j];
+            acc[j][2 * i + 1] = f[2 * j + 1];
+          }
+        }
+        // (rows past the tile's last hold anything: their results are dropped)
+        const uint32_t* at = vs + (half * kExpandTokens + 16 * s + g) * kWords + 2 * q;
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+          const uint2 lo = *reinterpret_cast<const uint2*>(at + 8 * k);
+          const uint2 hi = *reinterpret_cast<const uint2*>(at + 8 * kWords + 8 * k);
+          const uint32_t a[4] = {lo.x, hi.x, lo.y, hi.y};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma16816<T>(acc[j], a, b[j][k][0], b[j][k][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[2 * j] = acc[j][2 * i];
+            f[2 * j + 1] = acc[j][2 * i + 1];
+          }
+          Raw<T, 8> raw;
+          raw.pack(f);
+          r[i] = raw.v;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (in && row[2 * s + i] >= 0)
+          *reinterpret_cast<uint4*>(static_cast<T*>(p.y) + row[2 * s + i] * p.ldy + col) = r[i];
+    }
+    if (fresh) half ^= 1;
   }
   cp_async_wait_all();
-  if (!in && !named) return;
-  for (int s = 0; s < steps; ++s) {
-    float acc[4][4];
-    uint4 r[2];
-    int row[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = 16 * s + 8 * i + g;
-      row[i] = at < tile.count ? __ldg(order + at) : -1;
-      r[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (p.res != nullptr && in && row[i] >= 0) r[i] = slots[(2 * s + i) * kExpandThreads];
-    }
-    if (named) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {  // the products are added to res
-        Raw<T, 8> raw;
-        raw.v = r[i];
-        float f[8];
-        raw.unpack(f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[j][2 * i] = f[2 * j];
-          acc[j][2 * i + 1] = f[2 * j + 1];
-        }
-      }
-      // (rows past the tile's last hold anything: their results are dropped)
-      const uint32_t* at = vs + (16 * s + g) * kWords + 2 * q;
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        const uint2 lo = *reinterpret_cast<const uint2*>(at + 8 * k);
-        const uint2 hi = *reinterpret_cast<const uint2*>(at + 8 * kWords + 8 * k);
-        const uint32_t a[4] = {lo.x, hi.x, lo.y, hi.y};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mma16816<T>(acc[j], a, b[j][k][0], b[j][k][1]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (row[i] < 0 || !in) continue;
-      Raw<T, 8> raw;
-      raw.v = r[i];
-      if (named) {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[2 * j] = acc[j][2 * i];
-          f[2 * j + 1] = acc[j][2 * i + 1];
-        }
-        raw.pack(f);
-      }
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.y) + row[i] * p.ldy + col) = raw.v;
-    }
-  }
 }
 
 // --------------------------------------------------------------- host side
@@ -529,6 +714,7 @@ bool map_pool(CUtensorMap* m, const void* base, uint64_t K, uint64_t rank, uint6
 }
 
 constexpr int kMostSms = 192;  // any device of this kind has fewer
+constexpr int kShrinkSmem = 110 * 1024;  // two CTAs to an SM
 
 cudaError_t allow_smem(const void* kern, std::atomic<bool> (&set)[64], int bytes) {
   int dev = 0;
@@ -541,6 +727,35 @@ cudaError_t allow_smem(const void* kern, std::atomic<bool> (&set)[64], int bytes
   return err;
 }
 
+template <typename T>
+cudaError_t launch_shrink(const ShrinkParams& p, const CUtensorMap& mx, const CUtensorMap& mr, const CUtensorMap& ma,
+                          int grid, size_t bytes, cudaStream_t s) {
+  static std::atomic<bool> set[64];
+  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(shrink_kernel<T>), set, kShrinkSmem);
+  if (err != cudaSuccess) return err;
+  shrink_kernel<T><<<grid, kShrinkThreads, bytes, s>>>(mx, mr, ma, p);
+  const cudaError_t launched = cudaGetLastError();
+  if (launched != cudaSuccess || p.join) return launched;
+  JoinParams j{};
+  j.head = p.head;
+  j.tiles = p.tiles;
+  j.parts = p.parts;
+  j.scale = p.scale;
+  j.v = p.v;
+  j.n = p.n;
+  j.slots = p.slots;
+  j.width = p.width;
+  j.kblocks = p.kblocks;
+  j.shrink_grid = grid;
+  cudaLaunchAttribute overlap = overlap_attribute();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * sm_count()));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<T>, j);
+}
 template <typename T, int KB>
 cudaError_t launch_expand(const ExpandParams& p, dim3 grid, cudaStream_t s) {
   static std::atomic<bool> set[64];
@@ -570,10 +785,19 @@ cudaError_t launch_expand(const ExpandParams& p, dim3 grid, int kb, cudaStream_t
 size_t adapter_plan_bytes(int64_t T, int slots) {
   return plan_order_at(T, slots) + (static_cast<size_t>(T) * 4 + 255) / 256 * 256;
 }
-size_t adapter_ws_bytes(const moe_adapter_dims& d) {
-  // cuts * live tokens: one cut, or as many as make the tiles of 128 tokens fill the grid
-  return (static_cast<size_t>(d.T) + 2 * static_cast<size_t>(kMostSms) * kTile) * d.rank * sizeof(float);
-}
+// Workspace: the tiles' counters (zero between calls), v, the parts: as many
+// cuts as make the tiles of 128 tokens fill the grid.
+struct AdapterLayout {
+  size_t v, parts, all;
+  explicit AdapterLayout(const moe_adapter_dims& d) {
+    const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    const size_t width = (d.rank + 15) / 16 * 16;
+    v = up(static_cast<size_t>(most_tiles(d.T, d.slots)) * 4);
+    parts = v + up(static_cast<size_t>(d.T) * width * 2);
+    all = parts + 2 * static_cast<size_t>(kMostSms) * kTile * width * 4;
+  }
+};
+size_t adapter_ws_bytes(const moe_adapter_dims& d) { return AdapterLayout(d).all; }
 
 cudaError_t launch_adapter_plan(const int32_t* ids, int32_t n, int32_t T, int32_t slots, void* plan,
                                 int32_t* dev_status, cudaStream_t s) {
@@ -595,7 +819,13 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   p.head = reinterpret_cast<const PlanHead*>(at);
   p.tiles = reinterpret_cast<const PlanTile*>(at + sizeof(PlanHead));
   p.order = reinterpret_cast<const int32_t*>(at + plan_order_at(d.T, d.slots));
-  p.v = static_cast<float*>(c.ws);
+  const AdapterLayout ws(d);
+  uint8_t* scratch = static_cast<uint8_t*>(c.ws);
+  p.arrived = reinterpret_cast<int32_t*>(scratch);
+  p.v = scratch + ws.v;
+  p.parts = reinterpret_cast<float*>(scratch + ws.parts);
+  p.scale = c.scale;
+  p.join = c.n <= 256;
   p.n = c.n;
   p.slots = d.slots;
   p.rank = d.rank;
@@ -605,12 +835,8 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   p.status = c.dev_status;
   p.limit_ns = kDefaultWaitLimitNs;
   const size_t stage = kTokenStage + static_cast<size_t>(p.width) * kBlockK * 2;
-  // two CTAs to an SM
-  p.stages = static_cast<int>(std::min<size_t>(kMaxStages, (110 * 1024 - 1024 - sizeof(ShrinkCtl)) / stage));
+  p.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kShrinkSmem - 1024 - sizeof(ShrinkCtl)) / stage));
   const size_t bytes = 1024 + p.stages * stage + sizeof(ShrinkCtl);
-  static std::atomic<bool> set[64];
-  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(shrink_kernel), set, 110 * 1024);
-  if (err != cudaSuccess) return err;
   CUtensorMap mx, mr, ma;
   if (!map_tokens(&mx, c.x, d.K, c.n, c.ldx, 1) || !map_tokens(&mr, c.x, d.K, c.n, c.ldx, kTile) ||
       !map_pool(&ma, c.a, d.K, d.rank, d.slots, p.width))
@@ -618,9 +844,9 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   // no more CTAs than units of the fewest blocks
   const int grid = static_cast<int>(std::min<int64_t>(
       2 * std::min(sm_count(), kMostSms), most * std::max(1, p.kblocks / kLeastCutBlocks)));
-  shrink_kernel<<<grid, kShrinkThreads, bytes, s>>>(mx, mr, ma, p);
-  const cudaError_t launched = cudaGetLastError();
-  if (launched != cudaSuccess) return launched;
+  const cudaError_t err = d.type == MOE_BF16 ? launch_shrink<__nv_bfloat16>(p, mx, mr, ma, grid, bytes, s)
+                                             : launch_shrink<__half>(p, mx, mr, ma, grid, bytes, s);
+  if (err != cudaSuccess) return err;
 
   ExpandParams e{};
   e.head = p.head;
@@ -630,17 +856,18 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   e.b = c.b;
   e.res = c.res;
   e.ldres = c.ldres;
-  e.scale = c.scale;
   e.y = c.y;
   e.ldy = c.ldy;
   e.n = c.n;
   e.slots = d.slots;
   e.N = d.N;
   e.rank = d.rank;
-  e.kblocks = p.kblocks;
-  e.shrink_grid = grid;
-  const dim3 blocks(static_cast<unsigned>(most), static_cast<unsigned>((d.N + kExpandCols - 1) / kExpandCols));
-  const int kb = p.width / 16;
+  e.width = p.width;
+  e.halves = c.n <= kExpandTokens ? 1 : kTile / kExpandTokens;
+  e.in_place = c.y == c.res && c.ldy == c.ldres;
+  const int64_t units = most * e.halves * ((d.N + kExpandCols - 1) / kExpandCols);
+  const int kb = p.width / 16, per_sm = kb > 4 ? 3 : kExpandBlocks;
+  const dim3 blocks(static_cast<unsigned>(std::min<int64_t>(units, per_sm * sm_count())));
   return d.type == MOE_BF16 ? launch_expand<__nv_bfloat16>(e, blocks, kb, s) : launch_expand<__half>(e, blocks, kb, s);
 }
 

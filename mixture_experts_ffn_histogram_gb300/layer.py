@@ -520,7 +520,7 @@ class LowRankAdapters:
         self._y = torch.empty((T, N), dtype=dtype, device=dev)
         self.device = dev = self._y.device
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        self.ws = torch.zeros(need, dtype=torch.uint8, device=dev)
         self._my, self._p_status, self._p_ws = _own(self._y), self.status.data_ptr(), self.ws.data_ptr()
         self._x, self._res = _Arg("x", dtype, dev), _Arg("res", dtype, dev)
         self._a, self._b = (_Arg(n, dtype, dev, contiguous=True) for n in ("a", "b"))
