@@ -675,3 +675,44 @@ class MoELayer:
         du = self.up.backward(dh, u, g["w1"], dx_add=du, stream=stream)
         du = self.gate.backward(dlogits, u, g["wr"], dx_add=du, need_db=False, stream=stream)
         return self.norm.backward(du, self.norm.r, g["gamma"], dres=dr, stream=stream)
+
+
+class DecodeLayer:
+    """A feed-forward layer that serves up to T tokens, a few: routed experts
+    beside a shared dense one with the requests' adapters on its second
+    product, and the norms around them.
+
+        l  = u wr                                        (Linear, fp32)
+        h  = act(u w1 + b1),  s = h w2 + b2              (two Linears)
+        s += scale[a] (h a_a^T) b_a^T                    (LowRankAdapters, with a batch)
+        m  = experts(u; l, bias) + s                     (MoEDecode)
+        r' = r + branch * norm(m) (post + offset)        (BlockNorm)
+        u' = norm(r') (pre + offset)
+
+    ``forward`` takes the residual stream r and u, its norm, and returns both
+    behind the layer (views of the norm's buffers, ``norm.r`` and ``norm.u``)."""
+
+    WEIGHTS = ("wr", "wi", "wo", "w1", "b1", "w2", "b2", "post", "pre")
+    ADAPTERS = ("a", "b", "scale")
+
+    def __init__(self, T, D, E, K, F, shared, score_mode=B.SCORE_SOFTMAX_TOPK, act="silu",
+                 dtype=torch.bfloat16, eps=1e-6, branch=1.0, offset=0.0, slots=0, rank=8, device="cuda"):
+        self.gate = Linear(T, D, E, dtype, torch.float32, device=device)
+        self.up = Linear(T, D, shared, dtype, act=act, device=device)
+        self.down = Linear(T, shared, D, dtype, device=device)
+        self.adapters = LowRankAdapters(T, shared, D, slots, rank, dtype, device) if slots else None
+        self.experts = MoEDecode(T, D, E, K, F, score_mode, dtype, device)
+        self.norm = BlockNorm(T, D, dtype, torch.float32, eps, branch, offset, train=False, device=device)
+
+    def forward(self, r, u, weights, bias=None, batch=None, stream=None):
+        g = weights
+        if batch is not None and self.adapters is None:
+            raise ValueError("the layer was built without adapters (slots=0)")
+        logits = self.gate.forward(u, g["wr"], stream=stream)
+        h = self.up.forward(u, g["w1"], g["b1"], stream=stream)
+        s = self.down.forward(h, g["w2"], g["b2"], stream=stream)
+        if batch is not None:
+            s = self.adapters.forward(batch, h, g["a"], g["b"], g["scale"], res=s, stream=stream)
+        m = self.experts.forward(u, g["wi"], g["wo"], logits=logits, bias=bias, res=s, stream=stream)
+        u = self.norm.forward(r, m, g["post"], g["pre"], stream=stream)
+        return self.norm.r, u
