@@ -268,6 +268,6 @@ def test_the_kernels_need_a_device():
 
 
 def test_the_layer_refuses_a_batch_without_adapters():
-    lay = DecodeLayer(4, 64, 4, 2, 64, 64, device="cpu")
+    lay = DecodeLayer(4, 64, 8, 2, 64, 64, device="cpu")
     with pytest.raises(ValueError, match="without adapters"):
         lay.forward(t(4, 64), t(4, 64), {}, batch=AdapterBatch(4, 2, device="cpu"))
