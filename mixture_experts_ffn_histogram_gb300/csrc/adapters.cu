@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
   constexpr int kSlices = 4;
   for (int u = blockIdx.x; u < head.tiles * kSlices; u += gridDim.x) {
     const PlanTile tile = p.tiles[u / kSlices];
-    const float scale = __ldg(p.scale + tile.adapter);
+    const float scale = p.scale[tile.adapter];
     const int64_t first = static_cast<int64_t>(tile.start) * per_row;
     for (int i = u % kSlices * kJoinThreads + threadIdx.x; i < tile.count * per_row; i += kSlices * kJoinThreads) {
       float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandBlocks) expand_kernel(c
     count_next = max(0, min(kExpandTokens, tile_next.count - t_next % p.halves * kExpandTokens));
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
-      row_next[i] = 8 * i + g < count_next ? __ldg(p.order + tile_next.start + 8 * i + g) : -1;
+      row_next[i] = 8 * i + g < count_next ? p.order[tile_next.start + 8 * i + g] : -1;
   };
   // v of the next unit's tokens, by the whole block: 16-byte pieces of rows, and
   // zeros past the ranks that there are
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandBlocks) expand_kernel(c
         for (int k = 0; k < KB; ++k) {
           uint2 w = make_uint2(0u, 0u);
           if (bc < p.N && 16 * k + 4 * q < p.rank)
-            w = __ldg(reinterpret_cast<const uint2*>(pool + static_cast<int64_t>(bc) * p.rank + 16 * k + 4 * q));
+            w = *reinterpret_cast<const uint2*>(pool + static_cast<int64_t>(bc) * p.rank + 16 * k + 4 * q);
           b[j][k][0] = w.x;
           b[j][k][1] = w.y;
         }
