@@ -9,9 +9,8 @@
 // list of tiles of up to 128 tokens of one adapter (those without one come
 // last).  Made once for a batch: all of its projections share it.
 // shrink: v = x a_s^T by tile on the tensor cores.  The tile's tokens are
-// gathered straight from x (four rows of 128 bytes to a TMA gather, or one box
-// where they follow one another) as the 128 side, the rank is the narrow side,
-// and the reduction over K is cut among CTAs where tiles are few.  Bound by
+// copied straight from their places in x as the 128 side, the rank is the narrow
+// side, and the reduction over K is cut among CTAs where tiles are few.  Bound by
 // reading x; for a few tokens by latency.
 // expand: y = res + scale v b_s^T.  Its reduction is the rank, one to eight
 // MMAs deep, so that nearly all of it is moving res and y: the products are
@@ -161,6 +160,9 @@ __device__ __forceinline__ int cuts_of(int tiles, int grid, int kblocks) {
 }
 
 struct ShrinkParams {
+  const void* x;
+  int64_t ldx;
+  int K;
   const PlanHead* head;
   const PlanTile* tiles;
   const int32_t* order;
@@ -168,7 +170,7 @@ struct ShrinkParams {
   float* parts;      // [cuts][live tokens][width], where there is more than one cut
   int32_t* arrived;  // [tile]: cuts whose part is stored; zero between calls
   const float* scale;
-  bool join;         // here, not in a kernel of its own
+  bool few;          // tokens: gathered by TMA, and parts joined here
   int n, slots, rank, width, kblocks, stages;  // width: rank in whole 16s
   uint32_t type;
   int32_t* status;
@@ -308,13 +310,72 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
   }
 }
 
+// Many tokens: the four epilogue warps copy a tile's, wherever they lie, in
+// 16-byte pieces (eight lanes to a row's 128 bytes, swizzled like a TMA box),
+// some stages ahead of telling the products.
+constexpr int kMostLag = 4;
+template <typename T>
+struct TokenCopies {
+  uint8_t* ring;
+  int stage_bytes, q, lane, lag;
+  int stage = 0, told = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ TokenCopies(const ShrinkParams& p, uint8_t* ring, int stage_bytes, int q, int lane)
+      : ring(ring), stage_bytes(stage_bytes), q(q), lane(lane), lag(min(kMostLag, p.stages - 1)) {}
+
+  __device__ __forceinline__ bool run(const ShrinkParams& p, ShrinkCtl& s, const WaitCtl& wc, const PlanTile& tile,
+                                      Blocks blocks) {
+    const int piece = lane % 8;
+    const T* from[8];  // rows 32 q + 4 i + lane / 8
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 32 * q + 4 * i + lane / 8;
+      from[i] = r < tile.count ? static_cast<const T*>(p.x) + __ldg(p.order + tile.start + r) * p.ldx + piece * 8
+                               : nullptr;
+    }
+    for (int i = 0; i < blocks.count + lag; ++i) {
+      if (i < blocks.count) {
+        if (!warp_wait(&s.empty[stage], phase ^ 1u, wc)) {
+          cp_async_wait_all();
+          return false;
+        }
+        uint8_t* to = ring + stage * stage_bytes;
+        const int k = blocks.kb * kBlockK;
+        const int bytes = k + piece * 8 < p.K ? 16 : 0;  // zeros past the last column
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = 32 * q + 4 * j + lane / 8;
+          if (from[j] != nullptr)
+            cp_async16_zfill(to + r * 128 + (piece ^ (r & 7)) * 16, bytes != 0 ? from[j] + k : from[j], bytes);
+        }
+        blocks.next();
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      cp_async_commit();
+      if (i >= lag) {
+        if (lag == 4) cp_async_wait_group<4>();
+        else if (lag == 3) cp_async_wait_group<3>();
+        else cp_async_wait_group<2>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.full[told]);
+        if (++told == p.stages) told = 0;
+      }
+    }
+    return true;
+  }
+};
+
 // A CTA takes every so manieth unit (tile, cut): the tile's products over every
 // so manieth reduction block, so that a tile's CTAs read neighbouring pieces of
 // its rows at the same time.
 template <typename T>
 __global__ void __launch_bounds__(kShrinkThreads)
-    shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_rows,
-                  const __grid_constant__ CUtensorMap map_a, const ShrinkParams p) {
+    shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
+                  const ShrinkParams p) {
   extern __shared__ uint8_t smem_raw[];
   let_next_launch();
   const PlanHead head = *p.head;
@@ -331,7 +392,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   const int cols = tmem_width(p.width);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&s.full[i], 1);
+      mbar_init(&s.full[i], p.few ? 1 : 1 + 4);  // warp 0, and the four warps that copy tokens
       mbar_init(&s.empty[i], 1);
     }
     mbar_init(&s.done, 1);
@@ -339,7 +400,6 @@ __global__ void __launch_bounds__(kShrinkThreads)
     s.abort_flag = 0;
     mbar_fence_init();
     tma_prefetch_map(&map_x);
-    tma_prefetch_map(&map_rows);
     tma_prefetch_map(&map_a);
   }
   if (warp == 1) {
@@ -358,29 +418,23 @@ __global__ void __launch_bounds__(kShrinkThreads)
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const PlanTile tile = p.tiles[u / cuts];
-      // Tokens that follow one another come as one box of 128 rows.  Others
-      // are gathered, lane i the tile's tokens 4i .. 4i + 3 (past the last: the
-      // last again).  Rows of the product past the tile's are not stored.
-      const int t0 = __ldg(p.order + tile.start), t1 = __ldg(p.order + tile.start + tile.count - 1);
-      const bool run = t1 - t0 == tile.count - 1;
-      const int groups = run ? 0 : (tile.count + 3) / 4;
+      // Few tokens: lane i gathers the tile's tokens 4i .. 4i + 3 (past the
+      // last: the last again; their rows of the product are not stored).
+      const int groups = p.few ? (tile.count + 3) / 4 : 0;
       int row[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) row[i] = run ? 0 : __ldg(p.order + tile.start + min(4 * lane + i, tile.count - 1));
-      const int bytes = (run ? kTokenStage : groups * 512) + p.width * kBlockK * 2;
-      Blocks at(u, cuts, p.kblocks);
-      for (int i = 0; i < at.count; ++i, at.next()) {
-        const int kb = at.kb;
+      for (int i = 0; i < 4; ++i) row[i] = p.few ? __ldg(p.order + tile.start + min(4 * lane + i, tile.count - 1)) : 0;
+      Blocks blocks(u, cuts, p.kblocks);
+      for (int i = 0; i < blocks.count; ++i, blocks.next()) {
         ok = warp_wait(&s.empty[stage], phase ^ 1u, wc);
         if (!ok) break;
         uint8_t* to = ring + stage * stage_bytes;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&s.full[stage], bytes);
-          if (run) tma_load_2d(to, &map_rows, &s.full[stage], kb * kBlockK, t0);
-          tma_load_3d(to + kTokenStage, &map_a, &s.full[stage], kb * kBlockK, 0, tile.adapter);
+          mbar_arrive_expect_tx(&s.full[stage], groups * 512 + p.width * kBlockK * 2);
+          tma_load_3d(to + kTokenStage, &map_a, &s.full[stage], blocks.kb * kBlockK, 0, tile.adapter);
         }
         __syncwarp();  // armed before any gather lands
-        if (lane < groups) gather4(to + 512 * lane, &map_x, &s.full[stage], kb * kBlockK, row);
+        if (lane < groups) gather4(to + 512 * lane, &map_x, &s.full[stage], blocks.kb * kBlockK, row);
         ++filled;
         if (++stage == p.stages) {
           stage = 0;
@@ -428,11 +482,13 @@ __global__ void __launch_bounds__(kShrinkThreads)
     }
   } else {
     const int q = warp & 3, tid = q * 32 + lane;  // also this thread's token of the tile
+    TokenCopies<T> copies(p, ring, stage_bytes, q, lane);
     int unit = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++unit) {
       const PlanTile tile = p.tiles[u / cuts];
+      const bool copied = p.few || copies.run(p, s, wc, tile, Blocks(u, cuts, p.kblocks));
       // the four warps meet at barriers below: all go on or none does
-      if (!epi_all(warp_wait(&s.done, unit & 1, wc))) break;
+      if (!epi_all(copied && warp_wait(&s.done, unit & 1, wc))) break;
       tc_fence_after();
       const int64_t at = static_cast<int64_t>(tile.start + tid) * p.width;
       const float scale = __ldg(p.scale + tile.adapter);
@@ -462,7 +518,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.drained);
-      if (cuts > 1 && p.join) {
+      if (cuts > 1 && p.few) {
         epi_sync();
         if (tid == 0) {  // releases the four warps' part, and acquires the others' where it is the last
           int before;
@@ -691,12 +747,12 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandBlocks) expand_kernel(c
 }
 
 // --------------------------------------------------------------- host side
-// Rows of x in boxes of 64 elements of `rows_per_box` rows (one: for gathers).
-bool map_tokens(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld, uint32_t rows_per_box) {
+// Rows of x for four-row gathers.
+bool map_tokens(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {inner, rows}, strides[1] = {ld * 2};
-  const cuuint32_t box[2] = {64, rows_per_box}, es[2] = {1, 1};
+  const cuuint32_t box[2] = {64, 1}, es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -728,14 +784,13 @@ cudaError_t allow_smem(const void* kern, std::atomic<bool> (&set)[64], int bytes
 }
 
 template <typename T>
-cudaError_t launch_shrink(const ShrinkParams& p, const CUtensorMap& mx, const CUtensorMap& mr, const CUtensorMap& ma,
-                          int grid, size_t bytes, cudaStream_t s) {
+cudaError_t launch_shrink(const ShrinkParams& p, const CUtensorMap& mx, const CUtensorMap& ma, int grid, size_t bytes, cudaStream_t s) {
   static std::atomic<bool> set[64];
   const cudaError_t err = allow_smem(reinterpret_cast<const void*>(shrink_kernel<T>), set, kShrinkSmem);
   if (err != cudaSuccess) return err;
-  shrink_kernel<T><<<grid, kShrinkThreads, bytes, s>>>(mx, mr, ma, p);
+  shrink_kernel<T><<<grid, kShrinkThreads, bytes, s>>>(mx, ma, p);
   const cudaError_t launched = cudaGetLastError();
-  if (launched != cudaSuccess || p.join) return launched;
+  if (launched != cudaSuccess || p.few) return launched;
   JoinParams j{};
   j.head = p.head;
   j.tiles = p.tiles;
@@ -816,6 +871,9 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   const uint8_t* at = static_cast<const uint8_t*>(c.plan);
   const int64_t most = most_tiles(c.n, d.slots);
   ShrinkParams p{};
+  p.x = c.x;
+  p.ldx = c.ldx;
+  p.K = d.K;
   p.head = reinterpret_cast<const PlanHead*>(at);
   p.tiles = reinterpret_cast<const PlanTile*>(at + sizeof(PlanHead));
   p.order = reinterpret_cast<const int32_t*>(at + plan_order_at(d.T, d.slots));
@@ -825,7 +883,11 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   p.v = scratch + ws.v;
   p.parts = reinterpret_cast<float*>(scratch + ws.parts);
   p.scale = c.scale;
-  p.join = c.n <= 256;
+  // Few tokens make tiles of few tokens, whose latency counts: a TMA gather for
+  // every four, no second kernel to join parts (61 tokens of 64 adapters: 14.0
+  // us against 15.9).  Many fill their tiles: gathers keep to 31 bytes a ns and
+  // SM, four warps' copies do not (32768 tokens: 86 us against 78).
+  p.few = c.n <= 256;
   p.n = c.n;
   p.slots = d.slots;
   p.rank = d.rank;
@@ -837,15 +899,13 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   const size_t stage = kTokenStage + static_cast<size_t>(p.width) * kBlockK * 2;
   p.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kShrinkSmem - 1024 - sizeof(ShrinkCtl)) / stage));
   const size_t bytes = 1024 + p.stages * stage + sizeof(ShrinkCtl);
-  CUtensorMap mx, mr, ma;
-  if (!map_tokens(&mx, c.x, d.K, c.n, c.ldx, 1) || !map_tokens(&mr, c.x, d.K, c.n, c.ldx, kTile) ||
-      !map_pool(&ma, c.a, d.K, d.rank, d.slots, p.width))
-    return cudaErrorInvalidValue;
+  CUtensorMap mx, ma;
+  if (!map_tokens(&mx, c.x, d.K, c.n, c.ldx) || !map_pool(&ma, c.a, d.K, d.rank, d.slots, p.width)) return cudaErrorInvalidValue;
   // no more CTAs than units of the fewest blocks
   const int grid = static_cast<int>(std::min<int64_t>(
       2 * std::min(sm_count(), kMostSms), most * std::max(1, p.kblocks / kLeastCutBlocks)));
-  const cudaError_t err = d.type == MOE_BF16 ? launch_shrink<__nv_bfloat16>(p, mx, mr, ma, grid, bytes, s)
-                                             : launch_shrink<__half>(p, mx, mr, ma, grid, bytes, s);
+  const cudaError_t err = d.type == MOE_BF16 ? launch_shrink<__nv_bfloat16>(p, mx, ma, grid, bytes, s)
+                                             : launch_shrink<__half>(p, mx, ma, grid, bytes, s);
   if (err != cudaSuccess) return err;
 
   ExpandParams e{};
