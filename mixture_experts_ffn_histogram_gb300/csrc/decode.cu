@@ -57,6 +57,17 @@ constexpr uint16_t kNone = 0xffff;
 static_assert(!fits_beside_pair(kMinStages * (kWeightStage + 16 * kBlockK * 2)),
               "CTAs that wait for one another must not fit beside a pair's: tmem_share.h");
 
+// What the combine reads and writes.
+struct CombineParams {
+  const uint2* slots;  // [n * K]: slot_word, the weight's bits; [n * K].x: virtual experts
+  const float *y, *part;
+  const void* res;
+  void* out;
+  int64_t ldres, ldout;
+  int n, D, F, K, nt;
+  uint32_t grid;  // of the first kernel
+};
+
 struct Params {
   const float *logits, *bias, *w_in;
   const int32_t* ids_in;
@@ -64,12 +75,13 @@ struct Params {
   float* w_out;
   int n, D, E, K, F;  // n: tokens of this call
   int mode;
-  int nt, stages;     // tokens of a tile at most (16, 32 or 64)
+  int nt, nt_log;     // tokens of a tile at most (16, 32 or 64)
+  int stages;
   uint32_t type;      // of the instruction descriptor
   void* h;            // [n * K][F]
   float* y;           // [n * K][D]: FC2's rows of tiles that one CTA summed alone
   float* part;        // [2 phases][CTA][head, tail][nt][128]: sums of parts of tiles
-  uint2* slots;       // [n * K]: for the combine (slot_word, the weight's bits); [n * K].x: virtual experts
+  uint2* slots;       // for the combine's kernel
   int32_t* gids;      // [n * K] and its weights: selections that the CTAs exchange
   float* gw;
   int32_t* leave;     // CTAs that read no more flags
@@ -100,6 +112,7 @@ struct Route {
   uint16_t *vexp, *vstart, *vcnt;            // [V]
   uint16_t* before;                          // [warps][E]: slots of the expert in the warps ahead
   uint16_t *first, *start;                   // [E]: its first virtual expert, its place in the list
+  // w holds scores until weigh() has turned them into weights, where `raw`
 };
 constexpr int kWarps = kThreads / 32;
 __host__ __device__ inline int most_virtual(int R, int E, int nt) {
@@ -161,6 +174,14 @@ __device__ __forceinline__ bool epi_all(bool ok) {
   return r != 0;
 }
 
+// Adds to a counter; what this thread has seen written is written before, and
+// what others had written before they added is seen after.
+__device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
+  int before;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(before) : "l"(p), "r"(v) : "memory");
+  return before;
+}
+
 // Waits until *at is `want`, for wc's limit.
 __device__ __forceinline__ bool wait_for(const int32_t* at, int want, const WaitCtl& wc) {
   if (ld_acquire(at) == want) return true;
@@ -205,9 +226,9 @@ __device__ __forceinline__ float score_of(uint32_t u) {
 
 // The K best of a token's E scores by one warp: K rounds of a maximum over the
 // lanes' own best, the lower expert first among equal scores.
-// Lane k < K of the warp gets slot k.
+// Lane k < K of the warp gets slot k's expert and score.
 template <int PER>
-__device__ __forceinline__ void select_token(const Params& p, int t, int lane, int* id, float* weight) {
+__device__ __forceinline__ void select_token(const Params& p, int t, int lane, int* id, float* score) {
   uint32_t key[PER];
   const float* row = p.logits + static_cast<int64_t>(t) * p.E;
 #pragma unroll
@@ -245,22 +266,27 @@ __device__ __forceinline__ void select_token(const Params& p, int t, int lane, i
       mine_e = e;
     }
   }
-  const float v = score_of(mine), first = __shfl_sync(0xffffffffu, v, 0);
+  *id = mine_e;
+  *score = score_of(mine);
+}
+__device__ __forceinline__ void select_one(const Params& p, int t, int lane, int* id, float* score) {
+  if (p.E <= 128) select_token<4>(p, t, lane, id, score);
+  else if (p.E <= 256) select_token<8>(p, t, lane, id, score);
+  else select_token<32>(p, t, lane, id, score);
+}
+// The weights of the K scores that the first lanes hold.
+__device__ __forceinline__ float weigh(const Params& p, float v, int lane) {
+  const float first = __shfl_sync(0xffffffffu, v, 0);
   float ex = 0.0f;
   if (lane < p.K) ex = p.mode == MOE_SCORE_SOFTMAX_TOPK ? expf(v - first) : 1.0f / (1.0f + expf(-v));
   float sum = 0.0f;  // in the slots' order
   for (int k = 0; k < p.K; ++k) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, ex, k));
-  *id = mine_e;
-  *weight = __fdiv_rn(ex, sum);
-}
-__device__ __forceinline__ void select_one(const Params& p, int t, int lane, int* id, float* weight) {
-  if (p.E <= 128) select_token<4>(p, t, lane, id, weight);
-  else if (p.E <= 256) select_token<8>(p, t, lane, id, weight);
-  else select_token<32>(p, t, lane, id, weight);
+  return __fdiv_rn(ex, sum);
 }
 
 // Everyone's selection in r.expert and r.w.  Up to a token for each of its warps a
-// CTA selects all for itself; of more tokens each CTA selects its own, and they
+// CTA selects all for itself (and leaves the scores in r.w: only the combine
+// needs weights, and that is far off); of more tokens each CTA selects its own, and they
 // exchange them through global memory (128 tokens of 128 experts: 42 us when
 // every CTA selected all).  False: a wait gave up.
 __device__ __forceinline__ bool select_all(const Params& p, const Route& r, const WaitCtl& wc, int warp, int lane) {
@@ -277,16 +303,11 @@ __device__ __forceinline__ bool select_all(const Params& p, const Route& r, cons
   } else if (p.n <= kWarps) {
     if (warp < p.n) {
       int e;
-      float w;
-      select_one(p, warp, lane, &e, &w);
+      float v;
+      select_one(p, warp, lane, &e, &v);
       if (lane < p.K) {
-        const int j = warp * p.K + lane;
-        r.expert[j] = static_cast<uint16_t>(e);
-        r.w[j] = w;
-        if (blockIdx.x == 0) {
-          if (p.ids_out != nullptr) p.ids_out[j] = e;
-          if (p.w_out != nullptr) p.w_out[j] = w;
-        }
+        r.expert[warp * p.K + lane] = static_cast<uint16_t>(e);
+        r.w[warp * p.K + lane] = v;
       }
     }
   } else {
@@ -294,16 +315,16 @@ __device__ __forceinline__ bool select_all(const Params& p, const Route& r, cons
       int e;
       float w;
       select_one(p, t, lane, &e, &w);
+      w = weigh(p, w, lane);
       if (lane < p.K) {
         const int j = t * p.K + lane;
         p.gids[j] = e;
         p.gw[j] = w;
         if (p.ids_out != nullptr) p.ids_out[j] = e;
         if (p.w_out != nullptr) p.w_out[j] = w;
-        __threadfence();
       }
       __syncwarp();
-      if (lane == 0) atomicAdd(p.routed, 1);
+      if (lane == 0) (void)add_acq_rel(p.routed, 1);
     }
     if (threadIdx.x == 0) ok = wait_for(p.routed, p.n, wc);
     ok = __syncthreads_and(ok);
@@ -320,8 +341,10 @@ __device__ __forceinline__ bool select_all(const Params& p, const Route& r, cons
 // expert's counts are summed over the warps, then over the experts.
 __device__ __forceinline__ int build_list(const Params& p, const Route& r, Ctl& s, int warp, int lane) {
   const int R = p.n * p.K, span = (R + kThreads - 1) / kThreads * 32;
+  const int warps = (R + span - 1) / span;  // that have slots
   uint16_t* mine = r.before + warp * p.E;
-  for (int e = lane; e < p.E; e += 32) mine[e] = 0;
+  if (warp < warps)
+    for (int e = lane; e < p.E; e += 32) mine[e] = 0;
   __syncwarp();
   for (int j0 = warp * span; j0 < min(R, (warp + 1) * span); j0 += 32) {
     const int j = j0 + lane;
@@ -342,15 +365,14 @@ __device__ __forceinline__ int build_list(const Params& p, const Route& r, Ctl& 
   int slots = 0, lists = 0;
   for (int e = e0; e < e1; ++e) {
     int sum = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < warps; ++w) {
       const int c = r.before[w * p.E + e];
       r.before[w * p.E + e] = static_cast<uint16_t>(sum);
       sum += c;
     }
     r.start[e] = static_cast<uint16_t>(sum);  // the count, until its place is known
     slots += sum;
-    lists += (sum + p.nt - 1) / p.nt;
+    lists += (sum + p.nt - 1) >> p.nt_log;
   }
   int ss = slots, sl = lists;
 #pragma unroll
@@ -390,15 +412,39 @@ __device__ __forceinline__ int build_list(const Params& p, const Route& r, Ctl& 
     const int j = j0 + lane;
     if (j >= R) break;
     const int e = r.expert[j];
-    const int rank = e != kNone ? r.rank[j] + mine[e] : 0;
     if (e != kNone) {
+      const int rank = r.rank[j] + mine[e];
       r.list[r.start[e] + rank] = static_cast<uint16_t>(j);
-      r.at[j] = static_cast<uint16_t>(r.first[e] + rank / p.nt);
+      r.at[j] = static_cast<uint16_t>(r.first[e] + (rank >> p.nt_log));
+      r.rank[j] = static_cast<uint16_t>(rank & (p.nt - 1));  // in its virtual expert
     }
-    if (blockIdx.x == 0) p.slots[j] = make_uint2(e != kNone ? slot_word(r.at[j], rank & (p.nt - 1)) : 0u, __float_as_uint(r.w[j]));
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.slots[R] = make_uint2(entries, 0u);
   return entries;
+}
+// Slot j as the combine reads it.
+__device__ __forceinline__ uint32_t word_of(const Route& r, int j) {
+  return r.expert[j] != kNone ? slot_word(r.at[j], r.rank[j]) : 0u;
+}
+
+// What is left of the routing once the tiles are known, by the epilogue's warps
+// while there is nothing to finish: weights, and (block 0) the caller's copies
+// and the combine's table.
+__device__ __forceinline__ void finish_routing(const Params& p, const Route& r, int entries, int ew, int lane) {
+  const bool raw = p.mode != MOE_SCORE_GIVEN && p.n <= kWarps, block0 = blockIdx.x == 0;
+  if (!raw && !block0) return;
+  for (int t = ew; t < p.n; t += 4) {
+    const int j = t * p.K + lane;
+    float w = lane < p.K ? r.w[j] : 0.0f;
+    if (raw) w = weigh(p, w, lane);
+    if (lane >= p.K) continue;
+    if (raw) r.w[j] = w;
+    if (block0) {
+      p.slots[j] = make_uint2(word_of(r, j), __float_as_uint(w));
+      if (raw && p.ids_out != nullptr) p.ids_out[j] = r.expert[j];
+      if (raw && p.w_out != nullptr) p.w_out[j] = w;
+    }
+  }
+  if (block0 && ew == 0 && lane == 0) p.slots[p.n * p.K] = make_uint2(entries, 0u);
 }
 
 // One phase's tiles and blocks.  (At most 1056 virtual experts of 256 tiles; the
@@ -480,31 +526,14 @@ __device__ __forceinline__ void add8(const float* at, float (&f)[8]) {
 }
 
 // out[t, 128 col ..] by one warp, four columns a lane: the token's slots in
-// order, each the sum of its tile's parts in the reduction's order.  The
-// first kernel's tables and sums are read by ordinary loads (see
-// wait_for_previous).
-struct CombineParams {
-  const uint2* slots;
-  const float *y, *part;
-  const void* res;
-  void* out;
-  int64_t ldres, ldout;
-  int n, D, F, K, nt;
-  uint32_t grid;  // of the first kernel
-};
-constexpr int kCombineWarps = 4;
+// order, each the sum of its tile's parts in the reduction's order.  Lane k < K
+// brings slot k's word and weight.
 template <typename T>
-__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const CombineParams p) {
+__device__ __forceinline__ void combine_unit(const CombineParams& p, const Phase& f, int t, int col, int lane,
+                                             uint32_t word, float w) {
   constexpr int kAhead = 8;
-  const int lane = threadIdx.x & 31;
-  const int tiles = (p.D + kCols - 1) / kCols;
-  const int unit = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
-  const int t = unit / tiles, col = unit - t * tiles;
-  wait_for_previous();
-  if (t >= p.n) return;
   const int c4 = col * kCols + lane * 4;
   const bool in = c4 < p.D;
-  const Phase f(p.D, p.F, p.grid, 1, __ldcg(&p.slots[static_cast<int64_t>(p.n) * p.K].x));
   float r4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (p.res != nullptr && in) {
     const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.res) + t * p.ldres + c4);
@@ -514,15 +543,11 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Combi
   // lane k looks at slot k: the CTAs of its tile's first and last part (the
   // same where one summed it alone) and its row in their parts
   uint32_t first = 0, last = 0, row = 0;
-  float w = 0.0f;
-  bool valid = false;
-  if (lane < p.K) {
-    const uint2 q = __ldcg(p.slots + static_cast<int64_t>(t) * p.K + lane);
-    valid = (q.x & 0x80000000u) != 0u;
-    w = __uint_as_float(q.y);
-    row = (q.x >> 16) & 0xffu;
-    const uint32_t tile = (q.x & 0xffffu) * f.cols + col;
-    if (valid && tile >= f.waves * f.grid) {
+  const bool valid = lane < p.K && (word & 0x80000000u) != 0u;
+  if (valid) {
+    row = (word >> 16) & 0xffu;
+    const uint32_t tile = (word & 0xffffu) * f.cols + col;
+    if (tile >= f.waves * f.grid) {
       const uint32_t b = (tile - f.waves * f.grid) * f.kb;
       first = f.owner(b);
       last = f.owner(b + f.kb - 1);
@@ -575,6 +600,23 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Combi
       make_uint2(pack_pair(acc[0] + r4[0], acc[1] + r4[1], T{}), pack_pair(acc[2] + r4[2], acc[3] + r4[3], T{}));
 }
 
+// The combine as a kernel of its own: a warp to a token's 128 columns.  (What
+// the first kernel wrote is read by ordinary loads: see wait_for_previous.)
+constexpr int kCombineWarps = 4;
+template <typename T>
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const CombineParams p) {
+  const int lane = threadIdx.x & 31;
+  const int tiles = (p.D + kCols - 1) / kCols;
+  const int unit = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+  const int t = unit / tiles, col = unit - t * tiles;
+  wait_for_previous();
+  if (t >= p.n) return;
+  uint2 slot = make_uint2(0u, 0u);
+  if (lane < p.K) slot = __ldcg(p.slots + static_cast<int64_t>(t) * p.K + lane);
+  const Phase f(p.D, p.F, p.grid, 1, __ldcg(&p.slots[static_cast<int64_t>(p.n) * p.K].x));
+  combine_unit<T>(p, f, t, col, lane, slot.x, __uint_as_float(slot.y));
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap map_wi, const __grid_constant__ CUtensorMap map_wo,
@@ -616,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int entries = 0;
   if (routed) {
     entries = build_list(p, r, s, warp, lane);
-  } else if (blockIdx.x == 0) {  // the combine finds no slot
+  } else if (blockIdx.x == 0) {  // the combine's kernel finds no slot
     for (int j = threadIdx.x; j <= p.n * p.K; j += kThreads) p.slots[j] = make_uint2(0u, 0u);
   }
   tc_fence_before();
@@ -768,9 +810,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kFirstEpiWarp) {
     // -------------------------------------------------------------- epilogue
-    const int tid = threadIdx.x - kFirstEpiWarp * 32;
+    const int tid = threadIdx.x - kFirstEpiWarp * 32, ew = warp - kFirstEpiWarp;
     const int col = (warp & 3) * 32 + lane;  // the tile's column: this thread's TMEM lane
     const uint32_t tq = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    if (routed) finish_routing(p, r, entries, ew, lane);
     int piece = 0;
     bool ok = true;
     for (int ph = 0; ph < 2 && ok; ++ph) {
@@ -920,6 +963,7 @@ cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   p.F = d.F;
   p.mode = c.mode;
   p.nt = tile_tokens(d.T);
+  p.nt_log = p.nt == 16 ? 4 : p.nt == 32 ? 5 : 6;
   p.type = c.type == MOE_BF16 ? 1u : 0u;
   p.status = c.dev_status;
   p.limit_ns = kDefaultWaitLimitNs;
