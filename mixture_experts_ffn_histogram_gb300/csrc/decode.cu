@@ -14,7 +14,11 @@
 // neighbouring columns are read at the same time; the tiles that are left (all
 // of them for one token, some 90) are cut into equal runs of blocks, which
 // begin and end inside a tile.  Whole tiles alone would leave a tenth to a
-// third of the SMs idle in the last wave.  The CTA that has a tile's first
+// third of the SMs idle in the last wave.  FC2's tiles, where there are several
+// for each CTA, are claimed one by one instead: an SM in a large group of SMs
+// gets an eighth less of the memory's rate than one in a small group, so that
+// equal shares end 20 us apart for 16 tokens, and whoever is done with FC1 early
+// makes up for it here.  The CTA that has a tile's first
 // part joins the others to it, in their order: it comes to that part last, the
 // others to theirs first, so it need not wait, and results do not depend on
 // who was faster.  (Joining by whoever adds the last part took 3 us longer from
@@ -54,6 +58,8 @@ constexpr int kBufBytes = 16 * kBufLd * 4;  // 16 tokens of a tile
 constexpr size_t kSmemLimit = 227 * 1024;
 constexpr int kFirstEpiWarp = 4;
 constexpr uint16_t kNone = 0xffff;
+constexpr int kQueue = 4;
+constexpr int kQueueReaders = 1 + 1 + 4;
 static_assert(!fits_beside_pair(kMinStages * (kWeightStage + 16 * kBlockK * 2)),
               "CTAs that wait for one another must not fit beside a pair's: tmem_share.h");
 
@@ -84,6 +90,7 @@ struct Params {
   uint2* slots;       // for the combine's kernel
   int32_t* gids;      // [n * K] and its weights: selections that the CTAs exchange
   float* gw;
+  int32_t* claimed;   // tiles of FC2 that CTAs took
   int32_t* leave;     // CTAs that read no more flags
   int32_t* routed;    // tokens whose selection is stored
   int32_t* done;      // [tile of FC1]: its h is stored
@@ -101,6 +108,9 @@ struct Ctl {
   uint32_t tmem_base;
   int abort_flag;
   uint2 warp_sums[kThreads / 32];
+  uint64_t qfull[kQueue];   // a claimed tile is in the queue
+  uint64_t qempty[kQueue];  // ... and has been read by the tokens', products' and epilogue's warps
+  uint32_t qtile[kQueue];
 };
 
 // The routing, in shared memory.  Slot j = t * K + k.  An expert with more than
@@ -447,31 +457,42 @@ __device__ __forceinline__ void finish_routing(const Params& p, const Route& r, 
   if (block0 && ew == 0 && lane == 0) p.slots[p.n * p.K] = make_uint2(entries, 0u);
 }
 
-// One phase's tiles and blocks.  (At most 1056 virtual experts of 256 tiles; the
-// blocks cut into runs are of fewer tiles than CTAs: 32 bits hold all products.)
-constexpr uint32_t kLeastBlocks = 4;  // of a run: shorter ones cost more to join than they save
-struct Phase {
-  uint32_t kb;                       // blocks of a tile
-  uint32_t cols;                     // tiles of a virtual expert
-  uint32_t grid, waves;              // every CTA takes `waves` whole tiles
-  uint32_t blocks, ctas;             // of the tiles behind them; the CTAs that take runs of these
-  __device__ __forceinline__ Phase(int D, int F, uint32_t grid, int which, uint32_t entries) : grid(grid) {
-    kb = (which == 0 ? D : F) / kBlockK;
-    cols = which == 0 ? F / 64 : (D + kCols - 1) / kCols;
-    const uint32_t tiles = entries * cols;
-    waves = tiles / grid;
-    blocks = (tiles - waves * grid) * kb;
-    ctas = min(grid, (blocks + kLeastBlocks - 1) / kLeastBlocks);
-  }
-  __device__ __forceinline__ uint32_t run(uint32_t c) const { return blocks * c / ctas; }
-  // the CTA whose run holds block b
-  __device__ __forceinline__ uint32_t owner(uint32_t b) const { return ((b + 1) * ctas - 1) / blocks; }
-};
 // A part of a tile: blocks [k0, k1) of tile `col` of virtual expert `v`.
 struct Piece {
   uint32_t tile, v, col;
   int k0, k1;
 };
+
+// One phase's tiles and blocks.  (At most 1056 virtual experts of 256 tiles; the
+// blocks cut into runs are of fewer tiles than CTAs: 32 bits hold all products.)
+constexpr uint32_t kLeastBlocks = 4;  // of a run: shorter ones cost more to join than they save
+constexpr uint32_t kLeastClaims = 4;  // tiles for each CTA, for these to be claimed one by one
+struct Phase {
+  uint32_t kb;                       // blocks of a tile
+  uint32_t cols;                     // tiles of a virtual expert
+  uint32_t grid, tiles;
+  bool claims;                       // tiles are claimed, whole
+  uint32_t waves;                    // else every CTA takes `waves` whole tiles
+  uint32_t blocks, ctas;             // of the tiles behind them; the CTAs that take runs of these
+  __device__ __forceinline__ Phase(int D, int F, uint32_t grid, int which, uint32_t entries) : grid(grid) {
+    kb = (which == 0 ? D : F) / kBlockK;
+    cols = which == 0 ? F / 64 : (D + kCols - 1) / kCols;
+    tiles = entries * cols;
+    claims = which == 1 && tiles >= kLeastClaims * grid;
+    waves = tiles / grid;
+    blocks = (tiles - waves * grid) * kb;
+    ctas = min(grid, (blocks + kLeastBlocks - 1) / kLeastBlocks);
+  }
+  __device__ __forceinline__ uint32_t run(uint32_t c) const { return blocks * c / ctas; }
+  __device__ __forceinline__ bool whole(uint32_t tile) const { return claims || tile < waves * grid; }
+  __device__ __forceinline__ void place(Piece& q) const;
+  // the CTA whose run holds block b
+  __device__ __forceinline__ uint32_t owner(uint32_t b) const { return ((b + 1) * ctas - 1) / blocks; }
+};
+__device__ __forceinline__ void Phase::place(Piece& q) const {
+  q.v = q.tile / cols;
+  q.col = q.tile - q.v * cols;
+}
 // The CTA's pieces in their order.
 struct Walk {
   uint32_t wave, b, end;
@@ -496,8 +517,33 @@ struct Walk {
     } else {
       return false;
     }
-    q.v = q.tile / f.cols;
-    q.col = q.tile - q.v * f.cols;
+    f.place(q);
+    return true;
+  }
+};
+// Where a role gets its pieces from: the walk, or the queue of claimed tiles.
+// `Walk`s end by themselves; a queue ends with a tile past the last.
+struct Feed {
+  Walk walk;
+  uint32_t taken;  // from the queue
+  __device__ __forceinline__ explicit Feed(const Phase& f) : walk(f), taken(0) {}
+
+  // by one thread, or (WARP) a whole warp; ok becomes false where a wait gave up
+  template <bool WARP>
+  __device__ __forceinline__ bool next(const Phase& f, Piece& q, Ctl& s, const WaitCtl& wc, int lane, bool& ok) {
+    if (!f.claims) return walk.next(f, q);
+    const int slot = taken % kQueue;
+    const uint32_t parity = taken / kQueue & 1u;
+    ok = WARP ? warp_wait(&s.qfull[slot], parity, wc) : mbar_wait(&s.qfull[slot], parity, wc);
+    if (!ok) return false;
+    q.tile = s.qtile[slot];
+    if (WARP) __syncwarp();
+    if (!WARP || lane == 0) mbar_arrive(&s.qempty[slot]);
+    ++taken;
+    if (q.tile >= f.tiles) return false;
+    q.k0 = 0;
+    q.k1 = static_cast<int>(f.kb);
+    f.place(q);
     return true;
   }
 };
@@ -547,7 +593,7 @@ __device__ __forceinline__ void combine_unit(const CombineParams& p, const Phase
   if (valid) {
     row = (word >> 16) & 0xffu;
     const uint32_t tile = (word & 0xffffu) * f.cols + col;
-    if (tile >= f.waves * f.grid) {
+    if (!f.whole(tile)) {
       const uint32_t b = (tile - f.waves * f.grid) * f.kb;
       first = f.owner(b);
       last = f.owner(b + f.kb - 1);
@@ -645,6 +691,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.tfull[i], 1);
       mbar_init(&s.tempty[i], 4);
     }
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(&s.qfull[i], 1);
+      mbar_init(&s.qempty[i], kQueueReaders);
+    }
     mbar_fence_init();
     tma_prefetch_map(&map_wi);
     tma_prefetch_map(&map_x);
@@ -677,7 +727,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Phase f(p.D, p.F, gridDim.x, ph, entries);
         Walk walk(f);
         Piece q;
-        while (ok && walk.next(f, q)) {
+        int ahead = f.claims ? atomicAdd(p.claimed, 1) : 0;  // a tile ahead: its latency is hidden
+        for (uint32_t put = 0; ok; ++put) {
+          if (f.claims) {
+            const int slot = put % kQueue;
+            q.tile = static_cast<uint32_t>(ahead);
+            if (put >= kQueue) ok = mbar_wait(&s.qempty[slot], (put / kQueue - 1) & 1u, wc);
+            if (!ok) break;
+            s.qtile[slot] = q.tile;
+            mbar_arrive(&s.qfull[slot]);
+            if (q.tile >= f.tiles) break;
+            ahead = atomicAdd(p.claimed, 1);
+            q.k0 = 0;
+            q.k1 = static_cast<int>(f.kb);
+            f.place(q);
+          } else if (!walk.next(f, q)) {
+            break;
+          }
           const int e = r.vexp[q.v];
           const int c0 = ph == 0 ? q.col * 64 : q.col * kCols;
           const int c1 = ph == 0 ? p.F + c0 : c0 + 64;
@@ -714,10 +780,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int ph = 0; ph < 2 && ok; ++ph) {
       const Phase f(p.D, p.F, gridDim.x, ph, entries);
-      Walk walk(f);
+      Feed feed(f);
       Piece q;
       const int flags = p.F / 64;  // of a virtual expert
-      while (ok && walk.next(f, q)) {
+      while (ok && feed.next<true>(f, q, s, wc, lane, ok)) {
         const int cnt = r.vcnt[q.v], groups = (cnt + 3) / 4;
         int row[4];
 #pragma unroll
@@ -762,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = entries * (p.F / 64);
       for (int i = lane; i < n; i += 32) p.done[i] = 0;
       for (int i = lane; i < static_cast<int>(gridDim.x); i += 32) p.stored[i] = 0;
-      if (lane == 0) *p.leave = *p.routed = 0;
+      if (lane == 0) *p.leave = *p.routed = *p.claimed = 0;
     }
     if (!ok && lane == 0) {
       for (int i = 0; i < p.stages; ++i) {
@@ -780,9 +846,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
         const Phase f(p.D, p.F, gridDim.x, ph, entries);
-        Walk walk(f);
+        Feed feed(f);
         Piece q;
-        for (; ok && walk.next(f, q); ++piece) {
+        for (; ok && feed.next<false>(f, q, s, wc, lane, ok); ++piece) {
           const int slot = piece & 1;
           const uint32_t idesc = dense_idesc(kCols, (r.vcnt[q.v] + 15) & ~15, true, false, p.type);
           if (piece >= 2) ok = mbar_wait(&s.tempty[slot], ((piece >> 1) - 1) & 1, wc);
@@ -818,9 +884,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int ph = 0; ph < 2 && ok; ++ph) {
       const Phase f(p.D, p.F, gridDim.x, ph, entries);
-      Walk walk(f);
+      Feed feed(f);
       Piece q;
-      for (; walk.next(f, q); ++piece) {
+      for (;; ++piece) {
+        // the four warps meet at barriers below: all go on or none does
+        const bool more = feed.next<true>(f, q, s, wc, lane, ok);
+        ok = epi_all(ok);
+        if (!ok || !more) break;
         const int slot = piece & 1, cnt = r.vcnt[q.v], start = r.vstart[q.v];
         const bool whole = q.k1 - q.k0 == static_cast<int>(f.kb);
         const int i16 = tid / 8, c8 = (tid % 8) * 8;  // FC1: this thread's token of 16, its columns
@@ -830,7 +900,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           join1 = f.owner((q.tile - f.waves * f.grid + 1) * f.kb - 1);
           for (uint32_t c = join0 + tid; c <= join1 && ok; c += 128) ok = wait_for(p.stored + c, 1, wc);
         }
-        // the four warps meet at barriers below: all go on or none does
         ok = epi_all(ok);
         if (!ok) break;
         const auto joined = [&](int t0, float (&g)[8], float (&u)[8]) {
@@ -973,6 +1042,7 @@ cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   p.leave = reinterpret_cast<int32_t*>(ws);
   p.done = reinterpret_cast<int32_t*>(ws + at.done);
   p.routed = p.leave + 1;
+  p.claimed = p.leave + 2;
   p.stored = p.leave + 32;
   p.slots = reinterpret_cast<uint2*>(ws + at.slots);
   p.gids = reinterpret_cast<int32_t*>(ws + at.gids);

@@ -150,6 +150,25 @@ def test_fewer_tokens_strides_and_reproducible_results():
     assert int(op.status.item()) == 0
 
 
+def test_claimed_tiles_repeat_bit_for_bit():
+    """Enough tiles that CTAs claim them one by one: whoever takes one, the
+    result is the same; shorter calls through the same operator in between."""
+    need_gpu()
+    T, D, E, K, F = 24, 1088, 96, 6, 192
+    d = _data(T, D, E, K, F, BF, 31)
+    op = _op(T, D, E, K, F, "sigmoid")
+    first = op.forward(d["x"], d["wi"], d["wo"], logits=d["logits"], res=d["res"]).clone()
+    ids, w = select(d["logits"], None, K, "sigmoid")
+    assert len(set(ids.flatten().tolist())) * ((D + 127) // 128) >= 4 * 152
+    _check(op, d, ids, w, d["res"], first, True)
+    for n in (24, 1, 24, 12, 24):
+        out = op.forward(d["x"][:n], d["wi"], d["wo"], logits=d["logits"][:n], res=d["res"][:n])
+        if n == T:
+            assert torch.equal(out, first)
+    torch.cuda.synchronize()
+    assert int(op.status.item()) == 0 and not bool(op.ws[:1024].any())
+
+
 def test_another_stream_and_a_graph():
     need_gpu()
     T, D, E, K, F = 8, 512, 16, 4, 256
