@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 constexpr int kShrinkThreads = 192;
 constexpr int kTokenStage = kTile * kBlockK * 2;  // 16 KB
 constexpr int kMaxStages = 8;
+constexpr int kMinStages = 3;
 constexpr int kLeastCutBlocks = 4;
 
 // The cuts of a tile's reduction: as many as give every CTA of the grid (two
@@ -312,7 +313,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
 
 // Many tokens: the four epilogue warps copy a tile's, wherever they lie, in
 // 16-byte pieces (eight lanes to a row's 128 bytes, swizzled like a TMA box),
-// some stages ahead of telling the products.
+// some stages ahead of telling the products: all stages but two, so that a
+// stage's products and the word that it is free again take their time while
+// others land (all but one: 32768 mixed tokens 81 us against 73).
 constexpr int kMostLag = 4;
 template <typename T>
 struct TokenCopies {
@@ -321,7 +324,7 @@ struct TokenCopies {
   int stage = 0, told = 0;
   uint32_t phase = 0;
   __device__ __forceinline__ TokenCopies(const ShrinkParams& p, uint8_t* ring, int stage_bytes, int q, int lane)
-      : ring(ring), stage_bytes(stage_bytes), q(q), lane(lane), lag(min(kMostLag, p.stages - 1)) {}
+      : ring(ring), stage_bytes(stage_bytes), q(q), lane(lane), lag(min(kMostLag, p.stages - 2)) {}
 
   __device__ __forceinline__ bool run(const ShrinkParams& p, ShrinkCtl& s, const WaitCtl& wc, const PlanTile& tile,
                                       Blocks blocks) {
@@ -358,7 +361,8 @@ struct TokenCopies {
       if (i >= lag) {
         if (lag == 4) cp_async_wait_group<4>();
         else if (lag == 3) cp_async_wait_group<3>();
-        else cp_async_wait_group<2>();
+        else if (lag == 2) cp_async_wait_group<2>();
+        else cp_async_wait_group<1>();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.full[told]);
@@ -771,6 +775,7 @@ bool map_pool(CUtensorMap* m, const void* base, uint64_t K, uint64_t rank, uint6
 
 constexpr int kMostSms = 192;  // any device of this kind has fewer
 constexpr int kShrinkSmem = 110 * 1024;  // two CTAs to an SM
+static_assert(1024 + kMinStages * (kTokenStage + 128 * kBlockK * 2) + sizeof(ShrinkCtl) <= kShrinkSmem, "rank 128");
 
 cudaError_t allow_smem(const void* kern, std::atomic<bool> (&set)[64], int bytes) {
   int dev = 0;
@@ -886,7 +891,7 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   // Few tokens make tiles of few tokens, whose latency counts: a TMA gather for
   // every four, no second kernel to join parts (61 tokens of 64 adapters: 14.0
   // us against 15.9).  Many fill their tiles: gathers keep to 31 bytes a ns and
-  // SM, four warps' copies do not (32768 tokens: 86 us against 78).
+  // SM, four warps' copies do not (32768 tokens: 87 us against 73).
   p.few = c.n <= 256;
   p.n = c.n;
   p.slots = d.slots;
