@@ -73,18 +73,28 @@ __global__ void __launch_bounds__(kPlanThreads)
   int32_t* mine = before + warp * buckets;
   for (int b = lane; b < buckets; b += 32) mine[b] = 0;
   __syncwarp();
-  const auto bucket_of = [&](int j) {
-    if (j >= j1) return -1;
-    const int id = __ldg(ids + j);
-    return id >= 0 && id < slots ? id : slots;
+  // the buckets of eight times 32 tokens at a time: eight loads under way
+  const auto each = [&](const auto& visit) {
+    constexpr int kLoads = 8;
+    for (int j = j0; j < j1; j += 32 * kLoads) {
+      int id[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = j + 32 * i + lane;
+        id[i] = at < j1 ? __ldg(ids + at) : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = j + 32 * i + lane;
+        const int b = at >= j1 ? -1 : id[i] >= 0 && id[i] < slots ? id[i] : slots;
+        visit(at, b, id[i]);
+      }
+    }
   };
-  for (int j = j0; j < j1; j += 32) {
-    const int b = bucket_of(j + lane);
-    if (b == slots && __ldg(ids + j + lane) != -1) report(status, MOE_ERR_DEVICE);
-    const uint32_t peers = __match_any_sync(0xffffffffu, b);
-    if (b >= 0 && lane == __ffs(peers) - 1) mine[b] += __popc(peers);
-    __syncwarp();
-  }
+  each([&](int, int b, int id) {
+    if (b == slots && id != -1) report(status, MOE_ERR_DEVICE);
+    if (b >= 0) atomicAdd(mine + b, 1);
+  });
   __syncthreads();
   // thread i has bucket i (there are at most 1025: the last thread has two)
   const int per = buckets > kPlanThreads && threadIdx.x == kPlanThreads - 1 ? 2 : 1;
@@ -134,17 +144,16 @@ __global__ void __launch_bounds__(kPlanThreads)
     at += c;
   }
   __syncthreads();
-  for (int j = j0; j < j1; j += 32) {
-    const int b = bucket_of(j + lane);
+  each([&](int j, int b, int) {
     const uint32_t peers = __match_any_sync(0xffffffffu, b);
     const int first = b >= 0 ? mine[b] : 0;
     __syncwarp();
     if (b >= 0) {
-      order[first + __popc(peers & ((1u << lane) - 1u))] = j + lane;
+      order[first + __popc(peers & ((1u << lane) - 1u))] = j;
       if (lane == __ffs(peers) - 1) mine[b] = first + __popc(peers);
     }
     __syncwarp();
-  }
+  });
 }
 
 // ------------------------------------------------------------------ shrink

@@ -209,3 +209,32 @@ def test_one_bad_token_leaves_the_others():
     keep = [t for t in range(T) if t not in (3, 11)]
     assert torch.equal(got[keep], want[keep])
     assert bool(torch.isnan(got[3]).all()) and not bool(torch.isfinite(got[11]).any())
+
+
+def test_two_layers_at_once_and_among_other_kernels():
+    """Layers on streams of their own, each of which wants all SMs at once, with
+    products and copies in between: every result as when alone, no wait given
+    up."""
+    need_gpu()
+    from mixture_experts_ffn_histogram_gb300.layer import Linear
+    T, D, E, K, F = 12, 512, 32, 4, 256
+    cases = [_data(T, D, E, K, F, BF, i) for i in range(3)]
+    ops = [_op(T, D, E, K, F, "softmax") for _ in cases]
+    lins = [Linear(300, D, 1024) for _ in cases]
+    wide = [torch.randn(300, D, device="cuda").to(BF) for _ in cases]
+    w = torch.randn(D, 1024, device="cuda").to(BF)
+    want = [op.forward(d["x"], d["wi"], d["wo"], logits=d["logits"]).clone() for op, d in zip(ops, cases)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    wrong = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for i in range(60):
+        for op, d, lin, x, ref, s in zip(ops, cases, lins, wide, want, streams):
+            with torch.cuda.stream(s):
+                if i % 3 == 0:
+                    lin.forward(x, w)
+                out = op.forward(d["x"], d["wi"], d["wo"], logits=d["logits"])
+                if i % 20 == 19:
+                    wrong.add_((out != ref).sum())
+    torch.cuda.synchronize()
+    assert [int(op.status.item()) for op in ops] == [0, 0, 0]
+    assert int(wrong.item()) == 0
