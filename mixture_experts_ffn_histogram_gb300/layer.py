@@ -1,15 +1,19 @@
-"""The operators around the expert block, and a whole layer of them.
+"""The operators around the expert block, and whole layers of them.
 
 ``LayerNorm`` (with the residual add in front of it), ``TopKRouter`` (expert
 selection with a balance bias and expert groups) and ``Linear`` (bias,
-activation and residual in the product's epilogue) each own their output
-buffers and workspace, like ``MoEBlock``: allocated once for a largest number
+activation and residual in the product's epilogue), and those that serve and
+wrap the block, ``MoEDecode`` (the whole expert layer for a few tokens),
+``BlockNorm`` (RMS norms after and before a block) and ``LowRankAdapters``
+(beside a shared projection; grouped by an ``AdapterBatch``), each own their
+output buffers and workspace, like ``MoEBlock``: allocated once for a largest number
 of rows, written by every call (a call's outputs are views of them and hold
 until the next one).  Calls run on the current stream, or the one given, of
 the device that the operator was built on, which has to be the current one.
 
-``MoELayer`` runs them together with the expert block as one pre-norm
-feed-forward layer, forward and backward.
+``MoELayer`` runs the first three together with the expert block as one
+pre-norm feed-forward layer, forward and backward; ``DecodeLayer`` runs
+``Linear`` and the others as one served layer.
 """
 from __future__ import annotations
 
@@ -228,8 +232,11 @@ class BlockNorm:
             self.ws = torch.empty(max(B.moe_block_norm_workspace_bytes(self.d), 256), dtype=torch.uint8,
                                   device=dev)
             self._mdres, self._mdy = _own(self._dres), _own(self._dy_out)
-            self._p_stats = tuple(t.data_ptr() for t in self._stats)
-            self._p_dw, self._p_ws = [t.data_ptr() for t in self._dw], self.ws.data_ptr()
+            self._sy, self._sr = self._stats[0], self._stats[1]
+            self._p_stats = (self._sy.data_ptr(), self._sr.data_ptr())
+            self._grads = tuple(self._dw.unbind(0))     # of post, pre and gate
+            self._p_dpost, self._p_dpre, self._p_dgate = (t.data_ptr() for t in self._grads)
+            self._p_ws = self.ws.data_ptr()
             self._p_dtg = self._dtg.data_ptr()
         self._res, self._y, self._rin, self._du, self._dr = (
             _Arg(n, dtype, dev) for n in ("res", "y", "r", "du", "dr"))
@@ -263,8 +270,8 @@ class BlockNorm:
         self.r = res if y is None else (self._r if whole else self._r[:n])
         self.u = None if pre is None else (self._u if whole else self._u[:n])
         if self.train:
-            self.rstd_y = None if post is None else self._stats[0, :n]
-            self.rstd_r = None if pre is None else self._stats[1, :n]
+            self.rstd_y = None if post is None else (self._sy if whole else self._sy[:n])
+            self.rstd_r = None if pre is None else (self._sr if whole else self._sr[:n])
         return self.r if pre is None else self.u
 
     def backward(self, du, dr, r=None, y=None, post=None, pre=None, gate=None, token_gate=None,
@@ -298,20 +305,19 @@ class BlockNorm:
                     raise RuntimeError("backward needs a forward first, or its rstd_y")
                 py = self._rowwise[1].pointer(rstd_y, (n,))
         self.d.rows = n
-        dpost, dpre, dgate = (a if given else None for a, given in zip(self._p_dw, (post is not None,
-                                                                                   pre is not None,
-                                                                                   gate is not None)))
-        st = self._bwd(mdu, mdr, mr, my, *p, py, pr, self._mdres, _NO if y is None else self._mdy, dpost, dpre,
-                       dgate, self._p_dtg if token_gate is not None else None, self._p_ws, self.d,
-                       B.stream_of(stream, self.device))
+        st = self._bwd(mdu, mdr, mr, my, *p, py, pr, self._mdres, _NO if y is None else self._mdy,
+                       None if post is None else self._p_dpost, None if pre is None else self._p_dpre,
+                       None if gate is None else self._p_dgate, None if token_gate is None else self._p_dtg,
+                       self._p_ws, self.d, B.stream_of(stream, self.device))
         if st:
             _refused("moe_block_norm_bwd", st)
         whole = n == self.rows
         self.dy = None if y is None else (self._dy_out if whole else self._dy_out[:n])
-        self.dpost = None if post is None else self._dw[0]
-        self.dpre = None if pre is None else self._dw[1]
-        self.dgate = None if gate is None else self._dw[2]
-        self.dtoken_gate = None if token_gate is None else self._dtg[:n]
+        dpost, dpre, dgate = self._grads
+        self.dpost = None if post is None else dpost
+        self.dpre = None if pre is None else dpre
+        self.dgate = None if gate is None else dgate
+        self.dtoken_gate = None if token_gate is None else (self._dtg if whole else self._dtg[:n])
         return self._dres if whole else self._dres[:n]
 
 
@@ -525,7 +531,7 @@ class LowRankAdapters:
         self._x, self._res = _Arg("x", dtype, dev), _Arg("res", dtype, dev)
         self._a, self._b = (_Arg(n, dtype, dev, contiguous=True) for n in ("a", "b"))
         self._scale = _Arg("scale", torch.float32, dev, contiguous=True)
-        self._ashape, self._bshape = (slots, rank, K), (slots, N, rank)
+        self._ashape, self._bshape, self._sshape = (slots, rank, K), (slots, N, rank), (slots,)
         self._fwd = _entry("moe_adapters", dev)
 
     def forward(self, batch, x, a, b, scale, res=None, stream=None):
@@ -536,7 +542,7 @@ class LowRankAdapters:
         if batch.n != n:
             raise ValueError(f"the batch was grouped for {batch.n} tokens, the call has {n}")
         pa, pb = self._a.pointer(a, self._ashape), self._b.pointer(b, self._bshape)
-        ps = self._scale.pointer(scale, (self.slots,))
+        ps = self._scale.pointer(scale, self._sshape)
         mres = _NO if res is None else self._res.matrix(res, (n, self.N))
         st = self._fwd(self._x.mat, pa, pb, ps, mres, self._my, batch._p_plan, self._p_status, self._p_ws, n,
                        self.d, B.stream_of(stream, self.device))
@@ -580,13 +586,14 @@ class MoEDecode:
         if not self._given:
             self._ids = torch.empty((T, K), dtype=torch.int32, device=dev)
             self._w = torch.empty((T, K), dtype=torch.float32, device=dev)
+            self._p_ids, self._p_w = self._ids.data_ptr(), self._w.data_ptr()
         self._mout, self._p_status, self._p_ws = _own(self._out), self.status.data_ptr(), self.ws.data_ptr()
         f32 = torch.float32
         self._x, self._res = _Arg("x", dtype, dev), _Arg("res", dtype, dev)
         self._wi, self._wo = (_Arg(n, dtype, dev, contiguous=True) for n in ("wi", "wo"))
         self._l, self._b = (_Arg(n, f32, dev, contiguous=True) for n in ("logits", "bias"))
         self._i, self._win = _Arg("ids", torch.int32, dev, contiguous=True), _Arg("w", f32, dev, contiguous=True)
-        self._wishape, self._woshape = (E, D, 2 * F), (E, F, D)
+        self._wishape, self._woshape, self._experts = (E, D, 2 * F), (E, F, D), (E,)
         self._type, self._fwd = B.DTYPES[dtype], _entry("moe_decode", dev)
 
     def forward(self, x, wi, wo, logits=None, bias=None, ids=None, w=None, res=None, stream=None):
@@ -602,9 +609,9 @@ class MoEDecode:
             if logits is None:
                 raise ValueError("the layer selects the experts itself: it needs logits")
             pl = self._l.pointer(logits, (n, self.E))
-            pb = None if bias is None else self._b.pointer(bias, (self.E,))
-            ids, w = self._ids[:n], self._w[:n]
-            pi, pw = ids.data_ptr(), w.data_ptr()
+            pb = None if bias is None else self._b.pointer(bias, self._experts)
+            ids, w = (self._ids, self._w) if n == self.T else (self._ids[:n], self._w[:n])
+            pi, pw = self._p_ids, self._p_w
         mres = _NO if res is None else self._res.matrix(res, (n, self.D))
         st = self._fwd(self._x.mat, pwi, pwo, pl, pb, self.mode, pi, pw, mres, self._mout, self._p_status,
                        self._p_ws, n, self.d, self._type, B.stream_of(stream, self.device))
