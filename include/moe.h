@@ -684,8 +684,8 @@ moe_status moe_linear_bwd(moe_mat dy, moe_mat z, moe_mat x, moe_mat w, moe_mat d
                           cudaStream_t stream);
 
 /*
- * The whole expert layer for a few tokens, in one kernel: routing, FC1 with
- * SwiGLU, FC2 and the weighted combine.
+ * The whole expert layer for a few tokens, in two kernels: routing, FC1 with
+ * SwiGLU and FC2; the weighted combine.
  *   ids, w  as moe_route_histogram's (mode, logits, bias), or given
  *   h[t,k]  = round(silu(a[:F]) * a[F:]),  a = x[t] . wi[ids[t,k]]   (fp32 sums)
  *   out[t]  = round(sum_{k ascending} w[t,k] * (h[t,k] . wo[ids[t,k]]) + res[t])

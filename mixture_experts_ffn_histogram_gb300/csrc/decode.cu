@@ -82,6 +82,7 @@ struct Params {
   int n, D, E, K, F;  // n: tokens of this call
   int mode;
   int nt, nt_log;     // tokens of a tile at most (16, 32 or 64)
+  uint32_t k_inverse;  // 2^16 / K, rounded up: slot * k_inverse >> 16 = slot / K for slots below 2048
   int stages;
   uint32_t type;      // of the instruction descriptor
   void* h;            // [n * K][F]
@@ -125,17 +126,17 @@ struct Route {
   // w holds scores until weigh() has turned them into weights, where `raw`
 };
 constexpr int kWarps = kThreads / 32;
-__host__ __device__ inline int most_virtual(int R, int E, int nt) {
-  const int v = E + R / nt;
+__host__ __device__ inline int most_virtual(int R, int E, int nt_log) {
+  const int v = E + (R >> nt_log);
   return v < R ? v : R;
 }
-__host__ __device__ inline size_t route_bytes(int R, int E, int nt) {
-  const size_t half = 4 * static_cast<size_t>(R) + 3 * static_cast<size_t>(most_virtual(R, E, nt)) +
+__host__ __device__ inline size_t route_bytes(int R, int E, int nt_log) {
+  const size_t half = 4 * static_cast<size_t>(R) + 3 * static_cast<size_t>(most_virtual(R, E, nt_log)) +
                       (kWarps + 2) * static_cast<size_t>(E);
   return 4 * static_cast<size_t>(R) + (half * 2 + 15) / 16 * 16;
 }
-__device__ __forceinline__ Route route_at(uint8_t* p, int R, int E, int nt) {
-  const int V = most_virtual(R, E, nt);
+__device__ __forceinline__ Route route_at(uint8_t* p, int R, int E, int nt_log) {
+  const int V = most_virtual(R, E, nt_log);
   Route r;
   r.w = reinterpret_cast<float*>(p);
   uint16_t* q = reinterpret_cast<uint16_t*>(p + 4 * static_cast<size_t>(R));
@@ -463,8 +464,18 @@ struct Piece {
   int k0, k1;
 };
 
+// a / b for a below 2^24 and quotients below 2^20: the fast division is then off
+// by one at most.  (The compiler's own takes three times as many instructions,
+// and each role's first ones are fetched from far: with these, 2 us fewer lie
+// between the routing and the first rows asked for.)
+__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b) {
+  const uint32_t q = __float2uint_rz(__fdividef(__uint2float_rn(a), __uint2float_rn(b)));
+  const int r = static_cast<int>(a - q * b);
+  return r < 0 ? q - 1 : r >= static_cast<int>(b) ? q + 1 : q;
+}
+
 // One phase's tiles and blocks.  (At most 1056 virtual experts of 256 tiles; the
-// blocks cut into runs are of fewer tiles than CTAs: 32 bits hold all products.)
+// blocks cut into runs are of fewer tiles than CTAs: products stay below 2^24.)
 constexpr uint32_t kLeastBlocks = 4;  // of a run: shorter ones cost more to join than they save
 constexpr uint32_t kLeastClaims = 4;  // tiles for each CTA, for these to be claimed one by one
 struct Phase {
@@ -475,22 +486,22 @@ struct Phase {
   uint32_t waves;                    // else every CTA takes `waves` whole tiles
   uint32_t blocks, ctas;             // of the tiles behind them; the CTAs that take runs of these
   __device__ __forceinline__ Phase(int D, int F, uint32_t grid, int which, uint32_t entries) : grid(grid) {
-    kb = (which == 0 ? D : F) / kBlockK;
-    cols = which == 0 ? F / 64 : (D + kCols - 1) / kCols;
+    kb = static_cast<uint32_t>(which == 0 ? D : F) / kBlockK;
+    cols = static_cast<uint32_t>(which == 0 ? F : D + 64) / (which == 0 ? 64 : kCols);  // D: whole 64s
     tiles = entries * cols;
     claims = which == 1 && tiles >= kLeastClaims * grid;
-    waves = tiles / grid;
+    waves = quotient(tiles, grid);
     blocks = (tiles - waves * grid) * kb;
     ctas = min(grid, (blocks + kLeastBlocks - 1) / kLeastBlocks);
   }
-  __device__ __forceinline__ uint32_t run(uint32_t c) const { return blocks * c / ctas; }
+  __device__ __forceinline__ uint32_t run(uint32_t c) const { return quotient(blocks * c, ctas); }
   __device__ __forceinline__ bool whole(uint32_t tile) const { return claims || tile < waves * grid; }
   __device__ __forceinline__ void place(Piece& q) const;
   // the CTA whose run holds block b
-  __device__ __forceinline__ uint32_t owner(uint32_t b) const { return ((b + 1) * ctas - 1) / blocks; }
+  __device__ __forceinline__ uint32_t owner(uint32_t b) const { return quotient((b + 1) * ctas - 1, blocks); }
 };
 __device__ __forceinline__ void Phase::place(Piece& q) const {
-  q.v = q.tile / cols;
+  q.v = quotient(q.tile, cols);
   q.col = q.tile - q.v * cols;
 }
 // The CTA's pieces in their order.
@@ -509,7 +520,7 @@ struct Walk {
       q.k1 = static_cast<int>(f.kb);
       ++wave;
     } else if (b < end) {
-      const uint32_t t = b / f.kb;
+      const uint32_t t = quotient(b, f.kb);
       q.tile = f.waves * f.grid + t;
       q.k0 = static_cast<int>(b - t * f.kb);
       q.k1 = static_cast<int>(min(f.kb, q.k0 + (end - b)));
@@ -673,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int stage_bytes = kWeightStage + p.nt * kBlockK * 2;
   float* buf = reinterpret_cast<float*>(ring + p.stages * stage_bytes);
   Ctl& s = *reinterpret_cast<Ctl*>(reinterpret_cast<uint8_t*>(buf) + kBufBytes);
-  const Route r = route_at(reinterpret_cast<uint8_t*>(&s) + sizeof(Ctl), p.n * p.K, p.E, p.nt);
+  const Route r = route_at(reinterpret_cast<uint8_t*>(&s) + sizeof(Ctl), p.n * p.K, p.E, p.nt_log);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // set up by the last warps, while the first ones select
@@ -789,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int slot = r.list[r.vstart[q.v] + min(4 * lane + i, cnt - 1)];
-          row[i] = ph == 0 ? slot / p.K : slot;
+          row[i] = ph == 0 ? static_cast<int>(slot * p.k_inverse >> 16) : slot;
         }
         if (ph == 1) {
           const int32_t* flag = p.done + static_cast<int64_t>(q.v) * flags;
@@ -992,6 +1003,7 @@ bool map_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, u
 // Tokens of a tile at most.  Up to 64, so that a stage's rows leave 128 KB of
 // the ring to the weights; an expert with more tokens reads its weights again.
 int tile_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+int log_of(int nt) { return nt == 16 ? 4 : nt == 32 ? 5 : 6; }
 
 constexpr int kMaxGrid = 192;  // CTAs that the workspace has room for: no device of this kind has more SMs
 static_assert((32 + kMaxGrid) * 4 <= 1024, "counters and flags ahead of the tiles' flags");
@@ -1003,7 +1015,7 @@ struct Layout {
   size_t done, slots, gids, gw, h, y, part, all;
   explicit Layout(const moe_dims& d) {
     const size_t R = static_cast<size_t>(d.T) * d.K, nt = tile_tokens(d.T);
-    const size_t tiles = static_cast<size_t>(most_virtual(static_cast<int>(R), d.E, static_cast<int>(nt))) * (d.F / 64);
+    const size_t tiles = static_cast<size_t>(most_virtual(static_cast<int>(R), d.E, log_of(tile_tokens(d.T)))) * (d.F / 64);
     done = 1024;  // behind the two counters and the CTAs' flags
     slots = done + up(tiles * 4);
     gids = slots + up((R + 1) * 8);
@@ -1032,7 +1044,8 @@ cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   p.F = d.F;
   p.mode = c.mode;
   p.nt = tile_tokens(d.T);
-  p.nt_log = p.nt == 16 ? 4 : p.nt == 32 ? 5 : 6;
+  p.nt_log = log_of(p.nt);
+  p.k_inverse = static_cast<uint32_t>((65536 + d.K - 1) / d.K);
   p.type = c.type == MOE_BF16 ? 1u : 0u;
   p.status = c.dev_status;
   p.limit_ns = kDefaultWaitLimitNs;
@@ -1051,7 +1064,7 @@ cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   p.y = reinterpret_cast<float*>(ws + at.y);
   p.part = reinterpret_cast<float*>(ws + at.part);
   const size_t R = static_cast<size_t>(c.n) * d.K;
-  const size_t fixed = 1024 + kBufBytes + sizeof(Ctl) + route_bytes(static_cast<int>(R), d.E, p.nt);
+  const size_t fixed = 1024 + kBufBytes + sizeof(Ctl) + route_bytes(static_cast<int>(R), d.E, p.nt_log);
   const size_t stage = kWeightStage + static_cast<size_t>(p.nt) * kBlockK * 2;
   p.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemLimit - fixed) / stage));
   if (p.stages < kMinStages) return cudaErrorInvalidValue;

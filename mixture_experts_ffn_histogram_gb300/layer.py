@@ -553,8 +553,8 @@ class LowRankAdapters:
 
 class MoEDecode:
     """The whole expert layer for up to T tokens, a few (T <= 256): routing,
-    both expert products with SwiGLU and the weighted combine, in one kernel
-    that reads the weights of the experts named, once.
+    both expert products with SwiGLU and the weighted combine, in two kernels
+    that read the weights of the experts named, once.
 
     ``score_mode`` and the routing arguments are ``MoEBlock``'s: logits (and
     bias), or ids and w of a router's own (``SCORE_GIVEN``).  ``forward``

@@ -1,4 +1,4 @@
-"""The expert layer for a few tokens (one kernel) against its definition in 64
+"""The expert layer for a few tokens against its definition in 64
 bits: sizes, types, routings, and how it is called."""
 import pytest
 import torch
