@@ -169,6 +169,15 @@ __device__ __forceinline__ int cuts_of(int tiles, int grid, int kblocks) {
   return tiles > 0 ? max(1, min(grid / tiles, kblocks / kLeastCutBlocks)) : 1;
 }
 
+// Whether tiles are of few tokens, whose latency counts: their rows come by a TMA
+// gather for every four, and the CTA that stores a tile's last part joins them
+// (61 tokens of 64 adapters: 14.0 us against 15.9 the other way; 2000 of 1024: 100
+// against 125).  Else the epilogue's warps copy the rows, and parts are joined by
+// a kernel of their own (2000 tokens of 16 adapters: 18 against 23; 32768 of 16:
+// 73 against 87, since gathers keep to 31 bytes a ns and SM).
+constexpr int kFewTokens = 256;  // of a call: no kernel for parts
+__device__ __forceinline__ bool few_tokens(const PlanHead& h) { return h.n <= kFewTokens || h.live <= 32 * h.tiles; }
+
 struct ShrinkParams {
   const void* x;
   int64_t ldx;
@@ -180,7 +189,6 @@ struct ShrinkParams {
   float* parts;      // [cuts][live tokens][width], where there is more than one cut
   int32_t* arrived;  // [tile]: cuts whose part is stored; zero between calls
   const float* scale;
-  bool few;          // tokens: gathered by TMA, and parts joined here
   int n, slots, rank, width, kblocks, stages;  // width: rank in whole 16s
   uint32_t type;
   int32_t* status;
@@ -239,11 +247,11 @@ __device__ __forceinline__ bool epi_all(bool ok) {
   return r != 0;
 }
 
-// v of a tile from its parts.  Few tokens: by the 128 epilogue threads of the
+// v of a tile from its parts.  Tiles of few tokens: by the 128 epilogue threads of the
 // CTA that stored the last part, four neighbouring ranks of a token to a thread;
 // where there are fewer of those than threads, 2^k threads take the cuts in
 // turns and their sums are added in the threads' order.  (61 tokens: 1.2 us,
-// about a launch.)  Many tokens: by a kernel of its own, as wide as there are
+// about a launch.)  Others: by a kernel of its own, as wide as there are
 // values, since the last CTAs' 128 threads took 14 us of 73 for 8191 tokens.
 template <typename T>
 __device__ __forceinline__ void join_parts(const ShrinkParams& p, const PlanTile& tile, int live, int cuts, int tid,
@@ -293,11 +301,16 @@ constexpr int kJoinThreads = 256;
 // A block takes a tile at a time.
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) {
-  let_next_launch();
   const PlanHead head = *p.head;
   const int cuts = cuts_of(head.tiles, p.shrink_grid, p.kblocks);
+  const bool few = few_tokens(head), work = head.n == p.n && head.slots == p.slots && cuts > 1 && !few;
+  // Of tiles of few tokens, expand's blocks are better let in together once
+  // shrink's have gone than one by one between them (2000 tokens of 1024 adapters
+  // of rank 64: 188 us against 234; of rank 16: 100 against 99), of others the
+  // other way (32768 of 16: 73 against 75).
+  if (!few) let_next_launch();
   wait_for_previous();
-  if (head.n != p.n || head.slots != p.slots || cuts == 1) return;
+  if (!work) return;
   const int per_row = p.width / 4;
   const int64_t cut = static_cast<int64_t>(head.live) * per_row;
   const float4* parts = reinterpret_cast<const float4*>(p.parts);
@@ -320,7 +333,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
   }
 }
 
-// Many tokens: the four epilogue warps copy a tile's, wherever they lie, in
+// Tiles of many tokens: the four epilogue warps copy them, wherever they lie, in
 // 16-byte pieces (eight lanes to a row's 128 bytes, swizzled like a TMA box),
 // some stages ahead of telling the products: all stages but two, so that a
 // stage's products and the word that it is free again take their time while
@@ -398,6 +411,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   }
   const int cuts = cuts_of(head.tiles, gridDim.x, p.kblocks), units = head.tiles * cuts;
   if (static_cast<int>(blockIdx.x) >= units) return;
+  const bool few = few_tokens(head);
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int stage_bytes = kTokenStage + p.width * kBlockK * 2;
   ShrinkCtl& s = *reinterpret_cast<ShrinkCtl*>(ring + p.stages * stage_bytes);
@@ -405,7 +419,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   const int cols = tmem_width(p.width);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&s.full[i], p.few ? 1 : 1 + 4);  // warp 0, and the four warps that copy tokens
+      mbar_init(&s.full[i], few ? 1 : 1 + 4);  // warp 0, and the four warps that copy tokens
       mbar_init(&s.empty[i], 1);
     }
     mbar_init(&s.done, 1);
@@ -431,12 +445,12 @@ __global__ void __launch_bounds__(kShrinkThreads)
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const PlanTile tile = p.tiles[u / cuts];
-      // Few tokens: lane i gathers the tile's tokens 4i .. 4i + 3 (past the
+      // Tiles of few tokens: lane i gathers the tile's tokens 4i .. 4i + 3 (past the
       // last: the last again; their rows of the product are not stored).
-      const int groups = p.few ? (tile.count + 3) / 4 : 0;
+      const int groups = few ? (tile.count + 3) / 4 : 0;
       int row[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) row[i] = p.few ? __ldg(p.order + tile.start + min(4 * lane + i, tile.count - 1)) : 0;
+      for (int i = 0; i < 4; ++i) row[i] = few ? __ldg(p.order + tile.start + min(4 * lane + i, tile.count - 1)) : 0;
       Blocks blocks(u, cuts, p.kblocks);
       for (int i = 0; i < blocks.count; ++i, blocks.next()) {
         ok = warp_wait(&s.empty[stage], phase ^ 1u, wc);
@@ -499,7 +513,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
     int unit = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++unit) {
       const PlanTile tile = p.tiles[u / cuts];
-      const bool copied = p.few || copies.run(p, s, wc, tile, Blocks(u, cuts, p.kblocks));
+      const bool copied = few || copies.run(p, s, wc, tile, Blocks(u, cuts, p.kblocks));
       // the four warps meet at barriers below: all go on or none does
       if (!epi_all(copied && warp_wait(&s.done, unit & 1, wc))) break;
       tc_fence_after();
@@ -531,7 +545,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.drained);
-      if (cuts > 1 && p.few) {
+      if (cuts > 1 && few) {
         epi_sync();
         if (tid == 0) {  // releases the four warps' part, and acquires the others' where it is the last
           int before;
@@ -804,7 +818,7 @@ cudaError_t launch_shrink(const ShrinkParams& p, const CUtensorMap& mx, const CU
   if (err != cudaSuccess) return err;
   shrink_kernel<T><<<grid, kShrinkThreads, bytes, s>>>(mx, ma, p);
   const cudaError_t launched = cudaGetLastError();
-  if (launched != cudaSuccess || p.few) return launched;
+  if (launched != cudaSuccess || p.n <= kFewTokens) return launched;
   JoinParams j{};
   j.head = p.head;
   j.tiles = p.tiles;
@@ -897,11 +911,6 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   p.v = scratch + ws.v;
   p.parts = reinterpret_cast<float*>(scratch + ws.parts);
   p.scale = c.scale;
-  // Few tokens make tiles of few tokens, whose latency counts: a TMA gather for
-  // every four, no second kernel to join parts (61 tokens of 64 adapters: 14.0
-  // us against 15.9).  Many fill their tiles: gathers keep to 31 bytes a ns and
-  // SM, four warps' copies do not (32768 tokens: 87 us against 73).
-  p.few = c.n <= 256;
   p.n = c.n;
   p.slots = d.slots;
   p.rank = d.rank;

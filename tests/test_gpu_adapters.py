@@ -78,6 +78,7 @@ def test_the_plan(T, slots):
     (1, 64, 64, 1, 8, BF), (1, 7168, 2048, 8, 16, BF), (2, 72, 40, 3, 24, HF), (61, 2816, 2816, 64, 16, HF),
     (17, 512, 1000, 4, 128, BF), (300, 200, 136, 2, 40, BF), (128, 1024, 512, 1, 64, HF), (129, 8, 8, 1, 8, BF),
     (4097, 704, 2816, 5, 32, BF), (2000, 2048, 8, 300, 16, BF), (9000, 320, 520, 2, 64, BF),
+    (257, 1600, 96, 3, 24, HF), (300, 1992, 72, 40, 128, BF), (2000, 264, 136, 1024, 8, BF),
 ])
 @pytest.mark.parametrize("with_res", [False, True])
 def test_the_adapters(T, K, N, slots, rank, dt, with_res):
