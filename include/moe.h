@@ -691,11 +691,12 @@ moe_status moe_linear_bwd(moe_mat dy, moe_mat z, moe_mat x, moe_mat w, moe_mat d
  *   out[t]  = round(sum_{k ascending} w[t,k] * (h[t,k] . wo[ids[t,k]]) + res[t])
  *   x, res, out  `type` [n, D] (bf16 or fp16);  wi [E, D, 2F], wo [E, F, D]
  *                dense, of the same type; res.p may be NULL; out may be res's
- *                memory (same ld), not x's
+ *                memory (same ld), and x's
  *   logits  fp32 [n, E], bias fp32 [E] or NULL (both ignored for GIVEN)
  *   ids, w  int32 and fp32 [n, K]: in for GIVEN (a token may name an expert
  *           more than once), else out (either may be NULL).  logits, bias,
  *           ids, w and dev_status need only their elements' alignment.
+ *           A NaN among a token's scores is taken as 0, as there.
  *   n       tokens of this call, at most d.T
  * d.T is the capacity, which fixes the workspace's layout: T <= 256,
  * T * K <= 2048, K <= min(E, 32), E <= 1024; D and F multiples of 64 up to
@@ -786,7 +787,7 @@ moe_status moe_adapter_plan(const int32_t* ids, int32_t n, int32_t T, int32_t sl
  *   v = x[t] . a[s]^T  (fp32 sums),  y[t] = round(res[t] + round(scale[s] v) . b[s]^T),
  *   s = ids[t];  y[t] = res[t] where the token names none (res.p NULL: 0)
  *   x  `type` [n, K] (bf16 or fp16);  res, y  `type` [n, N], y may be res's
- *   memory (same ld);  a, b  dense, of the same type;  scale  fp32 [slots]
+ *   memory (same ld), and x's;  a, b  dense, of the same type;  scale  fp32 [slots]
  *   (4-byte aligned, as ids)
  * K, N and rank multiples of 8, rank <= 128.  plan: of d.T, d.slots and the
  * call's n tokens; one of another number of tokens or slots is reported as

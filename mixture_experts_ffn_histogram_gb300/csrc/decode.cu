@@ -245,11 +245,11 @@ __device__ __forceinline__ void select_token(const Params& p, int t, int lane, i
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = i * 32 + lane;
-    key[i] = 0u;  // below every score's (a NaN with all bits set apart, which counts as this)
+    key[i] = 0u;  // below every score's; a NaN is taken as 0, like the block's routing takes it
     if (e < p.E) {
       float s = __ldg(row + e);
       if (p.bias != nullptr) s = __fadd_rn(s, __ldg(p.bias + e));
-      key[i] = max(order_of(s), 1u);
+      key[i] = order_of(s == s ? s : 0.0f);
     }
   }
   uint32_t mine = 0u;

@@ -187,3 +187,40 @@ def test_one_bad_token_leaves_the_others():
     keep = [t for t in range(T) if t not in (5, 40)]
     assert torch.equal(got[keep], want[keep])
     assert bool(torch.isnan(got[5]).all()) and not bool(torch.isfinite(got[40]).any())
+
+
+@pytest.mark.parametrize("T,slots", [(30, 4), (700, 9), (900, 300)])
+def test_a_layer_on_its_own_result_and_in_a_graph(T, slots):
+    """The result of a call is the rows, and the residual, of the next; one by
+    one and captured, with the plan of other ids for each replay."""
+    need_gpu()
+    K, rank = 328, 24
+    d = _data(T, K, K, slots, rank, HF, T)
+    batch, op = _ops(T, K, K, slots, rank, HF)
+    ids, x = d["ids"].clone(), d["x"].clone()
+
+    def step(a, res):
+        return op.forward(batch, a, d["a"], d["b"], d["scale"], res=res)
+
+    def chain():
+        batch.group(ids)
+        y = step(x, d["res"])
+        return step(y, y)
+
+    want = []
+    cases = [d["ids"], d["ids"].flip(0).contiguous(), torch.full_like(ids, slots - 1)]
+    for i in cases:
+        batch.group(i)
+        y = step(x, d["res"]).clone()
+        want.append(step(y, y).clone())
+        ids.copy_(i)
+        assert torch.equal(chain(), want[-1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = chain()
+    for i, ref in zip(cases, want):
+        ids.copy_(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref)
+    assert int(op.status.item()) == 0

@@ -240,3 +240,30 @@ def test_another_stream_and_a_graph():
     torch.cuda.synchronize()
     for a, b in zip(want, (op.u, op._dres, op.dpost)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows,D,dt", [(300, 256, BF), (2500, 301, BF), (40, 33, F32), (3, 7168, HF)])
+def test_norms_on_their_own_results(rows, D, dt):
+    """The stream and the normalised rows of a call are res and y of the next;
+    backward, dres and dy are dr and du of the one before."""
+    need_gpu()
+    from mixture_experts_ffn_histogram_gb300.layer import BlockNorm
+    for parts in (("po", "pr", "ga", "to"), ("pr",)):
+        d, w = _data(rows, D, dt, F32, parts, rows)
+        op = BlockNorm(rows, D, dtype=dt, scale=0.5)
+        op.forward(d["res"], d["y"], **w)
+        r, u = op.r.clone(), op.u.clone()
+        op.forward(r, u, **w)
+        want = [op.r.clone(), op.u.clone()]
+        ry, rr = op.rstd_y, op.rstd_r
+        saved = dict(r=want[0], y=u, **w, rstd_y=None if ry is None else ry.clone(), rstd_r=rr.clone())
+        op.forward(d["res"], d["y"], **w)
+        op.forward(op.r, op.u, **w)
+        assert torch.equal(op.r, want[0]) and torch.equal(op.u, want[1])
+        op.backward(d["du"], d["dr"], **saved)
+        dr, du = op._dres.clone(), op.dy.clone()
+        want = [op.backward(du, dr, **saved).clone(), op.dy.clone(), op.dpre.clone()]
+        op.backward(d["du"], d["dr"], **saved)
+        got = op.backward(op.dy, op._dres, **saved)
+        for a, b in zip((got, op.dy, op.dpre), want):
+            assert torch.equal(a, b)

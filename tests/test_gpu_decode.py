@@ -238,3 +238,46 @@ def test_two_layers_at_once_and_among_other_kernels():
     torch.cuda.synchronize()
     assert [int(op.status.item()) for op in ops] == [0, 0, 0]
     assert int(wrong.item()) == 0
+
+
+@pytest.mark.parametrize("T", [9, 40])   # selected by every block, and exchanged between them
+@pytest.mark.parametrize("mode", ["softmax", "sigmoid"])
+def test_odd_scores_select_as_the_block_does(T, mode):
+    """Rows with NaN and infinities, all masked or all equal: the ids and weights
+    of the block's routing."""
+    need_gpu()
+    from mixture_experts_ffn_histogram_gb300 import binding as B
+    D, E, K, F = 64, 70, 6, 64
+    d = _data(T, D, E, K, F, BF, 13)
+    l, inf = d["logits"], float("inf")
+    l[0], l[1, 3], l[2, 5], l[3] = -inf, float("nan"), inf, float("nan")
+    l[4, 4:], l[5], l[6, :10], l[7, 66:] = -inf, torch.finfo(torch.float32).min, inf, float("nan")
+    l[8] = 200.0 * l[8]
+    op = _op(T, D, E, K, F, mode)
+    dims = B.dims(T, D, E, K, F)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids, w = torch.empty(T, K, **i32), torch.empty(T, K, device="cuda")
+    ws = torch.zeros(B.moe_workspace_bytes(dims), dtype=torch.uint8, device="cuda")
+    for bias in (d["bias"], None):
+        op.forward(d["x"], d["wi"], d["wo"], logits=l, bias=bias)
+        B.moe_route_histogram(l, bias, MODES[mode], ids, w, torch.empty(E, **i32), torch.empty(E + 1, **i32),
+                              torch.empty(T, K, **i32), torch.empty(T * K, **i32), torch.zeros(1, **i32), ws, dims)
+        torch.cuda.synchronize()
+        assert torch.equal(op.ids, ids) and int(op.status.item()) == 0
+        # each is within its own bound of the exact weight
+        assert torch.allclose(op.w, w, rtol=2 * (K + 12) * 2.0 ** -24, atol=2.0 ** -126, equal_nan=True)
+
+
+def test_the_layer_on_its_own_result():
+    """The result of a call is the rows, and the residual, of the next."""
+    need_gpu()
+    for T in (1, 7, 90):
+        d = _data(T, 192, 12, 3, 128, BF, T)
+        op = _op(T, 192, 12, 3, 128, "softmax")
+
+        def step(x, res):
+            return op.forward(x, d["wi"], d["wo"], logits=d["logits"], res=res)
+
+        first = step(d["x"], None).clone()
+        want = step(first, first).clone()
+        assert torch.equal(step(step(d["x"], None), op._out), want)
