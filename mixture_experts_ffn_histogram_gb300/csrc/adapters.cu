@@ -21,8 +21,10 @@
 //
 // v is summed in fp32 (over the cuts in a fixed order, by the CTA that stores a
 // tile's last part) and rounded once, with the scale, to the operands' type for
-// the second product: half a step on each of r terms, below the result's own
-// rounding.
+// the second product, as a layer of the model would hand it on: half a step on
+// each of r terms, together about what the result's own rounding is.  (What that
+// leaves, kept as a second part with products of its own: 73 to 77 us for 32768
+// tokens of rank 32, 52 to 55 for 8191 of rank 64, 118 to 141 for 16000 of 128.)
 #include <cuda.h>
 
 #include <algorithm>
