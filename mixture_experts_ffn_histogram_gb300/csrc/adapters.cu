@@ -615,7 +615,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // a time.  The next unit's part of res is on its way into the threads' own
 // slots of shared memory meanwhile (64 KB to an SM; one unit to a block, with
 // its loads, its products and its stores one after another, took 60 us where
-// this takes 40, at 32768 tokens of 1536 columns), and so is v where the tokens
+// this takes 36, at 32768 tokens of 1536 columns), and so is v where the tokens
 // change.  In a fragment, lane 4 g + q holds reduction elements 4 q .. 4 q + 3 of
 // each 16 (in both operands), and the columns 8 q .. 8 q + 7 of rows g and g + 8:
 // column c of the j-th of its four MMAs is column 8 (c / 2) + 2 j + c % 2 of the
@@ -713,9 +713,11 @@ __global__ void __launch_bounds__(kExpandThreads, KB > 4 ? 3 : kExpandBlocks) ex
       }
     }
     fetch(buffer ^ 1);
-    // Full tiles' b comes as soon as the unit before has done with its own; of
-    // few tokens, where it comes from HBM, it is better asked for after res.
-    // (32768 tokens of 16 adapters 69 us, 73 all here; 2000 of 1024 97, 106 the other way.)
+    // Past rank 16, full tiles' b comes as soon as the unit before has done with
+    // its own (32768 tokens of rank 32 69 us, 73 all here); of few tokens, where it
+    // comes from HBM, it is better asked for after res (2000 of 1024 adapters 97
+    // us, 106 the other way); of rank 16 the further code costs as much as it gives
+    // (61 tokens 13.5 us against 14.3 with it, 32000 98 against 96).
     if (named && count > 0 && (!early || u == u0)) load_b(adapter, c0);
     cp_async_wait_group<1>();
     if (first) __syncthreads();  // the same for the whole block
