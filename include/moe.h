@@ -91,7 +91,8 @@ typedef struct {
 
 typedef enum {
   MOE_SCORE_SOFTMAX_TOPK = 0, /* w = softmax over the K selected scores */
-  MOE_SCORE_SIGMOID_NORM = 1, /* w = sigmoid(selected) / sum of the K sigmoids */
+  MOE_SCORE_SIGMOID_NORM = 1, /* w = sigmoid(selected) / sum of the K sigmoids; the shares
+                                 hold where the sigmoids are too small for fp32 */
   MOE_SCORE_GIVEN = 2         /* ids and w are inputs; only the histogram runs */
 } moe_score_mode;
 

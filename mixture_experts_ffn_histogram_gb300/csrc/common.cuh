@@ -423,6 +423,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 __device__ __forceinline__ float bf16lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
+// ------------------------------------------------------- routing weights
+// sigmoid(l) e^-base for weights that are shares of such scores, base being 0
+// or below -kDeep: a sigmoid that deep is e^l to fp32's precision, down to the
+// smallest numbers, and shares of deep ones are taken relative to the largest.
+constexpr float kDeep = 64.0f;
+__device__ __forceinline__ float sigmoid_num(float l, float base) {
+  return l < -kDeep ? expf(l - base) : 1.0f / (1.0f + expf(-l));
+}
+
 // ------------------------------------------------------- SwiGLU backward
 __device__ __forceinline__ float sigmoid_fast(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 

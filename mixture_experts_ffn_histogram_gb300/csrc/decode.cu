@@ -289,7 +289,8 @@ __device__ __forceinline__ void select_one(const Params& p, int t, int lane, int
 __device__ __forceinline__ float weigh(const Params& p, float v, int lane) {
   const float first = __shfl_sync(0xffffffffu, v, 0);
   float ex = 0.0f;
-  if (lane < p.K) ex = p.mode == MOE_SCORE_SOFTMAX_TOPK ? expf(v - first) : 1.0f / (1.0f + expf(-v));
+  if (lane < p.K)
+    ex = p.mode == MOE_SCORE_SOFTMAX_TOPK ? expf(v - first) : sigmoid_num(v, first < -kDeep ? first : 0.0f);
   float sum = 0.0f;  // in the slots' order
   for (int k = 0; k < p.K; ++k) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, ex, k));
   return __fdiv_rn(ex, sum);

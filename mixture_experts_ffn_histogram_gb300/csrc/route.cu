@@ -316,11 +316,11 @@ __device__ __forceinline__ long select_slots(const float* __restrict__ logits,
     const int my_e = key_expert(mine);
     // routing weights of the K selected scores; slot 0 holds the largest
     float ex = 0.f;
+    const float m = key_score(top[0]);
     if (mode == MOE_SCORE_SOFTMAX_TOPK) {
-      const float m = key_score(top[0]);
       if (gl < K) ex = expf(my_v - m);
     } else {
-      if (gl < K) ex = 1.0f / (1.0f + expf(-my_v));
+      if (gl < K) ex = sigmoid_num(my_v, m < -kDeep ? m : 0.0f);
     }
     float sum = 0.f;  // ascending slot order
     for (int k = 0; k < K; ++k) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, ex, gbase + k));

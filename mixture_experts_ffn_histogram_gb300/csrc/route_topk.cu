@@ -88,15 +88,9 @@ __device__ __forceinline__ float soft_num(float l, float m) {
 // for the sigmoid, the row's largest logit for the softmax), the scores are
 // taken relative to the largest chosen one instead, which leaves the shares as
 // they are.
-constexpr float kDeep = 64.0f;
 __device__ __forceinline__ bool shallow(float l, float base) { return l - base >= -kDeep || l == base; }
 __device__ __forceinline__ float deep_base(float most, float base) {
   return most > kNegInf && base < INFINITY ? most : base;
-}
-// sigmoid(l) e^-base, base being 0 or below -kDeep (there the sigmoid is e^l to
-// fp32's precision, down to the smallest numbers).
-__device__ __forceinline__ float sigmoid_num(float l, float base) {
-  return l < -kDeep ? expf(l - base) : 1.0f / (1.0f + expf(-l));
 }
 
 // Largest value over the warp, in one instruction (no NaN among them).

@@ -74,7 +74,8 @@ int oracle_num_threads(void) {
 #endif
 }
 
-static float sigmoidf_(float v) { return 1.0f / (1.0f + expf(-v)); }
+/* (Below -64 the sigmoid is e^v to fp32's precision, down to the smallest numbers.) */
+static float sigmoidf_(float v) { return v < -64.0f ? expf(v) : 1.0f / (1.0f + expf(-v)); }
 
 /* Step 1, routing [Gemma4 L/M row 6]: per token, the K largest scores in
  * descending order (ties: lower expert id first), and their weights:
@@ -107,6 +108,9 @@ int oracle_route(const float* logits, const float* bias, int mode, int T, int E,
     float sum = 0.0f;
     float* v = w + (size_t)t * K;
     if (mode == ORACLE_SOFTMAX_TOPK) {
+      float m = s[ids[(size_t)t * K]];
+      for (int k = 0; k < K; ++k) { v[k] = expf(s[ids[(size_t)t * K + k]] - m); sum = sum + v[k]; }
+    } else if (s[ids[(size_t)t * K]] < -64.0f) {  /* all are: shares relative to the largest */
       float m = s[ids[(size_t)t * K]];
       for (int k = 0; k < K; ++k) { v[k] = expf(s[ids[(size_t)t * K + k]] - m); sum = sum + v[k]; }
     } else {
