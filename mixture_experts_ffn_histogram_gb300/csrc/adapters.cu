@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kExpandThreads, KB > 4 ? 3 : kExpandBlocks) ex
       row_next[i] = 8 * i + g < count_next ? p.order[tile_next.start + 8 * i + g] : -1;
   };
   // v of the next unit's tokens, by the whole block: 16-byte pieces of rows, and
-  // zeros past the ranks that there are
+  // zeros past the ranks that there are (v holds an infinite row's x times 0 there)
   const auto fetch_v = [&](int half) {
     constexpr int kRow = 2 * KB;  // pieces
     const bool named = t_next / p.halves < head.tiles;
@@ -656,8 +656,8 @@ __global__ void __launch_bounds__(kExpandThreads, KB > 4 ? 3 : kExpandBlocks) ex
       const int r = i / kRow, e = i % kRow * 8;
       cp_async16_zfill(vs + (half * kExpandTokens + r) * kWords + e / 2,
                        static_cast<const T*>(p.v) + static_cast<int64_t>(tile_next.start + r) * p.width +
-                           (e < p.width ? e : 0),
-                       e < p.width ? 16 : 0);
+                           (e < p.rank ? e : 0),
+                       e < p.rank ? 16 : 0);
     }
   };
   const auto fetch = [&](int buffer) {  // the next unit's part of res
