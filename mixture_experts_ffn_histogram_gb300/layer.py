@@ -89,6 +89,17 @@ def _own(t):
     return B.MoeMat(t.data_ptr(), t.stride(0))
 
 
+def _zeros(size, dtype, dev):
+    """A buffer that holds zeros for a call on whatever stream: the fill has
+    ended.  (While a graph is captured it is part of that graph.)"""
+    t = torch.zeros(size, dtype=dtype, device=dev)
+    if t.is_cuda:
+        with torch.cuda.device(t.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+    return t
+
+
 _NO = B.MoeMat(None, 0)     # a matrix that is not given
 
 
@@ -408,7 +419,7 @@ class Linear:
         dev = torch.device(device)
         self._y = torch.empty((M, N), dtype=out_dtype, device=dev)
         self.device = dev = self._y.device
-        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.status = _zeros(1, torch.int32, dev)
         self.z = self._z = None
         self._mz = _NO
         self._my, self._p_status = _own(self._y), self.status.data_ptr()
@@ -483,9 +494,9 @@ class AdapterBatch:
             raise ValueError(f"unsupported sizes: T={T}, slots={slots} (T <= 2^20, 1 <= slots <= 1024)")
         self.T, self.slots, self.n = T, slots, None
         dev = torch.device(device)
-        self.plan = torch.zeros(need, dtype=torch.uint8, device=dev)
+        self.plan = _zeros(need, torch.uint8, dev)
         self.device = dev = self.plan.device
-        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.status = _zeros(1, torch.int32, dev)
         self._ids = _Arg("ids", torch.int32, dev, contiguous=True)
         self._p_plan, self._p_status = self.plan.data_ptr(), self.status.data_ptr()
         self._fwd = _entry("moe_adapter_plan", dev)
@@ -525,8 +536,8 @@ class LowRankAdapters:
         dev = torch.device(device)
         self._y = torch.empty((T, N), dtype=dtype, device=dev)
         self.device = dev = self._y.device
-        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+        self.status = _zeros(1, torch.int32, dev)
+        self.ws = _zeros(need, torch.uint8, dev)
         self._my, self._p_status, self._p_ws = _own(self._y), self.status.data_ptr(), self.ws.data_ptr()
         self._x, self._res = _Arg("x", dtype, dev), _Arg("res", dtype, dev)
         self._a, self._b = (_Arg(n, dtype, dev, contiguous=True) for n in ("a", "b"))
@@ -579,8 +590,8 @@ class MoEDecode:
         dev = torch.device(device)
         self._out = torch.empty((T, D), dtype=dtype, device=dev)
         self.device = dev = self._out.device
-        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+        self.status = _zeros(1, torch.int32, dev)
+        self.ws = _zeros(need, torch.uint8, dev)
         self._given = score_mode == B.SCORE_GIVEN
         self.ids = self.w = None
         if not self._given:
