@@ -707,6 +707,10 @@ class DecodeLayer:
         r' = r + branch * norm(m) (post + offset)        (BlockNorm)
         u' = norm(r') (pre + offset)
 
+    With ``SCORE_GIVEN`` a router of its own selects (``TopKRouter``, say, on
+    logits of any number of experts): ``forward`` takes its ids and w, there is
+    no gate and no wr.
+
     ``forward`` takes the residual stream r and u, its norm, and returns both
     behind the layer (views of the norm's buffers, ``norm.r`` and ``norm.u``)."""
 
@@ -715,22 +719,30 @@ class DecodeLayer:
 
     def __init__(self, T, D, E, K, F, shared, score_mode=B.SCORE_SOFTMAX_TOPK, act="silu",
                  dtype=torch.bfloat16, eps=1e-6, branch=1.0, offset=0.0, slots=0, rank=8, device="cuda"):
-        self.gate = Linear(T, D, E, dtype, torch.float32, device=device)
+        self.gate = None if score_mode == B.SCORE_GIVEN else Linear(T, D, E, dtype, torch.float32, device=device)
         self.up = Linear(T, D, shared, dtype, act=act, device=device)
         self.down = Linear(T, shared, D, dtype, device=device)
         self.adapters = LowRankAdapters(T, shared, D, slots, rank, dtype, device) if slots else None
         self.experts = MoEDecode(T, D, E, K, F, score_mode, dtype, device)
         self.norm = BlockNorm(T, D, dtype, torch.float32, eps, branch, offset, train=False, device=device)
 
-    def forward(self, r, u, weights, bias=None, batch=None, stream=None):
+    def forward(self, r, u, weights, bias=None, batch=None, ids=None, w=None, stream=None):
         g = weights
         if batch is not None and self.adapters is None:
             raise ValueError("the layer was built without adapters (slots=0)")
-        logits = self.gate.forward(u, g["wr"], stream=stream)
+        if self.gate is None:
+            if ids is None or w is None or bias is not None:
+                raise ValueError("the layer was built for a given selection: it needs ids and w, and no bias")
+            logits = None
+        elif ids is not None or w is not None:
+            raise ValueError("the layer selects the experts itself: no ids or w")
+        else:
+            logits = self.gate.forward(u, g["wr"], stream=stream)
         h = self.up.forward(u, g["w1"], g["b1"], stream=stream)
         s = self.down.forward(h, g["w2"], g["b2"], stream=stream)
         if batch is not None:
             s = self.adapters.forward(batch, h, g["a"], g["b"], g["scale"], res=s, stream=stream)
-        m = self.experts.forward(u, g["wi"], g["wo"], logits=logits, bias=bias, res=s, stream=stream)
+        m = self.experts.forward(u, g["wi"], g["wo"], logits=logits, bias=bias, ids=ids, w=w, res=s,
+                                 stream=stream)
         u = self.norm.forward(r, m, g["post"], g["pre"], stream=stream)
         return self.norm.r, u
