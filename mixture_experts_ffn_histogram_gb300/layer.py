@@ -225,6 +225,8 @@ class BlockNorm:
                  offset=0.0, train=True, device="cuda"):
         if dtype not in B.DTYPES or weight_dtype not in (dtype, torch.float32):
             raise ValueError(f"rows of {dtype} with weights of {weight_dtype} are not supported")
+        if not 1 <= D <= 8192:
+            raise ValueError(f"unsupported sizes: D={D} (1 <= D <= 8192)")
         self.rows, self.D, self.dtype, self.weight_dtype, self.train = rows, D, dtype, weight_dtype, train
         self.d = B.block_norm_dims(rows, D, dtype, weight_dtype, eps, scale, offset)
         dev = torch.device(device)
@@ -712,7 +714,8 @@ class DecodeLayer:
     no gate and no wr.
 
     ``forward`` takes the residual stream r and u, its norm, and returns both
-    behind the layer (views of the norm's buffers, ``norm.r`` and ``norm.u``)."""
+    behind the layer (views of the norm's buffers, ``norm.r`` and ``norm.u``).
+    D is ``BlockNorm``'s, up to 8192."""
 
     WEIGHTS = ("wr", "wi", "wo", "w1", "b1", "w2", "b2", "post", "pre")
     ADAPTERS = ("a", "b", "scale")
