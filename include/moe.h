@@ -699,6 +699,9 @@ moe_status moe_linear_bwd(moe_mat dy, moe_mat z, moe_mat x, moe_mat w, moe_mat d
  *           ids, w and dev_status need only their elements' alignment.
  *           A NaN among a token's scores is taken as 0, as there.
  *   n       tokens of this call, at most d.T
+ * h is held in `type`: in fp16 an |h| of 65520 or more becomes infinite, and
+ * the token's out with it, also where the sum that follows would be in range
+ * (bf16 has fp32's).
  * d.T is the capacity, which fixes the workspace's layout: T <= 256,
  * T * K <= 2048, K <= min(E, 32), E <= 1024; D and F multiples of 64 up to
  * 16384.  An id outside [0, E) is reported as MOE_ERR_DEVICE and its slot
@@ -790,6 +793,8 @@ moe_status moe_adapter_plan(const int32_t* ids, int32_t n, int32_t T, int32_t sl
  *   x  `type` [n, K] (bf16 or fp16);  res, y  `type` [n, N], y may be res's
  *   memory (same ld), and x's;  a, b  dense, of the same type;  scale  fp32 [slots]
  *   (4-byte aligned, as ids)
+ * scale v is held in `type`: in fp16 65520 or more becomes infinite, and the
+ * token's y with it (bf16 has fp32's range).
  * K, N and rank multiples of 8, rank <= 128.  plan: of d.T, d.slots and the
  * call's n tokens; one of another number of tokens or slots is reported as
  * MOE_ERR_DEVICE, and y is left as it was.

@@ -524,7 +524,8 @@ class LowRankAdapters:
     narrower ones padded with zeros): a [slots, rank, K], b [slots, N, rank]
     in bf16 or fp16 like the rows, scale fp32 [slots].  ``batch`` is an
     ``AdapterBatch`` of the same T and slots, grouped for these tokens on the
-    same stream or before.  ``status`` is the kernels' error word."""
+    same stream or before.  ``status`` is the kernels' error word.  In fp16 a
+    scale[s] x a[s]^T of 65520 or more is infinite; bf16 has fp32's range."""
 
     def __init__(self, T, K, N, slots, rank, dtype=torch.bfloat16, device="cuda"):
         if dtype not in (torch.bfloat16, torch.float16):
@@ -573,8 +574,9 @@ class MoEDecode:
     bias), or ids and w of a router's own (``SCORE_GIVEN``).  ``forward``
     returns out = experts(x) + res for bf16 or fp16 rows; ``ids`` and ``w``
     hold the selection.  ``status`` is MoEBlock's: an id outside [0, E) is
-    reported there and its slot dropped.  Longer batches and training:
-    ``MoEBlock``."""
+    reported there and its slot dropped.  In fp16 an inner value (silu of the
+    gate times up) of 65520 or more is infinite; bf16 has fp32's range.  Longer
+    batches and training: ``MoEBlock``."""
 
     def __init__(self, T, D, E, K, F, score_mode=B.SCORE_SOFTMAX_TOPK, dtype=torch.bfloat16,
                  device="cuda"):
