@@ -208,18 +208,6 @@ struct ShrinkCtl {
 };
 __host__ __device__ constexpr int tmem_width(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : 128; }
 
-// Four rows of a map whose box is 64 columns of one row, into 512 consecutive
-// bytes (swizzled by their address like any tile).
-__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
-                                        const int (&r)[4]) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-      "r"(r[3])
-      : "memory");
-}
-
 // The reduction blocks of unit u, in the order in which they are read: every
 // so manieth, from another one on for each unit.
 struct Blocks {
@@ -233,21 +221,6 @@ struct Blocks {
     if (kb >= kblocks) kb = first;
   }
 };
-
-// Barriers of the four epilogue warps; the second tells whether all had `ok`.
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool epi_all(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(ok ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
 
 // v of a tile from its parts.  Tiles of few tokens: by the 128 epilogue threads of the
 // CTA that stored the last part, four neighbouring ranks of a token to a thread;
@@ -781,16 +754,6 @@ __global__ void __launch_bounds__(kExpandThreads, KB > 4 ? 3 : kExpandBlocks) ex
 }
 
 // --------------------------------------------------------------- host side
-// Rows of x for four-row gathers.
-bool map_tokens(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[2] = {inner, rows}, strides[1] = {ld * 2};
-  const cuuint32_t box[2] = {64, 1}, es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 // The pool [slots][rank][K] in boxes of 64 elements of all of an adapter's
 // rows; rows past the rank and elements past K read as zero.
 bool map_pool(CUtensorMap* m, const void* base, uint64_t K, uint64_t rank, uint64_t slots, uint32_t width) {
@@ -930,7 +893,7 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   p.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kShrinkSmem - 1024 - sizeof(ShrinkCtl)) / stage));
   const size_t bytes = 1024 + p.stages * stage + sizeof(ShrinkCtl);
   CUtensorMap mx, ma;
-  if (!map_tokens(&mx, c.x, d.K, c.n, c.ldx) || !map_pool(&ma, c.a, d.K, d.rank, d.slots, p.width)) return cudaErrorInvalidValue;
+  if (!map_rows(&mx, c.x, d.K, c.n, c.ldx) || !map_pool(&ma, c.a, d.K, d.rank, d.slots, p.width)) return cudaErrorInvalidValue;
   // no more CTAs than units of the fewest blocks
   const int grid = static_cast<int>(std::min<int64_t>(
       2 * std::min(sm_count(), kMostSms), most * std::max(1, p.kblocks / kLeastCutBlocks)));

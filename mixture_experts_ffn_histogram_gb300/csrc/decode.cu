@@ -170,21 +170,6 @@ __device__ __forceinline__ void st_release(int32_t* p, int v) {
 __device__ __forceinline__ void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
-// Barriers of the four epilogue warps; the second tells whether all had `ok`.
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool epi_all(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(ok ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
-
 // Adds to a counter; what this thread has seen written is written before, and
 // what others had written before they added is seen after.
 __device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
@@ -212,18 +197,6 @@ __device__ __forceinline__ bool wait_for(const int32_t* at, int want, const Wait
 // A slot as the combine reads it: its virtual expert, its row there, and
 // whether it names an expert at all.
 __device__ __forceinline__ uint32_t slot_word(uint32_t v, uint32_t row) { return 0x80000000u | row << 16 | v; }
-
-// Four rows of a map whose box is 64 columns of one row, into 512 consecutive
-// bytes (swizzled by their address like any tile).
-__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
-                                        const int (&r)[4]) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-      "r"(r[3])
-      : "memory");
-}
 
 // A score as an unsigned number of the same order (-0 as +0).
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -988,16 +961,6 @@ bool map3(CUtensorMap* m, const void* base, uint64_t inner, uint64_t mid, uint64
   const cuuint32_t box[3] = {64, kBlockK, 1}, es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// 16-bit rows for four-row gathers: a box is 64 columns of one row.
-bool map_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[2] = {inner, rows}, strides[1] = {ld * 2};
-  const cuuint32_t box[2] = {64, 1}, es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
