@@ -191,7 +191,7 @@ struct ShrinkParams {
   float* parts;      // [cuts][live tokens][width], where there is more than one cut
   int32_t* arrived;  // [tile]: cuts whose part is stored; zero between calls
   const float* scale;
-  int n, slots, rank, width, kblocks, stages;  // width: rank in whole 16s
+  int n, slots, width, kblocks, stages;  // width: rank in whole 16s
   uint32_t type;
   int32_t* status;
   uint64_t limit_ns;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
       tc_fence_after();
       const int64_t at = static_cast<int64_t>(tile.start + tid) * p.width;
       const float scale = __ldg(p.scale + tile.adapter);
-      for (int c0 = 0; c0 < p.width; c0 += 16) {  // ranks past the last are zero, like their rows of a
+      for (int c0 = 0; c0 < p.width; c0 += 16) {  // ranks past the last: sums of x times 0
         uint32_t v[16];
         tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0, v);
         tmem_ld_wait();
@@ -883,7 +883,6 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   p.scale = c.scale;
   p.n = c.n;
   p.slots = d.slots;
-  p.rank = d.rank;
   p.width = (d.rank + 15) / 16 * 16;
   p.kblocks = (d.K + kBlockK - 1) / kBlockK;
   p.type = d.type == MOE_BF16 ? 1u : 0u;

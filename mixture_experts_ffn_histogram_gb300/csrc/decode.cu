@@ -118,12 +118,11 @@ struct Ctl {
 // nt slots makes several entries of the list that the tiles follow ("virtual
 // experts").
 struct Route {
-  float* w;                                  // [R]
+  float* w;  // [R]: block 0's weights, or (all blocks', up to kWarps tokens that select) scores
   uint16_t *expert, *rank, *at, *list;       // [R]; at: the slot's virtual expert
   uint16_t *vexp, *vstart, *vcnt;            // [V]
   uint16_t* before;                          // [warps][E]: slots of the expert in the warps ahead
   uint16_t *first, *start;                   // [E]: its first virtual expert, its place in the list
-  // w holds scores until weigh() has turned them into weights, where `raw`
 };
 constexpr int kWarps = kThreads / 32;
 __host__ __device__ inline int most_virtual(int R, int E, int nt_log) {
@@ -269,7 +268,7 @@ __device__ __forceinline__ float weigh(const Params& p, float v, int lane) {
   return __fdiv_rn(ex, sum);
 }
 
-// Everyone's selection in r.expert and r.w.  Up to a token for each of its warps a
+// Everyone's selection in r.expert (and block 0's r.w).  Up to a token for each of its warps a
 // CTA selects all for itself (and leaves the scores in r.w: only the combine
 // needs weights, and that is far off); of more tokens each CTA selects its own, and they
 // exchange them through global memory (128 tokens of 128 experts: 42 us when
@@ -282,7 +281,7 @@ __device__ __forceinline__ bool select_all(const Params& p, const Route& r, cons
       const int e = __ldg(p.ids_in + j);
       const bool in = e >= 0 && e < p.E;
       r.expert[j] = in ? static_cast<uint16_t>(e) : kNone;
-      r.w[j] = __ldg(p.w_in + j);
+      if (blockIdx.x == 0) r.w[j] = __ldg(p.w_in + j);
       if (!in && blockIdx.x == 0) report(p.status, MOE_ERR_DEVICE);
     }
   } else if (p.n <= kWarps) {
@@ -315,7 +314,7 @@ __device__ __forceinline__ bool select_all(const Params& p, const Route& r, cons
     ok = __syncthreads_and(ok);
     for (int j = threadIdx.x; j < R && ok; j += kThreads) {
       r.expert[j] = static_cast<uint16_t>(__ldcg(p.gids + j));
-      r.w[j] = __ldcg(p.gw + j);
+      if (blockIdx.x == 0) r.w[j] = __ldcg(p.gw + j);
     }
   }
   return ok;
@@ -411,25 +410,22 @@ __device__ __forceinline__ uint32_t word_of(const Route& r, int j) {
   return r.expert[j] != kNone ? slot_word(r.at[j], r.rank[j]) : 0u;
 }
 
-// What is left of the routing once the tiles are known, by the epilogue's warps
-// while there is nothing to finish: weights, and (block 0) the caller's copies
-// and the combine's table.
+// What is left of the routing once the tiles are known, by block 0's epilogue
+// warps while there is nothing to finish: weights, the caller's copies and the
+// combine's table.
 __device__ __forceinline__ void finish_routing(const Params& p, const Route& r, int entries, int ew, int lane) {
-  const bool raw = p.mode != MOE_SCORE_GIVEN && p.n <= kWarps, block0 = blockIdx.x == 0;
-  if (!raw && !block0) return;
+  const bool raw = p.mode != MOE_SCORE_GIVEN && p.n <= kWarps;  // r.w holds scores
+  if (blockIdx.x != 0) return;
   for (int t = ew; t < p.n; t += 4) {
     const int j = t * p.K + lane;
     float w = lane < p.K ? r.w[j] : 0.0f;
     if (raw) w = weigh(p, w, lane);
     if (lane >= p.K) continue;
-    if (raw) r.w[j] = w;
-    if (block0) {
-      p.slots[j] = make_uint2(word_of(r, j), __float_as_uint(w));
-      if (raw && p.ids_out != nullptr) p.ids_out[j] = r.expert[j];
-      if (raw && p.w_out != nullptr) p.w_out[j] = w;
-    }
+    p.slots[j] = make_uint2(word_of(r, j), __float_as_uint(w));
+    if (raw && p.ids_out != nullptr) p.ids_out[j] = r.expert[j];
+    if (raw && p.w_out != nullptr) p.w_out[j] = w;
   }
-  if (block0 && ew == 0 && lane == 0) p.slots[p.n * p.K] = make_uint2(entries, 0u);
+  if (ew == 0 && lane == 0) p.slots[p.n * p.K] = make_uint2(entries, 0u);
 }
 
 // A part of a tile: blocks [k0, k1) of tile `col` of virtual expert `v`.
