@@ -14,7 +14,10 @@ are larger than the 129 MB L2, so no L2 flush is needed between steps; a
 workload whose inputs fit in L2 gets L2 flushed (a 256 MB write, not timed)
 before every timed step.
 
-Prints one JSON line (rank 0).  Under torchrun every rank runs its own
+Prints one JSON line (rank 0) with the headline, and to stderr one more with
+the same keys and every kernel's and configuration's figures: some twenty
+thousand characters, more than what reads a benchmark's output keeps of it.
+Under torchrun every rank runs its own
 replica on its own tokens (weak scaling, no collective on the data path; a
 max-reduction of the timings only).  ``--impl reference`` times the CPU
 oracle on the host cores instead, on a bounded sample of the same workload.
@@ -1029,7 +1032,17 @@ def run_ours(args, dist, rank, world):
     if configs is not None:
         line["configs"] = configs
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        emit(line)
+
+
+# what of the line is figures of parts and of other configurations
+DETAILS = ("kernels", "mxfp8_forward", "mxfp8_train", "mxfp8_train_bf16_wgrad", "configs")
+
+
+def emit(line):
+    """The headline to stdout, everything to stderr."""
+    print(json.dumps(line), file=sys.stderr, flush=True)
+    print(json.dumps({k: v for k, v in line.items() if k not in DETAILS}), flush=True)
 
 
 def measure_e2e(step, inp, args, dist, fwd_only):
