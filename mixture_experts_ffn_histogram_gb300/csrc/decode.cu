@@ -6,7 +6,7 @@
 //
 // With a few tokens the layer is bound by reading the weights of the experts
 // that the tokens name, each once.  So the weights' columns are the 128 side
-// of the MMA and the expert's tokens its narrow side (16 to 64), and the work
+// of the MMA and the expert's tokens its narrow side (up to 64), and the work
 // is cut by weight bytes alone: a phase is a list of tiles of 128 weight
 // columns (64 of gate and 64 of up, or 128 of wo), expert by expert, each a
 // row of 64-deep blocks of 16 KB.  Each of the grid's CTAs (one to an SM)
@@ -24,16 +24,17 @@
 // who was faster.  (Joining by whoever adds the last part took 3 us longer from
 // the last product to h.)
 //
-// One ring of shared memory carries both phases' blocks and keeps 128 KB or
-// more under way (with 32 KB an SM streams at two thirds of the rate): FC2's
+// One ring of shared memory carries both phases' blocks and keeps 128 KB of
+// weights under way, 112 beside the routing tables of 2048 slots, 96 with those of
+// a thousand experts too (with 32 KB an SM streams at two thirds of the rate): FC2's
 // weights start to stream as soon as FC1's have been asked for, and only the
 // rows of h wait, block by block, for the flags that FC1's epilogue sets.  The
 // launch is cooperative: CTAs wait (bounded) for one another's flags, so all
 // have to be resident.
 //
 // h is rounded to the operands' type: the tensor core multiplies no wider one,
-// and its error, half a step on each of F terms of both signs, stays below the
-// result's own rounding.  Partial sums, routing weights and the combine are fp32.
+// and its error, half a step on each of F terms of both signs, is about as large
+// as the result's own rounding.  Partial sums, routing weights and the combine are fp32.
 #include <cuda.h>
 
 #include <algorithm>
@@ -51,7 +52,15 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCols = 128;                         // weight columns of a tile
 constexpr int kWeightStage = kCols * kBlockK * 2;  // 16 KB
-constexpr int kMaxStages = 12;
+// Tokens of a tile: an expert with more of them reads its weights again.  Tiles of
+// 16 or 32 for calls that need no more leave the ring more stages and are slower
+// all the same (4 tokens of 2816 -> 704: 71.0 us with 16, 67.0 with 64; of 7168 ->
+// 2048: 391 and 383; only 24 of 512 -> 192 and 256 experts: 41.2 with 32, 42.3), and
+// 256 tokens read too much twice (2816 -> 704: 291 us with 16, 255 with 32, 254).
+constexpr int kTokens = 64;
+constexpr int kStage = kWeightStage + kTokens * kBlockK * 2;  // 24 KB
+constexpr int kTmemCols = 2 * kTokens;
+constexpr int kMaxStages = 9;
 constexpr int kMinStages = 3;
 constexpr int kBufLd = kCols + 4;
 constexpr int kBufBytes = 16 * kBufLd * 4;  // 16 tokens of a tile
@@ -60,7 +69,7 @@ constexpr int kFirstEpiWarp = 4;
 constexpr uint16_t kNone = 0xffff;
 constexpr int kQueue = 4;
 constexpr int kQueueReaders = 1 + 1 + 4;
-static_assert(!fits_beside_pair(kMinStages * (kWeightStage + 16 * kBlockK * 2)),
+static_assert(!fits_beside_pair(kMinStages * kStage),
               "CTAs that wait for one another must not fit beside a pair's: tmem_share.h");
 
 // What the combine reads and writes.
@@ -70,7 +79,7 @@ struct CombineParams {
   const void* res;
   void* out;
   int64_t ldres, ldout;
-  int n, D, F, K, nt;
+  int n, D, F, K;
   uint32_t grid;  // of the first kernel
 };
 
@@ -81,13 +90,12 @@ struct Params {
   float* w_out;
   int n, D, E, K, F;  // n: tokens of this call
   int mode;
-  int nt, nt_log;     // tokens of a tile at most (16, 32 or 64)
   uint32_t k_inverse;  // 2^16 / K, rounded up: slot * k_inverse >> 16 = slot / K for slots below 2048
   int stages;
   uint32_t type;      // of the instruction descriptor
   void* h;            // [n * K][F]
   float* y;           // [n * K][D]: FC2's rows of tiles that one CTA summed alone
-  float* part;        // [2 phases][CTA][head, tail][nt][128]: sums of parts of tiles
+  float* part;        // [2 phases][CTA][head, tail][kTokens][128]: sums of parts of tiles
   uint2* slots;       // for the combine's kernel
   int32_t* gids;      // [n * K] and its weights: selections that the CTAs exchange
   float* gw;
@@ -115,7 +123,7 @@ struct Ctl {
 };
 
 // The routing, in shared memory.  Slot j = t * K + k.  An expert with more than
-// nt slots makes several entries of the list that the tiles follow ("virtual
+// kTokens slots makes several entries of the list that the tiles follow ("virtual
 // experts").
 struct Route {
   float* w;  // [R]: block 0's weights, or (all blocks', up to kWarps tokens that select) scores
@@ -125,17 +133,17 @@ struct Route {
   uint16_t *first, *start;                   // [E]: its first virtual expert, its place in the list
 };
 constexpr int kWarps = kThreads / 32;
-__host__ __device__ inline int most_virtual(int R, int E, int nt_log) {
-  const int v = E + (R >> nt_log);
+__host__ __device__ inline int most_virtual(int R, int E) {
+  const int v = E + R / kTokens;
   return v < R ? v : R;
 }
-__host__ __device__ inline size_t route_bytes(int R, int E, int nt_log) {
-  const size_t half = 4 * static_cast<size_t>(R) + 3 * static_cast<size_t>(most_virtual(R, E, nt_log)) +
+__host__ __device__ inline size_t route_bytes(int R, int E) {
+  const size_t half = 4 * static_cast<size_t>(R) + 3 * static_cast<size_t>(most_virtual(R, E)) +
                       (kWarps + 2) * static_cast<size_t>(E);
   return 4 * static_cast<size_t>(R) + (half * 2 + 15) / 16 * 16;
 }
-__device__ __forceinline__ Route route_at(uint8_t* p, int R, int E, int nt_log) {
-  const int V = most_virtual(R, E, nt_log);
+__device__ __forceinline__ Route route_at(uint8_t* p, int R, int E) {
+  const int V = most_virtual(R, E);
   Route r;
   r.w = reinterpret_cast<float*>(p);
   uint16_t* q = reinterpret_cast<uint16_t*>(p + 4 * static_cast<size_t>(R));
@@ -356,7 +364,7 @@ __device__ __forceinline__ int build_list(const Params& p, const Route& r, Ctl& 
     }
     r.start[e] = static_cast<uint16_t>(sum);  // the count, until its place is known
     slots += sum;
-    lists += (sum + p.nt - 1) >> p.nt_log;
+    lists += (sum + kTokens - 1) / kTokens;
   }
   int ss = slots, sl = lists;
 #pragma unroll
@@ -384,10 +392,10 @@ __device__ __forceinline__ int build_list(const Params& p, const Route& r, Ctl& 
     const int count = r.start[e];
     r.start[e] = static_cast<uint16_t>(at);
     r.first[e] = static_cast<uint16_t>(v);
-    for (int c = 0; c < count; c += p.nt, ++v) {
+    for (int c = 0; c < count; c += kTokens, ++v) {
       r.vexp[v] = static_cast<uint16_t>(e);
       r.vstart[v] = static_cast<uint16_t>(at + c);
-      r.vcnt[v] = static_cast<uint16_t>(min(p.nt, count - c));
+      r.vcnt[v] = static_cast<uint16_t>(min(kTokens, count - c));
     }
     at += count;
   }
@@ -397,10 +405,10 @@ __device__ __forceinline__ int build_list(const Params& p, const Route& r, Ctl& 
     if (j >= R) break;
     const int e = r.expert[j];
     if (e != kNone) {
-      const int rank = r.rank[j] + mine[e];
+      const uint32_t rank = static_cast<uint32_t>(r.rank[j]) + mine[e];
       r.list[r.start[e] + rank] = static_cast<uint16_t>(j);
-      r.at[j] = static_cast<uint16_t>(r.first[e] + (rank >> p.nt_log));
-      r.rank[j] = static_cast<uint16_t>(rank & (p.nt - 1));  // in its virtual expert
+      r.at[j] = static_cast<uint16_t>(r.first[e] + rank / kTokens);
+      r.rank[j] = static_cast<uint16_t>(rank % kTokens);  // in its virtual expert
     }
   }
   return entries;
@@ -446,8 +454,14 @@ __device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b) {
 
 // One phase's tiles and blocks.  (At most 1056 virtual experts of 256 tiles; the
 // blocks cut into runs are of fewer tiles than CTAs: products stay below 2^24.)
-constexpr uint32_t kLeastBlocks = 4;  // of a run: shorter ones cost more to join than they save
-constexpr uint32_t kLeastClaims = 4;  // tiles for each CTA, for these to be claimed one by one
+// Blocks of a run: shorter ones cost more to join than they save (1 token of 2816 ->
+// 704: 40.2 us with one at least, 40.0 with two, 38.0 with four, 37.8 with eight; of
+// 256 -> 512: 18.6, 16.6, 14.6, 16.7).
+constexpr uint32_t kLeastBlocks = 4;
+// FC2's tiles for each CTA, for these to be claimed one by one (2816 -> 704: 8 tokens,
+// eight tiles each, 103 us claimed and 109 not; 4 tokens, four each, 67.8 and 71.6; 2
+// tokens, two each, 48.7 and 47.4; 1 token, 40.4 and 38.0).
+constexpr uint32_t kLeastClaims = 4;
 struct Phase {
   uint32_t kb;                       // blocks of a tile
   uint32_t cols;                     // tiles of a virtual expert
@@ -530,8 +544,8 @@ struct Feed {
 };
 // Where CTA c keeps the sums of a part that starts its tile (tail = 1: it is
 // the last of the CTA's run) or not (tail = 0: its first).
-__device__ __forceinline__ float* part_rows(float* part, uint32_t grid, int nt, int phase, uint32_t c, int tail) {
-  return part + ((static_cast<int64_t>(phase) * grid + c) * 2 + tail) * nt * kCols;
+__device__ __forceinline__ float* part_rows(float* part, uint32_t grid, int phase, uint32_t c, int tail) {
+  return part + ((static_cast<int64_t>(phase) * grid + c) * 2 + tail) * kTokens * kCols;
 }
 
 template <typename T>
@@ -582,7 +596,7 @@ __device__ __forceinline__ void combine_unit(const CombineParams& p, const Phase
   }
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   const auto part = [&](uint32_t c, int tail, uint32_t at) {
-    return __ldcg(reinterpret_cast<const float4*>(part_rows(const_cast<float*>(p.part), p.grid, p.nt, 1, c, tail) +
+    return __ldcg(reinterpret_cast<const float4*>(part_rows(const_cast<float*>(p.part), p.grid, 1, c, tail) +
                                                   at * kCols + lane * 4));
   };
   for (int k0 = 0; k0 < p.K; k0 += kAhead) {
@@ -651,16 +665,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int stage_bytes = kWeightStage + p.nt * kBlockK * 2;
-  float* buf = reinterpret_cast<float*>(ring + p.stages * stage_bytes);
+  float* buf = reinterpret_cast<float*>(ring + p.stages * kStage);
   Ctl& s = *reinterpret_cast<Ctl*>(reinterpret_cast<uint8_t*>(buf) + kBufBytes);
-  const Route r = route_at(reinterpret_cast<uint8_t*>(&s) + sizeof(Ctl), p.n * p.K, p.E, p.nt_log);
+  const Route r = route_at(reinterpret_cast<uint8_t*>(&s) + sizeof(Ctl), p.n * p.K, p.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // set up by the last warps, while the first ones select
   if (threadIdx.x == 0) s.abort_flag = 0;
   if (warp == kWarps - 2) {
-    tmem_alloc<1>(&s.tmem_base, 2 * p.nt);
+    tmem_alloc<1>(&s.tmem_base, kTmemCols);
     tmem_relinquish<1>();
   } else if (threadIdx.x == 32 * (kWarps - 1)) {
     for (int i = 0; i < p.stages; ++i) {
@@ -732,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kb = q.k0; kb < q.k1; ++kb) {
             ok = mbar_wait(&s.empty[stage], phase ^ 1u, wc);
             if (!ok) break;
-            uint8_t* at = ring + stage * stage_bytes;
+            uint8_t* at = ring + stage * kStage;
             mbar_arrive_expect_tx(&s.fullw[stage], kWeightStage);
             tma_load_3d(at, map, &s.fullw[stage], c0, kb * kBlockK, e);
             tma_load_3d(at + kChunk, map, &s.fullw[stage], c1, kb * kBlockK, e);
@@ -786,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_expect_tx(&s.fullt[stage], groups * 512);
           __syncwarp();
           if (lane < groups)
-            gather4(ring + stage * stage_bytes + kWeightStage + 512 * lane, ph == 0 ? &map_x : &map_h,
+            gather4(ring + stage * kStage + kWeightStage + 512 * lane, ph == 0 ? &map_x : &map_h,
                     &s.fullt[stage], kb * kBlockK, row);
           ++filled;
           if (++stage == p.stages) {
@@ -838,8 +851,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait(&s.fullw[stage], phase, wc) && mbar_wait(&s.fullt[stage], phase, wc);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t at = base + stage * stage_bytes;
-            issue_block<1>(tmem + slot * p.nt, at, at + kWeightStage, weights, tokens, idesc, kb > q.k0 ? 1u : 0u);
+            const uint32_t at = base + stage * kStage;
+            issue_block<1>(tmem + slot * kTokens, at, at + kWeightStage, weights, tokens, idesc, kb > q.k0 ? 1u : 0u);
             umma_commit<1>(&s.empty[stage]);
             ++done;
             if (++stage == p.stages) {
@@ -885,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const auto joined = [&](int t0, float (&g)[8], float (&u)[8]) {
           for (uint32_t c = join0; c <= join1; ++c) {
-            const float* at = part_rows(p.part, gridDim.x, p.nt, 0, c, 0) + (t0 + i16) * kCols;
+            const float* at = part_rows(p.part, gridDim.x, 0, c, 0) + (t0 + i16) * kCols;
             add8<false>(at + c8, g);
             add8<false>(at + 64 + c8, u);
           }
@@ -895,10 +908,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = epi_all(warp_wait(&s.tfull[slot], (piece >> 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
-        float* rows = part_rows(p.part, gridDim.x, p.nt, ph, blockIdx.x, q.k0 == 0 ? 1 : 0);
+        float* rows = part_rows(p.part, gridDim.x, ph, blockIdx.x, q.k0 == 0 ? 1 : 0);
         for (int t0 = 0; t0 < cnt; t0 += 16) {
           uint32_t v[16];
-          tmem_ld_32x32b_x16(tq + slot * p.nt + t0, v);
+          tmem_ld_32x32b_x16(tq + slot * kTokens + t0, v);
           tmem_ld_wait();
           const int m = min(16, cnt - t0);
           if (ph == 0 && q.k0 == 0) {
@@ -943,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == kWarps - 2) {
     tc_fence_after();
-    tmem_dealloc<1>(tmem, 2 * p.nt);
+    tmem_dealloc<1>(tmem, kTmemCols);
   }
 }
 
@@ -960,11 +973,6 @@ bool map3(CUtensorMap* m, const void* base, uint64_t inner, uint64_t mid, uint64
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tokens of a tile at most.  Up to 64, so that a stage's rows leave 128 KB of
-// the ring to the weights; an expert with more tokens reads its weights again.
-int tile_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
-int log_of(int nt) { return nt == 16 ? 4 : nt == 32 ? 5 : 6; }
-
 constexpr int kMaxGrid = 192;  // CTAs that the workspace has room for: no device of this kind has more SMs
 static_assert((32 + kMaxGrid) * 4 <= 1024, "counters and flags ahead of the tiles' flags");
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
@@ -974,16 +982,16 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 struct Layout {
   size_t done, slots, gids, gw, h, y, part, all;
   explicit Layout(const moe_dims& d) {
-    const size_t R = static_cast<size_t>(d.T) * d.K, nt = tile_tokens(d.T);
-    const size_t tiles = static_cast<size_t>(most_virtual(static_cast<int>(R), d.E, log_of(tile_tokens(d.T)))) * (d.F / 64);
-    done = 1024;  // behind the two counters and the CTAs' flags
+    const size_t R = static_cast<size_t>(d.T) * d.K;
+    const size_t tiles = static_cast<size_t>(most_virtual(static_cast<int>(R), d.E)) * (d.F / 64);
+    done = 1024;  // behind the three counters and the CTAs' flags
     slots = done + up(tiles * 4);
     gids = slots + up((R + 1) * 8);
     gw = gids + up(R * 4);
     h = gw + up(R * 4);
     y = h + up(R * d.F * 2);
     part = y + up(R * d.D * 4);
-    all = part + up(static_cast<size_t>(kMaxGrid) * 4 * nt * kCols * 4);
+    all = part + up(static_cast<size_t>(kMaxGrid) * 4 * kTokens * kCols * 4);
   }
 };
 
@@ -1003,8 +1011,6 @@ cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   p.K = d.K;
   p.F = d.F;
   p.mode = c.mode;
-  p.nt = tile_tokens(d.T);
-  p.nt_log = log_of(p.nt);
   p.k_inverse = static_cast<uint32_t>((65536 + d.K - 1) / d.K);
   p.type = c.type == MOE_BF16 ? 1u : 0u;
   p.status = c.dev_status;
@@ -1024,9 +1030,8 @@ cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   p.y = reinterpret_cast<float*>(ws + at.y);
   p.part = reinterpret_cast<float*>(ws + at.part);
   const size_t R = static_cast<size_t>(c.n) * d.K;
-  const size_t fixed = 1024 + kBufBytes + sizeof(Ctl) + route_bytes(static_cast<int>(R), d.E, p.nt_log);
-  const size_t stage = kWeightStage + static_cast<size_t>(p.nt) * kBlockK * 2;
-  p.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemLimit - fixed) / stage));
+  const size_t fixed = 1024 + kBufBytes + sizeof(Ctl) + route_bytes(static_cast<int>(R), d.E);
+  p.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemLimit - fixed) / kStage));
   if (p.stages < kMinStages) return cudaErrorInvalidValue;
   CUtensorMap wi, wo, x, h;
   if (!map3(&wi, c.wi, 2 * static_cast<uint64_t>(d.F), d.D, d.E) || !map3(&wo, c.wo, d.D, d.F, d.E) ||
@@ -1049,7 +1054,7 @@ cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   attr[0].val.cooperative = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = fixed + p.stages * stage;
+  cfg.dynamicSmemBytes = fixed + p.stages * static_cast<size_t>(kStage);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -1067,7 +1072,6 @@ cudaError_t launch_typed(const DecodeCall& c, cudaStream_t s) {
   q.D = d.D;
   q.F = d.F;
   q.K = d.K;
-  q.nt = p.nt;
   q.grid = static_cast<uint32_t>(grid);
   cudaLaunchAttribute overlap = overlap_attribute();
   const int units = c.n * ((d.D + kCols - 1) / kCols);

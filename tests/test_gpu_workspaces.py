@@ -14,9 +14,8 @@ BF = torch.bfloat16
 def _decode_flags(op):
     """The counters, the blocks' flags and the tiles' flags of a MoEDecode: by the
     capacity, as the kernel's host side lays them out."""
-    tile = 16 if op.T <= 16 else 32 if op.T <= 32 else 64
     slots = op.T * op.K
-    tiles = min(slots, op.E + slots // tile) * (op.F // 64)
+    tiles = min(slots, op.E + slots // 64) * (op.F // 64)
     return op.ws[:1024 + 4 * tiles]
 
 
