@@ -163,6 +163,9 @@ constexpr int kShrinkThreads = 192;
 constexpr int kTokenStage = kTile * kBlockK * 2;  // 16 KB
 constexpr int kMaxStages = 8;
 constexpr int kMinStages = 3;
+// Blocks of a cut of the reduction (8 tokens of 8 adapters, 2816 -> 16 -> 2816: 10.5 us
+// with one at least, 9.9 with two, 10.2 with four, 11.4 with eight; 16 tokens of one of
+// rank 64: 14.4, 12.5, 12.4, 12.5).
 constexpr int kLeastCutBlocks = 4;
 
 // The cuts of a tile's reduction: as many as give every CTA of the grid (two
@@ -177,8 +180,19 @@ __device__ __forceinline__ int cuts_of(int tiles, int grid, int kblocks) {
 // against 125).  Else the epilogue's warps copy the rows, and parts are joined by
 // a kernel of their own (2000 tokens of 16 adapters: 18 against 23; 32768 of 16:
 // 73 against 87, since gathers keep to 31 bytes a ns and SM).
-constexpr int kFewTokens = 256;  // of a call: no kernel for parts
-__device__ __forceinline__ bool few_tokens(const PlanHead& h) { return h.n <= kFewTokens || h.live <= 32 * h.tiles; }
+// The border is 32 tokens to a tile (2816 -> 2816, one adapter, of rank 16 and of
+// 64: 32 tokens 10.5 and 16.6 us this way, 12.7 and 18.7 the other; 48: 12.4 and
+// 20.6, 12.6 and 14.6; 128: 20.2 and 39.3, 14.4 and 18.7).
+constexpr int kFewTokens = 32;  // of a tile
+// A call of up to 256 tokens and 32 to each of the pool's adapters is taken for
+// such a one whatever its plan, and its kernel for parts is not launched (256 of 16
+// adapters of rank 16: 12.5 us against 14.6 with it; if they all name one adapter
+// 20.6 against 14.4, which is why longer calls leave it to the plan).
+constexpr int kFewOfCall = 256;
+inline bool few_tokens(int n, int slots) { return n <= kFewOfCall && n <= static_cast<int64_t>(kFewTokens) * slots; }
+__device__ __forceinline__ bool few_tokens(const PlanHead& h, bool of_call) {
+  return of_call || h.live <= kFewTokens * h.tiles;
+}
 
 struct ShrinkParams {
   const void* x;
@@ -192,6 +206,7 @@ struct ShrinkParams {
   int32_t* arrived;  // [tile]: cuts whose part is stored; zero between calls
   const float* scale;
   int n, slots, width, kblocks, stages;  // width: rank in whole 16s
+  bool few;  // few_tokens whatever the plan: no kernel for parts
   uint32_t type;
   int32_t* status;
   uint64_t limit_ns;
@@ -278,7 +293,7 @@ template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) {
   const PlanHead head = *p.head;
   const int cuts = cuts_of(head.tiles, p.shrink_grid, p.kblocks);
-  const bool few = few_tokens(head), work = head.n == p.n && head.slots == p.slots && cuts > 1 && !few;
+  const bool few = few_tokens(head, false), work = head.n == p.n && head.slots == p.slots && cuts > 1 && !few;
   // Of tiles of few tokens, expand's blocks are better let in together once
   // shrink's have gone than one by one between them (2000 tokens of 1024 adapters
   // of rank 64: 188 us against 234; of rank 16: 100 against 99), of others the
@@ -386,7 +401,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   }
   const int cuts = cuts_of(head.tiles, gridDim.x, p.kblocks), units = head.tiles * cuts;
   if (static_cast<int>(blockIdx.x) >= units) return;
-  const bool few = few_tokens(head);
+  const bool few = few_tokens(head, p.few);
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int stage_bytes = kTokenStage + p.width * kBlockK * 2;
   ShrinkCtl& s = *reinterpret_cast<ShrinkCtl*>(ring + p.stages * stage_bytes);
@@ -559,6 +574,7 @@ struct ExpandParams {
   int64_t ldres, ldy;
   int n, slots, N, rank, width;
   int halves;    // of a tile: one where no tile can have more tokens than a unit
+  bool few;
   bool in_place;  // y is res: nothing to do for tokens without an adapter
 };
 // Words of a row of v in shared memory: 8 more than whole 32s, so that the
@@ -601,7 +617,7 @@ __global__ void __launch_bounds__(kExpandThreads, KB > 4 ? 3 : kExpandBlocks) ex
   constexpr int kWords = v_words(KB);
   // the plan and res are older than the call: no need to wait for those
   const PlanHead head = *p.head;
-  const bool mine = head.n == p.n && head.slots == p.slots, early = KB > 1 && !few_tokens(head);
+  const bool mine = head.n == p.n && head.slots == p.slots, early = KB > 1 && !few_tokens(head, p.few);
   const int chunks = (p.N + kExpandCols - 1) / kExpandCols;
   const int64_t units = mine ? static_cast<int64_t>(head.tiles + (p.in_place ? 0 : head.none)) * p.halves * chunks : 0;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
@@ -788,7 +804,7 @@ cudaError_t launch_shrink(const ShrinkParams& p, const CUtensorMap& mx, const CU
   if (err != cudaSuccess) return err;
   shrink_kernel<T><<<grid, kShrinkThreads, bytes, s>>>(mx, ma, p);
   const cudaError_t launched = cudaGetLastError();
-  if (launched != cudaSuccess || p.n <= kFewTokens) return launched;
+  if (launched != cudaSuccess || p.few) return launched;
   JoinParams j{};
   j.head = p.head;
   j.tiles = p.tiles;
@@ -883,6 +899,7 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   p.scale = c.scale;
   p.n = c.n;
   p.slots = d.slots;
+  p.few = few_tokens(c.n, d.slots);
   p.width = (d.rank + 15) / 16 * 16;
   p.kblocks = (d.K + kBlockK - 1) / kBlockK;
   p.type = d.type == MOE_BF16 ? 1u : 0u;
@@ -915,6 +932,7 @@ cudaError_t launch_adapters(const AdapterCall& c, cudaStream_t s) {
   e.N = d.N;
   e.rank = d.rank;
   e.width = p.width;
+  e.few = p.few;
   e.halves = c.n <= kExpandTokens ? 1 : kTile / kExpandTokens;
   e.in_place = c.y == c.res && c.ldy == c.ldres;
   const int64_t units = most * e.halves * ((d.N + kExpandCols - 1) / kExpandCols);
