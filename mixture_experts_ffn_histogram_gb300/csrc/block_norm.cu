@@ -367,7 +367,10 @@ __device__ __forceinline__ void sums_of(float (&v)[N], float (*red)[8], int nwar
 }
 
 constexpr int kBwdGroups = 4;  // ONE_WARP: warps of a block, each on rows of its own
-constexpr int64_t kOneBlockRows = 8;
+// Rows that one block takes, which needs no kernel to join sums (bf16, one block
+// against several and the join: 2 x 7168 9.5 us and 10.9, 4 x 2816 6.8 and 7.0, 4 x 7168
+// 13.5 and 11.1, 8 x 2816 9.6 and 7.0, 8 x 7168 21.1 and 11.2; 256 columns are equal).
+constexpr int64_t kOneBlockRows = 2;
 enum { kDu, kR, kDr, kY, kArrays };  // arrays of a row, each in its own slots
 
 // FULL: every array is given and all have the same ld, as between two blocks
@@ -848,7 +851,10 @@ cudaError_t bwd_full(const BlockNormCall& c, cudaStream_t s) {
   }
   return bwd_launch<T, W, VEC, NV, ONE_WARP, R, SHIFT, false>(c, s);
 }
-// Two rows at a time where a thread holds up to eight columns.
+// Two rows at a time where a thread holds up to eight columns (one against two:
+// 32768 x 2816 bf16 202 us and 172, x 1407 134 and 125, 4099 x 1001 fp32 22.1 and 21.0;
+// even rows of fp32 are better off with one, 8192 x 2048 64.4 and 68.5, but wide ones
+// of odd length and all of 16 bits are not).
 template <typename T, typename W, int VEC, bool SHIFT>
 cudaError_t bwd_rows(const BlockNormCall& c, cudaStream_t s) {
   const int nvec = SHIFT ? shifted_vectors(c.d.D, VEC) : c.d.D / VEC;

@@ -280,7 +280,8 @@ __device__ __forceinline__ float weigh(const Params& p, float v, int lane) {
 // CTA selects all for itself (and leaves the scores in r.w: only the combine
 // needs weights, and that is far off); of more tokens each CTA selects its own, and they
 // exchange them through global memory (128 tokens of 128 experts: 42 us when
-// every CTA selected all).  False: a wait gave up.
+// every CTA selected all; 8 tokens, 2816 -> 704, 102.9 us and 103.9 exchanged, 512 ->
+// 192 28.2 and 30.6).  False: a wait gave up.
 __device__ __forceinline__ bool select_all(const Params& p, const Route& r, const WaitCtl& wc, int warp, int lane) {
   const int R = p.n * p.K;
   bool ok = true;

@@ -45,6 +45,7 @@ def test_the_expert_layer(T, D, E, K, F, mode):
 
 # the reduction cut, its parts joined by the last to arrive; by a kernel of their own; not cut
 @pytest.mark.parametrize("T,K,N,slots,rank", [(61, 2816, 264, 30, 16), (900, 2048, 264, 400, 24),
+                                              (130, 2048, 264, 1, 24), (256, 1024, 264, 7, 8),
                                               (1500, 2048, 136, 3, 64), (5000, 192, 136, 2, 32)])
 def test_the_adapters(T, K, N, slots, rank):
     need_gpu()
