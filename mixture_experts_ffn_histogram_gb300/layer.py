@@ -731,7 +731,7 @@ class DecodeLayer:
         self.experts = MoEDecode(T, D, E, K, F, score_mode, dtype, device)
         self.norm = BlockNorm(T, D, dtype, torch.float32, eps, branch, offset, train=False, device=device)
 
-    def forward(self, r, u, weights, bias=None, batch=None, ids=None, w=None, stream=None):
+    def forward(self, r, u, weights, bias=None, batch=None, stream=None, ids=None, w=None):
         g = weights
         if batch is not None and self.adapters is None:
             raise ValueError("the layer was built without adapters (slots=0)")

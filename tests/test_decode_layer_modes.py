@@ -48,6 +48,15 @@ def test_a_given_selection_is_handed_on():
     assert lay.experts.ids is ids and lay.experts.w is p
 
 
+def test_arguments_by_place_are_as_before():
+    T, D, E, K, F, S = 4, 64, 8, 2, 64, 64
+    called = []
+    lay = _stand_ins(DecodeLayer(T, D, E, K, F, S, device="cpu"), called)
+    x = torch.zeros(T, D, dtype=BF)
+    lay.forward(x, x, _weights(D, E, F, S, 1, "cpu"), None, None, 0)    # bias, batch, stream
+    assert called == ["gate", "up", "down", "experts", "norm"]
+
+
 @pytest.mark.parametrize("mode,given,bias,message", [
     (B.SCORE_GIVEN, (), False, "needs ids and w"), (B.SCORE_GIVEN, ("ids",), False, "needs ids and w"),
     (B.SCORE_GIVEN, ("w",), False, "needs ids and w"), (B.SCORE_GIVEN, ("ids", "w"), True, "no bias"),
